@@ -387,6 +387,109 @@ int ds_vit_overlay_chunk(void* chunk, int64_t chunk_begin, int64_t chunk_rows, i
                          int64_t n_embeds, const void* sentinel, uint8_t* row_type,
                          void* stream);
 
+/* ---------------------------------------------------------------------------
+ * The paged K/V cache of the prompt's language model: what the rows that the
+ * overlay filled meet next, layer by layer.  The pages have no counterpart for
+ * it (their decoders are other programs); the calls follow the overlay's forms:
+ * packed rows of several sequences, chunked prefill, entries that live on the
+ * device and are checked there.
+ *
+ * A call covers n sequences.  Sequence s owns the packed rows row_off[s] ..
+ * row_off[s+1]-1, its newest tokens in order (one for a decoding step, a chunk
+ * of a prompt, or none), and has kv_len[s] tokens in the cache, these rows
+ * included.  With c rows, row i of s stands at position p = kv_len[s] - c + i.
+ * A row with p < 0 is padding in front of the sequence: it is not stored, and
+ * reads and attends to zeros.  Packed rows behind row_off[n] (a padded batch)
+ * and in front of row_off[0] are not touched.  Position p lives in page
+ * table[s * table_cols + p / page], slot p % page; entries for pages that a
+ * call has no need of (past kv_len, or hidden by the window) are not read.
+ *
+ * Contents: bf16, or e4m3 (8-bit floating point, largest value 448) with one
+ * exponent byte per token and head: for a = max |x| over the head's values, e
+ * is the least integer with a <= 448 * 2^e, at least -117; the byte is e + 127
+ * and the elements are e4m3(x * 2^-e), rounded to nearest even (at e = 120, at
+ * most 240 in magnitude, so that nothing overflows bf16).  What they stand for,
+ * element * 2^e, is exact in bf16.  A row with an infinity or NaN
+ * gets the byte 255 and reads as NaN.  Contents of e4m3 pages that
+ * ds_vit_cache_write did not make must follow the same rules.
+ * ------------------------------------------------------------------------- */
+#define DS_VIT_CACHE_BF16 0
+#define DS_VIT_CACHE_E4M3 1
+#define DS_VIT_MAX_SEQS 1024        /* sequences per call */
+#define DS_VIT_CACHE_MAX_HEADS 128  /* K/V heads */
+#define DS_VIT_CACHE_MAX_GROUP 128  /* query heads per K/V head */
+
+typedef struct ds_vit_cache {
+  void *k, *v;             /* device [n_pages, kv_heads, page, head_dim], bf16 or e4m3; 16-byte aligned */
+  uint8_t *k_exp, *v_exp;  /* device [n_pages, kv_heads, page], e4m3 only (else NULL) */
+  int64_t n_pages;
+  int32_t kv_heads;
+  int32_t page;            /* tokens per page: 16, 32, 64 or 128 */
+  int32_t head_dim;        /* 64 or 128 */
+  int32_t kind;            /* DS_VIT_CACHE_BF16 or DS_VIT_CACHE_E4M3 */
+} ds_vit_cache;
+
+typedef struct ds_vit_chunks {
+  const int32_t *row_off;  /* device [n + 1], not decreasing */
+  const int32_t *kv_len;   /* device [n] */
+  const int32_t *table;    /* device [n, table_cols] */
+  int32_t n;               /* 1 .. DS_VIT_MAX_SEQS */
+  int32_t table_cols;
+  int32_t max_rows;        /* no sequence has more rows than this */
+} ds_vit_chunks;
+
+/*
+ * The calls.  `rows` is the number of packed rows (row_off[n] <= rows); the
+ * strides are the distances between packed rows in elements, multiples of 8, so
+ * that k, v and q may be parts of one projection's output.  All are
+ * asynchronous on `stream`, allocate nothing and can be captured in a graph,
+ * whose replays read row_off, kv_len and table anew (max_rows, n and rows stay).
+ *   status: device int32.  The entries on the device are checked there: offsets
+ *           out of order, outside [0, rows] or more than max_rows apart record
+ *           DS_VIT_EINVAL; a kv_len outside [0, table_cols * page] and a needed
+ *           page outside [0, n_pages) record DS_VIT_ERANGE.  Rows of such a
+ *           sequence hold no meaningful value afterwards (or stay as they were);
+ *           the other sequences are served.  Never cleared here.
+ * DS_VIT_EINVAL for null or misaligned pointers (16 bytes; int32 arrays 4),
+ * unsupported sizes, a stride below its row's width; DS_VIT_ERANGE for
+ * n_pages * kv_heads * page, table_cols * page or 2 * rows past 2^31 - 1.
+ *
+ * ds_vit_cache_write: rows of k and v (device bf16 [rows, kv_heads, head_dim])
+ * into the pages.  Two rows with the same place leave either one's value.
+ * ds_vit_cache_read: the inverse, the c newest tokens of every sequence as bf16
+ * (all of them with c = kv_len).
+ */
+int ds_vit_cache_write(const ds_vit_cache* cache, const ds_vit_chunks* chunks, const void* k, int64_t k_stride,
+                       const void* v, int64_t v_stride, int64_t rows, int32_t* status, void* stream);
+int ds_vit_cache_read(const ds_vit_cache* cache, const ds_vit_chunks* chunks, void* k, int64_t k_stride, void* v,
+                      int64_t v_stride, int64_t rows, int32_t* status, void* stream);
+
+/*
+ * ds_vit_cache_attention: attention of the packed rows over the cache (written
+ * before, these rows included).  Query head h reads K/V head h / (heads /
+ * kv_heads); heads must be a multiple of kv_heads, at most
+ * DS_VIT_CACHE_MAX_GROUP times it.  The row at position p sees the keys
+ *   j <= p  and  (window == 0 or j > p - window or j < sinks):
+ * causal, optionally a sliding window of `window` tokens (the row's own among
+ * them) with the first `sinks` tokens staying visible; pages that no row's
+ * window reaches may have been given away.
+ *   out[row, h] = bf16(softmax_j(scale * q . k_j) v)        (fp32 sums)
+ * and zeros for a row that sees nothing.  Hidden keys have no part in it,
+ * whatever their values.
+ *   q, out: device bf16 [rows, heads, head_dim]; they may not overlap.
+ *   scale:  in (0, 1e30].
+ *   ws:     device workspace, 16-byte aligned, of at least
+ *           ds_vit_cache_attention_workspace_bytes (DS_VIT_ECAP otherwise);
+ *           needs no initial value.  Calls that may overlap on the GPU need
+ *           workspaces of their own.
+ * A bounded wait that gives up records DS_VIT_ETIMEOUT in *status.
+ */
+int ds_vit_cache_attention_workspace_bytes(const ds_vit_cache* cache, const ds_vit_chunks* chunks, int32_t heads,
+                                           size_t* bytes);
+int ds_vit_cache_attention(const ds_vit_cache* cache, const ds_vit_chunks* chunks, const void* q, int64_t q_stride,
+                           int64_t rows, int32_t heads, float scale, int32_t window, int32_t sinks, void* out,
+                           int64_t out_stride, void* ws, size_t ws_bytes, int32_t* status, void* stream);
+
 /* Kernel kinds reported by ds_vit_set_kernel_timer. */
 /* PATCH_GEMM patchifies and normalises the pixels inside its A-tile load;
  * MERGER_GEMM1 gathers the 3x3 windows inside its A-tile load. */

@@ -1,0 +1,644 @@
+"""The paged K/V cache on the GPU: writing, reading back and attention against
+plain implementations in 64 bits, their masks, paddings and refusals, and a
+prompt taken through them as a serving loop would."""
+import math
+
+import numpy as np
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+
+
+@pytest.fixture(scope="module")
+def dv():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    import __graft_entry__
+    __graft_entry__.build()
+    import vit_vision_encoder_gb300
+    return vit_vision_encoder_gb300
+
+
+# ------------------------------------------------------------------ a plain model of the cache
+
+def e4m3_values():
+    """The 256 values of the format: sign, 4 exponent bits (bias 7), 3 mantissa bits."""
+    out = np.empty(256)
+    for b in range(256):
+        e, m = (b >> 3) & 15, b & 7
+        x = math.nan if (b & 127) == 127 else (m / 8 * 2.0 ** -6 if e == 0 else (1 + m / 8) * 2.0 ** (e - 7))
+        out[b] = -x if b & 128 else x
+    return out
+
+
+E4M3 = e4m3_values()
+
+
+def quantise(x):
+    """Rows [..., d] of float64 -> (bytes, exponent bytes), by the definition: the
+    nearest value of the format, the one with the even last bit on a tie."""
+    x = np.asarray(x, dtype=np.float64)
+    a = np.abs(x).max(-1)
+    fine = np.isfinite(a)
+    e = np.full(a.shape, -117)
+    for cand in range(121, -118, -1):              # the least e with a <= 448 2^e
+        e = np.where(fine & (a <= 448 * 2.0 ** cand), cand, e)
+    scaled = np.where(fine[..., None], np.abs(x), 0) / 2.0 ** e[..., None]
+    pos = E4M3[:127]
+    hi = np.searchsorted(pos, scaled).clip(0, 126)
+    lo = (hi - 1).clip(0)
+    dl, dh = scaled - pos[lo], pos[hi] - scaled
+    pick = np.where((dl < dh) | ((dl == dh) & (lo % 2 == 0)), lo, hi)
+    pick = np.where(e[..., None] == 120, np.minimum(pick, 119), pick)     # at most 240 2^120: finite in bf16
+    bits = np.where(fine[..., None], pick | (np.signbit(x) * 128), 127)
+    return bits.astype(np.uint8), np.where(fine, e + 127, 255).astype(np.uint8)
+
+
+def f64(t):
+    return t.detach().cpu().double().numpy()
+
+
+class Setup:
+    """Sequences of q[s] new rows and kv[s] cached tokens; a random page table;
+    front / back extra packed rows that belong to no sequence."""
+
+    def __init__(self, dv, q, kv, kv_heads, dim, page, kind, seed=0, front=0, back=0, cols=None, max_rows=None,
+                 fill=None):
+        g = torch.Generator().manual_seed(seed)
+        self.q, self.kv, self.kv_heads, self.dim, self.page, self.kind = q, kv, kv_heads, dim, page, kind
+        n = len(q)
+        used = [-(-x // page) for x in kv]
+        self.n_pages = sum(used) + 2
+        cols = max(max(used), 1) if cols is None else cols
+        order = torch.randperm(self.n_pages, generator=g).int()
+        self.spare = int(order[-1])
+        self.table = torch.full((n, cols), -1, dtype=torch.int32)
+        at = 0
+        for s, u in enumerate(used):
+            self.table[s, :u] = order[at:at + u]
+            at += u
+        self.off = [front + sum(q[:s]) for s in range(n + 1)]
+        self.rows = self.off[-1] + back
+        self.chunks = dv.Chunks(torch.tensor(self.off, dtype=torch.int32).cuda(),
+                                torch.tensor(kv, dtype=torch.int32).cuda(), self.table.cuda(),
+                                max(max(q), 1) if max_rows is None else max_rows)
+        shape = (self.n_pages, kv_heads, page, dim)
+        if kind == "bf16":
+            k, v = (torch.randn(shape, generator=g) for _ in range(2))
+            k = k * torch.exp(0.5 * torch.randn((kv_heads, 1, dim), generator=g))
+            self.cache = dv.KvCache(k.bfloat16().cuda(), v.bfloat16().cuda())
+        else:
+            parts = []
+            for _ in range(2):
+                b, e = quantise(torch.randn(shape, generator=g).bfloat16().double().numpy()
+                                * 2.0 ** torch.randint(-3, 3, shape[:3] + (1,), generator=g).numpy())
+                parts.append((torch.from_numpy(b).cuda(), torch.from_numpy(e).cuda()))
+            self.cache = dv.KvCache(parts[0][0], parts[1][0], parts[0][1], parts[1][1])
+        self.g = g
+        if fill is not None:
+            self.spoil(fill)
+
+    def spoil(self, value):
+        """`value` in every slot that holds no token: whole spare pages and the ends of last pages."""
+        free = torch.ones((self.n_pages, self.page), dtype=torch.bool)
+        for s, x in enumerate(self.kv):
+            for j in range(x):
+                free[int(self.table[s, j // self.page]), j % self.page] = False
+        free = free.cuda()[:, None, :]
+        for t, e in ((self.cache.k, self.cache.k_exp), (self.cache.v, self.cache.v_exp)):
+            if e is None:
+                t.masked_fill_(free[..., None], value)
+            else:
+                t.masked_fill_(free[..., None], 127)
+                e.masked_fill_(free, 255)
+
+    def held(self):
+        """(k, v) float64 [n_pages, kv_heads, page, dim]: what the pages stand for."""
+        out = []
+        for t, e in ((self.cache.k, self.cache.k_exp), (self.cache.v, self.cache.v_exp)):
+            if e is None:
+                out.append(f64(t))
+            else:
+                ex = e.cpu().numpy().astype(np.int64)
+                x = E4M3[t.cpu().numpy()] * 2.0 ** (ex[..., None] - 127.0)
+                out.append(np.where(ex[..., None] == 255, math.nan, x))
+        return out
+
+    def tokens(self, held, s):
+        """[kv, kv_heads, dim] of sequence s in order."""
+        j = np.arange(self.kv[s])
+        return held[self.table[s].numpy()[j // self.page], :, j % self.page].reshape(-1, self.kv_heads, self.dim)
+
+    def queries(self, heads, scale=1.0, wide=0):
+        x = torch.randn((self.rows, heads + wide, self.dim), generator=self.g) * scale
+        return x.bfloat16().cuda()[:, :heads]
+
+
+def attention64(st, q, scale, window=0, sinks=0):
+    """(reference, tolerance) [rows, heads, dim] in 64 bits, NaN rows for rows
+    outside every sequence.
+
+    Tolerance of one output o = sum_j w_j v_j (w the softmax weights): the result
+    is rounded to bf16 (2^-8 |o|); each weight is rounded to bf16 before its
+    product (2^-8 A, A = sum_j w_j |v_j|); fp32 scores carry up to (dim + 2)
+    2^-24 sum_d |q_d k_d| each, in the weight and in their sum (twice that,
+    relative to A); exponentials, sums and rescalings in fp32 stay under 2^-12 A.
+    """
+    heads = q.shape[1]
+    g = heads // st.kv_heads
+    q = f64(q)
+    kh, vh = st.held()
+    ref = np.full(q.shape, math.nan)
+    tol = np.zeros(q.shape)
+    for s in range(len(st.q)):
+        k, v = st.tokens(kh, s), st.tokens(vh, s)
+        c = st.q[s]
+        for i in range(c):
+            r, p = st.off[s] + i, st.kv[s] - c + i
+            j = np.arange(p + 1)
+            if window:
+                j = j[(j > p - window) | (j < sinks)]
+            if len(j) == 0:
+                ref[r] = 0
+                continue
+            for h in range(heads):
+                kk, vv = k[j, h // g], v[j, h // g]
+                z = (kk @ q[r, h]) * scale
+                w = np.exp(z - z.max())
+                w /= w.sum()
+                ref[r, h] = w @ vv
+                big = (np.abs(kk) @ np.abs(q[r, h])).max() * scale
+                tol[r, h] = (2.0 ** -8 * np.abs(ref[r, h])
+                             + (w @ np.abs(vv)) * (2.0 ** -8 + 2.0 ** -12 + 2 * (st.dim + 2) * 2.0 ** -24 * big))
+    return ref, tol
+
+
+def check_attention(dv, st, heads, window=0, sinks=0, q=None, scale=None):
+    q = st.queries(heads) if q is None else q
+    scale = st.dim ** -0.5 if scale is None else scale
+    out = torch.full((st.rows, heads, st.dim), 7.0, dtype=torch.bfloat16, device="cuda")
+    got, status = dv.cache_attention(st.cache, st.chunks, q, scale=scale, window=window, sinks=sinks, out=out)
+    torch.cuda.synchronize()
+    assert int(status.item()) == dv.OK
+    ref, tol = attention64(st, q, scale, window, sinks)
+    got = f64(got)
+    mine = np.zeros(st.rows, dtype=bool)
+    mine[st.off[0]:st.off[-1]] = True
+    assert (got[~mine] == 7.0).all()                       # rows of no sequence stay as they were
+    err = np.abs(got[mine] - ref[mine])
+    bad = ~(err <= tol[mine])
+    assert not bad.any(), (f"{bad.sum()} of {bad.size} outside, worst "
+                           f"{np.nanmax(err / np.maximum(tol[mine], 1e-30))} times the tolerance at "
+                           f"{np.argwhere(bad)[:4].tolist()}")
+    return got
+
+
+# ------------------------------------------------------------------ writing and reading
+
+WRITE_CASES = [
+    # q, kv, kv_heads, dim, page, kind, front, back
+    ([1], [1], 1, 64, 16, "bf16", 0, 0),
+    ([1], [16], 1, 128, 16, "e4m3", 0, 0),
+    ([1, 1, 1, 1, 1], [1, 17, 32, 33, 500], 8, 128, 32, "bf16", 0, 3),
+    ([3, 0, 40, 1], [3, 100, 57, 64], 2, 64, 16, "e4m3", 2, 5),
+    ([130, 7, 300], [130, 20, 555], 3, 128, 64, "e4m3", 0, 1),
+    ([200, 0, 0, 129], [200, 0, 5, 1000], 5, 64, 128, "bf16", 4, 0),
+    ([9, 5], [4, 0], 4, 128, 16, "e4m3", 1, 1),            # rows in front of position 0
+    ([2] * 300, [2 + i for i in range(300)], 2, 64, 32, "bf16", 0, 0),
+    ([1, 0] * 512, [1 + i % 70 for i in range(1024)], 1, 64, 16, "e4m3", 0, 0),
+    ([33], [33], 10, 128, 16, "bf16", 0, 0),
+]
+
+
+@pytest.mark.parametrize("q,kv,kv_heads,dim,page,kind,front,back", WRITE_CASES)
+def test_write_and_read(dv, q, kv, kv_heads, dim, page, kind, front, back):
+    """Every byte of the pages after a write, and every row read back, equal the
+    definition's; slots without a new token keep their bytes."""
+    st = Setup(dv, q, kv, kv_heads, dim, page, kind, seed=len(q) + dim, front=front, back=back)
+    x = torch.randn((st.rows, 2 * kv_heads + 1, dim), generator=st.g) * torch.exp(
+        2 * torch.randn((st.rows, 2 * kv_heads + 1, 1), generator=st.g))
+    x = x.bfloat16().cuda()
+    k, v = x[:, 1:1 + kv_heads], x[:, 1 + kv_heads:]        # rows inside a wider tensor
+    want = []
+    for t, e, new in ((st.cache.k, st.cache.k_exp, k), (st.cache.v, st.cache.v_exp, v)):
+        bits = (t.view(torch.int16) if kind == "bf16" else t).cpu().numpy().copy()
+        ex = None if e is None else e.cpu().numpy().copy()
+        rows = new.contiguous().cpu()
+        nb, ne = (rows.view(torch.int16).numpy(), None) if kind == "bf16" else quantise(rows.double().numpy())
+        for s in range(len(q)):
+            for i in range(q[s]):
+                p = kv[s] - q[s] + i
+                if p < 0:
+                    continue
+                page_no, slot = int(st.table[s, p // page]), p % page
+                bits[page_no, :, slot] = nb[st.off[s] + i]
+                if ne is not None:
+                    ex[page_no, :, slot] = ne[st.off[s] + i]
+        want.append((bits, ex))
+    status = dv.cache_write(st.cache, st.chunks, k, v)
+    torch.cuda.synchronize()
+    assert int(status.item()) == dv.OK
+    for (bits, ex), t, e in zip(want, (st.cache.k, st.cache.v), (st.cache.k_exp, st.cache.v_exp)):
+        assert np.array_equal((t.view(torch.int16) if kind == "bf16" else t).cpu().numpy(), bits)
+        assert e is None or np.array_equal(e.cpu().numpy(), ex)
+    wide = torch.full((st.rows, 2 * kv_heads + 1, dim), 7.0, dtype=torch.bfloat16, device="cuda")
+    rk, rv, status = dv.cache_read(st.cache, st.chunks, st.rows, out=(wide[:, :kv_heads], wide[:, kv_heads + 1:]))
+    torch.cuda.synchronize()
+    assert int(status.item()) == dv.OK
+    assert bool((wide[:, kv_heads] == 7.0).all())
+    for got, held in zip((rk, rv), st.held()):
+        got = f64(got)
+        assert (got[:st.off[0]] == 7.0).all() and (got[st.off[-1]:] == 7.0).all()
+        for s in range(len(q)):
+            ref = np.zeros((q[s], kv_heads, dim))
+            t = min(q[s], kv[s])
+            if t:
+                ref[q[s] - t:] = st.tokens(held, s)[kv[s] - t:]
+            assert np.array_equal(got[st.off[s]:st.off[s + 1]], ref)
+
+
+def test_write_e4m3_special_values(dv):
+    """Zeros, every bf16 magnitude as a row's largest, ties, values far below the
+    largest, infinities and NaN."""
+    n = 32768
+    st = Setup(dv, [n], [n], 1, 64, 128, "e4m3", seed=3)
+    bits = torch.arange(n, dtype=torch.int32).to(torch.int16)
+    x = torch.zeros((n, 64), dtype=torch.int16)
+    x[:, 5] = bits
+    x[:, 6] = torch.where(bits > 128 * 20, bits - 128 * 17, torch.zeros_like(bits)) | -32768
+    x[:, 7] = torch.where(bits > 128 * 8, bits - 128 * 3 + 1, torch.zeros_like(bits))
+    x[:, 63] = torch.where(bits > 128 * 10, (bits & -128) - 128 * 9 + 24, torch.zeros_like(bits))
+    k = x.view(torch.bfloat16).view(n, 1, 64)
+    v = torch.flip(k, (0,)).contiguous()
+    dv.cache_write(st.cache, st.chunks, k.cuda(), v.cuda())
+    rk, rv, _ = dv.cache_read(st.cache, st.chunks, n)
+    torch.cuda.synchronize()
+    for src, t, e, back in ((k, st.cache.k, st.cache.k_exp, rk), (v, st.cache.v, st.cache.v_exp, rv)):
+        wb, we = quantise(src.double().numpy())
+        slots = st.table[0].numpy()[np.arange(n) // 128], np.arange(n) % 128
+        gb, ge = t.cpu().numpy()[slots[0], :, slots[1]], e.cpu().numpy()[slots[0], :, slots[1]]
+        assert np.array_equal(ge, we)
+        assert np.array_equal(gb, wb)
+        ref = np.where(we[..., None] == 255, math.nan, E4M3[wb] * 2.0 ** (we[..., None].astype(float) - 127))
+        assert np.array_equal(f64(back), ref, equal_nan=True)
+        fine = np.isfinite(src.double().numpy()).all(-1)
+        # what is read back is off by at most half a step of the format: 2^-4 of
+        # the value, or 2^-10 2^e where the scaled value is subnormal
+        err = np.abs(f64(back) - src.double().numpy())[fine]
+        step = 2.0 ** (we.astype(float)[..., None] - 127)[fine]
+        assert (err <= np.maximum(2.0 ** -4 * np.abs(src.double().numpy()[fine]), 2.0 ** -10 * step)).all()
+
+
+def test_read_every_byte(dv):
+    """Every element byte under every exponent byte that a write can leave; at the
+    largest exponent, elements above 240 (which a write does not leave there)
+    stand for more than bf16 holds and read as infinities."""
+    st = Setup(dv, [240], [240], 4, 64, 16, "e4m3", seed=1)
+    every = torch.arange(256, dtype=torch.uint8)
+    every[127], every[255] = 0, 128
+    for t, e in ((st.cache.k, st.cache.k_exp), (st.cache.v, st.cache.v_exp)):
+        t.copy_(every.view(1, 4, 1, 64).expand(t.shape))
+        e.copy_((torch.arange(e.numel(), dtype=torch.int64) % 238 + 10).to(torch.uint8).view(e.shape))
+    rk, rv, _ = dv.cache_read(st.cache, st.chunks, 240)
+    torch.cuda.synchronize()
+    for got, held in zip((rk, rv), st.held()):
+        want = st.tokens(held, 0)
+        want = np.where(np.abs(want) >= 2.0 ** 128, np.copysign(math.inf, want), want)
+        assert np.array_equal(f64(got), want)
+
+
+# ------------------------------------------------------------------ attention
+
+ATTENTION_CASES = [
+    # q, kv, heads, kv_heads, dim, page, kind
+    ([1], [1], 1, 1, 64, 16, "bf16"),
+    ([1], [2], 8, 8, 128, 16, "e4m3"),
+    ([1], [129], 5, 1, 128, 16, "bf16"),
+    ([1], [1000], 40, 8, 128, 64, "bf16"),
+    ([1], [1000], 40, 8, 128, 64, "e4m3"),
+    ([1] * 9, [1, 16, 17, 63, 64, 65, 300, 0, 777], 8, 2, 64, 32, "bf16"),
+    ([1] * 9, [1, 16, 17, 63, 64, 65, 300, 0, 777], 14, 2, 128, 128, "e4m3"),
+    ([1] * 70, [1 + 7 * i for i in range(70)], 4, 4, 64, 16, "e4m3"),
+    ([4, 1, 0, 3], [4, 50, 9, 260], 16, 2, 128, 32, "bf16"),          # a few rows each
+    ([5, 2, 6], [300, 2, 70], 7, 1, 64, 16, "e4m3"),
+    ([2, 1], [90, 131], 32, 1, 128, 64, "bf16"),                       # 32 query heads on one
+    ([1, 2], [40, 200], 128, 1, 64, 16, "bf16"),                       # the largest group
+    ([17], [17], 2, 2, 64, 16, "bf16"),
+    ([50], [400], 8, 8, 128, 16, "bf16"),                              # chunks
+    ([65], [65], 10, 2, 128, 64, "e4m3"),
+    ([128], [128], 2, 1, 64, 128, "bf16"),
+    ([129, 3], [129, 513], 4, 1, 128, 32, "bf16"),
+    ([100, 0, 260], [100, 7, 300], 6, 2, 64, 16, "e4m3"),
+    ([130, 61], [700, 61], 5, 1, 128, 16, "e4m3"),                     # 5 heads a group: 125 of 128 rows
+    ([90], [250], 21, 3, 64, 64, "bf16"),                              # 7 heads a group
+    ([40], [170], 33, 1, 64, 32, "e4m3"),
+    ([300], [1500], 4, 4, 128, 128, "bf16"),
+    ([3], [40], 128, 1, 128, 16, "e4m3"),
+]
+
+
+@pytest.mark.parametrize("q,kv,heads,kv_heads,dim,page,kind", ATTENTION_CASES)
+def test_attention(dv, q, kv, heads, kv_heads, dim, page, kind):
+    st = Setup(dv, q, kv, kv_heads, dim, page, kind, seed=sum(q) + dim, fill=math.nan)
+    check_attention(dv, st, heads)
+
+
+MASKS = [(1, 0), (1, 1), (2, 3), (16, 4), (17, 0), (64, 1), (100, 37), (128, 128), (129, 5), (1000, 4), (10 ** 9, 0),
+         (2 ** 31 - 1, 2 ** 31 - 1), (0, 7)]
+
+
+@pytest.mark.parametrize("window,sinks", MASKS)
+@pytest.mark.parametrize("q,kv,heads,kv_heads,dim,page,kind", [
+    ([1, 1, 1], [700, 33, 1], 6, 2, 128, 16, "bf16"),
+    ([3, 1], [520, 130], 8, 2, 64, 32, "e4m3"),
+    ([70, 20], [500, 20], 4, 1, 128, 64, "e4m3"),
+    ([200], [430], 2, 2, 64, 16, "bf16"),
+])
+def test_attention_window_and_sinks(dv, q, kv, heads, kv_heads, dim, page, kind, window, sinks):
+    """Pages that no row's window reaches are given away: their table entries name
+    no page, and nothing reads them."""
+    st = Setup(dv, q, kv, kv_heads, dim, page, kind, seed=window % 97 + dim, fill=math.nan)
+    check_attention(dv, st, heads, window, sinks, q=st.queries(heads))
+    if window:
+        away = st.chunks.table.clone()
+        for s in range(len(q)):
+            first = max(0, kv[s] - q[s] - window + 1)
+            for c in range(away.shape[1]):
+                if c * page >= sinks and (c + 1) * page <= first:
+                    away[s, c] = -1
+        st.chunks.table.copy_(away)
+        check_attention(dv, st, heads, window, sinks, q=st.queries(heads))
+
+
+@pytest.mark.parametrize("heads,kv_heads,dim,kind", [(4, 1, 128, "bf16"), (3, 3, 64, "e4m3"), (40, 8, 128, "e4m3")])
+def test_attention_front_padding(dv, heads, kv_heads, dim, kind):
+    """Rows in front of position 0 see nothing and give zeros, with rows of no
+    sequence around them."""
+    st = Setup(dv, [9, 5, 1, 70], [4, 0, 0, 30], kv_heads, dim, 16, kind, seed=5, front=3, back=6)
+    got = check_attention(dv, st, heads)
+    assert (got[3:8] == 0).all() and (got[12:18] == 0).all()
+
+
+@pytest.mark.parametrize("scale", [1.0, 6.0])
+@pytest.mark.parametrize("q,kv,heads,kv_heads,dim,kind", [
+    ([1], [600], 8, 1, 128, "bf16"), ([1], [600], 8, 1, 64, "e4m3"),
+    ([90], [600], 2, 1, 128, "bf16"), ([90], [600], 2, 1, 64, "e4m3")])
+def test_attention_large_scores(dv, q, kv, heads, kv_heads, dim, kind, scale):
+    """Scores of a hundred and more: the running maximum rises and stays right."""
+    st = Setup(dv, q, kv, kv_heads, dim, 32, kind, seed=8)
+    check_attention(dv, st, heads, q=st.queries(heads, 3.0), scale=scale * dim ** -0.5)
+
+
+def _plant(st, s, j, head, value, what):
+    """`value` into one element of token j's row (e4m3: the whole row becomes NaN)."""
+    page, slot = int(st.table[s, j // st.page]), j % st.page
+    t, e = (st.cache.k, st.cache.k_exp) if what == "k" else (st.cache.v, st.cache.v_exp)
+    if e is None:
+        t[page, head, slot, 3] = value
+    else:
+        t[page, head, slot] = 127
+        e[page, head, slot] = 255
+
+
+@pytest.mark.parametrize("what", ["k", "v"])
+@pytest.mark.parametrize("value", [math.nan, math.inf, -math.inf])
+@pytest.mark.parametrize("q,kv,kind,dim,window,sinks", [
+    ([4, 1], [200, 90], "bf16", 128, 0, 0), ([4, 1], [200, 90], "e4m3", 64, 0, 0),
+    ([70, 3], [300, 70], "bf16", 64, 0, 0), ([70, 3], [300, 70], "e4m3", 128, 0, 0),
+    ([70, 3], [300, 70], "bf16", 128, 30, 2), ([6, 2], [300, 70], "e4m3", 128, 30, 2),
+])
+def test_attention_hidden_values_have_no_part(dv, q, kv, kind, dim, window, sinks, value, what):
+    """An infinity or NaN in a key or value that a row does not see leaves that
+    row's result untouched; one that it sees gives NaN or the infinity."""
+    st = Setup(dv, q, kv, 2, dim, 16, kind, seed=6)
+    heads = 4
+    query = st.queries(heads)
+    clean, _ = dv.cache_attention(st.cache, st.chunks, query, window=window, sinks=sinks)
+    clean = f64(clean)
+    bad = kv[0] - q[0] + q[0] // 2            # a new token in the middle of the chunk
+    _plant(st, 0, bad, 1, value, what)
+    got, status = dv.cache_attention(st.cache, st.chunks, query, window=window, sinks=sinks)
+    torch.cuda.synchronize()
+    assert int(status.item()) == dv.OK
+    got = f64(got)
+    ref, tol = attention64(st, query, dim ** -0.5, window, sinks)
+    for i in range(q[0]):
+        p = kv[0] - q[0] + i
+        seen = bad <= p and (window == 0 or bad > p - window or bad < sinks)
+        assert np.array_equal(got[i, :2], clean[i, :2])                 # the other K/V head
+        if not seen:
+            assert (np.abs(got[i, 2:] - clean[i, 2:]) <= 2 * tol[i, 2:]).all(), i
+        elif what == "v" and kind == "bf16":
+            assert (np.isnan(got[i, 2:, 3]) if math.isnan(value) else got[i, 2:, 3] == value).all()
+            rest = np.arange(dim) != 3
+            assert (np.abs(got[i, 2:] - ref[i, 2:])[:, rest] <= tol[i, 2:][:, rest]).all()
+        elif what == "v" or math.isnan(value):
+            assert np.isnan(got[i, 2:]).all()
+    assert np.array_equal(got[q[0]:], clean[q[0]:])
+
+
+def test_attention_over_a_cache_past_32_bits(dv):
+    """Pages whose element offsets pass 2^31 and byte offsets 2^32, bf16."""
+    page, heads, dim = 128, 8, 128
+    n_pages = 2 ** 31 // (page * heads * dim) + 200
+    k = torch.empty((n_pages, heads, page, dim), dtype=torch.bfloat16, device="cuda")
+    v = torch.empty_like(k)
+    st = Setup(dv, [1, 40], [500, 300], heads, dim, page, "bf16", seed=4)
+    far = torch.arange(st.n_pages, dtype=torch.int64) + n_pages - st.n_pages
+    k[-st.n_pages:] = st.cache.k
+    v[-st.n_pages:] = st.cache.v
+    small = st.cache
+    st.cache = dv.KvCache(k, v)
+    table = st.chunks.table
+    table.copy_(torch.where(table >= 0, table + (n_pages - st.n_pages), table))
+    q = st.queries(heads)
+    got, status = dv.cache_attention(st.cache, st.chunks, q)
+    rk, rv, status2 = dv.cache_read(st.cache, st.chunks, st.rows)
+    st.cache = small
+    table.copy_(st.table)
+    want, _ = dv.cache_attention(small, st.chunks, q)
+    wk, wv, _ = dv.cache_read(small, st.chunks, st.rows)
+    torch.cuda.synchronize()
+    assert int(status.item()) == dv.OK and int(status2.item()) == dv.OK and int(far[-1]) == n_pages - 1
+    assert torch.equal(got, want) and torch.equal(rk, wk) and torch.equal(rv, wv)
+
+
+def test_attention_one_pass_over_splits_is_repeatable(dv):
+    """The same call twice gives the same bits, whatever was left in the workspace."""
+    st = Setup(dv, [1, 3, 1], [5000, 2000, 17], 2, 128, 64, "bf16", seed=2)
+    q = st.queries(8)
+    a, _ = dv.cache_attention(st.cache, st.chunks, q)
+    import ctypes
+    nb = ctypes.c_size_t()
+    dv.check(dv.lib.ds_vit_cache_attention_workspace_bytes(st.cache.ref, st.chunks.ref, 8, ctypes.byref(nb)), "size")
+    ws = torch.full((nb.value,), 255, dtype=torch.uint8, device="cuda")
+    b, _ = dv.cache_attention(st.cache, st.chunks, q, ws=ws)
+    torch.cuda.synchronize()
+    assert torch.equal(a, b)
+
+
+# ------------------------------------------------------------------ entries refused on the device
+
+def _calls(dv, st, heads=4):
+    k = st.queries(st.kv_heads)
+    yield lambda: dv.cache_write(st.cache, st.chunks, k, k)
+    yield lambda: dv.cache_read(st.cache, st.chunks, st.rows)[2]
+    q = st.queries(heads)
+    yield lambda: dv.cache_attention(st.cache, st.chunks, q)[1]
+
+
+@pytest.mark.parametrize("rows", [1, 60])
+def test_entries_refused_on_the_device(dv, rows):
+    """Bad offsets, lengths and pages set the status, and the other sequences are
+    served as ever."""
+    def make():
+        return Setup(dv, [rows, rows, rows], [100, 90, 120], 2, 128, 16, "bf16", seed=11)
+
+    def expect(st, code):
+        for call in _calls(dv, st):
+            status = call()
+            torch.cuda.synchronize()
+            assert int(status.item()) == code
+
+    st = make()
+    expect(st, dv.OK)
+    for entry in (-1, st.n_pages, 2 ** 31 - 1, -2 ** 31):
+        st = make()
+        st.chunks.table[1, (90 - 1) // 16] = entry
+        expect(st, dv.ERANGE)
+    for value in (-1, 16 * st.table.shape[1] + 1, 2 ** 31 - 1, -2 ** 31):
+        st = make()
+        st.chunks.kv_len[1] = value
+        expect(st, dv.ERANGE)
+    for at, value in ((1, -5), (1, 2 ** 31 - 1), (3, 3 * rows + 1), (0, -1), (2, 0), (2, -2 ** 31)):
+        st = make()
+        st.chunks.row_off[at] = value
+        expect(st, dv.EINVAL)
+    st = make()
+    q = st.queries(4)
+    want, _ = dv.cache_attention(st.cache, st.chunks, q)
+    st.chunks.table[1, 0] = -1
+    got, status = dv.cache_attention(st.cache, st.chunks, q)
+    torch.cuda.synchronize()
+    assert int(status.item()) == dv.ERANGE
+    assert torch.equal(got[:rows], want[:rows]) and torch.equal(got[2 * rows:], want[2 * rows:])
+
+
+def test_more_rows_than_max_rows_refused(dv):
+    st = Setup(dv, [4, 2], [40, 30], 2, 64, 16, "bf16", seed=12, max_rows=3)
+    q = st.queries(4)
+    got, status = dv.cache_attention(st.cache, st.chunks, q)
+    torch.cuda.synchronize()
+    assert int(status.item()) == dv.EINVAL
+    ref, tol = attention64(st, q, 64 ** -0.5)
+    assert (np.abs(f64(got)[4:] - ref[4:]) <= tol[4:]).all()
+
+
+# ------------------------------------------------------------------ as a serving loop uses them
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+def test_prompt_with_an_image_in_chunks_then_tokens(dv, kind):
+    """Two prompts with image spans: their rows are overlaid chunk by chunk, projected, written
+    to the cache and attended; then single tokens follow.  Every attention equals the
+    definition over what the cache holds, and the keys read back are those written."""
+    width, heads, kv_heads, dim, page = 512, 12, 2, 64, 16
+    n_out = (heads + 2 * kv_heads) * dim
+    g = torch.Generator().manual_seed(21)
+    w = (torch.randn((n_out, width), generator=g) / math.sqrt(width)).bfloat16().cuda()
+    bias = (0.1 * torch.randn(n_out, generator=g)).bfloat16().cuda()
+    embeds = torch.randn((12, width), generator=g).bfloat16().cuda()
+    sentinel = torch.randn((3, width), generator=g).bfloat16().cuda()
+    prompts = [torch.randn((70, width), generator=g).bfloat16().cuda() for _ in range(2)]
+    spans = [[(20, 9, 6, 0)], [(41, 6, 9, 6)]]          # 3 x 2 and 2 x 3 merged tokens
+    plan = [[(0, 33), (0, 20)], [(33, 60), (20, 70)], [(60, 70), (70, 70)], [(70, 71), (70, 71)], [(71, 72), (71, 72)]]
+    total = 80
+    st = Setup(dv, [1, 1], [total, total], kv_heads, dim, page, kind, seed=22)
+    st.spoil(math.nan)
+    ws = None
+    written = [[], []]
+    for step in plan:
+        parts, lens = [], []
+        for s, (a, b) in enumerate(step):
+            if b <= 70:
+                rows = prompts[s][a:b].clone()
+                if b > a:
+                    dv.overlay_chunk(rows, a, spans[s], embeds, sentinel)
+            else:
+                rows = torch.randn((b - a, width), generator=g).bfloat16().cuda()
+            parts.append(rows)
+            lens.append(b)
+        x = torch.cat(parts)
+        st.q, st.kv = [b - a for a, b in step], lens
+        st.off = [0, st.q[0], sum(st.q)]
+        st.rows = st.off[-1]
+        st.chunks = dv.Chunks(torch.tensor(st.off, dtype=torch.int32).cuda(),
+                              torch.tensor(lens, dtype=torch.int32).cuda(), st.table.cuda(), max(st.q))
+        qkv, lst = dv.op_linear(x, w, bias)
+        qkv = qkv.view(st.rows, heads + 2 * kv_heads, dim)
+        q, k, v = qkv[:, :heads], qkv[:, heads:heads + kv_heads], qkv[:, heads + kv_heads:]
+        status = dv.cache_write(st.cache, st.chunks, k, v)
+        out, _ = dv.cache_attention(st.cache, st.chunks, q, ws=ws, status=status)
+        torch.cuda.synchronize()
+        assert int(status.item()) == dv.OK and int(lst.item()) == dv.OK
+        ref, tol = attention64(st, q, dim ** -0.5)
+        assert (np.abs(f64(out) - ref) <= tol).all()
+        for s in range(2):
+            written[s].append(f64(k)[st.off[s]:st.off[s + 1]])
+    all_rows = dv.Chunks(torch.tensor([0, 72, 144], dtype=torch.int32).cuda(),
+                         torch.tensor([72, 72], dtype=torch.int32).cuda(), st.table.cuda(), 72)
+    rk, _, status = dv.cache_read(st.cache, all_rows, 144)
+    torch.cuda.synchronize()
+    assert int(status.item()) == dv.OK
+    for s in range(2):
+        want = np.concatenate([x for x in written[s] if len(x)])
+        if kind == "e4m3":
+            b, e = quantise(want)
+            want = E4M3[b] * 2.0 ** (e[..., None].astype(float) - 127)
+        assert np.array_equal(f64(rk)[72 * s:72 * s + 72], want)
+
+
+@pytest.mark.parametrize("rows", [1, 50])
+def test_captured_and_replayed_on_other_lengths(dv, rows):
+    """Two graphs with a workspace each, replayed at the same time on two streams
+    after their lengths, tables and queries changed."""
+    sets = []
+    for seed in (31, 32):
+        st = Setup(dv, [rows, rows], [900, 300], 2, 128, 32, "e4m3" if seed == 31 else "bf16", seed=seed)
+        q, k = st.queries(8), st.queries(2)
+        out = torch.zeros((st.rows, 8, 128), dtype=torch.bfloat16, device="cuda")
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        sets.append((st, q, k, out, status))
+    graphs, streams = [], []
+    for st, q, k, out, status in sets:
+        stream = torch.cuda.Stream()
+        graph = torch.cuda.CUDAGraph()
+        stream.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.graph(graph, stream=stream):
+            dv.cache_write(st.cache, st.chunks, k, k, status=status)
+            dv.cache_attention(st.cache, st.chunks, q, out=out, status=status)
+        graphs.append(graph)
+        streams.append(stream)
+    for lens in ([900, 300], [rows, 896], [513, rows + 1]):
+        for st, q, k, out, status in sets:
+            st.kv = lens
+            free = torch.randperm(st.n_pages, generator=st.g).int()
+            used = [-(-x // 32) for x in lens]
+            st.table.fill_(-1)
+            for s in range(2):
+                st.table[s, :used[s]] = free[sum(used[:s]):sum(used[:s + 1])]
+            st.chunks.table.copy_(st.table)
+            st.chunks.kv_len.copy_(torch.tensor(lens, dtype=torch.int32))
+            q.copy_(torch.randn(q.shape, generator=st.g))
+            k.copy_(torch.randn(k.shape, generator=st.g))
+        torch.cuda.synchronize()
+        for _ in range(3):
+            for graph, stream in zip(graphs, streams):
+                with torch.cuda.stream(stream):
+                    graph.replay()
+        torch.cuda.synchronize()
+        for st, q, k, out, status in sets:
+            assert int(status.item()) == dv.OK
+            ref, tol = attention64(st, q, 128 ** -0.5)
+            assert (np.abs(f64(out) - ref) <= tol).all()

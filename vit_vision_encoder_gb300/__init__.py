@@ -17,6 +17,7 @@ LIB_PATH = os.path.join(_HERE, "libdsvit.so")
 
 OK, EINVAL, ERANGE, ECAP, ECUDA, ETIMEOUT, ENOMEM = 0, -1, -2, -3, -4, -5, -6
 TOK_START, TOK_IMAGE, TOK_NEWLINE, TOK_END = 0, 1, 2, 3
+CACHE_BF16, CACHE_E4M3 = 0, 1
 EPI_BIAS, EPI_BIAS_GELU, EPI_BIAS_RESID, EPI_QKV_ROPE, EPI_SWIGLU = 0, 1, 2, 3, 4
 MAX_LAYERS, MAX_IMAGES, MAX_PATCHES, MAX_TOKENS = 32, 64, 9216, 1024
 NOALLOC_MAX_PATCHES, NOALLOC_SCRATCH_BYTES = 1024, 21 * 1024 * 1024
@@ -74,6 +75,17 @@ class Plan(C.Structure):
     _fields_ = [(f, C.c_int32) for f in ("H", "W", "h", "w", "Hc", "Wc", "Hr", "Wr", "y0", "x0")]
 
 
+class Cache(C.Structure):
+    _fields_ = [("k", C.c_void_p), ("v", C.c_void_p), ("k_exp", C.c_void_p), ("v_exp", C.c_void_p),
+                ("n_pages", C.c_int64), ("kv_heads", C.c_int32), ("page", C.c_int32), ("head_dim", C.c_int32),
+                ("kind", C.c_int32)]
+
+
+class ChunkArrays(C.Structure):
+    _fields_ = [("row_off", C.c_void_p), ("kv_len", C.c_void_p), ("table", C.c_void_p), ("n", C.c_int32),
+                ("table_cols", C.c_int32), ("max_rows", C.c_int32)]
+
+
 # Every symbol include/dsvit.h declares: name -> (restype, argtypes).
 _VP, _I32, _I64, _SZ, _F = C.c_void_p, C.c_int32, C.c_int64, C.c_size_t, C.c_float
 _P_I32, _P_I64 = C.POINTER(C.c_int32), C.POINTER(C.c_int64)
@@ -116,6 +128,12 @@ SIGNATURES = {
     "ds_vit_qwen_layout": (C.c_int, [_I32, _I32, _I32, _VP, _I64, _P_I32]),
     "ds_vit_preprocess_workspace_bytes": (C.c_int, [C.POINTER(Plan), C.POINTER(_SZ)]),
     "ds_vit_preprocess": (C.c_int, [C.POINTER(Plan), _VP, _VP, _VP, _SZ, _VP]),
+    "ds_vit_cache_write": (C.c_int, [C.POINTER(Cache), C.POINTER(ChunkArrays), _VP, _I64, _VP, _I64, _I64, _VP, _VP]),
+    "ds_vit_cache_read": (C.c_int, [C.POINTER(Cache), C.POINTER(ChunkArrays), _VP, _I64, _VP, _I64, _I64, _VP, _VP]),
+    "ds_vit_cache_attention_workspace_bytes": (C.c_int, [C.POINTER(Cache), C.POINTER(ChunkArrays), _I32,
+                                                         C.POINTER(_SZ)]),
+    "ds_vit_cache_attention": (C.c_int, [C.POINTER(Cache), C.POINTER(ChunkArrays), _VP, _I64, _I64, _I32, _F, _I32,
+                                         _I32, _VP, _I64, _VP, _SZ, _VP, _VP]),
 }
 
 
@@ -513,6 +531,129 @@ def overlay_chunk(chunk, chunk_begin, spans, embeds, sentinel, row_type=None):
                                    _ptr(row_type), _stream()),
           "ds_vit_overlay_chunk")
     return row_type
+
+
+# ---------------------------------------------------------------- paged K/V cache
+
+class KvCache:
+    """The pages of one layer's keys and values (ds_vit_cache): k, v CUDA
+    tensors [n_pages, kv_heads, page, head_dim], bfloat16, or uint8 (e4m3 bits)
+    with k_exp, v_exp uint8 [n_pages, kv_heads, page].  Holds its tensors."""
+
+    def __init__(self, k, v, k_exp=None, v_exp=None):
+        torch = _torch()
+        e4m3 = k.dtype != torch.bfloat16
+        held = (k, v, k_exp, v_exp) if e4m3 else (k, v)
+        for t in held:
+            if (t is None or not t.is_contiguous() or t.shape != k.shape[:t.dim()] or t.device != k.device
+                    or (e4m3 and t.dtype != torch.uint8) or (not e4m3 and t.dtype != torch.bfloat16)):
+                raise DsVitError(EINVAL, "KvCache")
+        if k.dim() != 4 or v.dim() != 4 or (e4m3 and (k_exp.dim() != 3 or v_exp.dim() != 3)):
+            raise DsVitError(EINVAL, "KvCache")
+        self.k, self.v, self.k_exp, self.v_exp = k, v, k_exp, v_exp
+        self.kv_heads, self.head_dim, self.device = k.shape[1], k.shape[3], k.device
+        self.c = Cache(k.data_ptr(), v.data_ptr(), k_exp.data_ptr() if e4m3 else None,
+                       v_exp.data_ptr() if e4m3 else None, *k.shape, CACHE_E4M3 if e4m3 else CACHE_BF16)
+        self.ref = C.byref(self.c)
+
+    @classmethod
+    def empty(cls, n_pages, kv_heads, page, head_dim, kind=CACHE_BF16, device="cuda"):
+        """A cache of new (uninitialised) pages."""
+        torch = _torch()
+        shape = (n_pages, kv_heads, page, head_dim)
+        if kind == CACHE_BF16:
+            return cls(*(torch.empty(shape, dtype=torch.bfloat16, device=device) for _ in range(2)))
+        return cls(*(torch.empty(s, dtype=torch.uint8, device=device) for s in (shape, shape, shape[:3], shape[:3])))
+
+
+class Chunks:
+    """The sequences of one call (ds_vit_chunks): int32 CUDA tensors row_off
+    [n + 1], kv_len [n] and table [n, table_cols], whose contents may change
+    between calls; max_rows bounds the rows of a sequence.  Holds its tensors."""
+
+    def __init__(self, row_off, kv_len, table, max_rows):
+        torch = _torch()
+        n = kv_len.numel()
+        for t, shape in ((row_off, (n + 1,)), (kv_len, (n,)), (table, (n, table.shape[-1]))):
+            if t.dtype != torch.int32 or tuple(t.shape) != shape or not t.is_contiguous() or t.device != table.device:
+                raise DsVitError(EINVAL, "Chunks")
+        self.row_off, self.kv_len, self.table = row_off, kv_len, table
+        self.device = table.device
+        self.c = ChunkArrays(row_off.data_ptr(), kv_len.data_ptr(), table.data_ptr(), n, table.shape[1], max_rows)
+        self.ref = C.byref(self.c)
+
+
+def _packed(t, cache, chunks, where):
+    """Row stride of a packed bf16 tensor [rows, heads, head_dim] on the cache's
+    device; its heads and their values must lie side by side."""
+    torch = _torch()
+    d = cache.head_dim
+    if (t.dtype != torch.bfloat16 or t.dim() != 3 or t.shape[2] != d or t.device != cache.device
+            or chunks.device != cache.device or (t.shape[0] > 0 and (t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != d)))):
+        raise DsVitError(EINVAL, where)
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1] * d)
+
+
+def _status_on(cache, status):
+    if status is None:
+        torch = _torch()
+        return torch.zeros(1, dtype=torch.int32, device=cache.device)
+    return status
+
+
+def cache_write(cache, chunks, k, v, status=None):
+    """Rows k, v (bf16 [rows, kv_heads, head_dim], rows may be strided) into the
+    pages (ds_vit_cache_write).  Returns ``status`` (int32 [1], zeroed here when
+    not given), which receives the first error found on the device."""
+    status = _status_on(cache, status)
+    ks, vs = _packed(k, cache, chunks, "ds_vit_cache_write"), _packed(v, cache, chunks, "ds_vit_cache_write")
+    if k.shape != v.shape or k.shape[1] != cache.kv_heads:
+        raise DsVitError(EINVAL, "ds_vit_cache_write")
+    check(lib.ds_vit_cache_write(cache.ref, chunks.ref, k.data_ptr(), ks, v.data_ptr(), vs, k.shape[0],
+                                 status.data_ptr(), _stream()), "ds_vit_cache_write")
+    return status
+
+
+def cache_read(cache, chunks, rows, out=None, status=None):
+    """The newest tokens of every sequence, as bf16 (k, v) of ``rows`` packed rows
+    (ds_vit_cache_read); ``out``: the two tensors to fill.  Returns (k, v, status)."""
+    torch = _torch()
+    status = _status_on(cache, status)
+    if out is None:
+        out = tuple(torch.empty((rows, cache.kv_heads, cache.head_dim), dtype=torch.bfloat16, device=cache.device)
+                    for _ in range(2))
+    k, v = out
+    ks, vs = _packed(k, cache, chunks, "ds_vit_cache_read"), _packed(v, cache, chunks, "ds_vit_cache_read")
+    if k.shape != v.shape or k.shape[0] != rows or k.shape[1] != cache.kv_heads:
+        raise DsVitError(EINVAL, "ds_vit_cache_read")
+    check(lib.ds_vit_cache_read(cache.ref, chunks.ref, k.data_ptr(), ks, v.data_ptr(), vs, rows, status.data_ptr(),
+                                _stream()), "ds_vit_cache_read")
+    return k, v, status
+
+
+def cache_attention(cache, chunks, q, scale=None, window=0, sinks=0, out=None, ws=None, status=None):
+    """Attention of the packed rows q (bf16 [rows, heads, head_dim], rows may be
+    strided) over the cache (ds_vit_cache_attention); scale defaults to
+    head_dim ** -0.5.  ``ws``: uint8 workspace (allocated here when not given).
+    Returns (out, status)."""
+    torch = _torch()
+    status = _status_on(cache, status)
+    rows, heads = q.shape[0], q.shape[1]
+    if out is None:
+        out = torch.empty((rows, heads, cache.head_dim), dtype=torch.bfloat16, device=cache.device)
+    qs, os_ = _packed(q, cache, chunks, "ds_vit_cache_attention"), _packed(out, cache, chunks, "ds_vit_cache_attention")
+    if out.shape != q.shape:
+        raise DsVitError(EINVAL, "ds_vit_cache_attention")
+    if ws is None:
+        nb = C.c_size_t()
+        check(lib.ds_vit_cache_attention_workspace_bytes(cache.ref, chunks.ref, heads, C.byref(nb)),
+              "ds_vit_cache_attention_workspace_bytes")
+        ws = torch.empty(nb.value, dtype=torch.uint8, device=cache.device)
+    check(lib.ds_vit_cache_attention(cache.ref, chunks.ref, q.data_ptr(), qs, rows, heads,
+                                     cache.head_dim ** -0.5 if scale is None else scale, window, sinks, out.data_ptr(),
+                                     os_, ws.data_ptr(), ws.numel(), status.data_ptr(), _stream()),
+          "ds_vit_cache_attention")
+    return out, status
 
 
 # ---------------------------------------------------------------- single kernels

@@ -1,0 +1,306 @@
+// The paged K/V cache of the prompt's language model: writing the rows of new
+// tokens, reading rows back, and the entry points (include/dsvit.h).
+//
+// Both kernels move each byte once and are bound by memory at prompt lengths,
+// by their chain of dependent loads (row -> sequence -> page -> slot) at one
+// token a sequence.  One warp takes one token: its keys and values of all
+// heads are two contiguous runs of the packed rows, read as 16-byte pieces.
+#include "cache.cuh"
+
+namespace dsvit {
+
+namespace {
+
+constexpr int kWarps = 4;     // tokens per block
+constexpr int kPieces = 4;    // 16-byte pieces in flight per lane
+
+// Quantisation of one row (a token's key or value of one head) to e4m3 with
+// a power-of-two factor: a = max |x|, e the least integer with a <= 448 2^e
+// (448 is the largest e4m3 value), at least -117 so that every value read
+// back is a normal bf16 number; q = e4m3(x 2^-e), rounded to nearest even.  In
+// the bits of a (exponent field E, mantissa M): 448 = 1.75 2^8, so
+// e + 127 = E - 8, plus 1 when M > 96.  A power of two costs no accuracy (the
+// elements are floating point) and makes the value read back exact in bf16;
+// at e = 120, where 256 2^e would be past bf16's largest number, elements end
+// at 240.
+__device__ __forceinline__ uint32_t exponent_byte(uint32_t amax_bits) {
+  const uint32_t E = amax_bits >> 7, M = amax_bits & 127u;
+  if (E == 255u) return 255u;
+  const int byte = static_cast<int>(E) - 8 + (M > 96u ? 1 : 0);
+  return static_cast<uint32_t>(byte < 10 ? 10 : byte);
+}
+
+__device__ __forceinline__ uint32_t max_abs_bits(uint4 u) {
+  // bf16 magnitudes order like their bits; NaN and infinity come out on top.
+  const uint32_t a = __vmaxu2(u.x & 0x7FFF7FFFu, u.y & 0x7FFF7FFFu);
+  const uint32_t b = __vmaxu2(u.z & 0x7FFF7FFFu, u.w & 0x7FFF7FFFu);
+  const uint32_t m = __vmaxu2(a, b);
+  return max(m & 0xFFFFu, m >> 16);
+}
+
+// Two bf16 values times f as e4m3, magnitudes at most `top`.
+__device__ __forceinline__ uint32_t e4m3x2(uint32_t two, float f, float top) {
+  const float lo = fminf(fmaxf(bf16lo(two) * f, -top), top), hi = fminf(fmaxf(bf16hi(two) * f, -top), top);
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// Every sequence's entries are checked, also those of sequences without rows.
+__device__ __forceinline__ void check_seqs(const ChunkView& b, int page_shift, int* status) {
+  const int threads = static_cast<int>(gridDim.x) * 32 * kWarps;
+  for (int s = static_cast<int>(blockIdx.x) * 32 * kWarps + threadIdx.x; s < b.n; s += threads)
+    load_seq(b, page_shift, s, status);
+}
+
+__device__ __forceinline__ bool has_row(const Seq& q, int r) {
+  return static_cast<unsigned>(r - q.row0) < static_cast<unsigned>(q.c);
+}
+
+// Lanes of D / 8 hold one row; piece i of a token is row i / (D / 8).
+template <int D, bool E4M3>
+__global__ void __launch_bounds__(32 * kWarps)
+    cache_write_kernel(const __grid_constant__ CacheView c, const __grid_constant__ ChunkView b,
+                       const bf16* __restrict__ k, int64_t k_stride, const bf16* __restrict__ v,
+                       int64_t v_stride, int* status) {
+  constexpr int kLanes = D / 8;
+  grid_dep_launch();
+  grid_dep_wait();
+  const int lane = threadIdx.x & 31;
+  const int r = static_cast<int>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
+  check_seqs(b, c.page_shift, status);
+  if (r >= b.rows) return;
+  const int per = c.kv_heads * kLanes;          // pieces of the keys; as many of the values follow
+  const uint4* kr = reinterpret_cast<const uint4*>(k + r * k_stride);
+  const uint4* vr = reinterpret_cast<const uint4*>(v + r * v_stride);
+  const int s = find_seq(b, r, lane);
+  if (s < 0) return;
+  const Seq q = load_seq(b, c.page_shift, s, status);
+  const int pos = q.kv - q.c + (r - q.row0);
+  if (!has_row(q, r) || pos < 0) return;        // refused sequence, or padding in front of position 0
+  const int64_t page = page_of(b, c, s, pos, status);
+  if (page < 0) return;
+  for (int i0 = 0; i0 < 2 * per; i0 += 32 * kPieces) {
+    uint4 u[kPieces];
+#pragma unroll
+    for (int t = 0; t < kPieces; ++t) {
+      const int i = i0 + 32 * t + lane;
+      if (i < 2 * per) u[t] = i < per ? __ldg(kr + i) : __ldg(vr + (i - per));
+    }
+#pragma unroll
+    for (int t = 0; t < kPieces; ++t) {
+      const int i = i0 + 32 * t + lane;
+      const bool is_v = i >= per;
+      const int p = is_v ? i - per : i;
+      const int64_t row = cache_row(c, page, p / kLanes, pos);
+      uint8_t* to = is_v ? c.v : c.k;
+      if constexpr (!E4M3) {
+        if (i < 2 * per) reinterpret_cast<uint4*>(to)[row * kLanes + p % kLanes] = u[t];
+      } else {
+        // A row's lanes are in or out of range together (2 per is a multiple of kLanes).
+        uint32_t a = i < 2 * per ? max_abs_bits(u[t]) : 0u;
+#pragma unroll
+        for (int o = kLanes / 2; o > 0; o >>= 1) a = max(a, __shfl_xor_sync(0xFFFFFFFFu, a, o));
+        if (i >= 2 * per) continue;
+        const uint32_t byte = exponent_byte(a);
+        uint2 w = make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu);
+        if (byte != 255u) {
+          const float f = __uint_as_float((254u - byte) << 23);   // 2^-e
+          const float top = byte == 247u ? 240.f : 448.f;
+          w.x = e4m3x2(u[t].x, f, top) | e4m3x2(u[t].y, f, top) << 16;
+          w.y = e4m3x2(u[t].z, f, top) | e4m3x2(u[t].w, f, top) << 16;
+        }
+        reinterpret_cast<uint2*>(to)[row * kLanes + p % kLanes] = w;
+        if (p % kLanes == 0) (is_v ? c.v_exp : c.k_exp)[row] = static_cast<uint8_t>(byte);
+      }
+    }
+  }
+}
+
+__device__ __forceinline__ uint32_t e4m3x2_to_bf16x2(uint32_t two, float f) {
+  const float2 x = e4m3x2_to_float2(static_cast<uint16_t>(two));
+  return pack_bf16x2(x.x * f, x.y * f);   // exact: 4 significant bits, a normal exponent
+}
+
+// The inverse: rows of the packed outputs from the pages.  Rows in front of
+// position 0 are zeros; rows behind the last sequence stay as they were.
+template <int D, bool E4M3>
+__global__ void __launch_bounds__(32 * kWarps)
+    cache_read_kernel(const __grid_constant__ CacheView c, const __grid_constant__ ChunkView b,
+                      bf16* __restrict__ k, int64_t k_stride, bf16* __restrict__ v, int64_t v_stride, int* status) {
+  constexpr int kLanes = D / 8;
+  grid_dep_launch();
+  grid_dep_wait();
+  const int lane = threadIdx.x & 31;
+  const int r = static_cast<int>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
+  check_seqs(b, c.page_shift, status);
+  if (r >= b.rows) return;
+  const int per = c.kv_heads * kLanes;
+  uint4* kr = reinterpret_cast<uint4*>(k + r * k_stride);
+  uint4* vr = reinterpret_cast<uint4*>(v + r * v_stride);
+  const int s = find_seq(b, r, lane);
+  if (s < 0) return;
+  const Seq q = load_seq(b, c.page_shift, s, status);
+  if (!has_row(q, r)) return;
+  const int pos = q.kv - q.c + (r - q.row0);
+  const int64_t page = pos < 0 ? -1 : page_of(b, c, s, pos, status);
+  if (page < 0 && pos >= 0) return;
+  for (int i0 = 0; i0 < 2 * per; i0 += 32 * kPieces) {
+    uint4 u[kPieces];
+    uint32_t byte[kPieces];
+#pragma unroll
+    for (int t = 0; t < kPieces; ++t) {
+      const int i = i0 + 32 * t + lane;
+      const bool is_v = i >= per;
+      const int p = is_v ? i - per : i;
+      u[t] = make_uint4(0, 0, 0, 0);
+      byte[t] = 127;
+      if (i < 2 * per && page >= 0) {
+        const int64_t row = cache_row(c, page, p / kLanes, pos);
+        const uint8_t* from = is_v ? c.v : c.k;
+        if constexpr (!E4M3) {
+          u[t] = reinterpret_cast<const uint4*>(from)[row * kLanes + p % kLanes];
+        } else {
+          const uint2 w = reinterpret_cast<const uint2*>(from)[row * kLanes + p % kLanes];
+          u[t].x = w.x;
+          u[t].y = w.y;
+          byte[t] = (is_v ? c.v_exp : c.k_exp)[row];
+        }
+      }
+    }
+#pragma unroll
+    for (int t = 0; t < kPieces; ++t) {
+      const int i = i0 + 32 * t + lane;
+      if (i >= 2 * per) continue;
+      uint4 w = u[t];
+      if constexpr (E4M3) {
+        const float f = exp_factor(byte[t]);
+        w = make_uint4(e4m3x2_to_bf16x2(u[t].x & 0xFFFFu, f), e4m3x2_to_bf16x2(u[t].x >> 16, f),
+                       e4m3x2_to_bf16x2(u[t].y & 0xFFFFu, f), e4m3x2_to_bf16x2(u[t].y >> 16, f));
+      }
+      if (i < per)
+        kr[i] = w;
+      else
+        vr[i - per] = w;
+    }
+  }
+}
+
+bool aligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
+
+// Checks of a cache and a chunk description (host values only); fills the
+// kernels' views.
+int check_cache(const ds_vit_cache* c, const ds_vit_chunks* b, int64_t rows, CacheView* cv, ChunkView* bv) {
+  if (!c || !b || !c->k || !c->v || !b->row_off || !b->kv_len || !b->table) return DS_VIT_EINVAL;
+  if ((c->kind != DS_VIT_CACHE_BF16 && c->kind != DS_VIT_CACHE_E4M3) || (c->head_dim != 64 && c->head_dim != 128) ||
+      c->kv_heads < 1 || c->kv_heads > DS_VIT_CACHE_MAX_HEADS || c->n_pages < 1)
+    return DS_VIT_EINVAL;
+  int shift = 4;
+  while (shift < 7 && (1 << shift) != c->page) ++shift;
+  if ((1 << shift) != c->page) return DS_VIT_EINVAL;
+  if (c->kind == DS_VIT_CACHE_E4M3 && (!c->k_exp || !c->v_exp)) return DS_VIT_EINVAL;
+  if (!aligned(c->k, 16) || !aligned(c->v, 16) || !aligned(b->row_off, 4) || !aligned(b->kv_len, 4) ||
+      !aligned(b->table, 4))
+    return DS_VIT_EINVAL;
+  if (b->n < 1 || b->n > DS_VIT_MAX_SEQS || b->table_cols < 1 || b->max_rows < 1 || rows < 0) return DS_VIT_EINVAL;
+  // Rows of the pages are TMA coordinates, and positions are int32.
+  if (c->n_pages > INT32_MAX / (c->page * c->kv_heads) || b->table_cols > INT32_MAX / c->page || rows > INT32_MAX / 2)
+    return DS_VIT_ERANGE;
+  *cv = CacheView{static_cast<uint8_t*>(c->k), static_cast<uint8_t*>(c->v), c->k_exp, c->v_exp,
+                  c->n_pages, c->kv_heads, shift};
+  *bv = ChunkView{b->row_off, b->kv_len, b->table, b->n, b->table_cols, b->max_rows, static_cast<int>(rows)};
+  return DS_VIT_OK;
+}
+
+// A packed tensor of `rows` rows, `width` values each, `stride` values apart.
+bool bad_rows(const void* p, int64_t stride, int64_t width) {
+  return !p || !aligned(p, 16) || stride < width || stride % 8 != 0;
+}
+
+int launched(cudaError_t e) {
+  if (e != cudaSuccess) cudaGetLastError();
+  return e == cudaSuccess ? DS_VIT_OK : DS_VIT_ECUDA;
+}
+
+}  // namespace
+
+}  // namespace dsvit
+
+using namespace dsvit;
+
+extern "C" {
+
+int ds_vit_cache_write(const ds_vit_cache* cache, const ds_vit_chunks* chunks, const void* k, int64_t k_stride,
+                       const void* v, int64_t v_stride, int64_t rows, int32_t* status, void* stream) {
+  CacheView c;
+  ChunkView b;
+  if (const int rc = check_cache(cache, chunks, rows, &c, &b)) return rc;
+  const int64_t width = static_cast<int64_t>(c.kv_heads) * cache->head_dim;
+  if (!status || !aligned(status, 4) || bad_rows(k, k_stride, width) || bad_rows(v, v_stride, width))
+    return DS_VIT_EINVAL;
+  if (rows == 0) return DS_VIT_OK;
+  const bool e4m3 = cache->kind == DS_VIT_CACHE_E4M3;
+  auto* fn = cache->head_dim == 128 ? (e4m3 ? cache_write_kernel<128, true> : cache_write_kernel<128, false>)
+                                    : (e4m3 ? cache_write_kernel<64, true> : cache_write_kernel<64, false>);
+  return launched(launch_pdl(fn, dim3(static_cast<unsigned>((rows + kWarps - 1) / kWarps)), dim3(32 * kWarps), 0,
+                             static_cast<cudaStream_t>(stream), c, b, static_cast<const bf16*>(k), k_stride,
+                             static_cast<const bf16*>(v), v_stride, reinterpret_cast<int*>(status)));
+}
+
+int ds_vit_cache_read(const ds_vit_cache* cache, const ds_vit_chunks* chunks, void* k, int64_t k_stride, void* v,
+                      int64_t v_stride, int64_t rows, int32_t* status, void* stream) {
+  CacheView c;
+  ChunkView b;
+  if (const int rc = check_cache(cache, chunks, rows, &c, &b)) return rc;
+  const int64_t width = static_cast<int64_t>(c.kv_heads) * cache->head_dim;
+  if (!status || !aligned(status, 4) || bad_rows(k, k_stride, width) || bad_rows(v, v_stride, width))
+    return DS_VIT_EINVAL;
+  if (rows == 0) return DS_VIT_OK;
+  const bool e4m3 = cache->kind == DS_VIT_CACHE_E4M3;
+  auto* fn = cache->head_dim == 128 ? (e4m3 ? cache_read_kernel<128, true> : cache_read_kernel<128, false>)
+                                    : (e4m3 ? cache_read_kernel<64, true> : cache_read_kernel<64, false>);
+  return launched(launch_pdl(fn, dim3(static_cast<unsigned>((rows + kWarps - 1) / kWarps)), dim3(32 * kWarps), 0,
+                             static_cast<cudaStream_t>(stream), c, b, static_cast<bf16*>(k), k_stride,
+                             static_cast<bf16*>(v), v_stride, reinterpret_cast<int*>(status)));
+}
+
+int ds_vit_cache_attention_workspace_bytes(const ds_vit_cache* cache, const ds_vit_chunks* chunks, int32_t heads,
+                                           size_t* bytes) {
+  CacheView c;
+  ChunkView b;
+  if (!bytes) return DS_VIT_EINVAL;
+  if (const int rc = check_cache(cache, chunks, 0, &c, &b)) return rc;
+  if (heads < 1 || heads % c.kv_heads != 0 || heads / c.kv_heads > DS_VIT_CACHE_MAX_GROUP) return DS_VIT_EINVAL;
+  *bytes = cache_attention_workspace(cache->head_dim, heads / c.kv_heads, b.max_rows);
+  return DS_VIT_OK;
+}
+
+int ds_vit_cache_attention(const ds_vit_cache* cache, const ds_vit_chunks* chunks, const void* q, int64_t q_stride,
+                           int64_t rows, int32_t heads, float scale, int32_t window, int32_t sinks, void* out,
+                           int64_t out_stride, void* ws, size_t ws_bytes, int32_t* status, void* stream) {
+  AttentionArgs a{};
+  if (const int rc = check_cache(cache, chunks, rows, &a.c, &a.b)) return rc;
+  if (heads < 1 || heads % a.c.kv_heads != 0 || heads / a.c.kv_heads > DS_VIT_CACHE_MAX_GROUP || !(scale > 0.f) ||
+      !(scale <= 1e30f) || window < 0 || sinks < 0)
+    return DS_VIT_EINVAL;
+  const int64_t width = static_cast<int64_t>(heads) * cache->head_dim;
+  if (!status || !aligned(status, 4) || bad_rows(q, q_stride, width) || bad_rows(out, out_stride, width) || !ws ||
+      !aligned(ws, 16))
+    return DS_VIT_EINVAL;
+  if (ws_bytes < cache_attention_workspace(cache->head_dim, heads / a.c.kv_heads, a.b.max_rows)) return DS_VIT_ECAP;
+  if (rows == 0) return DS_VIT_OK;
+  a.q = static_cast<const bf16*>(q);
+  a.q_stride = q_stride;
+  a.out = static_cast<bf16*>(out);
+  a.out_stride = out_stride;
+  a.heads = heads;
+  a.group = heads / a.c.kv_heads;
+  a.window = window;
+  a.sinks = sinks;
+  a.scale_log2 = 1.4426950408889634f * scale;
+  a.status = reinterpret_cast<int*>(status);
+  return launch_cache_attention(a, cache->head_dim, cache->kind == DS_VIT_CACHE_E4M3, ws,
+                                static_cast<cudaStream_t>(stream));
+}
+
+}  // extern "C"
