@@ -1,0 +1,100 @@
+"""The index arithmetic of the attention over the paged cache
+(csrc/cache_plan.h), compiled for the host and compared with brute force."""
+import ctypes as C
+import os
+import random
+import shutil
+import subprocess
+
+import pytest
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+SOURCE = r"""
+#include "cache_plan.h"
+using namespace dsvit;
+extern "C" {
+void blocks(int p0, int p1, int window, int sinks, int shift, int* out) {
+  const KeyBlocks b = key_blocks(p0, p1, window, sinks, shift);
+  out[0] = b.sink; out[1] = b.first; out[2] = b.count;
+}
+int block_at(int p0, int p1, int window, int sinks, int shift, int i) {
+  return key_blocks(p0, p1, window, sinks, shift).at(i);
+}
+int64_t begin(int64_t w, int64_t W, int64_t U) { return share_begin(w, W, U); }
+int64_t owner(int64_t x, int64_t W, int64_t U) { return share_of(x, W, U); }
+}
+"""
+
+
+@pytest.fixture(scope="module")
+def plan(tmp_path_factory):
+    cxx = shutil.which("g++")
+    if cxx is None:
+        pytest.skip("no g++")
+    d = tmp_path_factory.mktemp("plan")
+    src, lib = str(d / "plan.cpp"), str(d / "plan.so")
+    with open(src, "w") as f:
+        f.write(SOURCE)
+    subprocess.run([cxx, "-O1", "-std=c++17", "-fsanitize=undefined", "-fno-sanitize-recover", "-fPIC", "-shared",
+                    "-I", os.path.join(ROOT, "vit_vision_encoder_gb300", "csrc"), src, "-o", lib, "-lubsan"],
+                   check=True)
+    h = C.CDLL(lib)
+    for f in (h.begin, h.owner):
+        f.restype, f.argtypes = C.c_int64, [C.c_int64] * 3
+    return h
+
+
+def test_blocks_are_those_that_some_row_sees(plan):
+    rng = random.Random(1)
+    for _ in range(4000):
+        shift = rng.choice([4, 7])
+        c = rng.choice([1, 1, 2, 7, 60])
+        kv = rng.randrange(0, 700)
+        window = rng.choice([0, 1, 2, 16, 17, 100, 128, 300, 10 ** 9, 2 ** 31 - 1])
+        sinks = rng.choice([0, 1, 4, 16, 17, 130, 2 ** 31 - 1])
+        p0, p1 = kv - c, kv - 1
+        out = (C.c_int * 3)()
+        plan.blocks(p0, p1, window, sinks, shift, out)
+        got = [plan.block_at(p0, p1, window, sinks, shift, i) for i in range(out[2])]
+        lo = max(0, p0 - window + 1) if window else 0
+        seen = [j for j in range(kv) if j >= lo or j < sinks]
+        assert got == sorted({j >> shift for j in seen}), (p0, p1, window, sinks, shift)
+
+
+def test_blocks_at_the_ends_of_the_range(plan):
+    """No 32-bit overflow at the largest positions, windows and paddings."""
+    out = (C.c_int * 3)()
+    top = 2 ** 31 - 1
+    for p0, p1 in ((-2 ** 30, -1), (-2 ** 30, 5), (top - 1, top - 1), (0, top - 1), (-2 ** 30, top - 1)):
+        for window in (0, 1, 4096, top):
+            for sinks in (0, 5, top):
+                for shift in (4, 7):
+                    plan.blocks(p0, p1, window, sinks, shift, out)
+                    if p1 < 0:
+                        assert out[2] == 0
+                        continue
+                    lo = max(0, p0 - window + 1) if window else 0
+                    first = lo >> shift
+                    sink = min(-(-min(sinks, lo) // 2 ** shift), first)
+                    assert list(out) == [sink, first, sink + (p1 >> shift) - first + 1]
+
+
+def test_shares(plan):
+    """Every unit has one worker, shares differ by one unit at most and none is
+    empty; the largest counts do not overflow."""
+    rng = random.Random(2)
+    for _ in range(300):
+        W = rng.randrange(1, 300)
+        U = rng.randrange(W, 3000)
+        edge = [plan.begin(w, W, U) for w in range(W + 1)]
+        assert edge[0] == 0 and edge[-1] == U
+        sizes = [b - a for a, b in zip(edge, edge[1:])]
+        assert min(sizes) >= 1 and max(sizes) - min(sizes) <= 1
+        for w in range(W):
+            for x in (edge[w], edge[w + 1] - 1):
+                assert plan.owner(x, W, U) == w
+    U, W = 1024 * 128 * 2 ** 27, 1216
+    for w in (0, 1, 700, 1215):
+        x = plan.begin(w, W, U)
+        assert x == w * U // W and plan.owner(x, W, U) == w

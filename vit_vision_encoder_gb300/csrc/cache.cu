@@ -198,7 +198,8 @@ int check_cache(const ds_vit_cache* c, const ds_vit_chunks* b, int64_t rows, Cac
   int shift = 4;
   while (shift < 7 && (1 << shift) != c->page) ++shift;
   if ((1 << shift) != c->page) return DS_VIT_EINVAL;
-  if (c->kind == DS_VIT_CACHE_E4M3 && (!c->k_exp || !c->v_exp)) return DS_VIT_EINVAL;
+  if (c->kind == DS_VIT_CACHE_E4M3 && (!c->k_exp || !c->v_exp || !aligned(c->k_exp, 16) || !aligned(c->v_exp, 16)))
+    return DS_VIT_EINVAL;
   if (!aligned(c->k, 16) || !aligned(c->v, 16) || !aligned(b->row_off, 4) || !aligned(b->kv_len, 4) ||
       !aligned(b->table, 4))
     return DS_VIT_EINVAL;

@@ -70,9 +70,14 @@ __global__ void __launch_bounds__(128) row_attention_kernel(const __grid_constan
 
 }  // namespace
 
-size_t cache_attention_workspace(int head_dim, int group, int max_rows) { return 256; }
+size_t cache_attention_workspace(int head_dim, int group, int max_rows) {
+  const int64_t rows = static_cast<int64_t>(max_rows) * group;
+  return rows <= kDecodeRows ? cache_decode_workspace(head_dim, static_cast<int>(rows)) : 256;
+}
 
 int launch_cache_attention(const AttentionArgs& a, int head_dim, bool e4m3, void* ws, cudaStream_t stream) {
+  if (static_cast<int64_t>(a.b.max_rows) * a.group <= kDecodeRows)
+    return launch_cache_decode(a, head_dim, e4m3, ws, stream);
   auto* fn = head_dim == 128 ? (e4m3 ? row_attention_kernel<128, true> : row_attention_kernel<128, false>)
                              : (e4m3 ? row_attention_kernel<64, true> : row_attention_kernel<64, false>);
   const int64_t items = static_cast<int64_t>(a.b.rows) * a.heads;

@@ -52,6 +52,9 @@ bool make_tmap_bf16(CUtensorMap* map, const void* base, uint64_t rows, uint64_t 
 bool make_tmap_bf16_tail16(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols,
                            uint32_t box_rows);
 
+// A matrix of 32 columns (rows of 64 B): boxes [box_rows, 32 cols], 64-byte swizzle.
+bool make_tmap_bf16_sw64(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols, uint32_t box_rows);
+
 // Store map of a row-major bf16 output [rows, cols]: 32x32 boxes, 64-byte swizzle.
 bool make_tmap_store_bf16(CUtensorMap* map, void* base, uint64_t rows, uint64_t cols);
 
@@ -199,5 +202,9 @@ struct AttentionArgs;
 // Workspace of one call: the partial results of work split between CTAs.
 size_t cache_attention_workspace(int head_dim, int group, int max_rows);
 int launch_cache_attention(const AttentionArgs& a, int head_dim, bool e4m3, void* ws, cudaStream_t stream);
+// The path for at most kDecodeRows query rows per K/V head and sequence.
+constexpr int kDecodeRows = 32;
+size_t cache_decode_workspace(int head_dim, int rows);
+int launch_cache_decode(const AttentionArgs& a, int head_dim, bool e4m3, void* ws, cudaStream_t stream);
 
 }  // namespace dsvit
