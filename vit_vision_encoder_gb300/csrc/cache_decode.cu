@@ -18,11 +18,16 @@
 //
 // bf16: S = Q K^T with K fragments by ldmatrix, P V with V fragments by
 // ldmatrix.trans.  e4m3: a lane loads 16 bytes of a key (16 dims) or of two
-// values' rows and expands pairs to bf16 in registers: the byte's 7 low bits
-// put at bit 4 of a bf16 are the value times 2^-120, one exact multiply
-// restores it.  The order of dims within a product is free as long as both
-// operands share it, and so is the order of output columns, so a lane's bytes
-// are used where they lie.  The exponents scale scores and weights.
+// values' rows and widens pairs to fp16 in registers (one conversion a pair,
+// exact; bf16 has no such conversion, and bit operations to the same end took
+// five instructions a pair and 437 us where these take REPLACED).  The order
+// of dims within a product is free as long as both operands share it, and so is
+// the order of output columns, so a lane's bytes are used where they lie.
+// fp16's range is kept by powers of two: each query row is scaled to a largest
+// magnitude in [2^14, 2^15) (the scores are scaled back), and the weights carry
+// the values' exponents and are taken against the running maximum of score
+// plus exponent, the size of a key's contribution, so that the largest stay in
+// [2^6, 2^14]; contributions under 2^-20 of the largest lose bits.
 #include "cache_rows.cuh"
 
 namespace dsvit {
@@ -33,7 +38,13 @@ constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kBlockShift = 4;             // 16 keys
 constexpr int kRingBytes = 24 * 1024;      // per warp
-constexpr float kRescale = 8.f;            // log2 units a row's maximum may lag behind
+// A row's reference m (log2) is raised when a block's maximum passes m + kLag,
+// to kLead below that maximum; weights are 2^(x - m).
+template <bool E4M3>
+struct Reference {
+  static constexpr float kLag = E4M3 ? 14.f : 8.f;
+  static constexpr float kLead = E4M3 ? 6.f : 0.f;
+};
 
 template <int D, bool E4M3>
 struct Shape {
@@ -84,14 +95,6 @@ __device__ __forceinline__ Item item_at(const AttentionArgs& a, const Plan& pl, 
   const int64_t left = pl.end - u;
   it.end = left < it.kb.count - it.b ? it.b + static_cast<int>(left) : it.kb.count;
   return it;
-}
-
-// Two e4m3 values, given as bytes 1 and 3 of t (bytes 0 and 2 anything), as bf16.
-__device__ __forceinline__ uint32_t expand(uint32_t t) {
-  const uint32_t u = ((t >> 4) & 0x07F007F0u) | (t & 0x80008000u);
-  uint32_t r;
-  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(u), "r"(0x7B807B80u));   // 2^120
-  return r;
 }
 
 template <int D, bool E4M3, int MT>
@@ -241,6 +244,33 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
+    float qscale[MT][2];                   // scale_log2, and what scales an fp16 row back
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        qscale[mt][x] = a.scale_log2;
+        if constexpr (E4M3) {
+          uint32_t top = 0;
+#pragma unroll
+          for (int k = 0; k < kSteps; ++k)
+            top = __vmaxu2(top, __vmaxu2(qf[mt][k][x] & 0x7FFF7FFFu, qf[mt][k][2 + x] & 0x7FFF7FFFu));
+          top = max(top & 0xFFFFu, top >> 16);
+          top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+          top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+          // The largest's exponent field E: times 2^(141 - E), in two steps of normal powers of two.
+          const int E = max(static_cast<int>(top >> 7), 1), up = 141 - E, half = up / 2;
+          const float f0 = __int_as_float((127 + half) << 23), f1 = __int_as_float((127 + up - half) << 23);
+          const float g0 = __int_as_float((127 - half) << 23), g1 = __int_as_float((127 - up + half) << 23);
+          qscale[mt][x] = a.scale_log2 * g0 * g1;
+#pragma unroll
+          for (int k = 0; k < kSteps; ++k) {
+            qf[mt][k][x] = pack_f16x2(bf16lo(qf[mt][k][x]) * f0 * f1, bf16hi(qf[mt][k][x]) * f0 * f1);
+            qf[mt][k][2 + x] = pack_f16x2(bf16lo(qf[mt][k][2 + x]) * f0 * f1, bf16hi(qf[mt][k][2 + x]) * f0 * f1);
+          }
+        }
+      }
+    }
     float o[MT][kCols][4], m[MT][2], l[MT][2];
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
@@ -280,9 +310,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
-              const uint32_t b0 = expand(__byte_perm(ww[x], 0, 0x1100)), b1 = expand(__byte_perm(ww[x], 0, 0x3322));
+              const uint32_t b0 = e4m3x2_to_f16x2(ww[x] & 0xFFFFu), b1 = e4m3x2_to_f16x2(ww[x] >> 16);
 #pragma unroll
-              for (int mt = 0; mt < MT; ++mt) mma_bf16(sc[mt][n], qf[mt][4 * h + x], b0, b1);
+              for (int mt = 0; mt < MT; ++mt) mma_f16(sc[mt][n], qf[mt][4 * h + x], b0, b1);
             }
           }
         }
@@ -302,17 +332,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       // ---- softmax of the block
-      float kf[2][2], vf[2][2];
+      float kf[2][2], vf[2][2], ve[2][2];  // factors of keys and values, exponents of values
 #pragma unroll
       for (int n = 0; n < 2; ++n) {
-        kf[n][0] = kf[n][1] = a.scale_log2;
         if constexpr (E4M3) {
           const uint32_t ek = lds_u16(exps + slot * S::kExp + 8 * n + 2 * t);
           const uint32_t ev = lds_u16(exps + slot * S::kExp + 16 + 8 * n + 2 * t);
-          kf[n][0] *= exp_factor(ek & 255u);
-          kf[n][1] *= exp_factor(ek >> 8);
+          kf[n][0] = exp_factor(ek & 255u);
+          kf[n][1] = exp_factor(ek >> 8);
           vf[n][0] = exp_factor(ev & 255u);
           vf[n][1] = exp_factor(ev >> 8);
+          // byte - 127: the byte in the last bits of 2^23
+          ve[n][0] = __uint_as_float(0x4B000000u | (ev & 255u)) - 8388735.f;
+          ve[n][1] = __uint_as_float(0x4B000000u | (ev >> 8)) - 8388735.f;
         }
       }
       // Keys that every row sees: no later than the first row, inside the last row's window or all sinks.
@@ -334,26 +366,27 @@ __global__ void __launch_bounds__(kThreads, 1)
         float top[2];
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
+          top[x] = -INFINITY;
 #pragma unroll
           for (int n = 0; n < 2; ++n)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
               float& z = sc[mt][n][2 * x + e];
-              z *= kf[n][e];
+              z *= E4M3 ? qscale[mt][x] * kf[n][e] : qscale[mt][x];
               if (!open && !sees(a, pos[mt][x], key0 + 8 * n + 2 * t + e)) z = -INFINITY;
+              top[x] = fmaxf(top[x], E4M3 ? z + ve[n][e] : z);
             }
-          top[x] = fmaxf(fmaxf(sc[mt][0][2 * x], sc[mt][0][2 * x + 1]), fmaxf(sc[mt][1][2 * x], sc[mt][1][2 * x + 1]));
           top[x] = fmaxf(top[x], __shfl_xor_sync(0xFFFFFFFFu, top[x], 1));
           top[x] = fmaxf(top[x], __shfl_xor_sync(0xFFFFFFFFu, top[x], 2));
         }
-        // The maximum is raised (and O rescaled) only past kRescale, so weights stay below 2^8.
-        const bool up0 = top[0] > m[mt][0] + kRescale, up1 = top[1] > m[mt][1] + kRescale;
+        // The reference is raised (and O rescaled) rarely: weights stay below 2^kLag.
+        const bool up0 = top[0] > m[mt][0] + Reference<E4M3>::kLag, up1 = top[1] > m[mt][1] + Reference<E4M3>::kLag;
         if (__any_sync(0xFFFFFFFFu, up0 || up1)) {
           float f[2];
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
             const float old = m[mt][x];
-            if (x == 0 ? up0 : up1) m[mt][x] = top[x];
+            if (x == 0 ? up0 : up1) m[mt][x] = top[x] - Reference<E4M3>::kLead;
             f[x] = old == m[mt][x] ? 1.f : ex2_approx(old - m[mt][x]);
             l[mt][x] *= f[x];
           }
@@ -376,7 +409,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               w0 *= vf[n][0];
               w1 *= vf[n][1];
             }
-            pf[mt][2 * n + x] = pack_bf16x2(w0, w1);   // the product's operand: weights in bf16, sums in fp32
+            // The product's operand: weights in 16 bits (their sum stays in fp32).
+            pf[mt][2 * n + x] = E4M3 ? pack_f16x2(w0, w1) : pack_bf16x2(w0, w1);
           }
         }
       }
@@ -408,12 +442,17 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int y = 0; y < kCols / 4; ++y) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const uint32_t sel = static_cast<uint32_t>(e * 0x11 + (4 + e) * 0x1100);   // byte e of both rows
-            const uint32_t b0 = expand(__byte_perm(w[0][y], w[1][y], sel)) & vmask[0];
-            const uint32_t b1 = expand(__byte_perm(w[2][y], w[3][y], sel)) & vmask[1];
+          for (int e = 0; e < 4; e += 2) {
+            // Bytes e, e + 1 of both keys' words, side by side per dim.
+            const uint32_t sel = e == 0 ? 0x5140u : 0x7362u;
+            const uint32_t p0 = __byte_perm(w[0][y], w[1][y], sel), p1 = __byte_perm(w[2][y], w[3][y], sel);
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt) mma_bf16(o[mt][4 * y + e], pf[mt], b0, b1);
+            for (int z = 0; z < 2; ++z) {
+              const uint32_t b0 = e4m3x2_to_f16x2(z == 0 ? p0 & 0xFFFFu : p0 >> 16) & vmask[0];
+              const uint32_t b1 = e4m3x2_to_f16x2(z == 0 ? p1 & 0xFFFFu : p1 >> 16) & vmask[1];
+#pragma unroll
+              for (int mt = 0; mt < MT; ++mt) mma_f16(o[mt][4 * y + e + z], pf[mt], b0, b1);
+            }
           }
         }
       } else {
