@@ -1,43 +1,48 @@
-// Attention over the paged cache for few rows: at most 32 query rows (new
+// Attention over the paged cache for few rows: at most 16 query rows (new
 // tokens times query heads per K/V head) share a K/V head, as in decoding.
 //
 // Bound by the cache's bytes: each key and value is read once and meets at
-// most 32 rows, 64 flops a byte of bf16.  That is under a tenth of the tensor
-// rate the bytes could feed, so the products run as warp MMAs (m16n8k16),
-// whose fragments come straight from shared memory; what counts is bytes in
-// flight and few instructions per key.
+// most 16 rows, 32 flops a byte of bf16, a twentieth of the tensor rate the
+// bytes could feed.  So the products run as warp MMAs (m16n8k16), whose
+// fragments come straight from shared memory; what counts is bytes in flight
+// and a short chain of instructions per key.
 //
-// Work: the unit is a block of 16 keys (always inside one page) of one item
-// (sequence, K/V head).  All units of a call are counted from the lengths on
-// the device and dealt in order to the workers, the warps of the grid, in
-// equal shares (cache_plan.h), so a batch of unequal lengths and a single long
-// sequence both keep every SM reading.  A worker streams its blocks through
-// its own ring of TMA tiles, with its own barriers and running softmax; warps
-// never wait for one another.  Items that lie within one worker's share are
-// finished there, the others leave records that join_kernel adds up.
+// Work: the unit is a block of kKeys keys of one item (sequence, K/V head).
+// All units of a call are counted from the lengths on the device and dealt in
+// order to the workers, the consumer warps of the grid, in equal shares
+// (cache_plan.h), so a batch of unequal lengths and a single long sequence both
+// keep every SM reading.  A worker streams its blocks through its own ring of
+// TMA tiles with its own running softmax; consumer warps never wait for one
+// another.  One producer warp per CTA fills the rings, lane i that of warp i
+// (issued by the consumers themselves, the loads took 660 of the 2260 cycles a
+// block of 16 keys cost a warp).  A consumer takes a stage's fragments into
+// registers at once and gives the stage back before it computes.  Items that
+// lie within one worker's share are finished there, the others leave records
+// that join_kernel adds up.
 //
-// bf16: S = Q K^T with K fragments by ldmatrix, P V with V fragments by
-// ldmatrix.trans.  e4m3: a lane loads 16 bytes of a key (16 dims) or of two
-// values' rows and widens pairs to fp16 in registers (one conversion a pair,
-// exact; bf16 has no such conversion, and bit operations to the same end took
-// five instructions a pair and 437 us where these take REPLACED).  The order
-// of dims within a product is free as long as both operands share it, and so is
-// the order of output columns, so a lane's bytes are used where they lie.
-// fp16's range is kept by powers of two: each query row is scaled to a largest
-// magnitude in [2^14, 2^15) (the scores are scaled back), and the weights carry
-// the values' exponents and are taken against the running maximum of score
-// plus exponent, the size of a key's contribution, so that the largest stay in
-// [2^6, 2^14]; contributions under 2^-20 of the largest lose bits.
+// bf16: blocks of 16 keys (inside one page); S = Q K^T with K fragments by
+// ldmatrix, P V with V fragments by ldmatrix.trans.  e4m3: blocks of 32 keys; a
+// lane loads 16 bytes of a key (16 dims) or of two values' rows and widens
+// pairs to fp16 in registers (one conversion a pair, exact; bf16 has no such
+// conversion, and bit operations to the same end took five instructions a
+// pair).  The order of dims within a product is free as long as both operands
+// share it, and so is the order of output columns, so a lane's bytes are used
+// where they lie.  fp16's range is kept by powers of two: each query row is
+// scaled to a largest magnitude in [2^14, 2^15) (the scores are scaled back),
+// and the weights carry the values' exponents and are taken against the running
+// maximum of score plus exponent, the size of a key's contribution, so that the
+// largest stay in [2^6, 2^14]; contributions under 2^-20 of the largest lose
+// bits.
 #include "cache_rows.cuh"
 
 namespace dsvit {
 
 namespace {
 
-constexpr int kWarps = 8;
-constexpr int kThreads = 32 * kWarps;
-constexpr int kBlockShift = 4;             // 16 keys
-constexpr int kRingBytes = 24 * 1024;      // per warp
+constexpr int kWarps = 7;                  // consumer warps: with the producer two warps a scheduler, 255 registers each
+constexpr int kThreads = 32 * kWarps + 32;
+constexpr int kRingBytes = 24 * 1024;      // per consumer warp
+
 // A row's reference m (log2) is raised when a block's maximum passes m + kLag,
 // to kLead below that maximum; weights are 2^(x - m).
 template <bool E4M3>
@@ -48,12 +53,15 @@ struct Reference {
 
 template <int D, bool E4M3>
 struct Shape {
+  static constexpr int kKeyShift = E4M3 ? 5 : 4;
+  static constexpr int kKeys = 1 << kKeyShift;             // keys of a block
   static constexpr int kRow = E4M3 ? D : 2 * D;            // bytes of a key
-  static constexpr int kTile = 16 * kRow;
+  static constexpr int kTile = kKeys * kRow;
+  static constexpr int kPlane = kKeys * 128;               // bf16, D = 128: two planes of 64 dims
   static constexpr int kStage = 2 * kTile;                 // K, then V
   static constexpr int kStages = kRingBytes / kStage;
-  static constexpr int kExp = E4M3 ? 32 : 0;               // exponents of a stage: 16 K, 16 V
-  static constexpr int kSmem = 1024 + kWarps * (kRingBytes + kStages * (8 + kExp)) + 8 * (DS_VIT_MAX_SEQS + 1);
+  static constexpr int kExp = E4M3 ? 64 : 0;               // exponents of a stage: 32 K, 32 V
+  static constexpr int kSmem = 1024 + kWarps * (kRingBytes + kStages * (16 + kExp)) + 8 * (DS_VIT_MAX_SEQS + 1);
 };
 
 // An item and the part of its blocks that a worker takes.
@@ -69,13 +77,15 @@ struct Plan {
   int64_t begin, end;   // the worker's units
 };
 
+template <int kKeyShift>
 __device__ __forceinline__ KeyBlocks seq_blocks(const AttentionArgs& a, const Seq& q) {
-  KeyBlocks kb = key_blocks(q.kv - q.c, q.kv - 1, a.window, a.sinks, kBlockShift);
+  KeyBlocks kb = key_blocks(q.kv - q.c, q.kv - 1, a.window, a.sinks, kKeyShift);
   if (q.c > 0 && kb.count == 0) kb.count = 1;   // nothing visible: one block without keys, so that zeros get written
   return kb;
 }
 
 // The item of unit u and the worker's part of it.
+template <int kKeyShift>
 __device__ __forceinline__ Item item_at(const AttentionArgs& a, const Plan& pl, int64_t u) {
   int lo = 0, hi = a.b.n - 1;              // the last s with pre[s] <= u
   while (lo < hi) {
@@ -88,7 +98,7 @@ __device__ __forceinline__ Item item_at(const AttentionArgs& a, const Plan& pl, 
   Item it;
   it.s = lo;
   it.q = load_seq(a.b, a.c.page_shift, lo, nullptr);
-  it.kb = seq_blocks(a, it.q);
+  it.kb = seq_blocks<kKeyShift>(a, it.q);
   const int64_t r = u - pl.pre[lo];
   it.head = static_cast<int>(r / it.kb.count);
   it.b = static_cast<int>(r - static_cast<int64_t>(it.head) * it.kb.count);
@@ -97,30 +107,110 @@ __device__ __forceinline__ Item item_at(const AttentionArgs& a, const Plan& pl, 
   return it;
 }
 
-template <int D, bool E4M3, int MT>
+// The first key of the window of the row at position p.
+__device__ __forceinline__ int window_start(const AttentionArgs& a, int p) {
+  return a.window != 0 && p >= a.window ? p - a.window + 1 : 0;
+}
+
+template <bool F16>
+__device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  if constexpr (F16)
+    mma_f16(c, a, b0, b1);
+  else
+    mma_bf16(c, a, b0, b1);
+}
+
+// The producer's lane for one ring: loads the worker's blocks, a stage ahead
+// of its release at most.  Every wait is bounded; after one gives up the lane
+// stops loading and its consumer times out on its own.
+template <int D, bool E4M3>
+__device__ __forceinline__ void produce(const CUtensorMap* tm_k, const CUtensorMap* tm_v, const AttentionArgs& a,
+                                        const Plan& pl, uint32_t ring, uint32_t exps, uint32_t full, uint32_t empty) {
+  using S = Shape<D, E4M3>;
+  constexpr int kPage16 = 16;
+  const int halves = E4M3 && a.c.page_shift == 4 ? 2 : 1;   // pages of a block
+  int slot = 0;
+  uint32_t phase = 1;                      // a new barrier's preceding phase counts as complete
+  int64_t u = pl.begin;
+  while (u < pl.end) {
+    Item it = item_at<S::kKeyShift>(a, pl, u);
+    u += it.end - it.b;
+    const int p_last = it.q.kv - 1, lo = window_start(a, it.q.kv - it.q.c);
+    // Table entries are read a block ahead.  Of a block's pages only those that some row sees are needed.
+    int page[2], next[2] = {-1, -1};
+    auto look = [&](int b) {
+      const int key0 = it.kb.at(b) << S::kKeyShift;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int k0 = key0 + h * kPage16, k1 = halves == 2 ? k0 + kPage16 - 1 : key0 + S::kKeys - 1;
+        next[h] = -1;
+        if (h < halves && k0 <= p_last && (k1 >= lo || k0 < a.sinks))
+          next[h] = static_cast<int>(page_of(a.b, a.c, it.s, k0, a.status));
+      }
+    };
+    look(it.b);
+    for (; it.b < it.end; ++it.b) {
+      page[0] = next[0];
+      page[1] = next[1];
+      if (it.b + 1 < it.end) look(it.b + 1);
+      if (!mbar_wait(empty + 8 * slot, phase, a.status)) return;
+      const uint32_t bar = full + 8 * slot, to = ring + slot * S::kStage, ex = exps + slot * S::kExp;
+      const int key0 = it.kb.at(it.b) << S::kKeyShift;
+      const uint32_t per = (S::kStage + S::kExp) / halves;
+      mbar_expect_tx(bar, per * ((page[0] >= 0) + (page[1] >= 0)));
+#pragma unroll
+      for (int h = 0; h < (E4M3 ? 2 : 1); ++h) {
+        if (page[h] < 0) continue;
+        const int row = static_cast<int>(cache_row(a.c, page[h], it.head, key0 + h * kPage16));
+        if constexpr (E4M3) {
+          tma_load_2d(to + h * kPage16 * S::kRow, tm_k, bar, 0, row);
+          tma_load_2d(to + S::kTile + h * kPage16 * S::kRow, tm_v, bar, 0, row);
+          bulk_load(ex + h * kPage16, a.c.k_exp + row, 32 / halves, bar);
+          bulk_load(ex + 32 + h * kPage16, a.c.v_exp + row, 32 / halves, bar);
+        } else {
+#pragma unroll
+          for (int x = 0; x < D / 64; ++x) {
+            tma_load_2d(to + S::kPlane * x, tm_k, bar, 64 * x, row);
+            tma_load_2d(to + S::kTile + S::kPlane * x, tm_v, bar, 64 * x, row);
+          }
+        }
+      }
+      if (++slot == S::kStages) {
+        slot = 0;
+        phase ^= 1;
+      }
+    }
+  }
+}
+
+// kRowHalves: 1 when at most 8 rows share a K/V head (rows 8 .. 15 of the
+// MMAs' 16 are then zeros nobody looks at), else 2.
+template <int D, bool E4M3, int kRowHalves>
 __global__ void __launch_bounds__(kThreads, 1)
     decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                   const __grid_constant__ AttentionArgs a, const Records rec) {
   using S = Shape<D, E4M3>;
-  constexpr int kSteps = D / 16;           // k steps of S, and half the column tiles of O
+  constexpr int kSteps = D / 16;           // k steps of S
   constexpr int kCols = D / 8;             // column tiles of O
+  constexpr int kN = S::kKeys / 8;         // column tiles of S
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
-  const uint32_t ring = smem_u32(smem) + warp * kRingBytes;
-  uint8_t* tail = smem + kWarps * kRingBytes;
-  const uint32_t exps = smem_u32(tail) + warp * S::kStages * S::kExp;
-  tail += kWarps * S::kStages * S::kExp;
-  const uint32_t bar0 = smem_u32(tail) + warp * S::kStages * 8;
-  tail += kWarps * S::kStages * 8;
-  int64_t* pre = reinterpret_cast<int64_t*>(tail);
-  __shared__ int64_t part[kWarps];
+  // Per ring: tiles, exponents, full and empty barriers.
+  const uint32_t rings = smem_u32(smem);
+  const uint32_t exps0 = rings + kWarps * kRingBytes;
+  const uint32_t bars0 = exps0 + kWarps * S::kStages * S::kExp;
+  int64_t* pre = reinterpret_cast<int64_t*>(smem + kWarps * (kRingBytes + S::kStages * (S::kExp + 16)));
+  auto full_of = [&](int w) { return bars0 + w * S::kStages * 16; };
+  auto empty_of = [&](int w) { return full_of(w) + S::kStages * 8; };
+  __shared__ int64_t part[kWarps + 1];
 
-  if (lane == 0) {
-    for (int i = 0; i < S::kStages; ++i) mbar_init(bar0 + 8 * i, 1);
-    if (warp == 0) {
+  if (warp == kWarps) {
+    if (lane < kWarps)
+      for (int i = 0; i < 2 * S::kStages; ++i) mbar_init(full_of(lane) + 8 * i, 1);
+    if (lane == 0) {
       prefetch_tensormap(&tm_k);
       prefetch_tensormap(&tm_v);
     }
@@ -136,7 +226,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int64_t x = 0;
     if (s < a.b.n) {
       const Seq q = load_seq(a.b, a.c.page_shift, s, blockIdx.x == 0 ? a.status : nullptr);
-      x = static_cast<int64_t>(seq_blocks(a, q).count) * (q.c > 0 ? a.c.kv_heads : 0);
+      x = static_cast<int64_t>(seq_blocks<S::kKeyShift>(a, q).count) * (q.c > 0 ? a.c.kv_heads : 0);
     }
     int64_t inc = x;
 #pragma unroll
@@ -147,7 +237,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 31) part[warp] = inc;
     __syncthreads();
     int64_t before = total;
-    for (int w = 0; w < kWarps; ++w) {
+    for (int w = 0; w <= kWarps; ++w) {
       if (w < warp) before += part[w];
       total += part[w];
     }
@@ -159,395 +249,353 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   const int64_t all = static_cast<int64_t>(gridDim.x) * kWarps;
   const int64_t W = total < all ? total : all;
-  const int64_t me = static_cast<int64_t>(warp) * gridDim.x + blockIdx.x;
+  // Neighbouring shares go to different SMs.
+  auto worker = [&](int w) { return static_cast<int64_t>(w) * gridDim.x + blockIdx.x; };
+  if (warp == kWarps) {
+    if (lane < kWarps && worker(lane) < W) {
+      const Plan pl{pre, share_begin(worker(lane), W, total), share_begin(worker(lane) + 1, W, total)};
+      produce<D, E4M3>(&tm_k, &tm_v, a, pl, rings + lane * kRingBytes, exps0 + lane * S::kStages * S::kExp,
+                       full_of(lane), empty_of(lane));
+    }
+    return;
+  }
+  const int64_t me = worker(warp);
   if (me >= W) {
-    if (lane == 0) rec.headers[me] = SplitHeader{0, 0, 0, 0};
+    if (lane == 0) rec.headers[me] = SplitHeader{};
     return;
   }
   const Plan pl{pre, share_begin(me, W, total), share_begin(me + 1, W, total)};
-
-  // ---- the ring: lane 0 loads blocks, kStages ahead of their use
-  int64_t load_u = pl.begin;
-  Item ld = item_at(a, pl, load_u);
-  int pg = 0, pg_from = -32;               // table entries of blocks pg_from + lane of ld
-  int slot_ld = 0;
-  auto load_next = [&]() {
-    if (load_u >= pl.end) return;
-    if (ld.b >= ld.end) {
-      ld = item_at(a, pl, load_u);
-      pg_from = -32;
-    }
-    if (ld.b >= pg_from + 32 || pg_from < 0) {
-      pg_from = ld.b;
-      const int b = ld.b + lane;
-      pg = -1;
-      if (b < ld.end && ld.q.kv > ld.kb.at(b) << kBlockShift)
-        pg = static_cast<int>(page_of(a.b, a.c, ld.s, ld.kb.at(b) << kBlockShift, a.status));
-    }
-    const int page = __shfl_sync(0xFFFFFFFFu, pg, ld.b - pg_from);
-    if (lane == 0) {
-      const uint32_t bar = bar0 + 8 * slot_ld, to = ring + slot_ld * S::kStage;
-      if (page < 0) {
-        mbar_arrive(bar);                  // no such page (reported), or an item without keys
-      } else {
-        const int row = static_cast<int>(cache_row(a.c, page, ld.head, ld.kb.at(ld.b) << kBlockShift));
-        mbar_expect_tx(bar, S::kStage + S::kExp);
-        if constexpr (E4M3) {
-          tma_load_2d(to, &tm_k, bar, 0, row);
-          bulk_load(exps + slot_ld * S::kExp, a.c.k_exp + row, 16, bar);
-          tma_load_2d(to + S::kTile, &tm_v, bar, 0, row);
-          bulk_load(exps + slot_ld * S::kExp + 16, a.c.v_exp + row, 16, bar);
-        } else {
-#pragma unroll
-          for (int x = 0; x < D / 64; ++x) {
-            tma_load_2d(to + 2048 * x, &tm_k, bar, 64 * x, row);
-            tma_load_2d(to + S::kTile + 2048 * x, &tm_v, bar, 64 * x, row);
-          }
-        }
-      }
-    }
-    ++ld.b;
-    ++load_u;
-    if (++slot_ld == S::kStages) slot_ld = 0;
-  };
-  for (int i = 0; i < S::kStages; ++i) load_next();
+  const uint32_t ring = rings + warp * kRingBytes, exps = exps0 + warp * S::kStages * S::kExp;
+  const uint32_t full = full_of(warp), empty = empty_of(warp);
 
   // ---- the worker's items
   int slot = 0;
   uint32_t phase = 0;
-  SplitHeader header{0, 0, 0, 0};
-  bool ok = true;
-  int64_t used_u = pl.begin;               // blocks used so far
+  SplitHeader header{};
+  bool dead = false;                       // a wait gave up
   for (int64_t u = pl.begin; u < pl.end;) {
-    const Item it = item_at(a, pl, u);
+    const Item it = item_at<S::kKeyShift>(a, pl, u);
     const int R = it.q.c * a.group;
-    // Q fragments and positions of rows g, g + 8 of each row tile.
-    uint32_t qf[MT][kSteps][4];
-    int pos[MT][2];
+    // Q fragments and positions of rows g, g + 8; what scales an fp16 row's scores back, times scale_log2.
+    uint32_t qf[kSteps][4];
+    int pos[kRowHalves];
+    float qscale[kRowHalves];
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
+    for (int x = 0; x < 2; ++x) {
+      const int rho = 8 * x + g;
+      const int i = rho / a.group;
+      const bool on = x < kRowHalves && rho < R;
+      const uint32_t* src = reinterpret_cast<const uint32_t*>(
+          a.q + (it.q.row0 + i) * a.q_stride + (it.head * a.group + rho - i * a.group) * D);
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const int rho = 16 * mt + 8 * x + g;
-        const int i = rho / a.group;
-        pos[mt][x] = rho < R ? it.q.kv - it.q.c + i : -1;
-        const uint32_t* src = reinterpret_cast<const uint32_t*>(
-            a.q + (it.q.row0 + i) * a.q_stride + (it.head * a.group + rho - i * a.group) * D);
+      for (int k = 0; k < kSteps; ++k) {
+        // Dims of the k step held by this lane: 2t, 2t + 1 and 2t + 8, 2t + 9
+        // of 16, or (e4m3) four consecutive ones of its 16-byte piece.
+        const int d0 = E4M3 ? 16 * (D == 128 ? 2 * t + (k >> 2) : t) + 4 * (k & 3) : 16 * k + 2 * t;
+        const int d1 = E4M3 ? d0 + 2 : d0 + 8;
+        qf[k][x] = on ? __ldg(src + d0 / 2) : 0u;
+        qf[k][2 + x] = on ? __ldg(src + d1 / 2) : 0u;
+      }
+      if (x >= kRowHalves) continue;
+      pos[x] = on ? it.q.kv - it.q.c + i : -1;
+      qscale[x] = a.scale_log2;
+      if constexpr (E4M3) {
+        uint32_t top = 0;
+#pragma unroll
+        for (int k = 0; k < kSteps; ++k)
+          top = __vmaxu2(top, __vmaxu2(qf[k][x] & 0x7FFF7FFFu, qf[k][2 + x] & 0x7FFF7FFFu));
+        top = max(top & 0xFFFFu, top >> 16);
+        top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+        top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+        // The largest's exponent field E: times 2^(141 - E), in two steps of normal powers of two.
+        const int E = max(static_cast<int>(top >> 7), 1), up = 141 - E, half = up / 2;
+        const float f0 = __int_as_float((127 + half) << 23), f1 = __int_as_float((127 + up - half) << 23);
+        const float g0 = __int_as_float((127 - half) << 23), g1 = __int_as_float((127 - up + half) << 23);
+        qscale[x] = a.scale_log2 * g0 * g1;
 #pragma unroll
         for (int k = 0; k < kSteps; ++k) {
-          // Dims of the k step held by this lane: 2t, 2t + 1 and 2t + 8, 2t + 9
-          // of 16, or (e4m3) four consecutive ones of its 16-byte piece.
-          const int d0 = E4M3 ? 16 * (D == 128 ? 2 * t + (k >> 2) : t) + 4 * (k & 3) : 16 * k + 2 * t;
-          const int d1 = E4M3 ? d0 + 2 : d0 + 8;
-          qf[mt][k][x] = rho < R ? __ldg(src + d0 / 2) : 0u;
-          qf[mt][k][2 + x] = rho < R ? __ldg(src + d1 / 2) : 0u;
+          qf[k][x] = pack_f16x2(bf16lo(qf[k][x]) * f0 * f1, bf16hi(qf[k][x]) * f0 * f1);
+          qf[k][2 + x] = pack_f16x2(bf16lo(qf[k][2 + x]) * f0 * f1, bf16hi(qf[k][2 + x]) * f0 * f1);
         }
       }
     }
-    float qscale[MT][2];                   // scale_log2, and what scales an fp16 row back
+    float o[kCols][4], m[kRowHalves], l[kRowHalves];
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        qscale[mt][x] = a.scale_log2;
-        if constexpr (E4M3) {
-          uint32_t top = 0;
-#pragma unroll
-          for (int k = 0; k < kSteps; ++k)
-            top = __vmaxu2(top, __vmaxu2(qf[mt][k][x] & 0x7FFF7FFFu, qf[mt][k][2 + x] & 0x7FFF7FFFu));
-          top = max(top & 0xFFFFu, top >> 16);
-          top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
-          top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
-          // The largest's exponent field E: times 2^(141 - E), in two steps of normal powers of two.
-          const int E = max(static_cast<int>(top >> 7), 1), up = 141 - E, half = up / 2;
-          const float f0 = __int_as_float((127 + half) << 23), f1 = __int_as_float((127 + up - half) << 23);
-          const float g0 = __int_as_float((127 - half) << 23), g1 = __int_as_float((127 - up + half) << 23);
-          qscale[mt][x] = a.scale_log2 * g0 * g1;
-#pragma unroll
-          for (int k = 0; k < kSteps; ++k) {
-            qf[mt][k][x] = pack_f16x2(bf16lo(qf[mt][k][x]) * f0 * f1, bf16hi(qf[mt][k][x]) * f0 * f1);
-            qf[mt][k][2 + x] = pack_f16x2(bf16lo(qf[mt][k][2 + x]) * f0 * f1, bf16hi(qf[mt][k][2 + x]) * f0 * f1);
-          }
-        }
-      }
+    for (int x = 0; x < kRowHalves; ++x) {
+      m[x] = -INFINITY;
+      l[x] = 0.f;
     }
-    float o[MT][kCols][4], m[MT][2], l[MT][2];
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-      m[mt][0] = m[mt][1] = -INFINITY;
-      l[mt][0] = l[mt][1] = 0.f;
+    for (int n = 0; n < kCols; ++n)
 #pragma unroll
-      for (int n = 0; n < kCols; ++n)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o[mt][n][e] = 0.f;
-    }
+      for (int e = 0; e < 4; ++e) o[n][e] = 0.f;
     const int p_first = it.q.kv - it.q.c, p_last = it.q.kv - 1;
-    // First keys of the first and the last row's windows.
-    const int lo_first = a.window != 0 && p_first >= a.window ? p_first - a.window + 1 : 0;
-    const int lo_last = a.window != 0 && p_last >= a.window ? p_last - a.window + 1 : 0;
+    const int lo_first = window_start(a, p_first), lo_last = window_start(a, p_last);
 
     for (int b = it.b; b < it.end; ++b) {
-      const uint32_t bar = bar0 + 8 * slot, tk = ring + slot * S::kStage, tv = tk + S::kTile;
-      const int key0 = it.kb.at(b) << kBlockShift;
-      ok = __all_sync(0xFFFFFFFFu, mbar_wait(bar, phase, a.status));
-      if (!ok) break;
-      // ---- S = Q K^T, 16 rows x 16 keys per row tile
-      float sc[MT][2][4];
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-        for (int n = 0; n < 2; ++n)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) sc[mt][n][e] = 0.f;
+      const uint32_t tk = ring + slot * S::kStage, tv = tk + S::kTile, ex = exps + slot * S::kExp;
+      const int key0 = it.kb.at(b) << S::kKeyShift;
+      // Every row sees all keys of the block.
+      const bool open = key0 + S::kKeys - 1 <= p_first && (key0 >= lo_last || key0 + S::kKeys <= a.sinks);
+      auto any = [&](int j) { return j <= p_last && (j >= lo_first || j < a.sinks); };   // some row sees key j
+      dead |= !mbar_wait(full + 8 * slot, phase, a.status);
+      if (!open) {
+        // Values that no row sees (behind the last token, before every window)
+        // may be anything: zeros take their place, in the tile and (below) as weights.
+#pragma unroll 1
+        for (int x = lane; x < S::kTile / 16; x += 32) {
+          const int row = E4M3 ? x / (S::kRow / 16) : (x >> 3) & (S::kKeys - 1);
+          if (!any(key0 + row)) sts128(tv + 16 * x, make_uint4(0, 0, 0, 0));
+        }
+        fence_proxy_async_smem();          // before the loads that will follow into the tile
+        __syncwarp();
+      }
+      // ---- the block's fragments, all at once; then the stage is free again
+      constexpr int kWords = E4M3 ? D / 4 : D / 4;
+      uint32_t kw[kWords], vw[kWords], ke[kN], ve[kN];
       if constexpr (E4M3) {
+        // kw[n * kSteps + 4 h + x]: word x of piece h of key 8n + g
 #pragma unroll
-        for (int n = 0; n < 2; ++n) {
+        for (int n = 0; n < kN; ++n) {
           const int row = 8 * n + g;
 #pragma unroll
           for (int h = 0; h < D / 64; ++h) {
             const uint32_t piece = D == 128 ? (2 * t + h) ^ (row & 7) : t ^ ((row >> 1) & 3);
             const uint4 w = lds128(tk + row * S::kRow + piece * 16);
-            const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              const uint32_t b0 = e4m3x2_to_f16x2(ww[x] & 0xFFFFu), b1 = e4m3x2_to_f16x2(ww[x] >> 16);
-#pragma unroll
-              for (int mt = 0; mt < MT; ++mt) mma_f16(sc[mt][n], qf[mt][4 * h + x], b0, b1);
-            }
+            const int x = n * kSteps + 4 * h;
+            kw[x] = w.x, kw[x + 1] = w.y, kw[x + 2] = w.z, kw[x + 3] = w.w;
           }
         }
-      } else {
-        const int row = (lane & 7) + ((lane >> 4) << 3);
-        const uint32_t at = tk + row * 128;
 #pragma unroll
-        for (int k = 0; k < kSteps; ++k) {
-          uint32_t f[4];
-          const int piece = 2 * (k & 3) + ((lane >> 3) & 1);
-          ldmatrix_x4(at + (k >> 2) * 2048 + ((piece ^ (row & 7)) << 4), f);
-#pragma unroll
-          for (int mt = 0; mt < MT; ++mt) {
-            mma_bf16(sc[mt][0], qf[mt][k], f[0], f[1]);
-            mma_bf16(sc[mt][1], qf[mt][k], f[2], f[3]);
-          }
+        for (int n = 0; n < kN; ++n) {
+          ke[n] = lds_u16(ex + 8 * n + 2 * t);
+          ve[n] = lds_u16(ex + 32 + 8 * n + 2 * t);
         }
-      }
-      // ---- softmax of the block
-      float kf[2][2], vf[2][2], ve[2][2];  // factors of keys and values, exponents of values
+        // vw[(y * kN + n) * 2 + x]: word y of the row of key 8n + 2t + x
 #pragma unroll
-      for (int n = 0; n < 2; ++n) {
-        if constexpr (E4M3) {
-          const uint32_t ek = lds_u16(exps + slot * S::kExp + 8 * n + 2 * t);
-          const uint32_t ev = lds_u16(exps + slot * S::kExp + 16 + 8 * n + 2 * t);
-          kf[n][0] = exp_factor(ek & 255u);
-          kf[n][1] = exp_factor(ek >> 8);
-          vf[n][0] = exp_factor(ev & 255u);
-          vf[n][1] = exp_factor(ev >> 8);
-          // byte - 127: the byte in the last bits of 2^23
-          ve[n][0] = __uint_as_float(0x4B000000u | (ev & 255u)) - 8388735.f;
-          ve[n][1] = __uint_as_float(0x4B000000u | (ev >> 8)) - 8388735.f;
-        }
-      }
-      // Keys that every row sees: no later than the first row, inside the last row's window or all sinks.
-      const bool open = key0 + 15 <= p_first && (key0 >= lo_last || key0 + 16 <= a.sinks);
-      uint32_t vmask[2] = {0xFFFFFFFFu, 0xFFFFFFFFu};
-      if (!open) {
-        // Values that no row sees (behind the last token, before every window)
-        // may be anything: zeros stand in for them.
-        auto any = [&](int j) { return j <= p_last && (j >= lo_first || j < a.sinks); };
-#pragma unroll
-        for (int n = 0; n < 2; ++n) {
-          const int j = key0 + 8 * n + 2 * t;
-          vmask[n] = (any(j) ? 0xFFFFu : 0u) | (any(j + 1) ? 0xFFFF0000u : 0u);
-        }
-      }
-      uint32_t pf[MT][4];
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt) {
-        float top[2];
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          top[x] = -INFINITY;
-#pragma unroll
-          for (int n = 0; n < 2; ++n)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              float& z = sc[mt][n][2 * x + e];
-              z *= E4M3 ? qscale[mt][x] * kf[n][e] : qscale[mt][x];
-              if (!open && !sees(a, pos[mt][x], key0 + 8 * n + 2 * t + e)) z = -INFINITY;
-              top[x] = fmaxf(top[x], E4M3 ? z + ve[n][e] : z);
-            }
-          top[x] = fmaxf(top[x], __shfl_xor_sync(0xFFFFFFFFu, top[x], 1));
-          top[x] = fmaxf(top[x], __shfl_xor_sync(0xFFFFFFFFu, top[x], 2));
-        }
-        // The reference is raised (and O rescaled) rarely: weights stay below 2^kLag.
-        const bool up0 = top[0] > m[mt][0] + Reference<E4M3>::kLag, up1 = top[1] > m[mt][1] + Reference<E4M3>::kLag;
-        if (__any_sync(0xFFFFFFFFu, up0 || up1)) {
-          float f[2];
+        for (int n = 0; n < kN; ++n) {
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
-            const float old = m[mt][x];
-            if (x == 0 ? up0 : up1) m[mt][x] = top[x] - Reference<E4M3>::kLead;
-            f[x] = old == m[mt][x] ? 1.f : ex2_approx(old - m[mt][x]);
-            l[mt][x] *= f[x];
-          }
-#pragma unroll
-          for (int n = 0; n < kCols; ++n) {
-            o[mt][n][0] *= f[0];
-            o[mt][n][1] *= f[0];
-            o[mt][n][2] *= f[1];
-            o[mt][n][3] *= f[1];
-          }
-        }
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const float base = m[mt][x] == -INFINITY ? 0.f : m[mt][x];
-#pragma unroll
-          for (int n = 0; n < 2; ++n) {
-            float w0 = ex2_approx(sc[mt][n][2 * x] - base), w1 = ex2_approx(sc[mt][n][2 * x + 1] - base);
-            l[mt][x] += w0 + w1;
-            if constexpr (E4M3) {
-              w0 *= vf[n][0];
-              w1 *= vf[n][1];
-            }
-            // The product's operand: weights in 16 bits (their sum stays in fp32).
-            pf[mt][2 * n + x] = E4M3 ? pack_f16x2(w0, w1) : pack_bf16x2(w0, w1);
-          }
-        }
-      }
-      // ---- O += P V
-      if constexpr (E4M3) {
-        if (!open) {
-          // Such a value's exponent may be the NaN byte: the weight is zero, not NaN.
-#pragma unroll
-          for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-            for (int x = 0; x < 4; ++x) pf[mt][x] &= vmask[x >> 1];
-        }
-        uint32_t w[4][4];
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          const int row = 8 * (x >> 1) + 2 * t + (x & 1);
-          if constexpr (D == 128) {
-            const uint4 v = lds128(tv + row * S::kRow + ((g ^ (row & 7)) << 4));
-            w[x][0] = v.x;
-            w[x][1] = v.y;
-            w[x][2] = v.z;
-            w[x][3] = v.w;
-          } else {
-            const uint2 v = lds64(tv + row * S::kRow + (((g >> 1) ^ ((row >> 1) & 3)) << 4) + 8 * (g & 1));
-            w[x][0] = v.x;
-            w[x][1] = v.y;
-          }
-        }
-#pragma unroll
-        for (int y = 0; y < kCols / 4; ++y) {
-#pragma unroll
-          for (int e = 0; e < 4; e += 2) {
-            // Bytes e, e + 1 of both keys' words, side by side per dim.
-            const uint32_t sel = e == 0 ? 0x5140u : 0x7362u;
-            const uint32_t p0 = __byte_perm(w[0][y], w[1][y], sel), p1 = __byte_perm(w[2][y], w[3][y], sel);
-#pragma unroll
-            for (int z = 0; z < 2; ++z) {
-              const uint32_t b0 = e4m3x2_to_f16x2(z == 0 ? p0 & 0xFFFFu : p0 >> 16) & vmask[0];
-              const uint32_t b1 = e4m3x2_to_f16x2(z == 0 ? p1 & 0xFFFFu : p1 >> 16) & vmask[1];
-#pragma unroll
-              for (int mt = 0; mt < MT; ++mt) mma_f16(o[mt][4 * y + e + z], pf[mt], b0, b1);
+            const int row = 8 * n + 2 * t + x;
+            if constexpr (D == 128) {
+              const uint4 v = lds128(tv + row * S::kRow + ((g ^ (row & 7)) << 4));
+              vw[n * 2 + x] = v.x, vw[(kN + n) * 2 + x] = v.y, vw[(2 * kN + n) * 2 + x] = v.z,
+                         vw[(3 * kN + n) * 2 + x] = v.w;
+            } else {
+              const uint2 v = lds64(tv + row * S::kRow + (((g >> 1) ^ ((row >> 1) & 3)) << 4) + 8 * (g & 1));
+              vw[n * 2 + x] = v.x, vw[(kN + n) * 2 + x] = v.y;
             }
           }
         }
       } else {
-        const int row = lane & 15;
-        const uint32_t at = tv + row * 128;
+        const int kr = (lane & 7) + ((lane >> 4) << 3), vr = lane & 15;
+#pragma unroll
+        for (int k = 0; k < kSteps; ++k) {
+          const int piece = 2 * (k & 3) + ((lane >> 3) & 1);
+          ldmatrix_x4(tk + kr * 128 + (k >> 2) * S::kPlane + ((piece ^ (kr & 7)) << 4),
+                      *reinterpret_cast<uint32_t(*)[4]>(kw + 4 * k));
+        }
 #pragma unroll
         for (int n = 0; n < kCols; n += 2) {
-          uint32_t f[4];
           const int piece = (n & 7) + (lane >> 4);
-          ldmatrix_x4_trans(at + (n >> 3) * 2048 + ((piece ^ (row & 7)) << 4), f);
-#pragma unroll
-          for (int mt = 0; mt < MT; ++mt) {
-            mma_bf16(o[mt][n], pf[mt], f[0] & vmask[0], f[1] & vmask[1]);
-            mma_bf16(o[mt][n + 1], pf[mt], f[2] & vmask[0], f[3] & vmask[1]);
-          }
+          ldmatrix_x4_trans(tv + vr * 128 + (n >> 3) * S::kPlane + ((piece ^ (vr & 7)) << 4),
+                            *reinterpret_cast<uint32_t(*)[4]>(vw + 2 * n));
         }
       }
-      __syncwarp();                        // the stage has been read by every lane
-      load_next();
-      ++used_u;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(empty + 8 * slot);
       if (++slot == S::kStages) {
         slot = 0;
         phase ^= 1;
       }
+      // ---- S = Q K^T, 16 rows x kKeys keys
+      float sc[kN][4];
+#pragma unroll
+      for (int n = 0; n < kN; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sc[n][e] = 0.f;
+#pragma unroll
+      for (int k = 0; k < kSteps; ++k)
+#pragma unroll
+        for (int n = 0; n < kN; ++n) {
+          if constexpr (E4M3) {
+            const uint32_t w = kw[n * kSteps + k];
+            mma<true>(sc[n], qf[k], e4m3x2_to_f16x2(w & 0xFFFFu), e4m3x2_to_f16x2(w >> 16));
+          } else {
+            mma<false>(sc[n], qf[k], kw[4 * k + 2 * n], kw[4 * k + 2 * n + 1]);
+          }
+        }
+      // ---- softmax of the block: scores z = sc f (log2 units), f the scale and
+      // the key's factor; contributions z + the value's exponent
+      float f[kRowHalves][kN][2], add[kN][2], vf[kN][2], top[kRowHalves];
+#pragma unroll
+      for (int n = 0; n < kN; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float kf = 1.f;
+          add[n][e] = 0.f;
+          vf[n][e] = 1.f;
+          if constexpr (E4M3) {
+            // Rows with the NaN byte hold NaN elements, so plain shifts do for the factors.
+            const uint32_t kb = e == 0 ? ke[n] & 255u : ke[n] >> 8, vb = e == 0 ? ve[n] & 255u : ve[n] >> 8;
+            kf = __uint_as_float(kb << 23);
+            vf[n][e] = __uint_as_float(vb << 23);
+            add[n][e] = __uint_as_float(0x4B000000u | vb) - 8388735.f;   // byte - 127: the byte in the last bits of 2^23
+          }
+#pragma unroll
+          for (int x = 0; x < kRowHalves; ++x) f[x][n][e] = E4M3 ? qscale[x] * kf : qscale[x];
+        }
+#pragma unroll
+      for (int x = 0; x < kRowHalves; ++x) {
+        if (!open) {
+#pragma unroll
+          for (int n = 0; n < kN; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              if (!sees(a, pos[x], key0 + 8 * n + 2 * t + e)) {
+                sc[n][2 * x + e] = -INFINITY;      // with a factor of 1, whatever the key's is
+                f[x][n][e] = 1.f;
+              }
+        }
+        top[x] = -INFINITY;
+#pragma unroll
+        for (int n = 0; n < kN; ++n)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) top[x] = fmaxf(top[x], fmaf(sc[n][2 * x + e], f[x][n][e], add[n][e]));
+        top[x] = fmaxf(top[x], __shfl_xor_sync(0xFFFFFFFFu, top[x], 1));
+        top[x] = fmaxf(top[x], __shfl_xor_sync(0xFFFFFFFFu, top[x], 2));
+      }
+      // The reference is raised (and O rescaled) rarely: weights stay below 2^kLag.
+      bool up[kRowHalves], some = dead;
+#pragma unroll
+      for (int x = 0; x < kRowHalves; ++x) some |= up[x] = top[x] > m[x] + Reference<E4M3>::kLag;
+      if (__any_sync(0xFFFFFFFFu, some)) {
+        if (__any_sync(0xFFFFFFFFu, dead)) {
+          dead = true;
+          break;
+        }
+#pragma unroll
+        for (int x = 0; x < kRowHalves; ++x) {
+          const float old = m[x];
+          if (up[x]) m[x] = top[x] - Reference<E4M3>::kLead;
+          const float s = old == m[x] ? 1.f : ex2_approx(old - m[x]);
+          l[x] *= s;
+#pragma unroll
+          for (int n = 0; n < kCols; ++n) {
+            o[n][2 * x] *= s;
+            o[n][2 * x + 1] *= s;
+          }
+        }
+      }
+      uint32_t pf[kN / 2][4];
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const float base = x < kRowHalves && m[x % kRowHalves] != -INFINITY ? -m[x % kRowHalves] : 0.f;
+#pragma unroll
+        for (int n = 0; n < kN; ++n) {
+          uint32_t& p = pf[n / 2][2 * (n & 1) + x];
+          p = 0;
+          if (x >= kRowHalves) continue;
+          constexpr int kLast = kRowHalves - 1;
+          const int y = x < kLast ? x : kLast;
+          float w0 = ex2_approx(fmaf(sc[n][2 * x], f[y][n][0], base));
+          float w1 = ex2_approx(fmaf(sc[n][2 * x + 1], f[y][n][1], base));
+          l[y] += w0 + w1;
+          // The product's operand: weights in 16 bits (their sum stays in fp32).
+          p = E4M3 ? pack_f16x2(w0 * vf[n][0], w1 * vf[n][1]) : pack_bf16x2(w0, w1);
+          if (E4M3 && !open) {
+            // The exponent of a value that nobody sees may be the NaN byte.
+            const int j = key0 + 8 * n + 2 * t;
+            p &= (any(j) ? 0xFFFFu : 0u) | (any(j + 1) ? 0xFFFF0000u : 0u);
+          }
+        }
+      }
+      // ---- O += P V
+#pragma unroll
+      for (int h = 0; h < kN / 2; ++h) {
+        if constexpr (E4M3) {
+#pragma unroll
+          for (int y = 0; y < kCols / 4; ++y) {
+            const uint32_t* w = vw + (y * kN + 2 * h) * 2;      // keys 16h + 2t, + 1, + 8, + 9
+#pragma unroll
+            for (int e = 0; e < 4; e += 2) {
+              // Bytes e, e + 1 of both keys' words, side by side per dim.
+              const uint32_t sel = e == 0 ? 0x5140u : 0x7362u;
+              const uint32_t p0 = __byte_perm(w[0], w[1], sel), p1 = __byte_perm(w[2], w[3], sel);
+              mma<true>(o[4 * y + e], pf[h], e4m3x2_to_f16x2(p0 & 0xFFFFu), e4m3x2_to_f16x2(p1 & 0xFFFFu));
+              mma<true>(o[4 * y + e + 1], pf[h], e4m3x2_to_f16x2(p0 >> 16), e4m3x2_to_f16x2(p1 >> 16));
+            }
+          }
+        } else {
+#pragma unroll
+          for (int n = 0; n < kCols; ++n) mma<false>(o[n], pf[h], vw[2 * n], vw[2 * n + 1]);
+        }
+      }
     }
-    if (!ok) break;
+    if (dead) break;
 
     // ---- the item's end: finished here, or a record for the join
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        l[mt][x] += __shfl_xor_sync(0xFFFFFFFFu, l[mt][x], 1);
-        l[mt][x] += __shfl_xor_sync(0xFFFFFFFFu, l[mt][x], 2);
-      }
+    for (int x = 0; x < kRowHalves; ++x) {
+      l[x] += __shfl_xor_sync(0xFFFFFFFFu, l[x], 1);
+      l[x] += __shfl_xor_sync(0xFFFFFFFFu, l[x], 2);
+    }
     const bool begun = it.b > 0, whole = !begun && it.end == it.kb.count;
     if (!begun && !whole) {
       const int64_t last = u - it.b + it.kb.count - 1;
-      header = SplitHeader{static_cast<int>(share_of(last, W, total) - me) + 1, it.s, it.head, 0};
+      header = SplitHeader{static_cast<int>(share_of(last, W, total) - me) + 1, it.s, it.head, 0, it.q, 0};
     }
     float* r = rec.at(me, begun ? 0 : 1);
     uint32_t redo = 0;
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
+    for (int x = 0; x < kRowHalves; ++x) {
+      const int rho = 8 * x + g;
+      bool bad = false;
+      if (rho < R) {
+        const int i = rho / a.group;
+        bf16* dst = a.out + (it.q.row0 + i) * a.out_stride + (it.head * a.group + rho - i * a.group) * D;
+        const float inv = pos[x] < 0 ? 0.f : 1.f / l[x];
+        float* rr = r + rho * D;
+        if (!whole && t == 0) {
+          rec.max_of(r, D)[rho] = m[x];
+          rec.sum_of(r, D)[rho] = l[x];
+        }
+        // bf16: columns 8n + 2t, + 1.  e4m3: column tile n holds dim n of each
+        // lane group's D / 8, so this lane has dims (2t) D/8 + n and (2t + 1) D/8 + n.
+        if constexpr (E4M3) {
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const int rho = 16 * mt + 8 * x + g;
-        bool bad = false;
-        if (rho < R) {
-          const int i = rho / a.group;
-          bf16* dst = a.out + (it.q.row0 + i) * a.out_stride + (it.head * a.group + rho - i * a.group) * D;
-          const float inv = pos[mt][x] < 0 ? 0.f : 1.f / l[mt][x];
-          float* rr = r + rho * D;
-          if (!whole && t == 0) {
-            rec.max_of(r, D)[rho] = m[mt][x];
-            rec.sum_of(r, D)[rho] = l[mt][x];
-          }
-          // bf16: columns 8n + 2t, + 1.  e4m3: column tile n holds dim n of
-          // each lane group's D / 8, so this lane has dims (2t) D/8 + n and (2t + 1) D/8 + n.
-          if constexpr (E4M3) {
+          for (int e = 0; e < 2; ++e) {
+            const int d0 = (2 * t + e) * kCols;
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const int d0 = (2 * t + e) * kCols;
-#pragma unroll
-              for (int n = 0; n < kCols; n += 4) {
-                float4 y = make_float4(o[mt][n][2 * x + e], o[mt][n + 1][2 * x + e], o[mt][n + 2][2 * x + e],
-                                       o[mt][n + 3][2 * x + e]);
-                if (whole) {
-                  y = make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv);
-                  bad |= not_finite(y.x) || not_finite(y.y) || not_finite(y.z) || not_finite(y.w);
-                  *reinterpret_cast<uint2*>(dst + d0 + n) = make_uint2(pack_bf16x2(y.x, y.y), pack_bf16x2(y.z, y.w));
-                } else {
-                  *reinterpret_cast<float4*>(rr + d0 + n) = y;
-                }
-              }
-            }
-          } else {
-#pragma unroll
-            for (int n = 0; n < kCols; ++n) {
-              const float y0 = o[mt][n][2 * x], y1 = o[mt][n][2 * x + 1];
+            for (int n = 0; n < kCols; n += 4) {
+              float4 y = make_float4(o[n][2 * x + e], o[n + 1][2 * x + e], o[n + 2][2 * x + e], o[n + 3][2 * x + e]);
               if (whole) {
-                bad |= not_finite(y0 * inv) || not_finite(y1 * inv);
-                *reinterpret_cast<uint32_t*>(dst + 8 * n + 2 * t) = pack_bf16x2(y0 * inv, y1 * inv);
+                y = make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv);
+                bad |= not_finite(y.x) || not_finite(y.y) || not_finite(y.z) || not_finite(y.w);
+                *reinterpret_cast<uint2*>(dst + d0 + n) = make_uint2(pack_bf16x2(y.x, y.y), pack_bf16x2(y.z, y.w));
               } else {
-                *reinterpret_cast<float2*>(rr + 8 * n + 2 * t) = make_float2(y0, y1);
+                *reinterpret_cast<float4*>(rr + d0 + n) = y;
               }
             }
           }
-        }
-        if (it.q.c > 1) {
-          const uint32_t lanes = __ballot_sync(0xFFFFFFFFu, bad);
+        } else {
 #pragma unroll
-          for (int y = 0; y < 8; ++y)
-            if ((lanes >> (4 * y)) & 15u) redo |= 1u << (16 * mt + 8 * x + y);
+          for (int n = 0; n < kCols; ++n) {
+            const float y0 = o[n][2 * x], y1 = o[n][2 * x + 1];
+            if (whole) {
+              bad |= not_finite(y0 * inv) || not_finite(y1 * inv);
+              *reinterpret_cast<uint32_t*>(dst + 8 * n + 2 * t) = pack_bf16x2(y0 * inv, y1 * inv);
+            } else {
+              *reinterpret_cast<float2*>(rr + 8 * n + 2 * t) = make_float2(y0, y1);
+            }
+          }
         }
+      }
+      if (it.q.c > 1) {
+        const uint32_t lanes = __ballot_sync(0xFFFFFFFFu, bad);
+#pragma unroll
+        for (int y = 0; y < 8; ++y)
+          if ((lanes >> (4 * y)) & 15u) redo |= 1u << (8 * x + y);
       }
     }
     while (redo) {
@@ -555,56 +603,60 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int rho = __ffs(static_cast<int>(redo)) - 1;
       redo &= redo - 1;
       const int i = rho / a.group;
-      exact_row<D, E4M3>(a, it.s, it.q.row0, it.q.kv - it.q.c + i, i, it.head * a.group + rho - i * a.group, lane);
+      exact_row<D, E4M3>(a, it.s, it.q.row0, p_first + i, i, it.head * a.group + rho - i * a.group, lane);
     }
     u += it.end - it.b;
   }
-  // After a timeout: wait (bounded) for the loads still in flight.
-  for (; !ok && used_u < load_u; ++used_u) {
-    if (!__all_sync(0xFFFFFFFFu, mbar_wait(bar0 + 8 * slot, phase, nullptr))) break;
-    if (++slot == S::kStages) {
-      slot = 0;
-      phase ^= 1;
+  if (dead) {
+    // After a timeout: wait (bounded) for the loads that may still be in flight.
+    for (int i = 0; i < S::kStages; ++i) {
+      if (!mbar_wait(full + 8 * slot, phase, nullptr)) break;
+      if (++slot == S::kStages) {
+        slot = 0;
+        phase ^= 1;
+      }
     }
   }
-  if (lane == 0) rec.headers[me] = ok ? header : SplitHeader{0, 0, 0, 0};
+  if (lane == 0) rec.headers[me] = dead ? SplitHeader{} : header;
 }
 
-int decode_workers() { return num_sms() * kWarps; }
-
-template <int D, bool E4M3, int MT>
+template <int D, bool E4M3, int kRowHalves>
 int launch(const AttentionArgs& a, void* ws, cudaStream_t stream) {
   using S = Shape<D, E4M3>;
   CUtensorMap tk, tv;
   const uint64_t rows = static_cast<uint64_t>(a.c.n_pages) * a.c.kv_heads << a.c.page_shift;
   const uint64_t cols = S::kRow / 2;      // in 16-bit units
+  const uint32_t box = E4M3 && a.c.page_shift > 4 ? 32 : 16;
   auto map = [&](CUtensorMap* m, const void* p) {
-    return cols == 32 ? make_tmap_bf16_sw64(m, p, rows, cols, 16) : make_tmap_bf16(m, p, rows, cols, 16);
+    return cols == 32 ? make_tmap_bf16_sw64(m, p, rows, cols, box) : make_tmap_bf16(m, p, rows, cols, box);
   };
   if (!map(&tk, a.c.k) || !map(&tv, a.c.v)) return DS_VIT_ECUDA;
-  if (allow_smem(reinterpret_cast<const void*>(decode_kernel<D, E4M3, MT>), S::kSmem) != cudaSuccess)
+  if (allow_smem(reinterpret_cast<const void*>(decode_kernel<D, E4M3, kRowHalves>), S::kSmem) != cudaSuccess)
     return DS_VIT_ECUDA;
   const int R = a.b.max_rows * a.group, grid = num_sms();
-  const Records rec = records_in(ws, decode_workers(), R, D);
-  cudaError_t e = launch_pdl(decode_kernel<D, E4M3, MT>, dim3(grid), dim3(kThreads), S::kSmem, stream, tk, tv, a, rec);
-  if (e == cudaSuccess)
-    e = launch_pdl(join_kernel<D, E4M3>, dim3(grid, R), dim3(32 * kJoinWarps), 0, stream, a, rec, decode_workers());
+  const int workers = grid * kWarps;
+  const Records rec = records_in(ws, workers, R, D);
+  cudaError_t e = launch_pdl(decode_kernel<D, E4M3, kRowHalves>, dim3(grid), dim3(kThreads), S::kSmem, stream, tk, tv,
+                             a, rec);
+  if (e == cudaSuccess) e = launch_join<D, E4M3>(a, rec, grid, workers, stream);
   if (e != cudaSuccess) cudaGetLastError();
   return e == cudaSuccess ? DS_VIT_OK : DS_VIT_ECUDA;
 }
 
 }  // namespace
 
-size_t cache_decode_workspace(int head_dim, int rows) { return records_bytes(decode_workers(), rows, head_dim); }
+size_t cache_decode_workspace(int head_dim, int rows) {
+  return records_bytes(static_cast<int64_t>(num_sms()) * kWarps, rows, head_dim);
+}
 
 int launch_cache_decode(const AttentionArgs& a, int head_dim, bool e4m3, void* ws, cudaStream_t stream) {
   const int R = a.b.max_rows * a.group;
   if (R > kDecodeRows) return DS_VIT_EINVAL;
   if (head_dim == 128) {
-    if (R <= 16) return e4m3 ? launch<128, true, 1>(a, ws, stream) : launch<128, false, 1>(a, ws, stream);
+    if (R <= 8) return e4m3 ? launch<128, true, 1>(a, ws, stream) : launch<128, false, 1>(a, ws, stream);
     return e4m3 ? launch<128, true, 2>(a, ws, stream) : launch<128, false, 2>(a, ws, stream);
   }
-  if (R <= 16) return e4m3 ? launch<64, true, 1>(a, ws, stream) : launch<64, false, 1>(a, ws, stream);
+  if (R <= 8) return e4m3 ? launch<64, true, 1>(a, ws, stream) : launch<64, false, 1>(a, ws, stream);
   return e4m3 ? launch<64, true, 2>(a, ws, stream) : launch<64, false, 2>(a, ws, stream);
 }
 

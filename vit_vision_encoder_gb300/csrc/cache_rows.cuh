@@ -63,10 +63,14 @@ __device__ __noinline__ void exact_row(const AttentionArgs& a, int s, int row0, 
 __device__ __forceinline__ bool not_finite(float x) { return (__float_as_uint(x) & 0x7F800000u) == 0x7F800000u; }
 
 // Who shares the item that a worker begins and does not end: `parts` workers,
-// the first of them that worker (0: none).
+// the first of them that worker (0: none); the item's sequence, K/V head and
+// first row among the rows of the two.
 struct SplitHeader {
-  int parts, s, head, tile;
+  int parts, s, head, rho0;
+  Seq q;
+  int pad;
 };
+static_assert(sizeof(SplitHeader) == 32, "read as two 16-byte words");
 
 // Layout of the workspace: a header per worker, then two records per worker,
 // 0 for the item that it found begun, 1 for the item that it leaves unended.  A record:
@@ -90,80 +94,149 @@ inline Records records_in(void* ws, int64_t workers, int rows, int d) {
   return Records{h, reinterpret_cast<float*>(h + workers), rows, record_floats(rows, d)};
 }
 
-// Joins the parts of every split item: O = sum_p 2^(m_p - M) O_p, L alike.  One
-// block per (group of workers, row): its warps share the parts, each with a
-// running maximum, and are joined through shared memory in a fixed order, so
-// a result depends on the lengths alone.  Worker groups: blockIdx.x, then every
-// gridDim.x-th worker.
+// Joins the parts of every split item: O = sum_p 2^(m_p - M) O_p, L alike.
+// Block (x, y) looks after workers x, x + gridDim.x, ... and rows y, y +
+// gridDim.y, ... of their items.  Up to kJoinWarps parts, one warp adds up a
+// row; more parts are shared between the block's warps and joined through
+// shared memory.  The order is fixed, so a result depends on the lengths alone.
 constexpr int kJoinWarps = 8;
+constexpr int kJoinItems = 16;    // workers per block at most
+constexpr int kJoinRows = 8;      // grid rows at most
+
+// Adds parts first, first + step, ... of one row to (m, l, o), loads of four parts at a time.
+template <int D>
+__device__ __forceinline__ void join_parts(const Records& rec, int w, int parts, int row, int first, int step, int lane,
+                                           float& m, float& l, float (&o)[D / 32]) {
+  constexpr int kPer = D / 32, kBatch = 4;
+  for (int p0 = first; p0 < parts; p0 += kBatch * step) {
+    float mp[kBatch], lp[kBatch], op[kBatch][kPer];
+#pragma unroll
+    for (int y = 0; y < kBatch; ++y) {
+      const int part = p0 + y * step;
+      mp[y] = -INFINITY;
+      lp[y] = 0.f;
+#pragma unroll
+      for (int x = 0; x < kPer; ++x) op[y][x] = 0.f;
+      if (part < parts) {
+        float* r = rec.at(w + part, part == 0 ? 1 : 0);
+        mp[y] = rec.max_of(r, D)[row];
+        lp[y] = rec.sum_of(r, D)[row];
+        if constexpr (kPer == 4) {
+          const float4 v = *reinterpret_cast<const float4*>(r + row * D + 4 * lane);
+          op[y][0] = v.x, op[y][1] = v.y, op[y][2] = v.z, op[y][3] = v.w;
+        } else {
+          const float2 v = *reinterpret_cast<const float2*>(r + row * D + 2 * lane);
+          op[y][0] = v.x, op[y][1] = v.y;
+        }
+      }
+    }
+    float m_new = m;
+#pragma unroll
+    for (int y = 0; y < kBatch; ++y) m_new = fmaxf(m_new, mp[y]);
+    const float wa = m == m_new ? 1.f : exp2f(m - m_new);
+    l *= wa;
+#pragma unroll
+    for (int x = 0; x < kPer; ++x) o[x] *= wa;
+#pragma unroll
+    for (int y = 0; y < kBatch; ++y) {
+      const float wb = mp[y] == m_new ? 1.f : exp2f(mp[y] - m_new);
+      l += lp[y] * wb;
+#pragma unroll
+      for (int x = 0; x < kPer; ++x) o[x] += op[y][x] * wb;
+    }
+    m = m_new;
+  }
+}
+
+// One warp writes a joined row.
+template <int D, bool E4M3>
+__device__ __forceinline__ void join_finish(const AttentionArgs& a, const SplitHeader& hd, int rho, float l,
+                                            const float (&o)[D / 32], int lane) {
+  const int i = rho / a.group, h = hd.head * a.group + rho - i * a.group, p = hd.q.kv - hd.q.c + i;
+  bf16* to = a.out + (hd.q.row0 + i) * a.out_stride + h * D + lane * (D / 32);
+  const float inv = p < 0 ? 0.f : 1.f / l;
+  bool bad = false;
+  uint32_t w[D / 64];
+#pragma unroll
+  for (int x = 0; x < D / 64; ++x) {
+    const float y0 = o[2 * x] * inv, y1 = o[2 * x + 1] * inv;
+    bad |= not_finite(y0) || not_finite(y1);
+    w[x] = pack_bf16x2(y0, y1);
+  }
+  if constexpr (D == 128)
+    *reinterpret_cast<uint2*>(to) = make_uint2(w[0], w[1]);
+  else
+    *reinterpret_cast<uint32_t*>(to) = w[0];
+  if (hd.q.c > 1 && __any_sync(0xFFFFFFFFu, bad)) {
+    __syncwarp();
+    exact_row<D, E4M3>(a, hd.s, hd.q.row0, p, i, h, lane);
+  }
+}
 
 template <int D, bool E4M3>
 __global__ void __launch_bounds__(32 * kJoinWarps)
     join_kernel(const __grid_constant__ AttentionArgs a, const Records rec, int workers) {
   constexpr int kPer = D / 32;
   __shared__ float sm[kJoinWarps], sl[kJoinWarps], so[kJoinWarps][D];
+  __shared__ SplitHeader heads[kJoinItems];
   grid_dep_launch();
   grid_dep_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int w = blockIdx.x; w < workers; w += gridDim.x) {
-    const SplitHeader hd = rec.headers[w];
+  const int mine = (workers - static_cast<int>(blockIdx.x) + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x);
+  if (threadIdx.x < 2 * mine)
+    reinterpret_cast<int4*>(heads)[threadIdx.x] = reinterpret_cast<const int4*>(
+        rec.headers + blockIdx.x + (threadIdx.x >> 1) * gridDim.x)[threadIdx.x & 1];
+  __syncthreads();
+  int turn = 0;                       // rows dealt to the warps so far
+  for (int k = 0; k < mine; ++k) {
+    const SplitHeader& hd = heads[k];
     if (hd.parts == 0) continue;
-    const Seq sq = load_seq(a.b, a.c.page_shift, hd.s, nullptr);
-    const int row = static_cast<int>(blockIdx.y), rho = hd.tile * rec.rows + row;
-    if (rho >= sq.c * a.group) continue;
-    float m = -INFINITY, l = 0.f, o[kPer];
-#pragma unroll
-    for (int x = 0; x < kPer; ++x) o[x] = 0.f;
-    for (int part = warp; part < hd.parts; part += kJoinWarps) {
-      float* r = rec.at(w + part, part == 0 ? 1 : 0);
-      const float mp = rec.max_of(r, D)[row], lp = rec.sum_of(r, D)[row];
-      float op[kPer];
-#pragma unroll
-      for (int x = 0; x < kPer; ++x) op[x] = r[row * D + lane * kPer + x];
-      const float m_new = fmaxf(m, mp);
-      const float wa = m == m_new ? 1.f : exp2f(m - m_new), wb = mp == m_new ? 1.f : exp2f(mp - m_new);
-      l = l * wa + lp * wb;
-#pragma unroll
-      for (int x = 0; x < kPer; ++x) o[x] = o[x] * wa + op[x] * wb;
-      m = m_new;
-    }
-    __syncthreads();      // the previous item's results have been read
-    if (lane == 0) {
-      sm[warp] = m;
-      sl[warp] = l;
-    }
-#pragma unroll
-    for (int x = 0; x < kPer; ++x) so[warp][lane * kPer + x] = o[x];
-    __syncthreads();
-    if (warp == 0) {
-      float M = sm[0];
-#pragma unroll
-      for (int x = 1; x < kJoinWarps; ++x) M = fmaxf(M, sm[x]);
-      float L = 0.f;
+    const int w = blockIdx.x + k * gridDim.x;
+    const int64_t left = static_cast<int64_t>(hd.q.c) * a.group - hd.rho0;
+    const int rows = left < rec.rows ? static_cast<int>(left) : rec.rows;
+    for (int row = blockIdx.y; row < rows; row += gridDim.y) {
+      float m = -INFINITY, l = 0.f, o[kPer];
 #pragma unroll
       for (int x = 0; x < kPer; ++x) o[x] = 0.f;
-#pragma unroll
-      for (int y = 0; y < kJoinWarps; ++y) {
-        const float f = sm[y] == M ? 1.f : exp2f(sm[y] - M);
-        L += sl[y] * f;
-#pragma unroll
-        for (int x = 0; x < kPer; ++x) o[x] += so[y][lane * kPer + x] * f;
+      if (hd.parts <= kJoinWarps) {
+        if (turn++ % kJoinWarps != warp) continue;
+        join_parts<D>(rec, w, hd.parts, row, 0, 1, lane, m, l, o);
+        join_finish<D, E4M3>(a, hd, hd.rho0 + row, l, o, lane);
+        continue;
       }
-      const int i = rho / a.group, h = hd.head * a.group + rho % a.group, p = sq.kv - sq.c + i;
-      bool bad = false;
-      bf16* to = a.out + (sq.row0 + i) * a.out_stride + h * D + lane * kPer;
-#pragma unroll
-      for (int x = 0; x < kPer; ++x) {
-        const float y = p < 0 ? 0.f : o[x] / L;
-        bad |= not_finite(y);
-        to[x] = __float2bfloat16_rn(y);
+      join_parts<D>(rec, w, hd.parts, row, warp, kJoinWarps, lane, m, l, o);
+      __syncthreads();      // the previous row's results have been read
+      if (lane == 0) {
+        sm[warp] = m;
+        sl[warp] = l;
       }
-      if (sq.c > 1 && __any_sync(0xFFFFFFFFu, bad)) {
-        __syncwarp();
-        exact_row<D, E4M3>(a, hd.s, sq.row0, p, i, h, lane);
+#pragma unroll
+      for (int x = 0; x < kPer; ++x) so[warp][lane * kPer + x] = o[x];
+      __syncthreads();
+      if (warp == 0) {
+        float M = sm[0];
+#pragma unroll
+        for (int x = 1; x < kJoinWarps; ++x) M = fmaxf(M, sm[x]);
+        l = 0.f;
+#pragma unroll
+        for (int x = 0; x < kPer; ++x) o[x] = 0.f;
+#pragma unroll
+        for (int y = 0; y < kJoinWarps; ++y) {
+          const float f = sm[y] == M ? 1.f : exp2f(sm[y] - M);
+          l += sl[y] * f;
+#pragma unroll
+          for (int x = 0; x < kPer; ++x) o[x] += so[y][lane * kPer + x] * f;
+        }
+        join_finish<D, E4M3>(a, hd, hd.rho0 + row, l, o, lane);
       }
     }
   }
+}
+
+template <int D, bool E4M3>
+cudaError_t launch_join(const AttentionArgs& a, const Records& rec, int grid, int workers, cudaStream_t stream) {
+  return launch_pdl(join_kernel<D, E4M3>, dim3(grid, rec.rows < kJoinRows ? rec.rows : kJoinRows), dim3(32 * kJoinWarps),
+                    0, stream, a, rec, workers);
 }
 
 }  // namespace dsvit

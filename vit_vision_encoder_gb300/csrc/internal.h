@@ -203,7 +203,7 @@ struct AttentionArgs;
 size_t cache_attention_workspace(int head_dim, int group, int max_rows);
 int launch_cache_attention(const AttentionArgs& a, int head_dim, bool e4m3, void* ws, cudaStream_t stream);
 // The path for at most kDecodeRows query rows per K/V head and sequence.
-constexpr int kDecodeRows = 32;
+constexpr int kDecodeRows = 16;
 size_t cache_decode_workspace(int head_dim, int rows);
 int launch_cache_decode(const AttentionArgs& a, int head_dim, bool e4m3, void* ws, cudaStream_t stream);
 
