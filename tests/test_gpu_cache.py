@@ -536,6 +536,37 @@ def test_more_rows_than_max_rows_refused(dv):
     assert (np.abs(f64(got)[4:] - ref[4:]) <= tol[4:]).all()
 
 
+def test_binding_refuses_other_tensors(dv):
+    """Types, shapes, strides and devices that the binding refuses before the call."""
+    st = Setup(dv, [2, 3], [40, 30], 2, 64, 16, "bf16", seed=13)
+    q, kv = st.queries(4), st.queries(2)
+    cpu = dv.KvCache(st.cache.k.cpu(), st.cache.v.cpu())
+    i32 = dict(dtype=torch.int32, device="cuda")
+    bad = [lambda: dv.cache_write(st.cache, st.chunks, kv.float(), kv),
+           lambda: dv.cache_write(st.cache, st.chunks, kv, kv[:4]),
+           lambda: dv.cache_write(st.cache, st.chunks, kv[:, :1], kv),
+           lambda: dv.cache_write(st.cache, st.chunks, kv.cpu(), kv),
+           lambda: dv.cache_write(st.cache, st.chunks, kv.transpose(1, 2).contiguous().transpose(1, 2), kv),
+           lambda: dv.cache_write(cpu, st.chunks, kv, kv),
+           lambda: dv.cache_write(st.cache, st.chunks, kv, kv, status=torch.zeros(1, device="cuda")),
+           lambda: dv.cache_write(st.cache, st.chunks, kv, kv, status=torch.zeros(1, dtype=torch.int32)),
+           lambda: dv.cache_read(st.cache, st.chunks, 4, out=(kv, kv)),
+           lambda: dv.cache_read(st.cache, st.chunks, 5, out=(kv, kv.half())),
+           lambda: dv.cache_attention(st.cache, st.chunks, q[:, :3]),
+           lambda: dv.cache_attention(st.cache, st.chunks, q[..., :32]),
+           lambda: dv.cache_attention(st.cache, st.chunks, q.view(5, 256)),
+           lambda: dv.cache_attention(st.cache, st.chunks, q, out=q[:4].clone()),
+           lambda: dv.cache_attention(st.cache, st.chunks, q, scale=0.0),
+           lambda: dv.cache_attention(st.cache, st.chunks, q, ws=torch.empty(16, dtype=torch.uint8, device="cuda")),
+           lambda: dv.cache_attention(st.cache, st.chunks, q, ws=torch.empty(1 << 24, device="cuda")),
+           lambda: dv.cache_attention(st.cache, dv.Chunks(torch.zeros(2, **i32).cpu(), torch.zeros(1, **i32).cpu(),
+                                                          torch.zeros((1, 1), **i32).cpu(), 1), q)]
+    for i, call in enumerate(bad):
+        with pytest.raises(dv.DsVitError):
+            call()
+            pytest.fail(f"call {i} was not refused")
+
+
 # ------------------------------------------------------------------ as a serving loop uses them
 
 @pytest.mark.parametrize("kind", ["bf16", "e4m3"])

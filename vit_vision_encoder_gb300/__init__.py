@@ -535,13 +535,25 @@ def overlay_chunk(chunk, chunk_begin, spans, embeds, sentinel, row_type=None):
 
 # ---------------------------------------------------------------- paged K/V cache
 
+def _cache_names():
+    """torch, with the names that the cache calls use on every call."""
+    global _bf16, _u8, _i32_type, _cuda_device, _raw_stream
+    torch = _torch()
+    _bf16, _u8, _i32_type = torch.bfloat16, torch.uint8, torch.int32
+    _cuda_device = torch.cuda.current_device
+    # The stream's handle without a Stream object (0.2 us a call against 8).
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                          lambda d: torch.cuda.current_stream(d).cuda_stream)
+    return torch
+
+
 class KvCache:
     """The pages of one layer's keys and values (ds_vit_cache): k, v CUDA
     tensors [n_pages, kv_heads, page, head_dim], bfloat16, or uint8 (e4m3 bits)
     with k_exp, v_exp uint8 [n_pages, kv_heads, page].  Holds its tensors."""
 
     def __init__(self, k, v, k_exp=None, v_exp=None):
-        torch = _torch()
+        torch = _cache_names()
         e4m3 = k.dtype != torch.bfloat16
         held = (k, v, k_exp, v_exp) if e4m3 else (k, v)
         for t in held:
@@ -552,6 +564,7 @@ class KvCache:
             raise DsVitError(EINVAL, "KvCache")
         self.k, self.v, self.k_exp, self.v_exp = k, v, k_exp, v_exp
         self.kv_heads, self.head_dim, self.device = k.shape[1], k.shape[3], k.device
+        self.device_index = k.get_device()
         self.c = Cache(k.data_ptr(), v.data_ptr(), k_exp.data_ptr() if e4m3 else None,
                        v_exp.data_ptr() if e4m3 else None, *k.shape, CACHE_E4M3 if e4m3 else CACHE_BF16)
         self.ref = C.byref(self.c)
@@ -578,81 +591,107 @@ class Chunks:
             if t.dtype != torch.int32 or tuple(t.shape) != shape or not t.is_contiguous() or t.device != table.device:
                 raise DsVitError(EINVAL, "Chunks")
         self.row_off, self.kv_len, self.table = row_off, kv_len, table
-        self.device = table.device
+        self.device_index = table.get_device()
+        self.ws_bytes = {}
         self.c = ChunkArrays(row_off.data_ptr(), kv_len.data_ptr(), table.data_ptr(), n, table.shape[1], max_rows)
         self.ref = C.byref(self.c)
 
 
-def _packed(t, cache, chunks, where):
-    """Row stride of a packed bf16 tensor [rows, heads, head_dim] on the cache's
-    device; its heads and their values must lie side by side."""
-    torch = _torch()
-    d = cache.head_dim
-    if (t.dtype != torch.bfloat16 or t.dim() != 3 or t.shape[2] != d or t.device != cache.device
-            or chunks.device != cache.device or (t.shape[0] > 0 and (t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != d)))):
-        raise DsVitError(EINVAL, where)
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1] * d)
+def _refuse(where):
+    raise DsVitError(EINVAL, where)
 
 
-def _status_on(cache, status):
+def _packed(t, heads, dim, device, where):
+    """Row stride of a packed bf16 tensor [rows, heads, dim] on CUDA device number
+    ``device``; its heads and their values must lie side by side."""
+    shape, stride = t.shape, t.stride()
+    if (t.dtype is not _bf16 or len(shape) != 3 or shape[1] != heads or shape[2] != dim or t.get_device() != device
+            or (shape[0] and (stride[2] != 1 or (heads > 1 and stride[1] != dim)))):
+        _refuse(where)
+    return stride[0] if shape[0] > 1 else heads * dim
+
+
+def _on_device(cache, chunks, status, where):
+    """Device number and raw current stream of a cache call: everything lies on
+    the current device, where the library launches."""
+    d = cache.device_index
+    if d < 0 or chunks.device_index != d or _cuda_device() != d:
+        _refuse(where)
     if status is None:
-        torch = _torch()
-        return torch.zeros(1, dtype=torch.int32, device=cache.device)
-    return status
+        status = _torch().zeros(1, dtype=_torch().int32, device=cache.device)
+    elif status.dtype is not _i32_type or status.get_device() != d or not status.numel():
+        _refuse(where)
+    return d, _raw_stream(d), status
 
 
 def cache_write(cache, chunks, k, v, status=None):
     """Rows k, v (bf16 [rows, kv_heads, head_dim], rows may be strided) into the
     pages (ds_vit_cache_write).  Returns ``status`` (int32 [1], zeroed here when
     not given), which receives the first error found on the device."""
-    status = _status_on(cache, status)
-    ks, vs = _packed(k, cache, chunks, "ds_vit_cache_write"), _packed(v, cache, chunks, "ds_vit_cache_write")
-    if k.shape != v.shape or k.shape[1] != cache.kv_heads:
-        raise DsVitError(EINVAL, "ds_vit_cache_write")
-    check(lib.ds_vit_cache_write(cache.ref, chunks.ref, k.data_ptr(), ks, v.data_ptr(), vs, k.shape[0],
-                                 status.data_ptr(), _stream()), "ds_vit_cache_write")
+    d, stream, status = _on_device(cache, chunks, status, "ds_vit_cache_write")
+    ks = _packed(k, cache.kv_heads, cache.head_dim, d, "ds_vit_cache_write")
+    vs = _packed(v, cache.kv_heads, cache.head_dim, d, "ds_vit_cache_write")
+    rows = k.shape[0]
+    if v.shape[0] != rows:
+        _refuse("ds_vit_cache_write")
+    check(lib.ds_vit_cache_write(cache.ref, chunks.ref, k.data_ptr(), ks, v.data_ptr(), vs, rows, status.data_ptr(),
+                                 stream), "ds_vit_cache_write")
     return status
 
 
 def cache_read(cache, chunks, rows, out=None, status=None):
     """The newest tokens of every sequence, as bf16 (k, v) of ``rows`` packed rows
     (ds_vit_cache_read); ``out``: the two tensors to fill.  Returns (k, v, status)."""
-    torch = _torch()
-    status = _status_on(cache, status)
+    d, stream, status = _on_device(cache, chunks, status, "ds_vit_cache_read")
     if out is None:
-        out = tuple(torch.empty((rows, cache.kv_heads, cache.head_dim), dtype=torch.bfloat16, device=cache.device)
+        out = tuple(_torch().empty((rows, cache.kv_heads, cache.head_dim), dtype=_bf16, device=cache.device)
                     for _ in range(2))
     k, v = out
-    ks, vs = _packed(k, cache, chunks, "ds_vit_cache_read"), _packed(v, cache, chunks, "ds_vit_cache_read")
-    if k.shape != v.shape or k.shape[0] != rows or k.shape[1] != cache.kv_heads:
-        raise DsVitError(EINVAL, "ds_vit_cache_read")
+    ks = _packed(k, cache.kv_heads, cache.head_dim, d, "ds_vit_cache_read")
+    vs = _packed(v, cache.kv_heads, cache.head_dim, d, "ds_vit_cache_read")
+    if k.shape[0] != rows or v.shape[0] != rows:
+        _refuse("ds_vit_cache_read")
     check(lib.ds_vit_cache_read(cache.ref, chunks.ref, k.data_ptr(), ks, v.data_ptr(), vs, rows, status.data_ptr(),
-                                _stream()), "ds_vit_cache_read")
+                                stream), "ds_vit_cache_read")
     return k, v, status
+
+
+def cache_attention_workspace_bytes(cache, chunks, heads):
+    """Bytes of workspace that cache_attention needs for these sizes."""
+    nb = chunks.ws_bytes.get((heads, cache.kv_heads, cache.head_dim))
+    if nb is None:
+        n = C.c_size_t()
+        check(lib.ds_vit_cache_attention_workspace_bytes(cache.ref, chunks.ref, heads, C.byref(n)),
+              "ds_vit_cache_attention_workspace_bytes")
+        nb = chunks.ws_bytes[heads, cache.kv_heads, cache.head_dim] = n.value
+    return nb
 
 
 def cache_attention(cache, chunks, q, scale=None, window=0, sinks=0, out=None, ws=None, status=None):
     """Attention of the packed rows q (bf16 [rows, heads, head_dim], rows may be
     strided) over the cache (ds_vit_cache_attention); scale defaults to
-    head_dim ** -0.5.  ``ws``: uint8 workspace (allocated here when not given).
-    Returns (out, status)."""
-    torch = _torch()
-    status = _status_on(cache, status)
-    rows, heads = q.shape[0], q.shape[1]
+    head_dim ** -0.5.  ``ws``: uint8 workspace (allocated here when not given;
+    calls that may overlap need one each).  Returns (out, status)."""
+    d, stream, status = _on_device(cache, chunks, status, "ds_vit_cache_attention")
+    if q.dim() != 3:
+        _refuse("ds_vit_cache_attention")
+    rows, heads, dim = q.shape
+    qs = _packed(q, heads, cache.head_dim, d, "ds_vit_cache_attention")
     if out is None:
-        out = torch.empty((rows, heads, cache.head_dim), dtype=torch.bfloat16, device=cache.device)
-    qs, os_ = _packed(q, cache, chunks, "ds_vit_cache_attention"), _packed(out, cache, chunks, "ds_vit_cache_attention")
-    if out.shape != q.shape:
-        raise DsVitError(EINVAL, "ds_vit_cache_attention")
+        out = _torch().empty((rows, heads, dim), dtype=_bf16, device=cache.device)
+    os_ = _packed(out, heads, dim, d, "ds_vit_cache_attention")
+    if out.shape[0] != rows:
+        _refuse("ds_vit_cache_attention")
     if ws is None:
-        nb = C.c_size_t()
-        check(lib.ds_vit_cache_attention_workspace_bytes(cache.ref, chunks.ref, heads, C.byref(nb)),
-              "ds_vit_cache_attention_workspace_bytes")
-        ws = torch.empty(nb.value, dtype=torch.uint8, device=cache.device)
+        ws = _torch().empty(cache_attention_workspace_bytes(cache, chunks, heads), dtype=_u8, device=cache.device)
+        ws_bytes = ws.numel()
+    else:
+        if ws.dtype is not _u8 or ws.get_device() != d or not ws.is_contiguous():
+            _refuse("ds_vit_cache_attention")
+        ws_bytes = ws.numel()
     check(lib.ds_vit_cache_attention(cache.ref, chunks.ref, q.data_ptr(), qs, rows, heads,
-                                     cache.head_dim ** -0.5 if scale is None else scale, window, sinks, out.data_ptr(),
-                                     os_, ws.data_ptr(), ws.numel(), status.data_ptr(), _stream()),
-          "ds_vit_cache_attention")
+                                     dim ** -0.5 if scale is None else scale, window, sinks, out.data_ptr(), os_,
+                                     ws.data_ptr(), ws_bytes, status.data_ptr(), stream), "ds_vit_cache_attention")
     return out, status
 
 

@@ -61,7 +61,8 @@ struct Shape {
   static constexpr int kStage = 2 * kTile;                 // K, then V
   static constexpr int kStages = kRingBytes / kStage;
   static constexpr int kExp = E4M3 ? 64 : 0;               // exponents of a stage: 32 K, 32 V
-  static constexpr int kSmem = 1024 + kWarps * (kRingBytes + kStages * (16 + kExp)) + 8 * (DS_VIT_MAX_SEQS + 1);
+  static constexpr int kSmem = 1024 + kWarps * (kRingBytes + kStages * (16 + kExp)) +
+                               8 * (DS_VIT_MAX_SEQS + 1) + static_cast<int>(sizeof(Seq)) * DS_VIT_MAX_SEQS;
 };
 
 // An item and the part of its blocks that a worker takes.
@@ -74,6 +75,7 @@ struct Item {
 
 struct Plan {
   const int64_t* pre;   // [n + 1]: units of the sequences before each
+  const Seq* seqs;      // [n]
   int64_t begin, end;   // the worker's units
 };
 
@@ -97,7 +99,7 @@ __device__ __forceinline__ Item item_at(const AttentionArgs& a, const Plan& pl, 
   }
   Item it;
   it.s = lo;
-  it.q = load_seq(a.b, a.c.page_shift, lo, nullptr);
+  it.q = pl.seqs[lo];
   it.kb = seq_blocks<kKeyShift>(a, it.q);
   const int64_t r = u - pl.pre[lo];
   it.head = static_cast<int>(r / it.kb.count);
@@ -120,9 +122,11 @@ __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint3
     mma_bf16(c, a, b0, b1);
 }
 
-// The producer's lane for one ring: loads the worker's blocks, a stage ahead
-// of its release at most.  Every wait is bounded; after one gives up the lane
-// stops loading and its consumer times out on its own.
+// The producer warp: lane i loads the blocks of consumer warp i into its ring as
+// stages come free.  The lanes look at their rings in turn and stay together
+// (each waiting for its own ring, they fell apart and held one another up).
+// Lanes without a worker have an empty plan.  After two seconds without a free
+// stage a lane stops loading, and its consumer times out on its own.
 template <int D, bool E4M3>
 __device__ __forceinline__ void produce(const CUtensorMap* tm_k, const CUtensorMap* tm_v, const AttentionArgs& a,
                                         const Plan& pl, uint32_t ring, uint32_t exps, uint32_t full, uint32_t empty) {
@@ -132,36 +136,53 @@ __device__ __forceinline__ void produce(const CUtensorMap* tm_k, const CUtensorM
   int slot = 0;
   uint32_t phase = 1;                      // a new barrier's preceding phase counts as complete
   int64_t u = pl.begin;
-  while (u < pl.end) {
-    Item it = item_at<S::kKeyShift>(a, pl, u);
+  Item it{};
+  int p_last = 0, lo = 0, next[2] = {-1, -1};
+  // Table entries are read a block ahead.  Of a block's pages only those that some row sees are needed.
+  auto look = [&](int b) {
+    const int key0 = it.kb.at(b) << S::kKeyShift;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int k0 = key0 + h * kPage16, k1 = halves == 2 ? k0 + kPage16 - 1 : key0 + S::kKeys - 1;
+      next[h] = -1;
+      if (h < halves && k0 <= p_last && (k1 >= lo || k0 < a.sinks))
+        next[h] = __ldg(a.b.table + static_cast<int64_t>(it.s) * a.b.table_cols + (k0 >> a.c.page_shift));
+      else
+        next[h] = -2;                      // not needed
+    }
+  };
+  auto item = [&]() {
+    it = item_at<S::kKeyShift>(a, pl, u);
     u += it.end - it.b;
-    const int p_last = it.q.kv - 1, lo = window_start(a, it.q.kv - it.q.c);
-    // Table entries are read a block ahead.  Of a block's pages only those that some row sees are needed.
-    int page[2], next[2] = {-1, -1};
-    auto look = [&](int b) {
-      const int key0 = it.kb.at(b) << S::kKeyShift;
+    p_last = it.q.kv - 1;
+    lo = window_start(a, it.q.kv - it.q.c);
+    look(it.b);
+  };
+  bool active = u < pl.end;
+  if (active) item();
+  unsigned long long since = global_timer();
+  while (__any_sync(0xFFFFFFFFu, active)) {
+    if (active && mbar_test(empty + 8 * slot, phase)) {
+      const int page[2] = {next[0], next[1]};
+      const int key0 = it.kb.at(it.b) << S::kKeyShift, head = it.head;
+      if (++it.b < it.end)
+        look(it.b);
+      else if (u < pl.end)
+        item();
+      else
+        active = false;
+      const uint32_t bar = full + 8 * slot, to = ring + slot * S::kStage, ex = exps + slot * S::kExp;
+      bool on[2];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const int k0 = key0 + h * kPage16, k1 = halves == 2 ? k0 + kPage16 - 1 : key0 + S::kKeys - 1;
-        next[h] = -1;
-        if (h < halves && k0 <= p_last && (k1 >= lo || k0 < a.sinks))
-          next[h] = static_cast<int>(page_of(a.b, a.c, it.s, k0, a.status));
+        on[h] = page[h] >= 0 && page[h] < a.c.n_pages;
+        if (!on[h] && page[h] != -2) report_error(a.status, DS_VIT_ERANGE);
       }
-    };
-    look(it.b);
-    for (; it.b < it.end; ++it.b) {
-      page[0] = next[0];
-      page[1] = next[1];
-      if (it.b + 1 < it.end) look(it.b + 1);
-      if (!mbar_wait(empty + 8 * slot, phase, a.status)) return;
-      const uint32_t bar = full + 8 * slot, to = ring + slot * S::kStage, ex = exps + slot * S::kExp;
-      const int key0 = it.kb.at(it.b) << S::kKeyShift;
-      const uint32_t per = (S::kStage + S::kExp) / halves;
-      mbar_expect_tx(bar, per * ((page[0] >= 0) + (page[1] >= 0)));
+      mbar_expect_tx(bar, (S::kStage + S::kExp) / halves * (on[0] + on[1]));
 #pragma unroll
       for (int h = 0; h < (E4M3 ? 2 : 1); ++h) {
-        if (page[h] < 0) continue;
-        const int row = static_cast<int>(cache_row(a.c, page[h], it.head, key0 + h * kPage16));
+        if (!on[h]) continue;
+        const int row = static_cast<int>(cache_row(a.c, page[h], head, key0 + h * kPage16));
         if constexpr (E4M3) {
           tma_load_2d(to + h * kPage16 * S::kRow, tm_k, bar, 0, row);
           tma_load_2d(to + S::kTile + h * kPage16 * S::kRow, tm_v, bar, 0, row);
@@ -179,6 +200,10 @@ __device__ __forceinline__ void produce(const CUtensorMap* tm_k, const CUtensorM
         slot = 0;
         phase ^= 1;
       }
+      since = global_timer();
+    } else if (active && global_timer() - since > kWaitLimitNs) {
+      report_error(a.status, kErrTimeout);
+      active = false;
     }
   }
 }
@@ -203,6 +228,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t exps0 = rings + kWarps * kRingBytes;
   const uint32_t bars0 = exps0 + kWarps * S::kStages * S::kExp;
   int64_t* pre = reinterpret_cast<int64_t*>(smem + kWarps * (kRingBytes + S::kStages * (S::kExp + 16)));
+  Seq* seqs = reinterpret_cast<Seq*>(pre + DS_VIT_MAX_SEQS + 1);
   auto full_of = [&](int w) { return bars0 + w * S::kStages * 16; };
   auto empty_of = [&](int w) { return full_of(w) + S::kStages * 8; };
   __shared__ int64_t part[kWarps + 1];
@@ -226,6 +252,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int64_t x = 0;
     if (s < a.b.n) {
       const Seq q = load_seq(a.b, a.c.page_shift, s, blockIdx.x == 0 ? a.status : nullptr);
+      seqs[s] = q;
       x = static_cast<int64_t>(seq_blocks<S::kKeyShift>(a, q).count) * (q.c > 0 ? a.c.kv_heads : 0);
     }
     int64_t inc = x;
@@ -252,11 +279,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   // Neighbouring shares go to different SMs.
   auto worker = [&](int w) { return static_cast<int64_t>(w) * gridDim.x + blockIdx.x; };
   if (warp == kWarps) {
+    Plan pl{pre, seqs, 0, 0};
     if (lane < kWarps && worker(lane) < W) {
-      const Plan pl{pre, share_begin(worker(lane), W, total), share_begin(worker(lane) + 1, W, total)};
-      produce<D, E4M3>(&tm_k, &tm_v, a, pl, rings + lane * kRingBytes, exps0 + lane * S::kStages * S::kExp,
-                       full_of(lane), empty_of(lane));
+      pl.begin = share_begin(worker(lane), W, total);
+      pl.end = share_begin(worker(lane) + 1, W, total);
     }
+    produce<D, E4M3>(&tm_k, &tm_v, a, pl, rings + lane * kRingBytes, exps0 + lane * S::kStages * S::kExp,
+                     full_of(lane), empty_of(lane));
     return;
   }
   const int64_t me = worker(warp);
@@ -264,7 +293,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) rec.headers[me] = SplitHeader{};
     return;
   }
-  const Plan pl{pre, share_begin(me, W, total), share_begin(me + 1, W, total)};
+  const Plan pl{pre, seqs, share_begin(me, W, total), share_begin(me + 1, W, total)};
   const uint32_t ring = rings + warp * kRingBytes, exps = exps0 + warp * S::kStages * S::kExp;
   const uint32_t full = full_of(warp), empty = empty_of(warp);
 
