@@ -11,8 +11,8 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libdsvit.so")
 SOURCES = ("api.cu", "gemm.cu", "gemm_pair.cu", "attention.cu", "attention_qwen.cu", "kernels.cu", "noalloc.cu",
-           "preprocess.cu", "qwen.cu", "cache.cu", "cache_attention.cu",
-           "cache_decode.cu")
+           "preprocess.cu", "qwen.cu", "cache.cu", "cache_decode.cu",
+           "cache_prefill.cu")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
          "--expt-relaxed-constexpr"]

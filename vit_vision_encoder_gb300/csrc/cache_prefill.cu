@@ -1,0 +1,821 @@
+// Attention over the paged cache for many rows (chunks of a prompt) on tcgen05.
+//
+// The query rows that share a K/V head (new tokens times query heads per K/V
+// head, token by token) are taken 256 at a time, as two 128-row tiles A and B
+// that share every tile of 128 keys; an item is one such group of rows, and the
+// unit of work is one key tile of an item.  All units are counted from the
+// lengths on the device and dealt to the CTAs, one per SM, in equal shares
+// (cache_plan.h): causal items of unequal depth, short chunks over long caches
+// and ragged batches all end together.  A CTA finishes the items that lie within
+// its share; the others leave records that join_kernel adds up.
+//
+// Roles: warps 0-7 run the softmax of tile A and warps 8-15 that of tile B, two
+// threads a row (16x32bx2 TMEM accesses, as in the bidirectional kernel); warp
+// 16 loads pages by TMA (a box per page and 64 dims) into a ring of key and
+// value tiles; warps 17 and 18 issue the MMAs of A and B:
+//   S_X = Q_X K_j^T     (M 128, N 128, K D)    smem x smem -> TMEM
+//   O_X += P_X V_j      (M 128, N D,   K 128)  TMEM x smem -> TMEM
+// P_X (16-bit pairs) takes the first half of S_X's columns, so S_X of the next
+// tile waits for P_X V_j; the other tile's MMAs and softmax fill that time.
+// Rows of Q are loaded by their softmax threads, so any group size fills the
+// tiles.
+//
+// e4m3 pages: warps 20-23 widen the raw tiles to fp16 in shared memory (the
+// conversion is exact; the rows of a tile are scaled by powers of two to the
+// tile's largest exponent E, and elements 2^-24 below it lose bits).  Scores are
+// scaled by 2^E(K); the weights are taken against the running maximum of score
+// plus E(V), the size of a contribution, and their sum is scaled back.  Query
+// rows are scaled to fp16's range like in the kernel for few rows.
+//
+// Keys that a row does not see are masked in its scores.  Value rows that no row
+// of the item sees are zeroed in shared memory (they may hold anything); where
+// rows of an item see different keys and a result is not finite, the row is
+// computed again from the keys that it does see (exact_row).
+#include "cache_rows.cuh"
+
+namespace dsvit {
+
+namespace {
+
+constexpr int kTile = 128;                  // rows of a query tile, keys of a key tile
+constexpr int kTileShift = 7;
+constexpr int kItemRows = 2 * kTile;
+constexpr int kWarpTma = 16, kWarpMma = 17; // 17: tile A, 18: tile B
+constexpr int kWarpConvert = 20;            // 20 .. 23 (e4m3)
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kTmemO = 256;            // S_A, S_B at 0, 128; O_A, O_B from here
+
+template <int D, bool E4M3>
+struct Cfg {
+  static constexpr int kThreads = E4M3 ? 768 : 608;
+  static constexpr int kBytes = kTile * D * 2;             // a 16-bit tile of 128 rows
+  static constexpr int kHalf = kTile * 128;                // 64 dims of it
+  static constexpr int kRawBytes = kTile * D;              // an e4m3 tile
+  static constexpr int kRing = E4M3 ? 3 : (D == 128 ? 5 : 8);
+  static constexpr int kRaw = E4M3 ? 3 : 0;
+  static constexpr int kOffKv = 2 * kBytes;                // after Q_A, Q_B
+  static constexpr int kOffRaw = kOffKv + kRing * kBytes;
+  static constexpr int kOffExp = kOffRaw + kRaw * kRawBytes;   // exponents of the raw tiles
+  static constexpr int kOffBar = kOffExp + kRaw * kTile;
+  static constexpr int kSmem = kOffBar + 512 + 1024;
+  static_assert(kSmem <= 232448, "shared memory");
+  static constexpr float kLag = E4M3 ? 14.f : 8.f;         // see Reference in the kernel for few rows
+  static constexpr float kLead = E4M3 ? 6.f : 0.f;
+};
+
+// Barrier slots.
+enum : int {
+  kBarQ = 0,                // [2] tile X's query rows are in shared memory
+  kBarKvFull = 2,           // [8]
+  kBarKvEmpty = 10,         // [8] released by both MMA warps
+  kBarRawFull = 18,         // [4]
+  kBarRawEmpty = 22,        // [4]
+  kBarSFull = 26,           // [2]
+  kBarPFull = 28,           // [2]
+  kBarPvDone = 30,          // [2]
+  kBarRagged = 32,          // a value tile with rows to zero has landed
+  kBarDrain = 33,           // [2]
+  kBarCount = 35
+};
+
+struct PrefillArgs {
+  AttentionArgs a;
+  Records rec;
+};
+
+// Where a CTA's share of the units begins, and how many it has.
+struct Start {
+  int s, k, head, b;
+  int64_t units, total, first;
+};
+
+__device__ __forceinline__ int items_of(const AttentionArgs& a, const Seq& q) {
+  return static_cast<int>((static_cast<int64_t>(q.c) * a.group + kItemRows - 1) / kItemRows);
+}
+
+// Positions of the first and the last row of item k of a sequence.
+__device__ __forceinline__ void item_positions(const AttentionArgs& a, const Seq& q, int k, int& p0, int& p1) {
+  const int64_t r0 = static_cast<int64_t>(k) * kItemRows;
+  const int64_t r1 = min(r0 + kItemRows, static_cast<int64_t>(q.c) * a.group) - 1;
+  p0 = q.kv - q.c + static_cast<int>(r0 / a.group);
+  p1 = q.kv - q.c + static_cast<int>(r1 / a.group);
+}
+
+__device__ __forceinline__ KeyBlocks item_blocks(const AttentionArgs& a, const Seq& q, int k) {
+  int p0, p1;
+  item_positions(a, q, k, p0, p1);
+  KeyBlocks kb = key_blocks(p0, p1, a.window, a.sinks, kTileShift);
+  if (kb.count == 0) kb.count = 1;          // nothing visible: one tile without keys, so that zeros get written
+  return kb;
+}
+
+__device__ __forceinline__ int window_start(const AttentionArgs& a, int p) {
+  return a.window != 0 && p >= a.window ? p - a.window + 1 : 0;
+}
+
+// A role's walk over the CTA's items, in the order sequence, item, head.
+struct Walk {
+  int s, k, head, b, end;     // tiles b .. end - 1 of the item are this CTA's
+  Seq q;
+  KeyBlocks kb;
+  int64_t left;               // units left, this item's included
+  bool begun, whole;          // tiles before b / all tiles are in other hands / here
+
+  __device__ __forceinline__ void enter(const AttentionArgs& a, int b0) {
+    kb = item_blocks(a, q, k);
+    b = b0;
+    end = left < kb.count - b ? b + static_cast<int>(left) : kb.count;
+    begun = b > 0;
+    whole = !begun && end == kb.count;
+  }
+  __device__ __forceinline__ void start(const AttentionArgs& a, const Start& st) {
+    s = st.s, k = st.k, head = st.head;
+    left = st.units;
+    q = left > 0 ? load_seq(a.b, a.c.page_shift, s, nullptr) : Seq{0, 0, 0};
+    if (left > 0) enter(a, st.b);
+  }
+  // To the next item; left must be positive afterwards for it to exist.
+  __device__ __forceinline__ void next(const AttentionArgs& a) {
+    left -= end - b;
+    if (left <= 0) return;
+    if (++head == a.c.kv_heads) {
+      head = 0;
+      if (++k == items_of(a, q)) {
+        k = 0;
+        do {
+          q = load_seq(a.b, a.c.page_shift, ++s, nullptr);
+        } while (q.c == 0);
+      }
+    }
+    enter(a, 0);
+  }
+};
+
+// The plan of the call, by all threads of a CTA in scratch shared memory: a
+// flat list of (sequence, item) pairs, each thread adding up a run of it.
+template <int kThreads>
+__device__ __forceinline__ Start make_plan(const AttentionArgs& a, uint8_t* scratch, int* status) {
+  int* items = reinterpret_cast<int*>(scratch);                                   // [n + 1] items before each sequence
+  int64_t* sums = reinterpret_cast<int64_t*>(scratch + 4 * (DS_VIT_MAX_SEQS + 2));// [kThreads] units of each run
+  Start* found = reinterpret_cast<Start*>(sums + kThreads);
+  __shared__ int64_t warp_sum[kThreads / 32];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  auto scan = [&](int64_t x, int64_t& total) {      // exclusive prefix over the block
+    int64_t inc = x;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t y = __shfl_up_sync(0xFFFFFFFFu, inc, o);
+      if (lane >= o) inc += y;
+    }
+    if (lane == 31) warp_sum[warp] = inc;
+    __syncthreads();
+    int64_t before = 0;
+    total = 0;
+    for (int w = 0; w < kThreads / 32; ++w) {
+      if (w < warp) before += warp_sum[w];
+      total += warp_sum[w];
+    }
+    __syncthreads();
+    return before + inc - x;
+  };
+  int64_t all = 0;
+  for (int s0 = 0; s0 < a.b.n; s0 += kThreads) {
+    const int s = s0 + tid;
+    int64_t x = 0, t;
+    if (s < a.b.n) x = items_of(a, load_seq(a.b, a.c.page_shift, s, status));
+    const int64_t before = scan(x, t);
+    if (s < a.b.n) items[s] = static_cast<int>(all + before);
+    all += t;
+  }
+  if (tid == 0) items[a.b.n] = static_cast<int>(all);
+  __syncthreads();
+  // This thread's run of the list, and its units.
+  const int i0 = static_cast<int>(all * tid / kThreads), i1 = static_cast<int>(all * (tid + 1) / kThreads);
+  int s_run = 0;
+  if (i0 < i1) {
+    int lo = 0, hi = a.b.n - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (items[mid] <= i0)
+        lo = mid;
+      else
+        hi = mid - 1;
+    }
+    s_run = lo;
+  }
+  auto walk = [&](auto&& each) {
+    int s = s_run;
+    Seq q = load_seq(a.b, a.c.page_shift, s, nullptr);
+    for (int i = i0; i < i1; ++i) {
+      while (i >= items[s + 1]) q = load_seq(a.b, a.c.page_shift, ++s, nullptr);
+      if (!each(s, i - items[s], item_blocks(a, q, i - items[s]).count)) return;
+    }
+  };
+  int64_t mine = 0, total;
+  if (i0 < i1)
+    walk([&](int, int, int count) {
+      mine += static_cast<int64_t>(count) * a.c.kv_heads;
+      return true;
+    });
+  int64_t at = scan(mine, total);
+  const int64_t grid = gridDim.x, W = total < grid ? total : grid;
+  const int64_t first = blockIdx.x < W ? share_begin(blockIdx.x, W, total) : 0;
+  const int64_t units = blockIdx.x < W ? share_begin(blockIdx.x + 1, W, total) - first : 0;
+  if (tid == 0) *found = Start{0, 0, 0, 0, units, total, first};
+  __syncthreads();
+  if (units > 0 && first >= at && first < at + mine)
+    walk([&](int s, int k, int count) {
+      const int64_t here = static_cast<int64_t>(count) * a.c.kv_heads;
+      if (first < at + here) {
+        const int64_t r = first - at;
+        found->s = s;
+        found->k = k;
+        found->head = static_cast<int>(r / count);
+        found->b = static_cast<int>(r % count);
+        return false;
+      }
+      at += here;
+      return true;
+    });
+  __syncthreads();
+  const Start st = *found;
+  __syncthreads();
+  return st;
+}
+
+__device__ __forceinline__ uint64_t f2(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void f2_split(uint64_t v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t f2_fma(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+// Address of 16-byte piece `piece` (of D / 8) of row r in a 16-bit tile.
+template <int D, bool E4M3>
+__device__ __forceinline__ uint32_t tile_piece(uint32_t tile, int r, int piece) {
+  return tile + (piece >> 3) * Cfg<D, E4M3>::kHalf + r * 128 + (((piece & 7) ^ (r & 7)) << 4);
+}
+
+template <int D, bool E4M3>
+__global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
+    prefill_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                   const __grid_constant__ PrefillArgs p) {
+  using C = Cfg<D, E4M3>;
+  constexpr int kHalves = D / 64;
+  const AttentionArgs& a = p.a;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + kBarCount);
+  volatile int* tile_exp = reinterpret_cast<volatile int*>(bars + kBarCount + 1);   // [8] K, [8] V: E of recent tiles
+  const uint32_t base = smem_u32(smem), bar0 = smem_u32(bars);
+  auto bar = [&](int i) { return bar0 + 8u * static_cast<uint32_t>(i); };
+  auto sQ = [&](int x) { return base + x * C::kBytes; };
+  auto sKv = [&](int i) { return base + C::kOffKv + i * C::kBytes; };
+  auto sRaw = [&](int i) { return base + C::kOffRaw + i * C::kRawBytes; };
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int x = 0; x < 2; ++x) {
+      mbar_init(bar(kBarQ + x), 256);
+      mbar_init(bar(kBarSFull + x), 1);
+      mbar_init(bar(kBarPFull + x), 256);
+      mbar_init(bar(kBarPvDone + x), 1);
+      mbar_init(bar(kBarDrain + x), 1);
+    }
+    for (int i = 0; i < C::kRing; ++i) {
+      mbar_init(bar(kBarKvFull + i), E4M3 ? 4 : 1);
+      mbar_init(bar(kBarKvEmpty + i), 2);
+    }
+    for (int i = 0; i < C::kRaw; ++i) {
+      mbar_init(bar(kBarRawFull + i), 1);
+      mbar_init(bar(kBarRawEmpty + i), 4);
+    }
+    mbar_init(bar(kBarRagged), 1);
+    fence_barrier_init();
+  }
+  if (warp == kWarpTma) {
+    if (lane == 0) {
+      prefetch_tensormap(&tm_k);
+      prefetch_tensormap(&tm_v);
+    }
+    tmem_alloc(smem_u32(tmem_slot), kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  grid_dep_launch();
+  grid_dep_wait();
+  const Start st = make_plan<C::kThreads>(a, smem + C::kOffKv, blockIdx.x == 0 ? a.status : nullptr);
+  fence_proxy_async_smem();                 // the scratch becomes the ring
+  __syncthreads();
+  __shared__ int consumed[2];
+  int issued = 0;                           // ring or raw tiles whose loads were issued
+
+  if constexpr (E4M3) {
+    // 24 warps start with 80 registers each; 16 x 96 + 8 x 48 is the same sum.
+    if (warp < kWarpTma)
+      registers_inc<96>();
+    else
+      registers_dec<48>();
+  }
+  if (warp == kWarpTma) {
+    // ------------------------------------------------------------ TMA producer
+    // Lane i loads page i of a tile (of 128 / page pages).
+    const int page = 1 << a.c.page_shift, pages = kTile >> a.c.page_shift;
+    constexpr int kDepth = E4M3 ? C::kRaw : C::kRing;
+    constexpr int kFull = E4M3 ? kBarRawFull : kBarKvFull, kEmpty = E4M3 ? kBarRawEmpty : kBarKvEmpty;
+    int slot = 0, ragged = 0;
+    uint32_t phase = 1;
+    bool ok = true;
+    Walk w;
+    w.start(a, st);
+    while (ok && w.left > 0) {
+      int p0, p1;
+      item_positions(a, w.q, w.k, p0, p1);
+      const int lo = window_start(a, p0);
+      auto any = [&](int j0, int j1) { return j0 <= p1 && (j1 >= lo || j0 < a.sinks); };   // a key of j0 .. j1 is seen
+      auto look = [&](int b) {
+        const int key0 = w.kb.at(b) << kTileShift, j = key0 + lane * page;
+        if (lane >= pages || !any(j, j + page - 1)) return -2;
+        return __ldg(a.b.table + static_cast<int64_t>(w.s) * a.b.table_cols + (j >> a.c.page_shift));
+      };
+      int next = look(w.b);
+      for (int b = w.b; b < w.end; ++b) {
+        const int entry = next;
+        if (b + 1 < w.end) next = look(b + 1);
+        const bool on = entry >= 0 && entry < a.c.n_pages;
+        if (!on && entry != -2) report_error(a.status, DS_VIT_ERANGE);
+        const int loaded = __popc(__ballot_sync(0xFFFFFFFFu, on));
+        const int key0 = w.kb.at(b) << kTileShift;
+        const int row = on ? static_cast<int>(cache_row(a.c, entry, w.head, 0)) : 0;
+        // A value tile with rows that nobody sees: they are zeroed before it is used.
+        const bool whole = any(key0, key0) && key0 + kTile - 1 <= p1 && (key0 >= lo || key0 + kTile <= a.sinks) &&
+                           loaded == pages;
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv) {
+          ok = __all_sync(0xFFFFFFFFu, mbar_wait(bar(kEmpty + slot), phase, a.status));
+          if (!ok) break;
+          const bool fix = !E4M3 && kv == 1 && !whole;
+          const uint32_t full = fix ? bar(kBarRagged) : bar(kFull + slot);
+          const uint32_t per = page * D * (E4M3 ? 1 : 2) + (E4M3 ? page : 0);
+          if (lane == 0) mbar_expect_tx(full, loaded * per);
+          __syncwarp();
+          if (on) {
+            const CUtensorMap* tm = kv == 0 ? &tm_k : &tm_v;
+            if constexpr (E4M3) {
+              tma_load_2d(sRaw(slot) + lane * page * D, tm, full, 0, row);
+              bulk_load(base + C::kOffExp + slot * kTile + lane * page, (kv == 0 ? a.c.k_exp : a.c.v_exp) + row, page,
+                        full);
+            } else {
+#pragma unroll
+              for (int h = 0; h < kHalves; ++h)
+                tma_load_2d(sKv(slot) + h * C::kHalf + lane * page * 128, tm, full, 64 * h, row);
+            }
+          }
+          __syncwarp();
+          if (fix) {
+            ok = __all_sync(0xFFFFFFFFu, mbar_wait(bar(kBarRagged), ragged & 1, a.status));
+            if (!ok) break;
+            ++ragged;
+            const uint32_t loads = __ballot_sync(0xFFFFFFFFu, on);
+            for (int x = lane; x < kTile * 8 * kHalves; x += 32) {
+              const int r = (x >> 3) & (kTile - 1), j = key0 + r;
+              if (!any(j, j) || !((loads >> (r >> a.c.page_shift)) & 1u)) sts128(sKv(slot) + 16 * x, make_uint4(0, 0, 0, 0));
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(kFull + slot));
+            __syncwarp();
+          }
+          ++issued;
+          if (++slot == kDepth) {
+            slot = 0;
+            phase ^= 1;
+          }
+        }
+        if (!ok) break;
+      }
+      w.next(a);
+    }
+  } else if (warp == kWarpMma || warp == kWarpMma + 1) {
+    // ------------------------------------------------------------ MMA issuer of tile X
+    const int x = warp - kWarpMma;
+    if (lane == 0) {
+      constexpr uint32_t f16_bits = (1u << 7) | (1u << 10);   // bf16 marks of A and B in the instruction descriptor
+      constexpr uint32_t id_s = idesc_bf16_f32(128, 128, false, false) & ~(E4M3 ? f16_bits : 0u);
+      constexpr uint32_t id_o = idesc_bf16_f32(128, D, false, true) & ~(E4M3 ? f16_bits : 0u);   // V is MN-major
+      const uint32_t tS = tmem + x * 128, tO = tmem + kTmemO + x * D;
+      const uint64_t dq = sdesc_sw128(sQ(x), 16, 1024);
+      const uint64_t dk0 = sdesc_sw128(sKv(0), 16, 1024);
+      const uint64_t dv0 = sdesc_sw128(sKv(0), C::kHalf, 1024);
+      int slot = 0, used = 0;
+      uint32_t phase = 0, q_phase = 0, step = 0;
+      bool ok = true;
+      auto advance = [&]() {
+        ++used;
+        if (++slot == C::kRing) {
+          slot = 0;
+          phase ^= 1;
+        }
+      };
+      auto issue_s = [&]() {
+        const uint64_t dk = dk0 + static_cast<uint64_t>(slot * (C::kBytes >> 4));
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          const uint64_t off = (k >> 2) * (C::kHalf >> 4) + 2 * (k & 3);
+          umma_bf16(tS, dq + off, dk + off, id_s, k != 0);
+        }
+        umma_commit(bar(kBarSFull + x));
+        umma_commit(bar(kBarKvEmpty + slot));
+        advance();
+      };
+      Walk w;
+      w.start(a, st);
+      while (ok && w.left > 0) {
+        const int64_t rows = static_cast<int64_t>(w.q.c) * a.group - static_cast<int64_t>(w.k) * kItemRows;
+        if (rows <= x * kTile) {
+          // No rows in this tile: the buffers are only handed back.
+          for (int j = 0; j < 2 * (w.end - w.b); ++j) {
+            ok = mbar_wait(bar(kBarKvFull + slot), phase, a.status);
+            if (!ok) break;
+            mbar_arrive(bar(kBarKvEmpty + slot));
+            advance();
+          }
+          w.next(a);
+          continue;
+        }
+        ok = mbar_wait(bar(kBarQ + x), q_phase, a.status) && mbar_wait(bar(kBarKvFull + slot), phase, a.status);
+        if (!ok) break;
+        q_phase ^= 1;
+        tc_fence_after();
+        issue_s();
+        for (int b = w.b; b < w.end; ++b) {
+          ok = mbar_wait(bar(kBarPFull + x), step & 1, a.status) && mbar_wait(bar(kBarKvFull + slot), phase, a.status);
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t dv = dv0 + static_cast<uint64_t>(slot * (C::kBytes >> 4));
+#pragma unroll
+          for (int k = 0; k < kTile / 16; ++k)
+            umma_bf16_ts(tO, tS + k * 8, dv + 128 * k, id_o, (b != w.b) | (k != 0));   // 16 rows = 2048 B
+          umma_commit(bar(kBarPvDone + x));
+          umma_commit(bar(kBarKvEmpty + slot));
+          advance();
+          if (b + 1 < w.end) {
+            // S_X overwrites P_X: its product must be complete.
+            ok = mbar_wait(bar(kBarKvFull + slot), phase, a.status) && mbar_wait(bar(kBarPvDone + x), step & 1, a.status);
+            if (!ok) break;
+            tc_fence_after();
+            issue_s();
+          }
+          ++step;
+        }
+        w.next(a);
+      }
+      consumed[x] = used;
+      // All MMAs of this warp complete before TMEM is released.
+      umma_commit(bar(kBarDrain + x));
+      mbar_wait(bar(kBarDrain + x), 0, a.status);
+    }
+  } else if (E4M3 && warp >= kWarpConvert) {
+    // ------------------------------------------------------------ e4m3 -> fp16
+    const int tid = threadIdx.x - 32 * kWarpConvert;
+    int raw = 0, slot = 0, tile = 0;
+    uint32_t raw_phase = 0, phase = 1;
+    bool ok = true;
+    Walk w;
+    w.start(a, st);
+    while (ok && w.left > 0) {
+      int p0, p1;
+      item_positions(a, w.q, w.k, p0, p1);
+      const int lo = window_start(a, p0);
+      auto any = [&](int j) { return j <= p1 && (j >= lo || j < a.sinks); };
+      for (int b = w.b; b < w.end; ++b, ++tile) {
+        const int key0 = w.kb.at(b) << kTileShift;
+#pragma unroll 1
+        for (int kv = 0; kv < 2; ++kv) {
+          ok = __all_sync(0xFFFFFFFFu, mbar_wait(bar(kBarRawFull + raw), raw_phase, a.status));
+          if (!ok) break;
+          const uint8_t* ex = smem + C::kOffExp + raw * kTile;
+          // The largest exponent among rows that some row sees (255 marks a NaN row).
+          int top = 0;
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            const int r = 32 * y + lane, e = ex[r];
+            if (any(key0 + r) && e != 255) top = max(top, e);
+          }
+          top = __reduce_max_sync(0xFFFFFFFFu, top);
+          if (top == 0) top = 127;
+          ok = __all_sync(0xFFFFFFFFu, mbar_wait(bar(kBarKvEmpty + slot), phase, a.status));
+          if (!ok) break;
+          if (tid == 0) tile_exp[8 * kv + (tile & 7)] = top - 127;
+          constexpr int kPieces = D / 16;
+#pragma unroll 4
+          for (int x = tid; x < kTile * kPieces; x += 128) {
+            const int r = x / kPieces, piece = x % kPieces;
+            const uint32_t swz = D == 128 ? piece ^ (r & 7) : piece ^ ((r >> 1) & 3);
+            const uint4 v = lds128(sRaw(raw) + r * D + 16 * swz);
+            const int e = ex[r], down = top - e;
+            uint32_t f = e == 255 ? 0x3C00u : down <= 14 ? (15u - down) << 10 : down <= 24 ? 1u << (24 - down) : 0u;
+            f |= f << 16;
+            const bool on = any(key0 + r);
+            uint4 u0, u1;
+            auto widen = [&](uint32_t two) { return on ? mul_f16x2(e4m3x2_to_f16x2(two), f) : 0u; };
+            u0.x = widen(v.x & 0xFFFFu), u0.y = widen(v.x >> 16), u0.z = widen(v.y & 0xFFFFu), u0.w = widen(v.y >> 16);
+            u1.x = widen(v.z & 0xFFFFu), u1.y = widen(v.z >> 16), u1.z = widen(v.w & 0xFFFFu), u1.w = widen(v.w >> 16);
+            // Lanes of the two halves of the dims store their two pieces in opposite orders: no bank conflicts.
+            const int first = (piece >> 2) & 1;
+            sts128(tile_piece<D, E4M3>(sKv(slot), r, 2 * piece + first), first ? u1 : u0);
+            sts128(tile_piece<D, E4M3>(sKv(slot), r, 2 * piece + 1 - first), first ? u0 : u1);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(bar(kBarRawEmpty + raw));
+            mbar_arrive(bar(kBarKvFull + slot));
+          }
+          if (++raw == C::kRaw) {
+            raw = 0;
+            raw_phase ^= 1;
+          }
+          if (++slot == C::kRing) {
+            slot = 0;
+            phase ^= 1;
+          }
+        }
+        if (!ok) break;
+      }
+      w.next(a);
+    }
+  } else if (warp < kWarpTma) {
+    // ------------------------------------------------------------ softmax (warps 0-15)
+    const int x = warp >> 3;                 // query tile A (0) or B (1)
+    const int row0 = (warp & 3) * 32 + ((warp >> 2) & 1) * 16;   // the warp's first row
+    const int h = lane >> 4;                 // 64-key half of the score tile
+    const int r = row0 + (lane & 15);        // row inside the tile == TMEM lane
+    const uint32_t lane_sel = static_cast<uint32_t>(row0) << 16;
+    const uint32_t tS = tmem + x * 128 + lane_sel;
+    const uint32_t tO = tmem + kTmemO + x * D + lane_sel;
+    uint32_t step = 0;
+    int tile = 0;
+    bool ok = true;
+    SplitHeader header{};
+    Walk w;
+    w.start(a, st);
+    int64_t at = st.first;
+    while (ok && w.left > 0) {
+      const int64_t rho64 = static_cast<int64_t>(w.k) * kItemRows + x * kTile;    // first row of the tile
+      const int64_t R = static_cast<int64_t>(w.q.c) * a.group;
+      if (rho64 >= R) {
+        tile += w.end - w.b;
+        at += w.end - w.b;
+        w.next(a);
+        continue;
+      }
+      const int rho = static_cast<int>(rho64) + r;
+      const bool on = rho < R;
+      const int i = rho / a.group, hq = w.head * a.group + (rho - i * a.group);
+      const int first = w.q.kv - w.q.c;
+      const int pos = on ? first + i : -1;
+      // Positions of the tile's first and last rows, for tiles without a mask.
+      const int pa = first + static_cast<int>(rho64 / a.group);
+      const int pb = first + static_cast<int>((min(rho64 + kTile, R) - 1) / a.group);
+      const int lo = window_start(a, pos), lo_b = window_start(a, pb);
+      // ---- this thread's half of its query row
+      float c0 = a.scale_log2;
+      {
+        uint4 v[D / 16];
+        const uint4* src = reinterpret_cast<const uint4*>(a.q + (w.q.row0 + i) * a.q_stride + hq * D + h * (D / 2));
+#pragma unroll
+        for (int y = 0; y < D / 16; ++y) v[y] = on ? __ldg(src + y) : make_uint4(0, 0, 0, 0);
+        if constexpr (E4M3) {
+          uint32_t top = 0;
+#pragma unroll
+          for (int y = 0; y < D / 16; ++y)
+            top = __vmaxu2(top, __vmaxu2(__vmaxu2(v[y].x & 0x7FFF7FFFu, v[y].y & 0x7FFF7FFFu),
+                                         __vmaxu2(v[y].z & 0x7FFF7FFFu, v[y].w & 0x7FFF7FFFu)));
+          top = max(top & 0xFFFFu, top >> 16);
+          top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 16));
+          // The largest's exponent field E: times 2^(141 - E), in two steps of normal powers of two.
+          const int E = max(static_cast<int>(top >> 7), 1), up = 141 - E, half = up / 2;
+          const float f0 = __int_as_float((127 + half) << 23), f1 = __int_as_float((127 + up - half) << 23);
+          c0 = a.scale_log2 * __int_as_float((127 - half) << 23) * __int_as_float((127 - up + half) << 23);
+          auto to16 = [&](uint32_t two) { return pack_f16x2(bf16lo(two) * f0 * f1, bf16hi(two) * f0 * f1); };
+#pragma unroll
+          for (int y = 0; y < D / 16; ++y) v[y] = make_uint4(to16(v[y].x), to16(v[y].y), to16(v[y].z), to16(v[y].w));
+        }
+#pragma unroll
+        for (int y = 0; y < D / 16; ++y) sts128(tile_piece<D, E4M3>(sQ(x), r, h * (D / 16) + y), v[y]);
+      }
+      fence_proxy_async_smem();
+      mbar_arrive(bar(kBarQ + x));
+
+      float m = -INFINITY, l = 0.f;
+      for (int b = w.b; b < w.end; ++b, ++tile, ++step) {
+        const int key0 = w.kb.at(b) << kTileShift;
+        const bool open = key0 + kTile - 1 <= pa && (key0 >= lo_b || key0 + kTile <= a.sinks);
+        if (!mbar_wait(bar(kBarSFull + x), step & 1, a.status)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        float c = c0, ev = 0.f, unit = 1.f;
+        if constexpr (E4M3) {
+          // E(V) is known once the value tile is there (it stays until P V).
+          const uint32_t n = 2 * static_cast<uint32_t>(tile) + 1;
+          if (!mbar_wait(bar(kBarKvFull + n % C::kRing), (n / C::kRing) & 1, a.status)) {
+            ok = false;
+            break;
+          }
+          const int ek = tile_exp[tile & 7], e = tile_exp[8 + (tile & 7)];
+          // Not zero: a masked score of -inf stays -inf.
+          c = fmaxf(c * __int_as_float((ek + 127) << 23), 1e-35f);
+          ev = static_cast<float>(e);
+          unit = __int_as_float((127 - e) << 23);
+        }
+        uint32_t sr[64];
+        float top = tmem_ld32_max_x2<64>(tS, sr), top2 = tmem_ld32_max_x2<64>(tS + 32, sr + 32);
+        tmem_wait_ld();
+        top = fmaxf(tmem_after_wait(top), tmem_after_wait(top2));
+        if (!open) {
+          // Key i of this half is seen when i <= last and (i >= from or i < keep).
+          const int j0 = key0 + 64 * h;
+          const int last = pos - j0, from = lo - j0, keep = a.sinks - j0;
+          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int y = 0; y < 64; ++y) {
+            if (!(y <= last && (y >= from || y < keep))) sr[y] = __float_as_uint(-INFINITY);
+            mx[y & 3] = fmaxf(mx[y & 3], __uint_as_float(sr[y]));
+          }
+          top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+        }
+        // Both threads of the row derive the same reference.
+        top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 16));
+        const float reach = fmaf(top, c, ev);
+        float m_new = m, alpha = 1.f;
+        if (reach > m + C::kLag) {           // always true on the first visible key (m = -inf)
+          m_new = reach - C::kLead;
+          alpha = ex2_approx(m - m_new);
+        }
+        const float off = m_new == -INFINITY ? 0.f : ev - m_new;
+        const uint64_t c2 = f2(c, c), nm2 = f2(off, off);
+        uint64_t acc[4] = {f2(0.f, 0.f), f2(0.f, 0.f), f2(0.f, 0.f), f2(0.f, 0.f)};
+        uint32_t pk[32];
+#pragma unroll
+        for (int y = 0; y < 32; ++y) {
+          const uint64_t z = f2_fma(f2(__uint_as_float(sr[2 * y]), __uint_as_float(sr[2 * y + 1])), c2, nm2);
+          float z0, z1;
+          f2_split(z, z0, z1);
+          z0 = ex2_approx(z0);
+          z1 = ex2_approx(z1);
+          acc[y & 3] = f2_add(acc[y & 3], f2(z0, z1));
+          // The product's operand: weights in 16 bits (their sum stays in fp32).
+          pk[y] = E4M3 ? pack_f16x2(z0, z1) : pack_bf16x2(z0, z1);
+        }
+        const uint64_t s2 = f2_add(f2_add(acc[0], acc[1]), f2_add(acc[2], acc[3]));
+        float s0, s1;
+        f2_split(s2, s0, s1);
+        l = l * alpha + (s0 + s1) * unit;    // this half's share of the row sum
+        tmem_st32_x2<32>(tS, pk);
+        // O_X was last written by the product that S_X waited for: it is complete.
+        if (b != w.b && __any_sync(0xFFFFFFFFu, alpha != 1.f)) {
+#pragma unroll
+          for (int y = 0; y < D / 64; ++y) {
+            uint32_t o[32];
+            tmem_ld32_x2<D / 2>(tO + 32 * y, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int z = 0; z < 32; ++z) o[z] = __float_as_uint(__uint_as_float(o[z]) * alpha);
+            tmem_st32_x2<D / 2>(tO + 32 * y, o);
+          }
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(bar(kBarPFull + x));
+        m = m_new;
+      }
+      if (!ok || !mbar_wait(bar(kBarPvDone + x), (step - 1) & 1, a.status)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      // ---- the item's end: finished here, or a record for the join
+      l += __shfl_xor_sync(0xFFFFFFFFu, l, 16);
+      if (!w.begun && !w.whole) {
+        const int64_t W = st.total < gridDim.x ? st.total : gridDim.x;
+        header = SplitHeader{static_cast<int>(share_of(at - w.b + w.kb.count - 1, W, st.total) - blockIdx.x) + 1, w.s,
+                             w.head, w.k * kItemRows, w.q, 0};
+      }
+      const float inv = pos < 0 ? 0.f : 1.f / l;
+      float* rec = p.rec.at(blockIdx.x, w.begun ? 0 : 1);
+      const int rr = x * kTile + r;          // row of the record
+      bool bad = false;
+#pragma unroll
+      for (int y = 0; y < D / 64; ++y) {
+        uint32_t o[32];
+        tmem_ld32_x2<D / 2>(tO + 32 * y, o);
+        tmem_wait_ld();
+        const int d0 = h * (D / 2) + 32 * y;
+        if (!on) continue;
+        if (w.whole) {
+          uint4* dst = reinterpret_cast<uint4*>(a.out + (w.q.row0 + i) * a.out_stride + hq * D + d0);
+          uint32_t pk[16];
+#pragma unroll
+          for (int z = 0; z < 16; ++z) {
+            const float o0 = __uint_as_float(o[2 * z]) * inv, o1 = __uint_as_float(o[2 * z + 1]) * inv;
+            bad |= not_finite(o0) || not_finite(o1);
+            pk[z] = pack_bf16x2(o0, o1);
+          }
+#pragma unroll
+          for (int z = 0; z < 4; ++z) dst[z] = make_uint4(pk[4 * z], pk[4 * z + 1], pk[4 * z + 2], pk[4 * z + 3]);
+        } else {
+          uint4* dst = reinterpret_cast<uint4*>(rec + static_cast<int64_t>(rr) * D + d0);
+#pragma unroll
+          for (int z = 0; z < 8; ++z) dst[z] = make_uint4(o[4 * z], o[4 * z + 1], o[4 * z + 2], o[4 * z + 3]);
+        }
+      }
+      tc_fence_before();
+      if (!w.whole && on && h == 0) {
+        p.rec.max_of(rec, D)[rr] = m;
+        p.rec.sum_of(rec, D)[rr] = l;
+      }
+      if (w.q.c > 1) {
+        uint32_t redo = __ballot_sync(0xFFFFFFFFu, bad);
+        redo = (redo | (redo >> 16)) & 0xFFFFu;
+        while (redo) {
+          __syncwarp();
+          const int y = __ffs(static_cast<int>(redo)) - 1;
+          redo &= redo - 1;
+          const int rho_y = static_cast<int>(rho64) + row0 + y, iy = rho_y / a.group;
+          exact_row<D, E4M3>(a, w.s, w.q.row0, first + iy, iy, w.head * a.group + rho_y - iy * a.group, lane);
+        }
+      }
+      at += w.end - w.b;
+      w.next(a);
+    }
+    if (threadIdx.x == 0) p.rec.headers[blockIdx.x] = ok ? header : SplitHeader{};
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kWarpTma && status_failed(a.status)) {
+    // After an error: wait (bounded) for the loads that may still be in flight,
+    // so no TMA write lands in shared memory after the CTA has exited.
+    constexpr int kDepth = E4M3 ? C::kRaw : C::kRing;
+    constexpr int kFull = E4M3 ? kBarRawFull : kBarKvFull;
+    const int done = E4M3 ? max(0, issued - kDepth) : min(consumed[0], consumed[1]);
+    for (int j = done; j < issued; ++j)
+      if (!mbar_wait(bar(kFull + j % kDepth), (j / kDepth) & 1, nullptr)) break;
+  }
+  __syncthreads();
+  if (warp == kWarpTma) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+template <int D, bool E4M3>
+int launch(const AttentionArgs& a, void* ws, cudaStream_t stream) {
+  using C = Cfg<D, E4M3>;
+  CUtensorMap tk, tv;
+  const uint64_t rows = static_cast<uint64_t>(a.c.n_pages) * a.c.kv_heads << a.c.page_shift;
+  const uint64_t cols = E4M3 ? D / 2 : D;    // in 16-bit units
+  const uint32_t box = 1u << a.c.page_shift;
+  auto map = [&](CUtensorMap* m, const void* q) {
+    return cols == 32 ? make_tmap_bf16_sw64(m, q, rows, cols, box) : make_tmap_bf16(m, q, rows, cols, box);
+  };
+  if (!map(&tk, a.c.k) || !map(&tv, a.c.v)) return DS_VIT_ECUDA;
+  if (allow_smem(reinterpret_cast<const void*>(prefill_kernel<D, E4M3>), C::kSmem) != cudaSuccess) return DS_VIT_ECUDA;
+  const int grid = num_sms();
+  const PrefillArgs p{a, records_in(ws, grid, kItemRows, D)};
+  cudaError_t e = launch_pdl(prefill_kernel<D, E4M3>, dim3(grid), dim3(C::kThreads), C::kSmem, stream, tk, tv, p);
+  if (e == cudaSuccess) e = launch_join<D, E4M3>(a, p.rec, grid, grid, stream);
+  if (e != cudaSuccess) cudaGetLastError();
+  return e == cudaSuccess ? DS_VIT_OK : DS_VIT_ECUDA;
+}
+
+}  // namespace
+
+size_t cache_prefill_workspace(int head_dim) { return records_bytes(num_sms(), kItemRows, head_dim); }
+
+int launch_cache_prefill(const AttentionArgs& a, int head_dim, bool e4m3, void* ws, cudaStream_t stream) {
+  if (head_dim == 128) return e4m3 ? launch<128, true>(a, ws, stream) : launch<128, false>(a, ws, stream);
+  return e4m3 ? launch<64, true>(a, ws, stream) : launch<64, false>(a, ws, stream);
+}
+
+}  // namespace dsvit

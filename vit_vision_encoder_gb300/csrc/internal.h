@@ -197,11 +197,12 @@ int launch_overlay_rows(bf16* hidden, int64_t n_hidden, int width, const int32_t
                         const int32_t* src, int64_t n, const bf16* embeds, int64_t n_embeds, const bf16* sentinel,
                         int* status, cudaStream_t stream);
 
-// Attention of new tokens over the paged cache (cache.cuh).
+// Attention of new tokens over the paged cache (cache.cuh).  Workspaces hold
+// the partial results of work split between workers.
 struct AttentionArgs;
-// Workspace of one call: the partial results of work split between CTAs.
-size_t cache_attention_workspace(int head_dim, int group, int max_rows);
-int launch_cache_attention(const AttentionArgs& a, int head_dim, bool e4m3, void* ws, cudaStream_t stream);
+// The path for any number of rows.
+size_t cache_prefill_workspace(int head_dim);
+int launch_cache_prefill(const AttentionArgs& a, int head_dim, bool e4m3, void* ws, cudaStream_t stream);
 // The path for at most kDecodeRows query rows per K/V head and sequence.
 constexpr int kDecodeRows = 16;
 size_t cache_decode_workspace(int head_dim, int rows);
