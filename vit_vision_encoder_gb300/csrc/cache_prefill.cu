@@ -75,7 +75,8 @@ enum : int {
   kBarPvDone = 30,          // [2]
   kBarRagged = 32,          // a value tile with rows to zero has landed
   kBarDrain = 33,           // [2]
-  kBarCount = 35
+  kBarTurn = 35,            // [2 tiles][4 quadrants]: the quadrant's warps of tile X finished the exponents of a step
+  kBarCount = 43
 };
 
 struct PrefillArgs {
@@ -295,6 +296,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
       mbar_init(bar(kBarPFull + x), 256);
       mbar_init(bar(kBarPvDone + x), 1);
       mbar_init(bar(kBarDrain + x), 1);
+      for (int y = 0; y < 4; ++y) mbar_init(bar(kBarTurn + 4 * x + y), 64);
     }
     for (int i = 0; i < C::kRing; ++i) {
       mbar_init(bar(kBarKvFull + i), E4M3 ? 4 : 1);
@@ -327,13 +329,9 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
   __shared__ int consumed[2];
   int issued = 0;                           // ring or raw tiles whose loads were issued
 
-  if constexpr (E4M3) {
-    // 24 warps start with 80 registers each; 16 x 96 + 8 x 48 is the same sum.
-    if (warp < kWarpTma)
-      registers_inc<96>();
-    else
-      registers_dec<48>();
-  }
+  // e4m3: 24 warps start with 80 registers each; 16 x 96 + 8 x 48 is the same sum.
+  if (warp >= kWarpTma && (!E4M3 || warp < kWarpConvert)) {
+    if constexpr (E4M3) registers_dec<48>();
   if (warp == kWarpTma) {
     // ------------------------------------------------------------ TMA producer
     // Lane i loads page i of a tile (of 128 / page pages).
@@ -492,7 +490,9 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
       umma_commit(bar(kBarDrain + x));
       mbar_wait(bar(kBarDrain + x), 0, a.status);
     }
+  }
   } else if (E4M3 && warp >= kWarpConvert) {
+    if constexpr (E4M3) registers_dec<48>();
     // ------------------------------------------------------------ e4m3 -> fp16
     const int tid = threadIdx.x - 32 * kWarpConvert;
     int raw = 0, slot = 0, tile = 0;
@@ -562,7 +562,8 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
       }
       w.next(a);
     }
-  } else if (warp < kWarpTma) {
+  } else {
+    if constexpr (E4M3) registers_inc<96>();
     // ------------------------------------------------------------ softmax (warps 0-15)
     const int x = warp >> 3;                 // query tile A (0) or B (1)
     const int row0 = (warp & 3) * 32 + ((warp >> 2) & 1) * 16;   // the warp's first row
@@ -571,22 +572,21 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
     const uint32_t lane_sel = static_cast<uint32_t>(row0) << 16;
     const uint32_t tS = tmem + x * 128 + lane_sel;
     const uint32_t tO = tmem + kTmemO + x * D + lane_sel;
-    uint32_t step = 0;
+    uint32_t step = 0, turn = 0;             // steps of this tile, and those that both tiles took
     int tile = 0;
     bool ok = true;
-    SplitHeader header{};
+    if (threadIdx.x == 0) p.rec.headers[blockIdx.x] = SplitHeader{};
     Walk w;
     w.start(a, st);
-    int64_t at = st.first;
     while (ok && w.left > 0) {
       const int64_t rho64 = static_cast<int64_t>(w.k) * kItemRows + x * kTile;    // first row of the tile
       const int64_t R = static_cast<int64_t>(w.q.c) * a.group;
       if (rho64 >= R) {
         tile += w.end - w.b;
-        at += w.end - w.b;
         w.next(a);
         continue;
       }
+      const bool both = R - static_cast<int64_t>(w.k) * kItemRows > kTile;       // tile B has rows too
       const int rho = static_cast<int>(rho64) + r;
       const bool on = rho < R;
       const int i = rho / a.group, hq = w.head * a.group + (rho - i * a.group);
@@ -674,15 +674,31 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
         }
         const float off = m_new == -INFINITY ? 0.f : ev - m_new;
         const uint64_t c2 = f2(c, c), nm2 = f2(off, off);
-        uint64_t acc[4] = {f2(0.f, 0.f), f2(0.f, 0.f), f2(0.f, 0.f), f2(0.f, 0.f)};
-        uint32_t pk[32];
+        // The exponents of the two tiles take turns (A of step j, B of step j, A of
+        // step j + 1, ...), so that one tile's fill the time of the other's MMAs.
+        if (both && (x == 1 || turn > 0)) {
+          if (!mbar_wait(bar(kBarTurn + 4 * (x ^ 1) + (warp & 3)), (x == 1 ? turn : turn - 1) & 1, a.status)) {
+            ok = false;
+            break;
+          }
+        }
 #pragma unroll
         for (int y = 0; y < 32; ++y) {
           const uint64_t z = f2_fma(f2(__uint_as_float(sr[2 * y]), __uint_as_float(sr[2 * y + 1])), c2, nm2);
           float z0, z1;
           f2_split(z, z0, z1);
-          z0 = ex2_approx(z0);
-          z1 = ex2_approx(z1);
+          sr[2 * y] = __float_as_uint(ex2_approx(z0));
+          sr[2 * y + 1] = __float_as_uint(ex2_approx(z1));
+        }
+        if (both) {
+          mbar_arrive(bar(kBarTurn + 4 * x + (warp & 3)));
+          ++turn;
+        }
+        uint64_t acc[4] = {f2(0.f, 0.f), f2(0.f, 0.f), f2(0.f, 0.f), f2(0.f, 0.f)};
+        uint32_t pk[32];
+#pragma unroll
+        for (int y = 0; y < 32; ++y) {
+          const float z0 = __uint_as_float(sr[2 * y]), z1 = __uint_as_float(sr[2 * y + 1]);
           acc[y & 3] = f2_add(acc[y & 3], f2(z0, z1));
           // The product's operand: weights in 16 bits (their sum stays in fp32).
           pk[y] = E4M3 ? pack_f16x2(z0, z1) : pack_bf16x2(z0, z1);
@@ -716,10 +732,11 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
       tc_fence_after();
       // ---- the item's end: finished here, or a record for the join
       l += __shfl_xor_sync(0xFFFFFFFFu, l, 16);
-      if (!w.begun && !w.whole) {
+      if (threadIdx.x == 0 && !w.begun && !w.whole) {
         const int64_t W = st.total < gridDim.x ? st.total : gridDim.x;
-        header = SplitHeader{static_cast<int>(share_of(at - w.b + w.kb.count - 1, W, st.total) - blockIdx.x) + 1, w.s,
-                             w.head, w.k * kItemRows, w.q, 0};
+        const int64_t last = st.first + st.units - w.left + w.kb.count - 1;
+        p.rec.headers[blockIdx.x] = SplitHeader{static_cast<int>(share_of(last, W, st.total) - blockIdx.x) + 1, w.s,
+                                                w.head, w.k * kItemRows, w.q, 0};
       }
       const float inv = pos < 0 ? 0.f : 1.f / l;
       float* rec = p.rec.at(blockIdx.x, w.begun ? 0 : 1);
@@ -765,10 +782,9 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
           exact_row<D, E4M3>(a, w.s, w.q.row0, first + iy, iy, w.head * a.group + rho_y - iy * a.group, lane);
         }
       }
-      at += w.end - w.b;
       w.next(a);
     }
-    if (threadIdx.x == 0) p.rec.headers[blockIdx.x] = ok ? header : SplitHeader{};
+    if (threadIdx.x == 0 && !ok) p.rec.headers[blockIdx.x] = SplitHeader{};
   }
 
   tc_fence_before();
