@@ -477,6 +477,7 @@ int ds_vit_cache_read(const ds_vit_cache* cache, const ds_vit_chunks* chunks, vo
  * and zeros for a row that sees nothing.  Hidden keys have no part in it,
  * whatever their values.
  *   q, out: device bf16 [rows, heads, head_dim]; they may not overlap.
+ *           DS_VIT_ERANGE when rows * heads / kv_heads is 2^30 or more.
  *   scale:  in (0, 1e30].
  *   ws:     device workspace, 16-byte aligned, of at least
  *           ds_vit_cache_attention_workspace_bytes (DS_VIT_ECAP otherwise);

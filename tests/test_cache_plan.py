@@ -22,6 +22,8 @@ int block_at(int p0, int p1, int window, int sinks, int shift, int i) {
   return key_blocks(p0, p1, window, sinks, shift).at(i);
 }
 int64_t begin(int64_t w, int64_t W, int64_t U) { return share_begin(w, W, U); }
+int divide(int n, int d) { return fast_div(d)(n); }
+int64_t snapped(int64_t x, int64_t i0, int64_t i1, int64_t snap) { return snap_border(x, i0, i1, snap); }
 int64_t owner(int64_t x, int64_t W, int64_t U) { return share_of(x, W, U); }
 }
 """
@@ -42,6 +44,7 @@ def plan(tmp_path_factory):
     h = C.CDLL(lib)
     for f in (h.begin, h.owner):
         f.restype, f.argtypes = C.c_int64, [C.c_int64] * 3
+    h.snapped.restype, h.snapped.argtypes = C.c_int64, [C.c_int64] * 4
     return h
 
 
@@ -98,3 +101,43 @@ def test_shares(plan):
     for w in (0, 1, 700, 1215):
         x = plan.begin(w, W, U)
         assert x == w * U // W and plan.owner(x, W, U) == w
+
+
+def test_division_by_the_group(plan):
+    top = 2 ** 31 - 1
+    for d in list(range(1, 129)) + [2 ** 30, top]:
+        for q in (0, 1, 2, 77, top // d - 1, top // d):
+            for n in (q * d - 1, q * d, q * d + 1, q * d + d - 1):
+                if 0 <= n <= top:
+                    assert plan.divide(n, d) == n // d, (n, d)
+    rng = random.Random(3)
+    for _ in range(5000):
+        n, d = rng.randrange(top + 1), rng.randrange(1, 129)
+        assert plan.divide(n, d) == n // d
+
+
+def test_snapped_borders(plan):
+    """Borders keep their order, move at most `snap` units and never leave their
+    item; a worker between two borders inside one item keeps at least a unit."""
+    rng = random.Random(4)
+    for _ in range(400):
+        counts = [rng.randrange(1, 40) for _ in range(rng.randrange(1, 30))]
+        ends = [0]
+        for c in counts:
+            ends.append(ends[-1] + c)
+        U = ends[-1]
+        W = rng.randrange(1, min(U, 60) + 1)
+        snap = min(6, 3 * (U // W) // 8)
+        borders = []
+        for w in range(W + 1):
+            x = plan.begin(w, W, U)
+            if x < U:
+                i = max(j for j in range(len(counts)) if ends[j] <= x)
+                y = plan.snapped(x, ends[i], ends[i + 1], snap)
+                assert y in (x, ends[i], ends[i + 1]) and abs(y - x) <= snap
+                x = y
+            borders.append(x)
+        assert borders[0] == 0 and borders[-1] == U and borders == sorted(borders)
+        for i in range(len(counts)):
+            inside = [b for b in borders if ends[i] < b < ends[i + 1]]
+            assert len(inside) == len(set(inside))

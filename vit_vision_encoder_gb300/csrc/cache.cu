@@ -298,6 +298,8 @@ int ds_vit_cache_attention(const ds_vit_cache* cache, const ds_vit_chunks* chunk
       !aligned(ws, 16))
     return DS_VIT_EINVAL;
   if (ws_bytes < attention_workspace(a.b, cache->head_dim, heads / a.c.kv_heads)) return DS_VIT_ECAP;
+  // Rows that share a K/V head are counted in 32 bits.
+  if (rows > INT32_MAX / 2 / (heads / a.c.kv_heads)) return DS_VIT_ERANGE;
   if (rows == 0) return DS_VIT_OK;
   a.q = static_cast<const bf16*>(q);
   a.q_stride = q_stride;
@@ -305,6 +307,7 @@ int ds_vit_cache_attention(const ds_vit_cache* cache, const ds_vit_chunks* chunk
   a.out_stride = out_stride;
   a.heads = heads;
   a.group = heads / a.c.kv_heads;
+  a.by_group = fast_div(a.group);
   a.window = window;
   a.sinks = sinks;
   a.scale_log2 = 1.4426950408889634f * scale;

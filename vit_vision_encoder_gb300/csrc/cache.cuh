@@ -2,6 +2,7 @@
 // kernels that write it, read it back and attend over it.
 #pragma once
 
+#include "cache_plan.h"
 #include "internal.h"
 #include "ptx.cuh"
 
@@ -114,6 +115,7 @@ struct AttentionArgs {
   bf16* out;
   int64_t out_stride;
   int heads, group;     // group = heads / kv_heads
+  FastDiv by_group;
   int window, sinks;
   float scale_log2;     // scale * log2(e)
   int* status;
@@ -122,6 +124,11 @@ struct AttentionArgs {
 // Whether the row at position p sees key j (j < kv always holds).
 __device__ __forceinline__ bool sees(const AttentionArgs& a, int p, int j) {
   return j <= p && (a.window == 0 || j > p - a.window || j < a.sinks);
+}
+
+// The first key of the window of the row at position p.
+__device__ __forceinline__ int window_start(const AttentionArgs& a, int p) {
+  return a.window != 0 && p >= a.window ? p - a.window + 1 : 0;
 }
 
 }  // namespace dsvit

@@ -109,11 +109,6 @@ __device__ __forceinline__ Item item_at(const AttentionArgs& a, const Plan& pl, 
   return it;
 }
 
-// The first key of the window of the row at position p.
-__device__ __forceinline__ int window_start(const AttentionArgs& a, int p) {
-  return a.window != 0 && p >= a.window ? p - a.window + 1 : 0;
-}
-
 template <bool F16>
 __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   if constexpr (F16)
@@ -312,7 +307,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
       const int rho = 8 * x + g;
-      const int i = rho / a.group;
+      const int i = a.by_group(rho);
       const bool on = x < kRowHalves && rho < R;
       const uint32_t* src = reinterpret_cast<const uint32_t*>(
           a.q + (it.q.row0 + i) * a.q_stride + (it.head * a.group + rho - i * a.group) * D);
@@ -581,7 +576,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int rho = 8 * x + g;
       bool bad = false;
       if (rho < R) {
-        const int i = rho / a.group;
+        const int i = a.by_group(rho);
         bf16* dst = a.out + (it.q.row0 + i) * a.out_stride + (it.head * a.group + rho - i * a.group) * D;
         const float inv = pos[x] < 0 ? 0.f : 1.f / l[x];
         float* rr = r + rho * D;
@@ -631,7 +626,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       const int rho = __ffs(static_cast<int>(redo)) - 1;
       redo &= redo - 1;
-      const int i = rho / a.group;
+      const int i = a.by_group(rho);
       exact_row<D, E4M3>(a, it.s, it.q.row0, p_first + i, i, it.head * a.group + rho - i * a.group, lane);
     }
     u += it.end - it.b;

@@ -39,4 +39,31 @@ DSV_HD int64_t share_begin(int64_t w, int64_t W, int64_t U) { return w * U / W; 
 // The worker that takes unit x: the largest w with floor(w U / W) <= x.
 DSV_HD int64_t share_of(int64_t x, int64_t W, int64_t U) { return ((x + 1) * W - 1) / U; }
 
+// Division of 0 <= n < 2^31 by a fixed d >= 1 without a divide: with
+// 2^s >= d and m = ceil(2^(32 + s) / d) - 2^32, n / d = (mulhi(n, m) + n) >> s.
+struct FastDiv {
+  uint32_t m;
+  int s, d;
+  DSV_HD int operator()(int n) const {
+    const uint32_t u = static_cast<uint32_t>(n);
+    return static_cast<int>((static_cast<uint32_t>((static_cast<uint64_t>(u) * m) >> 32) + u) >> s);
+  }
+};
+inline FastDiv fast_div(int d) {
+  int s = 0;
+  while ((int64_t{1} << s) < d) ++s;
+  const uint64_t m = ((((uint64_t{1} << s) - static_cast<uint64_t>(d)) << 32) + static_cast<uint64_t>(d) - 1) /
+                     static_cast<uint64_t>(d);
+  return FastDiv{static_cast<uint32_t>(m), s, d};
+}
+
+// A share's border inside an item of units i0 .. i1 - 1 moves to the item's
+// nearer end when that is at most `snap` units away: a split item costs a second
+// load of its rows, a record of each part and their sum.
+DSV_HD int64_t snap_border(int64_t x, int64_t i0, int64_t i1, int64_t snap) {
+  const int64_t a = x - i0, b = i1 - x;
+  if (a <= b) return a <= snap ? i0 : x;
+  return b <= snap ? i1 : x;
+}
+
 }  // namespace dsvit

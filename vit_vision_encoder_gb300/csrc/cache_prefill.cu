@@ -84,22 +84,24 @@ struct PrefillArgs {
   Records rec;
 };
 
-// Where a CTA's share of the units begins, and how many it has.
+// Where a CTA's share of the units begins, and how many it has; how far
+// borders move to an item's end.
 struct Start {
   int s, k, head, b;
   int64_t units, total, first;
+  int snap;
 };
+constexpr int kSnap = 6;
 
 __device__ __forceinline__ int items_of(const AttentionArgs& a, const Seq& q) {
-  return static_cast<int>((static_cast<int64_t>(q.c) * a.group + kItemRows - 1) / kItemRows);
+  return (q.c * a.group + kItemRows - 1) / kItemRows;
 }
 
 // Positions of the first and the last row of item k of a sequence.
 __device__ __forceinline__ void item_positions(const AttentionArgs& a, const Seq& q, int k, int& p0, int& p1) {
-  const int64_t r0 = static_cast<int64_t>(k) * kItemRows;
-  const int64_t r1 = min(r0 + kItemRows, static_cast<int64_t>(q.c) * a.group) - 1;
-  p0 = q.kv - q.c + static_cast<int>(r0 / a.group);
-  p1 = q.kv - q.c + static_cast<int>(r1 / a.group);
+  const int r0 = k * kItemRows, r1 = min(r0 + kItemRows, q.c * a.group) - 1;
+  p0 = q.kv - q.c + a.by_group(r0);
+  p1 = q.kv - q.c + a.by_group(r1);
 }
 
 __device__ __forceinline__ KeyBlocks item_blocks(const AttentionArgs& a, const Seq& q, int k) {
@@ -108,10 +110,6 @@ __device__ __forceinline__ KeyBlocks item_blocks(const AttentionArgs& a, const S
   KeyBlocks kb = key_blocks(p0, p1, a.window, a.sinks, kTileShift);
   if (kb.count == 0) kb.count = 1;          // nothing visible: one tile without keys, so that zeros get written
   return kb;
-}
-
-__device__ __forceinline__ int window_start(const AttentionArgs& a, int p) {
-  return a.window != 0 && p >= a.window ? p - a.window + 1 : 0;
 }
 
 // A role's walk over the CTA's items, in the order sequence, item, head.
@@ -133,12 +131,18 @@ struct Walk {
     s = st.s, k = st.k, head = st.head;
     left = st.units;
     q = left > 0 ? load_seq(a.b, a.c.page_shift, s, nullptr) : Seq{0, 0, 0};
-    if (left > 0) enter(a, st.b);
+    if (left <= 0) return;
+    if (st.b < item_blocks(a, q, k).count)
+      enter(a, st.b);
+    else
+      step(a);                              // the border moved to this item's end
   }
   // To the next item; left must be positive afterwards for it to exist.
   __device__ __forceinline__ void next(const AttentionArgs& a) {
     left -= end - b;
-    if (left <= 0) return;
+    if (left > 0) step(a);
+  }
+  __device__ __forceinline__ void step(const AttentionArgs& a) {
     if (++head == a.c.kv_heads) {
       head = 0;
       if (++k == items_of(a, q)) {
@@ -156,42 +160,43 @@ struct Walk {
 // flat list of (sequence, item) pairs, each thread adding up a run of it.
 template <int kThreads>
 __device__ __forceinline__ Start make_plan(const AttentionArgs& a, uint8_t* scratch, int* status) {
-  int* items = reinterpret_cast<int*>(scratch);                                   // [n + 1] items before each sequence
-  int64_t* sums = reinterpret_cast<int64_t*>(scratch + 4 * (DS_VIT_MAX_SEQS + 2));// [kThreads] units of each run
-  Start* found = reinterpret_cast<Start*>(sums + kThreads);
-  __shared__ int64_t warp_sum[kThreads / 32];
+  int* items = reinterpret_cast<int*>(scratch);                                 // [n + 1] items before each sequence
+  Start* found = reinterpret_cast<Start*>(scratch + 4 * (DS_VIT_MAX_SEQS + 2));
+  constexpr int kWarps = kThreads / 32;
+  __shared__ int64_t warp_sum[kWarps];
+  __shared__ int64_t border[2];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   auto scan = [&](int64_t x, int64_t& total) {      // exclusive prefix over the block
-    int64_t inc = x;
+    auto inclusive = [&](int64_t v) {
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t y = __shfl_up_sync(0xFFFFFFFFu, inc, o);
-      if (lane >= o) inc += y;
-    }
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(0xFFFFFFFFu, v, o);
+        if (lane >= o) v += y;
+      }
+      return v;
+    };
+    const int64_t inc = inclusive(x);
+    __syncthreads();                        // warp_sum's last readers are done
     if (lane == 31) warp_sum[warp] = inc;
     __syncthreads();
-    int64_t before = 0;
-    total = 0;
-    for (int w = 0; w < kThreads / 32; ++w) {
-      if (w < warp) before += warp_sum[w];
-      total += warp_sum[w];
-    }
-    __syncthreads();
-    return before + inc - x;
+    const int64_t sums = inclusive(lane < kWarps ? warp_sum[lane] : 0);
+    total = __shfl_sync(0xFFFFFFFFu, sums, kWarps - 1);
+    const int64_t before = __shfl_sync(0xFFFFFFFFu, sums, (warp + 31) & 31);
+    return (warp > 0 ? before : 0) + inc - x;
   };
-  int64_t all = 0;
+  int all = 0;
   for (int s0 = 0; s0 < a.b.n; s0 += kThreads) {
     const int s = s0 + tid;
     int64_t x = 0, t;
     if (s < a.b.n) x = items_of(a, load_seq(a.b, a.c.page_shift, s, status));
     const int64_t before = scan(x, t);
-    if (s < a.b.n) items[s] = static_cast<int>(all + before);
-    all += t;
+    if (s < a.b.n) items[s] = all + static_cast<int>(before);
+    all += static_cast<int>(t);
   }
-  if (tid == 0) items[a.b.n] = static_cast<int>(all);
+  if (tid == 0) items[a.b.n] = all;
   __syncthreads();
   // This thread's run of the list, and its units.
-  const int i0 = static_cast<int>(all * tid / kThreads), i1 = static_cast<int>(all * (tid + 1) / kThreads);
+  const int per = (all + kThreads - 1) / kThreads, i0 = min(all, tid * per), i1 = min(all, i0 + per);
   int s_run = 0;
   if (i0 < i1) {
     int lo = 0, hi = a.b.n - 1;
@@ -209,37 +214,47 @@ __device__ __forceinline__ Start make_plan(const AttentionArgs& a, uint8_t* scra
     Seq q = load_seq(a.b, a.c.page_shift, s, nullptr);
     for (int i = i0; i < i1; ++i) {
       while (i >= items[s + 1]) q = load_seq(a.b, a.c.page_shift, ++s, nullptr);
-      if (!each(s, i - items[s], item_blocks(a, q, i - items[s]).count)) return;
+      each(s, i - items[s], item_blocks(a, q, i - items[s]).count);
     }
   };
   int64_t mine = 0, total;
-  if (i0 < i1)
-    walk([&](int, int, int count) {
-      mine += static_cast<int64_t>(count) * a.c.kv_heads;
-      return true;
-    });
+  if (i0 < i1) walk([&](int, int, int count) { mine += static_cast<int64_t>(count) * a.c.kv_heads; });
   int64_t at = scan(mine, total);
-  const int64_t grid = gridDim.x, W = total < grid ? total : grid;
-  const int64_t first = blockIdx.x < W ? share_begin(blockIdx.x, W, total) : 0;
-  const int64_t units = blockIdx.x < W ? share_begin(blockIdx.x + 1, W, total) - first : 0;
-  if (tid == 0) *found = Start{0, 0, 0, 0, units, total, first};
+  // This CTA's borders, moved to an item's end where one is near.
+  const int64_t W = total < gridDim.x ? total : gridDim.x, w = blockIdx.x;
+  const int64_t share = W > 0 ? total / W : 0, near = 3 * share / 8;
+  const int snap = near < kSnap ? static_cast<int>(near) : kSnap;
+  const int64_t x0 = w < W ? share_begin(w, W, total) : total, x1 = w < W ? share_begin(w + 1, W, total) : total;
+  if (tid == 0) {
+    border[0] = border[1] = total;
+    *found = Start{};
+  }
   __syncthreads();
-  if (units > 0 && first >= at && first < at + mine)
+  if (mine > 0 && ((x0 >= at && x0 < at + mine) || (x1 >= at && x1 < at + mine)))
     walk([&](int s, int k, int count) {
       const int64_t here = static_cast<int64_t>(count) * a.c.kv_heads;
-      if (first < at + here) {
-        const int64_t r = first - at;
-        found->s = s;
-        found->k = k;
-        found->head = static_cast<int>(r / count);
-        found->b = static_cast<int>(r % count);
-        return false;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int64_t x = e == 0 ? x0 : x1;
+        if (x < at || x >= at + here) continue;
+        const int head = static_cast<int>((x - at) / count);
+        const int64_t i0 = at + static_cast<int64_t>(head) * count, y = snap_border(x, i0, i0 + count, snap);
+        border[e] = y;
+        if (e == 0) {
+          found->s = s;
+          found->k = k;
+          found->head = head;
+          found->b = static_cast<int>(y - i0);
+        }
       }
       at += here;
-      return true;
     });
   __syncthreads();
-  const Start st = *found;
+  Start st = *found;
+  st.first = border[0];
+  st.units = border[1] - border[0];
+  st.total = total;
+  st.snap = snap;
   __syncthreads();
   return st;
 }
@@ -446,7 +461,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
       Walk w;
       w.start(a, st);
       while (ok && w.left > 0) {
-        const int64_t rows = static_cast<int64_t>(w.q.c) * a.group - static_cast<int64_t>(w.k) * kItemRows;
+        const int rows = w.q.c * a.group - w.k * kItemRows;
         if (rows <= x * kTile) {
           // No rows in this tile: the buffers are only handed back.
           for (int j = 0; j < 2 * (w.end - w.b); ++j) {
@@ -495,6 +510,13 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
     if constexpr (E4M3) registers_dec<48>();
     // ------------------------------------------------------------ e4m3 -> fp16
     const int tid = threadIdx.x - 32 * kWarpConvert;
+    // A thread takes 16-byte piece `piece` of rows r0, r0 + kStep, ...: their
+    // places differ by constants (kStep is a multiple of the swizzle's 8 rows).
+    constexpr int kPieces = D / 16, kStep = 128 / kPieces, kEach = 32 / kPieces;
+    const int piece = tid % kPieces, r0 = tid / kPieces, second = (piece >> 2) & 1;
+    const uint32_t raw_at = r0 * D + ((D == 128 ? piece ^ (r0 & 7) : piece ^ ((r0 >> 1) & 3)) << 4);
+    const uint32_t tile_at0 = tile_piece<D, E4M3>(0, r0, 2 * piece + second);
+    const uint32_t tile_at1 = tile_piece<D, E4M3>(0, r0, 2 * piece + 1 - second);
     int raw = 0, slot = 0, tile = 0;
     uint32_t raw_phase = 0, phase = 1;
     bool ok = true;
@@ -512,7 +534,9 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
           ok = __all_sync(0xFFFFFFFFu, mbar_wait(bar(kBarRawFull + raw), raw_phase, a.status));
           if (!ok) break;
           const uint8_t* ex = smem + C::kOffExp + raw * kTile;
-          // The largest exponent among rows that some row sees (255 marks a NaN row).
+          // The largest exponent among rows that some row sees (255 marks a NaN
+          // row), and the factor of one of this warp's 32 rows: lane y has row
+          // kStep (y / kEach) + kEach wc + y % kEach.
           int top = 0;
 #pragma unroll
           for (int y = 0; y < 4; ++y) {
@@ -521,27 +545,31 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
           }
           top = __reduce_max_sync(0xFFFFFFFFu, top);
           if (top == 0) top = 127;
+          uint32_t factor;
+          {
+            const int r = kStep * (lane / kEach) + kEach * (warp - kWarpConvert) + lane % kEach;
+            const int e = ex[r], down = top - e;
+            factor = e == 255 ? 0x3C00u : down <= 14 ? (15u - down) << 10 : down <= 24 ? 1u << (24 - down) : 0u;
+            factor = any(key0 + r) ? factor | factor << 16 : 0xFFFFFFFFu;      // marks a row that nobody sees
+          }
           ok = __all_sync(0xFFFFFFFFu, mbar_wait(bar(kBarKvEmpty + slot), phase, a.status));
           if (!ok) break;
           if (tid == 0) tile_exp[8 * kv + (tile & 7)] = top - 127;
-          constexpr int kPieces = D / 16;
-#pragma unroll 4
-          for (int x = tid; x < kTile * kPieces; x += 128) {
-            const int r = x / kPieces, piece = x % kPieces;
-            const uint32_t swz = D == 128 ? piece ^ (r & 7) : piece ^ ((r >> 1) & 3);
-            const uint4 v = lds128(sRaw(raw) + r * D + 16 * swz);
-            const int e = ex[r], down = top - e;
-            uint32_t f = e == 255 ? 0x3C00u : down <= 14 ? (15u - down) << 10 : down <= 24 ? 1u << (24 - down) : 0u;
-            f |= f << 16;
-            const bool on = any(key0 + r);
+          const uint32_t from = sRaw(raw) + raw_at;
+          const uint32_t to0 = sKv(slot) + tile_at0, to1 = sKv(slot) + tile_at1;
+#pragma unroll
+          for (int y = 0; y < 32 / kEach; ++y) {
+            const uint4 v = lds128(from + y * kStep * D);
+            const uint32_t f = __shfl_sync(0xFFFFFFFFu, factor, y * kEach + lane / kPieces);
             uint4 u0, u1;
-            auto widen = [&](uint32_t two) { return on ? mul_f16x2(e4m3x2_to_f16x2(two), f) : 0u; };
-            u0.x = widen(v.x & 0xFFFFu), u0.y = widen(v.x >> 16), u0.z = widen(v.y & 0xFFFFu), u0.w = widen(v.y >> 16);
-            u1.x = widen(v.z & 0xFFFFu), u1.y = widen(v.z >> 16), u1.z = widen(v.w & 0xFFFFu), u1.w = widen(v.w >> 16);
+            u0.x = mul_f16x2(e4m3x2_to_f16x2(v.x & 0xFFFFu), f), u0.y = mul_f16x2(e4m3x2_to_f16x2(v.x >> 16), f);
+            u0.z = mul_f16x2(e4m3x2_to_f16x2(v.y & 0xFFFFu), f), u0.w = mul_f16x2(e4m3x2_to_f16x2(v.y >> 16), f);
+            u1.x = mul_f16x2(e4m3x2_to_f16x2(v.z & 0xFFFFu), f), u1.y = mul_f16x2(e4m3x2_to_f16x2(v.z >> 16), f);
+            u1.z = mul_f16x2(e4m3x2_to_f16x2(v.w & 0xFFFFu), f), u1.w = mul_f16x2(e4m3x2_to_f16x2(v.w >> 16), f);
+            if (f == 0xFFFFFFFFu) u0 = u1 = make_uint4(0, 0, 0, 0);
             // Lanes of the two halves of the dims store their two pieces in opposite orders: no bank conflicts.
-            const int first = (piece >> 2) & 1;
-            sts128(tile_piece<D, E4M3>(sKv(slot), r, 2 * piece + first), first ? u1 : u0);
-            sts128(tile_piece<D, E4M3>(sKv(slot), r, 2 * piece + 1 - first), first ? u0 : u1);
+            sts128(to0 + y * kStep * 128, second ? u1 : u0);
+            sts128(to1 + y * kStep * 128, second ? u0 : u1);
           }
           fence_proxy_async_smem();
           __syncwarp();
@@ -579,22 +607,21 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
     Walk w;
     w.start(a, st);
     while (ok && w.left > 0) {
-      const int64_t rho64 = static_cast<int64_t>(w.k) * kItemRows + x * kTile;    // first row of the tile
-      const int64_t R = static_cast<int64_t>(w.q.c) * a.group;
-      if (rho64 >= R) {
+      const int rho0 = w.k * kItemRows + x * kTile;      // first row of the tile
+      const int R = w.q.c * a.group;
+      if (rho0 >= R) {
         tile += w.end - w.b;
         w.next(a);
         continue;
       }
-      const bool both = R - static_cast<int64_t>(w.k) * kItemRows > kTile;       // tile B has rows too
-      const int rho = static_cast<int>(rho64) + r;
+      const bool both = R - w.k * kItemRows > kTile;     // tile B has rows too
+      const int rho = rho0 + r;
       const bool on = rho < R;
-      const int i = rho / a.group, hq = w.head * a.group + (rho - i * a.group);
+      const int i = a.by_group(rho), hq = w.head * a.group + (rho - i * a.group);
       const int first = w.q.kv - w.q.c;
       const int pos = on ? first + i : -1;
       // Positions of the tile's first and last rows, for tiles without a mask.
-      const int pa = first + static_cast<int>(rho64 / a.group);
-      const int pb = first + static_cast<int>((min(rho64 + kTile, R) - 1) / a.group);
+      const int pa = first + a.by_group(rho0), pb = first + a.by_group(min(rho0 + kTile, R) - 1);
       const int lo = window_start(a, pos), lo_b = window_start(a, pb);
       // ---- this thread's half of its query row
       float c0 = a.scale_log2;
@@ -682,26 +709,22 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
             break;
           }
         }
+        uint64_t acc[4] = {f2(0.f, 0.f), f2(0.f, 0.f), f2(0.f, 0.f), f2(0.f, 0.f)};
+        uint32_t pk[32];
 #pragma unroll
         for (int y = 0; y < 32; ++y) {
           const uint64_t z = f2_fma(f2(__uint_as_float(sr[2 * y]), __uint_as_float(sr[2 * y + 1])), c2, nm2);
           float z0, z1;
           f2_split(z, z0, z1);
-          sr[2 * y] = __float_as_uint(ex2_approx(z0));
-          sr[2 * y + 1] = __float_as_uint(ex2_approx(z1));
+          z0 = ex2_approx(z0);
+          z1 = ex2_approx(z1);
+          acc[y & 3] = f2_add(acc[y & 3], f2(z0, z1));
+          // The product's operand: weights in 16 bits (their sum stays in fp32).
+          pk[y] = E4M3 ? pack_f16x2(z0, z1) : pack_bf16x2(z0, z1);
         }
         if (both) {
           mbar_arrive(bar(kBarTurn + 4 * x + (warp & 3)));
           ++turn;
-        }
-        uint64_t acc[4] = {f2(0.f, 0.f), f2(0.f, 0.f), f2(0.f, 0.f), f2(0.f, 0.f)};
-        uint32_t pk[32];
-#pragma unroll
-        for (int y = 0; y < 32; ++y) {
-          const float z0 = __uint_as_float(sr[2 * y]), z1 = __uint_as_float(sr[2 * y + 1]);
-          acc[y & 3] = f2_add(acc[y & 3], f2(z0, z1));
-          // The product's operand: weights in 16 bits (their sum stays in fp32).
-          pk[y] = E4M3 ? pack_f16x2(z0, z1) : pack_bf16x2(z0, z1);
         }
         const uint64_t s2 = f2_add(f2_add(acc[0], acc[1]), f2_add(acc[2], acc[3]));
         float s0, s1;
@@ -734,9 +757,11 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
       l += __shfl_xor_sync(0xFFFFFFFFu, l, 16);
       if (threadIdx.x == 0 && !w.begun && !w.whole) {
         const int64_t W = st.total < gridDim.x ? st.total : gridDim.x;
-        const int64_t last = st.first + st.units - w.left + w.kb.count - 1;
-        p.rec.headers[blockIdx.x] = SplitHeader{static_cast<int>(share_of(last, W, st.total) - blockIdx.x) + 1, w.s,
-                                                w.head, w.k * kItemRows, w.q, 0};
+        const int64_t i0 = st.first + st.units - w.left, i1 = i0 + w.kb.count;
+        int64_t last = share_of(i1 - 1, W, st.total);      // the last worker whose border is not at or behind the end
+        while (last > blockIdx.x && snap_border(share_begin(last, W, st.total), i0, i1, st.snap) >= i1) --last;
+        p.rec.headers[blockIdx.x] =
+            SplitHeader{static_cast<int>(last - blockIdx.x) + 1, w.s, w.head, w.k * kItemRows, w.q, 0};
       }
       const float inv = pos < 0 ? 0.f : 1.f / l;
       float* rec = p.rec.at(blockIdx.x, w.begun ? 0 : 1);
@@ -778,7 +803,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
           __syncwarp();
           const int y = __ffs(static_cast<int>(redo)) - 1;
           redo &= redo - 1;
-          const int rho_y = static_cast<int>(rho64) + row0 + y, iy = rho_y / a.group;
+          const int rho_y = rho0 + row0 + y, iy = a.by_group(rho_y);
           exact_row<D, E4M3>(a, w.s, w.q.row0, first + iy, iy, w.head * a.group + rho_y - iy * a.group, lane);
         }
       }

@@ -4,7 +4,6 @@
 #pragma once
 
 #include "cache.cuh"
-#include "cache_plan.h"
 
 namespace dsvit {
 
@@ -22,7 +21,7 @@ __device__ __noinline__ void exact_row(const AttentionArgs& a, int s, int row0, 
     q[x] = __bfloat162float(qr[x]);
     o[x] = 0.f;
   }
-  const int lo = a.window != 0 && p >= a.window ? p - a.window + 1 : 0;
+  const int lo = window_start(a, p);
   float m = -INFINITY, l = 0.f;
   for (int j = 0; j <= p; ++j) {
     if (j >= a.sinks && j < lo) j = lo;
@@ -101,7 +100,7 @@ inline Records records_in(void* ws, int64_t workers, int rows, int d) {
 // shared memory.  The order is fixed, so a result depends on the lengths alone.
 constexpr int kJoinWarps = 8;
 constexpr int kJoinItems = 16;    // workers per block at most
-constexpr int kJoinRows = 8;      // grid rows at most
+constexpr int kJoinRows = 32;     // grid rows at most
 
 // Adds parts first, first + step, ... of one row to (m, l, o), loads of four parts at a time.
 template <int D>
@@ -152,7 +151,7 @@ __device__ __forceinline__ void join_parts(const Records& rec, int w, int parts,
 template <int D, bool E4M3>
 __device__ __forceinline__ void join_finish(const AttentionArgs& a, const SplitHeader& hd, int rho, float l,
                                             const float (&o)[D / 32], int lane) {
-  const int i = rho / a.group, h = hd.head * a.group + rho - i * a.group, p = hd.q.kv - hd.q.c + i;
+  const int i = a.by_group(rho), h = hd.head * a.group + rho - i * a.group, p = hd.q.kv - hd.q.c + i;
   bf16* to = a.out + (hd.q.row0 + i) * a.out_stride + h * D + lane * (D / 32);
   const float inv = p < 0 ? 0.f : 1.f / l;
   bool bad = false;
