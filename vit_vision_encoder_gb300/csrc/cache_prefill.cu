@@ -278,6 +278,11 @@ __device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
   return r;
 }
 
+// The lowest n bits (none for n <= 0, all for n >= 64).
+__device__ __forceinline__ uint64_t bits_below(int n) {
+  return n <= 0 ? 0 : n >= 64 ? ~uint64_t{0} : (uint64_t{1} << n) - 1;
+}
+
 // Address of 16-byte piece `piece` (of D / 8) of row r in a 16-bit tile.
 template <int D, bool E4M3>
 __device__ __forceinline__ uint32_t tile_piece(uint32_t tile, int r, int piece) {
@@ -680,13 +685,14 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
         tmem_wait_ld();
         top = fmaxf(tmem_after_wait(top), tmem_after_wait(top2));
         if (!open) {
-          // Key i of this half is seen when i <= last and (i >= from or i < keep).
+          // Key y of this half is seen when y <= last and (y >= from or y < keep): one bit each.
           const int j0 = key0 + 64 * h;
-          const int last = pos - j0, from = lo - j0, keep = a.sinks - j0;
+          const uint64_t seen = bits_below(pos - j0 + 1) & (~bits_below(lo - j0) | bits_below(a.sinks - j0));
+          const uint32_t s0 = static_cast<uint32_t>(seen), s1 = static_cast<uint32_t>(seen >> 32);
           float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
           for (int y = 0; y < 64; ++y) {
-            if (!(y <= last && (y >= from || y < keep))) sr[y] = __float_as_uint(-INFINITY);
+            if (!((y < 32 ? s0 : s1) & (1u << (y & 31)))) sr[y] = __float_as_uint(-INFINITY);
             mx[y & 3] = fmaxf(mx[y & 3], __uint_as_float(sr[y]));
           }
           top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
