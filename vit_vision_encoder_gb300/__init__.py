@@ -658,12 +658,12 @@ def cache_read(cache, chunks, rows, out=None, status=None):
 
 def cache_attention_workspace_bytes(cache, chunks, heads):
     """Bytes of workspace that cache_attention needs for these sizes."""
-    nb = chunks.ws_bytes.get((heads, cache.kv_heads, cache.head_dim))
+    nb = chunks.ws_bytes.get((heads, cache.kv_heads, cache.head_dim, cache.c.kind))
     if nb is None:
         n = C.c_size_t()
         check(lib.ds_vit_cache_attention_workspace_bytes(cache.ref, chunks.ref, heads, C.byref(n)),
               "ds_vit_cache_attention_workspace_bytes")
-        nb = chunks.ws_bytes[heads, cache.kv_heads, cache.head_dim] = n.value
+        nb = chunks.ws_bytes[heads, cache.kv_heads, cache.head_dim, cache.c.kind] = n.value
     return nb
 
 

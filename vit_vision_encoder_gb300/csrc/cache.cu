@@ -218,13 +218,16 @@ bool bad_rows(const void* p, int64_t stride, int64_t width) {
   return !p || !aligned(p, 16) || stride < width || stride % 8 != 0;
 }
 
-// Rows that share a K/V head in one sequence: up to kDecodeRows the cache's
-// bytes bound the call, and the kernel that streams them through warp MMAs is
+// Rows that share a K/V head in one sequence: few of them leave the call bound
+// by the cache's bytes, and the kernel that streams those through warp MMAs is
 // taken; with more rows the tcgen05 one.
-bool few_rows(const ChunkView& b, int group) { return static_cast<int64_t>(b.max_rows) * group <= kDecodeRows; }
+bool few_rows(const ChunkView& b, int group, bool e4m3) {
+  return static_cast<int64_t>(b.max_rows) * group <= decode_rows(e4m3);
+}
 
-size_t attention_workspace(const ChunkView& b, int head_dim, int group) {
-  return few_rows(b, group) ? cache_decode_workspace(head_dim, b.max_rows * group) : cache_prefill_workspace(head_dim);
+size_t attention_workspace(const ChunkView& b, int head_dim, int group, bool e4m3) {
+  return few_rows(b, group, e4m3) ? cache_decode_workspace(head_dim, b.max_rows * group)
+                                  : cache_prefill_workspace(head_dim);
 }
 
 int launched(cudaError_t e) {
@@ -281,7 +284,7 @@ int ds_vit_cache_attention_workspace_bytes(const ds_vit_cache* cache, const ds_v
   if (!bytes) return DS_VIT_EINVAL;
   if (const int rc = check_cache(cache, chunks, 0, &c, &b)) return rc;
   if (heads < 1 || heads % c.kv_heads != 0 || heads / c.kv_heads > DS_VIT_CACHE_MAX_GROUP) return DS_VIT_EINVAL;
-  *bytes = attention_workspace(b, cache->head_dim, heads / c.kv_heads);
+  *bytes = attention_workspace(b, cache->head_dim, heads / c.kv_heads, cache->kind == DS_VIT_CACHE_E4M3);
   return DS_VIT_OK;
 }
 
@@ -297,7 +300,8 @@ int ds_vit_cache_attention(const ds_vit_cache* cache, const ds_vit_chunks* chunk
   if (!status || !aligned(status, 4) || bad_rows(q, q_stride, width) || bad_rows(out, out_stride, width) || !ws ||
       !aligned(ws, 16))
     return DS_VIT_EINVAL;
-  if (ws_bytes < attention_workspace(a.b, cache->head_dim, heads / a.c.kv_heads)) return DS_VIT_ECAP;
+  const bool e4m3 = cache->kind == DS_VIT_CACHE_E4M3;
+  if (ws_bytes < attention_workspace(a.b, cache->head_dim, heads / a.c.kv_heads, e4m3)) return DS_VIT_ECAP;
   // Rows that share a K/V head are counted in 32 bits.
   if (rows > INT32_MAX / 2 / (heads / a.c.kv_heads)) return DS_VIT_ERANGE;
   if (rows == 0) return DS_VIT_OK;
@@ -312,8 +316,8 @@ int ds_vit_cache_attention(const ds_vit_cache* cache, const ds_vit_chunks* chunk
   a.sinks = sinks;
   a.scale_log2 = 1.4426950408889634f * scale;
   a.status = reinterpret_cast<int*>(status);
-  auto* launch = few_rows(a.b, a.group) ? launch_cache_decode : launch_cache_prefill;
-  return launch(a, cache->head_dim, cache->kind == DS_VIT_CACHE_E4M3, ws, static_cast<cudaStream_t>(stream));
+  auto* launch = few_rows(a.b, a.group, e4m3) ? launch_cache_decode : launch_cache_prefill;
+  return launch(a, cache->head_dim, e4m3, ws, static_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

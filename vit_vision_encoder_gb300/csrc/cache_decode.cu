@@ -1,13 +1,14 @@
-// Attention over the paged cache for few rows: at most 16 query rows (new
-// tokens times query heads per K/V head) share a K/V head, as in decoding.
+// Attention over the paged cache for few rows, as in decoding: the query rows
+// that share a K/V head (new tokens times query heads per K/V head) are taken
+// 16 at a time, up to decode_rows of them.
 //
-// Bound by the cache's bytes: each key and value is read once and meets at
-// most 16 rows, 32 flops a byte of bf16, a twentieth of the tensor rate the
+// Bound by the cache's bytes: each key and value read meets at most 16 rows, 32 flops a byte of bf16, a twentieth of the tensor rate the
 // bytes could feed.  So the products run as warp MMAs (m16n8k16), whose
 // fragments come straight from shared memory; what counts is bytes in flight
 // and a short chain of instructions per key.
 //
-// Work: the unit is a block of kKeys keys of one item (sequence, K/V head).
+// Work: the unit is a block of kKeys keys of one item (sequence, K/V head, 16
+// rows).
 // All units of a call are counted from the lengths on the device and dealt in
 // order to the workers, the consumer warps of the grid, in equal shares
 // (cache_plan.h), so a batch of unequal lengths and a single long sequence both
@@ -35,13 +36,11 @@
 // bits.
 #include "cache_rows.cuh"
 
+#include <algorithm>
+
 namespace dsvit {
 
 namespace {
-
-constexpr int kWarps = 7;                  // consumer warps: with the producer two warps a scheduler, 255 registers each
-constexpr int kThreads = 32 * kWarps + 32;
-constexpr int kRingBytes = 24 * 1024;      // per consumer warp
 
 // A row's reference m (log2) is raised when a block's maximum passes m + kLag,
 // to kLead below that maximum; weights are 2^(x - m).
@@ -53,6 +52,11 @@ struct Reference {
 
 template <int D, bool E4M3>
 struct Shape {
+  // Consumer warps: with the producer a multiple of four, and as many registers
+  // as the fragments need (D 128: 255 each).
+  static constexpr int kWarps = D == 64 ? 11 : 7;
+  static constexpr int kThreads = 32 * kWarps + 32;
+  static constexpr int kRingBytes = (D == 64 ? 16 : 24) * 1024;      // per consumer warp
   static constexpr int kKeyShift = E4M3 ? 5 : 4;
   static constexpr int kKeys = 1 << kKeyShift;             // keys of a block
   static constexpr int kRow = E4M3 ? D : 2 * D;            // bytes of a key
@@ -67,7 +71,7 @@ struct Shape {
 
 // An item and the part of its blocks that a worker takes.
 struct Item {
-  int s, head;
+  int s, head, rho0;   // rho0: its first row among the rows that share the K/V head
   Seq q;
   KeyBlocks kb;
   int b, end;      // next block, end of the worker's part
@@ -86,6 +90,12 @@ __device__ __forceinline__ KeyBlocks seq_blocks(const AttentionArgs& a, const Se
   return kb;
 }
 
+constexpr int kRows = 16;   // rows of an item
+
+__device__ __forceinline__ int row_tiles(const AttentionArgs& a, const Seq& q) {
+  return (q.c * a.group + kRows - 1) / kRows;
+}
+
 // The item of unit u and the worker's part of it.
 template <int kKeyShift>
 __device__ __forceinline__ Item item_at(const AttentionArgs& a, const Plan& pl, int64_t u) {
@@ -102,8 +112,10 @@ __device__ __forceinline__ Item item_at(const AttentionArgs& a, const Plan& pl, 
   it.q = pl.seqs[lo];
   it.kb = seq_blocks<kKeyShift>(a, it.q);
   const int64_t r = u - pl.pre[lo];
-  it.head = static_cast<int>(r / it.kb.count);
-  it.b = static_cast<int>(r - static_cast<int64_t>(it.head) * it.kb.count);
+  const int n = static_cast<int>(r / it.kb.count), tiles = row_tiles(a, it.q);
+  it.head = n / tiles;
+  it.rho0 = (n - it.head * tiles) * kRows;
+  it.b = static_cast<int>(r - static_cast<int64_t>(n) * it.kb.count);
   const int64_t left = pl.end - u;
   it.end = left < it.kb.count - it.b ? it.b + static_cast<int>(left) : it.kb.count;
   return it;
@@ -206,10 +218,11 @@ __device__ __forceinline__ void produce(const CUtensorMap* tm_k, const CUtensorM
 // kRowHalves: 1 when at most 8 rows share a K/V head (rows 8 .. 15 of the
 // MMAs' 16 are then zeros nobody looks at), else 2.
 template <int D, bool E4M3, int kRowHalves>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Shape<D, E4M3>::kThreads, 1)
     decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                   const __grid_constant__ AttentionArgs a, const Records rec) {
   using S = Shape<D, E4M3>;
+  constexpr int kWarps = S::kWarps, kThreads = S::kThreads, kRingBytes = S::kRingBytes;
   constexpr int kSteps = D / 16;           // k steps of S
   constexpr int kCols = D / 8;             // column tiles of O
   constexpr int kN = S::kKeys / 8;         // column tiles of S
@@ -248,7 +261,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (s < a.b.n) {
       const Seq q = load_seq(a.b, a.c.page_shift, s, blockIdx.x == 0 ? a.status : nullptr);
       seqs[s] = q;
-      x = static_cast<int64_t>(seq_blocks<S::kKeyShift>(a, q).count) * (q.c > 0 ? a.c.kv_heads : 0);
+      x = static_cast<int64_t>(seq_blocks<S::kKeyShift>(a, q).count) * row_tiles(a, q) * a.c.kv_heads;
     }
     int64_t inc = x;
 #pragma unroll
@@ -299,16 +312,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   bool dead = false;                       // a wait gave up
   for (int64_t u = pl.begin; u < pl.end;) {
     const Item it = item_at<S::kKeyShift>(a, pl, u);
-    const int R = it.q.c * a.group;
+    const int R = min(it.q.c * a.group - it.rho0, kRows);       // rows of this item
     // Q fragments and positions of rows g, g + 8; what scales an fp16 row's scores back, times scale_log2.
     uint32_t qf[kSteps][4];
     int pos[kRowHalves];
     float qscale[kRowHalves];
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
-      const int rho = 8 * x + g;
+      const int rho = it.rho0 + 8 * x + g;
       const int i = a.by_group(rho);
-      const bool on = x < kRowHalves && rho < R;
+      const bool on = x < kRowHalves && 8 * x + g < R;
       const uint32_t* src = reinterpret_cast<const uint32_t*>(
           a.q + (it.q.row0 + i) * a.q_stride + (it.head * a.group + rho - i * a.group) * D);
 #pragma unroll
@@ -353,6 +366,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int n = 0; n < kCols; ++n)
 #pragma unroll
       for (int e = 0; e < 4; ++e) o[n][e] = 0.f;
+    // Positions of the sequence's first and last rows (its items share the key blocks).
     const int p_first = it.q.kv - it.q.c, p_last = it.q.kv - 1;
     const int lo_first = window_start(a, p_first), lo_last = window_start(a, p_last);
 
@@ -567,22 +581,22 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool begun = it.b > 0, whole = !begun && it.end == it.kb.count;
     if (!begun && !whole) {
       const int64_t last = u - it.b + it.kb.count - 1;
-      header = SplitHeader{static_cast<int>(share_of(last, W, total) - me) + 1, it.s, it.head, 0, it.q, 0};
+      header = SplitHeader{static_cast<int>(share_of(last, W, total) - me) + 1, it.s, it.head, it.rho0, it.q, 0};
     }
     float* r = rec.at(me, begun ? 0 : 1);
     uint32_t redo = 0;
 #pragma unroll
     for (int x = 0; x < kRowHalves; ++x) {
-      const int rho = 8 * x + g;
+      const int rr0 = 8 * x + g, rho = it.rho0 + rr0;
       bool bad = false;
-      if (rho < R) {
+      if (rr0 < R) {
         const int i = a.by_group(rho);
         bf16* dst = a.out + (it.q.row0 + i) * a.out_stride + (it.head * a.group + rho - i * a.group) * D;
         const float inv = pos[x] < 0 ? 0.f : 1.f / l[x];
-        float* rr = r + rho * D;
+        float* rr = r + rr0 * D;
         if (!whole && t == 0) {
-          rec.max_of(r, D)[rho] = m[x];
-          rec.sum_of(r, D)[rho] = l[x];
+          rec.max_of(r, D)[rr0] = m[x];
+          rec.sum_of(r, D)[rr0] = l[x];
         }
         // bf16: columns 8n + 2t, + 1.  e4m3: column tile n holds dim n of each
         // lane group's D / 8, so this lane has dims (2t) D/8 + n and (2t + 1) D/8 + n.
@@ -624,7 +638,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     while (redo) {
       __syncwarp();
-      const int rho = __ffs(static_cast<int>(redo)) - 1;
+      const int rho = it.rho0 + __ffs(static_cast<int>(redo)) - 1;
       redo &= redo - 1;
       const int i = a.by_group(rho);
       exact_row<D, E4M3>(a, it.s, it.q.row0, p_first + i, i, it.head * a.group + rho - i * a.group, lane);
@@ -657,10 +671,10 @@ int launch(const AttentionArgs& a, void* ws, cudaStream_t stream) {
   if (!map(&tk, a.c.k) || !map(&tv, a.c.v)) return DS_VIT_ECUDA;
   if (allow_smem(reinterpret_cast<const void*>(decode_kernel<D, E4M3, kRowHalves>), S::kSmem) != cudaSuccess)
     return DS_VIT_ECUDA;
-  const int R = a.b.max_rows * a.group, grid = num_sms();
-  const int workers = grid * kWarps;
+  const int R = std::min(a.b.max_rows * a.group, kRows), grid = num_sms();
+  const int workers = grid * S::kWarps;
   const Records rec = records_in(ws, workers, R, D);
-  cudaError_t e = launch_pdl(decode_kernel<D, E4M3, kRowHalves>, dim3(grid), dim3(kThreads), S::kSmem, stream, tk, tv,
+  cudaError_t e = launch_pdl(decode_kernel<D, E4M3, kRowHalves>, dim3(grid), dim3(S::kThreads), S::kSmem, stream, tk, tv,
                              a, rec);
   if (e == cudaSuccess) e = launch_join<D, E4M3>(a, rec, grid, workers, stream);
   if (e != cudaSuccess) cudaGetLastError();
@@ -670,12 +684,12 @@ int launch(const AttentionArgs& a, void* ws, cudaStream_t stream) {
 }  // namespace
 
 size_t cache_decode_workspace(int head_dim, int rows) {
-  return records_bytes(static_cast<int64_t>(num_sms()) * kWarps, rows, head_dim);
+  const int warps = head_dim == 64 ? Shape<64, false>::kWarps : Shape<128, false>::kWarps;
+  return records_bytes(static_cast<int64_t>(num_sms()) * warps, std::min(rows, kRows), head_dim);
 }
 
 int launch_cache_decode(const AttentionArgs& a, int head_dim, bool e4m3, void* ws, cudaStream_t stream) {
   const int R = a.b.max_rows * a.group;
-  if (R > kDecodeRows) return DS_VIT_EINVAL;
   if (head_dim == 128) {
     if (R <= 8) return e4m3 ? launch<128, true, 1>(a, ws, stream) : launch<128, false, 1>(a, ws, stream);
     return e4m3 ? launch<128, true, 2>(a, ws, stream) : launch<128, false, 2>(a, ws, stream);
