@@ -21,10 +21,10 @@ void blocks(int p0, int p1, int window, int sinks, int shift, int* out) {
 int block_at(int p0, int p1, int window, int sinks, int shift, int i) {
   return key_blocks(p0, p1, window, sinks, shift).at(i);
 }
-int64_t begin(int64_t w, int64_t W, int64_t U) { return share_begin(w, W, U); }
+int64_t begin(int64_t w, int64_t W, int64_t U) { return deal(U, W).begin(w); }
 int divide(int n, int d) { return fast_div(d)(n); }
 int64_t snapped(int64_t x, int64_t i0, int64_t i1, int64_t snap) { return snap_border(x, i0, i1, snap); }
-int64_t owner(int64_t x, int64_t W, int64_t U) { return share_of(x, W, U); }
+int64_t owner(int64_t x, int64_t W, int64_t U) { return deal(U, W).owner(x); }
 }
 """
 
@@ -97,10 +97,11 @@ def test_shares(plan):
         for w in range(W):
             for x in (edge[w], edge[w + 1] - 1):
                 assert plan.owner(x, W, U) == w
-    U, W = 1024 * 128 * 2 ** 27, 1216
+    U, W = 1024 * 128 * 2 ** 27 + 5, 1216
     for w in (0, 1, 700, 1215):
         x = plan.begin(w, W, U)
-        assert x == w * U // W and plan.owner(x, W, U) == w
+        assert x == w * (U // W) + min(w, U % W) and plan.owner(x, W, U) == w
+    assert plan.begin(0, 0, 0) == 0
 
 
 def test_division_by_the_group(plan):

@@ -284,13 +284,14 @@ __global__ void __launch_bounds__(Shape<D, E4M3>::kThreads, 1)
 
   const int64_t all = static_cast<int64_t>(gridDim.x) * kWarps;
   const int64_t W = total < all ? total : all;
+  const Shares shares = deal(total, W);
   // Neighbouring shares go to different SMs.
   auto worker = [&](int w) { return static_cast<int64_t>(w) * gridDim.x + blockIdx.x; };
   if (warp == kWarps) {
     Plan pl{pre, seqs, 0, 0};
     if (lane < kWarps && worker(lane) < W) {
-      pl.begin = share_begin(worker(lane), W, total);
-      pl.end = share_begin(worker(lane) + 1, W, total);
+      pl.begin = shares.begin(worker(lane));
+      pl.end = shares.begin(worker(lane) + 1);
     }
     produce<D, E4M3>(&tm_k, &tm_v, a, pl, rings + lane * kRingBytes, exps0 + lane * S::kStages * S::kExp,
                      full_of(lane), empty_of(lane));
@@ -301,7 +302,7 @@ __global__ void __launch_bounds__(Shape<D, E4M3>::kThreads, 1)
     if (lane == 0) rec.headers[me] = SplitHeader{};
     return;
   }
-  const Plan pl{pre, seqs, share_begin(me, W, total), share_begin(me + 1, W, total)};
+  const Plan pl{pre, seqs, shares.begin(me), shares.begin(me + 1)};
   const uint32_t ring = rings + warp * kRingBytes, exps = exps0 + warp * S::kStages * S::kExp;
   const uint32_t full = full_of(warp), empty = empty_of(warp);
 
@@ -581,7 +582,7 @@ __global__ void __launch_bounds__(Shape<D, E4M3>::kThreads, 1)
     const bool begun = it.b > 0, whole = !begun && it.end == it.kb.count;
     if (!begun && !whole) {
       const int64_t last = u - it.b + it.kb.count - 1;
-      header = SplitHeader{static_cast<int>(share_of(last, W, total) - me) + 1, it.s, it.head, it.rho0, it.q, 0};
+      header = SplitHeader{static_cast<int>(shares.owner(last) - me) + 1, it.s, it.head, it.rho0, it.q, 0};
     }
     float* r = rec.at(me, begun ? 0 : 1);
     uint32_t redo = 0;

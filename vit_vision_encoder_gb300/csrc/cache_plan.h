@@ -32,12 +32,21 @@ DSV_HD KeyBlocks key_blocks(int p0, int p1, int window, int sinks, int shift) {
   return KeyBlocks{sink, first, sink + (p1 >> shift) - first + 1};
 }
 
-// U units of work dealt to W <= U workers in order: worker w takes units
-// share_begin(w) .. share_begin(w + 1) - 1, at least one.
-DSV_HD int64_t share_begin(int64_t w, int64_t W, int64_t U) { return w * U / W; }
-
-// The worker that takes unit x: the largest w with floor(w U / W) <= x.
-DSV_HD int64_t share_of(int64_t x, int64_t W, int64_t U) { return ((x + 1) * W - 1) / U; }
+// U units of work dealt in order to W workers, W <= U (or both 0): the first
+// `more` take each + 1 units, the others `each`.
+struct Shares {
+  int64_t each, more;
+  DSV_HD int64_t begin(int64_t w) const { return w * each + (w < more ? w : more); }
+  // The worker that takes unit x.
+  DSV_HD int64_t owner(int64_t x) const {
+    const int64_t head = more * (each + 1);
+    return x < head ? x / (each + 1) : more + (x - head) / each;
+  }
+};
+DSV_HD Shares deal(int64_t U, int64_t W) {
+  const int64_t each = W > 0 ? U / W : 0;
+  return Shares{each, U - each * W};
+}
 
 // Division of 0 <= n < 2^31 by a fixed d >= 1 without a divide: with
 // 2^s >= d and m = ceil(2^(32 + s) / d) - 2^32, n / d = (mulhi(n, m) + n) >> s.

@@ -17,8 +17,12 @@
 //   O_X += P_X V_j      (M 128, N D,   K 128)  TMEM x smem -> TMEM
 // P_X (16-bit pairs) takes the first half of S_X's columns, so S_X of the next
 // tile waits for P_X V_j; the other tile's MMAs and softmax fill that time.
-// Rows of Q are loaded by their softmax threads, so any group size fills the
-// tiles.
+// Rows of Q are loaded by the softmax warps, so any group size fills the tiles.
+// Warp 19 walks the CTA's items and hands them to the other roles through a
+// ring in shared memory.  The rows' way in and out of the tiles is through
+// 16-byte pieces that lie side by side in memory (by way of the row's place in
+// the Q tile on the way out): as accesses of a thread to its own row, they took
+// 6000 cycles in and 10000 out an item.
 //
 // e4m3 pages: warps 20-23 widen the raw tiles to fp16 in shared memory (the
 // conversion is exact; the rows of a tile are scaled by powers of two to the
@@ -40,14 +44,14 @@ namespace {
 constexpr int kTile = 128;                  // rows of a query tile, keys of a key tile
 constexpr int kTileShift = 7;
 constexpr int kItemRows = 2 * kTile;
-constexpr int kWarpTma = 16, kWarpMma = 17; // 17: tile A, 18: tile B
+constexpr int kWarpTma = 16, kWarpMma = 17, kWarpJobs = 19;   // 17: tile A, 18: tile B
 constexpr int kWarpConvert = 20;            // 20 .. 23 (e4m3)
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kTmemO = 256;            // S_A, S_B at 0, 128; O_A, O_B from here
 
 template <int D, bool E4M3>
 struct Cfg {
-  static constexpr int kThreads = E4M3 ? 768 : 608;
+  static constexpr int kThreads = E4M3 ? 768 : 640;
   static constexpr int kBytes = kTile * D * 2;             // a 16-bit tile of 128 rows
   static constexpr int kHalf = kTile * 128;                // 64 dims of it
   static constexpr int kRawBytes = kTile * D;              // an e4m3 tile
@@ -57,7 +61,7 @@ struct Cfg {
   static constexpr int kOffRaw = kOffKv + kRing * kBytes;
   static constexpr int kOffExp = kOffRaw + kRaw * kRawBytes;   // exponents of the raw tiles
   static constexpr int kOffBar = kOffExp + kRaw * kTile;
-  static constexpr int kSmem = kOffBar + 512 + 1024;
+  static constexpr int kSmem = kOffBar + 1024 + 1024;
   static_assert(kSmem <= 232448, "shared memory");
   static constexpr float kLag = E4M3 ? 14.f : 8.f;         // see Reference in the kernel for few rows
   static constexpr float kLead = E4M3 ? 6.f : 0.f;
@@ -76,7 +80,9 @@ enum : int {
   kBarRagged = 32,          // a value tile with rows to zero has landed
   kBarDrain = 33,           // [2]
   kBarTurn = 35,            // [2 tiles][4 quadrants]: the quadrant's warps of tile X finished the exponents of a step
-  kBarCount = 43
+  kBarJobFull = 43,         // [4]
+  kBarJobEmpty = 47,        // [4]
+  kBarCount = 51
 };
 
 struct PrefillArgs {
@@ -112,37 +118,44 @@ __device__ __forceinline__ KeyBlocks item_blocks(const AttentionArgs& a, const S
   return kb;
 }
 
-// A role's walk over the CTA's items, in the order sequence, item, head.
+// What the roles need to know of an item, and the CTA's part of its tiles.
+struct alignas(16) Job {
+  int s, head;
+  int rho0;                   // first of its rows among those that share the K/V head
+  int whole;                  // 1: all tiles are the CTA's; 0: a record is left, 2: for an item begun elsewhere
+  Seq q;
+  int b;
+  KeyBlocks kb;
+  int end;                    // tiles b .. end - 1; none: no more items
+};
+constexpr int kJobs = 4;
+
+// The CTA's items in the order sequence, item, head.
 struct Walk {
-  int s, k, head, b, end;     // tiles b .. end - 1 of the item are this CTA's
+  int s, k, head, b, end;
   Seq q;
   KeyBlocks kb;
   int64_t left;               // units left, this item's included
-  bool begun, whole;          // tiles before b / all tiles are in other hands / here
 
   __device__ __forceinline__ void enter(const AttentionArgs& a, int b0) {
     kb = item_blocks(a, q, k);
     b = b0;
     end = left < kb.count - b ? b + static_cast<int>(left) : kb.count;
-    begun = b > 0;
-    whole = !begun && end == kb.count;
   }
   __device__ __forceinline__ void start(const AttentionArgs& a, const Start& st) {
     s = st.s, k = st.k, head = st.head;
     left = st.units;
     q = left > 0 ? load_seq(a.b, a.c.page_shift, s, nullptr) : Seq{0, 0, 0};
     if (left <= 0) return;
-    if (st.b < item_blocks(a, q, k).count)
-      enter(a, st.b);
-    else
-      step(a);                              // the border moved to this item's end
+    enter(a, st.b);
+    if (b >= kb.count) step(a);             // the border moved to this item's end
   }
   // To the next item; left must be positive afterwards for it to exist.
   __device__ __forceinline__ void next(const AttentionArgs& a) {
     left -= end - b;
     if (left > 0) step(a);
   }
-  __device__ __forceinline__ void step(const AttentionArgs& a) {
+  __device__ __noinline__ void step(const AttentionArgs& a) {
     if (++head == a.c.kv_heads) {
       head = 0;
       if (++k == items_of(a, q)) {
@@ -222,9 +235,10 @@ __device__ __forceinline__ Start make_plan(const AttentionArgs& a, uint8_t* scra
   int64_t at = scan(mine, total);
   // This CTA's borders, moved to an item's end where one is near.
   const int64_t W = total < gridDim.x ? total : gridDim.x, w = blockIdx.x;
-  const int64_t share = W > 0 ? total / W : 0, near = 3 * share / 8;
+  const Shares shares = deal(total, W);
+  const int64_t near = 3 * shares.each / 8;
   const int snap = near < kSnap ? static_cast<int>(near) : kSnap;
-  const int64_t x0 = w < W ? share_begin(w, W, total) : total, x1 = w < W ? share_begin(w + 1, W, total) : total;
+  const int64_t x0 = w < W ? shares.begin(w) : total, x1 = w < W ? shares.begin(w + 1) : total;
   if (tid == 0) {
     border[0] = border[1] = total;
     *found = Start{};
@@ -237,7 +251,8 @@ __device__ __forceinline__ Start make_plan(const AttentionArgs& a, uint8_t* scra
       for (int e = 0; e < 2; ++e) {
         const int64_t x = e == 0 ? x0 : x1;
         if (x < at || x >= at + here) continue;
-        const int head = static_cast<int>((x - at) / count);
+        const int head = static_cast<int>(x - at < INT32_MAX ? static_cast<uint32_t>(x - at) / static_cast<uint32_t>(count)
+                                                             : (x - at) / count);
         const int64_t i0 = at + static_cast<int64_t>(head) * count, y = snap_border(x, i0, i0 + count, snap);
         border[e] = y;
         if (e == 0) {
@@ -302,6 +317,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + kBarCount);
   volatile int* tile_exp = reinterpret_cast<volatile int*>(bars + kBarCount + 1);   // [8] K, [8] V: E of recent tiles
+  Job* jobs = reinterpret_cast<Job*>(smem + C::kOffBar + 512);
   const uint32_t base = smem_u32(smem), bar0 = smem_u32(bars);
   auto bar = [&](int i) { return bar0 + 8u * static_cast<uint32_t>(i); };
   auto sQ = [&](int x) { return base + x * C::kBytes; };
@@ -326,6 +342,10 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
       mbar_init(bar(kBarRawFull + i), 1);
       mbar_init(bar(kBarRawEmpty + i), 4);
     }
+    for (int i = 0; i < kJobs; ++i) {
+      mbar_init(bar(kBarJobFull + i), 1);
+      mbar_init(bar(kBarJobEmpty + i), 19 + (E4M3 ? 4 : 0));   // softmax, TMA, MMA and converter warps
+    }
     mbar_init(bar(kBarRagged), 1);
     fence_barrier_init();
   }
@@ -347,6 +367,18 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
   fence_proxy_async_smem();                 // the scratch becomes the ring
   __syncthreads();
   __shared__ int consumed[2];
+  // Job n of the ring: every thread of a role's warp reads it (MMA: the one
+  // that issues), then one of them hands the slot back.
+  auto take = [&](int n, Job& j, bool one) {
+    const int i = n % kJobs;
+    const bool ok = mbar_wait(bar(kBarJobFull + i), (n / kJobs) & 1, a.status);
+    const int4* src = reinterpret_cast<const int4*>(jobs + i);
+    int4* dst = reinterpret_cast<int4*>(&j);
+    dst[0] = src[0], dst[1] = src[1], dst[2] = src[2];
+    if (!one) __syncwarp();
+    if (one || lane == 0) mbar_arrive(bar(kBarJobEmpty + i));
+    return ok && j.b < j.end;
+  };
   int issued = 0;                           // ring or raw tiles whose loads were issued
 
   // e4m3: 24 warps start with 80 registers each; 16 x 96 + 8 x 48 is the same sum.
@@ -361,11 +393,10 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
     int slot = 0, ragged = 0;
     uint32_t phase = 1;
     bool ok = true;
-    Walk w;
-    w.start(a, st);
-    while (ok && w.left > 0) {
-      int p0, p1;
-      item_positions(a, w.q, w.k, p0, p1);
+    Job w;
+    for (int n = 0; ok && take(n, w, false); ++n) {
+      const int p0 = w.q.kv - w.q.c + a.by_group(w.rho0);
+      const int p1 = w.q.kv - w.q.c + a.by_group(min(w.rho0 + kItemRows, w.q.c * a.group) - 1);
       const int lo = window_start(a, p0);
       auto any = [&](int j0, int j1) { return j0 <= p1 && (j1 >= lo || j0 < a.sinks); };   // a key of j0 .. j1 is seen
       auto look = [&](int b) {
@@ -429,7 +460,31 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
         }
         if (!ok) break;
       }
-      w.next(a);
+    }
+  } else if (warp == kWarpJobs) {
+    // ------------------------------------------------------------ the items
+    if (lane == 0) {
+      SplitHeader header{};
+      Walk w;
+      w.start(a, st);
+      for (int n = 0;; ++n) {
+        const int i = n % kJobs;
+        if (!mbar_wait(bar(kBarJobEmpty + i), ((n / kJobs) & 1) ^ 1, a.status)) break;
+        const bool more = w.left > 0;
+        const bool whole = more && w.b == 0 && w.end == w.kb.count;
+        jobs[i] = more ? Job{w.s, w.head, w.k * kItemRows, whole ? 1 : w.b > 0 ? 2 : 0, w.q, w.b, w.kb, w.end} : Job{};
+        mbar_arrive(bar(kBarJobFull + i));
+        if (!more) break;
+        if (!whole && w.b == 0) {
+          const Shares shares = deal(st.total, st.total < gridDim.x ? st.total : gridDim.x);
+          const int64_t i0 = st.first + st.units - w.left, i1 = i0 + w.kb.count;
+          int64_t last = shares.owner(i1 - 1);       // the last worker whose border is not at or behind the end
+          while (last > blockIdx.x && snap_border(shares.begin(last), i0, i1, st.snap) >= i1) --last;
+          header = SplitHeader{static_cast<int>(last - blockIdx.x) + 1, w.s, w.head, w.k * kItemRows, w.q, 0};
+        }
+        w.next(a);
+      }
+      p.rec.headers[blockIdx.x] = header;
     }
   } else if (warp == kWarpMma || warp == kWarpMma + 1) {
     // ------------------------------------------------------------ MMA issuer of tile X
@@ -463,10 +518,9 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
         umma_commit(bar(kBarKvEmpty + slot));
         advance();
       };
-      Walk w;
-      w.start(a, st);
-      while (ok && w.left > 0) {
-        const int rows = w.q.c * a.group - w.k * kItemRows;
+      Job w;
+      for (int n = 0; ok && take(n, w, true); ++n) {
+        const int rows = w.q.c * a.group - w.rho0;
         if (rows <= x * kTile) {
           // No rows in this tile: the buffers are only handed back.
           for (int j = 0; j < 2 * (w.end - w.b); ++j) {
@@ -475,7 +529,6 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
             mbar_arrive(bar(kBarKvEmpty + slot));
             advance();
           }
-          w.next(a);
           continue;
         }
         ok = mbar_wait(bar(kBarQ + x), q_phase, a.status) && mbar_wait(bar(kBarKvFull + slot), phase, a.status);
@@ -503,7 +556,6 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
           }
           ++step;
         }
-        w.next(a);
       }
       consumed[x] = used;
       // All MMAs of this warp complete before TMEM is released.
@@ -525,11 +577,10 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
     int raw = 0, slot = 0, tile = 0;
     uint32_t raw_phase = 0, phase = 1;
     bool ok = true;
-    Walk w;
-    w.start(a, st);
-    while (ok && w.left > 0) {
-      int p0, p1;
-      item_positions(a, w.q, w.k, p0, p1);
+    Job w;
+    for (int n = 0; ok && take(n, w, false); ++n) {
+      const int p0 = w.q.kv - w.q.c + a.by_group(w.rho0);
+      const int p1 = w.q.kv - w.q.c + a.by_group(min(w.rho0 + kItemRows, w.q.c * a.group) - 1);
       const int lo = window_start(a, p0);
       auto any = [&](int j) { return j <= p1 && (j >= lo || j < a.sinks); };
       for (int b = w.b; b < w.end; ++b, ++tile) {
@@ -593,7 +644,6 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
         }
         if (!ok) break;
       }
-      w.next(a);
     }
   } else {
     if constexpr (E4M3) registers_inc<96>();
@@ -608,54 +658,56 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
     uint32_t step = 0, turn = 0;             // steps of this tile, and those that both tiles took
     int tile = 0;
     bool ok = true;
-    if (threadIdx.x == 0) p.rec.headers[blockIdx.x] = SplitHeader{};
-    Walk w;
-    w.start(a, st);
-    while (ok && w.left > 0) {
-      const int rho0 = w.k * kItemRows + x * kTile;      // first row of the tile
+    Job w;
+    for (int n = 0; ok && take(n, w, false); ++n) {
+      const int rho0 = w.rho0 + x * kTile;   // first row of the tile
       const int R = w.q.c * a.group;
       if (rho0 >= R) {
         tile += w.end - w.b;
-        w.next(a);
         continue;
       }
-      const bool both = R - w.k * kItemRows > kTile;     // tile B has rows too
-      const int rho = rho0 + r;
-      const bool on = rho < R;
-      const int i = a.by_group(rho), hq = w.head * a.group + (rho - i * a.group);
+      const bool both = R - w.rho0 > kTile;  // tile B has rows too
       const int first = w.q.kv - w.q.c;
-      const int pos = on ? first + i : -1;
-      // Positions of the tile's first and last rows, for tiles without a mask.
-      const int pa = first + a.by_group(rho0), pb = first + a.by_group(min(rho0 + kTile, R) - 1);
-      const int lo = window_start(a, pos), lo_b = window_start(a, pb);
-      // ---- this thread's half of its query row
+      // ---- the warp's 16 query rows: lane l takes piece l % kPieces of rows l / kPieces, + kEach, ...
       float c0 = a.scale_log2;
       {
-        uint4 v[D / 16];
-        const uint4* src = reinterpret_cast<const uint4*>(a.q + (w.q.row0 + i) * a.q_stride + hq * D + h * (D / 2));
+        constexpr int kPieces = D / 8, kEach = 32 / kPieces;
+        const int piece = lane % kPieces;
+        uint4 v[16 / kEach];
 #pragma unroll
-        for (int y = 0; y < D / 16; ++y) v[y] = on ? __ldg(src + y) : make_uint4(0, 0, 0, 0);
-        if constexpr (E4M3) {
-          uint32_t top = 0;
-#pragma unroll
-          for (int y = 0; y < D / 16; ++y)
-            top = __vmaxu2(top, __vmaxu2(__vmaxu2(v[y].x & 0x7FFF7FFFu, v[y].y & 0x7FFF7FFFu),
-                                         __vmaxu2(v[y].z & 0x7FFF7FFFu, v[y].w & 0x7FFF7FFFu)));
-          top = max(top & 0xFFFFu, top >> 16);
-          top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 16));
-          // The largest's exponent field E: times 2^(141 - E), in two steps of normal powers of two.
-          const int E = max(static_cast<int>(top >> 7), 1), up = 141 - E, half = up / 2;
-          const float f0 = __int_as_float((127 + half) << 23), f1 = __int_as_float((127 + up - half) << 23);
-          c0 = a.scale_log2 * __int_as_float((127 - half) << 23) * __int_as_float((127 - up + half) << 23);
-          auto to16 = [&](uint32_t two) { return pack_f16x2(bf16lo(two) * f0 * f1, bf16hi(two) * f0 * f1); };
-#pragma unroll
-          for (int y = 0; y < D / 16; ++y) v[y] = make_uint4(to16(v[y].x), to16(v[y].y), to16(v[y].z), to16(v[y].w));
+        for (int y = 0; y < 16 / kEach; ++y) {
+          const int rho = rho0 + row0 + y * kEach + lane / kPieces, i = a.by_group(rho);
+          const bf16* src = a.q + (w.q.row0 + i) * a.q_stride + (w.head * a.group + rho - i * a.group) * D + piece * 8;
+          v[y] = rho < R ? __ldg(reinterpret_cast<const uint4*>(src)) : make_uint4(0, 0, 0, 0);
         }
 #pragma unroll
-        for (int y = 0; y < D / 16; ++y) sts128(tile_piece<D, E4M3>(sQ(x), r, h * (D / 16) + y), v[y]);
+        for (int y = 0; y < 16 / kEach; ++y) {
+          if constexpr (E4M3) {
+            uint32_t top = __vmaxu2(__vmaxu2(v[y].x & 0x7FFF7FFFu, v[y].y & 0x7FFF7FFFu),
+                                    __vmaxu2(v[y].z & 0x7FFF7FFFu, v[y].w & 0x7FFF7FFFu));
+            top = max(top & 0xFFFFu, top >> 16);
+#pragma unroll
+            for (int o = kPieces / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+            // The largest's exponent field E: times 2^(141 - E), in two steps of normal powers of two.
+            const int E = max(static_cast<int>(top >> 7), 1), up = 141 - E, half = up / 2;
+            const float f0 = __int_as_float((127 + half) << 23), f1 = __int_as_float((127 + up - half) << 23);
+            auto to16 = [&](uint32_t two) { return pack_f16x2(bf16lo(two) * f0 * f1, bf16hi(two) * f0 * f1); };
+            v[y] = make_uint4(to16(v[y].x), to16(v[y].y), to16(v[y].z), to16(v[y].w));
+            // The row's own threads scale its scores back.
+            const int mine = __shfl_sync(0xFFFFFFFFu, up, (lane % kEach) * kPieces);
+            if ((lane & 15) / kEach == y)
+              c0 = a.scale_log2 * __int_as_float((127 - mine / 2) << 23) * __int_as_float((127 - mine + mine / 2) << 23);
+          }
+          sts128(tile_piece<D, E4M3>(sQ(x), row0 + y * kEach + lane / kPieces, piece), v[y]);
+        }
       }
       fence_proxy_async_smem();
       mbar_arrive(bar(kBarQ + x));
+      const int rho = rho0 + r;
+      const int pos = rho < R ? first + a.by_group(rho) : -1;
+      // Positions of the tile's first and last rows, for tiles without a mask.
+      const int pa = first + a.by_group(rho0), pb = first + a.by_group(min(rho0 + kTile, R) - 1);
+      const int lo = window_start(a, pos), lo_b = window_start(a, pb);
 
       float m = -INFINITY, l = 0.f;
       for (int b = w.b; b < w.end; ++b, ++tile, ++step) {
@@ -759,63 +811,87 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
         break;
       }
       tc_fence_after();
-      // ---- the item's end: finished here, or a record for the join
+      // ---- the item's end: finished here, or a record for the join.  The rows go
+      // through their place in the Q tile (its products are complete), 16 bytes a
+      // piece, and leave as whole rows.
       l += __shfl_xor_sync(0xFFFFFFFFu, l, 16);
-      if (threadIdx.x == 0 && !w.begun && !w.whole) {
-        const int64_t W = st.total < gridDim.x ? st.total : gridDim.x;
-        const int64_t i0 = st.first + st.units - w.left, i1 = i0 + w.kb.count;
-        int64_t last = share_of(i1 - 1, W, st.total);      // the last worker whose border is not at or behind the end
-        while (last > blockIdx.x && snap_border(share_begin(last, W, st.total), i0, i1, st.snap) >= i1) --last;
-        p.rec.headers[blockIdx.x] =
-            SplitHeader{static_cast<int>(last - blockIdx.x) + 1, w.s, w.head, w.k * kItemRows, w.q, 0};
-      }
-      const float inv = pos < 0 ? 0.f : 1.f / l;
-      float* rec = p.rec.at(blockIdx.x, w.begun ? 0 : 1);
-      const int rr = x * kTile + r;          // row of the record
-      bool bad = false;
-#pragma unroll
-      for (int y = 0; y < D / 64; ++y) {
-        uint32_t o[32];
-        tmem_ld32_x2<D / 2>(tO + 32 * y, o);
-        tmem_wait_ld();
-        const int d0 = h * (D / 2) + 32 * y;
-        if (!on) continue;
-        if (w.whole) {
-          uint4* dst = reinterpret_cast<uint4*>(a.out + (w.q.row0 + i) * a.out_stride + hq * D + d0);
-          uint32_t pk[16];
+      uint32_t redo = 0;
+      if (w.whole == 1) {
+        const float inv = pos < 0 ? 0.f : 1.f / l;
+        bool bad = false;
+#pragma unroll 1
+        for (int y = 0; y < D / 64; ++y) {
+          uint32_t o[32];
+          tmem_ld32_x2<D / 2>(tO + 32 * y, o);
+          tmem_wait_ld();
 #pragma unroll
           for (int z = 0; z < 16; ++z) {
             const float o0 = __uint_as_float(o[2 * z]) * inv, o1 = __uint_as_float(o[2 * z + 1]) * inv;
             bad |= not_finite(o0) || not_finite(o1);
-            pk[z] = pack_bf16x2(o0, o1);
+            o[z] = pack_bf16x2(o0, o1);
           }
 #pragma unroll
-          for (int z = 0; z < 4; ++z) dst[z] = make_uint4(pk[4 * z], pk[4 * z + 1], pk[4 * z + 2], pk[4 * z + 3]);
-        } else {
-          uint4* dst = reinterpret_cast<uint4*>(rec + static_cast<int64_t>(rr) * D + d0);
+          for (int z = 0; z < 4; ++z)
+            sts128(tile_piece<D, E4M3>(sQ(x), r, h * (D / 16) + 4 * y + z),
+                   make_uint4(o[4 * z], o[4 * z + 1], o[4 * z + 2], o[4 * z + 3]));
+        }
+        __syncwarp();
+        constexpr int kPieces = D / 8, kEach = 32 / kPieces;
 #pragma unroll
-          for (int z = 0; z < 8; ++z) dst[z] = make_uint4(o[4 * z], o[4 * z + 1], o[4 * z + 2], o[4 * z + 3]);
+        for (int y = 0; y < 16 / kEach; ++y) {
+          const int rr = row0 + y * kEach + lane / kPieces, piece = lane % kPieces;
+          const int i = a.by_group(rho0 + rr);
+          const uint4 v = lds128(tile_piece<D, E4M3>(sQ(x), rr, piece));
+          if (rho0 + rr < R)
+            *reinterpret_cast<uint4*>(a.out + (w.q.row0 + i) * a.out_stride +
+                                      (w.head * a.group + rho0 + rr - i * a.group) * D + piece * 8) = v;
+        }
+        if (w.q.c > 1) {
+          redo = __ballot_sync(0xFFFFFFFFu, bad && rho < R);
+          redo = (redo | (redo >> 16)) & 0xFFFFu;
+        }
+      } else {
+        float* rec = p.rec.at(blockIdx.x, w.whole == 2 ? 0 : 1);
+        if (h == 0) {
+          p.rec.max_of(rec, D)[x * kTile + r] = m;
+          p.rec.sum_of(rec, D)[x * kTile + r] = l;
+        }
+        // Passes of kCols columns of each half of the dims: a row's place holds both.
+        constexpr int kCols = D / 4;
+#pragma unroll 1
+        for (int y = 0; y < D / 2; y += kCols) {
+          uint32_t o[32];
+          if constexpr (kCols == 32)
+            tmem_ld32_x2<D / 2>(tO + y, o);
+          else
+            tmem_ld16_x2<D / 2>(tO + y, o);
+          tmem_wait_ld();
+          __syncwarp();                      // the last pass has been read
+#pragma unroll
+          for (int z = 0; z < kCols / 4; ++z)
+            sts128(tile_piece<D, E4M3>(sQ(x), r, h * (kCols / 4) + z),
+                   make_uint4(o[4 * z], o[4 * z + 1], o[4 * z + 2], o[4 * z + 3]));
+          __syncwarp();
+          constexpr int kPieces = kCols / 2, kEach = 32 / kPieces;      // pieces of a row's place
+#pragma unroll
+          for (int z = 0; z < 16 / kEach; ++z) {
+            const int rr = row0 + z * kEach + lane / kPieces, piece = lane % kPieces;
+            const int d0 = (piece / (kPieces / 2)) * (D / 2) + y + 4 * (piece % (kPieces / 2));
+            *reinterpret_cast<uint4*>(rec + static_cast<int64_t>(x * kTile + rr) * D + d0) =
+                lds128(tile_piece<D, E4M3>(sQ(x), rr, piece));
+          }
         }
       }
       tc_fence_before();
-      if (!w.whole && on && h == 0) {
-        p.rec.max_of(rec, D)[rr] = m;
-        p.rec.sum_of(rec, D)[rr] = l;
+      __syncwarp();                          // the rows' places are free for the next item's
+      while (redo) {
+        const int y = __ffs(static_cast<int>(redo)) - 1;
+        redo &= redo - 1;
+        const int rho_y = rho0 + row0 + y, iy = a.by_group(rho_y);
+        exact_row<D, E4M3>(a, w.s, w.q.row0, first + iy, iy, w.head * a.group + rho_y - iy * a.group, lane);
+        __syncwarp();
       }
-      if (w.q.c > 1) {
-        uint32_t redo = __ballot_sync(0xFFFFFFFFu, bad);
-        redo = (redo | (redo >> 16)) & 0xFFFFu;
-        while (redo) {
-          __syncwarp();
-          const int y = __ffs(static_cast<int>(redo)) - 1;
-          redo &= redo - 1;
-          const int rho_y = rho0 + row0 + y, iy = a.by_group(rho_y);
-          exact_row<D, E4M3>(a, w.s, w.q.row0, first + iy, iy, w.head * a.group + rho_y - iy * a.group, lane);
-        }
-      }
-      w.next(a);
     }
-    if (threadIdx.x == 0 && !ok) p.rec.headers[blockIdx.x] = SplitHeader{};
   }
 
   tc_fence_before();

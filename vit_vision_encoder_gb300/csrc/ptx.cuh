@@ -443,6 +443,17 @@ __device__ __forceinline__ void tmem_ld32_x2(uint32_t taddr, uint32_t (&r)[32]) 
       : "r"(taddr), "n"(kHalf));
 }
 
+// 16 columns per thread, into r[0 .. 15].
+template <int kHalf>
+__device__ __forceinline__ void tmem_ld16_x2(uint32_t taddr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x32bx2.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16], %17;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr), "n"(kHalf));
+}
+
 template <int kHalf>
 __device__ __forceinline__ void tmem_st32_x2(uint32_t taddr, const uint32_t (&r)[32]) {
   asm volatile(
