@@ -97,7 +97,10 @@ struct Start {
   int64_t units, total, first;
   int snap;
 };
-constexpr int kSnap = 6;
+// A split costs what some six tiles do (the second load of the rows, records of
+// 128 KB a part, their sum), so borders move to an item's end within six; and
+// where even the longest item is short and not much over a share, no item is split.
+constexpr int kSnap = 6, kUnsplit = 16;
 
 __device__ __forceinline__ int items_of(const AttentionArgs& a, const Seq& q) {
   return (q.c * a.group + kItemRows - 1) / kItemRows;
@@ -178,6 +181,7 @@ __device__ __forceinline__ Start make_plan(const AttentionArgs& a, uint8_t* scra
   constexpr int kWarps = kThreads / 32;
   __shared__ int64_t warp_sum[kWarps];
   __shared__ int64_t border[2];
+  __shared__ int longest;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   auto scan = [&](int64_t x, int64_t& total) {      // exclusive prefix over the block
     auto inclusive = [&](int64_t v) {
@@ -206,7 +210,10 @@ __device__ __forceinline__ Start make_plan(const AttentionArgs& a, uint8_t* scra
     if (s < a.b.n) items[s] = all + static_cast<int>(before);
     all += static_cast<int>(t);
   }
-  if (tid == 0) items[a.b.n] = all;
+  if (tid == 0) {
+    items[a.b.n] = all;
+    longest = 0;
+  }
   __syncthreads();
   // This thread's run of the list, and its units.
   const int per = (all + kThreads - 1) / kThreads, i0 = min(all, tid * per), i1 = min(all, i0 + per);
@@ -231,13 +238,22 @@ __device__ __forceinline__ Start make_plan(const AttentionArgs& a, uint8_t* scra
     }
   };
   int64_t mine = 0, total;
-  if (i0 < i1) walk([&](int, int, int count) { mine += static_cast<int64_t>(count) * a.c.kv_heads; });
-  int64_t at = scan(mine, total);
+  if (i0 < i1) {
+    int most = 0;
+    walk([&](int, int, int count) {
+      mine += static_cast<int64_t>(count) * a.c.kv_heads;
+      most = max(most, count);
+    });
+    atomicMax(&longest, most);
+  }
+  int64_t at = scan(mine, total);            // its barriers also settle `longest`
   // This CTA's borders, moved to an item's end where one is near.
   const int64_t W = total < gridDim.x ? total : gridDim.x, w = blockIdx.x;
   const Shares shares = deal(total, W);
   const int64_t near = 3 * shares.each / 8;
-  const int snap = near < kSnap ? static_cast<int>(near) : kSnap;
+  const int snap = longest <= kUnsplit && longest <= shares.each + 8 ? kUnsplit
+                   : near < kSnap                                    ? static_cast<int>(near)
+                                                                     : kSnap;
   const int64_t x0 = w < W ? shares.begin(w) : total, x1 = w < W ? shares.begin(w + 1) : total;
   if (tid == 0) {
     border[0] = border[1] = total;

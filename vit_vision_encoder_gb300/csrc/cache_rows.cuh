@@ -94,13 +94,15 @@ inline Records records_in(void* ws, int64_t workers, int rows, int d) {
 }
 
 // Joins the parts of every split item: O = sum_p 2^(m_p - M) O_p, L alike.
-// Block (x, y) looks after workers x, x + gridDim.x, ... and rows y, y +
-// gridDim.y, ... of their items.  Up to kJoinWarps parts, one warp adds up a
-// row; more parts are shared between the block's warps and joined through
-// shared memory.  The order is fixed, so a result depends on the lengths alone.
+// Block (y, x) looks after workers x, x + gridDim.y, ... and rows y, y +
+// gridDim.x, ... of their items (rows in the grid's fast dimension: the blocks
+// of the few workers with something to join then lie on many SMs).  One warp
+// adds up a row; where many parts meet few rows (a token over a long cache) the
+// parts are shared between the block's warps and joined through shared memory.
+// The order is fixed, so a result depends on the lengths alone.
 constexpr int kJoinWarps = 8;
 constexpr int kJoinItems = 16;    // workers per block at most
-constexpr int kJoinRows = 32;     // grid rows at most
+constexpr int kJoinRows = 16;     // grid rows at most
 
 // Adds parts first, first + step, ... of one row to (m, l, o), loads of four parts at a time.
 template <int D>
@@ -181,23 +183,24 @@ __global__ void __launch_bounds__(32 * kJoinWarps)
   grid_dep_launch();
   grid_dep_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int mine = (workers - static_cast<int>(blockIdx.x) + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x);
+  const int group = blockIdx.y, groups = gridDim.y;
+  const int mine = (workers - group + groups - 1) / groups;
   if (threadIdx.x < 2 * mine)
-    reinterpret_cast<int4*>(heads)[threadIdx.x] = reinterpret_cast<const int4*>(
-        rec.headers + blockIdx.x + (threadIdx.x >> 1) * gridDim.x)[threadIdx.x & 1];
+    reinterpret_cast<int4*>(heads)[threadIdx.x] =
+        reinterpret_cast<const int4*>(rec.headers + group + (threadIdx.x >> 1) * groups)[threadIdx.x & 1];
   __syncthreads();
   int turn = 0;                       // rows dealt to the warps so far
   for (int k = 0; k < mine; ++k) {
     const SplitHeader& hd = heads[k];
     if (hd.parts == 0) continue;
-    const int w = blockIdx.x + k * gridDim.x;
+    const int w = group + k * groups;
     const int64_t left = static_cast<int64_t>(hd.q.c) * a.group - hd.rho0;
     const int rows = left < rec.rows ? static_cast<int>(left) : rec.rows;
-    for (int row = blockIdx.y; row < rows; row += gridDim.y) {
+    for (int row = blockIdx.x; row < rows; row += gridDim.x) {
       float m = -INFINITY, l = 0.f, o[kPer];
 #pragma unroll
       for (int x = 0; x < kPer; ++x) o[x] = 0.f;
-      if (hd.parts <= kJoinWarps) {
+      if (hd.parts <= kJoinWarps || rows > 16) {
         if (turn++ % kJoinWarps != warp) continue;
         join_parts<D>(rec, w, hd.parts, row, 0, 1, lane, m, l, o);
         join_finish<D, E4M3>(a, hd, hd.rho0 + row, l, o, lane);
@@ -234,7 +237,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps)
 
 template <int D, bool E4M3>
 cudaError_t launch_join(const AttentionArgs& a, const Records& rec, int grid, int workers, cudaStream_t stream) {
-  return launch_pdl(join_kernel<D, E4M3>, dim3(grid, rec.rows < kJoinRows ? rec.rows : kJoinRows), dim3(32 * kJoinWarps),
+  return launch_pdl(join_kernel<D, E4M3>, dim3(rec.rows < kJoinRows ? rec.rows : kJoinRows, grid), dim3(32 * kJoinWarps),
                     0, stream, a, rec, workers);
 }
 
