@@ -12,13 +12,13 @@
 // Roles: warps 0-7 run the softmax of tile A and warps 8-15 that of tile B, two
 // threads a row (16x32bx2 TMEM accesses, as in the bidirectional kernel); warp
 // 16 loads pages by TMA (a box per page and 64 dims) into a ring of key and
-// value tiles; warps 17 and 18 issue the MMAs of A and B:
+// value tiles; warp 17 issues the MMAs:
 //   S_X = Q_X K_j^T     (M 128, N 128, K D)    smem x smem -> TMEM
 //   O_X += P_X V_j      (M 128, N D,   K 128)  TMEM x smem -> TMEM
 // P_X (16-bit pairs) takes the first half of S_X's columns, so S_X of the next
 // tile waits for P_X V_j; the other tile's MMAs and softmax fill that time.
 // Rows of Q are loaded by the softmax warps, so any group size fills the tiles.
-// Warp 19 walks the CTA's items and hands them to the other roles through a
+// Warp 18 walks the CTA's items and hands them to the other roles through a
 // ring in shared memory.  The rows' way in and out of the tiles is through
 // 16-byte pieces that lie side by side in memory (by way of the row's place in
 // the Q tile on the way out): as accesses of a thread to its own row, they took
@@ -44,14 +44,14 @@ namespace {
 constexpr int kTile = 128;                  // rows of a query tile, keys of a key tile
 constexpr int kTileShift = 7;
 constexpr int kItemRows = 2 * kTile;
-constexpr int kWarpTma = 16, kWarpMma = 17, kWarpJobs = 19;   // 17: tile A, 18: tile B
-constexpr int kWarpConvert = 20;            // 20 .. 23 (e4m3)
+constexpr int kWarpTma = 16, kWarpMma = 17, kWarpJobs = 18;
+constexpr int kWarpConvert = 20;            // 20 .. 23: key tiles, 24 .. 27: value tiles (e4m3)
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kTmemO = 256;            // S_A, S_B at 0, 128; O_A, O_B from here
 
 template <int D, bool E4M3>
 struct Cfg {
-  static constexpr int kThreads = E4M3 ? 768 : 640;
+  static constexpr int kThreads = E4M3 ? 896 : 608;
   static constexpr int kBytes = kTile * D * 2;             // a 16-bit tile of 128 rows
   static constexpr int kHalf = kTile * 128;                // 64 dims of it
   static constexpr int kRawBytes = kTile * D;              // an e4m3 tile
@@ -71,18 +71,17 @@ struct Cfg {
 enum : int {
   kBarQ = 0,                // [2] tile X's query rows are in shared memory
   kBarKvFull = 2,           // [8]
-  kBarKvEmpty = 10,         // [8] released by both MMA warps
+  kBarKvEmpty = 10,         // [8]
   kBarRawFull = 18,         // [4]
   kBarRawEmpty = 22,        // [4]
   kBarSFull = 26,           // [2]
   kBarPFull = 28,           // [2]
   kBarPvDone = 30,          // [2]
   kBarRagged = 32,          // a value tile with rows to zero has landed
-  kBarDrain = 33,           // [2]
-  kBarTurn = 35,            // [2 tiles][4 quadrants]: the quadrant's warps of tile X finished the exponents of a step
-  kBarJobFull = 43,         // [4]
-  kBarJobEmpty = 47,        // [4]
-  kBarCount = 51
+  kBarDrain = 33,
+  kBarJobFull = 34,         // [4]
+  kBarJobEmpty = 38,        // [4]
+  kBarCount = 42
 };
 
 struct PrefillArgs {
@@ -339,7 +338,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
   auto sQ = [&](int x) { return base + x * C::kBytes; };
   auto sKv = [&](int i) { return base + C::kOffKv + i * C::kBytes; };
   auto sRaw = [&](int i) { return base + C::kOffRaw + i * C::kRawBytes; };
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;   // alike in a warp's lanes
 
   if (threadIdx.x == 0) {
     for (int x = 0; x < 2; ++x) {
@@ -347,12 +346,10 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
       mbar_init(bar(kBarSFull + x), 1);
       mbar_init(bar(kBarPFull + x), 256);
       mbar_init(bar(kBarPvDone + x), 1);
-      mbar_init(bar(kBarDrain + x), 1);
-      for (int y = 0; y < 4; ++y) mbar_init(bar(kBarTurn + 4 * x + y), 64);
     }
     for (int i = 0; i < C::kRing; ++i) {
       mbar_init(bar(kBarKvFull + i), E4M3 ? 4 : 1);
-      mbar_init(bar(kBarKvEmpty + i), 2);
+      mbar_init(bar(kBarKvEmpty + i), 1);
     }
     for (int i = 0; i < C::kRaw; ++i) {
       mbar_init(bar(kBarRawFull + i), 1);
@@ -360,9 +357,10 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
     }
     for (int i = 0; i < kJobs; ++i) {
       mbar_init(bar(kBarJobFull + i), 1);
-      mbar_init(bar(kBarJobEmpty + i), 19 + (E4M3 ? 4 : 0));   // softmax, TMA, MMA and converter warps
+      mbar_init(bar(kBarJobEmpty + i), 18 + (E4M3 ? 8 : 0));   // softmax, TMA, MMA and converter warps
     }
     mbar_init(bar(kBarRagged), 1);
+    mbar_init(bar(kBarDrain), 1);
     fence_barrier_init();
   }
   if (warp == kWarpTma) {
@@ -382,24 +380,23 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
   const Start st = make_plan<C::kThreads>(a, smem + C::kOffKv, blockIdx.x == 0 ? a.status : nullptr);
   fence_proxy_async_smem();                 // the scratch becomes the ring
   __syncthreads();
-  __shared__ int consumed[2];
-  // Job n of the ring: every thread of a role's warp reads it (MMA: the one
-  // that issues), then one of them hands the slot back.
-  auto take = [&](int n, Job& j, bool one) {
+  __shared__ int consumed;
+  // Job n of the ring: every thread of a role's warp reads it, then one of them hands the slot back.
+  auto take = [&](int n, Job& j) {
     const int i = n % kJobs;
     const bool ok = mbar_wait(bar(kBarJobFull + i), (n / kJobs) & 1, a.status);
     const int4* src = reinterpret_cast<const int4*>(jobs + i);
     int4* dst = reinterpret_cast<int4*>(&j);
     dst[0] = src[0], dst[1] = src[1], dst[2] = src[2];
-    if (!one) __syncwarp();
-    if (one || lane == 0) mbar_arrive(bar(kBarJobEmpty + i));
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar(kBarJobEmpty + i));
     return ok && j.b < j.end;
   };
   int issued = 0;                           // ring or raw tiles whose loads were issued
 
-  // e4m3: 24 warps start with 80 registers each; 16 x 96 + 8 x 48 is the same sum.
+  // e4m3: 28 warps start with 72 registers each; 16 x 96 + 12 x 40 is the same sum.
   if (warp >= kWarpTma && (!E4M3 || warp < kWarpConvert)) {
-    if constexpr (E4M3) registers_dec<48>();
+    if constexpr (E4M3) registers_dec<40>();
   if (warp == kWarpTma) {
     // ------------------------------------------------------------ TMA producer
     // Lane i loads page i of a tile (of 128 / page pages).
@@ -410,7 +407,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
     uint32_t phase = 1;
     bool ok = true;
     Job w;
-    for (int n = 0; ok && take(n, w, false); ++n) {
+    for (int n = 0; ok && take(n, w); ++n) {
       const int p0 = w.q.kv - w.q.c + a.by_group(w.rho0);
       const int p1 = w.q.kv - w.q.c + a.by_group(min(w.rho0 + kItemRows, w.q.c * a.group) - 1);
       const int lo = window_start(a, p0);
@@ -502,87 +499,111 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
       }
       p.rec.headers[blockIdx.x] = header;
     }
-  } else if (warp == kWarpMma || warp == kWarpMma + 1) {
-    // ------------------------------------------------------------ MMA issuer of tile X
-    const int x = warp - kWarpMma;
-    if (lane == 0) {
-      constexpr uint32_t f16_bits = (1u << 7) | (1u << 10);   // bf16 marks of A and B in the instruction descriptor
-      constexpr uint32_t id_s = idesc_bf16_f32(128, 128, false, false) & ~(E4M3 ? f16_bits : 0u);
-      constexpr uint32_t id_o = idesc_bf16_f32(128, D, false, true) & ~(E4M3 ? f16_bits : 0u);   // V is MN-major
-      const uint32_t tS = tmem + x * 128, tO = tmem + kTmemO + x * D;
-      const uint64_t dq = sdesc_sw128(sQ(x), 16, 1024);
-      const uint64_t dk0 = sdesc_sw128(sKv(0), 16, 1024);
-      const uint64_t dv0 = sdesc_sw128(sKv(0), C::kHalf, 1024);
-      int slot = 0, used = 0;
-      uint32_t phase = 0, q_phase = 0, step = 0;
-      bool ok = true;
-      auto advance = [&]() {
-        ++used;
-        if (++slot == C::kRing) {
-          slot = 0;
-          phase ^= 1;
-        }
-      };
-      auto issue_s = [&]() {
-        const uint64_t dk = dk0 + static_cast<uint64_t>(slot * (C::kBytes >> 4));
-#pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-          const uint64_t off = (k >> 2) * (C::kHalf >> 4) + 2 * (k & 3);
-          umma_bf16(tS, dq + off, dk + off, id_s, k != 0);
-        }
-        umma_commit(bar(kBarSFull + x));
-        umma_commit(bar(kBarKvEmpty + slot));
-        advance();
-      };
-      Job w;
-      for (int n = 0; ok && take(n, w, true); ++n) {
-        const int rows = w.q.c * a.group - w.rho0;
-        if (rows <= x * kTile) {
-          // No rows in this tile: the buffers are only handed back.
-          for (int j = 0; j < 2 * (w.end - w.b); ++j) {
-            ok = mbar_wait(bar(kBarKvFull + slot), phase, a.status);
-            if (!ok) break;
-            mbar_arrive(bar(kBarKvEmpty + slot));
-            advance();
-          }
-          continue;
-        }
-        ok = mbar_wait(bar(kBarQ + x), q_phase, a.status) && mbar_wait(bar(kBarKvFull + slot), phase, a.status);
-        if (!ok) break;
-        q_phase ^= 1;
-        tc_fence_after();
-        issue_s();
-        for (int b = w.b; b < w.end; ++b) {
-          ok = mbar_wait(bar(kBarPFull + x), step & 1, a.status) && mbar_wait(bar(kBarKvFull + slot), phase, a.status);
-          if (!ok) break;
-          tc_fence_after();
-          const uint64_t dv = dv0 + static_cast<uint64_t>(slot * (C::kBytes >> 4));
-#pragma unroll
-          for (int k = 0; k < kTile / 16; ++k)
-            umma_bf16_ts(tO, tS + k * 8, dv + 128 * k, id_o, (b != w.b) | (k != 0));   // 16 rows = 2048 B
-          umma_commit(bar(kBarPvDone + x));
-          umma_commit(bar(kBarKvEmpty + slot));
-          advance();
-          if (b + 1 < w.end) {
-            // S_X overwrites P_X: its product must be complete.
-            ok = mbar_wait(bar(kBarKvFull + slot), phase, a.status) && mbar_wait(bar(kBarPvDone + x), step & 1, a.status);
-            if (!ok) break;
-            tc_fence_after();
-            issue_s();
-          }
-          ++step;
-        }
+  } else if (warp == kWarpMma) {
+    // ------------------------------------------------------------ MMA issuer
+    // Tile by tile in turn, P V of a step and S of the next together: one tile's
+    // pair runs while the other's softmax works.  The whole warp walks along, all
+    // it decides by being alike in its lanes (see umma_bf16_if).  A chunk of 2048
+    // over 32k keys, us: 957 so; 1100 with one lane issuing; 1130 with an issuer for
+    // each tile, whose pairs interleave (and the exponents of the two tiles taking
+    // turns, which this order makes needless); 1357 when whatever is ready goes first.
+    constexpr uint32_t f16_bits = (1u << 7) | (1u << 10);   // bf16 marks of A and B in the instruction descriptor
+    constexpr uint32_t id_s = idesc_bf16_f32(128, 128, false, false) & ~(E4M3 ? f16_bits : 0u);
+    constexpr uint32_t id_o = idesc_bf16_f32(128, D, false, true) & ~(E4M3 ? f16_bits : 0u);   // V is MN-major
+    const uint32_t tm = __shfl_sync(0xFFFFFFFFu, tmem, 0), go = elect_one();
+    const uint64_t dq0 = sdesc_sw128(sQ(0), 16, 1024);
+    const uint64_t dk0 = sdesc_sw128(sKv(0), 16, 1024);
+    const uint64_t dv0 = sdesc_sw128(sKv(0), C::kHalf, 1024);
+    int slot = 0, used = 0;
+    uint32_t phase = 0, q0 = 0, q1 = 0, step0 = 0, step1 = 0;
+    auto wait = [&](int i, uint32_t parity) { return __all_sync(0xFFFFFFFFu, mbar_wait(bar(i), parity, a.status)); };
+    auto advance = [&]() {
+      ++used;
+      if (++slot == C::kRing) {
+        slot = 0;
+        phase ^= 1;
       }
-      consumed[x] = used;
-      // All MMAs of this warp complete before TMEM is released.
-      umma_commit(bar(kBarDrain + x));
-      mbar_wait(bar(kBarDrain + x), 0, a.status);
+    };
+    auto issue_s = [&](int x, int at) {
+      const uint64_t dq = dq0 + static_cast<uint64_t>(x * (C::kBytes >> 4));
+      const uint64_t dk = dk0 + static_cast<uint64_t>(at * (C::kBytes >> 4));
+      tc_fence_after();
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k) {
+        const uint64_t off = (k >> 2) * (C::kHalf >> 4) + 2 * (k & 3);
+        umma_bf16_if(go, tm + x * 128, dq + off, dk + off, id_s, k != 0);
+      }
+      umma_commit_if(go, bar(kBarSFull + x));
+    };
+    auto issue_pv = [&](int x, int at, bool fresh) {
+      const uint64_t dv = dv0 + static_cast<uint64_t>(at * (C::kBytes >> 4));
+      tc_fence_after();
+#pragma unroll
+      for (int k = 0; k < kTile / 16; ++k)
+        umma_bf16_ts_if(go, tm + kTmemO + x * D, tm + x * 128 + k * 8, dv + 128 * k, id_o, !fresh | (k != 0));   // 16 rows = 2048 B
+      umma_commit_if(go, bar(kBarPvDone + x));
+    };
+    Job w;
+    for (int n = 0; __all_sync(0xFFFFFFFFu, take(n, w)); ++n) {
+      const bool both = __shfl_sync(0xFFFFFFFFu, w.q.c * a.group - w.rho0, 0) > kTile;
+      const int count = __shfl_sync(0xFFFFFFFFu, w.end - w.b, 0);
+      if (!wait(kBarKvFull + slot, phase) || !wait(kBarQ, q0)) break;
+      q0 ^= 1;
+      issue_s(0, slot);
+      if (both) {
+        if (!wait(kBarQ + 1, q1)) break;
+        q1 ^= 1;
+        issue_s(1, slot);
+      }
+      umma_commit_if(go, bar(kBarKvEmpty + slot));
+      advance();
+      bool ok = true;
+      for (int b = 0; b < count; ++b) {
+        const bool more = b + 1 < count;
+        const int v_slot = slot;
+        ok = wait(kBarKvFull + v_slot, phase);
+        advance();
+        ok = ok && wait(kBarPFull, step0 & 1);
+        if (!ok) break;
+        issue_pv(0, v_slot, b == 0);
+        if (!both) umma_commit_if(go, bar(kBarKvEmpty + v_slot));
+        if (more) {
+          // S_X overwrites P_X: its product must be complete.
+          ok = wait(kBarKvFull + slot, phase) && wait(kBarPvDone, step0 & 1);
+          if (!ok) break;
+          issue_s(0, slot);
+          if (!both) umma_commit_if(go, bar(kBarKvEmpty + slot));
+        }
+        ++step0;
+        if (both) {
+          ok = wait(kBarPFull + 1, step1 & 1);
+          if (!ok) break;
+          issue_pv(1, v_slot, b == 0);
+          umma_commit_if(go, bar(kBarKvEmpty + v_slot));
+          if (more) {
+            ok = wait(kBarPvDone + 1, step1 & 1);
+            if (!ok) break;
+            issue_s(1, slot);
+            umma_commit_if(go, bar(kBarKvEmpty + slot));
+          }
+          ++step1;
+        }
+        if (more) advance();
+      }
+      if (!ok) break;
     }
+    if (lane == 0) consumed = used;
+    // All MMAs complete before TMEM is released.
+    umma_commit_if(go, bar(kBarDrain));
+    mbar_wait(bar(kBarDrain), 0, a.status);
   }
   } else if (E4M3 && warp >= kWarpConvert) {
-    if constexpr (E4M3) registers_dec<48>();
+    if constexpr (E4M3) registers_dec<40>();
     // ------------------------------------------------------------ e4m3 -> fp16
-    const int tid = threadIdx.x - 32 * kWarpConvert;
+    // Four warps take the key tiles and four the value tiles (four for both were
+    // what the rest waited for: 5500 cycles a step of 256 rows x 128 keys).
+    const int part = (warp - kWarpConvert) / 4, wc = (warp - kWarpConvert) % 4;
+    const int tid = 32 * wc + lane;
     // A thread takes 16-byte piece `piece` of rows r0, r0 + kStep, ...: their
     // places differ by constants (kStep is a multiple of the swizzle's 8 rows).
     constexpr int kPieces = D / 16, kStep = 128 / kPieces, kEach = 32 / kPieces;
@@ -590,20 +611,20 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
     const uint32_t raw_at = r0 * D + ((D == 128 ? piece ^ (r0 & 7) : piece ^ ((r0 >> 1) & 3)) << 4);
     const uint32_t tile_at0 = tile_piece<D, E4M3>(0, r0, 2 * piece + second);
     const uint32_t tile_at1 = tile_piece<D, E4M3>(0, r0, 2 * piece + 1 - second);
-    int raw = 0, slot = 0, tile = 0;
-    uint32_t raw_phase = 0, phase = 1;
+    int tile = 0;
     bool ok = true;
     Job w;
-    for (int n = 0; ok && take(n, w, false); ++n) {
+    for (int n = 0; ok && take(n, w); ++n) {
       const int p0 = w.q.kv - w.q.c + a.by_group(w.rho0);
       const int p1 = w.q.kv - w.q.c + a.by_group(min(w.rho0 + kItemRows, w.q.c * a.group) - 1);
       const int lo = window_start(a, p0);
       auto any = [&](int j) { return j <= p1 && (j >= lo || j < a.sinks); };
       for (int b = w.b; b < w.end; ++b, ++tile) {
         const int key0 = w.kb.at(b) << kTileShift;
-#pragma unroll 1
-        for (int kv = 0; kv < 2; ++kv) {
-          ok = __all_sync(0xFFFFFFFFu, mbar_wait(bar(kBarRawFull + raw), raw_phase, a.status));
+        {
+          const uint32_t count = 2 * static_cast<uint32_t>(tile) + part;     // tiles before this one
+          const int raw = count % C::kRaw, slot = count % C::kRing;
+          ok = __all_sync(0xFFFFFFFFu, mbar_wait(bar(kBarRawFull + raw), (count / C::kRaw) & 1, a.status));
           if (!ok) break;
           const uint8_t* ex = smem + C::kOffExp + raw * kTile;
           // The largest exponent among rows that some row sees (255 marks a NaN
@@ -619,14 +640,14 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
           if (top == 0) top = 127;
           uint32_t factor;
           {
-            const int r = kStep * (lane / kEach) + kEach * (warp - kWarpConvert) + lane % kEach;
+            const int r = kStep * (lane / kEach) + kEach * wc + lane % kEach;
             const int e = ex[r], down = top - e;
             factor = e == 255 ? 0x3C00u : down <= 14 ? (15u - down) << 10 : down <= 24 ? 1u << (24 - down) : 0u;
             factor = any(key0 + r) ? factor | factor << 16 : 0xFFFFFFFFu;      // marks a row that nobody sees
           }
-          ok = __all_sync(0xFFFFFFFFu, mbar_wait(bar(kBarKvEmpty + slot), phase, a.status));
+          ok = __all_sync(0xFFFFFFFFu, mbar_wait(bar(kBarKvEmpty + slot), ((count / C::kRing) & 1) ^ 1, a.status));
           if (!ok) break;
-          if (tid == 0) tile_exp[8 * kv + (tile & 7)] = top - 127;
+          if (tid == 0) tile_exp[8 * part + (tile & 7)] = top - 127;
           const uint32_t from = sRaw(raw) + raw_at;
           const uint32_t to0 = sKv(slot) + tile_at0, to1 = sKv(slot) + tile_at1;
 #pragma unroll
@@ -649,16 +670,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
             mbar_arrive(bar(kBarRawEmpty + raw));
             mbar_arrive(bar(kBarKvFull + slot));
           }
-          if (++raw == C::kRaw) {
-            raw = 0;
-            raw_phase ^= 1;
-          }
-          if (++slot == C::kRing) {
-            slot = 0;
-            phase ^= 1;
-          }
         }
-        if (!ok) break;
       }
     }
   } else {
@@ -671,18 +683,17 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
     const uint32_t lane_sel = static_cast<uint32_t>(row0) << 16;
     const uint32_t tS = tmem + x * 128 + lane_sel;
     const uint32_t tO = tmem + kTmemO + x * D + lane_sel;
-    uint32_t step = 0, turn = 0;             // steps of this tile, and those that both tiles took
+    uint32_t step = 0;
     int tile = 0;
     bool ok = true;
     Job w;
-    for (int n = 0; ok && take(n, w, false); ++n) {
+    for (int n = 0; ok && take(n, w); ++n) {
       const int rho0 = w.rho0 + x * kTile;   // first row of the tile
       const int R = w.q.c * a.group;
       if (rho0 >= R) {
         tile += w.end - w.b;
         continue;
       }
-      const bool both = R - w.rho0 > kTile;  // tile B has rows too
       const int first = w.q.kv - w.q.c;
       // ---- the warp's 16 query rows: lane l takes piece l % kPieces of rows l / kPieces, + kEach, ...
       float c0 = a.scale_log2;
@@ -737,11 +748,13 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
         float c = c0, ev = 0.f, unit = 1.f;
         if constexpr (E4M3) {
           // E(V) is known once the value tile is there (it stays until P V).
-          const uint32_t n = 2 * static_cast<uint32_t>(tile) + 1;
-          if (!mbar_wait(bar(kBarKvFull + n % C::kRing), (n / C::kRing) & 1, a.status)) {
+          const uint32_t nv = 2 * static_cast<uint32_t>(tile) + 1;
+          if (!mbar_wait(bar(kBarKvFull + nv % C::kRing), (nv / C::kRing) & 1, a.status)) {
             ok = false;
             break;
           }
+        }
+        if constexpr (E4M3) {
           const int ek = tile_exp[tile & 7], e = tile_exp[8 + (tile & 7)];
           // Not zero: a masked score of -inf stays -inf.
           c = fmaxf(c * __int_as_float((ek + 127) << 23), 1e-35f);
@@ -775,14 +788,6 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
         }
         const float off = m_new == -INFINITY ? 0.f : ev - m_new;
         const uint64_t c2 = f2(c, c), nm2 = f2(off, off);
-        // The exponents of the two tiles take turns (A of step j, B of step j, A of
-        // step j + 1, ...), so that one tile's fill the time of the other's MMAs.
-        if (both && (x == 1 || turn > 0)) {
-          if (!mbar_wait(bar(kBarTurn + 4 * (x ^ 1) + (warp & 3)), (x == 1 ? turn : turn - 1) & 1, a.status)) {
-            ok = false;
-            break;
-          }
-        }
         uint64_t acc[4] = {f2(0.f, 0.f), f2(0.f, 0.f), f2(0.f, 0.f), f2(0.f, 0.f)};
         uint32_t pk[32];
 #pragma unroll
@@ -795,10 +800,6 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
           acc[y & 3] = f2_add(acc[y & 3], f2(z0, z1));
           // The product's operand: weights in 16 bits (their sum stays in fp32).
           pk[y] = E4M3 ? pack_f16x2(z0, z1) : pack_bf16x2(z0, z1);
-        }
-        if (both) {
-          mbar_arrive(bar(kBarTurn + 4 * x + (warp & 3)));
-          ++turn;
         }
         const uint64_t s2 = f2_add(f2_add(acc[0], acc[1]), f2_add(acc[2], acc[3]));
         float s0, s1;
@@ -917,7 +918,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
     // so no TMA write lands in shared memory after the CTA has exited.
     constexpr int kDepth = E4M3 ? C::kRaw : C::kRing;
     constexpr int kFull = E4M3 ? kBarRawFull : kBarKvFull;
-    const int done = E4M3 ? max(0, issued - kDepth) : min(consumed[0], consumed[1]);
+    const int done = E4M3 ? max(0, issued - kDepth) : consumed;
     for (int j = done; j < issued; ++j)
       if (!mbar_wait(bar(kFull + j % kDepth), (j / kDepth) & 1, nullptr)) break;
   }
