@@ -23,7 +23,9 @@ int block_at(int p0, int p1, int window, int sinks, int shift, int i) {
 }
 int64_t begin(int64_t w, int64_t W, int64_t U) { return deal(U, W).begin(w); }
 int divide(int n, int d) { return fast_div(d)(n); }
-int64_t snapped(int64_t x, int64_t i0, int64_t i1, int64_t snap) { return snap_border(x, i0, i1, snap); }
+int64_t snapped(int64_t x, int64_t i0, int64_t i1, int64_t snap, int64_t cost) {
+  return snap_border(x, i0, i1, snap, cost);
+}
 int64_t owner(int64_t x, int64_t W, int64_t U) { return deal(U, W).owner(x); }
 }
 """
@@ -44,7 +46,7 @@ def plan(tmp_path_factory):
     h = C.CDLL(lib)
     for f in (h.begin, h.owner):
         f.restype, f.argtypes = C.c_int64, [C.c_int64] * 3
-    h.snapped.restype, h.snapped.argtypes = C.c_int64, [C.c_int64] * 4
+    h.snapped.restype, h.snapped.argtypes = C.c_int64, [C.c_int64] * 5
     return h
 
 
@@ -118,11 +120,13 @@ def test_division_by_the_group(plan):
 
 
 def test_snapped_borders(plan):
-    """Borders keep their order, move at most `snap` units and never leave their
-    item; a worker between two borders inside one item keeps at least a unit."""
+    """Borders keep their order, move at most `snap` units (or out of an item's
+    first `cost`) and never leave their item; a worker between two borders inside one
+    item keeps at least a unit, and every part of an item has tiles."""
     rng = random.Random(4)
-    for _ in range(400):
-        counts = [rng.randrange(1, 40) for _ in range(rng.randrange(1, 30))]
+    cost = 4
+    for _ in range(600):
+        counts = [rng.randrange(1, 40) + cost for _ in range(rng.randrange(1, 30))]
         ends = [0]
         for c in counts:
             ends.append(ends[-1] + c)
@@ -134,8 +138,9 @@ def test_snapped_borders(plan):
             x = plan.begin(w, W, U)
             if x < U:
                 i = max(j for j in range(len(counts)) if ends[j] <= x)
-                y = plan.snapped(x, ends[i], ends[i + 1], snap)
-                assert y in (x, ends[i], ends[i + 1]) and abs(y - x) <= snap
+                y = plan.snapped(x, ends[i], ends[i + 1], snap, cost)
+                assert y in (x, ends[i], ends[i + 1]) and abs(y - x) <= max(snap, cost)
+                assert y == ends[i] or y - ends[i] > cost
                 x = y
             borders.append(x)
         assert borders[0] == 0 and borders[-1] == U and borders == sorted(borders)

@@ -66,13 +66,15 @@ inline FastDiv fast_div(int d) {
   return FastDiv{static_cast<uint32_t>(m), s, d};
 }
 
-// A share's border inside an item of units i0 .. i1 - 1 moves to the item's
-// nearer end when that is at most `snap` units away: a split item costs a second
-// load of its rows, a record of each part and their sum.
-DSV_HD int64_t snap_border(int64_t x, int64_t i0, int64_t i1, int64_t snap) {
+// A share's border inside an item of units i0 .. i1 - 1, the first `cost` of
+// which stand for what an item takes besides its tiles.  It moves to the item's
+// nearer end when that is at most `snap` units away (a split item costs a second
+// load of its rows, a record of each part and their sum), and never lies within
+// the first `cost`.
+DSV_HD int64_t snap_border(int64_t x, int64_t i0, int64_t i1, int64_t snap, int64_t cost) {
   const int64_t a = x - i0, b = i1 - x;
-  if (a <= b) return a <= snap ? i0 : x;
-  return b <= snap ? i1 : x;
+  if (a > b) return b <= snap ? i1 : a <= cost ? i0 : x;
+  return a <= snap || a <= cost ? i0 : x;
 }
 
 }  // namespace dsvit

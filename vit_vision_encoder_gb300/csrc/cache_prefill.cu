@@ -92,14 +92,17 @@ struct PrefillArgs {
 // Where a CTA's share of the units begins, and how many it has; how far
 // borders move to an item's end.
 struct Start {
-  int s, k, head, b;
+  int s, k, head, off;        // off: units of the item before the share
   int64_t units, total, first;
   int snap;
 };
+// Shares are counted in key tiles, an item weighing kItemCost more than it has:
+// what its rows' way in and out takes (5 us; a tile takes 1.4).
+constexpr int kItemCost = 4;
 // A split costs what some six tiles do (the second load of the rows, records of
 // 128 KB a part, their sum), so borders move to an item's end within six; and
 // where even the longest item is short and not much over a share, no item is split.
-constexpr int kSnap = 6, kUnsplit = 16;
+constexpr int kSnap = 6, kUnsplit = 16 + kItemCost;
 
 __device__ __forceinline__ int items_of(const AttentionArgs& a, const Seq& q) {
   return (q.c * a.group + kItemRows - 1) / kItemRows;
@@ -137,24 +140,28 @@ struct Walk {
   int s, k, head, b, end;
   Seq q;
   KeyBlocks kb;
+  int take;                   // units of this item
   int64_t left;               // units left, this item's included
 
-  __device__ __forceinline__ void enter(const AttentionArgs& a, int b0) {
+  // Into the item at unit `off`, which is 0 or behind its first kItemCost.
+  __device__ __forceinline__ void enter(const AttentionArgs& a, int off) {
     kb = item_blocks(a, q, k);
-    b = b0;
-    end = left < kb.count - b ? b + static_cast<int>(left) : kb.count;
+    const int rest = kb.count + kItemCost - off;
+    take = left < rest ? static_cast<int>(left) : rest;
+    b = off == 0 ? 0 : off - kItemCost;
+    end = off + take - kItemCost;
   }
   __device__ __forceinline__ void start(const AttentionArgs& a, const Start& st) {
     s = st.s, k = st.k, head = st.head;
     left = st.units;
     q = left > 0 ? load_seq(a.b, a.c.page_shift, s, nullptr) : Seq{0, 0, 0};
     if (left <= 0) return;
-    enter(a, st.b);
+    enter(a, st.off);
     if (b >= kb.count) step(a);             // the border moved to this item's end
   }
   // To the next item; left must be positive afterwards for it to exist.
   __device__ __forceinline__ void next(const AttentionArgs& a) {
-    left -= end - b;
+    left -= take;
     if (left > 0) step(a);
   }
   __device__ __noinline__ void step(const AttentionArgs& a) {
@@ -240,8 +247,8 @@ __device__ __forceinline__ Start make_plan(const AttentionArgs& a, uint8_t* scra
   if (i0 < i1) {
     int most = 0;
     walk([&](int, int, int count) {
-      mine += static_cast<int64_t>(count) * a.c.kv_heads;
-      most = max(most, count);
+      mine += static_cast<int64_t>(count + kItemCost) * a.c.kv_heads;
+      most = max(most, count + kItemCost);
     });
     atomicMax(&longest, most);
   }
@@ -261,20 +268,22 @@ __device__ __forceinline__ Start make_plan(const AttentionArgs& a, uint8_t* scra
   __syncthreads();
   if (mine > 0 && ((x0 >= at && x0 < at + mine) || (x1 >= at && x1 < at + mine)))
     walk([&](int s, int k, int count) {
-      const int64_t here = static_cast<int64_t>(count) * a.c.kv_heads;
+      const int weight = count + kItemCost;
+      const int64_t here = static_cast<int64_t>(weight) * a.c.kv_heads;
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int64_t x = e == 0 ? x0 : x1;
         if (x < at || x >= at + here) continue;
-        const int head = static_cast<int>(x - at < INT32_MAX ? static_cast<uint32_t>(x - at) / static_cast<uint32_t>(count)
-                                                             : (x - at) / count);
-        const int64_t i0 = at + static_cast<int64_t>(head) * count, y = snap_border(x, i0, i0 + count, snap);
+        const int head = static_cast<int>(x - at < INT32_MAX ? static_cast<uint32_t>(x - at) / static_cast<uint32_t>(weight)
+                                                             : (x - at) / weight);
+        const int64_t i0 = at + static_cast<int64_t>(head) * weight;
+        const int64_t y = snap_border(x, i0, i0 + weight, snap, kItemCost);
         border[e] = y;
         if (e == 0) {
           found->s = s;
           found->k = k;
           found->head = head;
-          found->b = static_cast<int>(y - i0);
+          found->off = static_cast<int>(y - i0);
         }
       }
       at += here;
@@ -490,9 +499,9 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
         if (!more) break;
         if (!whole && w.b == 0) {
           const Shares shares = deal(st.total, st.total < gridDim.x ? st.total : gridDim.x);
-          const int64_t i0 = st.first + st.units - w.left, i1 = i0 + w.kb.count;
+          const int64_t i0 = st.first + st.units - w.left, i1 = i0 + w.kb.count + kItemCost;
           int64_t last = shares.owner(i1 - 1);       // the last worker whose border is not at or behind the end
-          while (last > blockIdx.x && snap_border(shares.begin(last), i0, i1, st.snap) >= i1) --last;
+          while (last > blockIdx.x && snap_border(shares.begin(last), i0, i1, st.snap, kItemCost) >= i1) --last;
           header = SplitHeader{static_cast<int>(last - blockIdx.x) + 1, w.s, w.head, w.k * kItemRows, w.q, 0};
         }
         w.next(a);
