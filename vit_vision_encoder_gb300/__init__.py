@@ -537,10 +537,11 @@ def overlay_chunk(chunk, chunk_begin, spans, embeds, sentinel, row_type=None):
 
 def _cache_names():
     """torch, with the names that the cache calls use on every call."""
-    global _bf16, _u8, _i32_type, _cuda_device, _raw_stream
+    global _bf16, _u8, _i32_type, _cuda_device, _raw_stream, _capturing
     torch = _torch()
     _bf16, _u8, _i32_type = torch.bfloat16, torch.uint8, torch.int32
     _cuda_device = torch.cuda.current_device
+    _capturing = torch.cuda.is_current_stream_capturing
     # The stream's handle without a Stream object (0.2 us a call against 8).
     _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
                           lambda d: torch.cuda.current_stream(d).cuda_stream)
@@ -565,6 +566,7 @@ class KvCache:
         self.k, self.v, self.k_exp, self.v_exp = k, v, k_exp, v_exp
         self.kv_heads, self.head_dim, self.device = k.shape[1], k.shape[3], k.device
         self.device_index = k.get_device()
+        self._ws = {}                       # workspaces of cache_attention, one for each stream that called
         self.c = Cache(k.data_ptr(), v.data_ptr(), k_exp.data_ptr() if e4m3 else None,
                        v_exp.data_ptr() if e4m3 else None, *k.shape, CACHE_E4M3 if e4m3 else CACHE_BF16)
         self.ref = C.byref(self.c)
@@ -667,11 +669,24 @@ def cache_attention_workspace_bytes(cache, chunks, heads):
     return nb
 
 
+def _workspace(cache, chunks, heads, stream):
+    """A workspace that nothing else uses while the call's kernels run: the cache's
+    own for this stream, whose calls follow one another; a graph under capture
+    gets one of its own."""
+    need = cache_attention_workspace_bytes(cache, chunks, heads)
+    if _capturing():
+        return _torch().empty(need, dtype=_u8, device=cache.device)
+    ws = cache._ws.get(stream)
+    if ws is None or ws.numel() < need:
+        ws = cache._ws[stream] = _torch().empty(need, dtype=_u8, device=cache.device)
+    return ws
+
+
 def cache_attention(cache, chunks, q, scale=None, window=0, sinks=0, out=None, ws=None, status=None):
     """Attention of the packed rows q (bf16 [rows, heads, head_dim], rows may be
     strided) over the cache (ds_vit_cache_attention); scale defaults to
-    head_dim ** -0.5.  ``ws``: uint8 workspace (allocated here when not given;
-    calls that may overlap need one each).  Returns (out, status)."""
+    head_dim ** -0.5.  ``ws``: uint8 workspace (calls that may overlap need one
+    each; when not given, the cache keeps one per stream).  Returns (out, status)."""
     d, stream, status = _on_device(cache, chunks, status, "ds_vit_cache_attention")
     if q.dim() != 3:
         _refuse("ds_vit_cache_attention")
@@ -683,15 +698,12 @@ def cache_attention(cache, chunks, q, scale=None, window=0, sinks=0, out=None, w
     if out.shape[0] != rows:
         _refuse("ds_vit_cache_attention")
     if ws is None:
-        ws = _torch().empty(cache_attention_workspace_bytes(cache, chunks, heads), dtype=_u8, device=cache.device)
-        ws_bytes = ws.numel()
-    else:
-        if ws.dtype is not _u8 or ws.get_device() != d or not ws.is_contiguous():
-            _refuse("ds_vit_cache_attention")
-        ws_bytes = ws.numel()
+        ws = _workspace(cache, chunks, heads, stream)
+    elif ws.dtype is not _u8 or ws.get_device() != d or not ws.is_contiguous():
+        _refuse("ds_vit_cache_attention")
     check(lib.ds_vit_cache_attention(cache.ref, chunks.ref, q.data_ptr(), qs, rows, heads,
                                      dim ** -0.5 if scale is None else scale, window, sinks, out.data_ptr(), os_,
-                                     ws.data_ptr(), ws_bytes, status.data_ptr(), stream), "ds_vit_cache_attention")
+                                     ws.data_ptr(), ws.numel(), status.data_ptr(), stream), "ds_vit_cache_attention")
     return out, status
 
 
