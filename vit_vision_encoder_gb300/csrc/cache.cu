@@ -12,7 +12,7 @@ namespace dsvit {
 namespace {
 
 constexpr int kWarps = 4;     // tokens per block
-constexpr int kPieces = 4;    // 16-byte pieces in flight per lane
+constexpr int kPieces = 4;    // 16-byte pieces of the keys, and as many of the values, in flight per lane
 
 // Quantisation of one row (a token's key or value of one head) to e4m3 with
 // a power-of-two factor: a = max |x|, e the least integer with a <= 448 2^e
@@ -38,11 +38,10 @@ __device__ __forceinline__ uint32_t max_abs_bits(uint4 u) {
   return max(m & 0xFFFFu, m >> 16);
 }
 
-// Two bf16 values times f as e4m3, magnitudes at most `top`.
-__device__ __forceinline__ uint32_t e4m3x2(uint32_t two, float f, float top) {
-  const float lo = fminf(fmaxf(bf16lo(two) * f, -top), top), hi = fminf(fmaxf(bf16hi(two) * f, -top), top);
+// Two bf16 values times f as e4m3.
+__device__ __forceinline__ uint32_t e4m3x2(uint32_t two, float f) {
   uint16_t r;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(bf16hi(two) * f), "f"(bf16lo(two) * f));
   return r;
 }
 
@@ -57,22 +56,33 @@ __device__ __forceinline__ bool has_row(const Seq& q, int r) {
   return static_cast<unsigned>(r - q.row0) < static_cast<unsigned>(q.c);
 }
 
-// Lanes of D / 8 hold one row; piece i of a token is row i / (D / 8).
+// kLanes lanes hold one row (a head's key or value) in 16-byte pieces, a warp
+// kHeads heads at a time; a lane keeps its piece of the row throughout.
 template <int D, bool E4M3>
 __global__ void __launch_bounds__(32 * kWarps)
     cache_write_kernel(const __grid_constant__ CacheView c, const __grid_constant__ ChunkView b,
                        const bf16* __restrict__ k, int64_t k_stride, const bf16* __restrict__ v,
                        int64_t v_stride, int* status) {
-  constexpr int kLanes = D / 8;
+  constexpr int kLanes = D / 8, kHeads = 32 / kLanes;
   grid_dep_launch();
   grid_dep_wait();
   const int lane = threadIdx.x & 31;
   const int r = static_cast<int>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
   check_seqs(b, c.page_shift, status);
   if (r >= b.rows) return;
-  const int per = c.kv_heads * kLanes;          // pieces of the keys; as many of the values follow
-  const uint4* kr = reinterpret_cast<const uint4*>(k + r * k_stride);
-  const uint4* vr = reinterpret_cast<const uint4*>(v + r * v_stride);
+  const int piece = lane % kLanes, h0 = lane / kLanes;
+  const uint4* from[2] = {reinterpret_cast<const uint4*>(k + r * k_stride) + lane,
+                          reinterpret_cast<const uint4*>(v + r * v_stride) + lane};
+  // The token's first pieces are on their way while its place is looked up.
+  uint4 u[2][kPieces];
+  auto load = [&](int hb) {
+#pragma unroll
+    for (int x = 0; x < 2; ++x)
+#pragma unroll
+      for (int t = 0; t < kPieces; ++t)
+        u[x][t] = hb + h0 + t * kHeads < c.kv_heads ? __ldg(from[x] + hb * kLanes + 32 * t) : make_uint4(0, 0, 0, 0);
+  };
+  load(0);
   const int s = find_seq(b, r, lane);
   if (s < 0) return;
   const Seq q = load_seq(b, c.page_shift, s, status);
@@ -80,38 +90,41 @@ __global__ void __launch_bounds__(32 * kWarps)
   if (!has_row(q, r) || pos < 0) return;        // refused sequence, or padding in front of position 0
   const int64_t page = page_of(b, c, s, pos, status);
   if (page < 0) return;
-  for (int i0 = 0; i0 < 2 * per; i0 += 32 * kPieces) {
-    uint4 u[kPieces];
+  const int64_t row0 = cache_row(c, page, h0, pos);
+  for (int hb = 0; hb < c.kv_heads; hb += kHeads * kPieces) {
+    if (hb > 0) load(hb);
 #pragma unroll
-    for (int t = 0; t < kPieces; ++t) {
-      const int i = i0 + 32 * t + lane;
-      if (i < 2 * per) u[t] = i < per ? __ldg(kr + i) : __ldg(vr + (i - per));
-    }
+    for (int x = 0; x < 2; ++x) {
+      uint8_t* to = x == 0 ? c.k : c.v;
 #pragma unroll
-    for (int t = 0; t < kPieces; ++t) {
-      const int i = i0 + 32 * t + lane;
-      const bool is_v = i >= per;
-      const int p = is_v ? i - per : i;
-      const int64_t row = cache_row(c, page, p / kLanes, pos);
-      uint8_t* to = is_v ? c.v : c.k;
-      if constexpr (!E4M3) {
-        if (i < 2 * per) reinterpret_cast<uint4*>(to)[row * kLanes + p % kLanes] = u[t];
-      } else {
-        // A row's lanes are in or out of range together (2 per is a multiple of kLanes).
-        uint32_t a = i < 2 * per ? max_abs_bits(u[t]) : 0u;
+      for (int t = 0; t < kPieces; ++t) {
+        const int h = hb + t * kHeads;                             // head of the warp's first lanes
+        const int64_t row = row0 + (static_cast<int64_t>(h) << c.page_shift);
+        const bool on = h + h0 < c.kv_heads;
+        const uint4 w = u[x][t];
+        if constexpr (!E4M3) {
+          if (on) reinterpret_cast<uint4*>(to)[row * kLanes + piece] = w;
+        } else {
+          if (h >= c.kv_heads) break;
+          uint32_t a = max_abs_bits(w);
 #pragma unroll
-        for (int o = kLanes / 2; o > 0; o >>= 1) a = max(a, __shfl_xor_sync(0xFFFFFFFFu, a, o));
-        if (i >= 2 * per) continue;
-        const uint32_t byte = exponent_byte(a);
-        uint2 w = make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu);
-        if (byte != 255u) {
-          const float f = __uint_as_float((254u - byte) << 23);   // 2^-e
-          const float top = byte == 247u ? 240.f : 448.f;
-          w.x = e4m3x2(u[t].x, f, top) | e4m3x2(u[t].y, f, top) << 16;
-          w.y = e4m3x2(u[t].z, f, top) | e4m3x2(u[t].w, f, top) << 16;
+          for (int o = kLanes / 2; o > 0; o >>= 1) a = max(a, __shfl_xor_sync(0xFFFFFFFFu, a, o));
+          const uint32_t byte = exponent_byte(a);
+          const float f = __uint_as_float((254u - byte) << 23);    // 2^-e
+          uint2 y = make_uint2(e4m3x2(w.x, f) | e4m3x2(w.y, f) << 16, e4m3x2(w.z, f) | e4m3x2(w.w, f) << 16);
+          if (byte >= 247u) {
+            if (byte == 255u) {
+              y = make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu);
+            } else {                                               // magnitudes 256 (0x78) end at 240 (0x77)
+              y.x -= __vcmpgtu4(y.x & 0x7F7F7F7Fu, 0x77777777u) & 0x01010101u;
+              y.y -= __vcmpgtu4(y.y & 0x7F7F7F7Fu, 0x77777777u) & 0x01010101u;
+            }
+          }
+          if (on) {
+            reinterpret_cast<uint2*>(to)[row * kLanes + piece] = y;
+            if (piece == 0) (x == 0 ? c.k_exp : c.v_exp)[row] = static_cast<uint8_t>(byte);
+          }
         }
-        reinterpret_cast<uint2*>(to)[row * kLanes + p % kLanes] = w;
-        if (p % kLanes == 0) (is_v ? c.v_exp : c.k_exp)[row] = static_cast<uint8_t>(byte);
       }
     }
   }
@@ -128,16 +141,14 @@ template <int D, bool E4M3>
 __global__ void __launch_bounds__(32 * kWarps)
     cache_read_kernel(const __grid_constant__ CacheView c, const __grid_constant__ ChunkView b,
                       bf16* __restrict__ k, int64_t k_stride, bf16* __restrict__ v, int64_t v_stride, int* status) {
-  constexpr int kLanes = D / 8;
+  constexpr int kLanes = D / 8, kHeads = 32 / kLanes;
   grid_dep_launch();
   grid_dep_wait();
   const int lane = threadIdx.x & 31;
   const int r = static_cast<int>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
   check_seqs(b, c.page_shift, status);
   if (r >= b.rows) return;
-  const int per = c.kv_heads * kLanes;
-  uint4* kr = reinterpret_cast<uint4*>(k + r * k_stride);
-  uint4* vr = reinterpret_cast<uint4*>(v + r * v_stride);
+  const int piece = lane % kLanes, h0 = lane / kLanes;
   const int s = find_seq(b, r, lane);
   if (s < 0) return;
   const Seq q = load_seq(b, c.page_shift, s, status);
@@ -145,43 +156,45 @@ __global__ void __launch_bounds__(32 * kWarps)
   const int pos = q.kv - q.c + (r - q.row0);
   const int64_t page = pos < 0 ? -1 : page_of(b, c, s, pos, status);
   if (page < 0 && pos >= 0) return;
-  for (int i0 = 0; i0 < 2 * per; i0 += 32 * kPieces) {
-    uint4 u[kPieces];
-    uint32_t byte[kPieces];
+  const int64_t row0 = page < 0 ? 0 : cache_row(c, page, h0, pos);
+  for (int hb = 0; hb < c.kv_heads; hb += kHeads * kPieces) {
+    uint4 u[2][kPieces];
+    uint32_t byte[2][kPieces];
 #pragma unroll
-    for (int t = 0; t < kPieces; ++t) {
-      const int i = i0 + 32 * t + lane;
-      const bool is_v = i >= per;
-      const int p = is_v ? i - per : i;
-      u[t] = make_uint4(0, 0, 0, 0);
-      byte[t] = 127;
-      if (i < 2 * per && page >= 0) {
-        const int64_t row = cache_row(c, page, p / kLanes, pos);
-        const uint8_t* from = is_v ? c.v : c.k;
-        if constexpr (!E4M3) {
-          u[t] = reinterpret_cast<const uint4*>(from)[row * kLanes + p % kLanes];
-        } else {
-          const uint2 w = reinterpret_cast<const uint2*>(from)[row * kLanes + p % kLanes];
-          u[t].x = w.x;
-          u[t].y = w.y;
-          byte[t] = (is_v ? c.v_exp : c.k_exp)[row];
+    for (int x = 0; x < 2; ++x) {
+      const uint8_t* from = x == 0 ? c.k : c.v;
+#pragma unroll
+      for (int t = 0; t < kPieces; ++t) {
+        const int h = hb + t * kHeads;
+        const int64_t row = row0 + (static_cast<int64_t>(h) << c.page_shift);
+        u[x][t] = make_uint4(0, 0, 0, 0);
+        byte[x][t] = 127;
+        if (h + h0 < c.kv_heads && page >= 0) {
+          if constexpr (!E4M3) {
+            u[x][t] = reinterpret_cast<const uint4*>(from)[row * kLanes + piece];
+          } else {
+            const uint2 w = reinterpret_cast<const uint2*>(from)[row * kLanes + piece];
+            u[x][t].x = w.x;
+            u[x][t].y = w.y;
+            byte[x][t] = (x == 0 ? c.k_exp : c.v_exp)[row];
+          }
         }
       }
     }
 #pragma unroll
-    for (int t = 0; t < kPieces; ++t) {
-      const int i = i0 + 32 * t + lane;
-      if (i >= 2 * per) continue;
-      uint4 w = u[t];
-      if constexpr (E4M3) {
-        const float f = exp_factor(byte[t]);
-        w = make_uint4(e4m3x2_to_bf16x2(u[t].x & 0xFFFFu, f), e4m3x2_to_bf16x2(u[t].x >> 16, f),
-                       e4m3x2_to_bf16x2(u[t].y & 0xFFFFu, f), e4m3x2_to_bf16x2(u[t].y >> 16, f));
+    for (int x = 0; x < 2; ++x) {
+      uint4* to = reinterpret_cast<uint4*>(x == 0 ? k + r * k_stride : v + r * v_stride) + hb * kLanes + lane;
+#pragma unroll
+      for (int t = 0; t < kPieces; ++t) {
+        if (hb + t * kHeads + h0 >= c.kv_heads) continue;
+        uint4 w = u[x][t];
+        if constexpr (E4M3) {
+          const float f = exp_factor(byte[x][t]);
+          w = make_uint4(e4m3x2_to_bf16x2(w.x & 0xFFFFu, f), e4m3x2_to_bf16x2(w.x >> 16, f),
+                         e4m3x2_to_bf16x2(w.y & 0xFFFFu, f), e4m3x2_to_bf16x2(w.y >> 16, f));
+        }
+        to[32 * t] = w;
       }
-      if (i < per)
-        kr[i] = w;
-      else
-        vr[i - per] = w;
     }
   }
 }
