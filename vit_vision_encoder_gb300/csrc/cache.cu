@@ -234,12 +234,12 @@ bool bad_rows(const void* p, int64_t stride, int64_t width) {
 // Rows that share a K/V head in one sequence: few of them leave the call bound
 // by the cache's bytes, and the kernel that streams those through warp MMAs is
 // taken; with more rows the tcgen05 one.
-bool few_rows(const ChunkView& b, int group, bool e4m3) {
-  return static_cast<int64_t>(b.max_rows) * group <= decode_rows(e4m3);
+bool few_rows(const ChunkView& b, int head_dim, int group, bool e4m3) {
+  return static_cast<int64_t>(b.max_rows) * group <= decode_rows(head_dim, e4m3);
 }
 
 size_t attention_workspace(const ChunkView& b, int head_dim, int group, bool e4m3) {
-  return few_rows(b, group, e4m3) ? cache_decode_workspace(head_dim, b.max_rows * group)
+  return few_rows(b, head_dim, group, e4m3) ? cache_decode_workspace(head_dim, b.max_rows * group)
                                   : cache_prefill_workspace(head_dim);
 }
 
@@ -329,7 +329,7 @@ int ds_vit_cache_attention(const ds_vit_cache* cache, const ds_vit_chunks* chunk
   a.sinks = sinks;
   a.scale_log2 = 1.4426950408889634f * scale;
   a.status = reinterpret_cast<int*>(status);
-  auto* launch = few_rows(a.b, a.group, e4m3) ? launch_cache_decode : launch_cache_prefill;
+  auto* launch = few_rows(a.b, cache->head_dim, a.group, e4m3) ? launch_cache_decode : launch_cache_prefill;
   return launch(a, cache->head_dim, e4m3, ws, static_cast<cudaStream_t>(stream));
 }
 

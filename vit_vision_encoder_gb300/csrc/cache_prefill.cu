@@ -24,7 +24,12 @@
 // the Q tile on the way out): as accesses of a thread to its own row, they took
 // 6000 cycles in and 10000 out an item.
 //
-// e4m3 pages: warps 20-23 widen the raw tiles to fp16 in shared memory (the
+// An item of at most 128 rows leaves tile B without rows of its own: it then
+// takes the same rows and every other key tile, and the two results are added up
+// in TMEM (32 sequences of 8000 tokens, 32 rows, bf16, D 64: 130 us without, 104
+// with).
+//
+// e4m3 pages: warps 20-27 widen the raw tiles to fp16 in shared memory (the
 // conversion is exact; the rows of a tile are scaled by powers of two to the
 // tile's largest exponent E, and elements 2^-24 below it lose bits).  Scores are
 // scaled by 2^E(K); the weights are taken against the running maximum of score
@@ -36,6 +41,8 @@
 // rows of an item see different keys and a result is not finite, the row is
 // computed again from the keys that it does see (exact_row).
 #include "cache_rows.cuh"
+
+#include <type_traits>
 
 namespace dsvit {
 
@@ -55,14 +62,16 @@ struct Cfg {
   static constexpr int kBytes = kTile * D * 2;             // a 16-bit tile of 128 rows
   static constexpr int kHalf = kTile * 128;                // 64 dims of it
   static constexpr int kRawBytes = kTile * D;              // an e4m3 tile
-  static constexpr int kRing = E4M3 ? 3 : (D == 128 ? 5 : 8);
-  static constexpr int kRaw = E4M3 ? 3 : 0;
+  static constexpr int kRing = E4M3 ? (D == 128 ? 3 : 6) : (D == 128 ? 5 : 8);
+  static constexpr int kRaw = E4M3 ? (D == 128 ? 3 : 4) : 0;
+  // Tile B takes part in items without rows for it (with a ring of three tiles it would wait for A's).
+  static constexpr bool kShare = kRing > 3;
   static constexpr int kOffKv = 2 * kBytes;                // after Q_A, Q_B
   static constexpr int kOffRaw = kOffKv + kRing * kBytes;
   static constexpr int kOffExp = kOffRaw + kRaw * kRawBytes;   // exponents of the raw tiles
   static constexpr int kOffBar = kOffExp + kRaw * kTile;
   static constexpr int kSmem = kOffBar + 1024 + 1024;
-  static_assert(kSmem <= 232448, "shared memory");
+  static_assert(kSmem + 512 <= 232448, "shared memory, the static part included");
   static constexpr float kLag = E4M3 ? 14.f : 8.f;         // see Reference in the kernel for few rows
   static constexpr float kLead = E4M3 ? 6.f : 0.f;
 };
@@ -81,7 +90,9 @@ enum : int {
   kBarDrain = 33,
   kBarJobFull = 34,         // [4]
   kBarJobEmpty = 38,        // [4]
-  kBarCount = 42
+  kBarOther = 42,           // tile B's share of the keys is summed up
+  kBarMerged = 43,          // and has been read
+  kBarCount = 44
 };
 
 struct PrefillArgs {
@@ -370,6 +381,8 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
     }
     mbar_init(bar(kBarRagged), 1);
     mbar_init(bar(kBarDrain), 1);
+    mbar_init(bar(kBarOther), 256);
+    mbar_init(bar(kBarMerged), 256);
     fence_barrier_init();
   }
   if (warp == kWarpTma) {
@@ -401,6 +414,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
     if (lane == 0) mbar_arrive(bar(kBarJobEmpty + i));
     return ok && j.b < j.end;
   };
+  float2* other = reinterpret_cast<float2*>(smem + C::kBytes);   // tile B's maxima and sums, in place of its query rows
   int issued = 0;                           // ring or raw tiles whose loads were issued
 
   // e4m3: 28 warps start with 72 registers each; 16 x 96 + 12 x 40 is the same sum.
@@ -552,52 +566,84 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
         umma_bf16_ts_if(go, tm + kTmemO + x * D, tm + x * 128 + k * 8, dv + 128 * k, id_o, !fresh | (k != 0));   // 16 rows = 2048 B
       umma_commit_if(go, bar(kBarPvDone + x));
     };
+    // Place of a tile `ahead` of the next in the ring, and whether it has been filled.
+    auto place = [&](int ahead) { return slot + ahead < C::kRing ? slot + ahead : slot + ahead - C::kRing; };
+    auto there = [&](int ahead) {
+      return wait(kBarKvFull + place(ahead), slot + ahead < C::kRing ? phase : phase ^ 1);
+    };
+    auto release = [&](int at) { umma_commit_if(go, bar(kBarKvEmpty + at)); };
     Job w;
     for (int n = 0; __all_sync(0xFFFFFFFFu, take(n, w)); ++n) {
       const bool both = __shfl_sync(0xFFFFFFFFu, w.q.c * a.group - w.rho0, 0) > kTile;
       const int count = __shfl_sync(0xFFFFFFFFu, w.end - w.b, 0);
-      if (!wait(kBarKvFull + slot, phase) || !wait(kBarQ, q0)) break;
-      q0 ^= 1;
-      issue_s(0, slot);
-      if (both) {
-        if (!wait(kBarQ + 1, q1)) break;
-        q1 ^= 1;
-        issue_s(1, slot);
-      }
-      umma_commit_if(go, bar(kBarKvEmpty + slot));
-      advance();
       bool ok = true;
-      for (int b = 0; b < count; ++b) {
-        const bool more = b + 1 < count;
-        const int v_slot = slot;
-        ok = wait(kBarKvFull + v_slot, phase);
+      if (both) {
+        if (!there(0) || !wait(kBarQ, q0)) break;
+        issue_s(0, slot);
+        if (!wait(kBarQ + 1, q1)) break;
+        issue_s(1, slot);
+        release(slot);
+        q0 ^= 1;
+        q1 ^= 1;
         advance();
-        ok = ok && wait(kBarPFull, step0 & 1);
-        if (!ok) break;
-        issue_pv(0, v_slot, b == 0);
-        if (!both) umma_commit_if(go, bar(kBarKvEmpty + v_slot));
-        if (more) {
-          // S_X overwrites P_X: its product must be complete.
-          ok = wait(kBarKvFull + slot, phase) && wait(kBarPvDone, step0 & 1);
+        for (int b = 0; b < count; ++b) {
+          const bool more = b + 1 < count;
+          const int v_slot = slot;
+          ok = there(0);
+          advance();
+          ok = ok && wait(kBarPFull, step0 & 1);
           if (!ok) break;
-          issue_s(0, slot);
-          if (!both) umma_commit_if(go, bar(kBarKvEmpty + slot));
-        }
-        ++step0;
-        if (both) {
+          issue_pv(0, v_slot, b == 0);
+          if (more) {
+            // S_X overwrites P_X: its product must be complete.
+            ok = there(0) && wait(kBarPvDone, step0 & 1);
+            if (!ok) break;
+            issue_s(0, slot);
+          }
+          ++step0;
           ok = wait(kBarPFull + 1, step1 & 1);
           if (!ok) break;
           issue_pv(1, v_slot, b == 0);
-          umma_commit_if(go, bar(kBarKvEmpty + v_slot));
+          release(v_slot);
           if (more) {
             ok = wait(kBarPvDone + 1, step1 & 1);
             if (!ok) break;
             issue_s(1, slot);
-            umma_commit_if(go, bar(kBarKvEmpty + slot));
+            release(slot);
+            advance();
           }
           ++step1;
         }
-        if (more) advance();
+      } else {
+        // Key tiles 0, 2, .. are tile A's, 1, 3, .. tile B's.  The ring holds K0 V0 K1
+        // V1 ...; `slot` stays at the values of the step.
+        if (!there(0) || !wait(kBarQ, q0)) break;
+        q0 ^= 1;
+        issue_s(0, slot);
+        release(slot);
+        advance();
+        if (C::kShare && count > 1) {
+          if (!there(1) || !wait(kBarQ + 1, q1)) break;
+          q1 ^= 1;
+          issue_s(1, place(1));
+          release(place(1));
+        }
+        constexpr int kTurns = C::kShare ? 2 : 1;
+        auto turn = [&](int x, uint32_t& step, int b) {
+          if (!there(0) || !wait(kBarPFull + x, step & 1)) return false;
+          issue_pv(x, slot, b < kTurns);
+          release(slot);
+          if (b + kTurns < count) {
+            if (!there(2 * kTurns - 1) || !wait(kBarPvDone + x, step & 1)) return false;
+            issue_s(x, place(2 * kTurns - 1));
+            release(place(2 * kTurns - 1));
+          }
+          ++step;
+          advance();
+          if (b + 1 < count) advance();
+          return true;
+        };
+        for (int b = 0; ok && b < count; ++b) ok = kTurns == 1 || (b & 1) == 0 ? turn(0, step0, b) : turn(1, step1, b);
       }
       if (!ok) break;
     }
@@ -692,15 +738,18 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
     const uint32_t lane_sel = static_cast<uint32_t>(row0) << 16;
     const uint32_t tS = tmem + x * 128 + lane_sel;
     const uint32_t tO = tmem + kTmemO + x * D + lane_sel;
-    uint32_t step = 0;
+    uint32_t step = 0, merges = 0;
     int tile = 0;
     bool ok = true;
     Job w;
     for (int n = 0; ok && take(n, w); ++n) {
-      const int rho0 = w.rho0 + x * kTile;   // first row of the tile
-      const int R = w.q.c * a.group;
-      if (rho0 >= R) {
-        tile += w.end - w.b;
+      const int R = w.q.c * a.group, count = w.end - w.b;
+      // Tile B without rows of its own takes A's rows and every other key tile.
+      const bool shared = C::kShare && R - w.rho0 <= kTile;
+      const int rho0 = shared ? w.rho0 : w.rho0 + x * kTile;   // first row of the tile
+      const int stride = shared ? 2 : 1, b0 = shared ? w.b + x : w.b;
+      if (rho0 >= R || b0 >= w.end) {
+        tile += count;
         continue;
       }
       const int first = w.q.kv - w.q.c;
@@ -746,8 +795,8 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
       const int lo = window_start(a, pos), lo_b = window_start(a, pb);
 
       float m = -INFINITY, l = 0.f;
-      for (int b = w.b; b < w.end; ++b, ++tile, ++step) {
-        const int key0 = w.kb.at(b) << kTileShift;
+      for (int b = b0; b < w.end; b += stride, ++step) {
+        const int key0 = w.kb.at(b) << kTileShift, nth = tile + (b - w.b);     // the CTA's tiles before this one
         const bool open = key0 + kTile - 1 <= pa && (key0 >= lo_b || key0 + kTile <= a.sinks);
         if (!mbar_wait(bar(kBarSFull + x), step & 1, a.status)) {
           ok = false;
@@ -757,14 +806,14 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
         float c = c0, ev = 0.f, unit = 1.f;
         if constexpr (E4M3) {
           // E(V) is known once the value tile is there (it stays until P V).
-          const uint32_t nv = 2 * static_cast<uint32_t>(tile) + 1;
+          const uint32_t nv = 2 * static_cast<uint32_t>(nth) + 1;
           if (!mbar_wait(bar(kBarKvFull + nv % C::kRing), (nv / C::kRing) & 1, a.status)) {
             ok = false;
             break;
           }
         }
         if constexpr (E4M3) {
-          const int ek = tile_exp[tile & 7], e = tile_exp[8 + (tile & 7)];
+          const int ek = tile_exp[nth & 7], e = tile_exp[8 + (nth & 7)];
           // Not zero: a masked score of -inf stays -inf.
           c = fmaxf(c * __int_as_float((ek + 127) << 23), 1e-35f);
           ev = static_cast<float>(e);
@@ -816,7 +865,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
         l = l * alpha + (s0 + s1) * unit;    // this half's share of the row sum
         tmem_st32_x2<32>(tS, pk);
         // O_X was last written by the product that S_X waited for: it is complete.
-        if (b != w.b && __any_sync(0xFFFFFFFFu, alpha != 1.f)) {
+        if (b != b0 && __any_sync(0xFFFFFFFFu, alpha != 1.f)) {
 #pragma unroll
           for (int y = 0; y < D / 64; ++y) {
             uint32_t o[32];
@@ -841,6 +890,55 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
       // through their place in the Q tile (its products are complete), 16 bytes a
       // piece, and leave as whole rows.
       l += __shfl_xor_sync(0xFFFFFFFFu, l, 16);
+      tile += count;
+      float fa = 1.f, fb = 0.f;              // what the tiles' outputs are weighed by
+      const bool two = shared && count > 1;
+      if (two) {
+        if (x == 1) {
+          if (h == 0) other[r] = make_float2(m, l);
+          tc_fence_before();
+          mbar_arrive(bar(kBarOther));
+          if (!mbar_wait(bar(kBarMerged), merges & 1, a.status)) {
+            ok = false;
+            break;
+          }
+          ++merges;
+          tc_fence_after();
+          continue;
+        }
+        if (!mbar_wait(bar(kBarOther), merges & 1, a.status)) {
+          ok = false;
+          break;
+        }
+        ++merges;
+        tc_fence_after();
+        const float2 ml = other[r];
+        const float mb = ml.x, top = fmaxf(m, mb);
+        fa = m == top ? 1.f : exp2f(m - top);
+        fb = mb == top ? 1.f : exp2f(mb - top);
+        l = l * fa + ml.y * fb;
+        m = top;
+      }
+      // Columns col .. of the row's output (kCols of each half of the dims).
+      auto load_o = [&](auto cols, int col, uint32_t* o) {
+        constexpr int kCols = decltype(cols)::value;
+        if constexpr (kCols == 32)
+          tmem_ld32_x2<D / 2>(tO + col, *reinterpret_cast<uint32_t(*)[32]>(o));
+        else
+          tmem_ld16_x2<D / 2>(tO + col, o);
+        tmem_wait_ld();
+        if (two) {
+#pragma unroll
+          for (int c1 = 0; c1 < kCols; c1 += 16) {
+            uint32_t o2[16];
+            tmem_ld16_x2<D / 2>(tO + D + col + c1, o2);
+            tmem_wait_ld();
+#pragma unroll
+            for (int z = 0; z < 16; ++z)
+              o[c1 + z] = __float_as_uint(fmaf(__uint_as_float(o[c1 + z]), fa, __uint_as_float(o2[z]) * fb));
+          }
+        }
+      };
       uint32_t redo = 0;
       if (w.whole == 1) {
         const float inv = pos < 0 ? 0.f : 1.f / l;
@@ -848,8 +946,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
 #pragma unroll 1
         for (int y = 0; y < D / 64; ++y) {
           uint32_t o[32];
-          tmem_ld32_x2<D / 2>(tO + 32 * y, o);
-          tmem_wait_ld();
+          load_o(std::integral_constant<int, 32>{}, 32 * y, o);
 #pragma unroll
           for (int z = 0; z < 16; ++z) {
             const float o0 = __uint_as_float(o[2 * z]) * inv, o1 = __uint_as_float(o[2 * z + 1]) * inv;
@@ -887,11 +984,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
 #pragma unroll 1
         for (int y = 0; y < D / 2; y += kCols) {
           uint32_t o[32];
-          if constexpr (kCols == 32)
-            tmem_ld32_x2<D / 2>(tO + y, o);
-          else
-            tmem_ld16_x2<D / 2>(tO + y, o);
-          tmem_wait_ld();
+          load_o(std::integral_constant<int, kCols>{}, y, o);
           __syncwarp();                      // the last pass has been read
 #pragma unroll
           for (int z = 0; z < kCols / 4; ++z)
@@ -909,6 +1002,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
         }
       }
       tc_fence_before();
+      if (two) mbar_arrive(bar(kBarMerged));
       __syncwarp();                          // the rows' places are free for the next item's
       while (redo) {
         const int y = __ffs(static_cast<int>(redo)) - 1;

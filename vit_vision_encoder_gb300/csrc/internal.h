@@ -204,10 +204,11 @@ struct AttentionArgs;
 size_t cache_prefill_workspace(int head_dim);
 int launch_cache_prefill(const AttentionArgs& a, int head_dim, bool e4m3, void* ws, cudaStream_t stream);
 // The path for few query rows per K/V head and sequence, 16 at a time: at most
-// decode_rows.  Measured on 32 sequences of 8000 tokens (head dim 128, us, this
-// path against the other): bf16 16 rows 172 / 188, 24 rows 320 / 190; e4m3 32
-// rows 198 / 258, 40 rows 289 / 259.  Head dim 64 crosses at the same places.
-inline int decode_rows(bool e4m3) { return e4m3 ? 32 : 16; }
+// decode_rows.  Measured on 32 sequences of 8000 tokens and 8 K/V heads, us, this
+// path against the other: 16 rows bf16 171 / 182 (head dim 64: 108 / 103), e4m3 112
+// / 208 (102 / 125); 24 to 32 rows bf16 319 / 183 (194 / 103), e4m3 197 / 210 (175
+// / 126); 40 rows e4m3 287 / 210.
+inline int decode_rows(int head_dim, bool e4m3) { return e4m3 && head_dim == 128 ? 32 : 16; }
 size_t cache_decode_workspace(int head_dim, int rows);
 int launch_cache_decode(const AttentionArgs& a, int head_dim, bool e4m3, void* ws, cudaStream_t stream);
 
