@@ -479,6 +479,134 @@ def test_attention_one_pass_over_splits_is_repeatable(dv):
     assert torch.equal(a, b)
 
 
+def sampled64(st, q, scale, rows, window=0, sinks=0):
+    """(reference, tolerance) [len(rows), heads, dim] of some packed rows, in 64
+    bits on the GPU; the tolerance of attention64."""
+    heads = q.shape[1]
+    g = heads // st.kv_heads
+    held = [torch.from_numpy(x).cuda() for x in st.held()]
+    refs, tols = [], []
+    for r in rows:
+        s = max(i for i in range(len(st.q)) if st.off[i] <= r)
+        p = st.kv[s] - st.q[s] + r - st.off[s]
+        j = torch.arange(p + 1)
+        if window:
+            j = j[(j > p - window) | (j < sinks)]
+        page, slot = st.table[s][j // st.page].long().cuda(), (j % st.page).cuda()
+        k, v = (x[page, :, slot].repeat_interleave(g, 1) for x in held)          # [keys, heads, dim]
+        x = q[r].double()
+        z = torch.einsum("jhd,hd->hj", k, x) * scale
+        w = torch.softmax(z, 1)
+        ref = torch.einsum("hj,jhd->hd", w, v)
+        big = torch.einsum("jhd,hd->hj", k.abs(), x.abs()).amax(1, keepdim=True) * scale
+        refs.append(ref)
+        tols.append(2.0 ** -8 * ref.abs() + torch.einsum("hj,jhd->hd", w, v.abs())
+                    * (2.0 ** -8 + 2.0 ** -12 + 2 * (st.dim + 2) * 2.0 ** -24 * big))
+    return torch.stack(refs).cpu().numpy(), torch.stack(tols).cpu().numpy()
+
+
+LARGE = [
+    # q, kv, heads, kv_heads, dim, page, kind, window, sinks
+    ([900, 1300, 5], [9000, 1300, 4100], 8, 2, 128, 64, "bf16", 0, 0),          # many items a CTA, some of them split
+    ([900, 1300, 5], [9000, 1300, 4100], 8, 2, 128, 64, "e4m3", 0, 0),
+    ([2100], [2100], 12, 4, 64, 16, "bf16", 0, 0),                               # whole items
+    ([1500, 700], [6000, 2000], 10, 2, 64, 128, "e4m3", 600, 3),
+    ([400] * 20, [400 + 37 * i for i in range(20)], 6, 2, 128, 32, "bf16", 300, 20),
+    ([3] * 150, [3 + 11 * i for i in range(150)], 21, 1, 64, 32, "e4m3", 0, 0),  # 63 rows an item, other key tiles to tile B
+    ([3] * 150, [3 + 11 * i for i in range(150)], 21, 1, 128, 32, "bf16", 0, 0),
+    ([30], [20011], 4, 1, 128, 64, "bf16", 0, 0),                                # few rows over many keys: split and shared
+    ([30], [20011], 4, 1, 64, 16, "e4m3", 0, 0),
+    ([30], [20011], 4, 1, 128, 16, "e4m3", 0, 0),
+    ([1] * 60, [7000 - 111 * i for i in range(60)], 16, 4, 128, 64, "e4m3", 0, 0),
+    ([1] * 60, [7000 - 111 * i for i in range(60)], 16, 4, 64, 32, "bf16", 2000, 4),
+    ([1], [60007], 8, 1, 128, 128, "e4m3", 0, 0),                                # one item over every worker
+    ([1], [60007], 16, 1, 64, 16, "bf16", 0, 0),
+]
+
+
+@pytest.mark.parametrize("q,kv,heads,kv_heads,dim,page,kind,window,sinks", LARGE)
+def test_attention_of_larger_calls(dv, q, kv, heads, kv_heads, dim, page, kind, window, sinks):
+    """Calls that give every worker several items or a part of one: sampled rows
+    against 64 bits, and the same bits again over a workspace of other contents."""
+    st = Setup(dv, q, kv, kv_heads, dim, page, kind, seed=sum(q) % 1000, fill=math.nan)
+    x = st.queries(heads, wide=3)
+    ws = torch.full((dv.cache_attention_workspace_bytes(st.cache, st.chunks, heads),), 255, dtype=torch.uint8,
+                    device="cuda")
+    got, status = dv.cache_attention(st.cache, st.chunks, x, window=window, sinks=sinks)
+    again, _ = dv.cache_attention(st.cache, st.chunks, x, window=window, sinks=sinks, ws=ws)
+    torch.cuda.synchronize()
+    assert int(status.item()) == dv.OK
+    assert torch.equal(got, again)
+    rng = np.random.default_rng(5)
+    rows = sorted({0, st.rows - 1, *rng.integers(0, st.rows, 40).tolist(),
+                   *(st.off[s + 1] - 1 for s in range(0, len(q), 13))})
+    ref, tol = sampled64(st, x, dim ** -0.5, rows, window, sinks)
+    err = np.abs(f64(got)[rows] - ref)
+    bad = ~(err <= tol)
+    assert not bad.any(), f"{bad.sum()} of {bad.size} outside, worst {np.nanmax(err / tol)} at {np.argwhere(bad)[:3].tolist()}"
+
+
+@pytest.mark.parametrize("rows,heads", [(1, 8), (40, 8)])
+def test_sequences_that_share_pages(dv, rows, heads):
+    """Two sequences over the same pages (a common prompt) with the same queries
+    give the same rows."""
+    st = Setup(dv, [rows, rows], [300, 300], 2, 128, 16, "e4m3", seed=15)
+    st.chunks.table[1] = st.chunks.table[0]
+    x = st.queries(heads)
+    x[rows:] = x[:rows]
+    got, status = dv.cache_attention(st.cache, st.chunks, x)
+    torch.cuda.synchronize()
+    assert int(status.item()) == dv.OK and torch.equal(got[:rows], got[rows:])
+
+
+@pytest.mark.parametrize("rows", [1, 60])
+def test_two_streams_at_once(dv, rows):
+    """Calls on two streams that overlap on the GPU, with the workspaces that the
+    cache keeps for each."""
+    st = Setup(dv, [rows] * 3, [4000, 2500, 900], 2, 128, 64, "bf16", seed=16)
+    x = st.queries(8)
+    want, _ = dv.cache_attention(st.cache, st.chunks, x)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    outs = [[torch.zeros_like(want) for _ in range(6)] for _ in streams]
+    status = [torch.zeros(1, dtype=torch.int32, device="cuda") for _ in streams]
+    torch.cuda.synchronize()
+    for i in range(6):
+        for s, stream in enumerate(streams):
+            with torch.cuda.stream(stream):
+                dv.cache_attention(st.cache, st.chunks, x, out=outs[s][i], status=status[s])
+    torch.cuda.synchronize()
+    for s in range(2):
+        assert int(status[s].item()) == dv.OK
+        for o in outs[s]:
+            assert torch.equal(o, want)
+
+
+@pytest.mark.parametrize("rows", [1, 20, 140])
+@pytest.mark.parametrize("q_exp,k_exp,v_exp", [(-60, 20, -70), (40, -60, 60), (0, 0, 100), (-100, 90, -100)])
+def test_e4m3_far_exponents(dv, rows, q_exp, k_exp, v_exp):
+    """Queries, keys and values many powers of two from one: the result scales with
+    them.  Not bit for bit: the running reference (score plus exponent, fp32) rounds
+    otherwise with other exponents, which scales the weights and their sum by one
+    common factor 2^d, |d| <= 128 2^-24, and so moves the weights' own rounding.  Both
+    results stay within attention64's tolerance of one and the same value, so
+    they differ by at most twice that."""
+    st = Setup(dv, [rows], [700], 1, 128, 16, "e4m3", seed=17)
+    x = st.queries(4)
+    scale = 128 ** -0.5
+    want, _ = dv.cache_attention(st.cache, st.chunks, x, scale=scale)
+    ke, ve = st.cache.k_exp.int() + k_exp, st.cache.v_exp.int() + v_exp
+    assert int(ke.min()) >= 10 and int(ke.max()) <= 247 and int(ve.min()) >= 10 and int(ve.max()) <= 247
+    far = dv.KvCache(st.cache.k, st.cache.v, ke.to(torch.uint8), ve.to(torch.uint8))
+    got, status = dv.cache_attention(far, st.chunks, (x.float() * 2.0 ** q_exp).bfloat16(),
+                                     scale=scale * 2.0 ** -(q_exp + k_exp))
+    torch.cuda.synchronize()
+    assert int(status.item()) == dv.OK
+    picks = sorted({0, rows // 2, rows - 1})
+    _, tol = sampled64(st, x, scale, picks)
+    assert (np.abs(f64(got)[picks] * 2.0 ** -v_exp - f64(want)[picks]) <= 2 * tol).all()
+
+
 # ------------------------------------------------------------------ entries refused on the device
 
 def _calls(dv, st, heads=4):
