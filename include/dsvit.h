@@ -452,7 +452,8 @@ typedef struct ds_vit_chunks {
  *           the other sequences are served.  Never cleared here.
  * DS_VIT_EINVAL for null or misaligned pointers (16 bytes; int32 arrays 4),
  * unsupported sizes, a stride below its row's width; DS_VIT_ERANGE for
- * n_pages * kv_heads * page, table_cols * page or 2 * rows past 2^31 - 1.
+ * n_pages * kv_heads * page or 2 * rows past 2^31 - 1, table_cols * page past
+ * 2^31 - 256.
  *
  * ds_vit_cache_write: rows of k and v (device bf16 [rows, kv_heads, head_dim])
  * into the pages.  Two rows with the same place leave either one's value.

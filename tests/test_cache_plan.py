@@ -22,6 +22,10 @@ int block_at(int p0, int p1, int window, int sinks, int shift, int i) {
   return key_blocks(p0, p1, window, sinks, shift).at(i);
 }
 int64_t begin(int64_t w, int64_t W, int64_t U) { return deal(U, W).begin(w); }
+int refused(int row0, int row1, int kv, int rows, int max_rows, int64_t places) {
+  return seq_refused(row0, row1, kv, rows, max_rows, places);
+}
+int there(int page, int64_t n) { return page_there(page, n); }
 int divide(int n, int d) { return fast_div(d)(n); }
 int64_t snapped(int64_t x, int64_t i0, int64_t i1, int64_t snap, int64_t cost) {
   return snap_border(x, i0, i1, snap, cost);
@@ -147,3 +151,25 @@ def test_snapped_borders(plan):
         for i in range(len(counts)):
             inside = [b for b in borders if ends[i] < b < ends[i + 1]]
             assert len(inside) == len(set(inside))
+
+
+def test_sequences_and_pages_refused(plan):
+    """The checks that the kernels make of entries on the device."""
+    top = 2 ** 31 - 1
+    ok = (10, 14, 100, 20, 4, 160)
+    assert plan.refused(*ok[:5], C.c_int64(ok[5])) == 0
+
+    def at(code, **kw):
+        f = dict(zip(("row0", "row1", "kv", "rows", "max_rows", "places"), ok))
+        f.update(kw)
+        assert plan.refused(f["row0"], f["row1"], f["kv"], f["rows"], f["max_rows"], C.c_int64(f["places"])) == code, kw
+
+    for kw in (dict(row0=-1), dict(row1=9), dict(row1=21), dict(row1=15), dict(row0=-top - 1), dict(row1=top),
+               dict(row0=top, row1=-top - 1), dict(row0=0, row1=5), dict(row0=9), dict(row0=-2, row1=-1)):
+        at(1, **kw)
+    for kw in (dict(kv=-1), dict(kv=161), dict(kv=top), dict(kv=-top - 1)):
+        at(2, **kw)
+    for kw in (dict(kv=0), dict(kv=160), dict(row1=10), dict(row0=14), dict(kv=top, places=2 ** 40), dict(row0=0, row1=0)):
+        at(0, **kw)
+    for page, n, want in ((0, 1, 1), (1, 1, 0), (-1, 5, 0), (4, 5, 1), (5, 5, 0), (top, 2 ** 33, 1), (-top - 1, 2 ** 33, 0)):
+        assert plan.there(page, C.c_int64(n)) == want

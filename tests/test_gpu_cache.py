@@ -664,6 +664,20 @@ def test_more_rows_than_max_rows_refused(dv):
     assert (np.abs(f64(got)[4:] - ref[4:]) <= tol[4:]).all()
 
 
+def test_no_rows_and_sequences_without_rows(dv):
+    st = Setup(dv, [0, 0], [40, 0], 2, 64, 16, "bf16", seed=18)
+    x = st.queries(4)
+    assert x.shape[0] == 0
+    dv.cache_write(st.cache, st.chunks, st.queries(2), st.queries(2))
+    dv.cache_read(st.cache, st.chunks, 0)
+    out, status = dv.cache_attention(st.cache, st.chunks, x)
+    st = Setup(dv, [0, 0, 0], [40, 0, 7], 2, 64, 16, "bf16", seed=18, front=2, back=3)
+    for heads in (4, 64):
+        check_attention(dv, st, heads)
+    torch.cuda.synchronize()
+    assert out.shape == (0, 4, 64) and int(status.item()) == dv.OK
+
+
 def test_binding_refuses_other_tensors(dv):
     """Types, shapes, strides and devices that the binding refuses before the call."""
     st = Setup(dv, [2, 3], [40, 30], 2, 64, 16, "bf16", seed=13)

@@ -566,7 +566,6 @@ class KvCache:
         self.k, self.v, self.k_exp, self.v_exp = k, v, k_exp, v_exp
         self.kv_heads, self.head_dim, self.device = k.shape[1], k.shape[3], k.device
         self.device_index = k.get_device()
-        self._ws = {}                       # workspaces of cache_attention, one for each stream that called
         self.c = Cache(k.data_ptr(), v.data_ptr(), k_exp.data_ptr() if e4m3 else None,
                        v_exp.data_ptr() if e4m3 else None, *k.shape, CACHE_E4M3 if e4m3 else CACHE_BF16)
         self.ref = C.byref(self.c)
@@ -636,6 +635,8 @@ def cache_write(cache, chunks, k, v, status=None):
     rows = k.shape[0]
     if v.shape[0] != rows:
         _refuse("ds_vit_cache_write")
+    if rows == 0:                           # an empty tensor has no address
+        return status
     check(lib.ds_vit_cache_write(cache.ref, chunks.ref, k.data_ptr(), ks, v.data_ptr(), vs, rows, status.data_ptr(),
                                  stream), "ds_vit_cache_write")
     return status
@@ -653,6 +654,8 @@ def cache_read(cache, chunks, rows, out=None, status=None):
     vs = _packed(v, cache.kv_heads, cache.head_dim, d, "ds_vit_cache_read")
     if k.shape[0] != rows or v.shape[0] != rows:
         _refuse("ds_vit_cache_read")
+    if rows == 0:
+        return k, v, status
     check(lib.ds_vit_cache_read(cache.ref, chunks.ref, k.data_ptr(), ks, v.data_ptr(), vs, rows, status.data_ptr(),
                                 stream), "ds_vit_cache_read")
     return k, v, status
@@ -669,16 +672,20 @@ def cache_attention_workspace_bytes(cache, chunks, heads):
     return nb
 
 
+_workspaces = {}   # of cache_attention: (device, stream) -> tensor
+
+
 def _workspace(cache, chunks, heads, stream):
-    """A workspace that nothing else uses while the call's kernels run: the cache's
-    own for this stream, whose calls follow one another; a graph under capture
-    gets one of its own."""
+    """A workspace that nothing else uses while the call's kernels run: the one kept
+    for the stream, whose calls follow one another; a graph under capture gets one
+    of its own."""
     need = cache_attention_workspace_bytes(cache, chunks, heads)
     if _capturing():
         return _torch().empty(need, dtype=_u8, device=cache.device)
-    ws = cache._ws.get(stream)
+    key = cache.device_index, stream
+    ws = _workspaces.get(key)
     if ws is None or ws.numel() < need:
-        ws = cache._ws[stream] = _torch().empty(need, dtype=_u8, device=cache.device)
+        ws = _workspaces[key] = _torch().empty(need, dtype=_u8, device=cache.device)
     return ws
 
 
@@ -686,7 +693,7 @@ def cache_attention(cache, chunks, q, scale=None, window=0, sinks=0, out=None, w
     """Attention of the packed rows q (bf16 [rows, heads, head_dim], rows may be
     strided) over the cache (ds_vit_cache_attention); scale defaults to
     head_dim ** -0.5.  ``ws``: uint8 workspace (calls that may overlap need one
-    each; when not given, the cache keeps one per stream).  Returns (out, status)."""
+    each; when not given, one is kept for each stream).  Returns (out, status)."""
     d, stream, status = _on_device(cache, chunks, status, "ds_vit_cache_attention")
     if q.dim() != 3:
         _refuse("ds_vit_cache_attention")
@@ -697,6 +704,8 @@ def cache_attention(cache, chunks, q, scale=None, window=0, sinks=0, out=None, w
     os_ = _packed(out, heads, dim, d, "ds_vit_cache_attention")
     if out.shape[0] != rows:
         _refuse("ds_vit_cache_attention")
+    if rows == 0:
+        return out, status
     if ws is None:
         ws = _workspace(cache, chunks, heads, stream)
     elif ws.dtype is not _u8 or ws.get_device() != d or not ws.is_contiguous():

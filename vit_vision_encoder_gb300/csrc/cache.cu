@@ -218,7 +218,7 @@ int check_cache(const ds_vit_cache* c, const ds_vit_chunks* b, int64_t rows, Cac
     return DS_VIT_EINVAL;
   if (b->n < 1 || b->n > DS_VIT_MAX_SEQS || b->table_cols < 1 || b->max_rows < 1 || rows < 0) return DS_VIT_EINVAL;
   // Rows of the pages are TMA coordinates, and positions are int32.
-  if (c->n_pages > INT32_MAX / (c->page * c->kv_heads) || b->table_cols > INT32_MAX / c->page || rows > INT32_MAX / 2)
+  if (c->n_pages > INT32_MAX / (c->page * c->kv_heads) || b->table_cols > (INT32_MAX - 255) / c->page || rows > INT32_MAX / 2)
     return DS_VIT_ERANGE;
   *cv = CacheView{static_cast<uint8_t*>(c->k), static_cast<uint8_t*>(c->v), c->k_exp, c->v_exp,
                   c->n_pages, c->kv_heads, shift};

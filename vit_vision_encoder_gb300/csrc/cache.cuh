@@ -42,13 +42,9 @@ struct Seq {
 __device__ __forceinline__ Seq load_seq(const ChunkView& b, int page_shift, int s, int* status) {
   const int a = __ldg(b.row_off + s), e = __ldg(b.row_off + s + 1), kv = __ldg(b.kv_len + s);
   Seq q{a, e - a, kv};
-  int err = 0;
-  if (a < 0 || e < a || e > b.rows || e - a > b.max_rows)
-    err = DS_VIT_EINVAL;
-  else if (kv < 0 || kv > (static_cast<int64_t>(b.table_cols) << page_shift))
-    err = DS_VIT_ERANGE;
-  if (err) {
-    report_error(status, err);
+  const int why = seq_refused(a, e, kv, b.rows, b.max_rows, static_cast<int64_t>(b.table_cols) << page_shift);
+  if (why) {
+    report_error(status, why == 1 ? DS_VIT_EINVAL : DS_VIT_ERANGE);
     q = Seq{0, 0, 0};
   }
   return q;
@@ -78,7 +74,7 @@ __device__ __forceinline__ int find_seq(const ChunkView& b, int r, int lane) {
 // table's entry names no page.
 __device__ __forceinline__ int64_t page_of(const ChunkView& b, const CacheView& c, int s, int pos, int* status) {
   const int p = __ldg(b.table + static_cast<int64_t>(s) * b.table_cols + (pos >> c.page_shift));
-  if (p < 0 || p >= c.n_pages) {
+  if (!page_there(p, c.n_pages)) {
     report_error(status, DS_VIT_ERANGE);
     return -1;
   }

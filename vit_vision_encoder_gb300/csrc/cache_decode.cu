@@ -182,7 +182,7 @@ __device__ __forceinline__ void produce(const CUtensorMap* tm_k, const CUtensorM
       bool on[2];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        on[h] = page[h] >= 0 && page[h] < a.c.n_pages;
+        on[h] = page_there(page[h], a.c.n_pages);
         if (!on[h] && page[h] != -2) report_error(a.status, DS_VIT_ERANGE);
       }
       mbar_expect_tx(bar, (S::kStage + S::kExp) / halves * (on[0] + on[1]));

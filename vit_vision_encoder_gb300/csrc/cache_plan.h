@@ -12,6 +12,15 @@
 
 namespace dsvit {
 
+// Why a sequence is refused: 1 for rows out of order, outside the packed ones
+// or more than max_rows, 2 for a length that the table row has no places for, 0
+// if it is not.
+DSV_HD int seq_refused(int row0, int row1, int kv, int rows, int max_rows, int64_t places) {
+  if (row0 < 0 || row1 < row0 || row1 > rows || row1 - row0 > max_rows) return 1;
+  return kv < 0 || kv > places ? 2 : 0;
+}
+DSV_HD bool page_there(int page, int64_t n_pages) { return page >= 0 && page < n_pages; }
+
 // The blocks of 2^shift keys that rows at positions p0 .. p1 see: the blocks
 // of the first `sinks` keys that lie before the window of p0, then the
 // blocks from that window's first key to p1.  Rows before position 0 see none.

@@ -444,7 +444,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
       for (int b = w.b; b < w.end; ++b) {
         const int entry = next;
         if (b + 1 < w.end) next = look(b + 1);
-        const bool on = entry >= 0 && entry < a.c.n_pages;
+        const bool on = page_there(entry, a.c.n_pages);
         if (!on && entry != -2) report_error(a.status, DS_VIT_ERANGE);
         const int loaded = __popc(__ballot_sync(0xFFFFFFFFu, on));
         const int key0 = w.kb.at(b) << kTileShift;

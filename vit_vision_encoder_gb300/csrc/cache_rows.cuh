@@ -53,6 +53,11 @@ __device__ __noinline__ void exact_row(const AttentionArgs& a, int s, int row0, 
 #pragma unroll
     for (int x = 0; x < kPer; ++x) o[x] = o[x] * alpha + w * vx[x];
     m = m_new;
+    // Nothing more to find out: the row does see what makes it NaN throughout.
+    bool lost = true;
+#pragma unroll
+    for (int x = 0; x < kPer; ++x) lost &= o[x] != o[x];
+    if (__all_sync(0xFFFFFFFFu, lost)) break;
   }
   bf16* to = a.out + (row0 + i) * a.out_stride + h * D + lane * kPer;
 #pragma unroll
@@ -102,7 +107,7 @@ inline Records records_in(void* ws, int64_t workers, int rows, int d) {
 // The order is fixed, so a result depends on the lengths alone.
 constexpr int kJoinWarps = 8;
 constexpr int kJoinItems = 16;    // workers per block at most
-constexpr int kJoinRows = 16;     // grid rows at most
+constexpr int kJoinRows = 8;      // grid rows at most (16: 2 us more where nothing is split, 4 less where much is)
 
 // Adds parts first, first + step, ... of one row to (m, l, o), loads of four parts at a time.
 template <int D>
