@@ -441,6 +441,8 @@ __global__ void __launch_bounds__(Shape<D, E4M3>::kThreads, 1)
                             *reinterpret_cast<uint32_t(*)[4]>(vw + 2 * n));
         }
       }
+      // The reads come before the loads that the stage's return lets in.
+      fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(empty + 8 * slot);
       if (++slot == S::kStages) {
