@@ -63,7 +63,9 @@ struct Cfg {
   static constexpr int kHalf = kTile * 128;                // 64 dims of it
   static constexpr int kRawBytes = kTile * D;              // an e4m3 tile
   static constexpr int kRing = E4M3 ? (D == 128 ? 3 : 6) : (D == 128 ? 5 : 8);
-  static constexpr int kRaw = E4M3 ? (D == 128 ? 3 : 4) : 0;
+  // The converters of keys and those of values each wait for every use of their raw
+  // places and for no other (a wait by parity must not skip a use): an even number.
+  static constexpr int kRaw = E4M3 ? 4 : 0;
   // Tile B takes part in items without rows for it (with a ring of three tiles it would wait for A's).
   static constexpr bool kShare = kRing > 3;
   static constexpr int kOffKv = 2 * kBytes;                // after Q_A, Q_B
