@@ -661,6 +661,52 @@ __global__ void __launch_bounds__(Shape<D, E4M3>::kThreads, 1)
   if (lane == 0) rec.headers[me] = dead ? SplitHeader{} : header;
 }
 
+// Joins the parts of every split item.  Block (y, x) looks after workers x, x +
+// gridDim.y, ... and rows y, y + gridDim.x, ... of their items (rows in the grid's
+// fast dimension: the blocks of the few workers with something to join then lie on
+// many SMs).  One warp adds up a row; where many parts meet few rows (a token over
+// a long cache) the parts are shared between the block's warps.
+constexpr int kJoinItems = 16;    // workers per block at most
+constexpr int kJoinRows = 8;      // grid rows at most
+
+template <int D, bool E4M3>
+__global__ void __launch_bounds__(32 * kJoinWarps)
+    join_kernel(const __grid_constant__ AttentionArgs a, const Records rec, int workers) {
+  constexpr int kPer = D / 32;
+  __shared__ SplitHeader heads[kJoinItems];
+  grid_dep_launch();
+  grid_dep_wait();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int group = blockIdx.y, groups = gridDim.y;
+  const int mine = (workers - group + groups - 1) / groups;
+  if (threadIdx.x < 2 * mine)
+    reinterpret_cast<int4*>(heads)[threadIdx.x] =
+        reinterpret_cast<const int4*>(rec.headers + group + (threadIdx.x >> 1) * groups)[threadIdx.x & 1];
+  __syncthreads();
+  int turn = 0;                       // rows dealt to the warps so far
+  for (int k = 0; k < mine; ++k) {
+    const SplitHeader& hd = heads[k];
+    if (hd.parts == 0) continue;
+    const int w = group + k * groups;
+    const int64_t left = static_cast<int64_t>(hd.q.c) * a.group - hd.rho0;
+    const int rows = left < rec.rows ? static_cast<int>(left) : rec.rows;
+    for (int row = blockIdx.x; row < rows; row += gridDim.x) {
+      float m = -INFINITY, l = 0.f, o[kPer];
+#pragma unroll
+      for (int x = 0; x < kPer; ++x) o[x] = 0.f;
+      if (hd.parts <= kJoinWarps) {
+        if (turn++ % kJoinWarps != warp) continue;
+        join_parts<D, 4>(rec, w, hd.parts, row, 0, 1, lane, m, l, o);
+        join_finish<D, E4M3>(a, hd, hd.rho0 + row, l, o, lane);
+        continue;
+      }
+      join_parts<D, 4>(rec, w, hd.parts, row, warp, kJoinWarps, lane, m, l, o);
+      join_warps<D>(warp, lane, m, l, o);
+      if (warp == 0) join_finish<D, E4M3>(a, hd, hd.rho0 + row, l, o, lane);
+    }
+  }
+}
+
 template <int D, bool E4M3, int kRowHalves>
 int launch(const AttentionArgs& a, void* ws, cudaStream_t stream) {
   using S = Shape<D, E4M3>;
@@ -679,7 +725,9 @@ int launch(const AttentionArgs& a, void* ws, cudaStream_t stream) {
   const Records rec = records_in(ws, workers, R, D);
   cudaError_t e = launch_pdl(decode_kernel<D, E4M3, kRowHalves>, dim3(grid), dim3(S::kThreads), S::kSmem, stream, tk, tv,
                              a, rec);
-  if (e == cudaSuccess) e = launch_join<D, E4M3>(a, rec, grid, workers, stream);
+  if (e == cudaSuccess)
+    e = launch_pdl(join_kernel<D, E4M3>, dim3(rec.rows < kJoinRows ? rec.rows : kJoinRows, grid),
+                   dim3(32 * kJoinWarps), 0, stream, a, rec, workers);
   if (e != cudaSuccess) cudaGetLastError();
   return e == cudaSuccess ? DS_VIT_OK : DS_VIT_ECUDA;
 }

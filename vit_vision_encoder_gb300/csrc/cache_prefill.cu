@@ -7,7 +7,7 @@
 // lengths on the device and dealt to the CTAs, one per SM, in equal shares
 // (cache_plan.h): causal items of unequal depth, short chunks over long caches
 // and ragged batches all end together.  A CTA finishes the items that lie within
-// its share; the others leave records that join_kernel adds up.
+// its share; the others leave records that join_items_kernel adds up.
 //
 // Roles: warps 0-7 run the softmax of tile A and warps 8-15 that of tile B, two
 // threads a row (16x32bx2 TMEM accesses, as in the bidirectional kernel); warp
@@ -1034,6 +1034,66 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
   }
 }
 
+// Adds up the records of the split items and writes their rows: all those rows in one
+// list, dealt to the warps of one wave of blocks (two sequences of 60 rows and 32 heads
+// over 20 and 60 thousand tokens, 24 items in 152 parts: 8 us, eight parts
+// of a row in flight instead of four 12; with blocks bound to
+// items it took 16).  Where the rows are few, the warps of a block share a row's parts.
+constexpr int kMaxCtas = 256;        // of the kernel above; a thread here looks at each
+constexpr int kJoinBlocks = 4;       // per SM
+
+template <int D, bool E4M3>
+__global__ void __launch_bounds__(32 * kJoinWarps, kJoinBlocks)
+    join_items_kernel(const __grid_constant__ AttentionArgs a, const Records rec, int workers) {
+  static_assert(kMaxCtas == 32 * kJoinWarps, "a thread per worker");
+  constexpr int kPer = D / 32;
+  __shared__ SplitHeader heads[kMaxCtas];
+  __shared__ int before[kMaxCtas];     // rows of the workers before each
+  __shared__ int sums[kJoinWarps];
+  grid_dep_launch();
+  grid_dep_wait();
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  for (int i = tid; i < 2 * workers; i += 32 * kJoinWarps)
+    reinterpret_cast<int4*>(heads)[i] = reinterpret_cast<const int4*>(rec.headers)[i];
+  __syncthreads();
+  int rows = 0;
+  if (tid < workers && heads[tid].parts != 0)
+    rows = min(heads[tid].q.c * a.group - heads[tid].rho0, kItemRows);
+  int inc = rows;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xFFFFFFFFu, inc, o);
+    if (lane >= o) inc += y;
+  }
+  if (lane == 31) sums[warp] = inc;
+  __syncthreads();
+  int total = 0, ahead = 0;
+#pragma unroll
+  for (int y = 0; y < kJoinWarps; ++y) {
+    if (y == warp) ahead = total;
+    total += sums[y];
+  }
+  before[tid] = ahead + inc - rows;
+  __syncthreads();
+  const bool together = total <= 2 * static_cast<int>(gridDim.x);
+  const int first = together ? blockIdx.x : warp * gridDim.x + blockIdx.x;
+  const int step = together ? gridDim.x : kJoinWarps * gridDim.x;
+  for (int r = first; r < total; r += step) {
+    int w = 0;                         // the last worker with before[w] <= r
+#pragma unroll
+    for (int half = kMaxCtas / 2; half > 0; half >>= 1)
+      if (before[w + half] <= r) w += half;
+    const SplitHeader& hd = heads[w];
+    const int row = r - before[w];
+    float m = -INFINITY, l = 0.f, o[kPer];
+#pragma unroll
+    for (int x = 0; x < kPer; ++x) o[x] = 0.f;
+    join_parts<D, 4>(rec, w, hd.parts, row, together ? warp : 0, together ? kJoinWarps : 1, lane, m, l, o);
+    if (together) join_warps<D>(warp, lane, m, l, o);
+    if (!together || warp == 0) join_finish<D, E4M3>(a, hd, hd.rho0 + row, l, o, lane);
+  }
+}
+
 template <int D, bool E4M3>
 int launch(const AttentionArgs& a, void* ws, cudaStream_t stream) {
   using C = Cfg<D, E4M3>;
@@ -1046,10 +1106,11 @@ int launch(const AttentionArgs& a, void* ws, cudaStream_t stream) {
   };
   if (!map(&tk, a.c.k) || !map(&tv, a.c.v)) return DS_VIT_ECUDA;
   if (allow_smem(reinterpret_cast<const void*>(prefill_kernel<D, E4M3>), C::kSmem) != cudaSuccess) return DS_VIT_ECUDA;
-  const int grid = num_sms();
+  const int sms = num_sms(), grid = sms < kMaxCtas ? sms : kMaxCtas;
   const PrefillArgs p{a, records_in(ws, grid, kItemRows, D)};
   cudaError_t e = launch_pdl(prefill_kernel<D, E4M3>, dim3(grid), dim3(C::kThreads), C::kSmem, stream, tk, tv, p);
-  if (e == cudaSuccess) e = launch_join<D, E4M3>(a, p.rec, grid, grid, stream);
+  if (e == cudaSuccess)
+    e = launch_pdl(join_items_kernel<D, E4M3>, dim3(kJoinBlocks * sms), dim3(32 * kJoinWarps), 0, stream, a, p.rec, grid);
   if (e != cudaSuccess) cudaGetLastError();
   return e == cudaSuccess ? DS_VIT_OK : DS_VIT_ECUDA;
 }

@@ -98,22 +98,13 @@ inline Records records_in(void* ws, int64_t workers, int rows, int d) {
   return Records{h, reinterpret_cast<float*>(h + workers), rows, record_floats(rows, d)};
 }
 
-// Joins the parts of every split item: O = sum_p 2^(m_p - M) O_p, L alike.
-// Block (y, x) looks after workers x, x + gridDim.y, ... and rows y, y +
-// gridDim.x, ... of their items (rows in the grid's fast dimension: the blocks
-// of the few workers with something to join then lie on many SMs).  One warp
-// adds up a row; where many parts meet few rows (a token over a long cache) the
-// parts are shared between the block's warps and joined through shared memory.
-// The order is fixed, so a result depends on the lengths alone.
-constexpr int kJoinWarps = 8;
-constexpr int kJoinItems = 16;    // workers per block at most
-constexpr int kJoinRows = 8;      // grid rows at most (16: 2 us more where nothing is split, 4 less where much is)
-
-// Adds parts first, first + step, ... of one row to (m, l, o), loads of four parts at a time.
-template <int D>
+// Adds parts first, first + step, ... of one row of a split item, O = sum_p 2^(m_p - M) O_p and L
+// alike, to (m, l, o), loads of kBatch parts at a time.  The order is fixed, so a result depends
+// on the lengths alone.
+template <int D, int kBatch>
 __device__ __forceinline__ void join_parts(const Records& rec, int w, int parts, int row, int first, int step, int lane,
                                            float& m, float& l, float (&o)[D / 32]) {
-  constexpr int kPer = D / 32, kBatch = 4;
+  constexpr int kPer = D / 32;
   for (int p0 = first; p0 < parts; p0 += kBatch * step) {
     float mp[kBatch], lp[kBatch], op[kBatch][kPer];
 #pragma unroll
@@ -154,6 +145,36 @@ __device__ __forceinline__ void join_parts(const Records& rec, int w, int parts,
   }
 }
 
+constexpr int kJoinWarps = 8;
+// A row whose parts the warps of a block have added up: the warps' sums joined by the first.
+template <int D>
+__device__ __forceinline__ void join_warps(int warp, int lane, float m, float& l, float (&o)[D / 32]) {
+  constexpr int kPer = D / 32;
+  __shared__ float sm[kJoinWarps], sl[kJoinWarps], so[kJoinWarps][D];
+  __syncthreads();          // the previous row's results have been read
+  if (lane == 0) {
+    sm[warp] = m;
+    sl[warp] = l;
+  }
+#pragma unroll
+  for (int x = 0; x < kPer; ++x) so[warp][lane * kPer + x] = o[x];
+  __syncthreads();
+  if (warp != 0) return;
+  float M = sm[0];
+#pragma unroll
+  for (int x = 1; x < kJoinWarps; ++x) M = fmaxf(M, sm[x]);
+  l = 0.f;
+#pragma unroll
+  for (int x = 0; x < kPer; ++x) o[x] = 0.f;
+#pragma unroll
+  for (int y = 0; y < kJoinWarps; ++y) {
+    const float f = sm[y] == M ? 1.f : exp2f(sm[y] - M);
+    l += sl[y] * f;
+#pragma unroll
+    for (int x = 0; x < kPer; ++x) o[x] += so[y][lane * kPer + x] * f;
+  }
+}
+
 // One warp writes a joined row.
 template <int D, bool E4M3>
 __device__ __forceinline__ void join_finish(const AttentionArgs& a, const SplitHeader& hd, int rho, float l,
@@ -177,73 +198,6 @@ __device__ __forceinline__ void join_finish(const AttentionArgs& a, const SplitH
     __syncwarp();
     exact_row<D, E4M3>(a, hd.s, hd.q.row0, p, i, h, lane);
   }
-}
-
-template <int D, bool E4M3>
-__global__ void __launch_bounds__(32 * kJoinWarps)
-    join_kernel(const __grid_constant__ AttentionArgs a, const Records rec, int workers) {
-  constexpr int kPer = D / 32;
-  __shared__ float sm[kJoinWarps], sl[kJoinWarps], so[kJoinWarps][D];
-  __shared__ SplitHeader heads[kJoinItems];
-  grid_dep_launch();
-  grid_dep_wait();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int group = blockIdx.y, groups = gridDim.y;
-  const int mine = (workers - group + groups - 1) / groups;
-  if (threadIdx.x < 2 * mine)
-    reinterpret_cast<int4*>(heads)[threadIdx.x] =
-        reinterpret_cast<const int4*>(rec.headers + group + (threadIdx.x >> 1) * groups)[threadIdx.x & 1];
-  __syncthreads();
-  int turn = 0;                       // rows dealt to the warps so far
-  for (int k = 0; k < mine; ++k) {
-    const SplitHeader& hd = heads[k];
-    if (hd.parts == 0) continue;
-    const int w = group + k * groups;
-    const int64_t left = static_cast<int64_t>(hd.q.c) * a.group - hd.rho0;
-    const int rows = left < rec.rows ? static_cast<int>(left) : rec.rows;
-    for (int row = blockIdx.x; row < rows; row += gridDim.x) {
-      float m = -INFINITY, l = 0.f, o[kPer];
-#pragma unroll
-      for (int x = 0; x < kPer; ++x) o[x] = 0.f;
-      if (hd.parts <= kJoinWarps || rows > 16) {
-        if (turn++ % kJoinWarps != warp) continue;
-        join_parts<D>(rec, w, hd.parts, row, 0, 1, lane, m, l, o);
-        join_finish<D, E4M3>(a, hd, hd.rho0 + row, l, o, lane);
-        continue;
-      }
-      join_parts<D>(rec, w, hd.parts, row, warp, kJoinWarps, lane, m, l, o);
-      __syncthreads();      // the previous row's results have been read
-      if (lane == 0) {
-        sm[warp] = m;
-        sl[warp] = l;
-      }
-#pragma unroll
-      for (int x = 0; x < kPer; ++x) so[warp][lane * kPer + x] = o[x];
-      __syncthreads();
-      if (warp == 0) {
-        float M = sm[0];
-#pragma unroll
-        for (int x = 1; x < kJoinWarps; ++x) M = fmaxf(M, sm[x]);
-        l = 0.f;
-#pragma unroll
-        for (int x = 0; x < kPer; ++x) o[x] = 0.f;
-#pragma unroll
-        for (int y = 0; y < kJoinWarps; ++y) {
-          const float f = sm[y] == M ? 1.f : exp2f(sm[y] - M);
-          l += sl[y] * f;
-#pragma unroll
-          for (int x = 0; x < kPer; ++x) o[x] += so[y][lane * kPer + x] * f;
-        }
-        join_finish<D, E4M3>(a, hd, hd.rho0 + row, l, o, lane);
-      }
-    }
-  }
-}
-
-template <int D, bool E4M3>
-cudaError_t launch_join(const AttentionArgs& a, const Records& rec, int grid, int workers, cudaStream_t stream) {
-  return launch_pdl(join_kernel<D, E4M3>, dim3(rec.rows < kJoinRows ? rec.rows : kJoinRows, grid), dim3(32 * kJoinWarps),
-                    0, stream, a, rec, workers);
 }
 
 }  // namespace dsvit
