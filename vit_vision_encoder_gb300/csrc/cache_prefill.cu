@@ -16,7 +16,9 @@
 //   S_X = Q_X K_j^T     (M 128, N 128, K D)    smem x smem -> TMEM
 //   O_X += P_X V_j      (M 128, N D,   K 128)  TMEM x smem -> TMEM
 // P_X (16-bit pairs) takes the first half of S_X's columns, so S_X of the next
-// tile waits for P_X V_j; the other tile's MMAs and softmax fill that time.
+// tile waits for P_X V_j; the other tile's MMAs and softmax fill that time.  At head
+// dim 64 TMEM has room for a third score tile, and A and B take the three in turn
+// (e4m3, windowed chunks of 30 to 1500 rows: 54.5 -> 50.9 us).
 // Rows of Q are loaded by the softmax warps, so any group size fills the tiles.
 // Warp 18 walks the CTA's items and hands them to the other roles through a
 // ring in shared memory.  The rows' way in and out of the tiles is through
@@ -54,7 +56,6 @@ constexpr int kItemRows = 2 * kTile;
 constexpr int kWarpTma = 16, kWarpMma = 17, kWarpJobs = 18;
 constexpr int kWarpConvert = 20;            // 20 .. 23: key tiles, 24 .. 27: value tiles (e4m3)
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kTmemO = 256;            // S_A, S_B at 0, 128; O_A, O_B from here
 
 template <int D, bool E4M3>
 struct Cfg {
@@ -68,6 +69,10 @@ struct Cfg {
   static constexpr int kRaw = E4M3 ? 4 : 0;
   // Tile B takes part in items without rows for it (with a ring of three tiles it would wait for A's).
   static constexpr bool kShare = kRing > 3;
+  // Score tiles in TMEM, 128 columns each, then O_A and O_B: one each for A and B, or
+  // (where O leaves room) three for the two of them in turn.
+  static constexpr int kScores = D == 64 ? 3 : 2;
+  static constexpr uint32_t kTmemO = 128 * kScores;
   static constexpr int kOffKv = 2 * kBytes;                // after Q_A, Q_B
   static constexpr int kOffRaw = kOffKv + kRing * kBytes;
   static constexpr int kOffExp = kOffRaw + kRaw * kRawBytes;   // exponents of the raw tiles
@@ -85,16 +90,16 @@ enum : int {
   kBarKvEmpty = 10,         // [8]
   kBarRawFull = 18,         // [4]
   kBarRawEmpty = 22,        // [4]
-  kBarSFull = 26,           // [2]
-  kBarPFull = 28,           // [2]
-  kBarPvDone = 30,          // [2]
-  kBarRagged = 32,          // a value tile with rows to zero has landed
-  kBarDrain = 33,
-  kBarJobFull = 34,         // [4]
-  kBarJobEmpty = 38,        // [4]
-  kBarOther = 42,           // tile B's share of the keys is summed up
-  kBarMerged = 43,          // and has been read
-  kBarCount = 44
+  kBarSFull = 26,           // [3] by score tile
+  kBarPFull = 29,           // [2]
+  kBarPvDone = 31,          // [2]
+  kBarRagged = 33,          // a value tile with rows to zero has landed
+  kBarDrain = 34,
+  kBarJobFull = 35,         // [4]
+  kBarJobEmpty = 39,        // [4]
+  kBarOther = 43,           // tile B's share of the keys is summed up
+  kBarMerged = 44,          // and has been read
+  kBarCount = 45
 };
 
 struct PrefillArgs {
@@ -365,10 +370,10 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
   if (threadIdx.x == 0) {
     for (int x = 0; x < 2; ++x) {
       mbar_init(bar(kBarQ + x), 256);
-      mbar_init(bar(kBarSFull + x), 1);
       mbar_init(bar(kBarPFull + x), 256);
       mbar_init(bar(kBarPvDone + x), 1);
     }
+    for (int i = 0; i < C::kScores; ++i) mbar_init(bar(kBarSFull + i), 1);
     for (int i = 0; i < C::kRing; ++i) {
       mbar_init(bar(kBarKvFull + i), E4M3 ? 4 : 1);
       mbar_init(bar(kBarKvEmpty + i), 1);
@@ -540,7 +545,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
     const uint64_t dk0 = sdesc_sw128(sKv(0), 16, 1024);
     const uint64_t dv0 = sdesc_sw128(sKv(0), C::kHalf, 1024);
     int slot = 0, used = 0;
-    uint32_t phase = 0, q0 = 0, q1 = 0, step0 = 0, step1 = 0;
+    uint32_t phase = 0, q0 = 0, q1 = 0, step0 = 0, step1 = 0, seq = 0;
     auto wait = [&](int i, uint32_t parity) { return __all_sync(0xFFFFFFFFu, mbar_wait(bar(i), parity, a.status)); };
     auto advance = [&]() {
       ++used;
@@ -549,23 +554,23 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
         phase ^= 1;
       }
     };
-    auto issue_s = [&](int x, int at) {
+    auto issue_s = [&](int x, int at, int tile) {        // into score tile `tile`
       const uint64_t dq = dq0 + static_cast<uint64_t>(x * (C::kBytes >> 4));
       const uint64_t dk = dk0 + static_cast<uint64_t>(at * (C::kBytes >> 4));
       tc_fence_after();
 #pragma unroll
       for (int k = 0; k < D / 16; ++k) {
         const uint64_t off = (k >> 2) * (C::kHalf >> 4) + 2 * (k & 3);
-        umma_bf16_if(go, tm + x * 128, dq + off, dk + off, id_s, k != 0);
+        umma_bf16_if(go, tm + tile * 128, dq + off, dk + off, id_s, k != 0);
       }
-      umma_commit_if(go, bar(kBarSFull + x));
+      umma_commit_if(go, bar(kBarSFull + tile));
     };
-    auto issue_pv = [&](int x, int at, bool fresh) {
+    auto issue_pv = [&](int x, int at, bool fresh, int tile) {
       const uint64_t dv = dv0 + static_cast<uint64_t>(at * (C::kBytes >> 4));
       tc_fence_after();
 #pragma unroll
       for (int k = 0; k < kTile / 16; ++k)
-        umma_bf16_ts_if(go, tm + kTmemO + x * D, tm + x * 128 + k * 8, dv + 128 * k, id_o, !fresh | (k != 0));   // 16 rows = 2048 B
+        umma_bf16_ts_if(go, tm + C::kTmemO + x * D, tm + tile * 128 + k * 8, dv + 128 * k, id_o, !fresh | (k != 0));   // 16 rows = 2048 B
       umma_commit_if(go, bar(kBarPvDone + x));
     };
     // Place of a tile `ahead` of the next in the ring, and whether it has been filled.
@@ -579,11 +584,43 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
       const bool both = __shfl_sync(0xFFFFFFFFu, w.q.c * a.group - w.rho0, 0) > kTile;
       const int count = __shfl_sync(0xFFFFFFFFu, w.end - w.b, 0);
       bool ok = true;
-      if (both) {
+      if constexpr (C::kScores == 3) {
+        // Products n = 0, 1, ... of the item, A's and B's in turn, use score tiles seq + n
+        // mod 3: S of n + 3 follows P V of n, so that a softmax finds its next scores ready.
+        const int products = both ? 2 * count : count;
+        const uint32_t base = used;
+        auto at = [&](int i) { return static_cast<int>((base + i) % C::kRing); };
+        auto filled = [&](int i) { return wait(kBarKvFull + at(i), ((base + i) / C::kRing) & 1); };
+        auto scores = [&](int n) {
+          const int x = n & 1, i = both ? n & ~1 : 2 * n;       // the keys' place
+          if (!filled(i)) return false;
+          if (n < 2) {
+            if (!wait(kBarQ + x, x == 0 ? q0 : q1)) return false;
+            (x == 0 ? q0 : q1) ^= 1;
+          }
+          issue_s(x, at(i), (seq + n) % 3);
+          if (!both || x == 1) release(at(i));
+          return true;
+        };
+        for (int n = 0; ok && n < 3 && n < products; ++n) ok = scores(n);
+        for (int n = 0; ok && n < products; ++n) {
+          const int x = n & 1, i = (both ? n & ~1 : 2 * n) + 1;
+          const uint32_t step = x == 0 ? step0++ : step1++;
+          ok = filled(i) && wait(kBarPFull + x, step & 1);
+          if (!ok) break;
+          issue_pv(x, at(i), n < 2, (seq + n) % 3);
+          if (!both || x == 1) {
+            release(at(i));
+            used = base + i + 1;
+          }
+          if (n + 3 < products) ok = wait(kBarPvDone + x, step & 1) && scores(n + 3);
+        }
+        seq += products;
+      } else if (both) {
         if (!there(0) || !wait(kBarQ, q0)) break;
-        issue_s(0, slot);
+        issue_s(0, slot, 0);
         if (!wait(kBarQ + 1, q1)) break;
-        issue_s(1, slot);
+        issue_s(1, slot, 1);
         release(slot);
         q0 ^= 1;
         q1 ^= 1;
@@ -595,22 +632,22 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
           advance();
           ok = ok && wait(kBarPFull, step0 & 1);
           if (!ok) break;
-          issue_pv(0, v_slot, b == 0);
+          issue_pv(0, v_slot, b == 0, 0);
           if (more) {
             // S_X overwrites P_X: its product must be complete.
             ok = there(0) && wait(kBarPvDone, step0 & 1);
             if (!ok) break;
-            issue_s(0, slot);
+            issue_s(0, slot, 0);
           }
           ++step0;
           ok = wait(kBarPFull + 1, step1 & 1);
           if (!ok) break;
-          issue_pv(1, v_slot, b == 0);
+          issue_pv(1, v_slot, b == 0, 1);
           release(v_slot);
           if (more) {
             ok = wait(kBarPvDone + 1, step1 & 1);
             if (!ok) break;
-            issue_s(1, slot);
+            issue_s(1, slot, 1);
             release(slot);
             advance();
           }
@@ -621,23 +658,23 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
         // V1 ...; `slot` stays at the values of the step.
         if (!there(0) || !wait(kBarQ, q0)) break;
         q0 ^= 1;
-        issue_s(0, slot);
+        issue_s(0, slot, 0);
         release(slot);
         advance();
         if (C::kShare && count > 1) {
           if (!there(1) || !wait(kBarQ + 1, q1)) break;
           q1 ^= 1;
-          issue_s(1, place(1));
+          issue_s(1, place(1), 1);
           release(place(1));
         }
         constexpr int kTurns = C::kShare ? 2 : 1;
         auto turn = [&](int x, uint32_t& step, int b) {
           if (!there(0) || !wait(kBarPFull + x, step & 1)) return false;
-          issue_pv(x, slot, b < kTurns);
+          issue_pv(x, slot, b < kTurns, x);
           release(slot);
           if (b + kTurns < count) {
             if (!there(2 * kTurns - 1) || !wait(kBarPvDone + x, step & 1)) return false;
-            issue_s(x, place(2 * kTurns - 1));
+            issue_s(x, place(2 * kTurns - 1), x);
             release(place(2 * kTurns - 1));
           }
           ++step;
@@ -738,9 +775,9 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
     const int h = lane >> 4;                 // 64-key half of the score tile
     const int r = row0 + (lane & 15);        // row inside the tile == TMEM lane
     const uint32_t lane_sel = static_cast<uint32_t>(row0) << 16;
-    const uint32_t tS = tmem + x * 128 + lane_sel;
-    const uint32_t tO = tmem + kTmemO + x * D + lane_sel;
-    uint32_t step = 0, merges = 0;
+    uint32_t tS = tmem + x * 128 + lane_sel;
+    const uint32_t tO = tmem + C::kTmemO + x * D + lane_sel;
+    uint32_t step = 0, merges = 0, seq = 0;      // seq: as the MMA issuer's
     int tile = 0;
     bool ok = true;
     Job w;
@@ -750,6 +787,8 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
       const bool shared = C::kShare && R - w.rho0 <= kTile;
       const int rho0 = shared ? w.rho0 : w.rho0 + x * kTile;   // first row of the tile
       const int stride = shared ? 2 : 1, b0 = shared ? w.b + x : w.b;
+      const uint32_t seq0 = seq;
+      seq += R - w.rho0 <= kTile ? count : 2 * count;
       if (rho0 >= R || b0 >= w.end) {
         tile += count;
         continue;
@@ -800,7 +839,14 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
       for (int b = b0; b < w.end; b += stride, ++step) {
         const int key0 = w.kb.at(b) << kTileShift, nth = tile + (b - w.b);     // the CTA's tiles before this one
         const bool open = key0 + kTile - 1 <= pa && (key0 >= lo_b || key0 + kTile <= a.sinks);
-        if (!mbar_wait(bar(kBarSFull + x), step & 1, a.status)) {
+        int at = x;
+        uint32_t use = step;
+        if constexpr (C::kScores == 3) {
+          const uint32_t n = seq0 + (shared ? b - w.b : 2 * (b - w.b) + x);
+          at = n % 3, use = n / 3;
+          tS = tmem + at * 128 + lane_sel;
+        }
+        if (!mbar_wait(bar(kBarSFull + at), use & 1, a.status)) {
           ok = false;
           break;
         }
@@ -866,8 +912,12 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
         f2_split(s2, s0, s1);
         l = l * alpha + (s0 + s1) * unit;    // this half's share of the row sum
         tmem_st32_x2<32>(tS, pk);
-        // O_X was last written by the product that S_X waited for: it is complete.
+        // With a score tile each, S_X waited for the product that wrote O_X last.
         if (b != b0 && __any_sync(0xFFFFFFFFu, alpha != 1.f)) {
+          if (C::kScores == 3) {
+            if (!mbar_wait(bar(kBarPvDone + x), (step - 1) & 1, a.status)) ok = false;
+            tc_fence_after();
+          }
 #pragma unroll
           for (int y = 0; y < D / 64; ++y) {
             uint32_t o[32];
