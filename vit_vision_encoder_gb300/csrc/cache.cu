@@ -5,6 +5,9 @@
 // by their chain of dependent loads (row -> sequence -> page -> slot) at one
 // token a sequence.  One warp takes one token: its keys and values of all
 // heads are two contiguous runs of the packed rows, read as 16-byte pieces.
+// Measured at 8 heads of 128: 6900 rows quantised as they are written 11.8 us (53% of
+// the rate of a plain copy, pieces of 128 bytes scattered over the pages), 92 thousand
+// tokens read back out of e4m3 pages 86 us (98%), 48 single tokens 2.5 us.
 #include "cache.cuh"
 
 namespace dsvit {

@@ -2,14 +2,17 @@
 // that share a K/V head (new tokens times query heads per K/V head) are taken
 // 16 at a time, up to decode_rows of them.
 //
-// Bound by the cache's bytes: each key and value read meets at most 16 rows, 32 flops a byte of bf16, a twentieth of the tensor rate the
-// bytes could feed.  So the products run as warp MMAs (m16n8k16), whose
-// fragments come straight from shared memory; what counts is bytes in flight
-// and a short chain of instructions per key.
+// Bound by the cache's bytes: each key and value read meets at most 16 rows, 32
+// flops a byte of bf16, a twentieth of the tensor rate the bytes could feed.  So the
+// products run as warp MMAs (m16n8k16), whose fragments come straight from shared
+// memory; what counts is bytes in flight and a short chain of instructions per key.
+// Measured at 40 query and 8 K/V heads of 128: 32 sequences of 400 to 16000 tokens,
+// bf16, 87 us (5.8 TB/s; the loads alone 85); 64 of 2000 to 30000, e4m3, 246 us (5.6
+// TB/s; the loads alone 216, the rest is conversions and products of twice the keys
+// a byte); one of 1500 tokens 10.3 us, three quarters of it fixed (launches, plan, join).
 //
 // Work: the unit is a block of kKeys keys of one item (sequence, K/V head, 16
-// rows).
-// All units of a call are counted from the lengths on the device and dealt in
+// rows).  All units of a call are counted from the lengths on the device and dealt in
 // order to the workers, the consumer warps of the grid, in equal shares
 // (cache_plan.h), so a batch of unequal lengths and a single long sequence both
 // keep every SM reading.  A worker streams its blocks through its own ring of

@@ -9,6 +9,13 @@
 // and ragged batches all end together.  A CTA finishes the items that lie within
 // its share; the others leave records that join_items_kernel adds up.
 //
+// Bound by the tensor pipe and the chain S -> softmax -> P V of a tile, of which two
+// (A's and B's) overlap: 2048 rows over 34 thousand tokens, 40 query and 8 K/V heads
+// of 128, bf16, take 965 us (1.44 PFLOP/s; 2820 cycles a step of two tiles, 2048 of
+// them tensor work).  Short calls are bound by what comes before and after: launch,
+// plan, first loads (9 us) and join (2.5 us where nothing is split) of the 35 us that
+// 1090 rows with nothing cached take.
+//
 // Roles: warps 0-7 run the softmax of tile A and warps 8-15 that of tile B, two
 // threads a row (16x32bx2 TMEM accesses, as in the bidirectional kernel); warp
 // 16 loads pages by TMA (a box per page and 64 dims) into a ring of key and
@@ -18,7 +25,7 @@
 // P_X (16-bit pairs) takes the first half of S_X's columns, so S_X of the next
 // tile waits for P_X V_j; the other tile's MMAs and softmax fill that time.  At head
 // dim 64 TMEM has room for a third score tile, and A and B take the three in turn
-// (e4m3, windowed chunks of 30 to 1500 rows: 54.5 -> 50.9 us).
+// (e4m3, windowed chunks of 31 to 1008 rows: 54.5 -> 50.9 us).
 // Rows of Q are loaded by the softmax warps, so any group size fills the tiles.
 // Warp 18 walks the CTA's items and hands them to the other roles through a
 // ring in shared memory.  The rows' way in and out of the tiles is through
@@ -1085,8 +1092,8 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
 }
 
 // Adds up the records of the split items and writes their rows: all those rows in one
-// list, dealt to the warps of one wave of blocks (two sequences of 60 rows and 32 heads
-// over 20 and 60 thousand tokens, 24 items in 152 parts: 8 us, eight parts
+// list, dealt to the warps of one wave of blocks (51 and 115 rows, 32 query and 4 K/V heads,
+// over 23 and 43 thousand tokens, 24 items in 152 parts: 8 us, eight parts
 // of a row in flight instead of four 12; with blocks bound to
 // items it took 16).  Where the rows are few, the warps of a block share a row's parts.
 constexpr int kMaxCtas = 256;        // of the kernel above; a thread here looks at each
