@@ -60,14 +60,15 @@ struct Shape {
   static constexpr int kWarps = D == 64 ? 11 : 7;
   static constexpr int kThreads = 32 * kWarps + 32;
   static constexpr int kRingBytes = (D == 64 ? 16 : 24) * 1024;      // per consumer warp
-  static constexpr int kKeyShift = E4M3 ? 5 : 4;
+  static constexpr int kKeyShift = E4M3 ? (D == 64 ? 6 : 5) : 4;
   static constexpr int kKeys = 1 << kKeyShift;             // keys of a block
   static constexpr int kRow = E4M3 ? D : 2 * D;            // bytes of a key
   static constexpr int kTile = kKeys * kRow;
   static constexpr int kPlane = kKeys * 128;               // bf16, D = 128: two planes of 64 dims
   static constexpr int kStage = 2 * kTile;                 // K, then V
   static constexpr int kStages = kRingBytes / kStage;
-  static constexpr int kExp = E4M3 ? 64 : 0;               // exponents of a stage: 32 K, 32 V
+  static constexpr int kExp = E4M3 ? 2 * kKeys : 0;        // exponents of a stage: K, then V
+  static constexpr int kPieces = kKeys / 16;               // pages of a block at most
   static constexpr int kSmem = 1024 + kWarps * (kRingBytes + kStages * (16 + kExp)) +
                                8 * (DS_VIT_MAX_SEQS + 1) + static_cast<int>(sizeof(Seq)) * DS_VIT_MAX_SEQS;
 };
@@ -141,24 +142,21 @@ template <int D, bool E4M3>
 __device__ __forceinline__ void produce(const CUtensorMap* tm_k, const CUtensorMap* tm_v, const AttentionArgs& a,
                                         const Plan& pl, uint32_t ring, uint32_t exps, uint32_t full, uint32_t empty) {
   using S = Shape<D, E4M3>;
-  constexpr int kPage16 = 16;
-  const int halves = E4M3 && a.c.page_shift == 4 ? 2 : 1;   // pages of a block
+  const int step = min(1 << a.c.page_shift, S::kKeys), pieces = S::kKeys / step;   // keys of a piece, pieces of a block
   int slot = 0;
   uint32_t phase = 1;                      // a new barrier's preceding phase counts as complete
   int64_t u = pl.begin;
   Item it{};
-  int p_last = 0, lo = 0, next[2] = {-1, -1};
+  int p_last = 0, lo = 0, next[S::kPieces] = {};
   // Table entries are read a block ahead.  Of a block's pages only those that some row sees are needed.
   auto look = [&](int b) {
     const int key0 = it.kb.at(b) << S::kKeyShift;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int k0 = key0 + h * kPage16, k1 = halves == 2 ? k0 + kPage16 - 1 : key0 + S::kKeys - 1;
-      next[h] = -1;
-      if (h < halves && k0 <= p_last && (k1 >= lo || k0 < a.sinks))
+    for (int h = 0; h < S::kPieces; ++h) {
+      const int k0 = key0 + h * step, k1 = k0 + step - 1;
+      next[h] = -2;                        // not needed
+      if (h < pieces && k0 <= p_last && (k1 >= lo || k0 < a.sinks))
         next[h] = __ldg(a.b.table + static_cast<int64_t>(it.s) * a.b.table_cols + (k0 >> a.c.page_shift));
-      else
-        next[h] = -2;                      // not needed
     }
   };
   auto item = [&]() {
@@ -173,7 +171,9 @@ __device__ __forceinline__ void produce(const CUtensorMap* tm_k, const CUtensorM
   unsigned long long since = global_timer();
   while (__any_sync(0xFFFFFFFFu, active)) {
     if (active && mbar_test(empty + 8 * slot, phase)) {
-      const int page[2] = {next[0], next[1]};
+      int page[S::kPieces];
+#pragma unroll
+      for (int h = 0; h < S::kPieces; ++h) page[h] = next[h];
       const int key0 = it.kb.at(it.b) << S::kKeyShift, head = it.head;
       if (++it.b < it.end)
         look(it.b);
@@ -182,22 +182,24 @@ __device__ __forceinline__ void produce(const CUtensorMap* tm_k, const CUtensorM
       else
         active = false;
       const uint32_t bar = full + 8 * slot, to = ring + slot * S::kStage, ex = exps + slot * S::kExp;
-      bool on[2];
+      bool on[S::kPieces];
+      int loads = 0;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
+      for (int h = 0; h < S::kPieces; ++h) {
         on[h] = page_there(page[h], a.c.n_pages);
         if (!on[h] && page[h] != -2) report_error(a.status, DS_VIT_ERANGE);
+        loads += on[h];
       }
-      mbar_expect_tx(bar, (S::kStage + S::kExp) / halves * (on[0] + on[1]));
+      mbar_expect_tx(bar, (S::kStage + S::kExp) / pieces * loads);
 #pragma unroll
-      for (int h = 0; h < (E4M3 ? 2 : 1); ++h) {
+      for (int h = 0; h < S::kPieces; ++h) {
         if (!on[h]) continue;
-        const int row = static_cast<int>(cache_row(a.c, page[h], head, key0 + h * kPage16));
+        const int row = static_cast<int>(cache_row(a.c, page[h], head, key0 + h * step));
         if constexpr (E4M3) {
-          tma_load_2d(to + h * kPage16 * S::kRow, tm_k, bar, 0, row);
-          tma_load_2d(to + S::kTile + h * kPage16 * S::kRow, tm_v, bar, 0, row);
-          bulk_load(ex + h * kPage16, a.c.k_exp + row, 32 / halves, bar);
-          bulk_load(ex + 32 + h * kPage16, a.c.v_exp + row, 32 / halves, bar);
+          tma_load_2d(to + h * step * S::kRow, tm_k, bar, 0, row);
+          tma_load_2d(to + S::kTile + h * step * S::kRow, tm_v, bar, 0, row);
+          bulk_load(ex + h * step, a.c.k_exp + row, step, bar);
+          bulk_load(ex + S::kKeys + h * step, a.c.v_exp + row, step, bar);
         } else {
 #pragma unroll
           for (int x = 0; x < D / 64; ++x) {
@@ -392,41 +394,42 @@ __global__ void __launch_bounds__(Shape<D, E4M3>::kThreads, 1)
         fence_proxy_async_smem();          // before the loads that will follow into the tile
         __syncwarp();
       }
-      // ---- the block's fragments, all at once; then the stage is free again
-      constexpr int kWords = E4M3 ? D / 4 : D / 4;
+      // ---- S = Q K^T, 16 rows x kKeys keys.  bf16: the block's fragments, all at once,
+      // then the stage is free again; e4m3: key tile by key tile, the values later.
+      constexpr int kWords = E4M3 ? 1 : D / 4;
       uint32_t kw[kWords], vw[kWords], ke[kN], ve[kN];
+      float sc[kN][4];
+#pragma unroll
+      for (int n = 0; n < kN; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sc[n][e] = 0.f;
+      auto release = [&]() {
+        // The reads come before the loads that the stage's return lets in.
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(empty + 8 * slot);
+        if (++slot == S::kStages) {
+          slot = 0;
+          phase ^= 1;
+        }
+      };
       if constexpr (E4M3) {
-        // kw[n * kSteps + 4 h + x]: word x of piece h of key 8n + g
 #pragma unroll
         for (int n = 0; n < kN; ++n) {
-          const int row = 8 * n + g;
+          ke[n] = lds_u16(ex + 8 * n + 2 * t);
+          ve[n] = lds_u16(ex + S::kKeys + 8 * n + 2 * t);
+        }
+#pragma unroll
+        for (int n = 0; n < kN; ++n) {
+          const int row = 8 * n + g;         // this lane's key of the tile
 #pragma unroll
           for (int h = 0; h < D / 64; ++h) {
             const uint32_t piece = D == 128 ? (2 * t + h) ^ (row & 7) : t ^ ((row >> 1) & 3);
             const uint4 w = lds128(tk + row * S::kRow + piece * 16);
-            const int x = n * kSteps + 4 * h;
-            kw[x] = w.x, kw[x + 1] = w.y, kw[x + 2] = w.z, kw[x + 3] = w.w;
-          }
-        }
-#pragma unroll
-        for (int n = 0; n < kN; ++n) {
-          ke[n] = lds_u16(ex + 8 * n + 2 * t);
-          ve[n] = lds_u16(ex + 32 + 8 * n + 2 * t);
-        }
-        // vw[(y * kN + n) * 2 + x]: word y of the row of key 8n + 2t + x
-#pragma unroll
-        for (int n = 0; n < kN; ++n) {
-#pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            const int row = 8 * n + 2 * t + x;
-            if constexpr (D == 128) {
-              const uint4 v = lds128(tv + row * S::kRow + ((g ^ (row & 7)) << 4));
-              vw[n * 2 + x] = v.x, vw[(kN + n) * 2 + x] = v.y, vw[(2 * kN + n) * 2 + x] = v.z,
-                         vw[(3 * kN + n) * 2 + x] = v.w;
-            } else {
-              const uint2 v = lds64(tv + row * S::kRow + (((g >> 1) ^ ((row >> 1) & 3)) << 4) + 8 * (g & 1));
-              vw[n * 2 + x] = v.x, vw[(kN + n) * 2 + x] = v.y;
-            }
+            mma<true>(sc[n], qf[4 * h], e4m3x2_to_f16x2(w.x & 0xFFFFu), e4m3x2_to_f16x2(w.x >> 16));
+            mma<true>(sc[n], qf[4 * h + 1], e4m3x2_to_f16x2(w.y & 0xFFFFu), e4m3x2_to_f16x2(w.y >> 16));
+            mma<true>(sc[n], qf[4 * h + 2], e4m3x2_to_f16x2(w.z & 0xFFFFu), e4m3x2_to_f16x2(w.z >> 16));
+            mma<true>(sc[n], qf[4 * h + 3], e4m3x2_to_f16x2(w.w & 0xFFFFu), e4m3x2_to_f16x2(w.w >> 16));
           }
         }
       } else {
@@ -443,32 +446,12 @@ __global__ void __launch_bounds__(Shape<D, E4M3>::kThreads, 1)
           ldmatrix_x4_trans(tv + vr * 128 + (n >> 3) * S::kPlane + ((piece ^ (vr & 7)) << 4),
                             *reinterpret_cast<uint32_t(*)[4]>(vw + 2 * n));
         }
+        release();
+#pragma unroll
+        for (int k = 0; k < kSteps; ++k)
+#pragma unroll
+          for (int n = 0; n < kN; ++n) mma<false>(sc[n], qf[k], kw[4 * k + 2 * n], kw[4 * k + 2 * n + 1]);
       }
-      // The reads come before the loads that the stage's return lets in.
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(empty + 8 * slot);
-      if (++slot == S::kStages) {
-        slot = 0;
-        phase ^= 1;
-      }
-      // ---- S = Q K^T, 16 rows x kKeys keys
-      float sc[kN][4];
-#pragma unroll
-      for (int n = 0; n < kN; ++n)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) sc[n][e] = 0.f;
-#pragma unroll
-      for (int k = 0; k < kSteps; ++k)
-#pragma unroll
-        for (int n = 0; n < kN; ++n) {
-          if constexpr (E4M3) {
-            const uint32_t w = kw[n * kSteps + k];
-            mma<true>(sc[n], qf[k], e4m3x2_to_f16x2(w & 0xFFFFu), e4m3x2_to_f16x2(w >> 16));
-          } else {
-            mma<false>(sc[n], qf[k], kw[4 * k + 2 * n], kw[4 * k + 2 * n + 1]);
-          }
-        }
       // ---- softmax of the block: scores z = sc f (log2 units), f the scale and
       // the key's factor; contributions z + the value's exponent
       float f[kRowHalves][kN][2], add[kN][2], vf[kN][2], top[kRowHalves];
@@ -555,25 +538,37 @@ __global__ void __launch_bounds__(Shape<D, E4M3>::kThreads, 1)
         }
       }
       // ---- O += P V
+      if constexpr (E4M3) {
 #pragma unroll
-      for (int h = 0; h < kN / 2; ++h) {
-        if constexpr (E4M3) {
+        for (int h = 0; h < kN / 2; ++h) {
+          // w[4 y + x]: word y of the rows of keys 16h + 2t, + 1, + 8, + 9
+          uint32_t w[kCols];
 #pragma unroll
-          for (int y = 0; y < kCols / 4; ++y) {
-            const uint32_t* w = vw + (y * kN + 2 * h) * 2;      // keys 16h + 2t, + 1, + 8, + 9
+          for (int x = 0; x < 4; ++x) {
+            const int row = 16 * h + 8 * (x >> 1) + 2 * t + (x & 1);
+            if constexpr (D == 128) {
+              const uint4 v = lds128(tv + row * S::kRow + ((g ^ (row & 7)) << 4));
+              w[x] = v.x, w[4 + x] = v.y, w[8 + x] = v.z, w[12 + x] = v.w;
+            } else {
+              const uint2 v = lds64(tv + row * S::kRow + (((g >> 1) ^ ((row >> 1) & 3)) << 4) + 8 * (g & 1));
+              w[x] = v.x, w[4 + x] = v.y;
+            }
+          }
+#pragma unroll
+          for (int y = 0; y < kCols / 4; ++y)
 #pragma unroll
             for (int e = 0; e < 4; e += 2) {
               // Bytes e, e + 1 of both keys' words, side by side per dim.
               const uint32_t sel = e == 0 ? 0x5140u : 0x7362u;
-              const uint32_t p0 = __byte_perm(w[0], w[1], sel), p1 = __byte_perm(w[2], w[3], sel);
+              const uint32_t p0 = __byte_perm(w[4 * y], w[4 * y + 1], sel), p1 = __byte_perm(w[4 * y + 2], w[4 * y + 3], sel);
               mma<true>(o[4 * y + e], pf[h], e4m3x2_to_f16x2(p0 & 0xFFFFu), e4m3x2_to_f16x2(p1 & 0xFFFFu));
               mma<true>(o[4 * y + e + 1], pf[h], e4m3x2_to_f16x2(p0 >> 16), e4m3x2_to_f16x2(p1 >> 16));
             }
-          }
-        } else {
-#pragma unroll
-          for (int n = 0; n < kCols; ++n) mma<false>(o[n], pf[h], vw[2 * n], vw[2 * n + 1]);
         }
+        release();
+      } else {
+#pragma unroll
+        for (int n = 0; n < kCols; ++n) mma<false>(o[n], pf[0], vw[2 * n], vw[2 * n + 1]);
       }
     }
     if (dead) break;
@@ -716,7 +711,7 @@ int launch(const AttentionArgs& a, void* ws, cudaStream_t stream) {
   CUtensorMap tk, tv;
   const uint64_t rows = static_cast<uint64_t>(a.c.n_pages) * a.c.kv_heads << a.c.page_shift;
   const uint64_t cols = S::kRow / 2;      // in 16-bit units
-  const uint32_t box = E4M3 && a.c.page_shift > 4 ? 32 : 16;
+  const uint32_t box = std::min(1 << a.c.page_shift, S::kKeys);
   auto map = [&](CUtensorMap* m, const void* p) {
     return cols == 32 ? make_tmap_bf16_sw64(m, p, rows, cols, box) : make_tmap_bf16(m, p, rows, cols, box);
   };
@@ -738,7 +733,9 @@ int launch(const AttentionArgs& a, void* ws, cudaStream_t stream) {
 }  // namespace
 
 size_t cache_decode_workspace(int head_dim, int rows) {
-  const int warps = head_dim == 64 ? Shape<64, false>::kWarps : Shape<128, false>::kWarps;
+  // The larger of the two kinds': the size depends on head_dim and rows alone.
+  const int warps = head_dim == 64 ? std::max(Shape<64, false>::kWarps, Shape<64, true>::kWarps)
+                                   : std::max(Shape<128, false>::kWarps, Shape<128, true>::kWarps);
   return records_bytes(static_cast<int64_t>(num_sms()) * warps, std::min(rows, kRows), head_dim);
 }
 
