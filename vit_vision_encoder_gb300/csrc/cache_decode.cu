@@ -7,8 +7,8 @@
 // products run as warp MMAs (m16n8k16), whose fragments come straight from shared
 // memory; what counts is bytes in flight and a short chain of instructions per key.
 // Measured at 40 query and 8 K/V heads of 128: 32 sequences of 400 to 16000 tokens,
-// bf16, 87 us (5.8 TB/s; the loads alone 85); 64 of 2000 to 30000, e4m3, 246 us (5.6
-// TB/s; the loads alone 216, the rest is conversions and products of twice the keys
+// bf16, 87 us (5.8 TB/s; the loads alone 85); 64 of 2000 to 30000, e4m3, 224 us (6.1
+// TB/s, the loads alone 216: the rest is conversions and products of twice the keys
 // a byte); one of 1500 tokens 10.3 us, three quarters of it fixed (launches, plan, join).
 //
 // Work: the unit is a block of kKeys keys of one item (sequence, K/V head, 16
@@ -19,13 +19,14 @@
 // TMA tiles with its own running softmax; consumer warps never wait for one
 // another.  One producer warp per CTA fills the rings, lane i that of warp i
 // (issued by the consumers themselves, the loads took 660 of the 2260 cycles a
-// block of 16 keys cost a warp).  A consumer takes a stage's fragments into
+// block of 16 keys cost a warp).  bf16: a consumer takes a stage's fragments into
 // registers at once and gives the stage back before it computes.  Items that
 // lie within one worker's share are finished there, the others leave records
 // that join_kernel adds up.
 //
 // bf16: blocks of 16 keys (inside one page); S = Q K^T with K fragments by
-// ldmatrix, P V with V fragments by ldmatrix.trans.  e4m3: blocks of 32 keys; a
+// ldmatrix, P V with V fragments by ldmatrix.trans.  e4m3: blocks of 32 keys (64 at
+// head dim 64: 660 thousand tokens 137 us, 208 in blocks of 32); a
 // lane loads 16 bytes of a key (16 dims) or of two values' rows and widens
 // pairs to fp16 in registers (one conversion a pair, exact; bf16 has no such
 // conversion, and bit operations to the same end took five instructions a
@@ -133,11 +134,19 @@ __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint3
     mma_bf16(c, a, b0, b1);
 }
 
+// bf16, head dim 128: both 64-dim planes of a tile by one copy for pages up to this, by
+// two for larger ones.  64 sequences of 10 thousand tokens, one copy / two, us: pages of
+// 16 tokens 404 / 435, 32 403 / 414, 64 402 / 397, 128 404 / 389 (2.7 GB at 6.7 to 7.0 TB/s).
+constexpr int kPlanesShift = 5;
+
 // The producer warp: lane i loads the blocks of consumer warp i into its ring as
 // stages come free.  The lanes look at their rings in turn and stay together
 // (each waiting for its own ring, they fell apart and held one another up).
 // Lanes without a worker have an empty plan.  After two seconds without a free
-// stage a lane stops loading, and its consumer times out on its own.
+// stage a lane stops loading, and its consumer times out on its own.  The exponents
+// come by per-lane copies: a bulk or tensor copy costs the warp some 75 cycles a lane
+// (e4m3, head dim 128, 64 sequences of 10 thousand tokens, pages of 64 / 16 tokens: 240
+// / 384 us with bulk copies of the exponents, 224 / 311 so).
 template <int D, bool E4M3>
 __device__ __forceinline__ void produce(const CUtensorMap* tm_k, const CUtensorMap* tm_v, const AttentionArgs& a,
                                         const Plan& pl, uint32_t ring, uint32_t exps, uint32_t full, uint32_t empty) {
@@ -190,7 +199,7 @@ __device__ __forceinline__ void produce(const CUtensorMap* tm_k, const CUtensorM
         if (!on[h] && page[h] != -2) report_error(a.status, DS_VIT_ERANGE);
         loads += on[h];
       }
-      mbar_expect_tx(bar, (S::kStage + S::kExp) / pieces * loads);
+      mbar_expect_tx(bar, S::kStage / pieces * loads);
 #pragma unroll
       for (int h = 0; h < S::kPieces; ++h) {
         if (!on[h]) continue;
@@ -198,16 +207,24 @@ __device__ __forceinline__ void produce(const CUtensorMap* tm_k, const CUtensorM
         if constexpr (E4M3) {
           tma_load_2d(to + h * step * S::kRow, tm_k, bar, 0, row);
           tma_load_2d(to + S::kTile + h * step * S::kRow, tm_v, bar, 0, row);
-          bulk_load(ex + h * step, a.c.k_exp + row, step, bar);
-          bulk_load(ex + S::kKeys + h * step, a.c.v_exp + row, step, bar);
+          for (int i = 0; i < step; i += 16) {
+            cp_async_16(ex + h * step + i, a.c.k_exp + row + i, 16);
+            cp_async_16(ex + S::kKeys + h * step + i, a.c.v_exp + row + i, 16);
+          }
         } else {
+          if (D == 128 && a.c.page_shift <= kPlanesShift) {
+            tma_load_3d(to, tm_k, bar, 0, row, 0);
+            tma_load_3d(to + S::kTile, tm_v, bar, 0, row, 0);
+          } else {
 #pragma unroll
-          for (int x = 0; x < D / 64; ++x) {
-            tma_load_2d(to + S::kPlane * x, tm_k, bar, 64 * x, row);
-            tma_load_2d(to + S::kTile + S::kPlane * x, tm_v, bar, 64 * x, row);
+            for (int x = 0; x < D / 64; ++x) {
+              tma_load_2d(to + S::kPlane * x, tm_k, bar, 64 * x, row);
+              tma_load_2d(to + S::kTile + S::kPlane * x, tm_v, bar, 64 * x, row);
+            }
           }
         }
       }
+      if constexpr (E4M3) cp_async_arrive(bar);
       if (++slot == S::kStages) {
         slot = 0;
         phase ^= 1;
@@ -218,6 +235,7 @@ __device__ __forceinline__ void produce(const CUtensorMap* tm_k, const CUtensorM
       active = false;
     }
   }
+  if constexpr (E4M3) cp_async_wait<0>();   // no copy lands after the CTA has exited
 }
 
 // kRowHalves: 1 when at most 8 rows share a K/V head (rows 8 .. 15 of the
@@ -248,7 +266,10 @@ __global__ void __launch_bounds__(Shape<D, E4M3>::kThreads, 1)
 
   if (warp == kWarps) {
     if (lane < kWarps)
-      for (int i = 0; i < 2 * S::kStages; ++i) mbar_init(full_of(lane) + 8 * i, 1);
+      for (int i = 0; i < S::kStages; ++i) {
+        mbar_init(full_of(lane) + 8 * i, E4M3 ? 2 : 1);     // the tiles' bytes, the exponents' copies
+        mbar_init(empty_of(lane) + 8 * i, 1);
+      }
     if (lane == 0) {
       prefetch_tensormap(&tm_k);
       prefetch_tensormap(&tm_v);
@@ -713,6 +734,7 @@ int launch(const AttentionArgs& a, void* ws, cudaStream_t stream) {
   const uint64_t cols = S::kRow / 2;      // in 16-bit units
   const uint32_t box = std::min(1 << a.c.page_shift, S::kKeys);
   auto map = [&](CUtensorMap* m, const void* p) {
+    if (cols == 128 && a.c.page_shift <= kPlanesShift) return make_tmap_bf16_planes(m, p, rows, box);
     return cols == 32 ? make_tmap_bf16_sw64(m, p, rows, cols, box) : make_tmap_bf16(m, p, rows, cols, box);
   };
   if (!map(&tk, a.c.k) || !map(&tv, a.c.v)) return DS_VIT_ECUDA;

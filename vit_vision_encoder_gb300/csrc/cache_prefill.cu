@@ -386,7 +386,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
       mbar_init(bar(kBarKvEmpty + i), 1);
     }
     for (int i = 0; i < C::kRaw; ++i) {
-      mbar_init(bar(kBarRawFull + i), 1);
+      mbar_init(bar(kBarRawFull + i), 33);       // the tile's bytes, the lanes' copies of exponents
       mbar_init(bar(kBarRawEmpty + i), 4);
     }
     for (int i = 0; i < kJobs; ++i) {
@@ -472,21 +472,22 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
           if (!ok) break;
           const bool fix = !E4M3 && kv == 1 && !whole;
           const uint32_t full = fix ? bar(kBarRagged) : bar(kFull + slot);
-          const uint32_t per = page * D * (E4M3 ? 1 : 2) + (E4M3 ? page : 0);
+          const uint32_t per = page * D * (E4M3 ? 1 : 2);
           if (lane == 0) mbar_expect_tx(full, loaded * per);
           __syncwarp();
           if (on) {
             const CUtensorMap* tm = kv == 0 ? &tm_k : &tm_v;
             if constexpr (E4M3) {
               tma_load_2d(sRaw(slot) + lane * page * D, tm, full, 0, row);
-              bulk_load(base + C::kOffExp + slot * kTile + lane * page, (kv == 0 ? a.c.k_exp : a.c.v_exp) + row, page,
-                        full);
+              const uint8_t* from = (kv == 0 ? a.c.k_exp : a.c.v_exp) + row;
+              for (int i = 0; i < page; i += 16) cp_async_16(base + C::kOffExp + slot * kTile + lane * page + i, from + i, 16);
             } else {
 #pragma unroll
               for (int h = 0; h < kHalves; ++h)
                 tma_load_2d(sKv(slot) + h * C::kHalf + lane * page * 128, tm, full, 64 * h, row);
             }
           }
+          if constexpr (E4M3) cp_async_arrive(full);
           __syncwarp();
           if (fix) {
             ok = __all_sync(0xFFFFFFFFu, mbar_wait(bar(kBarRagged), ragged & 1, a.status));
@@ -511,6 +512,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
         if (!ok) break;
       }
     }
+    if constexpr (E4M3) cp_async_wait<0>();  // no copy lands after the CTA has exited
   } else if (warp == kWarpJobs) {
     // ------------------------------------------------------------ the items
     if (lane == 0) {

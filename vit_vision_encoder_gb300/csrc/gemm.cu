@@ -568,6 +568,16 @@ bool make_tmap_bf16_sw64(CUtensorMap* map, const void* base, uint64_t rows, uint
   return encode_tmap(map, base, rows, cols, 32, box_rows, CU_TENSOR_MAP_SWIZZLE_64B);
 }
 
+bool make_tmap_bf16_planes(CUtensorMap* map, const void* base, uint64_t rows, uint32_t box_rows) {
+  const PFN_cuTensorMapEncodeTiled_v12000 encode = tmap_encoder();
+  if (!encode || !base || rows == 0 || (reinterpret_cast<uintptr_t>(base) & 15) != 0) return false;
+  const cuuint64_t dims[3] = {64, rows, 2}, strides[2] = {256, 128};
+  const cuuint32_t box[3] = {64, box_rows, 2}, step[3] = {1, 1, 1};
+  return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, step,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 bool make_tmap_store_bf16(CUtensorMap* map, void* base, uint64_t rows, uint64_t cols) {
   return encode_tmap(map, base, rows, cols, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B);
 }

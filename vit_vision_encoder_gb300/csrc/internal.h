@@ -55,6 +55,10 @@ bool make_tmap_bf16_tail16(CUtensorMap* map, const void* base, uint64_t rows, ui
 // A matrix of 32 columns (rows of 64 B): boxes [box_rows, 32 cols], 64-byte swizzle.
 bool make_tmap_bf16_sw64(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols, uint32_t box_rows);
 
+// A matrix of 128 columns as two planes of 64 (coordinates: column, row, plane): boxes
+// [2 planes, box_rows, 64 cols], plane after plane, 128-byte swizzle.
+bool make_tmap_bf16_planes(CUtensorMap* map, const void* base, uint64_t rows, uint32_t box_rows);
+
 // Store map of a row-major bf16 output [rows, cols]: 32x32 boxes, 64-byte swizzle.
 bool make_tmap_store_bf16(CUtensorMap* map, void* base, uint64_t rows, uint64_t cols);
 
