@@ -546,6 +546,36 @@ def test_attention_of_larger_calls(dv, q, kv, heads, kv_heads, dim, page, kind, 
     assert not bad.any(), f"{bad.sum()} of {bad.size} outside, worst {np.nanmax(err / tol)} at {np.argwhere(bad)[:3].tolist()}"
 
 
+COLD = [
+    # q, kv, heads, kv_heads, page
+    ([3] * 12, [6000 + 7 * i for i in range(12)], 32, 4, 64),        # 24 rows a K/V head
+    ([1] * 24, [5000 - 90 * i for i in range(24)], 32, 4, 16),       # 8
+    ([16], [20000], 64, 2, 32),                                      # 512, one sequence
+    ([300, 41], [4000, 9000], 16, 2, 128),                           # whole tiles and a part of one
+]
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("q,kv,heads,kv_heads,page", COLD)
+def test_same_bits_from_cold_caches(dv, q, kv, heads, kv_heads, page, dim, kind):
+    """Pages that come late (nothing of them in L2) and early: every wait holds
+    whatever lands first, and the bits are the same."""
+    st = Setup(dv, q, kv, kv_heads, dim, page, kind, seed=dim + len(q), fill=math.nan)
+    x = st.queries(heads)
+    flush = torch.empty(300 << 20, dtype=torch.uint8, device="cuda")
+    first, status = dv.cache_attention(st.cache, st.chunks, x)
+    differ = torch.zeros((), dtype=torch.int64, device="cuda")
+    for i in range(24):
+        if i % 2 == 0:
+            flush.fill_(i)
+        got, _ = dv.cache_attention(st.cache, st.chunks, x, status=status)
+        differ += (got != first).sum()
+    torch.cuda.synchronize()
+    assert int(status.item()) == dv.OK
+    assert bool(torch.isfinite(first).all()) and int(differ.item()) == 0
+
+
 @pytest.mark.parametrize("rows,heads", [(1, 8), (40, 8)])
 def test_sequences_that_share_pages(dv, rows, heads):
     """Two sequences over the same pages (a common prompt) with the same queries

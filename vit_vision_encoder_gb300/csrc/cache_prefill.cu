@@ -97,16 +97,19 @@ enum : int {
   kBarKvEmpty = 10,         // [8]
   kBarRawFull = 18,         // [4]
   kBarRawEmpty = 22,        // [4]
-  kBarSFull = 26,           // [3] by score tile
-  kBarPFull = 29,           // [2]
-  kBarPvDone = 31,          // [2]
-  kBarRagged = 33,          // a value tile with rows to zero has landed
-  kBarDrain = 34,
-  kBarJobFull = 35,         // [4]
-  kBarJobEmpty = 39,        // [4]
-  kBarOther = 43,           // tile B's share of the keys is summed up
-  kBarMerged = 44,          // and has been read
-  kBarCount = 45
+  // By score tile, whose next scores wait for the product of its last weights: with
+  // three of them a softmax may be two steps ahead of the issuer, which a barrier by
+  // query tile would lose count of.
+  kBarSFull = 26,           // [3]
+  kBarPFull = 29,           // [3]
+  kBarPvDone = 32,          // [2]
+  kBarRagged = 34,          // a value tile with rows to zero has landed
+  kBarDrain = 35,
+  kBarJobFull = 36,         // [4]
+  kBarJobEmpty = 40,        // [4]
+  kBarOther = 44,           // tile B's share of the keys is summed up
+  kBarMerged = 45,          // and has been read
+  kBarCount = 46
 };
 
 struct PrefillArgs {
@@ -377,10 +380,12 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
   if (threadIdx.x == 0) {
     for (int x = 0; x < 2; ++x) {
       mbar_init(bar(kBarQ + x), 256);
-      mbar_init(bar(kBarPFull + x), 256);
       mbar_init(bar(kBarPvDone + x), 1);
     }
-    for (int i = 0; i < C::kScores; ++i) mbar_init(bar(kBarSFull + i), 1);
+    for (int i = 0; i < C::kScores; ++i) {
+      mbar_init(bar(kBarSFull + i), 1);
+      mbar_init(bar(kBarPFull + i), 256);
+    }
     for (int i = 0; i < C::kRing; ++i) {
       mbar_init(bar(kBarKvFull + i), E4M3 ? 4 : 1);
       mbar_init(bar(kBarKvEmpty + i), 1);
@@ -615,9 +620,10 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
         for (int n = 0; ok && n < products; ++n) {
           const int x = n & 1, i = (both ? n & ~1 : 2 * n) + 1;
           const uint32_t step = x == 0 ? step0++ : step1++;
-          ok = filled(i) && wait(kBarPFull + x, step & 1);
+          const int score = (seq + n) % 3;
+          ok = filled(i) && wait(kBarPFull + score, ((seq + n) / 3) & 1);
           if (!ok) break;
-          issue_pv(x, at(i), n < 2, (seq + n) % 3);
+          issue_pv(x, at(i), n < 2, score);
           if (!both || x == 1) {
             release(at(i));
             used = base + i + 1;
@@ -939,7 +945,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
         }
         tmem_wait_st();
         tc_fence_before();
-        mbar_arrive(bar(kBarPFull + x));
+        mbar_arrive(bar(kBarPFull + at));
         m = m_new;
       }
       if (!ok || !mbar_wait(bar(kBarPvDone + x), (step - 1) & 1, a.status)) {
