@@ -552,6 +552,8 @@ COLD = [
     ([1] * 24, [5000 - 90 * i for i in range(24)], 32, 4, 16),       # 8
     ([16], [20000], 64, 2, 32),                                      # 512, one sequence
     ([300, 41], [4000, 9000], 16, 2, 128),                           # whole tiles and a part of one
+    ([8 + 9 * i % 76 for i in range(56)], [90 + 41 * i % 537 for i in range(56)], 64, 4, 32),   # one key tile and several, in turn
+    ([3] * 200, [3 + 7 * i % 300 for i in range(200)], 42, 2, 16),   # 63 rows over one to three key tiles
 ]
 
 

@@ -35,7 +35,7 @@
 //
 // An item of at most 128 rows leaves tile B without rows of its own: it then
 // takes the same rows and every other key tile, and the two results are added up
-// in TMEM (32 sequences of 8000 tokens, 32 rows, bf16, D 64: 130 us without, 104
+// in TMEM (32 sequences of 8000 tokens, 32 rows, bf16, D 64: 130 us without, 106
 // with).
 //
 // e4m3 pages: warps 20-27 widen the raw tiles to fp16 in shared memory (the
@@ -806,6 +806,16 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
       seq += R - w.rho0 <= kTile ? count : 2 * count;
       if (rho0 >= R || b0 >= w.end) {
         tile += count;
+        if constexpr (C::kScores == 3) {
+          // Nothing for B here; it waits for A all the same.  Score tiles go round between
+          // the two, and a wait of B's must not come before A's use of the tile is complete.
+          mbar_arrive(bar(kBarOther));
+          if (!mbar_wait(bar(kBarMerged), merges & 1, a.status)) {
+            ok = false;
+            break;
+          }
+          ++merges;
+        }
         continue;
       }
       const int first = w.q.kv - w.q.c;
@@ -959,8 +969,8 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
       l += __shfl_xor_sync(0xFFFFFFFFu, l, 16);
       tile += count;
       float fa = 1.f, fb = 0.f;              // what the tiles' outputs are weighed by
-      const bool two = shared && count > 1;
-      if (two) {
+      const bool two = shared && count > 1, paired = shared && (two || C::kScores == 3);
+      if (paired) {
         if (x == 1) {
           if (h == 0) other[r] = make_float2(m, l);
           tc_fence_before();
@@ -979,12 +989,14 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
         }
         ++merges;
         tc_fence_after();
-        const float2 ml = other[r];
-        const float mb = ml.x, top = fmaxf(m, mb);
-        fa = m == top ? 1.f : exp2f(m - top);
-        fb = mb == top ? 1.f : exp2f(mb - top);
-        l = l * fa + ml.y * fb;
-        m = top;
+        if (two) {
+          const float2 ml = other[r];
+          const float mb = ml.x, top = fmaxf(m, mb);
+          fa = m == top ? 1.f : exp2f(m - top);
+          fb = mb == top ? 1.f : exp2f(mb - top);
+          l = l * fa + ml.y * fb;
+          m = top;
+        }
       }
       // Columns col .. of the row's output (kCols of each half of the dims).
       auto load_o = [&](auto cols, int col, uint32_t* o) {
@@ -1069,7 +1081,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
         }
       }
       tc_fence_before();
-      if (two) mbar_arrive(bar(kBarMerged));
+      if (paired) mbar_arrive(bar(kBarMerged));
       __syncwarp();                          // the rows' places are free for the next item's
       while (redo) {
         const int y = __ffs(static_cast<int>(redo)) - 1;

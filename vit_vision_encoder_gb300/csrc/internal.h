@@ -209,9 +209,9 @@ size_t cache_prefill_workspace(int head_dim);
 int launch_cache_prefill(const AttentionArgs& a, int head_dim, bool e4m3, void* ws, cudaStream_t stream);
 // The path for few query rows per K/V head and sequence, 16 at a time: at most
 // decode_rows.  Measured on 32 sequences of 8000 tokens and 8 K/V heads, us, this
-// path against the other: 16 rows bf16 171 / 182 (head dim 64: 108 / 103), e4m3 112
-// / 208 (102 / 125); 24 to 32 rows bf16 319 / 183 (194 / 103), e4m3 197 / 210 (175
-// / 126); 40 rows e4m3 287 / 210.
+// path against the other: 16 rows bf16 166 / 181 (head dim 64: 103 / 105), e4m3 107
+// / 207 (83 / 127); 24 to 32 rows bf16 314 / 182 (187 / 106), e4m3 190 / 208 (139
+// / 127); 40 rows e4m3 279 / 209.
 inline int decode_rows(int head_dim, bool e4m3) { return e4m3 && head_dim == 128 ? 32 : 16; }
 size_t cache_decode_workspace(int head_dim, int rows);
 int launch_cache_decode(const AttentionArgs& a, int head_dim, bool e4m3, void* ws, cudaStream_t stream);
