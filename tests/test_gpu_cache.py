@@ -259,6 +259,22 @@ def test_write_and_read(dv, q, kv, kv_heads, dim, page, kind, front, back):
             assert np.array_equal(got[st.off[s]:st.off[s + 1]], ref)
 
 
+MANY_ROWS = [
+    # More rows than run at once and few heads: several tokens a warp.
+    ([9000, 3000], [9000, 3500], 1, 128, 64, "e4m3", 0, 0),
+    ([11000], [11001], 1, 64, 16, "bf16", 3, 7),
+    ([20] * 600, [20 + i % 50 for i in range(600)], 2, 64, 32, "e4m3", 5, 1),
+    ([17, 0, 40, 1] * 250, [9, 3, 57, 64] * 250, 3, 64, 128, "bf16", 1, 200),    # rows in front of position 0
+    ([5000, 0, 4999], [5000, 0, 6000], 4, 128, 32, "e4m3", 0, 40),
+    ([10007], [10007], 7, 64, 16, "e4m3", 2, 2),
+]
+
+
+@pytest.mark.parametrize("q,kv,kv_heads,dim,page,kind,front,back", MANY_ROWS)
+def test_write_and_read_of_many_rows(dv, q, kv, kv_heads, dim, page, kind, front, back):
+    test_write_and_read(dv, q, kv, kv_heads, dim, page, kind, front, back)
+
+
 def test_write_e4m3_special_values(dv):
     """Zeros, every bf16 magnitude as a row's largest, ties, values far below the
     largest, infinities and NaN."""

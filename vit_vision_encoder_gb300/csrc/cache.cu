@@ -4,7 +4,8 @@
 // Both kernels move each byte once and are bound by memory at prompt lengths,
 // by their chain of dependent loads (row -> sequence -> page -> slot) at one
 // token a sequence.  One warp takes one token: its keys and values of all
-// heads are two contiguous runs of the packed rows, read as 16-byte pieces.
+// heads are two contiguous runs of the packed rows, read as 16-byte pieces (few
+// heads and many rows: several tokens, cache_read_tokens_kernel).
 // Measured at 8 heads of 128: 6900 rows quantised as they are written 11.8 us (53% of
 // the rate of a plain copy, pieces of 128 bytes scattered over the pages), 92 thousand
 // tokens read back out of e4m3 pages 86 us (98%), 48 single tokens 2.5 us.
@@ -46,6 +47,36 @@ __device__ __forceinline__ uint32_t e4m3x2(uint32_t two, float f) {
   uint16_t r;
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(bf16hi(two) * f), "f"(bf16lo(two) * f));
   return r;
+}
+
+// One 16-byte piece w of a row of keys (x 0) or values into its place; the lanes of
+// the row's other pieces are beside this one, and all lanes of the warp take part.
+template <int D, bool E4M3>
+__device__ __forceinline__ void write_piece(const CacheView& c, int x, int64_t row, int piece, bool on, uint4 w) {
+  constexpr int kLanes = D / 8;
+  uint8_t* to = x == 0 ? c.k : c.v;
+  if constexpr (!E4M3) {
+    if (on) reinterpret_cast<uint4*>(to)[row * kLanes + piece] = w;
+  } else {
+    uint32_t a = max_abs_bits(w);
+#pragma unroll
+    for (int o = kLanes / 2; o > 0; o >>= 1) a = max(a, __shfl_xor_sync(0xFFFFFFFFu, a, o));
+    const uint32_t byte = exponent_byte(a);
+    const float f = __uint_as_float((254u - byte) << 23);    // 2^-e
+    uint2 y = make_uint2(e4m3x2(w.x, f) | e4m3x2(w.y, f) << 16, e4m3x2(w.z, f) | e4m3x2(w.w, f) << 16);
+    if (byte >= 247u) {
+      if (byte == 255u) {
+        y = make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu);
+      } else {                                               // magnitudes 256 (0x78) end at 240 (0x77)
+        y.x -= __vcmpgtu4(y.x & 0x7F7F7F7Fu, 0x77777777u) & 0x01010101u;
+        y.y -= __vcmpgtu4(y.y & 0x7F7F7F7Fu, 0x77777777u) & 0x01010101u;
+      }
+    }
+    if (on) {
+      reinterpret_cast<uint2*>(to)[row * kLanes + piece] = y;
+      if (piece == 0) (x == 0 ? c.k_exp : c.v_exp)[row] = static_cast<uint8_t>(byte);
+    }
+  }
 }
 
 // Every sequence's entries are checked, also those of sequences without rows.
@@ -98,36 +129,14 @@ __global__ void __launch_bounds__(32 * kWarps)
     if (hb > 0) load(hb);
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
-      uint8_t* to = x == 0 ? c.k : c.v;
 #pragma unroll
       for (int t = 0; t < kPieces; ++t) {
         const int h = hb + t * kHeads;                             // head of the warp's first lanes
         const int64_t row = row0 + (static_cast<int64_t>(h) << c.page_shift);
         const bool on = h + h0 < c.kv_heads;
         const uint4 w = u[x][t];
-        if constexpr (!E4M3) {
-          if (on) reinterpret_cast<uint4*>(to)[row * kLanes + piece] = w;
-        } else {
-          if (h >= c.kv_heads) break;
-          uint32_t a = max_abs_bits(w);
-#pragma unroll
-          for (int o = kLanes / 2; o > 0; o >>= 1) a = max(a, __shfl_xor_sync(0xFFFFFFFFu, a, o));
-          const uint32_t byte = exponent_byte(a);
-          const float f = __uint_as_float((254u - byte) << 23);    // 2^-e
-          uint2 y = make_uint2(e4m3x2(w.x, f) | e4m3x2(w.y, f) << 16, e4m3x2(w.z, f) | e4m3x2(w.w, f) << 16);
-          if (byte >= 247u) {
-            if (byte == 255u) {
-              y = make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu);
-            } else {                                               // magnitudes 256 (0x78) end at 240 (0x77)
-              y.x -= __vcmpgtu4(y.x & 0x7F7F7F7Fu, 0x77777777u) & 0x01010101u;
-              y.y -= __vcmpgtu4(y.y & 0x7F7F7F7Fu, 0x77777777u) & 0x01010101u;
-            }
-          }
-          if (on) {
-            reinterpret_cast<uint2*>(to)[row * kLanes + piece] = y;
-            if (piece == 0) (x == 0 ? c.k_exp : c.v_exp)[row] = static_cast<uint8_t>(byte);
-          }
-        }
+        if (E4M3 && h >= c.kv_heads) break;
+        write_piece<D, E4M3>(c, x, row, piece, on, w);
       }
     }
   }
@@ -136,6 +145,28 @@ __global__ void __launch_bounds__(32 * kWarps)
 __device__ __forceinline__ uint32_t e4m3x2_to_bf16x2(uint32_t two, float f) {
   const float2 x = e4m3x2_to_float2(static_cast<uint16_t>(two));
   return pack_bf16x2(x.x * f, x.y * f);   // exact: 4 significant bits, a normal exponent
+}
+
+// What a piece of a row of keys or values holds, and the row's exponent byte.
+template <int D, bool E4M3>
+__device__ __forceinline__ void read_piece(const CacheView& c, int x, int64_t row, int piece, uint4& u, uint32_t& byte) {
+  constexpr int kLanes = D / 8;
+  const uint8_t* from = x == 0 ? c.k : c.v;
+  if constexpr (!E4M3) {
+    u = reinterpret_cast<const uint4*>(from)[row * kLanes + piece];
+  } else {
+    const uint2 w = reinterpret_cast<const uint2*>(from)[row * kLanes + piece];
+    u.x = w.x;
+    u.y = w.y;
+    byte = (x == 0 ? c.k_exp : c.v_exp)[row];
+  }
+}
+template <bool E4M3>
+__device__ __forceinline__ uint4 as_bf16(uint4 w, uint32_t byte) {
+  if constexpr (!E4M3) return w;
+  const float f = exp_factor(byte);
+  return make_uint4(e4m3x2_to_bf16x2(w.x & 0xFFFFu, f), e4m3x2_to_bf16x2(w.x >> 16, f),
+                    e4m3x2_to_bf16x2(w.y & 0xFFFFu, f), e4m3x2_to_bf16x2(w.y >> 16, f));
 }
 
 // The inverse: rows of the packed outputs from the pages.  Rows in front of
@@ -165,7 +196,6 @@ __global__ void __launch_bounds__(32 * kWarps)
     uint32_t byte[2][kPieces];
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
-      const uint8_t* from = x == 0 ? c.k : c.v;
 #pragma unroll
       for (int t = 0; t < kPieces; ++t) {
         const int h = hb + t * kHeads;
@@ -173,14 +203,7 @@ __global__ void __launch_bounds__(32 * kWarps)
         u[x][t] = make_uint4(0, 0, 0, 0);
         byte[x][t] = 127;
         if (h + h0 < c.kv_heads && page >= 0) {
-          if constexpr (!E4M3) {
-            u[x][t] = reinterpret_cast<const uint4*>(from)[row * kLanes + piece];
-          } else {
-            const uint2 w = reinterpret_cast<const uint2*>(from)[row * kLanes + piece];
-            u[x][t].x = w.x;
-            u[x][t].y = w.y;
-            byte[x][t] = (x == 0 ? c.k_exp : c.v_exp)[row];
-          }
+          read_piece<D, E4M3>(c, x, row, piece, u[x][t], byte[x][t]);
         }
       }
     }
@@ -190,16 +213,116 @@ __global__ void __launch_bounds__(32 * kWarps)
 #pragma unroll
       for (int t = 0; t < kPieces; ++t) {
         if (hb + t * kHeads + h0 >= c.kv_heads) continue;
-        uint4 w = u[x][t];
-        if constexpr (E4M3) {
-          const float f = exp_factor(byte[x][t]);
-          w = make_uint4(e4m3x2_to_bf16x2(w.x & 0xFFFFu, f), e4m3x2_to_bf16x2(w.x >> 16, f),
-                         e4m3x2_to_bf16x2(w.y & 0xFFFFu, f), e4m3x2_to_bf16x2(w.y >> 16, f));
-        }
-        to[32 * t] = w;
+        to[32 * t] = as_bf16<E4M3>(u[x][t], byte[x][t]);
       }
     }
   }
+}
+
+// Few K/V heads leave most of a warp's places for pieces empty; where the rows are
+// more than run at once, a warp then takes several tokens in a row: place y holds
+// head y % kv_heads of token y / kv_heads.  92 thousand tokens, one token a warp / several,
+// us, e4m3: one head of 128 read 36.6 / 12.9, written 35.3 / 16.6, four heads of 64 (four
+// tokens) 41.1 / 26.8 and 36.7 / 32.4; two tokens at a time gain nothing (51 / 49, 53 / 60).
+struct Place {
+  int r, head;     // packed row; r < 0: nothing here
+  int64_t row;     // in the pages; < 0: in front of position 0
+};
+
+__device__ __forceinline__ Place place_of(const CacheView& c, const ChunkView& b, int first, int tokens, int y, int s,
+                                          int* status) {
+  const Place none{-1, 0, -1};
+  const int i = y / c.kv_heads, r = first + i;
+  if (i >= tokens || r >= b.rows) return none;
+  while (s + 1 < b.n && r >= __ldg(b.row_off + s + 1)) ++s;
+  const Seq q = load_seq(b, c.page_shift, s, status);
+  if (!has_row(q, r)) return none;
+  const int pos = q.kv - q.c + (r - q.row0), head = y - i * c.kv_heads;
+  if (pos < 0) return Place{r, head, -1};
+  const int64_t page = page_of(b, c, s, pos, status);
+  return page < 0 ? none : Place{r, head, cache_row(c, page, head, pos)};
+}
+
+// The sequence to look from for rows first, first + 1, ...; -1 if all of them lie behind the last.
+__device__ __forceinline__ int seq_from(const ChunkView& b, int first, int lane) {
+  const int s = find_seq(b, first, lane);
+  return s >= 0 || first >= __ldg(b.row_off) ? s : 0;
+}
+
+template <int D, bool E4M3>
+__global__ void __launch_bounds__(32 * kWarps)
+    cache_write_tokens_kernel(const __grid_constant__ CacheView c, const __grid_constant__ ChunkView b,
+                              const bf16* __restrict__ k, int64_t k_stride, const bf16* __restrict__ v,
+                              int64_t v_stride, int tokens, int* status) {
+  constexpr int kLanes = D / 8, kHeads = 32 / kLanes;
+  grid_dep_launch();
+  grid_dep_wait();
+  const int lane = threadIdx.x & 31, piece = lane % kLanes, h0 = lane / kLanes;
+  const int first = (static_cast<int>(blockIdx.x) * kWarps + (threadIdx.x >> 5)) * tokens;
+  check_seqs(b, c.page_shift, status);
+  if (first >= b.rows) return;
+  uint4 u[2][kPieces];
+#pragma unroll
+  for (int t = 0; t < kPieces; ++t) {
+    const int y = t * kHeads + h0, i = y / c.kv_heads, r = first + i;
+    const int at = (y - i * c.kv_heads) * D + piece * 8;
+    const bool on = i < tokens && r < b.rows;
+    u[0][t] = on ? __ldg(reinterpret_cast<const uint4*>(k + r * k_stride + at)) : make_uint4(0, 0, 0, 0);
+    u[1][t] = on ? __ldg(reinterpret_cast<const uint4*>(v + r * v_stride + at)) : make_uint4(0, 0, 0, 0);
+  }
+  const int s = seq_from(b, first, lane);
+  if (s < 0) return;
+  Place to[kPieces];
+#pragma unroll
+  for (int t = 0; t < kPieces; ++t) to[t] = place_of(c, b, first, tokens, t * kHeads + h0, s, status);
+  __syncwarp();
+#pragma unroll
+  for (int t = 0; t < kPieces; ++t)
+#pragma unroll
+    for (int x = 0; x < 2; ++x) write_piece<D, E4M3>(c, x, to[t].row, piece, to[t].r >= 0 && to[t].row >= 0, u[x][t]);
+}
+
+template <int D, bool E4M3>
+__global__ void __launch_bounds__(32 * kWarps)
+    cache_read_tokens_kernel(const __grid_constant__ CacheView c, const __grid_constant__ ChunkView b,
+                             bf16* __restrict__ k, int64_t k_stride, bf16* __restrict__ v, int64_t v_stride, int tokens,
+                             int* status) {
+  constexpr int kLanes = D / 8, kHeads = 32 / kLanes;
+  grid_dep_launch();
+  grid_dep_wait();
+  const int lane = threadIdx.x & 31, piece = lane % kLanes, h0 = lane / kLanes;
+  const int first = (static_cast<int>(blockIdx.x) * kWarps + (threadIdx.x >> 5)) * tokens;
+  check_seqs(b, c.page_shift, status);
+  if (first >= b.rows) return;
+  const int s = seq_from(b, first, lane);
+  if (s < 0) return;
+  Place from[kPieces];
+#pragma unroll
+  for (int t = 0; t < kPieces; ++t) from[t] = place_of(c, b, first, tokens, t * kHeads + h0, s, status);
+  uint4 u[2][kPieces];
+  uint32_t byte[2][kPieces];
+#pragma unroll
+  for (int t = 0; t < kPieces; ++t)
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      u[x][t] = make_uint4(0, 0, 0, 0);
+      byte[x][t] = 127;
+      if (from[t].row >= 0) read_piece<D, E4M3>(c, x, from[t].row, piece, u[x][t], byte[x][t]);
+    }
+#pragma unroll
+  for (int t = 0; t < kPieces; ++t) {
+    if (from[t].r < 0) continue;
+    const int at = from[t].head * D + piece * 8;
+    *reinterpret_cast<uint4*>(k + from[t].r * k_stride + at) = as_bf16<E4M3>(u[0][t], byte[0][t]);
+    *reinterpret_cast<uint4*>(v + from[t].r * v_stride + at) = as_bf16<E4M3>(u[1][t], byte[1][t]);
+  }
+}
+
+// Tokens a warp takes: one, or as many as its places hold (four at least) where the
+// rows are more warps than the device runs at once.
+int tokens_per_warp(int head_dim, int kv_heads, int64_t rows) {
+  const int places = kPieces * 32 / (head_dim / 8);
+  return rows > 64 * static_cast<int64_t>(num_sms()) && places >= 4 * kv_heads ? places / kv_heads : 1;
 }
 
 bool aligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
@@ -269,11 +392,20 @@ int ds_vit_cache_write(const ds_vit_cache* cache, const ds_vit_chunks* chunks, c
     return DS_VIT_EINVAL;
   if (rows == 0) return DS_VIT_OK;
   const bool e4m3 = cache->kind == DS_VIT_CACHE_E4M3;
+  const int tokens = tokens_per_warp(cache->head_dim, c.kv_heads, rows);
+  const dim3 grid(static_cast<unsigned>((rows + kWarps * tokens - 1) / (kWarps * tokens))), block(32 * kWarps);
+  auto* s = static_cast<cudaStream_t>(stream);
+  auto* kp = static_cast<const bf16*>(k);
+  auto* vp = static_cast<const bf16*>(v);
+  auto* st = reinterpret_cast<int*>(status);
+  if (tokens > 1) {
+    auto* fn = cache->head_dim == 128 ? (e4m3 ? cache_write_tokens_kernel<128, true> : cache_write_tokens_kernel<128, false>)
+                                      : (e4m3 ? cache_write_tokens_kernel<64, true> : cache_write_tokens_kernel<64, false>);
+    return launched(launch_pdl(fn, grid, block, 0, s, c, b, kp, k_stride, vp, v_stride, tokens, st));
+  }
   auto* fn = cache->head_dim == 128 ? (e4m3 ? cache_write_kernel<128, true> : cache_write_kernel<128, false>)
                                     : (e4m3 ? cache_write_kernel<64, true> : cache_write_kernel<64, false>);
-  return launched(launch_pdl(fn, dim3(static_cast<unsigned>((rows + kWarps - 1) / kWarps)), dim3(32 * kWarps), 0,
-                             static_cast<cudaStream_t>(stream), c, b, static_cast<const bf16*>(k), k_stride,
-                             static_cast<const bf16*>(v), v_stride, reinterpret_cast<int*>(status)));
+  return launched(launch_pdl(fn, grid, block, 0, s, c, b, kp, k_stride, vp, v_stride, st));
 }
 
 int ds_vit_cache_read(const ds_vit_cache* cache, const ds_vit_chunks* chunks, void* k, int64_t k_stride, void* v,
@@ -286,11 +418,20 @@ int ds_vit_cache_read(const ds_vit_cache* cache, const ds_vit_chunks* chunks, vo
     return DS_VIT_EINVAL;
   if (rows == 0) return DS_VIT_OK;
   const bool e4m3 = cache->kind == DS_VIT_CACHE_E4M3;
+  const int tokens = tokens_per_warp(cache->head_dim, c.kv_heads, rows);
+  const dim3 grid(static_cast<unsigned>((rows + kWarps * tokens - 1) / (kWarps * tokens))), block(32 * kWarps);
+  auto* s = static_cast<cudaStream_t>(stream);
+  auto* kp = static_cast<bf16*>(k);
+  auto* vp = static_cast<bf16*>(v);
+  auto* st = reinterpret_cast<int*>(status);
+  if (tokens > 1) {
+    auto* fn = cache->head_dim == 128 ? (e4m3 ? cache_read_tokens_kernel<128, true> : cache_read_tokens_kernel<128, false>)
+                                      : (e4m3 ? cache_read_tokens_kernel<64, true> : cache_read_tokens_kernel<64, false>);
+    return launched(launch_pdl(fn, grid, block, 0, s, c, b, kp, k_stride, vp, v_stride, tokens, st));
+  }
   auto* fn = cache->head_dim == 128 ? (e4m3 ? cache_read_kernel<128, true> : cache_read_kernel<128, false>)
                                     : (e4m3 ? cache_read_kernel<64, true> : cache_read_kernel<64, false>);
-  return launched(launch_pdl(fn, dim3(static_cast<unsigned>((rows + kWarps - 1) / kWarps)), dim3(32 * kWarps), 0,
-                             static_cast<cudaStream_t>(stream), c, b, static_cast<bf16*>(k), k_stride,
-                             static_cast<bf16*>(v), v_stride, reinterpret_cast<int*>(status)));
+  return launched(launch_pdl(fn, grid, block, 0, s, c, b, kp, k_stride, vp, v_stride, st));
 }
 
 int ds_vit_cache_attention_workspace_bytes(const ds_vit_cache* cache, const ds_vit_chunks* chunks, int32_t heads,
