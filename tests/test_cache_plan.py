@@ -31,6 +31,8 @@ int64_t snapped(int64_t x, int64_t i0, int64_t i1, int64_t snap, int64_t cost) {
   return snap_border(x, i0, i1, snap, cost);
 }
 int64_t owner(int64_t x, int64_t W, int64_t U) { return deal(U, W).owner(x); }
+int64_t checks_from(unsigned block, int threads, int thread) { return check_first(block, threads, thread); }
+int64_t checks_step(unsigned blocks, int threads) { return check_step(blocks, threads); }
 }
 """
 
@@ -51,6 +53,8 @@ def plan(tmp_path_factory):
     for f in (h.begin, h.owner):
         f.restype, f.argtypes = C.c_int64, [C.c_int64] * 3
     h.snapped.restype, h.snapped.argtypes = C.c_int64, [C.c_int64] * 5
+    h.checks_from.restype, h.checks_from.argtypes = C.c_int64, [C.c_uint, C.c_int, C.c_int]
+    h.checks_step.restype, h.checks_step.argtypes = C.c_int64, [C.c_uint, C.c_int]
     return h
 
 
@@ -173,3 +177,20 @@ def test_sequences_and_pages_refused(plan):
         at(0, **kw)
     for page, n, want in ((0, 1, 1), (1, 1, 0), (-1, 5, 0), (4, 5, 1), (5, 5, 0), (top, 2 ** 33, 1), (-top - 1, 2 ** 33, 0)):
         assert plan.there(page, C.c_int64(n)) == want
+
+
+def test_sequences_checked_by_a_grid(plan):
+    """Every sequence is checked by one thread, and the first and the step stay positive
+    up to the grid of the most rows that a call admits (four a block)."""
+    for n in (1, 2, 127, 128, 129, 1024):
+        for blocks in (1, 2, 3, 8, 9, 1000):
+            step = plan.checks_step(blocks, 128)
+            mine = [s for b in range(blocks) for t in range(128) for s in range(plan.checks_from(b, 128, t), n, step)]
+            assert sorted(mine) == list(range(n))
+    most = 2 ** 30 - 1
+    for rows in (2 ** 26 - 4, 2 ** 26, 2 ** 27, 2 ** 27 + 4, 2 ** 28, 2 ** 29, most):
+        blocks = -(-rows // 4)
+        assert plan.checks_step(blocks, 128) == 128 * blocks
+        for b in (0, 7, 8, 2 ** 24 - 1, 2 ** 24, 2 ** 25, blocks - 1):
+            if b < blocks:
+                assert plan.checks_from(b, 128, 127) == 128 * b + 127

@@ -81,9 +81,9 @@ __device__ __forceinline__ void write_piece(const CacheView& c, int x, int64_t r
 
 // Every sequence's entries are checked, also those of sequences without rows.
 __device__ __forceinline__ void check_seqs(const ChunkView& b, int page_shift, int* status) {
-  const int threads = static_cast<int>(gridDim.x) * 32 * kWarps;
-  for (int s = static_cast<int>(blockIdx.x) * 32 * kWarps + threadIdx.x; s < b.n; s += threads)
-    load_seq(b, page_shift, s, status);
+  const int64_t step = check_step(gridDim.x, 32 * kWarps);
+  for (int64_t s = check_first(blockIdx.x, 32 * kWarps, threadIdx.x); s < b.n; s += step)
+    load_seq(b, page_shift, static_cast<int>(s), status);
 }
 
 __device__ __forceinline__ bool has_row(const Seq& q, int r) {

@@ -21,6 +21,13 @@ DSV_HD int seq_refused(int row0, int row1, int kv, int rows, int max_rows, int64
 }
 DSV_HD bool page_there(int page, int64_t n_pages) { return page >= 0 && page < n_pages; }
 
+// The sequences whose entries a thread of a grid checks: check_first, + check_step,
+// ... below n.  Grids of up to 2^28 blocks (rows are fewer than 2^30): 64 bits.
+DSV_HD int64_t check_first(uint32_t block, int threads, int thread) {
+  return static_cast<int64_t>(block) * threads + thread;
+}
+DSV_HD int64_t check_step(uint32_t blocks, int threads) { return static_cast<int64_t>(blocks) * threads; }
+
 // The blocks of 2^shift keys that rows at positions p0 .. p1 see: the blocks
 // of the first `sinks` keys that lie before the window of p0, then the
 // blocks from that window's first key to p1.  Rows before position 0 see none.
