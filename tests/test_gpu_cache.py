@@ -863,3 +863,65 @@ def test_captured_and_replayed_on_other_lengths(dv, rows):
             assert int(status.item()) == dv.OK
             ref, tol = attention64(st, q, 128 ** -0.5)
             assert (np.abs(f64(out) - ref) <= tol).all()
+
+
+# ------------------------------------------------------------------ rows of zeros
+
+def put_tokens(st, s, j, k=None, v=None):
+    """Keys and values (float64 [tokens, kv_heads, dim]) of tokens j of sequence s, as a write leaves them."""
+    at = torch.from_numpy(st.table[s].numpy()[j // st.page]).long().cuda(), torch.from_numpy(j % st.page).cuda()
+    for x, t, e in ((k, st.cache.k, st.cache.k_exp), (v, st.cache.v, st.cache.v_exp)):
+        if x is None:
+            continue
+        x = torch.from_numpy(np.ascontiguousarray(x)).bfloat16()
+        if e is None:
+            t[at[0], :, at[1]] = x.cuda()
+        else:
+            b, ex = quantise(x.double().numpy())
+            t[at[0], :, at[1]] = torch.from_numpy(b).cuda()
+            e[at[0], :, at[1]] = torch.from_numpy(ex).cuda()
+
+
+ZERO_LAYOUTS = [
+    # q, kv, heads, kv_heads, page
+    ([1], [1100], 8, 1, 64),                  # one token, one worker's blocks and a few
+    ([1, 1], [60007, 300], 8, 1, 128),        # a long one over every worker
+    ([4, 1], [900, 260], 6, 2, 16),           # a few rows
+    ([40], [900], 4, 2, 32),                  # chunks
+    ([300, 20], [1500, 700], 4, 1, 64),
+    ([30], [20011], 4, 1, 64),                # a chunk's items split between workers
+]
+
+
+@pytest.mark.parametrize("form", ["first", "middle", "last", "none seen", "all", "all rising", "rising"])
+@pytest.mark.parametrize("kind,dim", [("e4m3", 128), ("e4m3", 64), ("bf16", 128)])
+@pytest.mark.parametrize("q,kv,heads,kv_heads,page", ZERO_LAYOUTS)
+def test_attention_over_zero_rows(dv, q, kv, heads, kv_heads, page, kind, dim, form):
+    """Tokens whose values (and keys) are zeros, as padding and placeholders leave them: they
+    keep their weight in the sum, wherever they lie and however the scores run."""
+    st = Setup(dv, q, kv, kv_heads, dim, page, kind, seed=len(form) + dim)
+    x = st.queries(heads)
+    scale = dim ** -0.5
+    g = np.random.default_rng(7)
+    for s, n in enumerate(kv):
+        j = np.arange(n)
+        if form.endswith("rising"):           # positive scores that rise by some 40 (58 in powers of two)
+            base = np.abs(g.standard_normal((1, kv_heads, dim)))
+            put_tokens(st, s, j, k=base * ((j + 1) / n)[:, None, None])
+        some = {"first": j < max(n // 3, 128), "middle": (j >= n // 4) & (j < n // 4 + max(n // 2, 1)),
+                "last": j >= n - max(n // 3, 130), "none seen": j < n - q[s], "all": j >= 0, "all rising": j >= 0,
+                "rising": j < n - n // 5}[form]
+        z = np.zeros((int(some.sum()), kv_heads, dim))
+        put_tokens(st, s, j[some], k=z if form in ("first", "middle", "last") else None, v=z)
+    if form.endswith("rising"):
+        x, scale = x.abs(), 40 / (dim * 2 / math.pi)
+    out = torch.full((st.rows, heads, dim), 7.0, dtype=torch.bfloat16, device="cuda")
+    got, status = dv.cache_attention(st.cache, st.chunks, x, scale=scale, out=out)
+    torch.cuda.synchronize()
+    assert int(status.item()) == dv.OK
+    rows = sorted({0, st.rows - 1, st.rows // 2, *(st.off[s] for s in range(len(q)))})
+    ref, tol = sampled64(st, x, scale, rows)
+    bad = ~(np.abs(f64(got)[rows] - ref) <= tol)
+    assert not bad.any(), f"{bad.sum()} of {bad.size} outside, {f64(got)[rows][bad][:3]} for {ref[bad][:3]}"
+    if form.startswith("all"):
+        assert bool((got == 0).all())

@@ -37,7 +37,7 @@
 // and the weights carry the values' exponents and are taken against the running
 // maximum of score plus exponent, the size of a key's contribution, so that the
 // largest stay in [2^6, 2^14]; contributions under 2^-20 of the largest lose
-// bits.
+// bits.  The weights' sum has a reference of its own (Raise in cache_rows.cuh).
 #include "cache_rows.cuh"
 
 #include <algorithm>
@@ -46,13 +46,9 @@ namespace dsvit {
 
 namespace {
 
-// A row's reference m (log2) is raised when a block's maximum passes m + kLag,
-// to kLead below that maximum; weights are 2^(x - m).
-template <bool E4M3>
-struct Reference {
-  static constexpr float kLag = E4M3 ? 14.f : 8.f;
-  static constexpr float kLead = E4M3 ? 6.f : 0.f;
-};
+// bf16: a row's reference m (log2) is raised when a block's maximum passes m + kLag16, to
+// that maximum; weights are 2^(z - m).  e4m3: Raise in cache_rows.cuh.
+constexpr float kLag16 = 8.f;
 
 template <int D, bool E4M3>
 struct Shape {
@@ -383,11 +379,11 @@ __global__ void __launch_bounds__(Shape<D, E4M3>::kThreads, 1)
         }
       }
     }
-    float o[kCols][4], m[kRowHalves], l[kRowHalves];
+    float o[kCols][4], m[kRowHalves], l[kRowHalves], d[kRowHalves];   // d: e4m3, see Raise
 #pragma unroll
     for (int x = 0; x < kRowHalves; ++x) {
       m[x] = -INFINITY;
-      l[x] = 0.f;
+      l[x] = d[x] = 0.f;
     }
 #pragma unroll
     for (int n = 0; n < kCols; ++n)
@@ -475,23 +471,22 @@ __global__ void __launch_bounds__(Shape<D, E4M3>::kThreads, 1)
       }
       // ---- softmax of the block: scores z = sc f (log2 units), f the scale and
       // the key's factor; contributions z + the value's exponent
-      float f[kRowHalves][kN][2], add[kN][2], vf[kN][2], top[kRowHalves];
+      float add[kN][2], vf[kN][2], top[kRowHalves], most[kRowHalves];   // most: the largest contribution
 #pragma unroll
       for (int n = 0; n < kN; ++n)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          float kf = 1.f;
           add[n][e] = 0.f;
           vf[n][e] = 1.f;
           if constexpr (E4M3) {
             // Rows with the NaN byte hold NaN elements, so plain shifts do for the factors.
             const uint32_t kb = e == 0 ? ke[n] & 255u : ke[n] >> 8, vb = e == 0 ? ve[n] & 255u : ve[n] >> 8;
-            kf = __uint_as_float(kb << 23);
+            const float kf = __uint_as_float(kb << 23);
             vf[n][e] = __uint_as_float(vb << 23);
             add[n][e] = __uint_as_float(0x4B000000u | vb) - 8388735.f;   // byte - 127: the byte in the last bits of 2^23
-          }
 #pragma unroll
-          for (int x = 0; x < kRowHalves; ++x) f[x][n][e] = E4M3 ? qscale[x] * kf : qscale[x];
+            for (int x = 0; x < kRowHalves; ++x) sc[n][2 * x + e] *= qscale[x] * kf;
+          }
         }
 #pragma unroll
       for (int x = 0; x < kRowHalves; ++x) {
@@ -500,23 +495,27 @@ __global__ void __launch_bounds__(Shape<D, E4M3>::kThreads, 1)
           for (int n = 0; n < kN; ++n)
 #pragma unroll
             for (int e = 0; e < 2; ++e)
-              if (!sees(a, pos[x], key0 + 8 * n + 2 * t + e)) {
-                sc[n][2 * x + e] = -INFINITY;      // with a factor of 1, whatever the key's is
-                f[x][n][e] = 1.f;
-              }
+              if (!sees(a, pos[x], key0 + 8 * n + 2 * t + e)) sc[n][2 * x + e] = -INFINITY;
         }
-        top[x] = -INFINITY;
+        top[x] = most[x] = -INFINITY;
 #pragma unroll
         for (int n = 0; n < kN; ++n)
 #pragma unroll
-          for (int e = 0; e < 2; ++e) top[x] = fmaxf(top[x], fmaf(sc[n][2 * x + e], f[x][n][e], add[n][e]));
-        top[x] = fmaxf(top[x], __shfl_xor_sync(0xFFFFFFFFu, top[x], 1));
-        top[x] = fmaxf(top[x], __shfl_xor_sync(0xFFFFFFFFu, top[x], 2));
+          for (int e = 0; e < 2; ++e) {
+            top[x] = fmaxf(top[x], sc[n][2 * x + e]);
+            if constexpr (E4M3) most[x] = fmaxf(most[x], sc[n][2 * x + e] + add[n][e]);
+          }
+        if constexpr (!E4M3) {
+          top[x] *= qscale[x];
+          top[x] = fmaxf(top[x], __shfl_xor_sync(0xFFFFFFFFu, top[x], 1));
+          top[x] = fmaxf(top[x], __shfl_xor_sync(0xFFFFFFFFu, top[x], 2));
+        }
       }
-      // The reference is raised (and O rescaled) rarely: weights stay below 2^kLag.
-      bool up[kRowHalves], some = dead;
+      // References are raised (and O rescaled) rarely.
+      bool some = dead;
 #pragma unroll
-      for (int x = 0; x < kRowHalves; ++x) some |= up[x] = top[x] > m[x] + Reference<E4M3>::kLag;
+      for (int x = 0; x < kRowHalves; ++x)
+        some |= E4M3 ? must_raise(m[x], d[x], top[x], most[x]) : top[x] > m[x] + kLag16;
       if (__any_sync(0xFFFFFFFFu, some)) {
         if (__any_sync(0xFFFFFFFFu, dead)) {
           dead = true;
@@ -524,33 +523,45 @@ __global__ void __launch_bounds__(Shape<D, E4M3>::kThreads, 1)
         }
 #pragma unroll
         for (int x = 0; x < kRowHalves; ++x) {
-          const float old = m[x];
-          if (up[x]) m[x] = top[x] - Reference<E4M3>::kLead;
-          const float s = old == m[x] ? 1.f : ex2_approx(old - m[x]);
-          l[x] *= s;
+          float fl, fo;
+          if constexpr (E4M3) {
+#pragma unroll
+            for (int y = 1; y < 4; y <<= 1) {      // over the row's four lanes
+              top[x] = fmaxf(top[x], __shfl_xor_sync(0xFFFFFFFFu, top[x], y));
+              most[x] = fmaxf(most[x], __shfl_xor_sync(0xFFFFFFFFu, most[x], y));
+            }
+            const Raise r = raised(m[x], d[x], top[x], most[x]);
+            m[x] = r.m, d[x] = r.d, fl = r.l, fo = r.o;
+          } else {
+            const float old = m[x];
+            if (top[x] > old + kLag16) m[x] = top[x];
+            fl = fo = old == m[x] ? 1.f : ex2_approx(old - m[x]);
+          }
+          l[x] *= fl;
 #pragma unroll
           for (int n = 0; n < kCols; ++n) {
-            o[n][2 * x] *= s;
-            o[n][2 * x + 1] *= s;
+            o[n][2 * x] *= fo;
+            o[n][2 * x + 1] *= fo;
           }
         }
       }
       uint32_t pf[kN / 2][4];
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
-        const float base = x < kRowHalves && m[x % kRowHalves] != -INFINITY ? -m[x % kRowHalves] : 0.f;
+        constexpr int kLast = kRowHalves - 1;
+        const int y = x < kLast ? x : kLast;
+        const float base = m[y] != -INFINITY ? -m[y] : 0.f, down = E4M3 ? shift_down(d[y]) : 1.f;
 #pragma unroll
         for (int n = 0; n < kN; ++n) {
           uint32_t& p = pf[n / 2][2 * (n & 1) + x];
           p = 0;
           if (x >= kRowHalves) continue;
-          constexpr int kLast = kRowHalves - 1;
-          const int y = x < kLast ? x : kLast;
-          float w0 = ex2_approx(fmaf(sc[n][2 * x], f[y][n][0], base));
-          float w1 = ex2_approx(fmaf(sc[n][2 * x + 1], f[y][n][1], base));
+          const float f = E4M3 ? 1.f : qscale[y];
+          float w0 = ex2_approx(fmaf(sc[n][2 * x], f, base));
+          float w1 = ex2_approx(fmaf(sc[n][2 * x + 1], f, base));
           l[y] += w0 + w1;
           // The product's operand: weights in 16 bits (their sum stays in fp32).
-          p = E4M3 ? pack_f16x2(w0 * vf[n][0], w1 * vf[n][1]) : pack_bf16x2(w0, w1);
+          p = E4M3 ? pack_f16x2(w0 * down * vf[n][0], w1 * down * vf[n][1]) : pack_bf16x2(w0, w1);
           if (E4M3 && !open) {
             // The exponent of a value that nobody sees may be the NaN byte.
             const int j = key0 + 8 * n + 2 * t;
@@ -614,11 +625,12 @@ __global__ void __launch_bounds__(Shape<D, E4M3>::kThreads, 1)
       if (rr0 < R) {
         const int i = a.by_group(rho);
         bf16* dst = a.out + (it.q.row0 + i) * a.out_stride + (it.head * a.group + rho - i * a.group) * D;
-        const float inv = pos[x] < 0 ? 0.f : 1.f / l[x];
+        const float inv = pos[x] < 0 ? 0.f : 1.f / l[x], up = E4M3 ? shift_up(d[x]) : 1.f;
         float* rr = r + rr0 * D;
         if (!whole && t == 0) {
           rec.max_of(r, D)[rr0] = m[x];
           rec.sum_of(r, D)[rr0] = l[x];
+          if constexpr (E4M3) rec.shift_of(r, D)[rr0] = d[x];
         }
         // bf16: columns 8n + 2t, + 1.  e4m3: column tile n holds dim n of each
         // lane group's D / 8, so this lane has dims (2t) D/8 + n and (2t + 1) D/8 + n.
@@ -630,7 +642,7 @@ __global__ void __launch_bounds__(Shape<D, E4M3>::kThreads, 1)
             for (int n = 0; n < kCols; n += 4) {
               float4 y = make_float4(o[n][2 * x + e], o[n + 1][2 * x + e], o[n + 2][2 * x + e], o[n + 3][2 * x + e]);
               if (whole) {
-                y = make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv);
+                y = make_float4(y.x * inv * up, y.y * inv * up, y.z * inv * up, y.w * inv * up);
                 bad |= not_finite(y.x) || not_finite(y.y) || not_finite(y.z) || not_finite(y.w);
                 *reinterpret_cast<uint2*>(dst + d0 + n) = make_uint2(pack_bf16x2(y.x, y.y), pack_bf16x2(y.z, y.w));
               } else {
@@ -691,7 +703,6 @@ constexpr int kJoinRows = 8;      // grid rows at most
 template <int D, bool E4M3>
 __global__ void __launch_bounds__(32 * kJoinWarps)
     join_kernel(const __grid_constant__ AttentionArgs a, const Records rec, int workers) {
-  constexpr int kPer = D / 32;
   __shared__ SplitHeader heads[kJoinItems];
   grid_dep_launch();
   grid_dep_wait();
@@ -710,18 +721,16 @@ __global__ void __launch_bounds__(32 * kJoinWarps)
     const int64_t left = static_cast<int64_t>(hd.q.c) * a.group - hd.rho0;
     const int rows = left < rec.rows ? static_cast<int>(left) : rec.rows;
     for (int row = blockIdx.x; row < rows; row += gridDim.x) {
-      float m = -INFINITY, l = 0.f, o[kPer];
-#pragma unroll
-      for (int x = 0; x < kPer; ++x) o[x] = 0.f;
+      Sum<D> sum;
       if (hd.parts <= kJoinWarps) {
         if (turn++ % kJoinWarps != warp) continue;
-        join_parts<D, 4>(rec, w, hd.parts, row, 0, 1, lane, m, l, o);
-        join_finish<D, E4M3>(a, hd, hd.rho0 + row, l, o, lane);
+        join_parts<D, E4M3, 4>(rec, w, hd.parts, row, 0, 1, lane, sum);
+        join_finish<D, E4M3>(a, hd, hd.rho0 + row, sum, lane);
         continue;
       }
-      join_parts<D, 4>(rec, w, hd.parts, row, warp, kJoinWarps, lane, m, l, o);
-      join_warps<D>(warp, lane, m, l, o);
-      if (warp == 0) join_finish<D, E4M3>(a, hd, hd.rho0 + row, l, o, lane);
+      join_parts<D, E4M3, 4>(rec, w, hd.parts, row, warp, kJoinWarps, lane, sum);
+      join_warps<D, E4M3>(warp, lane, sum);
+      if (warp == 0) join_finish<D, E4M3>(a, hd, hd.rho0 + row, sum, lane);
     }
   }
 }

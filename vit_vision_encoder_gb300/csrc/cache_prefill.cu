@@ -42,8 +42,9 @@
 // conversion is exact; the rows of a tile are scaled by powers of two to the
 // tile's largest exponent E, and elements 2^-24 below it lose bits).  Scores are
 // scaled by 2^E(K); the weights are taken against the running maximum of score
-// plus E(V), the size of a contribution, and their sum is scaled back.  Query
-// rows are scaled to fp16's range like in the kernel for few rows.
+// plus E(V), the size of a contribution, and their sum is scaled back to a reference
+// of its own (Raise in cache_rows.cuh).  Query rows are scaled to fp16's range like
+// in the kernel for few rows.
 //
 // Keys that a row does not see are masked in its scores.  Value rows that no row
 // of the item sees are zeroed in shared memory (they may hold anything); where
@@ -86,8 +87,7 @@ struct Cfg {
   static constexpr int kOffBar = kOffExp + kRaw * kTile;
   static constexpr int kSmem = kOffBar + 1024 + 1024;
   static_assert(kSmem + 512 <= 232448, "shared memory, the static part included");
-  static constexpr float kLag = E4M3 ? 14.f : 8.f;         // see Reference in the kernel for few rows
-  static constexpr float kLead = E4M3 ? 6.f : 0.f;
+  static constexpr float kLag16 = 8.f;                     // bf16: see the kernel for few rows
 };
 
 // Barrier slots.
@@ -433,7 +433,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
     if (lane == 0) mbar_arrive(bar(kBarJobEmpty + i));
     return ok && j.b < j.end;
   };
-  float2* other = reinterpret_cast<float2*>(smem + C::kBytes);   // tile B's maxima and sums, in place of its query rows
+  float4* other = reinterpret_cast<float4*>(smem + C::kBytes);   // tile B's references and sums, in place of its query rows
   int issued = 0;                           // ring or raw tiles whose loads were issued
 
   // e4m3: 28 warps start with 72 registers each; 16 x 96 + 12 x 40 is the same sum.
@@ -860,7 +860,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
       const int pa = first + a.by_group(rho0), pb = first + a.by_group(min(rho0 + kTile, R) - 1);
       const int lo = window_start(a, pos), lo_b = window_start(a, pb);
 
-      float m = -INFINITY, l = 0.f;
+      float m = -INFINITY, d = 0.f, l = 0.f;      // d: e4m3, see Raise
       for (int b = b0; b < w.end; b += stride, ++step) {
         const int key0 = w.kb.at(b) << kTileShift, nth = tile + (b - w.b);     // the CTA's tiles before this one
         const bool open = key0 + kTile - 1 <= pa && (key0 >= lo_b || key0 + kTile <= a.sinks);
@@ -876,7 +876,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
           break;
         }
         tc_fence_after();
-        float c = c0, ev = 0.f, unit = 1.f;
+        float c = c0, ev = 0.f;
         if constexpr (E4M3) {
           // E(V) is known once the value tile is there (it stays until P V).
           const uint32_t nv = 2 * static_cast<uint32_t>(nth) + 1;
@@ -890,7 +890,6 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
           // Not zero: a masked score of -inf stays -inf.
           c = fmaxf(c * __int_as_float((ek + 127) << 23), 1e-35f);
           ev = static_cast<float>(e);
-          unit = __int_as_float((127 - e) << 23);
         }
         uint32_t sr[64];
         float top = tmem_ld32_max_x2<64>(tS, sr), top2 = tmem_ld32_max_x2<64>(tS + 32, sr + 32);
@@ -911,13 +910,23 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
         }
         // Both threads of the row derive the same reference.
         top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 16));
-        const float reach = fmaf(top, c, ev);
-        float m_new = m, alpha = 1.f;
-        if (reach > m + C::kLag) {           // always true on the first visible key (m = -inf)
-          m_new = reach - C::kLead;
-          alpha = ex2_approx(m - m_new);
+        const float reach = top * c;
+        float alpha = 1.f, off, unit = 1.f;  // alpha: of the outputs so far
+        if constexpr (E4M3) {
+          const Raise up = raised(m, d, reach, reach + ev);
+          m = up.m, d = up.d, alpha = up.o, l *= up.l;
+          // Operands 2^(z + x); their sum is scaled back by 2^-x.  Under -60 (a tile of
+          // values far below the row's largest) they are zeros in fp16 all the same.
+          const float x = fmaxf(ev - d, -60.f);
+          off = m == -INFINITY ? 0.f : x - m;
+          unit = __int_as_float(max(127 - static_cast<int>(x), 0) << 23);
+        } else {
+          if (reach > m + C::kLag16) {       // always true on the first visible key (m = -inf)
+            alpha = ex2_approx(m - reach);
+            m = reach;
+          }
+          off = m == -INFINITY ? 0.f : -m;
         }
-        const float off = m_new == -INFINITY ? 0.f : ev - m_new;
         const uint64_t c2 = f2(c, c), nm2 = f2(off, off);
         uint64_t acc[4] = {f2(0.f, 0.f), f2(0.f, 0.f), f2(0.f, 0.f), f2(0.f, 0.f)};
         uint32_t pk[32];
@@ -935,7 +944,8 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
         const uint64_t s2 = f2_add(f2_add(acc[0], acc[1]), f2_add(acc[2], acc[3]));
         float s0, s1;
         f2_split(s2, s0, s1);
-        l = l * alpha + (s0 + s1) * unit;    // this half's share of the row sum
+        // This half's share of the row sum.
+        l = E4M3 ? fmaf(s0 + s1, unit, l) : fmaf(l, alpha, s0 + s1);
         tmem_st32_x2<32>(tS, pk);
         // With a score tile each, S_X waited for the product that wrote O_X last.
         if (b != b0 && __any_sync(0xFFFFFFFFu, alpha != 1.f)) {
@@ -956,7 +966,6 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
         tmem_wait_st();
         tc_fence_before();
         mbar_arrive(bar(kBarPFull + at));
-        m = m_new;
       }
       if (!ok || !mbar_wait(bar(kBarPvDone + x), (step - 1) & 1, a.status)) {
         ok = false;
@@ -972,7 +981,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
       const bool two = shared && count > 1, paired = shared && (two || C::kScores == 3);
       if (paired) {
         if (x == 1) {
-          if (h == 0) other[r] = make_float2(m, l);
+          if (h == 0) other[r] = make_float4(m, d, l, 0.f);
           tc_fence_before();
           mbar_arrive(bar(kBarOther));
           if (!mbar_wait(bar(kBarMerged), merges & 1, a.status)) {
@@ -990,12 +999,12 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
         ++merges;
         tc_fence_after();
         if (two) {
-          const float2 ml = other[r];
-          const float mb = ml.x, top = fmaxf(m, mb);
-          fa = m == top ? 1.f : exp2f(m - top);
-          fb = mb == top ? 1.f : exp2f(mb - top);
-          l = l * fa + ml.y * fb;
-          m = top;
+          const float4 b = other[r];
+          const float to_m = fmaxf(m, b.x), to_d = E4M3 ? shift_at(to_m, fmaxf(m + d, b.x + b.y)) : 0.f;
+          fa = output_factor<E4M3>(m, d, to_m, to_d);
+          fb = output_factor<E4M3>(b.x, b.y, to_m, to_d);
+          l = l * sum_factor(m, to_m) + b.z * sum_factor(b.x, to_m);
+          m = to_m, d = to_d;
         }
       }
       // Columns col .. of the row's output (kCols of each half of the dims).
@@ -1020,7 +1029,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
       };
       uint32_t redo = 0;
       if (w.whole == 1) {
-        const float inv = pos < 0 ? 0.f : 1.f / l;
+        const float inv = pos < 0 ? 0.f : 1.f / l, up = E4M3 ? shift_up(d) : 1.f;
         bool bad = false;
 #pragma unroll 1
         for (int y = 0; y < D / 64; ++y) {
@@ -1028,7 +1037,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
           load_o(std::integral_constant<int, 32>{}, 32 * y, o);
 #pragma unroll
           for (int z = 0; z < 16; ++z) {
-            const float o0 = __uint_as_float(o[2 * z]) * inv, o1 = __uint_as_float(o[2 * z + 1]) * inv;
+            const float o0 = __uint_as_float(o[2 * z]) * inv * up, o1 = __uint_as_float(o[2 * z + 1]) * inv * up;
             bad |= not_finite(o0) || not_finite(o1);
             o[z] = pack_bf16x2(o0, o1);
           }
@@ -1057,6 +1066,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
         if (h == 0) {
           p.rec.max_of(rec, D)[x * kTile + r] = m;
           p.rec.sum_of(rec, D)[x * kTile + r] = l;
+          if constexpr (E4M3) p.rec.shift_of(rec, D)[x * kTile + r] = d;
         }
         // Passes of kCols columns of each half of the dims: a row's place holds both.
         constexpr int kCols = D / 4;
@@ -1123,7 +1133,6 @@ template <int D, bool E4M3>
 __global__ void __launch_bounds__(32 * kJoinWarps, kJoinBlocks)
     join_items_kernel(const __grid_constant__ AttentionArgs a, const Records rec, int workers) {
   static_assert(kMaxCtas == 32 * kJoinWarps, "a thread per worker");
-  constexpr int kPer = D / 32;
   __shared__ SplitHeader heads[kMaxCtas];
   __shared__ int before[kMaxCtas];     // rows of the workers before each
   __shared__ int sums[kJoinWarps];
@@ -1162,12 +1171,10 @@ __global__ void __launch_bounds__(32 * kJoinWarps, kJoinBlocks)
       if (before[w + half] <= r) w += half;
     const SplitHeader& hd = heads[w];
     const int row = r - before[w];
-    float m = -INFINITY, l = 0.f, o[kPer];
-#pragma unroll
-    for (int x = 0; x < kPer; ++x) o[x] = 0.f;
-    join_parts<D, 4>(rec, w, hd.parts, row, together ? warp : 0, together ? kJoinWarps : 1, lane, m, l, o);
-    if (together) join_warps<D>(warp, lane, m, l, o);
-    if (!together || warp == 0) join_finish<D, E4M3>(a, hd, hd.rho0 + row, l, o, lane);
+    Sum<D> sum;
+    join_parts<D, E4M3, 4>(rec, w, hd.parts, row, together ? warp : 0, together ? kJoinWarps : 1, lane, sum);
+    if (together) join_warps<D, E4M3>(warp, lane, sum);
+    if (!together || warp == 0) join_finish<D, E4M3>(a, hd, hd.rho0 + row, sum, lane);
   }
 }
 

@@ -64,6 +64,51 @@ __device__ __noinline__ void exact_row(const AttentionArgs& a, int s, int row0, 
   for (int x = 0; x < kPer; ++x) to[x] = __float2bfloat16_rn(p < 0 ? 0.f : o[x] / l);
 }
 
+// e4m3: the range of a softmax over values with exponents.  With scores z (log2 units) and a
+// value's exponent e, the weights 2^z and the products' operands 2^(z + e), in fp16,
+// need a reference each: the largest may differ by 2^237, and a row of zeros has the
+// least exponent there is (-117) and any score.  m refers the weights and their sum l:
+// l holds sum 2^(z - m), weights at most 2^kLag.  m + d refers the contributions, d an
+// integer, and o holds sum 2^(z + e - m - d) v 2^-e: contributions at most 2^kLag too, the
+// largest usually some 2^kLead.  Either one is raised when a block passes its lag.  (One
+// reference for both, that of the contributions, lets the weights of zeros reach 2^131.)
+// d is at least -110: contributions of the least exponents then stay under 2^7, and
+// 2^kLag 2^-d is finite; and at most 120: no contribution is past 2^kLag, as e <= 120.
+constexpr float kLag = 14.f, kLead = 6.f;
+struct Raise {
+  float m, d;             // the references from here on
+  float l, o;             // factors of l and o
+};
+// From the block's largest score and contribution (-inf: none).
+__device__ __forceinline__ bool must_raise(float m, float d, float score, float contribution) {
+  return score > m + kLag || contribution > m + d + kLag;
+}
+__device__ __forceinline__ Raise raised(float m, float d, float score, float contribution) {
+  if (!must_raise(m, d, score, contribution)) return Raise{m, d, 1.f, 1.f};
+  Raise r;
+  r.m = score > m + kLag ? score : m;
+  const float to = contribution > m + d + kLag ? contribution - kLead : m + d;
+  r.d = fminf(fmaxf(rintf(to - r.m), -110.f), 120.f);
+  r.l = ex2_approx(m - r.m);
+  r.o = ex2_approx((m - r.m) + (d - r.d));
+  return r;
+}
+// 2^d, 2^-d of such a d.
+__device__ __forceinline__ float shift_up(float d) { return __int_as_float((127 + static_cast<int>(d)) << 23); }
+__device__ __forceinline__ float shift_down(float d) { return __int_as_float((127 - static_cast<int>(d)) << 23); }
+
+// Results of a row are added up at the largest m and, next to it, the largest m + d (r):
+// the d there, and the factors of a result's l and o.
+__device__ __forceinline__ float shift_at(float m, float r) {
+  return m == -INFINITY ? 0.f : fminf(fmaxf(rintf(r - m), -110.f), 120.f);
+}
+__device__ __forceinline__ float sum_factor(float m, float to) { return m == to ? 1.f : exp2f(m - to); }
+template <bool E4M3>
+__device__ __forceinline__ float output_factor(float m, float d, float to_m, float to_d) {
+  if constexpr (!E4M3) return sum_factor(m, to_m);
+  return m == -INFINITY ? 0.f : exp2f((m - to_m) + (d - to_d));
+}
+
 __device__ __forceinline__ bool not_finite(float x) { return (__float_as_uint(x) & 0x7F800000u) == 0x7F800000u; }
 
 // Who shares the item that a worker begins and does not end: `parts` workers,
@@ -78,7 +123,8 @@ static_assert(sizeof(SplitHeader) == 32, "read as two 16-byte words");
 
 // Layout of the workspace: a header per worker, then two records per worker,
 // 0 for the item that it found begun, 1 for the item that it leaves unended.  A record:
-// unnormalised outputs [R][D], maxima [R], sums [R], fp32.
+// unnormalised outputs [R][D], references of the weights [R], sums [R] and (e4m3) the
+// outputs' shifts d [R], fp32.
 struct Records {
   SplitHeader* headers;
   float* base;
@@ -87,9 +133,10 @@ struct Records {
   __device__ __forceinline__ float* at(int64_t worker, int which) const { return base + (2 * worker + which) * size; }
   __device__ __forceinline__ float* max_of(float* r, int d) const { return r + rows * d; }
   __device__ __forceinline__ float* sum_of(float* r, int d) const { return r + rows * d + rows; }
+  __device__ __forceinline__ float* shift_of(float* r, int d) const { return r + rows * d + 2 * rows; }
 };
 
-inline int64_t record_floats(int rows, int d) { return (static_cast<int64_t>(rows) * (d + 2) + 3) & ~int64_t{3}; }
+inline int64_t record_floats(int rows, int d) { return (static_cast<int64_t>(rows) * (d + 3) + 3) & ~int64_t{3}; }
 inline size_t records_bytes(int64_t workers, int rows, int d) {
   return static_cast<size_t>(workers) * (sizeof(SplitHeader) + 2 * record_floats(rows, d) * sizeof(float));
 }
@@ -98,26 +145,32 @@ inline Records records_in(void* ws, int64_t workers, int rows, int d) {
   return Records{h, reinterpret_cast<float*>(h + workers), rows, record_floats(rows, d)};
 }
 
-// Adds parts first, first + step, ... of one row of a split item, O = sum_p 2^(m_p - M) O_p and L
-// alike, to (m, l, o), loads of kBatch parts at a time.  The order is fixed, so a result depends
-// on the lengths alone.
-template <int D, int kBatch>
+// What a warp has of a row: references, sum, outputs 4 or 2 a lane.
+template <int D>
+struct Sum {
+  float m = -INFINITY, d = 0.f, l = 0.f, o[D / 32] = {};
+};
+
+// Adds parts first, first + step, ... of one row of a split item to `sum`, loads of kBatch parts
+// at a time.  The order is fixed, so a result depends on the lengths alone.
+template <int D, bool E4M3, int kBatch>
 __device__ __forceinline__ void join_parts(const Records& rec, int w, int parts, int row, int first, int step, int lane,
-                                           float& m, float& l, float (&o)[D / 32]) {
+                                           Sum<D>& sum) {
   constexpr int kPer = D / 32;
   for (int p0 = first; p0 < parts; p0 += kBatch * step) {
-    float mp[kBatch], lp[kBatch], op[kBatch][kPer];
+    float mp[kBatch], dp[kBatch], lp[kBatch], op[kBatch][kPer];
 #pragma unroll
     for (int y = 0; y < kBatch; ++y) {
       const int part = p0 + y * step;
       mp[y] = -INFINITY;
-      lp[y] = 0.f;
+      dp[y] = lp[y] = 0.f;
 #pragma unroll
       for (int x = 0; x < kPer; ++x) op[y][x] = 0.f;
       if (part < parts) {
         float* r = rec.at(w + part, part == 0 ? 1 : 0);
         mp[y] = rec.max_of(r, D)[row];
         lp[y] = rec.sum_of(r, D)[row];
+        if constexpr (E4M3) dp[y] = rec.shift_of(r, D)[row];
         if constexpr (kPer == 4) {
           const float4 v = *reinterpret_cast<const float4*>(r + row * D + 4 * lane);
           op[y][0] = v.x, op[y][1] = v.y, op[y][2] = v.z, op[y][3] = v.w;
@@ -127,66 +180,76 @@ __device__ __forceinline__ void join_parts(const Records& rec, int w, int parts,
         }
       }
     }
-    float m_new = m;
-#pragma unroll
-    for (int y = 0; y < kBatch; ++y) m_new = fmaxf(m_new, mp[y]);
-    const float wa = m == m_new ? 1.f : exp2f(m - m_new);
-    l *= wa;
-#pragma unroll
-    for (int x = 0; x < kPer; ++x) o[x] *= wa;
+    float m = sum.m, r = sum.m + sum.d;
 #pragma unroll
     for (int y = 0; y < kBatch; ++y) {
-      const float wb = mp[y] == m_new ? 1.f : exp2f(mp[y] - m_new);
-      l += lp[y] * wb;
-#pragma unroll
-      for (int x = 0; x < kPer; ++x) o[x] += op[y][x] * wb;
+      m = fmaxf(m, mp[y]);
+      r = fmaxf(r, mp[y] + dp[y]);
     }
-    m = m_new;
+    const float d = E4M3 ? shift_at(m, r) : 0.f;
+    const float wa = output_factor<E4M3>(sum.m, sum.d, m, d);
+    sum.l *= sum_factor(sum.m, m);
+#pragma unroll
+    for (int x = 0; x < kPer; ++x) sum.o[x] *= wa;
+#pragma unroll
+    for (int y = 0; y < kBatch; ++y) {
+      const float wb = output_factor<E4M3>(mp[y], dp[y], m, d);
+      sum.l += lp[y] * sum_factor(mp[y], m);
+#pragma unroll
+      for (int x = 0; x < kPer; ++x) sum.o[x] += op[y][x] * wb;
+    }
+    sum.m = m, sum.d = d;
   }
 }
 
 constexpr int kJoinWarps = 8;
 // A row whose parts the warps of a block have added up: the warps' sums joined by the first.
-template <int D>
-__device__ __forceinline__ void join_warps(int warp, int lane, float m, float& l, float (&o)[D / 32]) {
+template <int D, bool E4M3>
+__device__ __forceinline__ void join_warps(int warp, int lane, Sum<D>& sum) {
   constexpr int kPer = D / 32;
-  __shared__ float sm[kJoinWarps], sl[kJoinWarps], so[kJoinWarps][D];
+  __shared__ float sm[kJoinWarps], sd[kJoinWarps], sl[kJoinWarps], so[kJoinWarps][D];
   __syncthreads();          // the previous row's results have been read
   if (lane == 0) {
-    sm[warp] = m;
-    sl[warp] = l;
+    sm[warp] = sum.m;
+    sd[warp] = sum.d;
+    sl[warp] = sum.l;
   }
 #pragma unroll
-  for (int x = 0; x < kPer; ++x) so[warp][lane * kPer + x] = o[x];
+  for (int x = 0; x < kPer; ++x) so[warp][lane * kPer + x] = sum.o[x];
   __syncthreads();
   if (warp != 0) return;
-  float M = sm[0];
+  float r = sm[0] + sd[0];
+  sum.m = sm[0];
 #pragma unroll
-  for (int x = 1; x < kJoinWarps; ++x) M = fmaxf(M, sm[x]);
-  l = 0.f;
+  for (int y = 1; y < kJoinWarps; ++y) {
+    sum.m = fmaxf(sum.m, sm[y]);
+    r = fmaxf(r, sm[y] + sd[y]);
+  }
+  sum.d = E4M3 ? shift_at(sum.m, r) : 0.f;
+  sum.l = 0.f;
 #pragma unroll
-  for (int x = 0; x < kPer; ++x) o[x] = 0.f;
+  for (int x = 0; x < kPer; ++x) sum.o[x] = 0.f;
 #pragma unroll
   for (int y = 0; y < kJoinWarps; ++y) {
-    const float f = sm[y] == M ? 1.f : exp2f(sm[y] - M);
-    l += sl[y] * f;
+    const float f = output_factor<E4M3>(sm[y], sd[y], sum.m, sum.d);
+    sum.l += sl[y] * sum_factor(sm[y], sum.m);
 #pragma unroll
-    for (int x = 0; x < kPer; ++x) o[x] += so[y][lane * kPer + x] * f;
+    for (int x = 0; x < kPer; ++x) sum.o[x] += so[y][lane * kPer + x] * f;
   }
 }
 
 // One warp writes a joined row.
 template <int D, bool E4M3>
-__device__ __forceinline__ void join_finish(const AttentionArgs& a, const SplitHeader& hd, int rho, float l,
-                                            const float (&o)[D / 32], int lane) {
+__device__ __forceinline__ void join_finish(const AttentionArgs& a, const SplitHeader& hd, int rho,
+                                            const Sum<D>& sum, int lane) {
   const int i = a.by_group(rho), h = hd.head * a.group + rho - i * a.group, p = hd.q.kv - hd.q.c + i;
   bf16* to = a.out + (hd.q.row0 + i) * a.out_stride + h * D + lane * (D / 32);
-  const float inv = p < 0 ? 0.f : 1.f / l;
+  const float inv = p < 0 ? 0.f : 1.f / sum.l, up = E4M3 ? shift_up(sum.d) : 1.f;
   bool bad = false;
   uint32_t w[D / 64];
 #pragma unroll
   for (int x = 0; x < D / 64; ++x) {
-    const float y0 = o[2 * x] * inv, y1 = o[2 * x + 1] * inv;
+    const float y0 = sum.o[2 * x] * inv * up, y1 = sum.o[2 * x + 1] * inv * up;
     bad |= not_finite(y0) || not_finite(y1);
     w[x] = pack_bf16x2(y0, y1);
   }
