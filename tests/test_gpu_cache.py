@@ -925,3 +925,88 @@ def test_attention_over_zero_rows(dv, q, kv, heads, kv_heads, page, kind, dim, f
     assert not bad.any(), f"{bad.sum()} of {bad.size} outside, {f64(got)[rows][bad][:3]} for {ref[bad][:3]}"
     if form.startswith("all"):
         assert bool((got == 0).all())
+
+
+# ------------------------------------------------------------------ rows far apart
+
+def far64(st, q, scale, rows, window=0, sinks=0):
+    """(reference, tolerance) [len(rows), heads, dim] in 64 bits where keys or values lie
+    far apart, e4m3.  As attention64's tolerance, but a score's error goes by its own key:
+    each weight w_j is off by (dim + 2) 2^-24 sum_d |q_d k_jd| of itself, and so is their
+    sum, weighed by w_j.  To this comes what fp16 operands lose under 2^-14: with the
+    reference at most 2^8 above the row's largest contribution c = max w_j 2^e_j (and that one
+    taken to 2^6 or more), up to 2^-25 / 2^-2 c of every operand, whose products are with the
+    elements v_j 2^-e_j."""
+    heads = q.shape[1]
+    g = heads // st.kv_heads
+    held = [torch.from_numpy(x).cuda() for x in st.held()]
+    e = st.cache.v_exp.double() - 127
+    refs, tols = [], []
+    for r in rows:
+        s = max(i for i in range(len(st.q)) if st.off[i] <= r)
+        p = st.kv[s] - st.q[s] + r - st.off[s]
+        j = torch.arange(p + 1)
+        if window:
+            j = j[(j > p - window) | (j < sinks)]
+        page, slot = st.table[s][j // st.page].long().cuda(), (j % st.page).cuda()
+        k, v = (x[page, :, slot].repeat_interleave(g, 1) for x in held)          # [keys, heads, dim]
+        ej = torch.exp2(e[page, :, slot].repeat_interleave(g, 1))                # [keys, heads]
+        x = q[r].double()
+        w = torch.softmax(torch.einsum("jhd,hd->jh", k, x) * scale, 0)
+        eps = (st.dim + 2) * 2.0 ** -24 * torch.einsum("jhd,hd->jh", k.abs(), x.abs()) * scale
+        # a factor exp(eps) - 1 where eps is not small; a weight of at most 2^-200 is nothing whatever its error
+        eps = torch.where(w > 2.0 ** -200, torch.expm1(eps), torch.zeros_like(eps))
+        ref = torch.einsum("jh,jhd->hd", w, v)
+        size = torch.einsum("jh,jhd->hd", w, v.abs())
+        most = (w * ej).amax(0)[:, None]
+        refs.append(ref)
+        tols.append(2.0 ** -8 * ref.abs() + size * (2.0 ** -8 + 2.0 ** -12 + torch.einsum("jh,jh->h", w, eps)[:, None])
+                    + torch.einsum("jh,jhd->hd", w * eps, v.abs())
+                    + 2.0 ** -23 * most * torch.einsum("jh,jhd->hd", 1 / ej, v.abs()))
+    return torch.stack(refs).cpu().numpy(), torch.stack(tols).cpu().numpy()
+
+
+@pytest.mark.parametrize("far", [10, 20, 40])
+@pytest.mark.parametrize("form", ["hidden k", "hidden v", "hidden both", "seen k", "seen v", "zeros"])
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("q,kv,heads,kv_heads,page,window,sinks", [
+    ([4, 1], [900, 260], 6, 2, 16, 0, 0),
+    ([40], [900], 4, 2, 32, 0, 0),
+    ([300], [900], 2, 1, 64, 0, 0),
+    ([300, 20], [1500, 700], 4, 1, 16, 200, 3),
+    ([30], [20011], 4, 1, 64, 0, 0),
+])
+def test_attention_over_rows_far_apart(dv, q, kv, heads, kv_heads, page, window, sinks, dim, form, far):
+    """A finite key or value 2^far times the others', hidden from some rows of its tile or seen
+    with next to no weight, takes nothing from the keys beside it; nor does a row of zeros
+    with the largest score beside such a value."""
+    st = Setup(dv, q, kv, kv_heads, dim, page, "e4m3", seed=far + dim)
+    x = st.queries(heads).abs()               # so that a sign decides a score
+    scale = dim ** -0.5
+    g = np.random.default_rng(far)
+    one = lambda f: f * np.abs(g.standard_normal((1, kv_heads, dim)))   # noqa: E731
+    for s, n in enumerate(kv):
+        c = q[s]
+        if form.startswith("hidden"):
+            # a later token of the chunk; every row before it, and (window) rows far behind it, do not see it
+            for at in (n - c + c // 2, n - c):
+                put_tokens(st, s, np.array([at]), k=one(2.0 ** far) if form != "hidden v" else None,
+                           v=one(2.0 ** far) if form != "hidden k" else None)
+        else:
+            for at in (5, n - c - 7, n - c // 2):
+                if at >= n - 1:
+                    continue
+                put_tokens(st, s, np.array([at]), k=one(-2.0 ** far if form == "seen k" else -12.0),
+                           v=one(2.0 ** far) if form != "seen k" else None)
+                if form == "zeros":
+                    put_tokens(st, s, np.array([at + 1]), k=one(3.0), v=one(0.0))
+    got, status = dv.cache_attention(st.cache, st.chunks, x, scale=scale, window=window, sinks=sinks)
+    torch.cuda.synchronize()
+    assert int(status.item()) == dv.OK
+    rows = sorted({0, st.rows - 1, *(st.off[s] + min(i, q[s] - 1) for s in range(len(q))
+                                     for i in (0, 1, q[s] // 4, q[s] // 2 - 1, q[s] // 2, 200, q[s] - 1) if i >= 0)})
+    ref, tol = far64(st, x, scale, rows, window, sinks)
+    err = np.abs(f64(got)[rows] - ref)
+    bad = ~(err <= tol)
+    assert not bad.any(), (f"{bad.sum()} of {bad.size} outside, worst {np.nanmax(err / tol)}, "
+                           f"rows {sorted({rows[i] for i in np.argwhere(bad)[:, 0]})}")

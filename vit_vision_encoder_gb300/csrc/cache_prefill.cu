@@ -40,7 +40,8 @@
 //
 // e4m3 pages: warps 20-27 widen the raw tiles to fp16 in shared memory (the
 // conversion is exact; the rows of a tile are scaled by powers of two to the
-// tile's largest exponent E, and elements 2^-24 below it lose bits).  Scores are
+// tile's largest exponent E, those of a tile whose exponents lie far apart are not:
+// kFar).  Scores are
 // scaled by 2^E(K); the weights are taken against the running maximum of score
 // plus E(V), the size of a contribution, and their sum is scaled back to a reference
 // of its own (Raise in cache_rows.cuh).  Query rows are scaled to fp16's range like
@@ -64,6 +65,13 @@ constexpr int kItemRows = 2 * kTile;
 constexpr int kWarpTma = 16, kWarpMma = 17, kWarpJobs = 18;
 constexpr int kWarpConvert = 20;            // 20 .. 23: key tiles, 24 .. 27: value tiles (e4m3)
 constexpr uint32_t kTmemCols = 512;
+// e4m3: a tile whose rows (those that some row of the item sees) lie further apart than
+// this is taken as it is, and the softmax multiplies by each key's own factors (kFar in
+// place of the tile's exponent).  Keys scaled by 2^-15 are still exact in fp16 (multiples of
+// 2^-9 2^-15).  A row's reference follows the tile's exponent E(V): where the value that has
+// it is hidden from the row, or its weight is nothing, it lies up to kSpanV above the row's
+// largest contribution, and those under 2^(kSpanV - 20) of that one lose bits.
+constexpr int kSpanK = 15, kSpanV = 8, kFar = 1024;
 
 template <int D, bool E4M3>
 struct Cfg {
@@ -355,6 +363,14 @@ template <int D, bool E4M3>
 __device__ __forceinline__ uint32_t tile_piece(uint32_t tile, int r, int piece) {
   return tile + (piece >> 3) * Cfg<D, E4M3>::kHalf + r * 128 + (((piece & 7) ^ (r & 7)) << 4);
 }
+
+// The exponent bytes of keys j .. j + 7 of a sequence, from the pages.
+__device__ __forceinline__ uint2 exponent_bytes(const AttentionArgs& a, const uint8_t* exps, int s, int head, int j) {
+  const int page = __ldg(a.b.table + static_cast<int64_t>(s) * a.b.table_cols + (j >> a.c.page_shift));
+  if (!page_there(page, a.c.n_pages)) return make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu);
+  return __ldg(reinterpret_cast<const uint2*>(exps + cache_row(a.c, page, head, j)));
+}
+__device__ __forceinline__ uint32_t byte_of(uint2 b, int y) { return ((y < 4 ? b.x : b.y) >> (8 * (y & 3))) & 255u; }
 
 template <int D, bool E4M3>
 __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
@@ -736,27 +752,32 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
           ok = __all_sync(0xFFFFFFFFu, mbar_wait(bar(kBarRawFull + raw), (count / C::kRaw) & 1, a.status));
           if (!ok) break;
           const uint8_t* ex = smem + C::kOffExp + raw * kTile;
-          // The largest exponent among rows that some row sees (255 marks a NaN
-          // row), and the factor of one of this warp's 32 rows: lane y has row
+          // The largest and the least exponent among rows that some row sees (255 marks
+          // a NaN row), and the factor of one of this warp's 32 rows: lane y has row
           // kStep (y / kEach) + kEach wc + y % kEach.
-          int top = 0;
+          int top = 0, least = 255;
 #pragma unroll
           for (int y = 0; y < 4; ++y) {
             const int r = 32 * y + lane, e = ex[r];
-            if (any(key0 + r) && e != 255) top = max(top, e);
+            if (any(key0 + r) && e != 255) {
+              top = max(top, e);
+              least = min(least, e);
+            }
           }
           top = __reduce_max_sync(0xFFFFFFFFu, top);
+          least = __reduce_min_sync(0xFFFFFFFFu, least);
+          const bool far = top - least > (part == 0 ? kSpanK : kSpanV);
           if (top == 0) top = 127;
           uint32_t factor;
           {
             const int r = kStep * (lane / kEach) + kEach * wc + lane % kEach;
-            const int e = ex[r], down = top - e;
+            const int e = ex[r], down = far ? 0 : top - e;
             factor = e == 255 ? 0x3C00u : down <= 14 ? (15u - down) << 10 : down <= 24 ? 1u << (24 - down) : 0u;
             factor = any(key0 + r) ? factor | factor << 16 : 0xFFFFFFFFu;      // marks a row that nobody sees
           }
           ok = __all_sync(0xFFFFFFFFu, mbar_wait(bar(kBarKvEmpty + slot), ((count / C::kRing) & 1) ^ 1, a.status));
           if (!ok) break;
-          if (tid == 0) tile_exp[8 * part + (tile & 7)] = top - 127;
+          if (tid == 0) tile_exp[8 * part + (tile & 7)] = far ? kFar : top - 127;
           const uint32_t from = sRaw(raw) + raw_at;
           const uint32_t to0 = sKv(slot) + tile_at0, to1 = sKv(slot) + tile_at1;
 #pragma unroll
@@ -877,6 +898,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
         }
         tc_fence_after();
         float c = c0, ev = 0.f;
+        int ek = 0, e = 0;
         if constexpr (E4M3) {
           // E(V) is known once the value tile is there (it stays until P V).
           const uint32_t nv = 2 * static_cast<uint32_t>(nth) + 1;
@@ -884,21 +906,107 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
             ok = false;
             break;
           }
-        }
-        if constexpr (E4M3) {
-          const int ek = tile_exp[nth & 7], e = tile_exp[8 + (nth & 7)];
+          ek = tile_exp[nth & 7], e = tile_exp[8 + (nth & 7)];
           // Not zero: a masked score of -inf stays -inf.
-          c = fmaxf(c * __int_as_float((ek + 127) << 23), 1e-35f);
+          if (ek != kFar) c = fmaxf(c * __int_as_float((ek + 127) << 23), 1e-35f);
           ev = static_cast<float>(e);
+        }
+        // Key y of this half is seen when y <= last and (y >= from or y < keep): one bit each.
+        const int j0 = key0 + 64 * h;
+        auto seen_keys = [&](int last, int from, int j) {
+          return bits_below(last - j + 1) & (~bits_below(from - j) | bits_below(a.sinks - j));
+        };
+        // With a score tile each, S_X waited for the product that wrote O_X last.
+        auto rescale = [&](float alpha) {
+          if (b == b0 || !__any_sync(0xFFFFFFFFu, alpha != 1.f)) return;
+          if (C::kScores == 3) {
+            if (!mbar_wait(bar(kBarPvDone + x), (step - 1) & 1, a.status)) ok = false;
+            tc_fence_after();
+          }
+#pragma unroll
+          for (int y = 0; y < D / 64; ++y) {
+            uint32_t o[32];
+            tmem_ld32_x2<D / 2>(tO + 32 * y, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int z = 0; z < 32; ++z) o[z] = __float_as_uint(__uint_as_float(o[z]) * alpha);
+            tmem_st32_x2<D / 2>(tO + 32 * y, o);
+          }
+        };
+        const bool far = E4M3 && (ek == kFar || e == kFar);
+        if (far) {
+          // A tile with factors by key.  The weights are added up here; for the products, the
+          // scores give way to those of the contributions (score + e - the row's largest e).
+          // Eight keys at a time, for few registers (out of line or all at once it took
+          // from every tile: a tail chunk 116 and 138 us, 111 so, 108.5 without).
+          // Copies, so that nothing of this is computed ahead of the loop and kept.
+          int seq_no = w.s, head = w.head, last = pos, from = lo, j1 = j0;
+          asm volatile("" : "+r"(seq_no), "+r"(head), "+r"(last), "+r"(from), "+r"(j1));
+          const uint64_t seen = seen_keys(last, from, j1);
+          float s8[8], top = -INFINITY, largest = -INFINITY;
+          auto load = [&](int g) {
+            uint32_t r8[8];
+            __syncwarp();
+            tmem_ld8_x2<64>(tS + g, r8);
+            tmem_wait_ld();
+#pragma unroll
+            for (int y = 0; y < 8; ++y) s8[y] = tmem_after_wait(__uint_as_float(r8[y]));
+          };
+          auto store = [&](int g) {
+            uint32_t r8[8];
+#pragma unroll
+            for (int y = 0; y < 8; ++y) r8[y] = __float_as_uint(s8[y]);
+            __syncwarp();
+            tmem_st8_x2<64>(tS + g, r8);
+          };
+          // Exponent bytes of keys g .. g + 7, of which some are seen (they lie in a page then).
+          auto bytes = [&](const uint8_t* exps, int g) {
+            return (seen >> g) & 255u ? exponent_bytes(a, exps, seq_no, head, j1 + g) : make_uint2(0, 0);
+          };
+          auto value_exponent = [&](uint2 v, int y) {
+            return e == kFar ? static_cast<float>(static_cast<int>(byte_of(v, y)) - 127) : static_cast<float>(e);
+          };
+#pragma unroll 1
+          for (int g = 0; g < 64; g += 8) {
+            const uint2 kb = bytes(a.c.k_exp, g), vb = bytes(a.c.v_exp, g);
+            load(g);
+#pragma unroll
+            for (int y = 0; y < 8; ++y) {
+              const bool on = (seen >> (g + y)) & 1u;
+              const float f = ek == kFar ? c0 * __uint_as_float(byte_of(kb, y) << 23) : c;
+              s8[y] = on ? s8[y] * f : -INFINITY;
+              top = fmaxf(top, s8[y]);
+              if (on) largest = fmaxf(largest, value_exponent(vb, y));
+            }
+            store(g);
+          }
+          tmem_wait_st();
+          largest = fmaxf(largest, __shfl_xor_sync(0xFFFFFFFFu, largest, 16));
+          ev = fminf(fmaxf(largest, -127.f), 120.f);       // 128: a row of NaN
+          const Raise up = raised(m, d, fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 16)), -INFINITY);
+          m = up.m, d = up.d, l *= up.l;
+          rescale(up.o);
+#pragma unroll 1
+          for (int g = 0; g < 64; g += 8) {
+            const uint2 vb = bytes(a.c.v_exp, g);
+            load(g);
+#pragma unroll
+            for (int y = 0; y < 8; ++y) {
+              if (s8[y] == -INFINITY) continue;            // hidden, its value's exponent may be anything
+              l += ex2_approx(s8[y] - m);
+              s8[y] += value_exponent(vb, y) - ev;
+            }
+            store(g);
+          }
+          tmem_wait_st();
+          c = 1.f;
         }
         uint32_t sr[64];
         float top = tmem_ld32_max_x2<64>(tS, sr), top2 = tmem_ld32_max_x2<64>(tS + 32, sr + 32);
         tmem_wait_ld();
         top = fmaxf(tmem_after_wait(top), tmem_after_wait(top2));
         if (!open) {
-          // Key y of this half is seen when y <= last and (y >= from or y < keep): one bit each.
-          const int j0 = key0 + 64 * h;
-          const uint64_t seen = bits_below(pos - j0 + 1) & (~bits_below(lo - j0) | bits_below(a.sinks - j0));
+          const uint64_t seen = seen_keys(pos, lo, j0);
           const uint32_t s0 = static_cast<uint32_t>(seen), s1 = static_cast<uint32_t>(seen >> 32);
           float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
@@ -919,7 +1027,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
           // values far below the row's largest) they are zeros in fp16 all the same.
           const float x = fmaxf(ev - d, -60.f);
           off = m == -INFINITY ? 0.f : x - m;
-          unit = __int_as_float(max(127 - static_cast<int>(x), 0) << 23);
+          unit = far ? 0.f : __int_as_float(max(127 - static_cast<int>(x), 0) << 23);
         } else {
           if (reach > m + C::kLag16) {       // always true on the first visible key (m = -inf)
             alpha = ex2_approx(m - reach);
@@ -947,22 +1055,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
         // This half's share of the row sum.
         l = E4M3 ? fmaf(s0 + s1, unit, l) : fmaf(l, alpha, s0 + s1);
         tmem_st32_x2<32>(tS, pk);
-        // With a score tile each, S_X waited for the product that wrote O_X last.
-        if (b != b0 && __any_sync(0xFFFFFFFFu, alpha != 1.f)) {
-          if (C::kScores == 3) {
-            if (!mbar_wait(bar(kBarPvDone + x), (step - 1) & 1, a.status)) ok = false;
-            tc_fence_after();
-          }
-#pragma unroll
-          for (int y = 0; y < D / 64; ++y) {
-            uint32_t o[32];
-            tmem_ld32_x2<D / 2>(tO + 32 * y, o);
-            tmem_wait_ld();
-#pragma unroll
-            for (int z = 0; z < 32; ++z) o[z] = __float_as_uint(__uint_as_float(o[z]) * alpha);
-            tmem_st32_x2<D / 2>(tO + 32 * y, o);
-          }
-        }
+        rescale(alpha);
         tmem_wait_st();
         tc_fence_before();
         mbar_arrive(bar(kBarPFull + at));
