@@ -1010,3 +1010,25 @@ def test_attention_over_rows_far_apart(dv, q, kv, heads, kv_heads, page, window,
     bad = ~(err <= tol)
     assert not bad.any(), (f"{bad.sum()} of {bad.size} outside, worst {np.nanmax(err / tol)}, "
                            f"rows {sorted({rows[i] for i in np.argwhere(bad)[:, 0]})}")
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (100, 5)])
+def test_same_bits_over_many_calls(dv, dim, kind, window, sinks):
+    """Ragged chunks of few key tiles: a warp that is done with its item's last tile while others
+    are two products behind must not take an earlier product's completion for its last one's."""
+    q, kv = [8 + 9 * i % 76 for i in range(56)], [90 + 41 * i % 537 for i in range(56)]
+    st = Setup(dv, q, kv, 4, dim, 32, kind, seed=dim + len(q), fill=math.nan)
+    x = st.queries(64)
+    flush = torch.empty(300 << 20, dtype=torch.uint8, device="cuda")
+    first, status = dv.cache_attention(st.cache, st.chunks, x, window=window, sinks=sinks)
+    differ = torch.zeros((), dtype=torch.int64, device="cuda")
+    for i in range(600):
+        if i % 2 == 0:
+            flush.fill_(i % 251)
+        got, _ = dv.cache_attention(st.cache, st.chunks, x, window=window, sinks=sinks, status=status)
+        differ += (got != first).sum()
+    torch.cuda.synchronize()
+    assert int(status.item()) == dv.OK
+    assert bool(torch.isfinite(first).all()) and int(differ.item()) == 0
