@@ -918,16 +918,17 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
         };
         // O_X times alpha.  With a score tile each, S_X waited for the product that wrote O_X last.
         // With three, a warp may come here before that product was even issued (others of
-        // its tile being a step behind), and every step waits for it, also where alpha is 1:
-        // a warp two products ahead would mistake the parity of the last but two for the
-        // last one's at the item's end and leave without both.
+        // its tile being a step behind).  The item's last step waits for it in any case: a warp two
+        // products ahead would mistake the parity of the last but two for the last one's
+        // at the item's end and leave without both.
         auto rescale = [&](float alpha) {
-          if (b == b0) return;
+          const bool change = __any_sync(0xFFFFFFFFu, alpha != 1.f);
+          if (b == b0 || !(change || (C::kScores == 3 && b + stride >= w.end))) return;
           if (C::kScores == 3) {
             if (!mbar_wait(bar(kBarPvDone + x), (step - 1) & 1, a.status)) ok = false;
             tc_fence_after();
           }
-          if (!__any_sync(0xFFFFFFFFu, alpha != 1.f)) return;
+          if (!change) return;
 #pragma unroll
           for (int y = 0; y < D / 64; ++y) {
             uint32_t o[32];
