@@ -1032,3 +1032,41 @@ def test_same_bits_over_many_calls(dv, dim, kind, window, sinks):
     torch.cuda.synchronize()
     assert int(status.item()) == dv.OK
     assert bool(torch.isfinite(first).all()) and int(differ.item()) == 0
+
+
+@pytest.mark.parametrize("first", [1, 3])
+@pytest.mark.parametrize("q,kv,dim,window,sinks", [([4], [200], 128, 0, 0), ([4], [200], 64, 20, 3),
+                                                   ([70], [300], 128, 0, 0), ([70], [300], 64, 30, 5),
+                                                   ([70, 70], [300, 70], 128, 0, 0)])
+def test_first_scores_of_minus_infinity(dv, q, kv, dim, window, sinks, first):
+    """Keys with an infinity against the query weigh nothing, in rows too that are computed
+    again because a value hidden from them is not finite."""
+    st = Setup(dv, q, kv, 2, dim, 16, "bf16", seed=9)
+    x = st.queries(4)
+    x[..., 3] = x[..., 3].abs() + 0.5
+    for j in range(first):
+        _plant(st, 0, j, 1, -math.inf, "k")
+    bad = kv[0] - q[0] + q[0] // 2
+    _plant(st, 0, bad, 1, math.nan, "v")
+    got, status = dv.cache_attention(st.cache, st.chunks, x, window=window, sinks=sinks)
+    torch.cuda.synchronize()
+    assert int(status.item()) == dv.OK
+    got = f64(got)
+    # the definition without those keys, with attention64's tolerance; the infinity's element plays no part in it
+    k, v = (y[:, 1] for y in (st.tokens(h, 0) for h in st.held()))
+    for i in (0, q[0] // 2 - 1):
+        p = kv[0] - q[0] + i
+        j = np.arange(first, p + 1)
+        if window:
+            j = j[(j > p - window) | (j < sinks)]
+        for h in (2, 3):
+            qq = f64(x[i, h])
+            z = k[j] @ qq * dim ** -0.5
+            w = np.exp(z - z.max())
+            w /= w.sum()
+            big = (np.abs(k[j]) @ np.abs(qq)).max() * dim ** -0.5
+            ref = w @ v[j]
+            tol = 2.0 ** -8 * np.abs(ref) + (w @ np.abs(v[j])) * (2.0 ** -8 + 2.0 ** -12 + 2 * (dim + 2) * 2.0 ** -24 * big)
+            assert (np.abs(got[i, h] - ref) <= tol).all()
+    sees = [i for i in range(q[0] // 2, q[0]) if not window or bad > kv[0] - q[0] + i - window]
+    assert np.isnan(got[sees, 2:, 3]).all()

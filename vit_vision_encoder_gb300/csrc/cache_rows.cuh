@@ -48,7 +48,8 @@ __device__ __noinline__ void exact_row(const AttentionArgs& a, int s, int row0, 
     d *= a.scale_log2;
     const float m_new = fmaxf(m, d);
     const float alpha = m == m_new ? 1.f : exp2f(m - m_new);
-    const float w = exp2f(d - m_new);
+    // A score of -inf weighs nothing, also while there is no other (NaN stays NaN).
+    const float w = d == -INFINITY ? 0.f : exp2f(d - m_new);
     l = l * alpha + w;
 #pragma unroll
     for (int x = 0; x < kPer; ++x) o[x] = o[x] * alpha + w * vx[x];
