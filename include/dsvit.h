@@ -483,7 +483,9 @@ int ds_vit_cache_read(const ds_vit_cache* cache, const ds_vit_chunks* chunks, vo
  *   ws:     device workspace, 16-byte aligned, of at least
  *           ds_vit_cache_attention_workspace_bytes (DS_VIT_ECAP otherwise);
  *           needs no initial value.  Calls that may overlap on the GPU need
- *           workspaces of their own.
+ *           workspaces of their own, and so do calls that several host threads
+ *           make on one stream (a call makes two launches, between which
+ *           another thread's may come).
  * A bounded wait that gives up records DS_VIT_ETIMEOUT in *status.
  */
 int ds_vit_cache_attention_workspace_bytes(const ds_vit_cache* cache, const ds_vit_chunks* chunks, int32_t heads,

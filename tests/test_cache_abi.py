@@ -1,6 +1,7 @@
 """The paged-cache entry points' argument checks, without a GPU: every refusal
 comes before any CUDA call, so made-up pointers are never followed."""
 import ctypes as C
+import threading
 
 import pytest
 
@@ -134,3 +135,32 @@ def test_binding_refuses_other_tensors(dv):
         dv.cache_attention(cache, ch, z((5, 4, 64)), out=z((5, 2, 64)), status=st)
     with pytest.raises(dv.DsVitError):
         dv.cache_read(cache, ch, 5, out=(z((4, 2, 64)), z((4, 2, 64))), status=st)
+
+
+def test_each_thread_has_a_workspace(dv, monkeypatch):
+    """Threads that share a stream do not share the workspace kept for it: a call makes two
+    launches, and another thread's may come between them."""
+    torch = pytest.importorskip("torch")
+    z = lambda shape, t=torch.bfloat16: torch.zeros(shape, dtype=t)   # noqa: E731
+    cache = dv.KvCache(z((3, 2, 16, 64)), z((3, 2, 16, 64)))
+    ch = dv.Chunks(z(3, torch.int32), z(2, torch.int32), z((2, 4), torch.int32), 1)
+    monkeypatch.setattr(dv, "_capturing", lambda: False)
+    got, both = {}, threading.Barrier(3, timeout=60)
+
+    def thread(name):
+        a = dv._workspace(cache, ch, 4, 77)
+        got[name] = a, dv._workspace(cache, ch, 4, 77), dv._workspace(cache, ch, 4, 78)
+        both.wait()                     # all are alive at once
+
+    threads = [threading.Thread(target=thread, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    both.wait()
+    for t in threads:
+        t.join()
+    mine = dv._workspace(cache, ch, 4, 77)
+    places = [mine.data_ptr()]
+    for a, again, other in got.values():
+        assert a.data_ptr() == again.data_ptr()
+        places += [a.data_ptr(), other.data_ptr()]
+    assert len(set(places)) == 5

@@ -1070,3 +1070,33 @@ def test_first_scores_of_minus_infinity(dv, q, kv, dim, window, sinks, first):
             assert (np.abs(got[i, h] - ref) <= tol).all()
     sees = [i for i in range(q[0] // 2, q[0]) if not window or bad > kv[0] - q[0] + i - window]
     assert np.isnan(got[sees, 2:, 3]).all()
+
+
+@pytest.mark.parametrize("rows", [1, 40])
+def test_two_threads_on_one_stream(dv, rows):
+    """Threads whose calls, split between workers, come between one another's launches on the
+    default stream."""
+    import threading
+    sets = []
+    for seed, n in ((41, 9000), (42, 7000)):
+        st = Setup(dv, [rows, rows + 1], [n, 300 + seed], 2, 128, 64, "bf16", seed=seed)
+        x = st.queries(8)
+        sets.append((st, x, dv.cache_attention(st.cache, st.chunks, x)[0]))
+    torch.cuda.synchronize()
+    start, wrong = threading.Barrier(2, timeout=60), [None, None]
+
+    def thread(i):
+        st, x, want = sets[i]
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        differ = torch.zeros((), dtype=torch.int64, device="cuda")
+        start.wait()
+        for _ in range(300):
+            differ += (dv.cache_attention(st.cache, st.chunks, x, status=status)[0] != want).sum()
+        wrong[i] = int(differ.item()), int(status.item())
+
+    threads = [threading.Thread(target=thread, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert wrong == [(0, dv.OK)] * 2

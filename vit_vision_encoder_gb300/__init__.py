@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes as C
 import os
+import threading
 
 import numpy as np
 
@@ -672,28 +673,37 @@ def cache_attention_workspace_bytes(cache, chunks, heads):
     return nb
 
 
-_workspaces = {}   # of cache_attention: (device, stream) -> tensor
+class _Workspaces(threading.local):
+    """Of cache_attention, for each host thread: (device, stream) -> tensor.  A call makes
+    two launches, and another thread's may come between them on the same stream."""
+
+    def __init__(self):
+        self.held = {}
+
+
+_workspaces = _Workspaces()
 
 
 def _workspace(cache, chunks, heads, stream):
-    """A workspace that nothing else uses while the call's kernels run: the one kept
-    for the stream, whose calls follow one another; a graph under capture gets one
-    of its own."""
+    """A workspace that nothing else uses while the call's kernels run: the one that this
+    thread keeps for the stream, whose calls follow one another; a graph under capture gets
+    one of its own."""
     need = cache_attention_workspace_bytes(cache, chunks, heads)
     if _capturing():
         return _torch().empty(need, dtype=_u8, device=cache.device)
     key = cache.device_index, stream
-    ws = _workspaces.get(key)
+    ws = _workspaces.held.get(key)
     if ws is None or ws.numel() < need:
-        ws = _workspaces[key] = _torch().empty(need, dtype=_u8, device=cache.device)
+        ws = _workspaces.held[key] = _torch().empty(need, dtype=_u8, device=cache.device)
     return ws
 
 
 def cache_attention(cache, chunks, q, scale=None, window=0, sinks=0, out=None, ws=None, status=None):
     """Attention of the packed rows q (bf16 [rows, heads, head_dim], rows may be
     strided) over the cache (ds_vit_cache_attention); scale defaults to
-    head_dim ** -0.5.  ``ws``: uint8 workspace (calls that may overlap need one
-    each; when not given, one is kept for each stream).  Returns (out, status)."""
+    head_dim ** -0.5.  ``ws``: uint8 workspace (calls that may overlap, or that other
+    threads make on the same stream, need one each; when not given, each thread keeps one
+    for each stream, up to 41 MB, until it ends).  Returns (out, status)."""
     d, stream, status = _on_device(cache, chunks, status, "ds_vit_cache_attention")
     if q.dim() != 3:
         _refuse("ds_vit_cache_attention")
