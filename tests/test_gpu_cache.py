@@ -1100,3 +1100,91 @@ def test_two_threads_on_one_stream(dv, rows):
     for t in threads:
         t.join()
     assert wrong == [(0, dv.OK)] * 2
+
+
+@pytest.mark.parametrize("n,c,kv,heads,dim,kind", [
+    (152, 2, 400000, 16, 64, "bf16"), (152, 2, 200000, 16, 128, "e4m3"),      # many rows: an item a CTA and more
+    (1024, 2, 100000, 4, 128, "bf16"), (1024, 2, 100000, 8, 64, "e4m3"),      # few rows: several items a worker
+    (2, 40, 150000, 4, 128, "bf16"), (1, 3, 300000, 4, 64, "e4m3"),           # items split between workers
+])
+def test_hidden_value_behind_a_long_cache(dv, n, c, kv, heads, dim, kind):
+    """Rows to be computed again over long caches (shared by the sequences): it takes its time, and
+    no wait runs into its limit meanwhile.  The newest token's value, seen by the last
+    row alone, is not finite."""
+    st = Setup(dv, [c], [kv], 1, dim, 128, kind, seed=19)
+    rows = torch.randn((n * c, heads, dim), generator=st.g).bfloat16().cuda()
+    off = torch.arange(0, n * c + 1, c, dtype=torch.int32, device="cuda")
+    chunks = dv.Chunks(off, torch.full((n,), kv, dtype=torch.int32, device="cuda"),
+                       st.table.cuda().expand(n, -1).contiguous(), c)
+    clean, _ = dv.cache_attention(st.cache, chunks, rows)
+    _plant(st, 0, kv - 1, 0, math.nan, "v")
+    got, status = dv.cache_attention(st.cache, chunks, rows)
+    torch.cuda.synchronize()
+    assert int(status.item()) == dv.OK
+    assert bool(torch.isnan(got[c - 1::c, :, 3]).all())
+    hidden = torch.ones(n * c, dtype=torch.bool, device="cuda")
+    hidden[c - 1::c] = False
+    a, b = got[hidden].float(), clean[hidden].float()
+    # Both within attention64's tolerance of one value, so at most twice that apart; of it, taken from
+    # what is at hand: 2^-8 |o|, and A (2^-8 + 2^-12 + 2 (dim + 2) 2^-24 big) with the weighed mean size A of the
+    # values and the largest sum |q_d k_d| scale, `big`, each bounded over all rows.
+    assert bool(torch.isfinite(a).all())
+    held = [torch.from_numpy(x).cuda() for x in st.held()]
+    k, v = (st.tokens(x.cpu().numpy(), 0)[:kv - 1, 0] for x in held)
+    picks = [0, int(hidden.nonzero()[-1])]
+    for r in picks:
+        s, i = divmod(r, c)
+        p = kv - c + i
+        kk, vv = torch.from_numpy(k[:p + 1]).cuda(), torch.from_numpy(v[:p + 1]).cuda()
+        q = rows[r].double()
+        w = torch.softmax(q @ kk.T * dim ** -0.5, 1)
+        ref, size = w @ vv, w @ vv.abs()
+        big = (q.abs() @ kk.abs().T).amax(1, keepdim=True) * dim ** -0.5
+        tol = 2.0 ** -8 * ref.abs() + size * (2.0 ** -8 + 2.0 ** -12 + 2 * (dim + 2) * 2.0 ** -24 * big)
+        assert bool(((got[r].double() - ref).abs() <= tol).all())
+    # every row against the same of the clean call: rows of one position share keys, sizes are alike to a factor of two
+    top = 2 * float(size.max())
+    lim = 2 * (2.0 ** -8 * b.abs() + top * (2.0 ** -8 + 2.0 ** -12 + 2 * (dim + 2) * 2.0 ** -24 * 2 * float(big.max())))
+    assert bool(((a - b).abs() <= lim).all())
+
+
+@pytest.mark.parametrize("q,kv,kind", [([4, 1], [200, 90], "bf16"), ([70, 3], [300, 70], "bf16"), ([70, 3], [300, 70], "e4m3"),
+                                       ([300], [2000], "bf16")])
+def test_values_seen_and_hidden_that_are_not_finite(dv, q, kv, kind):
+    """An infinity or NaN among the first tokens, seen by every row, stays in its elements; with
+    another one hidden from the earlier rows, those have the first one's alone."""
+    st = Setup(dv, q, kv, 2, 128, 16, kind, seed=23)
+    x = st.queries(4)
+    page, slot = int(st.table[0, 0]), 5
+    if kind == "bf16":
+        st.cache.v[page, 1, slot, 7] = math.inf
+    seen, status = dv.cache_attention(st.cache, st.chunks, x)
+    bad = kv[0] - q[0] // 2
+    _plant(st, 0, bad, 1, math.nan, "v")
+    both, _ = dv.cache_attention(st.cache, st.chunks, x, status=status)
+    torch.cuda.synchronize()
+    assert int(status.item()) == dv.OK
+    ref, tol = sampled64(st, x, 128 ** -0.5, rows := [0, q[0] // 4, bad - kv[0] + q[0] - 1])
+    for i, r in enumerate(rows):
+        for y in (seen, both):
+            y = f64(y[r])
+            if kind == "bf16":
+                assert (y[2:, 7] == math.inf).all()
+            rest = np.arange(128) != 7
+            assert np.isfinite(y[:, rest]).all() and (np.abs(y - ref[i])[:, rest] <= tol[i][:, rest]).all()
+    late = f64(both[bad - kv[0] + q[0]:q[0]])
+    assert np.isnan(late[:, 2:, 3]).all() and np.isfinite(late[:, :2]).all()
+
+
+def test_front_padding_beside_hidden_values(dv):
+    """Rows in front of position 0 stay zeros beside tokens that are not finite."""
+    for kind in ("bf16", "e4m3"):
+        for heads in (4, 64):
+            st = Setup(dv, [9, 40], [4, 30], 2, 64, 16, kind, seed=24)
+            _plant(st, 0, 3, 1, math.nan, "v")
+            _plant(st, 1, 20, 0, math.nan, "v")
+            got, status = dv.cache_attention(st.cache, st.chunks, st.queries(heads))
+            torch.cuda.synchronize()
+            assert int(status.item()) == dv.OK
+            got = f64(got)
+            assert (got[:5] == 0).all() and (got[9:19] == 0).all() and np.isfinite(got[5:8]).all()

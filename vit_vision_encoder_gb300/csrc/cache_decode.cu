@@ -333,6 +333,7 @@ __global__ void __launch_bounds__(Shape<D, E4M3>::kThreads, 1)
   uint32_t phase = 0;
   SplitHeader header{};
   bool dead = false;                       // a wait gave up
+  bool marked = false;                     // whole items have rows that may be to compute again
   for (int64_t u = pl.begin; u < pl.end;) {
     const Item it = item_at<S::kKeyShift>(a, pl, u);
     const int R = min(it.q.c * a.group - it.rho0, kRows);       // rows of this item
@@ -617,7 +618,7 @@ __global__ void __launch_bounds__(Shape<D, E4M3>::kThreads, 1)
       header = SplitHeader{static_cast<int>(shares.owner(last) - me) + 1, it.s, it.head, it.rho0, it.q, 0};
     }
     float* r = rec.at(me, begun ? 0 : 1);
-    uint32_t redo = 0;
+    bool redo = false;                     // a row that may be to compute again
 #pragma unroll
     for (int x = 0; x < kRowHalves; ++x) {
       const int rr0 = 8 * x + g, rho = it.rho0 + rr0;
@@ -625,7 +626,8 @@ __global__ void __launch_bounds__(Shape<D, E4M3>::kThreads, 1)
       if (rr0 < R) {
         const int i = a.by_group(rho);
         bf16* dst = a.out + (it.q.row0 + i) * a.out_stride + (it.head * a.group + rho - i * a.group) * D;
-        const float inv = pos[x] < 0 ? 0.f : 1.f / l[x], up = E4M3 ? shift_up(d[x]) : 1.f;
+        const float inv = 1.f / l[x], up = E4M3 ? shift_up(d[x]) : 1.f;
+        auto value = [&](float y) { return pos[x] < 0 ? 0.f : y * inv * up; };
         float* rr = r + rr0 * D;
         if (!whole && t == 0) {
           rec.max_of(r, D)[rr0] = m[x];
@@ -642,7 +644,7 @@ __global__ void __launch_bounds__(Shape<D, E4M3>::kThreads, 1)
             for (int n = 0; n < kCols; n += 4) {
               float4 y = make_float4(o[n][2 * x + e], o[n + 1][2 * x + e], o[n + 2][2 * x + e], o[n + 3][2 * x + e]);
               if (whole) {
-                y = make_float4(y.x * inv * up, y.y * inv * up, y.z * inv * up, y.w * inv * up);
+                y = make_float4(value(y.x), value(y.y), value(y.z), value(y.w));
                 bad |= not_finite(y.x) || not_finite(y.y) || not_finite(y.z) || not_finite(y.w);
                 *reinterpret_cast<uint2*>(dst + d0 + n) = make_uint2(pack_bf16x2(y.x, y.y), pack_bf16x2(y.z, y.w));
               } else {
@@ -653,30 +655,20 @@ __global__ void __launch_bounds__(Shape<D, E4M3>::kThreads, 1)
         } else {
 #pragma unroll
           for (int n = 0; n < kCols; ++n) {
-            const float y0 = o[n][2 * x], y1 = o[n][2 * x + 1];
+            float y0 = o[n][2 * x], y1 = o[n][2 * x + 1];
             if (whole) {
-              bad |= not_finite(y0 * inv) || not_finite(y1 * inv);
-              *reinterpret_cast<uint32_t*>(dst + 8 * n + 2 * t) = pack_bf16x2(y0 * inv, y1 * inv);
+              y0 = value(y0), y1 = value(y1);
+              bad |= not_finite(y0) || not_finite(y1);
+              *reinterpret_cast<uint32_t*>(dst + 8 * n + 2 * t) = pack_bf16x2(y0, y1);
             } else {
               *reinterpret_cast<float2*>(rr + 8 * n + 2 * t) = make_float2(y0, y1);
             }
           }
         }
       }
-      if (it.q.c > 1) {
-        const uint32_t lanes = __ballot_sync(0xFFFFFFFFu, bad);
-#pragma unroll
-        for (int y = 0; y < 8; ++y)
-          if ((lanes >> (4 * y)) & 15u) redo |= 1u << (8 * x + y);
-      }
+      redo |= bad && it.q.c > 1;
     }
-    while (redo) {
-      __syncwarp();
-      const int rho = it.rho0 + __ffs(static_cast<int>(redo)) - 1;
-      redo &= redo - 1;
-      const int i = a.by_group(rho);
-      exact_row<D, E4M3>(a, it.s, it.q.row0, p_first + i, i, it.head * a.group + rho - i * a.group, lane);
-    }
+    marked |= redo;
     u += it.end - it.b;
   }
   if (dead) {
@@ -690,6 +682,19 @@ __global__ void __launch_bounds__(Shape<D, E4M3>::kThreads, 1)
     }
   }
   if (lane == 0) rec.headers[me] = dead ? SplitHeader{} : header;
+  // Rows to compute again, now that the producer has nothing left to wait for.
+  if (!dead && __any_sync(0xFFFFFFFFu, marked))
+    for (int64_t u = pl.begin; u < pl.end;) {
+      const Item it = item_at<S::kKeyShift>(a, pl, u);
+      u += it.end - it.b;
+      if (it.b != 0 || it.end != it.kb.count || it.q.c <= 1) continue;
+      const int p0 = it.q.kv - it.q.c, p1 = it.q.kv - 1, end = min(it.rho0 + kRows, it.q.c * a.group);
+      for (int rho = it.rho0; rho < end; ++rho) {
+        const int i = a.by_group(rho), h = it.head * a.group + rho - i * a.group;
+        if (row_not_finite<D>(a, it.q.row0 + i, h, lane))
+          mend_row<D, E4M3>(a, it.s, it.q.row0, p0 + i, i, h, p0, p1, lane);
+      }
+    }
 }
 
 // Joins the parts of every split item.  Block (y, x) looks after workers x, x +
@@ -701,7 +706,7 @@ constexpr int kJoinItems = 16;    // workers per block at most
 constexpr int kJoinRows = 8;      // grid rows at most
 
 template <int D, bool E4M3>
-__global__ void __launch_bounds__(32 * kJoinWarps)
+__global__ void __launch_bounds__(32 * kJoinWarps, 4)
     join_kernel(const __grid_constant__ AttentionArgs a, const Records rec, int workers) {
   __shared__ SplitHeader heads[kJoinItems];
   grid_dep_launch();
@@ -720,17 +725,21 @@ __global__ void __launch_bounds__(32 * kJoinWarps)
     const int w = group + k * groups;
     const int64_t left = static_cast<int64_t>(hd.q.c) * a.group - hd.rho0;
     const int rows = left < rec.rows ? static_cast<int>(left) : rec.rows;
+    auto positions = [&](int& p0, int& p1) {         // a sequence's items share the key blocks
+      p0 = hd.q.kv - hd.q.c;
+      p1 = hd.q.kv - 1;
+    };
     for (int row = blockIdx.x; row < rows; row += gridDim.x) {
       Sum<D> sum;
       if (hd.parts <= kJoinWarps) {
         if (turn++ % kJoinWarps != warp) continue;
         join_parts<D, E4M3, 4>(rec, w, hd.parts, row, 0, 1, lane, sum);
-        join_finish<D, E4M3>(a, hd, hd.rho0 + row, sum, lane);
+        join_finish<D, E4M3>(a, hd, hd.rho0 + row, sum, lane, positions);
         continue;
       }
       join_parts<D, E4M3, 4>(rec, w, hd.parts, row, warp, kJoinWarps, lane, sum);
       join_warps<D, E4M3>(warp, lane, sum);
-      if (warp == 0) join_finish<D, E4M3>(a, hd, hd.rho0 + row, sum, lane);
+      if (warp == 0) join_finish<D, E4M3>(a, hd, hd.rho0 + row, sum, lane, positions);
     }
   }
 }

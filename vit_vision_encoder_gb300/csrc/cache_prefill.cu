@@ -49,8 +49,9 @@
 //
 // Keys that a row does not see are masked in its scores.  Value rows that no row
 // of the item sees are zeroed in shared memory (they may hold anything); where
-// rows of an item see different keys and a result is not finite, the row is
-// computed again from the keys that it does see (exact_row).
+// rows of an item see different keys and a result is not finite because of a value
+// hidden from it, the row is computed again from the keys that it does see (mend_row):
+// by the join, as waits here have a limit.
 #include "cache_rows.cuh"
 
 #include <type_traits>
@@ -120,11 +121,6 @@ enum : int {
   kBarCount = 46
 };
 
-struct PrefillArgs {
-  AttentionArgs a;
-  Records rec;
-};
-
 // Where a CTA's share of the units begins, and how many it has; how far
 // borders move to an item's end.
 struct Start {
@@ -132,6 +128,11 @@ struct Start {
   int64_t units, total, first;
   int snap;
 };
+struct PrefillArgs {
+  AttentionArgs a;
+  Records rec;
+};
+
 // Shares are counted in key tiles, an item weighing kItemCost more than it has:
 // what its rows' way in and out takes (5 us; a tile takes 1.4).
 constexpr int kItemCost = 4;
@@ -435,9 +436,10 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
   grid_dep_launch();
   grid_dep_wait();
   const Start st = make_plan<C::kThreads>(a, smem + C::kOffKv, blockIdx.x == 0 ? a.status : nullptr);
+  __shared__ int consumed, marked;
+  if (threadIdx.x == 0) marked = 0;
   fence_proxy_async_smem();                 // the scratch becomes the ring
   __syncthreads();
-  __shared__ int consumed;
   // Job n of the ring: every thread of a role's warp reads it, then one of them hands the slot back.
   auto take = [&](int n, Job& j) {
     const int i = n % kJobs;
@@ -1126,9 +1128,8 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
           }
         }
       };
-      uint32_t redo = 0;
       if (w.whole == 1) {
-        const float inv = pos < 0 ? 0.f : 1.f / l, up = E4M3 ? shift_up(d) : 1.f;
+        const float inv = 1.f / l, up = E4M3 ? shift_up(d) : 1.f;
         bool bad = false;
 #pragma unroll 1
         for (int y = 0; y < D / 64; ++y) {
@@ -1138,7 +1139,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
           for (int z = 0; z < 16; ++z) {
             const float o0 = __uint_as_float(o[2 * z]) * inv * up, o1 = __uint_as_float(o[2 * z + 1]) * inv * up;
             bad |= not_finite(o0) || not_finite(o1);
-            o[z] = pack_bf16x2(o0, o1);
+            o[z] = pos < 0 ? 0u : pack_bf16x2(o0, o1);
           }
 #pragma unroll
           for (int z = 0; z < 4; ++z)
@@ -1156,10 +1157,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
             *reinterpret_cast<uint4*>(a.out + (w.q.row0 + i) * a.out_stride +
                                       (w.head * a.group + rho0 + rr - i * a.group) * D + piece * 8) = v;
         }
-        if (w.q.c > 1) {
-          redo = __ballot_sync(0xFFFFFFFFu, bad && rho < R);
-          redo = (redo | (redo >> 16)) & 0xFFFFu;
-        }
+        if (w.q.c > 1 && bad) marked = 1;
       } else {
         float* rec = p.rec.at(blockIdx.x, w.whole == 2 ? 0 : 1);
         if (h == 0) {
@@ -1192,13 +1190,6 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
       tc_fence_before();
       if (paired) mbar_arrive(bar(kBarMerged));
       __syncwarp();                          // the rows' places are free for the next item's
-      while (redo) {
-        const int y = __ffs(static_cast<int>(redo)) - 1;
-        redo &= redo - 1;
-        const int rho_y = rho0 + row0 + y, iy = a.by_group(rho_y);
-        exact_row<D, E4M3>(a, w.s, w.q.row0, first + iy, iy, w.head * a.group + rho_y - iy * a.group, lane);
-        __syncwarp();
-      }
     }
   }
 
@@ -1218,6 +1209,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);
   }
+  if (threadIdx.x == 32 * kWarpJobs) p.rec.headers[blockIdx.x].marked = marked;
 }
 
 // Adds up the records of the split items and writes their rows: all those rows in one
@@ -1227,6 +1219,31 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
 // items it took 16).  Where the rows are few, the warps of a block share a row's parts.
 constexpr int kMaxCtas = 256;        // of the kernel above; a thread here looks at each
 constexpr int kJoinBlocks = 4;       // per SM
+
+// All rows of whole items that are not finite: computed again where they have to be.  A rare
+// pass over the whole output, by all warps of the join; out of line, and looking up what
+// belongs to a row, for the join's registers (walking the shares' items, 3 us a tail chunk).
+template <int D, bool E4M3>
+__device__ __noinline__ void mend_rows(const AttentionArgs& a, const SplitHeader* heads, int workers, int warp, int lane) {
+  const int64_t total = static_cast<int64_t>(a.b.rows) * a.heads, step = static_cast<int64_t>(gridDim.x) * kJoinWarps;
+  for (int64_t x = static_cast<int64_t>(blockIdx.x) * kJoinWarps + warp; x < total; x += step) {
+    const int r = static_cast<int>(x / a.heads), h = static_cast<int>(x - static_cast<int64_t>(r) * a.heads);
+    if (!row_not_finite<D>(a, r, h, lane)) continue;
+    const int s = find_seq(a.b, r, lane);
+    if (s < 0) continue;
+    const Seq q = load_seq(a.b, a.c.page_shift, s, nullptr);
+    const int i = r - q.row0, head = h / a.group;
+    if (i < 0 || i >= q.c || q.c <= 1) continue;
+    const int k = (i * a.group + h - head * a.group) / kItemRows;
+    bool split = false;                      // its rows are being joined: they are looked at there
+    for (int w = lane; w < workers; w += 32)
+      split |= heads[w].parts != 0 && heads[w].s == s && heads[w].head == head && heads[w].rho0 == k * kItemRows;
+    if (__any_sync(0xFFFFFFFFu, split)) continue;
+    int p0, p1;
+    item_positions(a, q, k, p0, p1);
+    mend_row<D, E4M3>(a, s, q.row0, q.kv - q.c + i, i, h, p0, p1, lane);
+  }
+}
 
 template <int D, bool E4M3>
 __global__ void __launch_bounds__(32 * kJoinWarps, kJoinBlocks)
@@ -1251,7 +1268,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps, kJoinBlocks)
     if (lane >= o) inc += y;
   }
   if (lane == 31) sums[warp] = inc;
-  __syncthreads();
+  const bool marks = __syncthreads_or(tid < workers && heads[tid].marked);
   int total = 0, ahead = 0;
 #pragma unroll
   for (int y = 0; y < kJoinWarps; ++y) {
@@ -1273,8 +1290,12 @@ __global__ void __launch_bounds__(32 * kJoinWarps, kJoinBlocks)
     Sum<D> sum;
     join_parts<D, E4M3, 4>(rec, w, hd.parts, row, together ? warp : 0, together ? kJoinWarps : 1, lane, sum);
     if (together) join_warps<D, E4M3>(warp, lane, sum);
-    if (!together || warp == 0) join_finish<D, E4M3>(a, hd, hd.rho0 + row, sum, lane);
+    if (!together || warp == 0)
+      join_finish<D, E4M3>(a, hd, hd.rho0 + row, sum, lane, [&](int& p0, int& p1) {
+        item_positions(a, hd.q, hd.rho0 / kItemRows, p0, p1);
+      });
   }
+  if (marks) mend_rows<D, E4M3>(a, heads, workers, warp, lane);
 }
 
 template <int D, bool E4M3>

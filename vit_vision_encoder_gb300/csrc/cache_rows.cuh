@@ -7,13 +7,65 @@
 
 namespace dsvit {
 
-// One row of the result, key by key, by one warp.  The matrix products give a
-// hidden key the weight 0, and 0 times an infinity or NaN in its value is NaN;
-// where a chunk's rows see different keys, a row whose result is not finite
-// comes here and is computed from the keys that it does see.
+__device__ __forceinline__ bool not_finite(float x) { return (__float_as_uint(x) & 0x7F800000u) == 0x7F800000u; }
+
+// A lane's D / 32 values of a row of keys (from c.k, its exponent from c.k_exp) or values.
 template <int D, bool E4M3>
-__device__ __noinline__ void exact_row(const AttentionArgs& a, int s, int row0, int p, int i, int h, int lane) {
+__device__ __forceinline__ void load_row(const uint8_t* held, const uint8_t* exps, int64_t row, int lane,
+                                         float (&x)[D / 32]) {
   constexpr int kPer = D / 32;
+  const int64_t at = row * D + lane * kPer;
+  if constexpr (E4M3) {
+    const float f = exp_factor(exps[row]);
+#pragma unroll
+    for (int y = 0; y < kPer; y += 2) {
+      const float2 two = e4m3x2_to_float2(*reinterpret_cast<const uint16_t*>(held + at + y));
+      x[y] = two.x * f;
+      x[y + 1] = two.y * f;
+    }
+  } else {
+#pragma unroll
+    for (int y = 0; y < kPer; y += 2) {
+      const uint32_t two = *reinterpret_cast<const uint32_t*>(held + 2 * (at + y));
+      x[y] = bf16lo(two);
+      x[y + 1] = bf16hi(two);
+    }
+  }
+}
+
+// The matrix products give a hidden key the weight 0, and 0 times an infinity or NaN in its
+// value is NaN.  Where rows of an item (positions p0 .. p1) see different keys and the
+// result of the one at p is not finite: whether that may come from such a value, one
+// that the item sees and the row does not.  By one warp.
+template <int D, bool E4M3>
+__device__ __forceinline__ bool hidden_not_finite(const AttentionArgs& a, int s, int kv_head, int p, int p0, int p1, int lane) {
+  constexpr int kKeys = 2;
+  bool bad = false;
+  auto look = [&](int from, int to) {        // keys from .. to - 1
+    for (int j = from; j < to; j += kKeys) {
+      float v[kKeys][D / 32];
+#pragma unroll
+      for (int y = 0; y < kKeys; ++y) {
+        const int64_t page = j + y < to ? page_of(a.b, a.c, s, j + y, a.status) : -1;
+#pragma unroll
+        for (int x = 0; x < D / 32; ++x) v[y][x] = 0.f;
+        if (page >= 0) load_row<D, E4M3>(a.c.v, a.c.v_exp, cache_row(a.c, page, kv_head, j + y), lane, v[y]);
+      }
+#pragma unroll
+      for (int y = 0; y < kKeys; ++y)
+#pragma unroll
+        for (int x = 0; x < D / 32; ++x) bad |= not_finite(v[y][x]);
+    }
+  };
+  look(p + 1, p1 + 1);
+  look(max(window_start(a, p0), a.sinks), window_start(a, p));
+  return __any_sync(0xFFFFFFFFu, bad);
+}
+
+// One row of the result from the keys that it does see, by one warp, two keys at a time.
+template <int D, bool E4M3>
+__device__ __forceinline__ void exact_row(const AttentionArgs& a, int s, int row0, int p, int i, int h, int lane) {
+  constexpr int kPer = D / 32, kKeys = 2;
   const bf16* qr = a.q + (row0 + i) * a.q_stride + h * D + lane * kPer;
   float q[kPer], o[kPer];
 #pragma unroll
@@ -21,38 +73,47 @@ __device__ __noinline__ void exact_row(const AttentionArgs& a, int s, int row0, 
     q[x] = __bfloat162float(qr[x]);
     o[x] = 0.f;
   }
-  const int lo = window_start(a, p);
+  const int lo = window_start(a, p), kv_head = h / a.group;
   float m = -INFINITY, l = 0.f;
-  for (int j = 0; j <= p; ++j) {
-    if (j >= a.sinks && j < lo) j = lo;
-    const int64_t page = page_of(a.b, a.c, s, j, a.status);
+  for (int j0 = 0; j0 <= p; j0 += kKeys) {
+    if (j0 >= a.sinks && j0 + kKeys <= lo) j0 = lo & ~(kKeys - 1);
+    const int64_t page = page_of(a.b, a.c, s, j0, a.status);      // a block lies in one page
     if (page < 0) return;
-    const int64_t row = cache_row(a.c, page, h / a.group, j);
-    float kx[kPer], vx[kPer];
+    const int64_t row = cache_row(a.c, page, kv_head, j0);
+    float z[kKeys], v[kKeys][kPer];
+    auto on = [&](int y) { return sees(a, p, j0 + y); };
 #pragma unroll
-    for (int x = 0; x < kPer; ++x) {
-      const int64_t at = row * D + lane * kPer + x;
-      if constexpr (E4M3) {
-        kx[x] = e4m3x2_to_float2(a.c.k[at]).x * exp_factor(a.c.k_exp[row]);
-        vx[x] = e4m3x2_to_float2(a.c.v[at]).x * exp_factor(a.c.v_exp[row]);
-      } else {
-        kx[x] = __bfloat162float(reinterpret_cast<const bf16*>(a.c.k)[at]);
-        vx[x] = __bfloat162float(reinterpret_cast<const bf16*>(a.c.v)[at]);
+    for (int y = 0; y < kKeys; ++y) {
+      z[y] = 0.f;
+      if (on(y)) {
+        float k[kPer];
+        load_row<D, E4M3>(a.c.k, a.c.k_exp, row + y, lane, k);
+        load_row<D, E4M3>(a.c.v, a.c.v_exp, row + y, lane, v[y]);
+#pragma unroll
+        for (int x = 0; x < kPer; ++x) z[y] = fmaf(q[x], k[x], z[y]);
       }
     }
-    float d = 0.f;
+    float m_new = m;
 #pragma unroll
-    for (int x = 0; x < kPer; ++x) d = fmaf(q[x], kx[x], d);
+    for (int y = 0; y < kKeys; ++y) {
 #pragma unroll
-    for (int x = 16; x > 0; x >>= 1) d += __shfl_xor_sync(0xFFFFFFFFu, d, x);
-    d *= a.scale_log2;
-    const float m_new = fmaxf(m, d);
+      for (int x = 16; x > 0; x >>= 1) z[y] += __shfl_xor_sync(0xFFFFFFFFu, z[y], x);
+      z[y] *= a.scale_log2;
+      if (on(y)) m_new = fmaxf(m_new, z[y]);
+    }
     const float alpha = m == m_new ? 1.f : exp2f(m - m_new);
-    // A score of -inf weighs nothing, also while there is no other (NaN stays NaN).
-    const float w = d == -INFINITY ? 0.f : exp2f(d - m_new);
-    l = l * alpha + w;
+    l *= alpha;
 #pragma unroll
-    for (int x = 0; x < kPer; ++x) o[x] = o[x] * alpha + w * vx[x];
+    for (int x = 0; x < kPer; ++x) o[x] *= alpha;
+#pragma unroll
+    for (int y = 0; y < kKeys; ++y) {
+      if (!on(y)) continue;
+      // A score of -inf weighs nothing, also while there is no other (NaN stays NaN).
+      const float w = z[y] == -INFINITY ? 0.f : exp2f(z[y] - m_new);
+      l += w;
+#pragma unroll
+      for (int x = 0; x < kPer; ++x) o[x] = fmaf(w, v[y][x], o[x]);
+    }
     m = m_new;
     // Nothing more to find out: the row does see what makes it NaN throughout.
     bool lost = true;
@@ -62,7 +123,27 @@ __device__ __noinline__ void exact_row(const AttentionArgs& a, int s, int row0, 
   }
   bf16* to = a.out + (row0 + i) * a.out_stride + h * D + lane * kPer;
 #pragma unroll
-  for (int x = 0; x < kPer; ++x) to[x] = __float2bfloat16_rn(p < 0 ? 0.f : o[x] / l);
+  for (int x = 0; x < kPer; ++x) to[x] = __float2bfloat16_rn(o[x] / l);
+}
+
+// The row at p of an item (positions p0 .. p1) again, if its result is not finite because of
+// a value that it does not see.  Long caches take their time (half a second for a million
+// keys), so this is done where nobody waits for the warp with a limit.  Out of line, and
+// two keys at a time, for the registers of the kernels that call it (four keys: 2 us a call).
+template <int D, bool E4M3>
+__device__ __noinline__ void mend_row(const AttentionArgs& a, int s, int row0, int p, int i, int h, int p0, int p1,
+                                      int lane) {
+  if (hidden_not_finite<D, E4M3>(a, s, h / a.group, p, p0, p1, lane)) exact_row<D, E4M3>(a, s, row0, p, i, h, lane);
+}
+
+// Whether a row of the output, written before, is not finite.
+template <int D>
+__device__ __forceinline__ bool row_not_finite(const AttentionArgs& a, int64_t row, int h, int lane) {
+  const uint32_t* at = reinterpret_cast<const uint32_t*>(a.out + row * a.out_stride + h * D) + lane * (D / 64);
+  bool bad = false;
+#pragma unroll
+  for (int x = 0; x < D / 64; ++x) bad |= not_finite(bf16lo(at[x])) || not_finite(bf16hi(at[x]));
+  return __any_sync(0xFFFFFFFFu, bad);
 }
 
 // e4m3: the range of a softmax over values with exponents.  With scores z (log2 units) and a
@@ -110,15 +191,14 @@ __device__ __forceinline__ float output_factor(float m, float d, float to_m, flo
   return m == -INFINITY ? 0.f : exp2f((m - to_m) + (d - to_d));
 }
 
-__device__ __forceinline__ bool not_finite(float x) { return (__float_as_uint(x) & 0x7F800000u) == 0x7F800000u; }
-
 // Who shares the item that a worker begins and does not end: `parts` workers,
 // the first of them that worker (0: none); the item's sequence, K/V head and
-// first row among the rows of the two.
+// first row among the rows of the two.  marked: rows of the worker's whole items may have
+// to be computed again (many rows alone).
 struct SplitHeader {
   int parts, s, head, rho0;
   Seq q;
-  int pad;
+  int marked;
 };
 static_assert(sizeof(SplitHeader) == 32, "read as two 16-byte words");
 
@@ -239,18 +319,18 @@ __device__ __forceinline__ void join_warps(int warp, int lane, Sum<D>& sum) {
   }
 }
 
-// One warp writes a joined row.
-template <int D, bool E4M3>
-__device__ __forceinline__ void join_finish(const AttentionArgs& a, const SplitHeader& hd, int rho,
-                                            const Sum<D>& sum, int lane) {
+// One warp writes a joined row; positions(p0, p1): those of the rows that share its item's key blocks.
+template <int D, bool E4M3, typename F>
+__device__ __forceinline__ void join_finish(const AttentionArgs& a, const SplitHeader& hd, int rho, const Sum<D>& sum,
+                                            int lane, F&& positions) {
   const int i = a.by_group(rho), h = hd.head * a.group + rho - i * a.group, p = hd.q.kv - hd.q.c + i;
   bf16* to = a.out + (hd.q.row0 + i) * a.out_stride + h * D + lane * (D / 32);
-  const float inv = p < 0 ? 0.f : 1.f / sum.l, up = E4M3 ? shift_up(sum.d) : 1.f;
+  const float inv = 1.f / sum.l, up = E4M3 ? shift_up(sum.d) : 1.f;
   bool bad = false;
   uint32_t w[D / 64];
 #pragma unroll
   for (int x = 0; x < D / 64; ++x) {
-    const float y0 = sum.o[2 * x] * inv * up, y1 = sum.o[2 * x + 1] * inv * up;
+    const float y0 = p < 0 ? 0.f : sum.o[2 * x] * inv * up, y1 = p < 0 ? 0.f : sum.o[2 * x + 1] * inv * up;
     bad |= not_finite(y0) || not_finite(y1);
     w[x] = pack_bf16x2(y0, y1);
   }
@@ -260,7 +340,9 @@ __device__ __forceinline__ void join_finish(const AttentionArgs& a, const SplitH
     *reinterpret_cast<uint32_t*>(to) = w[0];
   if (hd.q.c > 1 && __any_sync(0xFFFFFFFFu, bad)) {
     __syncwarp();
-    exact_row<D, E4M3>(a, hd.s, hd.q.row0, p, i, h, lane);
+    int p0, p1;
+    positions(p0, p1);
+    mend_row<D, E4M3>(a, hd.s, hd.q.row0, p, i, h, p0, p1, lane);
   }
 }
 
