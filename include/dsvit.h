@@ -456,7 +456,9 @@ typedef struct ds_vit_chunks {
  * 2^31 - 256.
  *
  * ds_vit_cache_write: rows of k and v (device bf16 [rows, kv_heads, head_dim])
- * into the pages.  Two rows with the same place leave either one's value.
+ * into the pages.  No two rows of a call may have the same place (two sequences
+ * that share a page there) unless their values are alike: what is left is made
+ * of both.
  * ds_vit_cache_read: the inverse, the c newest tokens of every sequence as bf16
  * (all of them with c = kv_len).
  */
