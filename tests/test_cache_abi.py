@@ -164,3 +164,13 @@ def test_each_thread_has_a_workspace(dv, monkeypatch):
         assert a.data_ptr() == again.data_ptr()
         places += [a.data_ptr(), other.data_ptr()]
     assert len(set(places)) == 5
+
+
+@pytest.mark.parametrize("max_rows", [2 ** 31, 2 ** 32, 2 ** 32 + 3, -1])
+def test_counts_past_32_bits_refused(dv, max_rows):
+    """ctypes would hand on what is left modulo 2^32."""
+    torch = pytest.importorskip("torch")
+    z = lambda shape: torch.zeros(shape, dtype=torch.int32)   # noqa: E731
+    with pytest.raises(dv.DsVitError):
+        dv.Chunks(z(3), z(2), z((2, 4)), max_rows)
+    assert dv.Chunks(z(3), z(2), z((2, 4)), 2 ** 31 - 1).c.max_rows == 2 ** 31 - 1

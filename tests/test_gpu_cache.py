@@ -1188,3 +1188,10 @@ def test_front_padding_beside_hidden_values(dv):
             assert int(status.item()) == dv.OK
             got = f64(got)
             assert (got[:5] == 0).all() and (got[9:19] == 0).all() and np.isfinite(got[5:8]).all()
+
+
+@pytest.mark.parametrize("bad", [dict(window=2 ** 32 + 5), dict(window=2 ** 31), dict(sinks=2 ** 32), dict(window=-1)])
+def test_windows_past_32_bits_refused(dv, bad):
+    st = Setup(dv, [2], [40], 2, 64, 16, "bf16", seed=13)
+    with pytest.raises(dv.DsVitError):
+        dv.cache_attention(st.cache, st.chunks, st.queries(4), **bad)

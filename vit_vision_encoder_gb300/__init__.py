@@ -592,6 +592,8 @@ class Chunks:
         for t, shape in ((row_off, (n + 1,)), (kv_len, (n,)), (table, (n, table.shape[-1]))):
             if t.dtype != torch.int32 or tuple(t.shape) != shape or not t.is_contiguous() or t.device != table.device:
                 raise DsVitError(EINVAL, "Chunks")
+        if not 0 <= max_rows < 1 << 31:         # ctypes would take it modulo 2^32
+            raise DsVitError(EINVAL, "Chunks")
         self.row_off, self.kv_len, self.table = row_off, kv_len, table
         self.device_index = table.get_device()
         self.ws_bytes = {}
@@ -705,7 +707,7 @@ def cache_attention(cache, chunks, q, scale=None, window=0, sinks=0, out=None, w
     threads make on the same stream, need one each; when not given, each thread keeps one
     for each stream, up to 41 MB, until it ends).  Returns (out, status)."""
     d, stream, status = _on_device(cache, chunks, status, "ds_vit_cache_attention")
-    if q.dim() != 3:
+    if q.dim() != 3 or not (0 <= window < 1 << 31 and 0 <= sinks < 1 << 31):
         _refuse("ds_vit_cache_attention")
     rows, heads, dim = q.shape
     qs = _packed(q, heads, cache.head_dim, d, "ds_vit_cache_attention")
