@@ -683,6 +683,7 @@ __global__ void __launch_bounds__(Shape<D, E4M3>::kThreads, 1)
   }
   if (lane == 0) rec.headers[me] = dead ? SplitHeader{} : header;
   // Rows to compute again, now that the producer has nothing left to wait for.
+  __syncwarp();                            // what the lanes wrote is there for all of them
   if (!dead && __any_sync(0xFFFFFFFFu, marked))
     for (int64_t u = pl.begin; u < pl.end;) {
       const Item it = item_at<S::kKeyShift>(a, pl, u);
