@@ -389,10 +389,12 @@ int ds_vit_overlay_chunk(void* chunk, int64_t chunk_begin, int64_t chunk_rows, i
 
 /* ---------------------------------------------------------------------------
  * The paged K/V cache of the prompt's language model: what the rows that the
- * overlay filled meet next, layer by layer.  The pages have no counterpart for
- * it (their decoders are other programs); the calls follow the overlay's forms:
- * packed rows of several sequences, chunked prefill, entries that live on the
- * device and are checked there.
+ * overlay filled meet next, layer by layer.  For models whose query heads share
+ * keys and values in groups, heads of 64 or 128, as go with the Qwen3-VL-style
+ * tower; a decoder that attends to compressed latents keeps another cache.  The
+ * pages have no counterpart for it (their decoders are other programs); the
+ * calls follow the overlay's forms: packed rows of several sequences, chunked
+ * prefill, entries that live on the device and are checked there.
  *
  * A call covers n sequences.  Sequence s owns the packed rows row_off[s] ..
  * row_off[s+1]-1, its newest tokens in order (one for a decoding step, a chunk
@@ -476,9 +478,14 @@ int ds_vit_cache_read(const ds_vit_cache* cache, const ds_vit_chunks* chunks, vo
  * causal, optionally a sliding window of `window` tokens (the row's own among
  * them) with the first `sinks` tokens staying visible; pages that no row's
  * window reaches may have been given away.
- *   out[row, h] = bf16(softmax_j(scale * q . k_j) v)        (fp32 sums)
+ *   out[row, h] = bf16(softmax_j(scale * q . k_j) v)
  * and zeros for a row that sees nothing.  Hidden keys have no part in it,
- * whatever their values.
+ * whatever their values.  Scores, the softmax's maxima and sums and the outputs'
+ * sums are fp32; each weight is rounded before its product with the value, to
+ * bf16 (2^-8 of it) over bf16 pages, to fp16 (2^-11) over e4m3 pages.  There,
+ * of a row's contributions (weight * 2^e of the value) those under 2^-12 of the
+ * largest lose bits and those under 2^-23 of it vanish (more where all its
+ * values lie under 2^-95).
  *   q, out: device bf16 [rows, heads, head_dim]; they may not overlap.
  *           DS_VIT_ERANGE when rows * heads / kv_heads is 2^30 or more.
  *   scale:  in (0, 1e30].
@@ -488,7 +495,9 @@ int ds_vit_cache_read(const ds_vit_cache* cache, const ds_vit_chunks* chunks, vo
  *           workspaces of their own, and so do calls that several host threads
  *           make on one stream (a call makes two launches, between which
  *           another thread's may come).
- * A bounded wait that gives up records DS_VIT_ETIMEOUT in *status.
+ * A bounded wait that gives up records DS_VIT_ETIMEOUT in *status.  A row that is
+ * made non-finite by a value hidden from it is computed again key by key (some
+ * 0.7 us a key), with no such limit.
  */
 int ds_vit_cache_attention_workspace_bytes(const ds_vit_cache* cache, const ds_vit_chunks* chunks, int32_t heads,
                                            size_t* bytes);

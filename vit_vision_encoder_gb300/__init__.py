@@ -551,8 +551,9 @@ def _cache_names():
 
 class KvCache:
     """The pages of one layer's keys and values (ds_vit_cache): k, v CUDA
-    tensors [n_pages, kv_heads, page, head_dim], bfloat16, or uint8 (e4m3 bits)
-    with k_exp, v_exp uint8 [n_pages, kv_heads, page].  Holds its tensors."""
+    tensors [n_pages, kv_heads, page, head_dim], bfloat16, or uint8 (e4m3 bits;
+    float8_e4m3fn tensors by .view(torch.uint8)) with k_exp, v_exp uint8 [n_pages,
+    kv_heads, page].  Holds its tensors."""
 
     def __init__(self, k, v, k_exp=None, v_exp=None):
         torch = _cache_names()
@@ -703,7 +704,7 @@ def _workspace(cache, chunks, heads, stream):
 def cache_attention(cache, chunks, q, scale=None, window=0, sinks=0, out=None, ws=None, status=None):
     """Attention of the packed rows q (bf16 [rows, heads, head_dim], rows may be
     strided) over the cache (ds_vit_cache_attention); scale defaults to
-    head_dim ** -0.5.  ``ws``: uint8 workspace (calls that may overlap, or that other
+    head_dim ** -0.5.  A new ``out`` holds anything in rows of no sequence.  ``ws``: uint8 workspace (calls that may overlap, or that other
     threads make on the same stream, need one each; when not given, each thread keeps one
     for each stream, up to 41 MB, until it ends).  Returns (out, status)."""
     d, stream, status = _on_device(cache, chunks, status, "ds_vit_cache_attention")

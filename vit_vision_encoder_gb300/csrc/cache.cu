@@ -6,9 +6,10 @@
 // token a sequence.  One warp takes one token: its keys and values of all
 // heads are two contiguous runs of the packed rows, read as 16-byte pieces (few
 // heads and many rows: several tokens, cache_read_tokens_kernel).
-// Measured at 8 heads of 128: 6900 rows quantised as they are written 11.8 us (53% of
-// the rate of a plain copy, pieces of 128 bytes scattered over the pages), 92 thousand
-// tokens read back out of e4m3 pages 86 us (98%), 48 single tokens 2.5 us.
+// Measured at 8 heads of 128, inputs not in L2: 6900 rows quantised as they are written
+// 12.9 us (49% of the rate of a plain copy, pieces of 128 bytes scattered over the pages;
+// 8.4 with everything in L2), 92 thousand tokens read back out of e4m3 pages 86 us (98%),
+// 48 single tokens 2.7 us.
 #include "cache.cuh"
 
 namespace dsvit {

@@ -7,9 +7,9 @@
 // products run as warp MMAs (m16n8k16), whose fragments come straight from shared
 // memory; what counts is bytes in flight and a short chain of instructions per key.
 // Measured at 40 query and 8 K/V heads of 128: 32 sequences of 400 to 16000 tokens,
-// bf16, 87 us (5.8 TB/s; the loads alone 85); 64 of 2000 to 30000, e4m3, 224 us (6.1
+// bf16, 88 us (5.7 TB/s; the loads alone 85); 64 of 2000 to 30000, e4m3, 224 us (6.1
 // TB/s, the loads alone 216: the rest is conversions and products of twice the keys
-// a byte); one of 1500 tokens 10.3 us, three quarters of it fixed (launches, plan, join).
+// a byte); one of 1500 tokens 11.8 us, three quarters of it fixed (launches, plan, join).
 //
 // Work: the unit is a block of kKeys keys of one item (sequence, K/V head, 16
 // rows).  All units of a call are counted from the lengths on the device and dealt in

@@ -11,10 +11,11 @@
 //
 // Bound by the tensor pipe and the chain S -> softmax -> P V of a tile, of which two
 // (A's and B's) overlap: 2048 rows over 34 thousand tokens, 40 query and 8 K/V heads
-// of 128, bf16, take 965 us (1.44 PFLOP/s; 2820 cycles a step of two tiles, 2048 of
-// them tensor work).  Short calls are bound by what comes before and after: launch,
-// plan, first loads (9 us) and join (2.5 us where nothing is split) of the 35 us that
-// 1090 rows with nothing cached take.
+// of 128, bf16, take 863 us (1.60 PFLOP/s; 2820 cycles a step of two tiles, 2048 of
+// them tensor work), 940 to 1000 us in calls back to back, where power lowers the
+// clock.  Short calls are bound by what comes before and after: launch, plan, first loads
+// (9 us) and join (2.5 us where nothing is split) of the 37 us that 1090 rows with
+// nothing cached take.
 //
 // Roles: warps 0-7 run the softmax of tile A and warps 8-15 that of tile B, two
 // threads a row (16x32bx2 TMEM accesses, as in the bidirectional kernel); warp
@@ -25,7 +26,7 @@
 // P_X (16-bit pairs) takes the first half of S_X's columns, so S_X of the next
 // tile waits for P_X V_j; the other tile's MMAs and softmax fill that time.  At head
 // dim 64 TMEM has room for a third score tile, and A and B take the three in turn
-// (e4m3, windowed chunks of 31 to 1008 rows: 54.5 -> 50.9 us).
+// (e4m3, windowed chunks of 31 to 1008 rows, 55 us now: 3.6 us less by it).
 // Rows of Q are loaded by the softmax warps, so any group size fills the tiles.
 // Warp 18 walks the CTA's items and hands them to the other roles through a
 // ring in shared memory.  The rows' way in and out of the tiles is through
@@ -35,7 +36,7 @@
 //
 // An item of at most 128 rows leaves tile B without rows of its own: it then
 // takes the same rows and every other key tile, and the two results are added up
-// in TMEM (32 sequences of 8000 tokens, 32 rows, bf16, D 64: 130 us without, 106
+// in TMEM (32 sequences of 8000 tokens, 32 rows, bf16, D 64: 130 us without, 105
 // with).
 //
 // e4m3 pages: warps 20-27 widen the raw tiles to fp16 in shared memory (the
@@ -71,7 +72,9 @@ constexpr uint32_t kTmemCols = 512;
 // place of the tile's exponent).  Keys scaled by 2^-15 are still exact in fp16 (multiples of
 // 2^-9 2^-15).  A row's reference follows the tile's exponent E(V): where the value that has
 // it is hidden from the row, or its weight is nothing, it lies up to kSpanV above the row's
-// largest contribution, and those under 2^(kSpanV - 20) of that one lose bits.
+// largest contribution, and those under 2^(kSpanV - 20) of that one lose bits.  Rows of zeros
+// count, with their exponent of -117: the score of one may be the tile's largest, and E(V)
+// then says nothing about the contributions.
 constexpr int kSpanK = 15, kSpanV = 8, kFar = 1024;
 
 template <int D, bool E4M3>
@@ -566,7 +569,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
     // Tile by tile in turn, P V of a step and S of the next together: one tile's
     // pair runs while the other's softmax works.  The whole warp walks along, all
     // it decides by being alike in its lanes (see umma_bf16_if).  A chunk of 2048
-    // over 32k keys, us: 957 so; 1100 with one lane issuing; 1130 with an issuer for
+    // over 32k keys, us, calls back to back: 957 so; 1100 with one lane issuing; 1130 with an issuer for
     // each tile, whose pairs interleave (and the exponents of the two tiles taking
     // turns, which this order makes needless); 1357 when whatever is ready goes first.
     constexpr uint32_t f16_bits = (1u << 7) | (1u << 10);   // bf16 marks of A and B in the instruction descriptor
@@ -946,7 +949,9 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
           // A tile with factors by key.  The weights are added up here; for the products, the
           // scores give way to those of the contributions (score + e - the row's largest e).
           // Eight keys at a time, for few registers (out of line or all at once it took
-          // from every tile: a tail chunk 116 and 138 us, 111 so, 108.5 without).
+          // from every tile: a tail chunk 116 and 138 us, 111 so, 108.5 without).  Such a
+          // tile takes some five times as long as another (a tail chunk with a zero value row
+          // in every 16 tokens, so that all are: 501 us).
           // Copies, so that nothing of this is computed ahead of the loop and kept.
           int seq_no = w.s, head = w.head, last = pos, from = lo, j1 = j0;
           asm volatile("" : "+r"(seq_no), "+r"(head), "+r"(last), "+r"(from), "+r"(j1));
@@ -1157,7 +1162,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
             *reinterpret_cast<uint4*>(a.out + (w.q.row0 + i) * a.out_stride +
                                       (w.head * a.group + rho0 + rr - i * a.group) * D + piece * 8) = v;
         }
-        if (w.q.c > 1 && bad) marked = 1;
+        if (w.q.c > 1 && bad && pos >= 0) marked = 1;      // a row that sees nothing has no sum
       } else {
         float* rec = p.rec.at(blockIdx.x, w.whole == 2 ? 0 : 1);
         if (h == 0) {

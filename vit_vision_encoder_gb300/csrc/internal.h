@@ -208,10 +208,13 @@ struct AttentionArgs;
 size_t cache_prefill_workspace(int head_dim);
 int launch_cache_prefill(const AttentionArgs& a, int head_dim, bool e4m3, void* ws, cudaStream_t stream);
 // The path for few query rows per K/V head and sequence, 16 at a time: at most
-// decode_rows.  Measured on 32 sequences of 8000 tokens and 8 K/V heads, us, this
-// path against the other: 16 rows bf16 166 / 181 (head dim 64: 103 / 105), e4m3 107
-// / 207 (83 / 127); 24 to 32 rows bf16 314 / 182 (187 / 106), e4m3 190 / 208 (139
-// / 127); 40 rows e4m3 279 / 209.
+// decode_rows.  Measured at 8 K/V heads, us, this path / the other, 32 sequences of 8000
+// tokens: 16 rows bf16 165 / 175 (head dim 64: 100 / 104), e4m3 107 / 219 (77 / 133);
+// 24 rows bf16 312 / 176 (183 / 104), e4m3 188 / 220 (129 / 133); 32 rows e4m3 190 / 220
+// (131 / 133); 40 rows e4m3 279 / 209.  Shorter calls, which the host cannot tell (the
+// lengths are on the device): 4 sequences of 4000, 16 rows bf16 25 / 24, 24 rows 31 / 26,
+// 32 rows e4m3 35 / 34; one of 500, 24 rows bf16 12 / 17, 32 rows e4m3 14 / 20, so
+// that up to 5 us are lost there.
 inline int decode_rows(int head_dim, bool e4m3) { return e4m3 && head_dim == 128 ? 32 : 16; }
 size_t cache_decode_workspace(int head_dim, int rows);
 int launch_cache_decode(const AttentionArgs& a, int head_dim, bool e4m3, void* ws, cudaStream_t stream);
