@@ -1109,7 +1109,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
           const float to_m = fmaxf(m, b.x), to_d = E4M3 ? shift_at(to_m, fmaxf(m + d, b.x + b.y)) : 0.f;
           fa = output_factor<E4M3>(m, d, to_m, to_d);
           fb = output_factor<E4M3>(b.x, b.y, to_m, to_d);
-          l = l * sum_factor(m, to_m) + b.z * sum_factor(b.x, to_m);
+          l = l * sum_factor<E4M3>(m, to_m) + b.z * sum_factor<E4M3>(b.x, to_m);
           m = to_m, d = to_d;
         }
       }

@@ -185,11 +185,15 @@ __device__ __forceinline__ float shift_down(float d) { return __int_as_float((12
 __device__ __forceinline__ float shift_at(float m, float r) {
   return m == -INFINITY ? 0.f : fminf(fmaxf(rintf(r - m), -110.f), 120.f);
 }
-__device__ __forceinline__ float sum_factor(float m, float to) { return m == to ? 1.f : exp2f(m - to); }
+// (e4m3, with two of them a part: the approximation, off by 2^-22, 1 us of a tail chunk.)
+template <bool E4M3>
+__device__ __forceinline__ float sum_factor(float m, float to) {
+  return m == to ? 1.f : E4M3 ? ex2_approx(m - to) : exp2f(m - to);
+}
 template <bool E4M3>
 __device__ __forceinline__ float output_factor(float m, float d, float to_m, float to_d) {
-  if constexpr (!E4M3) return sum_factor(m, to_m);
-  return m == -INFINITY ? 0.f : exp2f((m - to_m) + (d - to_d));
+  if constexpr (!E4M3) return sum_factor<false>(m, to_m);
+  return m == -INFINITY ? 0.f : ex2_approx((m - to_m) + (d - to_d));
 }
 
 // Who shares the item that a worker begins and does not end: `parts` workers,
@@ -270,13 +274,13 @@ __device__ __forceinline__ void join_parts(const Records& rec, int w, int parts,
     }
     const float d = E4M3 ? shift_at(m, r) : 0.f;
     const float wa = output_factor<E4M3>(sum.m, sum.d, m, d);
-    sum.l *= sum_factor(sum.m, m);
+    sum.l *= sum_factor<E4M3>(sum.m, m);
 #pragma unroll
     for (int x = 0; x < kPer; ++x) sum.o[x] *= wa;
 #pragma unroll
     for (int y = 0; y < kBatch; ++y) {
       const float wb = output_factor<E4M3>(mp[y], dp[y], m, d);
-      sum.l += lp[y] * sum_factor(mp[y], m);
+      sum.l += lp[y] * sum_factor<E4M3>(mp[y], m);
 #pragma unroll
       for (int x = 0; x < kPer; ++x) sum.o[x] += op[y][x] * wb;
     }
@@ -314,7 +318,7 @@ __device__ __forceinline__ void join_warps(int warp, int lane, Sum<D>& sum) {
 #pragma unroll
   for (int y = 0; y < kJoinWarps; ++y) {
     const float f = output_factor<E4M3>(sm[y], sd[y], sum.m, sum.d);
-    sum.l += sl[y] * sum_factor(sm[y], sum.m);
+    sum.l += sl[y] * sum_factor<E4M3>(sm[y], sum.m);
 #pragma unroll
     for (int x = 0; x < kPer; ++x) sum.o[x] += so[y][lane * kPer + x] * f;
   }
