@@ -452,7 +452,7 @@ def _shared_query(q, hk):
     while step < g:
         step *= 2
     frac, ex = torch.frexp(q.abs().amax((2, 3)) * step)
-    e = torch.where(frac <= 1016 / 1024, ex - 10, ex - 9)
+    e = torch.where(frac <= 1016 / 1024, ex - 10, ex - 9).clamp_min(-100)
     n = torch.ldexp(q, -e[..., None, None]).round()
     return torch.stack((n.clamp_min(0).sum(2), n.clamp_max(0).sum(2)), 2)
 
