@@ -388,6 +388,63 @@ int ds_vit_overlay_chunk(void* chunk, int64_t chunk_begin, int64_t chunk_rows, i
                          void* stream);
 
 /* ---------------------------------------------------------------------------
+ * Queries and keys on their way from the projection into the attention: the norm
+ * of every head and the rotation by its position, in one pass.  The positions may
+ * have one axis or the three of ds_vit_qwen_layout ([A] "Qwen3-VL has two layers
+ * of positional meaning").
+ *
+ * A head x of d values is normed where a weight g is given,
+ *   n = x / sqrt(mean(x^2) + eps) * g        (else n = x),
+ * and pair i of its d/2 pairs (a, b) turned by t = pos[axis(i)] * freq_i:
+ *   (n_a cos t - n_b sin t,  n_b cos t + n_a sin t),
+ * in fp32, rounded to bf16 once.  Pairs: (i, i + d/2) with
+ * DS_VIT_ROPE_HALF_VECTOR, (2i, 2i + 1) with DS_VIT_ROPE_ADJACENT.
+ * ------------------------------------------------------------------------- */
+#define DS_VIT_ROPE_ADJACENT 2      /* of ds_vit_rotary alone */
+
+/* Filled by ds_vit_rotary_init; a plain value, which calls copy. */
+typedef struct ds_vit_rotary {
+  uint64_t turn[64];   /* freq_i / 2 pi in units of 2^-64, modulo 1: positions are whole, so
+                          pos * turn modulo 2^64 is the angle at any of them */
+  uint8_t axis[64];    /* position axis of each pair */
+  int32_t head_dim, axes, pairing;
+} ds_vit_rotary;
+
+/*
+ * ds_vit_rotary_init (host only): freq_i = theta^(-2i/head_dim), or inv_freq[i]
+ * (host double [head_dim/2]; theta is then not looked at) for scaled ones.
+ * axes is 1, or 3 with sections[3], the pairs of each axis (t, h, w), which add up to
+ * head_dim/2: one section behind the other, or with `interleaved` pair i at axis
+ * a = i mod 3 for a > 0 and i < 3 sections[a], at axis 0 otherwise (then
+ * 3 sections[a] is at most head_dim/2 + 2 - a for a = 1, 2).  sections is not
+ * looked at with one axis.  Angles are right to 2^-55 turns a position.
+ * DS_VIT_EINVAL for another head_dim than 64 or 128, other axes, sections or
+ * pairings, theta or a frequency that is not positive and finite (theta: over 1).
+ */
+int ds_vit_rotary_init(int32_t head_dim, double theta, const double* inv_freq, int32_t axes,
+                       const int32_t* sections, int32_t interleaved, int32_t pairing, ds_vit_rotary* out);
+
+/*
+ * ds_vit_qk_norm_rope: q (device bf16 [rows, heads, head_dim]) and k (device bf16
+ * [rows, kv_heads, head_dim]), each with the distance between its rows in
+ * elements (a multiple of 8), as parts of one projection's output may be, to
+ * q_out and k_out of the same shapes.  An output may be its own input (same
+ * address and stride), and otherwise overlaps no input.
+ *   pos:  device int32 [axes, rows], axis a at pos + a * pos_stride (one axis:
+ *         pos_stride is not looked at); any values, negative ones among them.
+ *   q_norm, k_norm: device bf16 [head_dim] or NULL (that norm is left out).
+ *   eps:  positive and finite (not looked at without norms).
+ * DS_VIT_EINVAL for null or misaligned pointers (16 bytes; pos 4), a stride
+ * below its row's width, pos_stride below rows, heads outside 1 .. 16384, kv_heads
+ * outside 1 .. DS_VIT_CACHE_MAX_HEADS, rows < 0, a rotary that
+ * ds_vit_rotary_init did not make; DS_VIT_ERANGE for rows of 2^30 or more.
+ */
+int ds_vit_qk_norm_rope(const ds_vit_rotary* rotary, const void* q, int64_t q_stride, int32_t heads,
+                        const void* k, int64_t k_stride, int32_t kv_heads, int64_t rows, const int32_t* pos,
+                        int64_t pos_stride, const void* q_norm, const void* k_norm, float eps, void* q_out,
+                        int64_t q_out_stride, void* k_out, int64_t k_out_stride, void* stream);
+
+/* ---------------------------------------------------------------------------
  * The paged K/V cache of the prompt's language model: what the rows that the
  * overlay filled meet next, layer by layer.  For models whose query heads share
  * keys and values in groups, heads of 64 or 128, as go with the Qwen3-VL-style

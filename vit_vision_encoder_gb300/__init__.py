@@ -19,6 +19,7 @@ LIB_PATH = os.path.join(_HERE, "libdsvit.so")
 OK, EINVAL, ERANGE, ECAP, ECUDA, ETIMEOUT, ENOMEM = 0, -1, -2, -3, -4, -5, -6
 TOK_START, TOK_IMAGE, TOK_NEWLINE, TOK_END = 0, 1, 2, 3
 CACHE_BF16, CACHE_E4M3 = 0, 1
+ROPE_HALF_VECTOR, ROPE_ADJACENT = 1, 2
 EPI_BIAS, EPI_BIAS_GELU, EPI_BIAS_RESID, EPI_QKV_ROPE, EPI_SWIGLU = 0, 1, 2, 3, 4
 MAX_LAYERS, MAX_IMAGES, MAX_PATCHES, MAX_TOKENS = 32, 64, 9216, 1024
 NOALLOC_MAX_PATCHES, NOALLOC_SCRATCH_BYTES = 1024, 21 * 1024 * 1024
@@ -87,6 +88,11 @@ class ChunkArrays(C.Structure):
                 ("table_cols", C.c_int32), ("max_rows", C.c_int32)]
 
 
+class RotaryTable(C.Structure):
+    _fields_ = [("turn", C.c_uint64 * 64), ("axis", C.c_uint8 * 64), ("head_dim", C.c_int32), ("axes", C.c_int32),
+                ("pairing", C.c_int32)]
+
+
 # Every symbol include/dsvit.h declares: name -> (restype, argtypes).
 _VP, _I32, _I64, _SZ, _F = C.c_void_p, C.c_int32, C.c_int64, C.c_size_t, C.c_float
 _P_I32, _P_I64 = C.POINTER(C.c_int32), C.POINTER(C.c_int64)
@@ -135,6 +141,9 @@ SIGNATURES = {
                                                          C.POINTER(_SZ)]),
     "ds_vit_cache_attention": (C.c_int, [C.POINTER(Cache), C.POINTER(ChunkArrays), _VP, _I64, _I64, _I32, _F, _I32,
                                          _I32, _VP, _I64, _VP, _SZ, _VP, _VP]),
+    "ds_vit_rotary_init": (C.c_int, [_I32, C.c_double, _VP, _I32, _VP, _I32, _I32, C.POINTER(RotaryTable)]),
+    "ds_vit_qk_norm_rope": (C.c_int, [C.POINTER(RotaryTable), _VP, _I64, _I32, _VP, _I64, _I32, _I64, _VP, _I64, _VP,
+                                      _VP, _F, _VP, _I64, _VP, _I64, _VP]),
 }
 
 
@@ -727,6 +736,68 @@ def cache_attention(cache, chunks, q, scale=None, window=0, sinks=0, out=None, w
                                      dim ** -0.5 if scale is None else scale, window, sinks, out.data_ptr(), os_,
                                      ws.data_ptr(), ws.numel(), status.data_ptr(), stream), "ds_vit_cache_attention")
     return out, status
+
+
+# ---------------------------------------------------------------- norms and rotation in front of the cache
+
+class Rotary:
+    """Frequencies and position axes of a rotation (ds_vit_rotary_init): theta, or
+    ``inv_freq`` (head_dim / 2 scaled frequencies); ``sections`` of one or three axes;
+    ``pairing`` "half_vector" or "adjacent"."""
+
+    def __init__(self, head_dim, theta=10000.0, sections=None, interleaved=False, pairing="half_vector", inv_freq=None):
+        _cache_names()
+        axes = 1 if sections is None else len(sections)
+        kinds = {"half_vector": ROPE_HALF_VECTOR, "adjacent": ROPE_ADJACENT}
+        if pairing not in kinds or not 0 <= head_dim < 1 << 31 or (
+                inv_freq is not None and len(inv_freq) != head_dim // 2) or any(
+                    not 0 <= x < 1 << 31 for x in sections or ()):
+            raise DsVitError(EINVAL, "ds_vit_rotary_init")
+        if axes == 1 and sections is not None and sections[0] != head_dim // 2:
+            raise DsVitError(EINVAL, "ds_vit_rotary_init")
+        freq = None if inv_freq is None else (C.c_double * len(inv_freq))(*map(float, inv_freq))
+        self.c = RotaryTable()
+        self.ref = C.byref(self.c)
+        check(lib.ds_vit_rotary_init(head_dim, theta, freq, axes, _i32(sections or ()), bool(interleaved),
+                                     kinds[pairing], self.ref), "ds_vit_rotary_init")
+        self.head_dim, self.axes = head_dim, axes
+
+
+def qk_norm_rope(rotary, q, k, positions, q_norm=None, k_norm=None, eps=1e-6, out=None):
+    """Norm of every head (weights q_norm, k_norm bf16 [head_dim]; None leaves it out) and
+    rotation by position (ds_vit_qk_norm_rope): q bf16 [rows, heads, head_dim] and k
+    [rows, kv_heads, head_dim], rows may be strided; positions int32 [axes, rows], or
+    [rows] with one axis.  ``out``: the two tensors to fill, (q, k) itself for
+    in place.  Returns them."""
+    where = "ds_vit_qk_norm_rope"
+    d, dim = q.get_device(), rotary.head_dim
+    if d < 0 or _cuda_device() != d or q.dim() != 3 or k.dim() != 3:
+        _refuse(where)
+    rows, heads, kv_heads = q.shape[0], q.shape[1], k.shape[1]
+    qs, ks = _packed(q, heads, dim, d, where), _packed(k, kv_heads, dim, d, where)
+    if out is None:
+        out = (_torch().empty((rows, heads, dim), dtype=_bf16, device=q.device),
+               _torch().empty((rows, kv_heads, dim), dtype=_bf16, device=q.device))
+    qo, ko = out
+    qos, kos = _packed(qo, heads, dim, d, where), _packed(ko, kv_heads, dim, d, where)
+    axes = rotary.axes
+    if (k.shape[0] != rows or qo.shape[0] != rows or ko.shape[0] != rows or positions.dtype is not _i32_type
+            or positions.get_device() != d
+            or (positions.shape != (axes, rows) and (axes != 1 or positions.shape != (rows,)))
+            or (rows > 1 and positions.stride(-1) != 1)):
+        _refuse(where)
+    for g in (q_norm, k_norm):
+        if g is not None and (g.dtype is not _bf16 or g.shape != (dim,) or g.get_device() != d
+                              or not g.is_contiguous()):
+            _refuse(where)
+    if rows == 0:                           # an empty tensor has no address
+        return out
+    check(lib.ds_vit_qk_norm_rope(rotary.ref, q.data_ptr(), qs, heads, k.data_ptr(), ks, kv_heads, rows,
+                                  positions.data_ptr(), positions.stride(0) if axes > 1 else 0,
+                                  q_norm.data_ptr() if q_norm is not None else None,
+                                  k_norm.data_ptr() if k_norm is not None else None, eps, qo.data_ptr(), qos,
+                                  ko.data_ptr(), kos, _raw_stream(d)), where)
+    return out
 
 
 # ---------------------------------------------------------------- single kernels

@@ -326,10 +326,8 @@ int tokens_per_warp(int head_dim, int kv_heads, int64_t rows) {
   return rows > 64 * static_cast<int64_t>(num_sms()) && places >= 4 * kv_heads ? places / kv_heads : 1;
 }
 
-bool aligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
+}  // namespace
 
-// Checks of a cache and a chunk description (host values only); fills the
-// kernels' views.
 int check_cache(const ds_vit_cache* c, const ds_vit_chunks* b, int64_t rows, CacheView* cv, ChunkView* bv) {
   if (!c || !b || !c->k || !c->v || !b->row_off || !b->kv_len || !b->table) return DS_VIT_EINVAL;
   if ((c->kind != DS_VIT_CACHE_BF16 && c->kind != DS_VIT_CACHE_E4M3) || (c->head_dim != 64 && c->head_dim != 128) ||
@@ -353,10 +351,7 @@ int check_cache(const ds_vit_cache* c, const ds_vit_chunks* b, int64_t rows, Cac
   return DS_VIT_OK;
 }
 
-// A packed tensor of `rows` rows, `width` values each, `stride` values apart.
-bool bad_rows(const void* p, int64_t stride, int64_t width) {
-  return !p || !aligned(p, 16) || stride < width || stride % 8 != 0;
-}
+namespace {
 
 // Rows that share a K/V head in one sequence: few of them leave the call bound
 // by the cache's bytes, and the kernel that streams those through warp MMAs is
@@ -368,11 +363,6 @@ bool few_rows(const ChunkView& b, int head_dim, int group, bool e4m3) {
 size_t attention_workspace(const ChunkView& b, int head_dim, int group, bool e4m3) {
   return few_rows(b, head_dim, group, e4m3) ? cache_decode_workspace(head_dim, b.max_rows * group)
                                   : cache_prefill_workspace(head_dim);
-}
-
-int launched(cudaError_t e) {
-  if (e != cudaSuccess) cudaGetLastError();
-  return e == cudaSuccess ? DS_VIT_OK : DS_VIT_ECUDA;
 }
 
 }  // namespace

@@ -28,6 +28,22 @@ struct ChunkView {
   int rows;
 };
 
+// Checks of a cache and a chunk description (host values only); fills the
+// kernels' views.
+int check_cache(const ds_vit_cache* c, const ds_vit_chunks* b, int64_t rows, CacheView* cv, ChunkView* bv);
+
+inline bool aligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
+
+// A packed tensor, rows of `width` values `stride` values apart.
+inline bool bad_rows(const void* p, int64_t stride, int64_t width) {
+  return !p || !aligned(p, 16) || stride < width || stride % 8 != 0;
+}
+
+inline int launched(cudaError_t e) {
+  if (e != cudaSuccess) cudaGetLastError();
+  return e == cudaSuccess ? DS_VIT_OK : DS_VIT_ECUDA;
+}
+
 // One sequence's part of the packed rows.
 struct Seq {
   int row0;   // its first packed row

@@ -1,0 +1,243 @@
+// Norms of queries and keys for each head and their rotation by position, in one
+// pass (include/dsvit.h, ds_vit_qk_norm_rope).
+//
+// Every byte is read once and written once: bound by memory at prompt lengths and by
+// the chain load -> norm -> store at one token a sequence.  D / 16 lanes hold one head, 16
+// values each: the 16-byte pieces l and l + D / 16 of the row, so that both loads
+// of a warp are whole lines and both members of every pair lie in one lane under either
+// pairing (the norm's sum is the only exchange between lanes).  A warp takes a row's
+// heads kBatch passes at a time, or a part of them where there are few rows.
+//
+// Angles: positions are whole numbers, so the fraction of a turn is
+// pos * (freq / 2 pi) modulo 1 in 64-bit fixed point, exact but for the frequency's own
+// rounding, with no reduction of large arguments; sincospif takes its upper 32 bits.
+// A lane works out D / 64 pairs' sines and cosines for the whole warp.
+#include <algorithm>
+#include <cmath>
+
+#include "cache.cuh"
+
+namespace dsvit {
+
+namespace {
+
+constexpr int kWarps = 4;
+constexpr int kBatch = 4;    // passes whose loads are in flight together
+
+struct RotaryArgs {
+  ds_vit_rotary r;
+  const bf16* x[2];          // q, k
+  bf16* y[2];
+  int64_t x_stride[2], y_stride[2];
+  const bf16* norm[2];
+  int heads[2];
+  const int32_t* pos;
+  int64_t pos_stride;
+  int64_t rows;
+  int parts;                 // warps a row's passes are dealt to
+  float eps;
+};
+
+// Pair j of a lane's eight, of those of a head: pieces l and l + D / 16 hold them as
+// halves of pairs, or as four pairs each.
+template <int D, bool kAdjacent>
+__device__ __forceinline__ int pair_of(int l, int j) {
+  if constexpr (!kAdjacent) return 8 * l + j;
+  return j < 4 ? 4 * l + j : D / 4 + 4 * l + j - 4;
+}
+
+template <int D, bool kAdjacent>
+__global__ void __launch_bounds__(32 * kWarps) qk_norm_rope_kernel(const __grid_constant__ RotaryArgs a) {
+  constexpr int kLanes = D / 16, kHeads = 32 / kLanes, kOwn = D / 64;
+  grid_dep_launch();
+  const int lane = threadIdx.x & 31, l = lane % kLanes, h0 = lane / kLanes;
+  uint64_t turn[kOwn];
+  int axis[kOwn];
+#pragma unroll
+  for (int i = 0; i < kOwn; ++i) {
+    turn[i] = a.r.turn[lane * kOwn + i];
+    axis[i] = a.r.axis[lane * kOwn + i];
+  }
+  grid_dep_wait();
+  const int total = a.heads[0] + a.heads[1], passes = (total + kHeads - 1) / kHeads;
+  uint4 g[2][2];
+#pragma unroll
+  for (int x = 0; x < 2; ++x) {
+    g[x][0] = g[x][1] = make_uint4(0, 0, 0, 0);
+    if (a.norm[x] != nullptr) {
+      g[x][0] = __ldg(reinterpret_cast<const uint4*>(a.norm[x]) + l);
+      g[x][1] = __ldg(reinterpret_cast<const uint4*>(a.norm[x]) + l + kLanes);
+    }
+  }
+  const int64_t units = a.rows * a.parts, step = static_cast<int64_t>(gridDim.x) * kWarps;
+  for (int64_t u = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5); u < units; u += step) {
+    const int64_t row = u / a.parts;
+    const int part = static_cast<int>(u - row * a.parts);
+    int32_t at[kOwn];
+#pragma unroll
+    for (int i = 0; i < kOwn; ++i) at[i] = __ldg(a.pos + axis[i] * a.pos_stride + row);
+    float c[8], s[8];
+    for (int p0 = part; p0 < passes; p0 += kBatch * a.parts) {
+      uint4 lo[kBatch], hi[kBatch];
+#pragma unroll
+      for (int y = 0; y < kBatch; ++y) {
+        const int h = (p0 + y * a.parts) * kHeads + h0;
+        if (h < total) {
+          const int x = h >= a.heads[0];
+          const uint4* from =
+              reinterpret_cast<const uint4*>(a.x[x] + row * a.x_stride[x] + (x ? h - a.heads[0] : h) * D) + l;
+          lo[y] = from[0];
+          hi[y] = from[kLanes];
+        } else {
+          lo[y] = hi[y] = make_uint4(0, 0, 0, 0);
+        }
+      }
+      if (p0 == part) {
+        float co[kOwn], so[kOwn];
+#pragma unroll
+        for (int i = 0; i < kOwn; ++i) {
+          const uint64_t t = static_cast<uint64_t>(static_cast<int64_t>(at[i])) * turn[i];
+          sincospif(static_cast<float>(static_cast<int32_t>(t >> 32)) * 0x1p-31f, &so[i], &co[i]);
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int p = pair_of<D, kAdjacent>(l, j), i = kOwn == 2 ? j & 1 : 0;
+          c[j] = __shfl_sync(0xFFFFFFFFu, co[i], p / kOwn);
+          s[j] = __shfl_sync(0xFFFFFFFFu, so[i], p / kOwn);
+        }
+      }
+#pragma unroll
+      for (int y = 0; y < kBatch; ++y) {
+        const int h = (p0 + y * a.parts) * kHeads + h0;
+        if ((p0 + y * a.parts) >= passes) break;
+        const int x = h >= a.heads[0];
+        float v[16];
+        const uint32_t w[8] = {lo[y].x, lo[y].y, lo[y].z, lo[y].w, hi[y].x, hi[y].y, hi[y].z, hi[y].w};
+        float sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          v[2 * i] = bf16lo(w[i]);
+          v[2 * i + 1] = bf16hi(w[i]);
+          sum = fmaf(v[2 * i], v[2 * i], sum);
+          sum = fmaf(v[2 * i + 1], v[2 * i + 1], sum);
+        }
+#pragma unroll
+        for (int o = kLanes / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+        if (a.norm[x] != nullptr) {
+          const float f = rsqrtf(sum * (1.f / D) + a.eps);
+          const uint4 g0 = x ? g[1][0] : g[0][0], g1 = x ? g[1][1] : g[0][1];
+          const uint32_t gw[8] = {g0.x, g0.y, g0.z, g0.w, g1.x, g1.y, g1.z, g1.w};
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            v[2 * i] *= f * bf16lo(gw[i]);
+            v[2 * i + 1] *= f * bf16hi(gw[i]);
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          // Pair j's members among the lane's values: (j, j + 8), or (2j, 2j + 1).
+          const int m0 = kAdjacent ? 2 * j : j, m1 = kAdjacent ? 2 * j + 1 : j + 8;
+          const float v0 = v[m0], v1 = v[m1];
+          v[m0] = v0 * c[j] - v1 * s[j];
+          v[m1] = v1 * c[j] + v0 * s[j];
+        }
+        if (h < total) {
+          uint4* to = reinterpret_cast<uint4*>(a.y[x] + row * a.y_stride[x] + (x ? h - a.heads[0] : h) * D) + l;
+          to[0] = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                             pack_bf16x2(v[6], v[7]));
+          to[kLanes] = make_uint4(pack_bf16x2(v[8], v[9]), pack_bf16x2(v[10], v[11]), pack_bf16x2(v[12], v[13]),
+                                  pack_bf16x2(v[14], v[15]));
+        }
+      }
+    }
+  }
+}
+
+}  // namespace
+
+}  // namespace dsvit
+
+using namespace dsvit;
+
+extern "C" {
+
+int ds_vit_rotary_init(int32_t head_dim, double theta, const double* inv_freq, int32_t axes,
+                       const int32_t* sections, int32_t interleaved, int32_t pairing, ds_vit_rotary* out) {
+  if (!out || (head_dim != 64 && head_dim != 128) || (axes != 1 && axes != 3) ||
+      (pairing != DS_VIT_ROPE_HALF_VECTOR && pairing != DS_VIT_ROPE_ADJACENT) || (axes == 3 && !sections) ||
+      (!inv_freq && !(theta > 1.0 && std::isfinite(theta))))
+    return DS_VIT_EINVAL;
+  const int pairs = head_dim / 2;
+  if (axes == 3) {
+    int64_t sum = 0;
+    for (int a = 0; a < 3; ++a) {
+      if (sections[a] < 0 || (interleaved && a > 0 && 3 * static_cast<int64_t>(sections[a]) > pairs + 2 - a))
+        return DS_VIT_EINVAL;
+      sum += sections[a];
+    }
+    if (sum != pairs) return DS_VIT_EINVAL;
+  }
+  ds_vit_rotary r{};
+  r.head_dim = head_dim;
+  r.axes = axes;
+  r.pairing = pairing;
+  for (int i = 0; i < pairs; ++i) {
+    const double f = inv_freq ? inv_freq[i] : std::pow(theta, -static_cast<double>(i) / pairs);
+    if (!(f > 0.0 && std::isfinite(f))) return DS_VIT_EINVAL;
+    double turns = f * 0.15915494309189533577;   // 1 / 2 pi
+    turns -= std::floor(turns);
+    // Under 1 by 2^-53 at least, so that the product is under 2^64.
+    r.turn[i] = static_cast<uint64_t>(turns * 0x1p64);
+    if (axes == 3 && interleaved)
+      r.axis[i] = static_cast<uint8_t>(i % 3 && i < 3 * sections[i % 3] ? i % 3 : 0);
+    else if (axes == 3)
+      r.axis[i] = static_cast<uint8_t>((i >= sections[0]) + (i >= sections[0] + sections[1]));
+  }
+  *out = r;
+  return DS_VIT_OK;
+}
+
+int ds_vit_qk_norm_rope(const ds_vit_rotary* rotary, const void* q, int64_t q_stride, int32_t heads,
+                        const void* k, int64_t k_stride, int32_t kv_heads, int64_t rows, const int32_t* pos,
+                        int64_t pos_stride, const void* q_norm, const void* k_norm, float eps, void* q_out,
+                        int64_t q_out_stride, void* k_out, int64_t k_out_stride, void* stream) {
+  if (!rotary || (rotary->head_dim != 64 && rotary->head_dim != 128) || (rotary->axes != 1 && rotary->axes != 3) ||
+      (rotary->pairing != DS_VIT_ROPE_HALF_VECTOR && rotary->pairing != DS_VIT_ROPE_ADJACENT) || heads < 1 ||
+      heads > DS_VIT_CACHE_MAX_HEADS * DS_VIT_CACHE_MAX_GROUP || kv_heads < 1 || kv_heads > DS_VIT_CACHE_MAX_HEADS ||
+      rows < 0)
+    return DS_VIT_EINVAL;
+  const int d = rotary->head_dim;
+  for (int i = 0; i < d / 2; ++i)
+    if (rotary->axis[i] >= rotary->axes) return DS_VIT_EINVAL;
+  const int64_t qw = static_cast<int64_t>(heads) * d, kw = static_cast<int64_t>(kv_heads) * d;
+  if (bad_rows(q, q_stride, qw) || bad_rows(k, k_stride, kw) || bad_rows(q_out, q_out_stride, qw) ||
+      bad_rows(k_out, k_out_stride, kw) || !pos || !aligned(pos, 4) || (rotary->axes > 1 && pos_stride < rows) ||
+      !aligned(q_norm, 16) || !aligned(k_norm, 16) || ((q_norm || k_norm) && !(eps > 0.f && std::isfinite(eps))))
+    return DS_VIT_EINVAL;
+  if (rows > INT32_MAX / 2) return DS_VIT_ERANGE;
+  if (rows == 0) return DS_VIT_OK;
+  RotaryArgs a{};
+  a.r = *rotary;
+  a.x[0] = static_cast<const bf16*>(q), a.x[1] = static_cast<const bf16*>(k);
+  a.y[0] = static_cast<bf16*>(q_out), a.y[1] = static_cast<bf16*>(k_out);
+  a.x_stride[0] = q_stride, a.x_stride[1] = k_stride;
+  a.y_stride[0] = q_out_stride, a.y_stride[1] = k_out_stride;
+  a.norm[0] = static_cast<const bf16*>(q_norm), a.norm[1] = static_cast<const bf16*>(k_norm);
+  a.heads[0] = heads, a.heads[1] = kv_heads;
+  a.pos = pos;
+  a.pos_stride = rotary->axes > 1 ? pos_stride : 0;
+  a.rows = rows;
+  a.eps = eps;
+  // Few rows: a pass a warp, as long as that is no more warps than run at once.
+  const int passes = (heads + kv_heads + 512 / d - 1) / (512 / d);
+  const int64_t warps = 32 * static_cast<int64_t>(num_sms());
+  a.parts = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(passes, warps / rows)));
+  const int64_t units = rows * a.parts;
+  const unsigned blocks = static_cast<unsigned>(std::min((units + kWarps - 1) / kWarps, warps / kWarps));
+  const bool adj = rotary->pairing == DS_VIT_ROPE_ADJACENT;
+  auto* fn = d == 128 ? (adj ? qk_norm_rope_kernel<128, true> : qk_norm_rope_kernel<128, false>)
+                      : (adj ? qk_norm_rope_kernel<64, true> : qk_norm_rope_kernel<64, false>);
+  return launched(launch_pdl(fn, dim3(blocks), dim3(32 * kWarps), 0, static_cast<cudaStream_t>(stream), a));
+}
+
+}  // extern "C"
