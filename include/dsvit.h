@@ -562,6 +562,103 @@ int ds_vit_cache_attention(const ds_vit_cache* cache, const ds_vit_chunks* chunk
                            int64_t rows, int32_t heads, float scale, int32_t window, int32_t sinks, void* out,
                            int64_t out_stride, void* ws, size_t ws_bytes, int32_t* status, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Pages of many sequences.  A pool counts for every page how many table entries
+ * name it; a page of count 0 is free.  Layers share one pool and one table: the
+ * calls below change those on the device, and list the pages whose contents have
+ * to move, which ds_vit_cache_copy then copies in the cache of each layer.
+ *
+ * Slot s of the tables is one sequence: kv_len[s] tokens, position p in page
+ * table[s * table_cols + p / page].  An entry below 0 is a page given away; entries
+ * behind the last token's are not looked at.  ds_vit_chunks may point to the same
+ * arrays (slots up to DS_VIT_MAX_SEQS), or to rows gathered from them.
+ *
+ * New pages are the free ones with the lowest numbers, in the order of the
+ * call's list, so equal states give equal results.  The calls are asynchronous on
+ * `stream`, allocate nothing and can be captured; two calls on one pool must not
+ * overlap.
+ *   copies: receives the pages to copy (from[i] to to[i], i < *count), no page twice in
+ *           `to` and none of `to` in `from`.  Copy them before the pool's next call, and
+ *           before the new pages are written.
+ *   status: device int32, as above.  An entry of the lists that is not in range
+ *           records DS_VIT_ERANGE, one that may not be there DS_VIT_EINVAL; it is
+ *           left out and the others are served.  Where the free pages (or copies.cap)
+ *           do not suffice, DS_VIT_ECAP is recorded, *count is 0 and nobody gets a page.
+ * DS_VIT_EINVAL for null or misaligned pointers (refs 16 bytes, others 4), n outside
+ * 1 .. DS_VIT_MAX_SEQS, slots outside 1 .. DS_VIT_MAX_SLOTS, cap < 1, n_pages < 1, another
+ * page than 16, 32, 64 or 128; DS_VIT_ERANGE for n_pages past 2^31 - 65536, table_cols *
+ * page past 2^31 - 256.
+ * ------------------------------------------------------------------------- */
+#define DS_VIT_MAX_SLOTS 65536
+
+typedef struct ds_vit_page_pool {
+  int32_t* refs;        /* device [n_pages], at least 0: in how many table entries a page is named */
+  int64_t n_pages;
+  int32_t page;         /* tokens per page: 16, 32, 64 or 128 */
+} ds_vit_page_pool;
+
+typedef struct ds_vit_page_tables {
+  int32_t* table;       /* device [slots, table_cols] */
+  int32_t* kv_len;      /* device [slots] */
+  int32_t slots;
+  int32_t table_cols;
+} ds_vit_page_tables;
+
+typedef struct ds_vit_page_copies {
+  int32_t *from, *to;   /* device [cap] */
+  int32_t* count;       /* device */
+  int32_t cap;
+} ds_vit_page_copies;
+
+/*
+ * ds_vit_pages_resize: sequence slot[i] (device int32 [n], no slot twice:
+ * DS_VIT_EINVAL for both) gets length[i] tokens (device int32 [n]).  Shorter ones
+ * (0: the sequence ends) give back the pages behind their last token, entries become -1;
+ * longer ones get pages for the tokens to come.  What shrinks is served first, and in any
+ * case.  A sequence that grows within a page that another one names as well (one
+ * cut back to the middle of a shared page) gets a copy of it; one whose last page was
+ * given away records DS_VIT_ERANGE.
+ *
+ * ds_vit_pages_release: gives back the pages of sequence slot[i] that lie wholly in
+ * its tokens begin[i] .. end[i] - 1 (device int32 [n] each; 0 <= begin <= end, the last page
+ * only if it is full): what a sliding window has left behind.  Entries become -1,
+ * lengths stay.
+ *
+ * ds_vit_pages_fork: sequence dst[i] (length 0 so far, no slot twice, none of them
+ * in src: DS_VIT_EINVAL) becomes the same as src[i]; a sequence may have many children.
+ * Full pages are shared, a page with room left is copied.  Entries that name no
+ * page are passed on as -1.
+ *
+ * ds_vit_pages_compact: afterwards the used pages are 0 .. u - 1, u their number: in
+ * order, the used pages from u on take the free places before u, and all tables
+ * (every slot) name the new ones.  At most cap pages move; a further call goes on.
+ */
+int ds_vit_pages_resize(const ds_vit_page_pool* pool, const ds_vit_page_tables* tables, const int32_t* slot,
+                        const int32_t* length, int32_t n, const ds_vit_page_copies* copies, int32_t* status,
+                        void* stream);
+int ds_vit_pages_release(const ds_vit_page_pool* pool, const ds_vit_page_tables* tables, const int32_t* slot,
+                         const int32_t* begin, const int32_t* end, int32_t n, int32_t* status, void* stream);
+int ds_vit_pages_fork(const ds_vit_page_pool* pool, const ds_vit_page_tables* tables, const int32_t* src,
+                      const int32_t* dst, int32_t n, const ds_vit_page_copies* copies, int32_t* status,
+                      void* stream);
+int ds_vit_pages_compact(const ds_vit_page_pool* pool, const ds_vit_page_tables* tables,
+                         const ds_vit_page_copies* copies, int32_t* status, void* stream);
+
+/*
+ * ds_vit_cache_copy: page from[i] of one layer's cache to page to[i], i < *count: keys,
+ * values and exponents, and their bounds (see ds_vit_cache_bounds; NULL: none).
+ * Lists made elsewhere follow the same rule: no page twice in `to`, none of `to`
+ * in `from`.  A count outside 0 .. cap records DS_VIT_EINVAL (nothing is copied), a page
+ * outside [0, n_pages) DS_VIT_ERANGE (that copy is left out).
+ */
+typedef struct ds_vit_key_bounds {
+  int8_t* hi_lo;        /* device [n_pages, kv_heads, 2, head_dim]; 16-byte aligned */
+  uint8_t* exp;         /* device [n_pages, kv_heads] */
+} ds_vit_key_bounds;
+
+int ds_vit_cache_copy(const ds_vit_cache* cache, const ds_vit_key_bounds* bounds, const ds_vit_page_copies* copies,
+                      int32_t* status, void* stream);
+
 /* Kernel kinds reported by ds_vit_set_kernel_timer. */
 /* PATCH_GEMM patchifies and normalises the pixels inside its A-tile load;
  * MERGER_GEMM1 gathers the 3x3 windows inside its A-tile load. */

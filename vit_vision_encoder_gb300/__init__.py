@@ -93,6 +93,22 @@ class RotaryTable(C.Structure):
                 ("pairing", C.c_int32)]
 
 
+class PoolArrays(C.Structure):
+    _fields_ = [("refs", C.c_void_p), ("n_pages", C.c_int64), ("page", C.c_int32)]
+
+
+class TableArrays(C.Structure):
+    _fields_ = [("table", C.c_void_p), ("kv_len", C.c_void_p), ("slots", C.c_int32), ("table_cols", C.c_int32)]
+
+
+class CopyArrays(C.Structure):
+    _fields_ = [("src", C.c_void_p), ("dst", C.c_void_p), ("count", C.c_void_p), ("cap", C.c_int32)]
+
+
+class BoundArrays(C.Structure):
+    _fields_ = [("hi_lo", C.c_void_p), ("exp", C.c_void_p)]
+
+
 # Every symbol include/dsvit.h declares: name -> (restype, argtypes).
 _VP, _I32, _I64, _SZ, _F = C.c_void_p, C.c_int32, C.c_int64, C.c_size_t, C.c_float
 _P_I32, _P_I64 = C.POINTER(C.c_int32), C.POINTER(C.c_int64)
@@ -144,6 +160,14 @@ SIGNATURES = {
     "ds_vit_rotary_init": (C.c_int, [_I32, C.c_double, _VP, _I32, _VP, _I32, _I32, C.POINTER(RotaryTable)]),
     "ds_vit_qk_norm_rope": (C.c_int, [C.POINTER(RotaryTable), _VP, _I64, _I32, _VP, _I64, _I32, _I64, _VP, _I64, _VP,
                                       _VP, _F, _VP, _I64, _VP, _I64, _VP]),
+    "ds_vit_pages_resize": (C.c_int, [C.POINTER(PoolArrays), C.POINTER(TableArrays), _VP, _VP, _I32,
+                                      C.POINTER(CopyArrays), _VP, _VP]),
+    "ds_vit_pages_release": (C.c_int, [C.POINTER(PoolArrays), C.POINTER(TableArrays), _VP, _VP, _VP, _I32, _VP, _VP]),
+    "ds_vit_pages_fork": (C.c_int, [C.POINTER(PoolArrays), C.POINTER(TableArrays), _VP, _VP, _I32,
+                                    C.POINTER(CopyArrays), _VP, _VP]),
+    "ds_vit_pages_compact": (C.c_int, [C.POINTER(PoolArrays), C.POINTER(TableArrays), C.POINTER(CopyArrays), _VP,
+                                       _VP]),
+    "ds_vit_cache_copy": (C.c_int, [C.POINTER(Cache), C.POINTER(BoundArrays), C.POINTER(CopyArrays), _VP, _VP]),
 }
 
 
@@ -736,6 +760,164 @@ def cache_attention(cache, chunks, q, scale=None, window=0, sinks=0, out=None, w
                                      dim ** -0.5 if scale is None else scale, window, sinks, out.data_ptr(), os_,
                                      ws.data_ptr(), ws.numel(), status.data_ptr(), stream), "ds_vit_cache_attention")
     return out, status
+
+
+# ---------------------------------------------------------------- pages of many sequences
+
+def _int32s(t, shape, device, where):
+    if t.dtype is not _i32_type or tuple(t.shape) != shape or not t.is_contiguous() or t.device != device:
+        _refuse(where)
+    return t
+
+
+class PagePool:
+    """Which pages are in use (ds_vit_page_pool): refs int32 CUDA tensor [n_pages], the
+    number of table entries that name each page.  Holds it."""
+
+    def __init__(self, refs, page):
+        _cache_names()
+        self.refs = _int32s(refs, (refs.numel(),), refs.device, "PagePool")
+        if page not in (16, 32, 64, 128):
+            _refuse("PagePool")
+        self.page, self.device_index = page, refs.get_device()
+        self.c = PoolArrays(refs.data_ptr(), refs.numel(), page)
+        self.ref = C.byref(self.c)
+
+    @classmethod
+    def empty(cls, n_pages, page, device="cuda"):
+        """A pool of free pages."""
+        return cls(_torch().zeros(n_pages, dtype=_torch().int32, device=device), page)
+
+
+class PageTables:
+    """The pages of every sequence (ds_vit_page_tables): int32 CUDA tensors table [slots,
+    table_cols] and kv_len [slots].  Holds them; Chunks may be given the same ones."""
+
+    def __init__(self, table, kv_len):
+        _cache_names()
+        if table.dim() != 2:
+            _refuse("PageTables")
+        self.table = _int32s(table, tuple(table.shape), kv_len.device, "PageTables")
+        self.kv_len = _int32s(kv_len, (table.shape[0],), kv_len.device, "PageTables")
+        self.device_index = table.get_device()
+        self.c = TableArrays(table.data_ptr(), kv_len.data_ptr(), *table.shape)
+        self.ref = C.byref(self.c)
+
+    @classmethod
+    def empty(cls, slots, table_cols, device="cuda"):
+        """Tables of sequences without tokens."""
+        torch = _torch()
+        return cls(torch.full((slots, table_cols), -1, dtype=torch.int32, device=device),
+                   torch.zeros(slots, dtype=torch.int32, device=device))
+
+
+class PageCopies:
+    """The pages to copy after a call (ds_vit_page_copies): int32 CUDA tensors src [cap], dst
+    [cap] and count [1], of which the first ``count`` pairs are meant."""
+
+    def __init__(self, cap, device="cuda"):
+        torch = _cache_names()
+        if not 1 <= cap < 1 << 31:
+            _refuse("PageCopies")
+        self.src, self.dst = (torch.zeros(cap, dtype=torch.int32, device=device) for _ in range(2))
+        self.count = torch.zeros(1, dtype=torch.int32, device=device)
+        self.device_index = self.count.get_device()
+        self.c = CopyArrays(self.src.data_ptr(), self.dst.data_ptr(), self.count.data_ptr(), cap)
+        self.ref = C.byref(self.c)
+
+
+def _pages_call(fn, where, pool, tables, lists, copies, status):
+    d = pool.device_index
+    if (d < 0 or tables.device_index != d or _cuda_device() != d
+            or (copies is not None and copies.device_index != d)):
+        _refuse(where)
+    if status is None:
+        status = _torch().zeros(1, dtype=_i32_type, device=pool.refs.device)
+    elif status.dtype is not _i32_type or status.get_device() != d or not status.numel():
+        _refuse(where)
+    n = lists[0].numel() if lists else 0
+    for t in lists:
+        if t.dtype is not _i32_type or t.dim() != 1 or t.numel() != n or not t.is_contiguous() or t.get_device() != d:
+            _refuse(where)
+    if lists and n == 0:                    # an empty tensor has no address
+        if copies is not None:
+            copies.count.zero_()
+        return status
+    args = [t.data_ptr() for t in lists]
+    if lists:
+        args.append(n)
+    if copies is not None:
+        args.append(copies.ref)
+    check(fn(pool.ref, tables.ref, *args, status.data_ptr(), _raw_stream(d)), where)
+    return status
+
+
+def pages_resize(pool, tables, slots, lengths, copies, status=None):
+    """Sequences ``slots`` get ``lengths`` tokens (int32 CUDA tensors [n]): pages are taken or
+    given back (ds_vit_pages_resize).  ``copies`` receives the pages to copy
+    (cache_copy, before anything else is done with the pool).  Returns ``status``."""
+    return _pages_call(lib.ds_vit_pages_resize, "ds_vit_pages_resize", pool, tables, (slots, lengths), copies, status)
+
+
+def pages_release(pool, tables, slots, begin, end, status=None):
+    """Gives back the pages that lie wholly in tokens begin[i] .. end[i] - 1 of
+    sequence slots[i] (ds_vit_pages_release).  Returns ``status``."""
+    return _pages_call(lib.ds_vit_pages_release, "ds_vit_pages_release", pool, tables, (slots, begin, end), None,
+                       status)
+
+
+def pages_fork(pool, tables, src, dst, copies, status=None):
+    """Sequence dst[i], without tokens so far, becomes the same as src[i]: full pages are
+    shared, the last one is copied (ds_vit_pages_fork, then cache_copy).  Returns ``status``."""
+    return _pages_call(lib.ds_vit_pages_fork, "ds_vit_pages_fork", pool, tables, (src, dst), copies, status)
+
+
+def pages_compact(pool, tables, copies, status=None):
+    """Moves the pages in use to the front of the pool (ds_vit_pages_compact, then
+    cache_copy).  Returns ``status``."""
+    return _pages_call(lib.ds_vit_pages_compact, "ds_vit_pages_compact", pool, tables, (), copies, status)
+
+
+def cache_copy(cache, copies, bounds=None, status=None):
+    """Copies the pages that ``copies`` lists in one layer's cache, their KeyBounds with
+    them (ds_vit_cache_copy).  Returns ``status``."""
+    d, stream, status = _on_device(cache, copies, status, "ds_vit_cache_copy")
+    if bounds is not None and not bounds.of(cache):
+        _refuse("ds_vit_cache_copy")
+    check(lib.ds_vit_cache_copy(cache.ref, None if bounds is None else bounds.ref, copies.ref, status.data_ptr(),
+                                stream), "ds_vit_cache_copy")
+    return status
+
+
+# ---------------------------------------------------------------- the blocks of a cache that a row attends to
+
+class KeyBounds:
+    """Bounds of the keys of every page (ds_vit_key_bounds): hi_lo int8 CUDA tensor [n_pages,
+    kv_heads, 2, head_dim] and exp uint8 [n_pages, kv_heads].  Holds them."""
+
+    def __init__(self, hi_lo, exp):
+        torch = _cache_names()
+        if (hi_lo.dtype != torch.int8 or hi_lo.dim() != 4 or hi_lo.shape[2] != 2 or not hi_lo.is_contiguous()
+                or exp.dtype != torch.uint8 or exp.shape != hi_lo.shape[:2] or not exp.is_contiguous()
+                or exp.device != hi_lo.device):
+            _refuse("KeyBounds")
+        self.hi_lo, self.exp, self.device_index = hi_lo, exp, hi_lo.get_device()
+        self.shape = tuple(hi_lo.shape)
+        self.c = BoundArrays(hi_lo.data_ptr(), exp.data_ptr())
+        self.ref = C.byref(self.c)
+
+    @classmethod
+    def empty(cls, cache):
+        """Bounds of a cache's pages, of none of which they are known yet."""
+        torch = _torch()
+        n, heads, _, dim = cache.k.shape
+        return cls(torch.empty((n, heads, 2, dim), dtype=torch.int8, device=cache.device),
+                   torch.empty((n, heads), dtype=torch.uint8, device=cache.device))
+
+    def of(self, cache):
+        """Whether they are bounds of such a cache, on its device."""
+        return (self.device_index == cache.device_index
+                and self.shape == (cache.c.n_pages, cache.kv_heads, 2, cache.head_dim))
 
 
 # ---------------------------------------------------------------- norms and rotation in front of the cache

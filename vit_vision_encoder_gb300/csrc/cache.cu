@@ -328,8 +328,8 @@ int tokens_per_warp(int head_dim, int kv_heads, int64_t rows) {
 
 }  // namespace
 
-int check_cache(const ds_vit_cache* c, const ds_vit_chunks* b, int64_t rows, CacheView* cv, ChunkView* bv) {
-  if (!c || !b || !c->k || !c->v || !b->row_off || !b->kv_len || !b->table) return DS_VIT_EINVAL;
+int check_pages_of(const ds_vit_cache* c, CacheView* cv) {
+  if (!c || !c->k || !c->v) return DS_VIT_EINVAL;
   if ((c->kind != DS_VIT_CACHE_BF16 && c->kind != DS_VIT_CACHE_E4M3) || (c->head_dim != 64 && c->head_dim != 128) ||
       c->kv_heads < 1 || c->kv_heads > DS_VIT_CACHE_MAX_HEADS || c->n_pages < 1)
     return DS_VIT_EINVAL;
@@ -338,15 +338,23 @@ int check_cache(const ds_vit_cache* c, const ds_vit_chunks* b, int64_t rows, Cac
   if ((1 << shift) != c->page) return DS_VIT_EINVAL;
   if (c->kind == DS_VIT_CACHE_E4M3 && (!c->k_exp || !c->v_exp || !aligned(c->k_exp, 16) || !aligned(c->v_exp, 16)))
     return DS_VIT_EINVAL;
-  if (!aligned(c->k, 16) || !aligned(c->v, 16) || !aligned(b->row_off, 4) || !aligned(b->kv_len, 4) ||
-      !aligned(b->table, 4))
-    return DS_VIT_EINVAL;
-  if (b->n < 1 || b->n > DS_VIT_MAX_SEQS || b->table_cols < 1 || b->max_rows < 1 || rows < 0) return DS_VIT_EINVAL;
-  // Rows of the pages are TMA coordinates, and positions are int32.
-  if (c->n_pages > INT32_MAX / (c->page * c->kv_heads) || b->table_cols > (INT32_MAX - 255) / c->page || rows > INT32_MAX / 2)
-    return DS_VIT_ERANGE;
+  if (!aligned(c->k, 16) || !aligned(c->v, 16)) return DS_VIT_EINVAL;
+  // Rows of the pages are TMA coordinates.
+  if (c->n_pages > INT32_MAX / (c->page * c->kv_heads)) return DS_VIT_ERANGE;
   *cv = CacheView{static_cast<uint8_t*>(c->k), static_cast<uint8_t*>(c->v), c->k_exp, c->v_exp,
                   c->n_pages, c->kv_heads, shift};
+  return DS_VIT_OK;
+}
+
+int check_cache(const ds_vit_cache* c, const ds_vit_chunks* b, int64_t rows, CacheView* cv, ChunkView* bv) {
+  if (!b || !b->row_off || !b->kv_len || !b->table) return DS_VIT_EINVAL;
+  const int rc = check_pages_of(c, cv);
+  if (rc == DS_VIT_EINVAL) return rc;
+  if (!aligned(b->row_off, 4) || !aligned(b->kv_len, 4) || !aligned(b->table, 4)) return DS_VIT_EINVAL;
+  if (b->n < 1 || b->n > DS_VIT_MAX_SEQS || b->table_cols < 1 || b->max_rows < 1 || rows < 0) return DS_VIT_EINVAL;
+  if (rc) return rc;
+  // Positions are int32.
+  if (b->table_cols > (INT32_MAX - 255) / c->page || rows > INT32_MAX / 2) return DS_VIT_ERANGE;
   *bv = ChunkView{b->row_off, b->kv_len, b->table, b->n, b->table_cols, b->max_rows, static_cast<int>(rows)};
   return DS_VIT_OK;
 }

@@ -28,8 +28,9 @@ struct ChunkView {
   int rows;
 };
 
-// Checks of a cache and a chunk description (host values only); fills the
+// Checks of a cache, and of one with a chunk description (host values only); they fill the
 // kernels' views.
+int check_pages_of(const ds_vit_cache* c, CacheView* cv);
 int check_cache(const ds_vit_cache* c, const ds_vit_chunks* b, int64_t rows, CacheView* cv, ChunkView* bv);
 
 inline bool aligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
