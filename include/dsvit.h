@@ -659,6 +659,70 @@ typedef struct ds_vit_key_bounds {
 int ds_vit_cache_copy(const ds_vit_cache* cache, const ds_vit_key_bounds* bounds, const ds_vit_page_copies* copies,
                       int32_t* status, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Attention over a part of a long cache that each row chooses: the blocks are the
+ * pages of its sequence (block j: tokens j * page and on), and a cheap score from
+ * bounds of their keys ranks them.
+ *
+ * Bounds of a full block and K/V head, over its keys k_j (as the pages hold them):
+ *   H_d = ceil(max_j k_jd / 2^e),  L_d = floor(min_j k_jd / 2^e),
+ * e the least integer, at least -100, with |k_jd| <= 127 * 2^e throughout: 8 bits
+ * each, hi_lo[page, head] = H, L and exp[page, head] = e + 127, or 255 for a block that
+ * holds an infinity or NaN.
+ *
+ * Score of a block for a row and K/V head, whose g query heads choose together:
+ * with G the least power of two not below g and f the least integer, at least -100, with
+ * |q_hd| * G <= 1016 * 2^f throughout,
+ *   n_hd = q_hd / 2^f rounded to a whole number (halves to even),
+ *   score = 2^e * sum_d (H_d sum_h max(n_hd, 0) + L_d sum_h min(n_hd, 0)),
+ * an upper bound, but for the rounding of q, of the sum over h of q_h . k_j for every
+ * key of the block.  The sum is a whole number under 2^24: no order of additions
+ * changes it, and equal inputs give equal lists.  A block of exponent 255 comes before
+ * all others; a row with an infinity or NaN scores 0 everywhere.
+ * ------------------------------------------------------------------------- */
+#define DS_VIT_SELECT_MAX_COLS 49152  /* table columns */
+#define DS_VIT_SELECT_MAX_TOP 4096    /* blocks of a list */
+
+/*
+ * The calls take cache, chunks, rows and status as the calls on the cache do.
+ *
+ * ds_vit_cache_bounds: bounds of the blocks that the call's rows completed (written
+ * before, by ds_vit_cache_write): those whose last token is among them.  Others
+ * stay as they were.
+ *
+ * ds_vit_cache_select: for each row and K/V head the list of blocks to attend to,
+ * blocks (device int32 [rows, kv_heads, top]), ascending and filled up with -1.  The row
+ * at position p has the blocks 0 .. b, b = p / page: of these the first `first` and the
+ * last `last` (b among them), then those of the highest scores, the lower of equals
+ * first, `top` in all.  Blocks whose table entry is below 0 (given away) are not
+ * taken.  Rows in front of position 0 get -1 throughout, packed rows of no sequence
+ * stay as they were.  Bounds are read of every block of the sequences but the
+ * rows' own.
+ * DS_VIT_EINVAL for first < 0, last < 1, top outside first + last ..
+ * DS_VIT_SELECT_MAX_TOP, bounds or blocks null or misaligned (hi_lo and blocks 16 bytes);
+ * DS_VIT_ERANGE for table_cols past DS_VIT_SELECT_MAX_COLS, rows * kv_heads of 2^31 or
+ * more.  Otherwise as ds_vit_cache_attention.
+ *
+ * ds_vit_cache_attention_blocks: attention of each row over the tokens of its
+ * list's blocks up to its own position,
+ *   out[row, h] = bf16(softmax_j(scale * q . k_j) v),
+ * zeros for a row that sees nothing.  Lists may be in any order and made anywhere: an
+ * entry outside 0 .. p / page names no token, a block named twice counts twice.  A named
+ * block without a page in the table records DS_VIT_ERANGE and is left out.  Scores,
+ * maxima and sums are fp32; weights are rounded before their product with the
+ * value as in ds_vit_cache_attention.  Needs no workspace.
+ * DS_VIT_ERANGE for rows * heads of 2^31 or more; otherwise as ds_vit_cache_attention.
+ */
+int ds_vit_cache_bounds(const ds_vit_cache* cache, const ds_vit_chunks* chunks, const ds_vit_key_bounds* bounds,
+                        int64_t rows, int32_t* status, void* stream);
+int ds_vit_cache_select(const ds_vit_cache* cache, const ds_vit_chunks* chunks, const ds_vit_key_bounds* bounds,
+                        const void* q, int64_t q_stride, int64_t rows, int32_t heads, int32_t top, int32_t first,
+                        int32_t last, int32_t* blocks, int32_t* status, void* stream);
+int ds_vit_cache_attention_blocks(const ds_vit_cache* cache, const ds_vit_chunks* chunks, const void* q,
+                                  int64_t q_stride, int64_t rows, int32_t heads, float scale,
+                                  const int32_t* blocks, int32_t top, void* out, int64_t out_stride,
+                                  int32_t* status, void* stream);
+
 /* Kernel kinds reported by ds_vit_set_kernel_timer. */
 /* PATCH_GEMM patchifies and normalises the pixels inside its A-tile load;
  * MERGER_GEMM1 gathers the 3x3 windows inside its A-tile load. */

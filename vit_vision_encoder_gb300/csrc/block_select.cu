@@ -1,0 +1,512 @@
+// Bounds of the keys of a cache's pages and the choice of the blocks that each row
+// attends to (include/dsvit.h, ds_vit_cache_bounds and ds_vit_cache_select).
+//
+// Bounds: each completed page is read once, by one warp a K/V head; bound by memory.
+//
+// Selection: a CTA takes a K/V head of up to eight rows of one sequence.  The scores are
+// a product of the blocks' bounds [blocks, 2 D] with the rows' shared queries [2 D, 8]
+// on warp MMAs, blocks in the place of M: both operands are small whole numbers, exact in
+// fp16 (|n| <= 1024, |H| <= 127), and so is every partial sum (< 2^24), so the list does not depend on
+// the order of anything.  The order of the 2 D terms is free, so a lane uses the 16 bytes
+// that it loads where they lie.  Scores stay in shared memory as whole numbers that order like
+// them; a search for the threshold, bit by bit, counts how many are above it, by one warp
+// a row (or the whole CTA where it has one row), and stops as soon as the count fits.  Single
+// rows of few sequences share the scoring among the CTAs of a cluster, which put
+// their scores into the first one's shared memory.
+#include <cuda_fp16.h>
+
+#include <algorithm>
+
+#include "cache.cuh"
+
+namespace dsvit {
+
+namespace {
+
+// ------------------------------------------------------------------ bounds
+
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float min_nan(float a, float b) {
+  float r;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+// The least e >= -100 with a <= (1 + 126/128) 2^(e + shift), a the bf16 value of bits `bits` << 16.
+__device__ __forceinline__ int least_exponent(uint32_t bits, int shift) {
+  const int e = static_cast<int>(bits >> 7) - 127 - shift + ((bits & 127u) > 126u ? 1 : 0);
+  return max(e, -100);
+}
+__device__ __forceinline__ float power_of_two(int e) { return __int_as_float((e + 127) << 23); }
+
+struct BoundsArgs {
+  CacheView c;
+  ChunkView b;
+  int8_t* hi_lo;
+  uint8_t* exp;
+  int* status;
+};
+
+constexpr int kBoundWarps = 8;
+
+template <int D, bool E4M3>
+__global__ void __launch_bounds__(32 * kBoundWarps) cache_bounds_kernel(const __grid_constant__ BoundsArgs a) {
+  constexpr int kPer = E4M3 ? 16 : 8;                       // values in 16 bytes
+  constexpr int kLanes = D / kPer, kKeys = 32 / kLanes;     // lanes of a key, keys of a load
+  constexpr int kLoads = 16 / kKeys;                        // of 16 keys
+  grid_dep_launch();
+  grid_dep_wait();
+  const int lane = threadIdx.x & 31, s = blockIdx.y;
+  const Seq q = load_seq(a.b, a.c.page_shift, s, a.status);
+  const int end = q.kv >> a.c.page_shift, page = 1 << a.c.page_shift;
+  for (int j = (max(q.kv - q.c, 0) >> a.c.page_shift) + blockIdx.x; j < end; j += gridDim.x) {
+    const int64_t at = page_of(a.b, a.c, s, j << a.c.page_shift, a.status);
+    if (at < 0) continue;
+    for (int head = threadIdx.x >> 5; head < a.c.kv_heads; head += kBoundWarps) {
+      const int64_t row0 = cache_row(a.c, at, head, 0) + lane / kLanes;
+      const uint4* from = reinterpret_cast<const uint4*>(a.c.k) + row0 * kLanes + lane % kLanes;
+      float hi[kPer], lo[kPer];
+#pragma unroll
+      for (int x = 0; x < kPer; ++x) hi[x] = -INFINITY, lo[x] = INFINITY;
+      for (int k0 = 0; k0 < page; k0 += 16) {
+        uint4 u[kLoads];
+        uint32_t byte[kLoads];
+#pragma unroll
+        for (int y = 0; y < kLoads; ++y) {
+          u[y] = from[(k0 + y * kKeys) * kLanes];
+          byte[y] = E4M3 ? a.c.k_exp[row0 + k0 + y * kKeys] : 0u;
+        }
+#pragma unroll
+        for (int y = 0; y < kLoads; ++y) {
+          const uint32_t w[4] = {u[y].x, u[y].y, u[y].z, u[y].w};
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            if constexpr (E4M3) {
+              const float f = exp_factor(byte[y]);
+              const float2 p = e4m3x2_to_float2(static_cast<uint16_t>(w[x])),
+                           r = e4m3x2_to_float2(static_cast<uint16_t>(w[x] >> 16));
+              const float v[4] = {p.x * f, p.y * f, r.x * f, r.y * f};
+#pragma unroll
+              for (int z = 0; z < 4; ++z) {
+                hi[4 * x + z] = max_nan(hi[4 * x + z], v[z]);
+                lo[4 * x + z] = min_nan(lo[4 * x + z], v[z]);
+              }
+            } else {
+              hi[2 * x] = max_nan(hi[2 * x], bf16lo(w[x]));
+              lo[2 * x] = min_nan(lo[2 * x], bf16lo(w[x]));
+              hi[2 * x + 1] = max_nan(hi[2 * x + 1], bf16hi(w[x]));
+              lo[2 * x + 1] = min_nan(lo[2 * x + 1], bf16hi(w[x]));
+            }
+          }
+        }
+      }
+      uint32_t top = 0;      // magnitudes order like their bits, infinities and NaN on top
+#pragma unroll
+      for (int x = 0; x < kPer; ++x) {
+#pragma unroll
+        for (int o = kLanes; o < 32; o <<= 1) {
+          hi[x] = max_nan(hi[x], __shfl_xor_sync(0xFFFFFFFFu, hi[x], o));
+          lo[x] = min_nan(lo[x], __shfl_xor_sync(0xFFFFFFFFu, lo[x], o));
+        }
+        top = max(top, max(__float_as_uint(hi[x]) & 0x7FFFFFFFu, __float_as_uint(lo[x]) & 0x7FFFFFFFu));
+      }
+#pragma unroll
+      for (int o = 1; o < kLanes; o <<= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+      const bool fine = top < 0x7F800000u;
+      const int e = least_exponent(top >> 16, 6);
+      const float f = power_of_two(-e);
+      if (lane < kLanes) {
+        int8_t* to = a.hi_lo + (at * a.c.kv_heads + head) * 2 * D + lane * kPer;
+        uint32_t h[kPer / 4] = {}, l[kPer / 4] = {};
+#pragma unroll
+        for (int x = 0; x < kPer; ++x) {
+          if (!fine) continue;
+          h[x / 4] |= (static_cast<uint32_t>(__float2int_ru(hi[x] * f)) & 255u) << 8 * (x & 3);
+          l[x / 4] |= (static_cast<uint32_t>(__float2int_rd(lo[x] * f)) & 255u) << 8 * (x & 3);
+        }
+        if constexpr (E4M3) {
+          *reinterpret_cast<uint4*>(to) = make_uint4(h[0], h[1], h[2], h[3]);
+          *reinterpret_cast<uint4*>(to + D) = make_uint4(l[0], l[1], l[2], l[3]);
+        } else {
+          *reinterpret_cast<uint2*>(to) = make_uint2(h[0], h[1]);
+          *reinterpret_cast<uint2*>(to + D) = make_uint2(l[0], l[1]);
+        }
+        if (lane == 0) a.exp[at * a.c.kv_heads + head] = static_cast<uint8_t>(fine ? e + 127 : 255);
+      }
+    }
+  }
+}
+
+// ------------------------------------------------------------------ selection
+
+struct SelectArgs {
+  ChunkView b;
+  int64_t n_pages;
+  int kv_heads, page_shift;
+  const int8_t* hi_lo;
+  const uint8_t* exp;
+  const bf16* q;
+  int64_t q_stride;
+  int group, log2_group;     // G of the header: 2^log2_group >= group
+  int top, first, last;
+  int32_t* blocks;
+  int* status;
+  int tile_rows;             // rows of a CTA
+  int places;                // scores of a row in shared memory
+};
+
+constexpr int kSelectWarps = 8, kSelectThreads = 32 * kSelectWarps;
+constexpr uint32_t kForced = 0xFFFFFFFFu, kNotFinite = 0xFFFFFFFEu;   // above every score's number; 0: not a candidate
+
+// A whole number that orders like the float (finite: under kNotFinite, over 0).
+__device__ __forceinline__ uint32_t ordered(float x) {
+  const uint32_t u = __float_as_uint(x + 0.f);
+  return u ^ (static_cast<uint32_t>(static_cast<int32_t>(u) >> 31) | 0x80000000u);
+}
+
+// Four signed bytes -> fp16 pairs: bytes + 128 become the low bits of 1024 + x.
+__device__ __forceinline__ uint32_t f16_of_bytes(uint32_t biased, uint32_t which) {
+  uint32_t r;
+  const uint32_t h = __byte_perm(biased, 0x64646464u, which);
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(h), "r"(0x64806480u));
+  return r;
+}
+
+// The shared query of one row: w[0 .. D - 1] sums of positive, w[D .. 2 D - 1] of negative parts.  By one warp.
+template <int D>
+__device__ __forceinline__ void shared_query(const SelectArgs& a, const bf16* q, __half* w, int lane) {
+  constexpr int kPer = D / 32;
+  auto load = [&](int h, float (&x)[kPer]) {
+    const uint32_t* at = reinterpret_cast<const uint32_t*>(q + h * D) + lane * (kPer / 2);
+#pragma unroll
+    for (int y = 0; y < kPer / 2; ++y) {
+      const uint32_t u = __ldg(at + y);
+      x[2 * y] = bf16lo(u);
+      x[2 * y + 1] = bf16hi(u);
+    }
+  };
+  uint32_t top = 0;
+#pragma unroll 4
+  for (int h = 0; h < a.group; ++h) {
+    float x[kPer];
+    load(h, x);
+#pragma unroll
+    for (int y = 0; y < kPer; ++y) top = max(top, __float_as_uint(x[y]) & 0x7FFFFFFFu);
+  }
+  top = __reduce_max_sync(0xFFFFFFFFu, top);
+  // 1016 = (1 + 126/128) 2^9
+  const int f = least_exponent(top >> 16, 9 - a.log2_group);
+  const float by = power_of_two(-f / 2), rest = power_of_two(-f - -f / 2);     // 2^-f may be no float
+  int up[kPer] = {}, down[kPer] = {};
+  if (top < 0x7F800000u) {
+#pragma unroll 4
+    for (int h = 0; h < a.group; ++h) {
+      float x[kPer];
+      load(h, x);
+#pragma unroll
+      for (int y = 0; y < kPer; ++y) {
+        const int n = __float2int_rn(x[y] * by * rest);
+        up[y] += max(n, 0);
+        down[y] += min(n, 0);
+      }
+    }
+  }
+#pragma unroll
+  for (int y = 0; y < kPer; ++y) {
+    w[lane * kPer + y] = __int2half_rn(up[y]);
+    w[D + lane * kPer + y] = __int2half_rn(down[y]);
+  }
+}
+
+// The list of one row from its keys, by `kThreads` threads (a warp or the CTA).
+template <int kThreads>
+__device__ __forceinline__ void pick(const uint32_t* keys, int n, int top, int32_t* out, int (*sums)[kSelectWarps]) {
+  const int tid = threadIdx.x & (kThreads - 1), lane = threadIdx.x & 31, warp = tid >> 5;
+  int turn = 0;
+  auto total = [&](int x) {             // over the group
+    x = __reduce_add_sync(0xFFFFFFFFu, x);
+    if constexpr (kThreads > 32) {
+      if (lane == 0) sums[turn][warp] = x;
+      __syncthreads();
+      x = 0;
+#pragma unroll
+      for (int y = 0; y < kSelectWarps; ++y) x += sums[turn][y];
+      turn ^= 1;
+    }
+    return x;
+  };
+  auto count = [&](uint32_t from) {     // keys >= from
+    int x = 0;
+#pragma unroll 4
+    for (int i = tid; i < n; i += kThreads) x += keys[i] >= from;
+    return total(x);
+  };
+  // The threshold: all keys over it are taken, and the first `ties` of those equal to it.
+  uint32_t over = 0;
+  int ties = 0;
+  if (count(1) > top) {
+    uint32_t t = 0;                     // the largest with at least `top` keys >= t, built from the top bit
+    bool fits = false;
+    for (int bit = 31; bit >= 0 && !fits; --bit) {
+      const uint32_t to = t | 1u << bit;
+      const int x = count(to);
+      if (x >= top) t = to;
+      fits = x == top;
+    }
+    over = fits ? t - 1 : t;
+    ties = fits ? 0 : top - (t == kForced ? 0 : count(t + 1));
+  }
+  const auto lower = (1u << lane) - 1;
+  // Each warp of the group has a run of blocks; what the warps before it take comes first.
+  const int each = (n + kThreads - 1) / kThreads * 32, begin = min(n, warp * each), end = min(n, begin + each);
+  int taken = 0, equal = 0;
+  if constexpr (kThreads > 32) {
+    int x = 0, e = 0;
+    for (int i = begin + lane; i < end; i += 32) {
+      x += keys[i] > over;
+      e += keys[i] == over;
+    }
+    x = __reduce_add_sync(0xFFFFFFFFu, x);
+    e = __reduce_add_sync(0xFFFFFFFFu, e);
+    __syncthreads();                    // the counts' sums have been read
+    if (lane == 0) sums[0][warp] = x, sums[1][warp] = e;
+    __syncthreads();
+    for (int y = 0; y < warp; ++y) {
+      taken += sums[0][y];
+      equal += sums[1][y];
+    }
+    taken += min(equal, ties);
+  }
+  for (int i0 = begin; i0 < end; i0 += 32) {
+    const int i = i0 + lane;
+    const uint32_t k = i < end ? keys[i] : 0u;
+    const uint32_t same = __ballot_sync(0xFFFFFFFFu, i < end && k == over);
+    const bool on = i < end && (k > over || (k == over && equal + __popc(same & lower) < ties));
+    const uint32_t all = __ballot_sync(0xFFFFFFFFu, on);
+    if (on) out[taken + __popc(all & lower)] = i;
+    taken += __popc(all);
+    equal += __popc(same);
+  }
+  if constexpr (kThreads > 32) {
+    __syncthreads();
+    if (warp == kSelectWarps - 1 && lane == 0) sums[0][0] = taken;
+    __syncthreads();
+    taken = sums[0][0];
+  }
+  for (int i = taken + tid; i < top; i += kThreads) out[i] = -1;
+}
+
+// kSingle: a row a CTA, or a cluster.
+template <int D, bool kSingle>
+__global__ void __launch_bounds__(kSelectThreads) cache_select_kernel(const __grid_constant__ SelectArgs a) {
+  constexpr int kSteps = 2 * D / 64;                // 16-byte loads of a block, four MMAs each
+  extern __shared__ uint4 dynamic[];
+  uint32_t* const keys = reinterpret_cast<uint32_t*>(dynamic);
+  __shared__ __align__(16) __half w[8][2 * D + 8];
+  __shared__ int sums[2][kSelectWarps];
+  grid_dep_launch();
+  grid_dep_wait();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+  uint32_t rank = 0, ranks = 1;
+  if constexpr (kSingle) {
+    rank = cluster_rank();
+    asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(ranks));
+    if (ranks > 1) cluster_sync();                  // the first CTA's shared memory is there
+  }
+  const int64_t tile = blockIdx.x / ranks;
+  const int head = static_cast<int>(tile % a.kv_heads);
+  const int64_t r_end = min(static_cast<int64_t>(a.b.rows), (tile / a.kv_heads + 1) * a.tile_rows);
+  const int page = 1 << a.page_shift;
+  // The rows of one sequence after another.
+  for (int64_t ra = tile / a.kv_heads * a.tile_rows; ra < r_end;) {
+    const int s = find_seq(a.b, static_cast<int>(ra), lane);
+    const Seq q = s < 0 ? Seq{0, 0, 0} : load_seq(a.b, a.page_shift, s, a.status);
+    if (static_cast<unsigned>(ra - q.row0) >= static_cast<unsigned>(q.c)) {     // of no sequence, or refused
+      ++ra;
+      continue;
+    }
+    const int n_rows = static_cast<int>(min(r_end, static_cast<int64_t>(q.row0) + q.c) - ra);
+    const int p0 = q.kv - q.c + static_cast<int>(ra - q.row0);                  // position of the first
+    const int blocks = max(p0 + n_rows - 1 + page, 0) >> a.page_shift;          // of the last
+    if (warp < n_rows)
+      shared_query<D>(a, a.q + (ra + warp) * a.q_stride + static_cast<int64_t>(head) * a.group * D, w[warp], lane);
+    __syncthreads();
+    uint32_t qf[kSteps][4][2];
+#pragma unroll
+    for (int j = 0; j < kSteps; ++j) {
+      const uint32_t* from = reinterpret_cast<const uint32_t*>(&w[g][64 * j + 16 * t]);
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        qf[j][x][0] = g < n_rows ? from[2 * x] : 0u;
+        qf[j][x][1] = g < n_rows ? from[2 * x + 1] : 0u;
+      }
+    }
+    const int32_t* table = a.b.table + static_cast<int64_t>(s) * a.b.table_cols;
+    const int step = 16 * kSelectWarps * static_cast<int>(ranks);
+    for (int k0 = 16 * (warp * static_cast<int>(ranks) + static_cast<int>(rank)); k0 < blocks; k0 += step) {
+      int32_t at[2];
+      uint4 u[2][kSteps];
+      uint32_t byte[2];
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        const int k = k0 + g + 8 * y;
+        at[y] = k < blocks ? __ldg(table + k) : -1;
+      }
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        if (at[y] >= a.n_pages) {
+          report_error(a.status, DS_VIT_ERANGE);
+          at[y] = -1;
+        }
+        const int64_t row = static_cast<int64_t>(max(at[y], 0)) * a.kv_heads + head;
+        const uint4* from = reinterpret_cast<const uint4*>(a.hi_lo + row * 2 * D) + t;
+        byte[y] = __ldg(a.exp + row);
+#pragma unroll
+        for (int j = 0; j < kSteps; ++j) u[y][j] = __ldg(from + 4 * j);
+      }
+      float c[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int j = 0; j < kSteps; ++j) {
+        const uint32_t b0[4] = {u[0][j].x, u[0][j].y, u[0][j].z, u[0][j].w};
+        const uint32_t b1[4] = {u[1][j].x, u[1][j].y, u[1][j].z, u[1][j].w};
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const uint32_t v0 = b0[x] ^ 0x80808080u, v1 = b1[x] ^ 0x80808080u;
+          const uint32_t m[4] = {f16_of_bytes(v0, 0x4140u), f16_of_bytes(v1, 0x4140u), f16_of_bytes(v0, 0x4342u),
+                                 f16_of_bytes(v1, 0x4342u)};
+          mma_f16(c, m, qf[j][x][0], qf[j][x][1]);
+        }
+      }
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        const int k = k0 + g + 8 * y;
+        const float f = power_of_two(max(static_cast<int>(byte[y]), 21) - 147);   // 2^(e - 20): every score is a float
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const int i = 2 * t + x, own = (p0 + i) >> a.page_shift;                // row, and its own block
+          if (i >= n_rows || k >= blocks) continue;
+          uint32_t key = byte[y] == 255u ? kNotFinite : ordered(c[2 * y + x] * f);
+          if (k < a.first || k > own - a.last) key = kForced;
+          if (k > own || at[y] < 0 || p0 + i < 0) key = 0;
+          if (kSingle && ranks > 1) {
+            const uint32_t to = mapa_shared(smem_u32(keys + k), 0);
+            asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(to), "r"(key) : "memory");
+          } else {
+            keys[i * a.places + k] = key;
+          }
+        }
+      }
+    }
+    if (kSingle && ranks > 1) {
+      cluster_sync();
+      if (rank != 0) return;
+    } else {
+      __syncthreads();
+    }
+    if constexpr (kSingle) {
+      pick<kSelectThreads>(keys, blocks, a.top, a.blocks + (ra * a.kv_heads + head) * a.top, sums);
+      return;
+    } else {
+      if (warp < n_rows)
+        pick<32>(keys + warp * a.places, blocks, a.top, a.blocks + ((ra + warp) * a.kv_heads + head) * a.top, sums);
+      __syncthreads();
+    }
+    ra += n_rows;
+  }
+}
+
+constexpr int kSelectKeyBytes = 200 * 1024;      // of shared memory, for scores
+static_assert(4 * DS_VIT_SELECT_MAX_COLS <= kSelectKeyBytes, "one row's scores");
+
+bool bad_bounds(const ds_vit_key_bounds* b) { return !b || !b->hi_lo || !aligned(b->hi_lo, 16) || !b->exp; }
+
+}  // namespace
+
+}  // namespace dsvit
+
+using namespace dsvit;
+
+extern "C" {
+
+int ds_vit_cache_bounds(const ds_vit_cache* cache, const ds_vit_chunks* chunks, const ds_vit_key_bounds* bounds,
+                        int64_t rows, int32_t* status, void* stream) {
+  BoundsArgs a{};
+  if (const int rc = check_cache(cache, chunks, rows, &a.c, &a.b)) return rc;
+  if (bad_bounds(bounds) || !status || !aligned(status, 4)) return DS_VIT_EINVAL;
+  if (rows == 0) return DS_VIT_OK;
+  a.hi_lo = bounds->hi_lo;
+  a.exp = bounds->exp;
+  a.status = reinterpret_cast<int*>(status);
+  const int64_t most = (std::min<int64_t>(rows, chunks->max_rows) + cache->page - 1) / cache->page;   // of a sequence
+  const dim3 grid(static_cast<unsigned>(std::min<int64_t>(most, 4096)), static_cast<unsigned>(chunks->n));
+  const bool e4m3 = cache->kind == DS_VIT_CACHE_E4M3;
+  auto* fn = cache->head_dim == 128 ? (e4m3 ? cache_bounds_kernel<128, true> : cache_bounds_kernel<128, false>)
+                                    : (e4m3 ? cache_bounds_kernel<64, true> : cache_bounds_kernel<64, false>);
+  return launched(launch_pdl(fn, grid, dim3(32 * kBoundWarps), 0, static_cast<cudaStream_t>(stream), a));
+}
+
+int ds_vit_cache_select(const ds_vit_cache* cache, const ds_vit_chunks* chunks, const ds_vit_key_bounds* bounds,
+                        const void* q, int64_t q_stride, int64_t rows, int32_t heads, int32_t top, int32_t first,
+                        int32_t last, int32_t* blocks, int32_t* status, void* stream) {
+  CacheView c;
+  SelectArgs a{};
+  if (const int rc = check_cache(cache, chunks, rows, &c, &a.b)) return rc;
+  if (bad_bounds(bounds) || !status || !aligned(status, 4) || heads < 1 || heads % c.kv_heads != 0 ||
+      heads / c.kv_heads > DS_VIT_CACHE_MAX_GROUP ||
+      bad_rows(q, q_stride, static_cast<int64_t>(heads) * cache->head_dim) || first < 0 || last < 1 ||
+      top > DS_VIT_SELECT_MAX_TOP || static_cast<int64_t>(first) + last > top || !blocks || !aligned(blocks, 16))
+    return DS_VIT_EINVAL;
+  if (chunks->table_cols > DS_VIT_SELECT_MAX_COLS || rows > INT32_MAX / c.kv_heads) return DS_VIT_ERANGE;
+  if (rows == 0) return DS_VIT_OK;
+  a.n_pages = c.n_pages;
+  a.kv_heads = c.kv_heads;
+  a.page_shift = c.page_shift;
+  a.hi_lo = bounds->hi_lo;
+  a.exp = bounds->exp;
+  a.q = static_cast<const bf16*>(q);
+  a.q_stride = q_stride;
+  a.group = heads / c.kv_heads;
+  while (1 << a.log2_group < a.group) ++a.log2_group;
+  a.top = top;
+  a.first = first;
+  a.last = last;
+  a.blocks = blocks;
+  a.status = reinterpret_cast<int*>(status);
+  a.places = (chunks->table_cols + 31) / 32 * 32 + 4;
+  // Rows of one sequence share the loads of its bounds where there are more than enough CTAs.
+  const int64_t units = rows * c.kv_heads;
+  const bool single = chunks->max_rows < 8 || units <= 4 * static_cast<int64_t>(num_sms()) || 8 * a.places > kSelectKeyBytes;
+  a.tile_rows = 1;
+  if (!single)
+    for (a.tile_rows = 8; 4 * static_cast<int64_t>(a.tile_rows) * a.places > kSelectKeyBytes;) a.tile_rows /= 2;
+  int ranks = 1;
+  if (single)
+    while (ranks < 8 && 2 * ranks * units <= 2 * static_cast<int64_t>(num_sms()) &&
+           2 * ranks * 16 * kSelectWarps <= chunks->table_cols)
+      ranks *= 2;
+  const int bytes = std::max(4 * a.tile_rows * a.places, 1024);
+  auto* fn = cache->head_dim == 128 ? (single ? cache_select_kernel<128, true> : cache_select_kernel<128, false>)
+                                    : (single ? cache_select_kernel<64, true> : cache_select_kernel<64, false>);
+  if (allow_smem(reinterpret_cast<const void*>(fn), kSelectKeyBytes + 1024) != cudaSuccess) return DS_VIT_ECUDA;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>((rows + a.tile_rows - 1) / a.tile_rows * c.kv_heads * ranks));
+  cfg.blockDim = dim3(kSelectThreads);
+  cfg.dynamicSmemBytes = bytes;
+  cfg.stream = static_cast<cudaStream_t>(stream);
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = ranks;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = ranks > 1 ? 2 : 1;
+  return launched(cudaLaunchKernelEx(&cfg, fn, a));
+}
+
+}  // extern "C"
