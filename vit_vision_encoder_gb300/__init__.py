@@ -21,6 +21,7 @@ TOK_START, TOK_IMAGE, TOK_NEWLINE, TOK_END = 0, 1, 2, 3
 CACHE_BF16, CACHE_E4M3 = 0, 1
 ROPE_HALF_VECTOR, ROPE_ADJACENT = 1, 2
 EPI_BIAS, EPI_BIAS_GELU, EPI_BIAS_RESID, EPI_QKV_ROPE, EPI_SWIGLU = 0, 1, 2, 3, 4
+SELECT_MAX_COLS, SELECT_MAX_TOP = 49152, 4096
 MAX_LAYERS, MAX_IMAGES, MAX_PATCHES, MAX_TOKENS = 32, 64, 9216, 1024
 NOALLOC_MAX_PATCHES, NOALLOC_SCRATCH_BYTES = 1024, 21 * 1024 * 1024
 
@@ -168,6 +169,12 @@ SIGNATURES = {
     "ds_vit_pages_compact": (C.c_int, [C.POINTER(PoolArrays), C.POINTER(TableArrays), C.POINTER(CopyArrays), _VP,
                                        _VP]),
     "ds_vit_cache_copy": (C.c_int, [C.POINTER(Cache), C.POINTER(BoundArrays), C.POINTER(CopyArrays), _VP, _VP]),
+    "ds_vit_cache_bounds": (C.c_int, [C.POINTER(Cache), C.POINTER(ChunkArrays), C.POINTER(BoundArrays), _I64, _VP,
+                                      _VP]),
+    "ds_vit_cache_select": (C.c_int, [C.POINTER(Cache), C.POINTER(ChunkArrays), C.POINTER(BoundArrays), _VP, _I64,
+                                      _I64, _I32, _I32, _I32, _I32, _VP, _VP, _VP]),
+    "ds_vit_cache_attention_blocks": (C.c_int, [C.POINTER(Cache), C.POINTER(ChunkArrays), _VP, _I64, _I64, _I32, _F,
+                                                _VP, _I32, _VP, _I64, _VP, _VP]),
 }
 
 
@@ -918,6 +925,72 @@ class KeyBounds:
         """Whether they are bounds of such a cache, on its device."""
         return (self.device_index == cache.device_index
                 and self.shape == (cache.c.n_pages, cache.kv_heads, 2, cache.head_dim))
+
+
+def _block_lists(t, rows, kv_heads, device, where):
+    """The length of lists int32 [rows, kv_heads, top] on CUDA device number ``device``."""
+    if (t.dtype is not _i32_type or t.dim() != 3 or t.shape[0] != rows or t.shape[1] != kv_heads
+            or t.get_device() != device or not t.is_contiguous()):
+        _refuse(where)
+    return t.shape[2]
+
+
+def cache_bounds(cache, chunks, bounds, rows, status=None):
+    """Bounds of the keys of the pages that the call's ``rows`` packed rows completed
+    (ds_vit_cache_bounds; after cache_write).  Returns ``status``."""
+    d, stream, status = _on_device(cache, chunks, status, "ds_vit_cache_bounds")
+    if not bounds.of(cache):
+        _refuse("ds_vit_cache_bounds")
+    check(lib.ds_vit_cache_bounds(cache.ref, chunks.ref, bounds.ref, rows, status.data_ptr(), stream),
+          "ds_vit_cache_bounds")
+    return status
+
+
+def cache_select(cache, chunks, bounds, q, top, first=1, last=1, out=None, status=None):
+    """The blocks (pages of its sequence) that each row of q (bf16 [rows, heads, head_dim],
+    rows may be strided) attends to (ds_vit_cache_select): int32 [rows, kv_heads, top],
+    ascending, -1 at the end; the ``first`` and the ``last`` ones and those of the highest
+    scores.  A new ``out`` holds -1 in rows of no sequence.  Returns (blocks, status)."""
+    where = "ds_vit_cache_select"
+    d, stream, status = _on_device(cache, chunks, status, where)
+    if q.dim() != 3 or not bounds.of(cache) or not all(0 <= x < 1 << 31 for x in (top, first, last)):
+        _refuse(where)
+    rows, heads, _ = q.shape
+    qs = _packed(q, heads, cache.head_dim, d, where)
+    if out is None:
+        out = _torch().full((rows, cache.kv_heads, top), -1, dtype=_i32_type, device=cache.device)
+    elif _block_lists(out, rows, cache.kv_heads, d, where) != top:
+        _refuse(where)
+    if rows == 0:                           # an empty tensor has no address
+        return out, status
+    check(lib.ds_vit_cache_select(cache.ref, chunks.ref, bounds.ref, q.data_ptr(), qs, rows, heads, top, first, last,
+                                  out.data_ptr(), status.data_ptr(), stream), where)
+    return out, status
+
+
+def cache_attention_blocks(cache, chunks, q, blocks, scale=None, out=None, status=None):
+    """Attention of the packed rows q (bf16 [rows, heads, head_dim], rows may be strided)
+    over the blocks that each lists (int32 [rows, kv_heads, top], as cache_select makes
+    them; ds_vit_cache_attention_blocks); scale defaults to head_dim ** -0.5.  A new
+    ``out`` holds anything in rows of no sequence.  Returns (out, status)."""
+    where = "ds_vit_cache_attention_blocks"
+    d, stream, status = _on_device(cache, chunks, status, where)
+    if q.dim() != 3:
+        _refuse(where)
+    rows, heads, dim = q.shape
+    qs = _packed(q, heads, cache.head_dim, d, where)
+    if out is None:
+        out = _torch().empty((rows, heads, dim), dtype=_bf16, device=cache.device)
+    os_ = _packed(out, heads, dim, d, where)
+    top = _block_lists(blocks, rows, cache.kv_heads, d, where)
+    if out.shape[0] != rows:
+        _refuse(where)
+    if rows == 0:
+        return out, status
+    check(lib.ds_vit_cache_attention_blocks(cache.ref, chunks.ref, q.data_ptr(), qs, rows, heads,
+                                            dim ** -0.5 if scale is None else scale, blocks.data_ptr(), top,
+                                            out.data_ptr(), os_, status.data_ptr(), stream), where)
+    return out, status
 
 
 # ---------------------------------------------------------------- norms and rotation in front of the cache

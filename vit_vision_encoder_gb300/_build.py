@@ -13,7 +13,7 @@ LIB = os.path.join(PKG, "libdsvit.so")
 SOURCES = ("api.cu", "gemm.cu", "gemm_pair.cu", "attention.cu", "attention_qwen.cu", "kernels.cu", "noalloc.cu",
            "preprocess.cu", "qwen.cu", "cache.cu", "cache_decode.cu",
            "cache_prefill.cu", "rotary.cu",
-           "pages.cu")
+           "pages.cu", "block_select.cu", "block_attention.cu")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
          "--expt-relaxed-constexpr"]

@@ -305,7 +305,10 @@ __global__ void __launch_bounds__(kThreads) block_attention_kernel(const __grid_
 #pragma unroll
       for (int x = 0; x < 4; ++x) {
         float z = c[n][x];
-        if constexpr (E4M3) z = z * kf[x >> 1] * back[n][x & 1];
+        if constexpr (E4M3) {
+          const float f = kf[x >> 1] * back[n][x & 1];
+          z *= f > 3e38f ? 3e38f : f;            // 0 times it stays 0; NaN stays
+        }
         z *= a.scale_log2;
         if (n_here < 16 && g + 8 * (x >> 1) >= n_here) z = -INFINITY;
         c[n][x] = z;
