@@ -690,16 +690,19 @@ int ds_vit_cache_copy(const ds_vit_cache* cache, const ds_vit_key_bounds* bounds
  * before, by ds_vit_cache_write): those whose last token is among them.  Others
  * stay as they were.
  *
+ * Lists are device int32, `top` entries for each row and K/V head: entry i of row r
+ * and head h at blocks[r * row_stride + h * head_stride + i].
+ *
  * ds_vit_cache_select: for each row and K/V head the list of blocks to attend to,
- * blocks (device int32 [rows, kv_heads, top]), ascending and filled up with -1.  The row
- * at position p has the blocks 0 .. b, b = p / page: of these the first `first` and the
+ * ascending and filled up with -1.  The row at position p has the blocks 0 .. b, b = p / page: of these the first `first` and the
  * last `last` (b among them), then those of the highest scores, the lower of equals
  * first, `top` in all.  Blocks whose table entry is below 0 (given away) are not
  * taken.  Rows in front of position 0 get -1 throughout, packed rows of no sequence
  * stay as they were.  Bounds are read of every block of the sequences but the
  * rows' own.
  * DS_VIT_EINVAL for first < 0, last < 1, top outside first + last ..
- * DS_VIT_SELECT_MAX_TOP, bounds or blocks null or misaligned (hi_lo and blocks 16 bytes);
+ * DS_VIT_SELECT_MAX_TOP, bounds or blocks null or misaligned (hi_lo 16 bytes, blocks 4), a
+ * stride of the lists below top (not looked at for one row or one head);
  * DS_VIT_ERANGE for table_cols past DS_VIT_SELECT_MAX_COLS, rows * kv_heads of 2^31 or
  * more.  Otherwise as ds_vit_cache_attention.
  *
@@ -717,11 +720,12 @@ int ds_vit_cache_bounds(const ds_vit_cache* cache, const ds_vit_chunks* chunks, 
                         int64_t rows, int32_t* status, void* stream);
 int ds_vit_cache_select(const ds_vit_cache* cache, const ds_vit_chunks* chunks, const ds_vit_key_bounds* bounds,
                         const void* q, int64_t q_stride, int64_t rows, int32_t heads, int32_t top, int32_t first,
-                        int32_t last, int32_t* blocks, int32_t* status, void* stream);
+                        int32_t last, int32_t* blocks, int64_t row_stride, int64_t head_stride, int32_t* status,
+                        void* stream);
 int ds_vit_cache_attention_blocks(const ds_vit_cache* cache, const ds_vit_chunks* chunks, const void* q,
                                   int64_t q_stride, int64_t rows, int32_t heads, float scale,
-                                  const int32_t* blocks, int32_t top, void* out, int64_t out_stride,
-                                  int32_t* status, void* stream);
+                                  const int32_t* blocks, int64_t row_stride, int64_t head_stride, int32_t top,
+                                  void* out, int64_t out_stride, int32_t* status, void* stream);
 
 /* Kernel kinds reported by ds_vit_set_kernel_timer. */
 /* PATCH_GEMM patchifies and normalises the pixels inside its A-tile load;

@@ -26,15 +26,16 @@ def _bounds(dv, cache, chunks, b=GOOD, rows=0, status=P):
     return dv.lib.ds_vit_cache_bounds(cache, chunks, _ref(dv.BoundArrays(P, P) if b is GOOD else b), rows, status, None)
 
 
-def _select(dv, cache, chunks, b=GOOD, q=P, qs=1024, rows=0, heads=8, top=5, first=1, last=2, blocks=P, status=P):
-    return dv.lib.ds_vit_cache_select(cache, chunks, _ref(dv.BoundArrays(P, P) if b is GOOD else b), q, qs, rows, heads,
-                                      top, first, last, blocks, status, None)
-
-
-def _attend(dv, cache, chunks, q=P, qs=1024, rows=0, heads=8, scale=0.1, blocks=P, top=5, out=2 * P, os_=1024,
+def _select(dv, cache, chunks, b=GOOD, q=P, qs=1024, rows=0, heads=8, top=5, first=1, last=2, blocks=P, rs=40, hs=5,
             status=P):
-    return dv.lib.ds_vit_cache_attention_blocks(cache, chunks, q, qs, rows, heads, scale, blocks, top, out, os_, status,
-                                                None)
+    return dv.lib.ds_vit_cache_select(cache, chunks, _ref(dv.BoundArrays(P, P) if b is GOOD else b), q, qs, rows, heads,
+                                      top, first, last, blocks, rs, max(hs, top if hs == 5 else 0), status, None)
+
+
+def _attend(dv, cache, chunks, q=P, qs=1024, rows=0, heads=8, scale=0.1, blocks=P, rs=40, hs=5, top=5, out=2 * P,
+            os_=1024, status=P):
+    return dv.lib.ds_vit_cache_attention_blocks(cache, chunks, q, qs, rows, heads, scale, blocks, rs, hs, top, out, os_,
+                                                status, None)
 
 
 @pytest.mark.parametrize("call", [_bounds, _select, _attend])
@@ -64,7 +65,8 @@ def test_select_refused(dv):
     ca, ch = C.byref(_cache(dv)), C.byref(_chunks(dv))
     for kw in (dict(q=None), dict(q=P + 8), dict(qs=1016), dict(qs=1028), dict(heads=0), dict(heads=6),
                dict(heads=4 * 129), dict(top=2), dict(top=0), dict(top=4097), dict(first=-1), dict(last=0),
-               dict(last=-3), dict(first=2 ** 31 - 1, last=2 ** 31 - 1), dict(blocks=None), dict(blocks=P + 4)):
+               dict(last=-3), dict(first=2 ** 31 - 1, last=2 ** 31 - 1), dict(blocks=None), dict(blocks=P + 2), dict(hs=4),
+               dict(rows=2, rs=3)):
         assert _select(dv, ca, ch, **kw) == dv.EINVAL, kw
     assert _select(dv, ca, ch, top=3) == dv.OK and _select(dv, ca, ch, top=4096) == dv.OK
     wide = C.byref(_chunks(dv, table_cols=dv.SELECT_MAX_COLS))
@@ -77,7 +79,8 @@ def test_attention_refused(dv):
     ca, ch = C.byref(_cache(dv)), C.byref(_chunks(dv))
     for kw in (dict(q=None), dict(out=None), dict(q=P + 8), dict(out=P + 8), dict(qs=1016), dict(os_=1020),
                dict(heads=0), dict(heads=6), dict(heads=4 * 129), dict(scale=0.0), dict(scale=-1.0),
-               dict(scale=float("nan")), dict(scale=float("inf")), dict(blocks=None), dict(blocks=P + 4), dict(top=0),
+               dict(scale=float("nan")), dict(scale=float("inf")), dict(blocks=None), dict(blocks=P + 2), dict(hs=4),
+               dict(rows=2, rs=3), dict(top=0),
                dict(top=-1), dict(top=4097)):
         assert _attend(dv, ca, ch, **kw) == dv.EINVAL, kw
     assert _attend(dv, ca, ch, rows=2 ** 28) == dv.ERANGE                       # 8 heads

@@ -586,6 +586,23 @@ def test_captured_step(dv):
         assert torch.equal(got[0], blocks) and torch.equal(got[1], out) and int(status.item()) == dv.OK
 
 
+def test_lists_laid_out_otherwise(dv):
+    """Heads in front of rows, and room between the lists."""
+    st = make(dv, [1, 130], [500, 300], 4, 64, 16, "bf16")
+    q = st.queries(20)
+    blocks, _ = dv.cache_select(st.cache, st.chunks, st.bounds, q, 9, 1, 2)
+    out, _ = dv.cache_attention_blocks(st.cache, st.chunks, q, blocks)
+    wide = torch.full((4, st.rows, 13), 99, dtype=torch.int32, device="cuda")
+    lists = wide.transpose(0, 1)[..., 2:11]
+    got, _ = dv.cache_select(st.cache, st.chunks, st.bounds, q, 9, 1, 2, out=lists)
+    again, status = dv.cache_attention_blocks(st.cache, st.chunks, q, lists)
+    torch.cuda.synchronize()
+    assert int(status.item()) == dv.OK and torch.equal(lists, blocks) and torch.equal(again, out)
+    assert (wide[..., :2] == 99).all() and (wide[..., 11:] == 99).all()
+    with pytest.raises(dv.DsVitError):
+        dv.cache_attention_blocks(st.cache, st.chunks, q, blocks.transpose(1, 2).contiguous().transpose(1, 2))
+
+
 def test_no_rows(dv):
     st = make(dv, [1], [20], 2, 64, 16, "bf16")
     q = torch.zeros((0, 4, 64), dtype=torch.bfloat16, device="cuda")

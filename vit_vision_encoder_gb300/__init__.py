@@ -172,9 +172,9 @@ SIGNATURES = {
     "ds_vit_cache_bounds": (C.c_int, [C.POINTER(Cache), C.POINTER(ChunkArrays), C.POINTER(BoundArrays), _I64, _VP,
                                       _VP]),
     "ds_vit_cache_select": (C.c_int, [C.POINTER(Cache), C.POINTER(ChunkArrays), C.POINTER(BoundArrays), _VP, _I64,
-                                      _I64, _I32, _I32, _I32, _I32, _VP, _VP, _VP]),
+                                      _I64, _I32, _I32, _I32, _I32, _VP, _I64, _I64, _VP, _VP]),
     "ds_vit_cache_attention_blocks": (C.c_int, [C.POINTER(Cache), C.POINTER(ChunkArrays), _VP, _I64, _I64, _I32, _F,
-                                                _VP, _I32, _VP, _I64, _VP, _VP]),
+                                                _VP, _I64, _I64, _I32, _VP, _I64, _VP, _VP]),
 }
 
 
@@ -928,11 +928,13 @@ class KeyBounds:
 
 
 def _block_lists(t, rows, kv_heads, device, where):
-    """The length of lists int32 [rows, kv_heads, top] on CUDA device number ``device``."""
-    if (t.dtype is not _i32_type or t.dim() != 3 or t.shape[0] != rows or t.shape[1] != kv_heads
-            or t.get_device() != device or not t.is_contiguous()):
+    """Length, row and head stride of lists int32 [rows, kv_heads, top] on CUDA device number
+    ``device``; a list's entries must lie side by side."""
+    shape, stride = t.shape, t.stride()
+    if (t.dtype is not _i32_type or len(shape) != 3 or shape[0] != rows or shape[1] != kv_heads
+            or t.get_device() != device or (shape[2] > 1 and stride[2] != 1)):
         _refuse(where)
-    return t.shape[2]
+    return shape[2], stride[0], stride[1]
 
 
 def cache_bounds(cache, chunks, bounds, rows, status=None):
@@ -959,12 +961,13 @@ def cache_select(cache, chunks, bounds, q, top, first=1, last=1, out=None, statu
     qs = _packed(q, heads, cache.head_dim, d, where)
     if out is None:
         out = _torch().full((rows, cache.kv_heads, top), -1, dtype=_i32_type, device=cache.device)
-    elif _block_lists(out, rows, cache.kv_heads, d, where) != top:
+    length, rs, hs = _block_lists(out, rows, cache.kv_heads, d, where)
+    if length != top:
         _refuse(where)
     if rows == 0:                           # an empty tensor has no address
         return out, status
     check(lib.ds_vit_cache_select(cache.ref, chunks.ref, bounds.ref, q.data_ptr(), qs, rows, heads, top, first, last,
-                                  out.data_ptr(), status.data_ptr(), stream), where)
+                                  out.data_ptr(), rs, hs, status.data_ptr(), stream), where)
     return out, status
 
 
@@ -982,14 +985,14 @@ def cache_attention_blocks(cache, chunks, q, blocks, scale=None, out=None, statu
     if out is None:
         out = _torch().empty((rows, heads, dim), dtype=_bf16, device=cache.device)
     os_ = _packed(out, heads, dim, d, where)
-    top = _block_lists(blocks, rows, cache.kv_heads, d, where)
+    top, rs, hs = _block_lists(blocks, rows, cache.kv_heads, d, where)
     if out.shape[0] != rows:
         _refuse(where)
     if rows == 0:
         return out, status
     check(lib.ds_vit_cache_attention_blocks(cache.ref, chunks.ref, q.data_ptr(), qs, rows, heads,
-                                            dim ** -0.5 if scale is None else scale, blocks.data_ptr(), top,
-                                            out.data_ptr(), os_, status.data_ptr(), stream), where)
+                                            dim ** -0.5 if scale is None else scale, blocks.data_ptr(), rs, hs,
+                                            top, out.data_ptr(), os_, status.data_ptr(), stream), where)
     return out, status
 
 

@@ -44,6 +44,7 @@ struct BlockArgs {
   int group, head_tiles;     // query heads per K/V head; items that share them
   float scale_log2;
   const int32_t* blocks;
+  int64_t row_stride, head_stride;
   int top;
   int* status;
   int64_t items;
@@ -184,12 +185,12 @@ __global__ void __launch_bounds__(kThreads) block_attention_kernel(const __grid_
 
   // The list, 32 entries at a time: a lane has one entry's block and page.
   const int tile_shift = a.c.page_shift - 4;
-  const int64_t list = (row * a.c.kv_heads + kv_head) * a.top;
+  const int32_t* const list = a.blocks + row * a.row_stride + kv_head * a.head_stride;
   int base = 0, block = -1, at = -1;
   auto window = [&](int e0) {
     base = e0;
     const int e = e0 + lane;
-    block = e < a.top ? __ldg(a.blocks + list + e) : -1;
+    block = e < a.top ? __ldg(list + e) : -1;
     if (static_cast<unsigned>(block) > static_cast<unsigned>(p >> a.c.page_shift)) block = -1;
     at = -1;
     if (block >= 0) {
@@ -539,12 +540,14 @@ using namespace dsvit;
 
 extern "C" int ds_vit_cache_attention_blocks(const ds_vit_cache* cache, const ds_vit_chunks* chunks, const void* q,
                                              int64_t q_stride, int64_t rows, int32_t heads, float scale,
-                                             const int32_t* blocks, int32_t top, void* out, int64_t out_stride,
-                                             int32_t* status, void* stream) {
+                                             const int32_t* blocks, int64_t row_stride, int64_t head_stride,
+                                             int32_t top, void* out, int64_t out_stride, int32_t* status,
+                                             void* stream) {
   BlockArgs a{};
   if (const int rc = check_cache(cache, chunks, rows, &a.c, &a.b)) return rc;
   if (heads < 1 || heads % a.c.kv_heads != 0 || heads / a.c.kv_heads > DS_VIT_CACHE_MAX_GROUP || !(scale > 0.f) ||
-      !(scale <= 1e30f) || top < 1 || top > DS_VIT_SELECT_MAX_TOP || !blocks || !aligned(blocks, 16))
+      !(scale <= 1e30f) || top < 1 || top > DS_VIT_SELECT_MAX_TOP ||
+      bad_lists(blocks, row_stride, head_stride, rows, a.c.kv_heads, top))
     return DS_VIT_EINVAL;
   const int64_t width = static_cast<int64_t>(heads) * cache->head_dim;
   if (!status || !aligned(status, 4) || bad_rows(q, q_stride, width) || bad_rows(out, out_stride, width))
@@ -558,6 +561,8 @@ extern "C" int ds_vit_cache_attention_blocks(const ds_vit_cache* cache, const ds
   a.group = heads / a.c.kv_heads;
   a.scale_log2 = 1.4426950408889634f * scale;
   a.blocks = blocks;
+  a.row_stride = row_stride;
+  a.head_stride = head_stride;
   a.top = top;
   a.status = reinterpret_cast<int*>(status);
   const bool e4m3 = cache->kind == DS_VIT_CACHE_E4M3;

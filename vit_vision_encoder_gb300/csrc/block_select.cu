@@ -154,6 +154,7 @@ struct SelectArgs {
   int group, log2_group;     // G of the header: 2^log2_group >= group
   int top, first, last;
   int32_t* blocks;
+  int64_t row_stride, head_stride;
   int* status;
   int tile_rows;             // rows of a CTA
   int places;                // scores of a row in shared memory
@@ -408,11 +409,12 @@ __global__ void __launch_bounds__(kSelectThreads) cache_select_kernel(const __gr
       __syncthreads();
     }
     if constexpr (kSingle) {
-      pick<kSelectThreads>(keys, blocks, a.top, a.blocks + (ra * a.kv_heads + head) * a.top, sums);
+      pick<kSelectThreads>(keys, blocks, a.top, a.blocks + ra * a.row_stride + head * a.head_stride, sums);
       return;
     } else {
       if (warp < n_rows)
-        pick<32>(keys + warp * a.places, blocks, a.top, a.blocks + ((ra + warp) * a.kv_heads + head) * a.top, sums);
+        pick<32>(keys + warp * a.places, blocks, a.top, a.blocks + (ra + warp) * a.row_stride + head * a.head_stride,
+                 sums);
       __syncthreads();
     }
     ra += n_rows;
@@ -451,14 +453,16 @@ int ds_vit_cache_bounds(const ds_vit_cache* cache, const ds_vit_chunks* chunks, 
 
 int ds_vit_cache_select(const ds_vit_cache* cache, const ds_vit_chunks* chunks, const ds_vit_key_bounds* bounds,
                         const void* q, int64_t q_stride, int64_t rows, int32_t heads, int32_t top, int32_t first,
-                        int32_t last, int32_t* blocks, int32_t* status, void* stream) {
+                        int32_t last, int32_t* blocks, int64_t row_stride, int64_t head_stride, int32_t* status,
+                        void* stream) {
   CacheView c;
   SelectArgs a{};
   if (const int rc = check_cache(cache, chunks, rows, &c, &a.b)) return rc;
   if (bad_bounds(bounds) || !status || !aligned(status, 4) || heads < 1 || heads % c.kv_heads != 0 ||
       heads / c.kv_heads > DS_VIT_CACHE_MAX_GROUP ||
       bad_rows(q, q_stride, static_cast<int64_t>(heads) * cache->head_dim) || first < 0 || last < 1 ||
-      top > DS_VIT_SELECT_MAX_TOP || static_cast<int64_t>(first) + last > top || !blocks || !aligned(blocks, 16))
+      top > DS_VIT_SELECT_MAX_TOP || static_cast<int64_t>(first) + last > top ||
+      bad_lists(blocks, row_stride, head_stride, rows, c.kv_heads, top))
     return DS_VIT_EINVAL;
   if (chunks->table_cols > DS_VIT_SELECT_MAX_COLS || rows > INT32_MAX / c.kv_heads) return DS_VIT_ERANGE;
   if (rows == 0) return DS_VIT_OK;
@@ -475,6 +479,8 @@ int ds_vit_cache_select(const ds_vit_cache* cache, const ds_vit_chunks* chunks, 
   a.first = first;
   a.last = last;
   a.blocks = blocks;
+  a.row_stride = row_stride;
+  a.head_stride = head_stride;
   a.status = reinterpret_cast<int*>(status);
   a.places = (chunks->table_cols + 31) / 32 * 32 + 4;
   // Rows of one sequence share the loads of its bounds where there are more than enough CTAs.

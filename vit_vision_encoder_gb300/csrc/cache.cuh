@@ -40,6 +40,11 @@ inline bool bad_rows(const void* p, int64_t stride, int64_t width) {
   return !p || !aligned(p, 16) || stride < width || stride % 8 != 0;
 }
 
+// Lists of blocks, `top` entries for each row and K/V head.
+inline bool bad_lists(const int32_t* p, int64_t row_stride, int64_t head_stride, int64_t rows, int kv_heads, int top) {
+  return !p || !aligned(p, 4) || (rows > 1 && row_stride < top) || (kv_heads > 1 && head_stride < top);
+}
+
 inline int launched(cudaError_t e) {
   if (e != cudaSuccess) cudaGetLastError();
   return e == cudaSuccess ? DS_VIT_OK : DS_VIT_ECUDA;
