@@ -72,8 +72,21 @@ __device__ __forceinline__ float4 ld_cluster4(uint32_t addr) {
   return x;
 }
 
-// What 2^(x - ref) stands for where nothing has been seen yet.
-__device__ __forceinline__ float at_least(float ref) { return ref == -INFINITY ? 0.f : ref; }
+// A reference before anything has been seen: every finite score is at or above it.
+constexpr float kNone = -3.402823466e38f;
+
+__device__ __forceinline__ float min_nan(float a, float b) {
+  float r;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+// The two e4m3 values in the upper half of a register as fp16.
+__device__ __forceinline__ uint32_t e4m3x2_hi_to_f16x2(uint32_t four) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, h;\n\t}" : "=r"(r) : "r"(four));
+  return r;
+}
 
 template <int D, bool E4M3, int NT>
 struct Frag {
@@ -94,7 +107,7 @@ struct Record {
 };
 
 template <int D, bool E4M3, int NT>
-__global__ void __launch_bounds__(kThreads) block_attention_kernel(const __grid_constant__ BlockArgs a) {
+__global__ void __launch_bounds__(kThreads, NT == 2 ? 2 : D == 128 && !E4M3 ? 3 : 4) block_attention_kernel(const __grid_constant__ BlockArgs a) {
   using F = Frag<D, E4M3, NT>;
   using R = Record<D, NT>;
   constexpr int kK = F::kK, kV = F::kV, kM = F::kM;
@@ -128,7 +141,7 @@ __global__ void __launch_bounds__(kThreads) block_attention_kernel(const __grid_
 
   // Queries, B fragments of S^T: lane (g, t) has of head g what it has of a key.
   uint32_t qf[NT][kK][E4M3 ? 8 : 4];
-  float back[NT][2];                       // e4m3: 1 / the scale of heads 2t, 2t + 1
+  float unit[NT][2];                       // what an accumulated score of heads 2t, 2t + 1 counts (log2)
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
     const bool on = mine && 8 * n + g < heads;
@@ -166,8 +179,8 @@ __global__ void __launch_bounds__(kThreads) block_attention_kernel(const __grid_
 #pragma unroll
           for (int x = 0; x < 4; ++x) qf[n][j][4 * y + x] = pack_f16x2(bf16lo(w[x]) * f, bf16hi(w[x]) * f);
         }
-      back[n][0] = __shfl_sync(0xFFFFFFFFu, undo, 8 * t);
-      back[n][1] = __shfl_sync(0xFFFFFFFFu, undo, 8 * t + 4);
+      unit[n][0] = fminf(__shfl_sync(0xFFFFFFFFu, undo, 8 * t) * a.scale_log2, 3e38f);
+      unit[n][1] = fminf(__shfl_sync(0xFFFFFFFFu, undo, 8 * t + 4) * a.scale_log2, 3e38f);
     }
   }
 
@@ -175,7 +188,7 @@ __global__ void __launch_bounds__(kThreads) block_attention_kernel(const __grid_
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
 #pragma unroll
-    for (int x = 0; x < 2; ++x) m[n][x] = r[n][x] = -INFINITY, l[n][x] = 0.f;
+    for (int x = 0; x < 2; ++x) m[n][x] = r[n][x] = kNone, l[n][x] = 0.f;
 #pragma unroll
     for (int y = 0; y < kM; ++y)
 #pragma unroll
@@ -226,33 +239,48 @@ __global__ void __launch_bounds__(kThreads) block_attention_kernel(const __grid_
   uint4 k[2][kK];
   uint4 v[4][kV];                             // e4m3 at D 64: 8 bytes of each
   uint32_t kb[2], vb[2];                      // exponents of keys g, g + 8
+  // Whole tiles, all but the last of a row's own block, are loaded without conditions.
+  const uint8_t* const k_lane = a.c.k + g * kRow + 16 * t;
+  const uint8_t* const v_lane = a.c.v + 2 * t * kRow + (E4M3 && D == 64 ? 8 : 16) * g;
   auto load_k = [&](int64_t r0, int n) {
+    auto load = [&](auto on) {
+      const uint8_t* const from = k_lane + r0 * kRow;
 #pragma unroll
-    for (int y = 0; y < 2; ++y) {
-      const bool on = g + 8 * y < n;
-      const uint4* from = reinterpret_cast<const uint4*>(a.c.k + (r0 + g + 8 * y) * kRow) + t;
+      for (int y = 0; y < 2; ++y) {
 #pragma unroll
-      for (int j = 0; j < kK; ++j) k[y][j] = on ? __ldg(from + 4 * j) : make_uint4(0, 0, 0, 0);
-      if constexpr (E4M3) {
-        kb[y] = on ? __ldg(a.c.k_exp + r0 + g + 8 * y) : 127u;
-        vb[y] = on ? __ldg(a.c.v_exp + r0 + g + 8 * y) : 127u;
+        for (int j = 0; j < kK; ++j)
+          k[y][j] = on(g + 8 * y) ? __ldg(reinterpret_cast<const uint4*>(from + 8 * y * kRow) + 4 * j) : make_uint4(0, 0, 0, 0);
+        if constexpr (E4M3) {
+          kb[y] = on(g + 8 * y) ? __ldg(a.c.k_exp + r0 + g + 8 * y) : 127u;
+          vb[y] = on(g + 8 * y) ? __ldg(a.c.v_exp + r0 + g + 8 * y) : 127u;
+        }
       }
-    }
+    };
+    if (n == 16)
+      load([](int) { return true; });
+    else
+      load([n](int key) { return key < n; });
   };
   auto load_v = [&](int64_t r0, int n) {
+    auto load = [&](auto on) {
+      const uint8_t* const from = v_lane + r0 * kRow;
 #pragma unroll
-    for (int y = 0; y < 4; ++y) {
-      const int key = 2 * t + (y & 1) + 8 * (y >> 1);
-      const bool on = key < n;
-      const uint8_t* from = a.c.v + (r0 + key) * kRow;
-      if constexpr (E4M3 && D == 64) {
-        const uint2 u = on ? __ldg(reinterpret_cast<const uint2*>(from) + g) : make_uint2(0, 0);
-        v[y][0] = make_uint4(u.x, u.y, 0, 0);
-      } else {
+      for (int y = 0; y < 4; ++y) {
+        const int key = (y & 1) + 8 * (y >> 1);
+        if constexpr (E4M3 && D == 64) {
+          const uint2 u = on(2 * t + key) ? __ldg(reinterpret_cast<const uint2*>(from + key * kRow)) : make_uint2(0, 0);
+          v[y][0] = make_uint4(u.x, u.y, 0, 0);
+        } else {
 #pragma unroll
-        for (int z = 0; z < kV; ++z) v[y][z] = on ? __ldg(reinterpret_cast<const uint4*>(from) + g + 8 * z) : make_uint4(0, 0, 0, 0);
+          for (int z = 0; z < kV; ++z)
+            v[y][z] = on(2 * t + key) ? __ldg(reinterpret_cast<const uint4*>(from + key * kRow) + 8 * z) : make_uint4(0, 0, 0, 0);
+        }
       }
-    }
+    };
+    if (n == 16)
+      load([](int) { return true; });
+    else
+      load([n](int key) { return key < n; });
   };
   auto word = [](const uint4& u, int i) { return i == 0 ? u.x : i == 1 ? u.y : i == 2 ? u.z : u.w; };
 
@@ -274,7 +302,7 @@ __global__ void __launch_bounds__(kThreads) block_attention_kernel(const __grid_
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
           const uint32_t k0 = word(k[0][j], x), k1 = word(k[1][j], x);
-          const uint32_t af[4] = {e4m3x2_to_f16x2(k0), e4m3x2_to_f16x2(k1), e4m3x2_to_f16x2(k0 >> 16), e4m3x2_to_f16x2(k1 >> 16)};
+          const uint32_t af[4] = {e4m3x2_to_f16x2(k0), e4m3x2_to_f16x2(k1), e4m3x2_hi_to_f16x2(k0), e4m3x2_hi_to_f16x2(k1)};
 #pragma unroll
           for (int n = 0; n < NT; ++n) mma_f16(c[n], af, qf[n][j][2 * x], qf[n][j][2 * x + 1]);
         }
@@ -305,12 +333,8 @@ __global__ void __launch_bounds__(kThreads) block_attention_kernel(const __grid_
     for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int x = 0; x < 4; ++x) {
-        float z = c[n][x];
-        if constexpr (E4M3) {
-          const float f = kf[x >> 1] * back[n][x & 1];
-          z *= f > 3e38f ? 3e38f : f;            // 0 times it stays 0; NaN stays
-        }
-        z *= a.scale_log2;
+        // (0 times a factor past all floats stays 0, NaN stays.)
+        float z = c[n][x] * (E4M3 ? min_nan(kf[x >> 1] * unit[n][x & 1], 3e38f) : a.scale_log2);
         if (n_here < 16 && g + 8 * (x >> 1) >= n_here) z = -INFINITY;
         c[n][x] = z;
         raise |= z > m[n][x & 1] + (E4M3 ? kLag8 : kLag16);
@@ -327,12 +351,12 @@ __global__ void __launch_bounds__(kThreads) block_attention_kernel(const __grid_
             top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
             if constexpr (E4M3) most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, o));
           }
-          const float to = fmaxf(m[n][x], top), lf = ex2_approx(m[n][x] - at_least(to));
+          const float to = fmaxf(m[n][x], top), lf = ex2_approx(m[n][x] - to);
           float of = lf;
           if constexpr (E4M3) {
             // Contributions may lie up to kLag8 over their reference: it moves when one is further up.
             const float ref = most > r[n][x] + kLag8 ? most - kLead8 : r[n][x];
-            of = ex2_approx(r[n][x] - at_least(ref));
+            of = ex2_approx(r[n][x] - ref);
             r[n][x] = ref;
           }
           m[n][x] = to;
@@ -350,9 +374,9 @@ __global__ void __launch_bounds__(kThreads) block_attention_kernel(const __grid_
       float w[4];
 #pragma unroll
       for (int x = 0; x < 4; ++x) {
-        const float y = ex2_approx(c[n][x] - at_least(m[n][x & 1]));
+        const float y = ex2_approx(c[n][x] - m[n][x & 1]);
         l[n][x & 1] += y;
-        w[x] = E4M3 ? ex2_approx(c[n][x] + ve[x >> 1] - at_least(r[n][x & 1])) : y;
+        w[x] = E4M3 ? ex2_approx(c[n][x] + ve[x >> 1] - r[n][x & 1]) : y;
       }
       pf[n][0] = transposed(E4M3 ? pack_f16x2(w[0], w[1]) : pack_bf16x2(w[0], w[1]));
       pf[n][1] = transposed(E4M3 ? pack_f16x2(w[2], w[3]) : pack_bf16x2(w[2], w[3]));
@@ -364,8 +388,8 @@ __global__ void __launch_bounds__(kThreads) block_attention_kernel(const __grid_
         const uint32_t sel = y & 1 ? 0x7362u : 0x5140u;
         const uint32_t u0 = __byte_perm(word(v[0][0], y >> 1), word(v[1][0], y >> 1), sel);
         const uint32_t u1 = __byte_perm(word(v[2][0], y >> 1), word(v[3][0], y >> 1), sel);
-        af[0] = e4m3x2_to_f16x2(u0), af[1] = e4m3x2_to_f16x2(u0 >> 16);
-        af[2] = e4m3x2_to_f16x2(u1), af[3] = e4m3x2_to_f16x2(u1 >> 16);
+        af[0] = e4m3x2_to_f16x2(u0), af[1] = e4m3x2_hi_to_f16x2(u0);
+        af[2] = e4m3x2_to_f16x2(u1), af[3] = e4m3x2_hi_to_f16x2(u1);
       } else if constexpr (kV == 2) {
         const uint32_t sel = y & 1 ? 0x7632u : 0x5410u;
         af[0] = __byte_perm(word(v[0][0], y >> 1), word(v[1][0], y >> 1), sel);
@@ -463,7 +487,7 @@ __global__ void __launch_bounds__(kThreads) block_attention_kernel(const __grid_
     constexpr uint32_t kBytes = R::kFloats * 4;
     for (int w = 32 * me + lane; w < heads * (D / 4); w += 32 * sharers) {
       const int h = w / (D / 4), d = 4 * (w - h * (D / 4));
-      float mm = -INFINITY, rr = -INFINITY;
+      float mm = kNone, rr = kNone;
       bool any = false;
       auto part = [&](int y) {
         return mapa_shared(first + (y & ((1 << a.warp_shift) - 1)) * kBytes, y >> a.warp_shift);
@@ -480,10 +504,10 @@ __global__ void __launch_bounds__(kThreads) block_attention_kernel(const __grid_
 #pragma unroll 4
       for (int y = 0; y < sharers; ++y) {
         const uint32_t at_y = part(y);
-        const float lf = ex2_approx(ld_cluster(at_y + 4 * (R::kM + h)) - at_least(mm));
-        const float of = ex2_approx(ld_cluster(at_y + 4 * (R::kR + h)) - at_least(rr));
+        const float lf = ex2_approx(ld_cluster(at_y + 4 * (R::kM + h)) - mm);
+        const float of = ex2_approx(ld_cluster(at_y + 4 * (R::kR + h)) - rr);
         const float4 oy = ld_cluster4(at_y + 4 * (h * R::kPitch + d));
-        // A part that saw nothing has references of -inf: factor 0, and zeros.
+        // A part that saw nothing has the lowest references, and zeros.
         ll = fmaf(ld_cluster(at_y + 4 * (R::kL + h)), lf, ll);
         o.x = fmaf(oy.x, of, o.x), o.y = fmaf(oy.y, of, o.y), o.z = fmaf(oy.z, of, o.z), o.w = fmaf(oy.w, of, o.w);
       }
