@@ -107,10 +107,10 @@ struct Record {
 };
 
 template <int D, bool E4M3, int NT>
-__global__ void __launch_bounds__(kThreads, NT == 2 ? 2 : D == 128 && !E4M3 ? 3 : 4) block_attention_kernel(const __grid_constant__ BlockArgs a) {
+__global__ void __launch_bounds__(kThreads, NT == 2 ? 2 : D == 128 ? 3 : 4) block_attention_kernel(const __grid_constant__ BlockArgs a) {
   using F = Frag<D, E4M3, NT>;
   using R = Record<D, NT>;
-  constexpr int kK = F::kK, kV = F::kV, kM = F::kM;
+  constexpr int kK = F::kK, kV = F::kV, kM = F::kM, kChains = 2;
   __shared__ __align__(16) float records[kWarps][R::kFloats];
   grid_dep_launch();
   grid_dep_wait();
@@ -293,9 +293,12 @@ __global__ void __launch_bounds__(kThreads, NT == 2 ? 2 : D == 128 && !E4M3 ? 3 
   while (n_keys > 0) {
     seen = true;
     const int n_here = n_keys;
-    float c[NT][4];
+    // Products that follow one another into the same sum wait for each other: kChains sums.
+    float part[kChains][NT][4];
 #pragma unroll
-    for (int n = 0; n < NT; ++n) c[n][0] = c[n][1] = c[n][2] = c[n][3] = 0.f;
+    for (int i = 0; i < kChains; ++i)
+#pragma unroll
+      for (int n = 0; n < NT; ++n) part[i][n][0] = part[i][n][1] = part[i][n][2] = part[i][n][3] = 0.f;
 #pragma unroll
     for (int j = 0; j < kK; ++j) {
       if constexpr (E4M3) {
@@ -304,18 +307,27 @@ __global__ void __launch_bounds__(kThreads, NT == 2 ? 2 : D == 128 && !E4M3 ? 3 
           const uint32_t k0 = word(k[0][j], x), k1 = word(k[1][j], x);
           const uint32_t af[4] = {e4m3x2_to_f16x2(k0), e4m3x2_to_f16x2(k1), e4m3x2_hi_to_f16x2(k0), e4m3x2_hi_to_f16x2(k1)};
 #pragma unroll
-          for (int n = 0; n < NT; ++n) mma_f16(c[n], af, qf[n][j][2 * x], qf[n][j][2 * x + 1]);
+          for (int n = 0; n < NT; ++n) mma_f16(part[x % kChains][n], af, qf[n][j][2 * x], qf[n][j][2 * x + 1]);
         }
       } else {
         const uint32_t a0[4] = {k[0][j].x, k[1][j].x, k[0][j].y, k[1][j].y};
         const uint32_t a1[4] = {k[0][j].z, k[1][j].z, k[0][j].w, k[1][j].w};
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-          mma_bf16(c[n], a0, qf[n][j][0], qf[n][j][1]);
-          mma_bf16(c[n], a1, qf[n][j][2], qf[n][j][3]);
+          mma_bf16(part[2 * j % kChains][n], a0, qf[n][j][0], qf[n][j][1]);
+          mma_bf16(part[(2 * j + 1) % kChains][n], a1, qf[n][j][2], qf[n][j][3]);
         }
       }
     }
+    float c[NT][4];
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        c[n][x] = part[0][n][x];
+#pragma unroll
+        for (int i = 1; i < kChains; ++i) c[n][x] += part[i][n][x];
+      }
     float kf[2] = {1.f, 1.f}, ve[2] = {0.f, 0.f};
     if constexpr (E4M3) {
 #pragma unroll
