@@ -45,8 +45,9 @@ struct Shared {
   int chunk[DS_VIT_MAX_SEQS + 1];                  // chunks of table entries before each
   int fresh[DS_VIT_MAX_SEQS + 1];                  // fresh pages taken before each
   int copies[DS_VIT_MAX_SEQS + 1];                 // of them, copies
-  int64_t sums[kWarps];
-  int64_t all[3][kCtas];                           // what the CTAs tell one another
+  int64_t sums[2][kWarps];                         // of warps: one scan's, and the next one's
+  int counts[3][kWarps];                           // of warps, in the first, second and third count
+  int all[3][kCtas];                               // what the CTAs tell one another
 };
 static_assert(sizeof(Shared) <= 48 * 1024, "static shared memory");
 
@@ -58,41 +59,39 @@ __device__ __forceinline__ bool length_there(const PageArgs& a, int len) {
 }
 __device__ __forceinline__ bool slot_there(const PageArgs& a, int s) { return s >= 0 && s < a.slots; }
 
-// Sum of v over the threads before this one, and over all; by all threads of the CTA.
-__device__ __forceinline__ int64_t scan(Shared& sh, int64_t v, int64_t* total) {
+// Sum of v over the threads before this one, and over all; by all threads of the CTA, which
+// take turns 0, 1, 0, ... from scan to scan (the other turn's sums may still be read).
+template <typename T>
+__device__ __forceinline__ T scan(Shared& sh, int turn, T v, T* total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int64_t x = v;
+  T x = v;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int64_t y = __shfl_up_sync(0xFFFFFFFFu, x, o);
+    const T y = __shfl_up_sync(0xFFFFFFFFu, x, o);
     if (lane >= o) x += y;
   }
-  __syncthreads();               // the sums of an earlier scan have been read
-  if (lane == 31) sh.sums[warp] = x;
+  if (lane == 31) sh.sums[turn][warp] = x;
   __syncthreads();
-  int64_t w = sh.sums[lane];
+  T w = static_cast<T>(sh.sums[turn][lane]);
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int64_t y = __shfl_up_sync(0xFFFFFFFFu, w, o);
+    const T y = __shfl_up_sync(0xFFFFFFFFu, w, o);
     if (lane >= o) w += y;
   }
   *total = __shfl_sync(0xFFFFFFFFu, w, 31);
-  const int64_t before = __shfl_sync(0xFFFFFFFFu, w, warp > 0 ? warp - 1 : 0);
+  const T before = __shfl_sync(0xFFFFFFFFu, w, warp > 0 ? warp - 1 : 0);
   return x - v + (warp > 0 ? before : 0);
 }
 
-__device__ __forceinline__ int64_t sum(Shared& sh, int64_t v) {
-  int64_t total;
-  scan(sh, v, &total);
-  return total;
-}
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
 
 // Value v of this CTA (the same in its threads) to all CTAs' all[which]; they have it behind the
 // cluster's next barrier, which also orders what the CTAs wrote to memory.
-__device__ __forceinline__ void tell(Shared& sh, int which, int64_t v) {
+__device__ __forceinline__ void tell(Shared& sh, int which, int v) {
   if (threadIdx.x < kCtas) {
     const uint32_t to = mapa_shared(smem_u32(&sh.all[which][cluster_rank()]), threadIdx.x);
-    asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(to), "l"(v) : "memory");
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(to), "r"(v) : "memory");
   }
 }
 __device__ __forceinline__ int64_t told_before(const Shared& sh, int which) {
@@ -115,41 +114,55 @@ __device__ __forceinline__ Stripe stripe(const PageArgs& a) {
   const int64_t begin = cluster_rank() * each;
   return Stripe{min(begin, a.n_pages), min(begin + each, a.n_pages)};
 }
-// The counts of pages p .. p + 3 of a stripe that ends at `end`, past L1 (other CTAs change them); -1
+// The counts of pages p .. p + 3 of a stripe that ends at `end`, past L1 (other CTAs change them); kBehind
 // behind the end.  p is a multiple of four.
+constexpr int kBehind = INT32_MIN;
 __device__ __forceinline__ int4 counts_at(const PageArgs& a, int64_t p, int64_t end) {
   if (p + 4 <= end) return __ldcg(reinterpret_cast<const int4*>(a.refs + p));
-  int4 v = make_int4(-1, -1, -1, -1);
+  int4 v = make_int4(kBehind, kBehind, kBehind, kBehind);
   if (p < end) v.x = __ldcg(a.refs + p);
   if (p + 1 < end) v.y = __ldcg(a.refs + p + 1);
   if (p + 2 < end) v.z = __ldcg(a.refs + p + 2);
   return v;
 }
-
-// How many pages of the stripe satisfy f(page, count).
-template <typename F>
-__device__ __forceinline__ int64_t count_pages(Shared& sh, const PageArgs& a, F&& f) {
+// Those of this thread in the first round over its stripe.
+__device__ __forceinline__ int4 first_counts(const PageArgs& a) {
   const Stripe st = stripe(a);
-  int64_t n = 0;
-  for (int64_t p = st.begin + 4 * threadIdx.x; p < st.end; p += 4 * kThreads) {
-    const int4 v = counts_at(a, p, st.end);
+  return counts_at(a, st.begin + 4 * threadIdx.x, st.end);
+}
+
+// How many pages of the stripe satisfy f(page, count); `first` as of first_counts.
+template <typename F>
+__device__ __forceinline__ int count_pages(Shared& sh, const PageArgs& a, int which, int4& first, F&& f) {
+  const Stripe st = stripe(a);
+  int n = 0;
+  int4 v = first;
+  for (int64_t p = st.begin + 4 * threadIdx.x; p < st.end;) {
     n += f(p, v.x) + f(p + 1, v.y) + f(p + 2, v.z) + f(p + 3, v.w);
+    if (p < st.begin + 4 * kThreads) first = v;
+    p += 4 * kThreads;
+    if (p < st.end) v = counts_at(a, p, st.end);
   }
-  return sum(sh, n);
+  n = __reduce_add_sync(0xFFFFFFFFu, n);
+  if ((threadIdx.x & 31) == 0) sh.counts[which][threadIdx.x >> 5] = n;
+  __syncthreads();
+  return __reduce_add_sync(0xFFFFFFFFu, sh.counts[which][threadIdx.x & 31]);
 }
 
 // Calls g(j, page) for the pages of the stripe that satisfy f, j = `before` + their number in
-// order, as long as j < limit.
+// order, as long as j < limit.  Takes turns of scan from `turn` on.
 template <typename F, typename G>
-__device__ __forceinline__ void number_pages(Shared& sh, const PageArgs& a, int64_t before, int64_t limit, F&& f,
-                                             G&& g) {
+__device__ __forceinline__ void number_pages(Shared& sh, const PageArgs& a, int turn, int4 first, int64_t before,
+                                             int64_t limit, F&& f, G&& g) {
   const Stripe st = stripe(a);
+  int4 v = first;
   for (int64_t p0 = st.begin; p0 < st.end && before < limit; p0 += 4 * kThreads) {
     const int64_t p = p0 + 4 * threadIdx.x;
-    const int4 v = counts_at(a, p, st.end);
+    if (p0 != st.begin) v = counts_at(a, p, st.end);
     const bool on[4] = {f(p, v.x), f(p + 1, v.y), f(p + 2, v.z), f(p + 3, v.w)};
-    int64_t total;
-    int64_t j = before + scan(sh, on[0] + on[1] + on[2] + on[3], &total);
+    int total;
+    int64_t j = before + scan<int>(sh, turn, on[0] + on[1] + on[2] + on[3], &total);
+    turn ^= 1;
 #pragma unroll
     for (int y = 0; y < 4; ++y) {
       if (on[y]) {
@@ -174,15 +187,11 @@ __device__ __forceinline__ int part_of(const int* from, int n, int x) {
   return lo;
 }
 
-// Fills part[i] (i <= n) with the sum of the v of the entries before i; thread i has entry i's.  Sums
-// past 2^31 end there: returns the true total.
-__device__ __forceinline__ int64_t fill_parts(Shared& sh, int* part, int n, int64_t v) {
-  int64_t total;
-  const int64_t before = scan(sh, v, &total);
+// Fills part[i] (i <= n) with the sum of the v of the entries before i, at most 2^31 - 1; thread i has
+// entry i's.  A barrier has to follow.
+__device__ __forceinline__ void fill_parts(int* part, int n, int64_t before, int64_t total) {
   if (threadIdx.x < n) part[threadIdx.x] = static_cast<int>(min(before, int64_t{INT32_MAX}));
   if (threadIdx.x == 0) part[n] = static_cast<int>(min(total, int64_t{INT32_MAX}));
-  __syncthreads();
-  return total;
 }
 
 // Calls f(i, column) for columns begin(i) .. end(i) - 1 of every entry, warps of the whole cluster a chunk
@@ -201,7 +210,7 @@ __device__ __forceinline__ void each_column(const Shared& sh, const PageArgs& a,
   }
 }
 
-// Takes a page out of one table entry.
+// Takes a page out of one table entry (where nothing else tells that the table and the counts do not agree).
 __device__ __forceinline__ void give_back(const PageArgs& a, int32_t page) {
   if (page < 0) return;
   if (page >= a.n_pages) {
@@ -240,12 +249,13 @@ __device__ __forceinline__ int32_t& entry(const PageArgs& a, int slot, int64_t c
   return a.table[static_cast<int64_t>(slot) * a.cols + col];
 }
 
+__device__ __forceinline__ bool is_free(int64_t, int count) { return count == 0; }
+
 __global__ void __launch_bounds__(kThreads) pages_resize_kernel(const __grid_constant__ PageArgs a) {
   __shared__ Shared sh;
   grid_dep_launch();
   clear_bits(sh, a);
   grid_dep_wait();
-  cluster_sync();                       // all CTAs have begun: their shared memory is there
   const int i = threadIdx.x;
   const int slot = i < a.n ? __ldg(a.a + i) : -1, to = i < a.n ? __ldg(a.b + i) : 0;
   bool on = one_of_its_own(sh, a, slot);
@@ -263,15 +273,22 @@ __global__ void __launch_bounds__(kThreads) pages_resize_kernel(const __grid_con
     sh.len[i] = on ? len : -1;
   }
   const int64_t had = on ? ceil_page(a, len) : 0, gets = on ? ceil_page(a, to) : 0;
-  fill_parts(sh, sh.chunk, a.n, on && gets < had ? (had - gets + kChunk - 1) / kChunk : 0);
+  int chunks;
+  const int chunks_before = scan<int>(sh, 0, on && gets < had ? static_cast<int>((had - gets + kChunk - 1) / kChunk) : 0, &chunks);
+  fill_parts(sh.chunk, a.n, chunks_before, chunks);
+  __syncthreads();
   each_column(
       sh, a, [&](int x) { return ceil_page(a, sh.b[x]); }, [&](int x) { return ceil_page(a, sh.len[x]); },
       [&](int x, int64_t c) {
         int32_t& e = entry(a, sh.a[x], c);
-        give_back(a, e);
+        if (page_there(e, a.n_pages))
+          atomicSub(a.refs + e, 1);     // below 0 is found when they are counted
+        else if (e >= 0)
+          report_error(a.status, DS_VIT_ERANGE);
         e = -1;
       });
-  cluster_sync();                       // the counts without what was given back
+  cluster_sync();                       // the counts without what was given back; and all CTAs have begun
+  int4 v = first_counts(a);
   // What grows: fresh pages, and a copy of the last one where another sequence names it too.
   bool copy = false;
   int32_t last = -1;
@@ -286,14 +303,25 @@ __global__ void __launch_bounds__(kThreads) pages_resize_kernel(const __grid_con
     }
   }
   const bool grows = on && to > len;
-  const int64_t want = fill_parts(sh, sh.fresh, a.n, grows ? gets - had + copy : 0);
-  const int64_t n_copies = fill_parts(sh, sh.copies, a.n, copy);
-  tell(sh, 0, count_pages(sh, a, [](int64_t, int v) { return v == 0; }));
+  // Both sums in one: at most 1024 copies, 11 bits.
+  int64_t both;
+  const int64_t before = scan<int64_t>(sh, 1, (grows ? gets - had + copy : 0) << 11 | copy, &both);
+  const int64_t want = both >> 11, n_copies = both & 2047;
+  fill_parts(sh.fresh, a.n, before >> 11, want);
+  fill_parts(sh.copies, a.n, before & 2047, n_copies);
+  tell(sh, 0, count_pages(sh, a, 0, v, [&](int64_t p, int& count) {
+         if (count < 0 && count != kBehind) {      // the tables and the counts did not agree
+           report_error(a.status, DS_VIT_EINVAL);
+           a.refs[p] = count = 0;
+         }
+         return count == 0;
+       }));
   cluster_sync();
   const bool served = want <= told(sh, 0) && n_copies <= a.cap;
   if (served) {
+    // (Counts below 0 of a further round have been put right in memory.)
     number_pages(
-        sh, a, told_before(sh, 0), want, [](int64_t, int v) { return v == 0; },
+        sh, a, 0, v, told_before(sh, 0), want, is_free,
         [&](int64_t j, int32_t page) {
           const int x = part_of(sh.fresh, a.n, static_cast<int>(j));
           const int64_t col = ceil_page(a, sh.len[x]);
@@ -339,7 +367,10 @@ __global__ void __launch_bounds__(kThreads) pages_release_kernel(const __grid_co
     sh.b[i] = static_cast<int>(first);
     sh.len[i] = static_cast<int>(last);
   }
-  fill_parts(sh, sh.chunk, a.n, (last - first + kChunk - 1) / kChunk);
+  int chunks;
+  const int before = scan<int>(sh, 0, static_cast<int>((last - first + kChunk - 1) / kChunk), &chunks);
+  fill_parts(sh.chunk, a.n, before, chunks);
+  __syncthreads();
   // A slot may be in the list more than once: whoever takes the page out of the entry gives it back.
   each_column(
       sh, a, [&](int x) { return static_cast<int64_t>(sh.b[x]); }, [&](int x) { return static_cast<int64_t>(sh.len[x]); },
@@ -350,8 +381,9 @@ __global__ void __launch_bounds__(kThreads) pages_fork_kernel(const __grid_const
   __shared__ Shared sh;
   grid_dep_launch();
   clear_bits(sh, a);
+  cluster_arrive();
   grid_dep_wait();
-  cluster_sync();
+  int4 v = first_counts(a);
   const int i = threadIdx.x;
   const int src = i < a.n ? __ldg(a.a + i) : -1, dst = i < a.n ? __ldg(a.b + i) : -1;
   bool on = one_of_its_own(sh, a, dst);
@@ -379,9 +411,14 @@ __global__ void __launch_bounds__(kThreads) pages_fork_kernel(const __grid_const
     sh.len[i] = on ? len : -1;
   }
   const int64_t full = on ? len >> a.page_shift : 0;
-  fill_parts(sh, sh.chunk, a.n, (full + kChunk - 1) / kChunk);
-  const int64_t want = fill_parts(sh, sh.fresh, a.n, copy);
-  tell(sh, 0, count_pages(sh, a, [](int64_t, int v) { return v == 0; }));
+  int64_t both;
+  const int64_t before = scan<int64_t>(sh, 0, (full + kChunk - 1) / kChunk << 32 | copy, &both);
+  const int want = static_cast<int>(both);
+  fill_parts(sh.chunk, a.n, before >> 32, both >> 32);
+  fill_parts(sh.fresh, a.n, static_cast<int>(before), want);
+  const int free_pages = count_pages(sh, a, 0, v, is_free);
+  cluster_wait();                       // all CTAs have begun: their shared memory is there
+  tell(sh, 0, free_pages);
   cluster_sync();
   if (want > told(sh, 0) || want > a.cap) {
     if (i == 0 && cluster_rank() == 0) {
@@ -391,7 +428,7 @@ __global__ void __launch_bounds__(kThreads) pages_fork_kernel(const __grid_const
     return;
   }
   number_pages(
-      sh, a, told_before(sh, 0), want, [](int64_t, int v) { return v == 0; },
+      sh, a, 1, v, told_before(sh, 0), want, is_free,
       [&](int64_t j, int32_t page) {
         const int x = part_of(sh.fresh, a.n, static_cast<int>(j));
         const int64_t col = sh.len[x] >> a.page_shift;
@@ -415,7 +452,7 @@ __global__ void __launch_bounds__(kThreads) pages_fork_kernel(const __grid_const
     if ((len & ((1 << a.page_shift) - 1)) != 0 && !copy) entry(a, dst, full) = -1;
     a.kv_len[dst] = len;
   }
-  if (i == 0) *a.count = static_cast<int>(want);
+  if (i == 0) *a.count = want;
 }
 
 __global__ void __launch_bounds__(kThreads) pages_compact_kernel(const __grid_constant__ PageArgs a) {
@@ -424,21 +461,23 @@ __global__ void __launch_bounds__(kThreads) pages_compact_kernel(const __grid_co
   grid_dep_wait();
   cluster_sync();
   const int64_t lane = threadIdx.x + static_cast<int64_t>(cluster_rank()) * kThreads, lanes = kCtas * kThreads;
-  tell(sh, 0, count_pages(sh, a, [&](int64_t p, int v) {
-         if (v < 0 && p < a.n_pages) report_error(a.status, DS_VIT_EINVAL);
-         return v > 0;
+  int4 v = first_counts(a);
+  tell(sh, 0, count_pages(sh, a, 0, v, [&](int64_t, int count) {
+         if (count < 0 && count != kBehind) report_error(a.status, DS_VIT_EINVAL);
+         return count > 0;
        }));
   cluster_sync();
   const int64_t used = told(sh, 0);
-  const auto hole = [&](int64_t p, int v) { return v == 0 && p < used; };
-  const auto mover = [&](int64_t p, int v) { return v > 0 && p >= used; };
-  tell(sh, 1, count_pages(sh, a, hole));
-  tell(sh, 2, count_pages(sh, a, mover));
+  const auto hole = [&](int64_t p, int count) { return count == 0 && p < used; };
+  const auto mover = [&](int64_t p, int count) { return count > 0 && p >= used; };
+  tell(sh, 1, count_pages(sh, a, 1, v, hole));
+  tell(sh, 2, count_pages(sh, a, 2, v, mover));
   cluster_sync();
   // As many holes as movers, unless a count is below 0.
   const int64_t moved = min(min(told(sh, 1), told(sh, 2)), static_cast<int64_t>(a.cap));
-  number_pages(sh, a, told_before(sh, 1), moved, hole, [&](int64_t j, int32_t page) { a.to[j] = page; });
-  number_pages(sh, a, told_before(sh, 2), moved, mover, [&](int64_t j, int32_t page) { a.from[j] = page; });
+  number_pages(sh, a, 0, v, told_before(sh, 1), moved, hole, [&](int64_t j, int32_t page) { a.to[j] = page; });
+  __syncthreads();                      // the last scan's sums have been read
+  number_pages(sh, a, 0, v, told_before(sh, 2), moved, mover, [&](int64_t j, int32_t page) { a.from[j] = page; });
   cluster_sync();
   // The counts move along; in the place of the old one stands where the page went.
   for (int64_t j = lane; j < moved; j += lanes) {
@@ -475,56 +514,57 @@ __global__ void __launch_bounds__(kThreads) pages_compact_kernel(const __grid_co
 // ------------------------------------------------------------------ contents
 
 struct CopyArgs {
-  uint4* at[5];            // keys, values, their exponents, bounds: 16-byte words
-  int64_t words[5];        // of each a page has, summed up to there
+  uint4* held[2];          // keys, values, in 16-byte words
+  int64_t held_words;      // of either, a page's
+  uint4* small[3];         // their exponents, bounds (nullptr: none)
+  int small_words[3];
   uint8_t* bound_exp;
   int heads;
   int64_t n_pages;
   const int32_t *from, *to, *count;
   int cap;
-  int64_t tiles;           // per page
+  int held_tiles;          // CTAs in x: these for the keys, as many for the values, one for the rest
   int* status;
 };
 
 constexpr int kCopyThreads = 256, kCopyWords = 4;    // words a thread has in flight
 
-__global__ void __launch_bounds__(kCopyThreads) cache_copy_kernel(const __grid_constant__ CopyArgs a) {
+// CTA (x, y) copies its part x of pages y, y + gridDim.y, ...: what it has to look up is one pair of
+// page numbers, ahead of the words of the pair before.  920 pages of 2 x 131 KB: KFIGURE.
+__global__ void __launch_bounds__(kCopyThreads, 8) cache_copy_kernel(const __grid_constant__ CopyArgs a) {
   grid_dep_launch();
   grid_dep_wait();
   const int n = __ldg(a.count);
   if (n < 0 || n > a.cap) {
-    if (blockIdx.x == 0 && threadIdx.x == 0) report_error(a.status, DS_VIT_EINVAL);
+    if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) report_error(a.status, DS_VIT_EINVAL);
     return;
   }
-  const int64_t all = n * a.tiles;
-  for (int64_t u = blockIdx.x; u < all; u += gridDim.x) {
-    const int64_t i = u / a.tiles, tile = u - i * a.tiles;
+  const int x = static_cast<int>(blockIdx.x);
+  const int64_t first = static_cast<int64_t>(x % a.held_tiles) * (kCopyThreads * kCopyWords) + threadIdx.x;
+  uint4* const base = a.held[x >= a.held_tiles && x < 2 * a.held_tiles];
+  for (int i = static_cast<int>(blockIdx.y); i < n; i += static_cast<int>(gridDim.y)) {
     const int from = __ldg(a.from + i), to = __ldg(a.to + i);
     if (!page_there(from, a.n_pages) || !page_there(to, a.n_pages)) {
       if (threadIdx.x == 0) report_error(a.status, DS_VIT_ERANGE);
       continue;
     }
-    uint4 v[kCopyWords];
-    uint4* put[kCopyWords];
+    if (x < 2 * a.held_tiles) {
+      const uint4* const get = base + from * a.held_words + first;
+      uint4* const put = base + to * a.held_words + first;
+      uint4 v[kCopyWords];
 #pragma unroll
-    for (int y = 0; y < kCopyWords; ++y) {
-      const int64_t w = (tile * kCopyWords + y) * kCopyThreads + threadIdx.x;
-      put[y] = nullptr;
-      int64_t before = 0;
+      for (int y = 0; y < kCopyWords; ++y)
+        if (first + y * kCopyThreads < a.held_words) v[y] = __ldcs(get + y * kCopyThreads);
 #pragma unroll
-      for (int x = 0; x < 5; ++x) {
-        if (w >= before && w < a.words[x]) {
-          const int64_t each = a.words[x] - before;
-          v[y] = __ldcs(a.at[x] + from * each + (w - before));
-          put[y] = a.at[x] + to * each + (w - before);
-        }
-        before = a.words[x];
-      }
+      for (int y = 0; y < kCopyWords; ++y)
+        if (first + y * kCopyThreads < a.held_words) put[y * kCopyThreads] = v[y];
+      continue;
     }
 #pragma unroll
-    for (int y = 0; y < kCopyWords; ++y)
-      if (put[y] != nullptr) *put[y] = v[y];
-    if (a.bound_exp != nullptr && tile == 0)
+    for (int y = 0; y < 3; ++y)
+      for (int w = threadIdx.x; w < a.small_words[y]; w += kCopyThreads)
+        a.small[y][to * static_cast<int64_t>(a.small_words[y]) + w] = a.small[y][from * static_cast<int64_t>(a.small_words[y]) + w];
+    if (a.bound_exp != nullptr)
       for (int h = threadIdx.x; h < a.heads; h += kCopyThreads)
         a.bound_exp[static_cast<int64_t>(to) * a.heads + h] = a.bound_exp[static_cast<int64_t>(from) * a.heads + h];
   }
@@ -645,27 +685,29 @@ int ds_vit_cache_copy(const ds_vit_cache* cache, const ds_vit_key_bounds* bounds
     return DS_VIT_EINVAL;
   const bool e4m3 = cache->kind == DS_VIT_CACHE_E4M3;
   const int64_t rows = static_cast<int64_t>(c.kv_heads) * cache->page;      // of a page
-  const int64_t held = rows * cache->head_dim * (e4m3 ? 1 : 2) / 16;
   CopyArgs a{};
-  a.at[0] = reinterpret_cast<uint4*>(c.k), a.at[1] = reinterpret_cast<uint4*>(c.v);
-  a.at[2] = reinterpret_cast<uint4*>(c.k_exp), a.at[3] = reinterpret_cast<uint4*>(c.v_exp);
-  a.at[4] = bounds ? reinterpret_cast<uint4*>(bounds->hi_lo) : nullptr;
-  const int64_t words[5] = {held, held, e4m3 ? rows / 16 : 0, e4m3 ? rows / 16 : 0,
-                            bounds ? int64_t{2} * c.kv_heads * cache->head_dim / 16 : 0};
-  for (int x = 0; x < 5; ++x) a.words[x] = (x ? a.words[x - 1] : 0) + words[x];
-  a.bound_exp = bounds ? bounds->exp : nullptr;
+  a.held[0] = reinterpret_cast<uint4*>(c.k), a.held[1] = reinterpret_cast<uint4*>(c.v);
+  a.held_words = rows * cache->head_dim * (e4m3 ? 1 : 2) / 16;
+  if (e4m3) {
+    a.small[0] = reinterpret_cast<uint4*>(c.k_exp), a.small[1] = reinterpret_cast<uint4*>(c.v_exp);
+    a.small_words[0] = a.small_words[1] = static_cast<int>(rows / 16);
+  }
+  if (bounds) {
+    a.small[2] = reinterpret_cast<uint4*>(bounds->hi_lo);
+    a.small_words[2] = 2 * c.kv_heads * cache->head_dim / 16;
+    a.bound_exp = bounds->exp;
+  }
   a.heads = c.kv_heads;
   a.n_pages = c.n_pages;
   a.from = copies->from;
   a.to = copies->to;
   a.count = copies->count;
   a.cap = copies->cap;
-  a.tiles = (a.words[4] + kCopyThreads * kCopyWords - 1) / (kCopyThreads * kCopyWords);
+  a.held_tiles = static_cast<int>((a.held_words + kCopyThreads * kCopyWords - 1) / (kCopyThreads * kCopyWords));
   a.status = reinterpret_cast<int*>(status);
-  const int64_t most = a.tiles * copies->cap;
-  const unsigned blocks = static_cast<unsigned>(std::min<int64_t>(most, 8 * static_cast<int64_t>(num_sms())));
-  return launched(launch_pdl(cache_copy_kernel, dim3(blocks), dim3(kCopyThreads), 0,
-                             static_cast<cudaStream_t>(stream), a));
+  const int parts = 2 * a.held_tiles + (e4m3 || bounds);
+  const dim3 grid(static_cast<unsigned>(parts), static_cast<unsigned>(std::min(copies->cap, (8 * num_sms() + parts - 1) / parts)));
+  return launched(launch_pdl(cache_copy_kernel, grid, dim3(kCopyThreads), 0, static_cast<cudaStream_t>(stream), a));
 }
 
 }  // extern "C"
