@@ -301,6 +301,69 @@ __device__ __forceinline__ void pick(const uint32_t* keys, int n, int top, int32
   for (int i = taken + tid; i < top; i += kThreads) out[i] = -1;
 }
 
+// The same by one warp where few blocks are looked for: the smallest of the `need` largest among the
+// lanes' own maxima is a lower bound of the threshold that hardly more keys than needed
+// reach; the rest happens among those, kept with their blocks in `kept`.  False, with nothing written,
+// where there are more than kKept of them or more than 32 are looked for.  (532 blocks, 16 of them: 83 us for 16 thousand lists,
+// 137 by the threshold's bits.)
+constexpr int kKept = 64;
+__device__ __forceinline__ bool pick_few(const uint32_t* keys, int n, int top, int32_t* out, uint2* kept) {
+  const int lane = threadIdx.x & 31;
+  uint32_t most = 0;                    // largest key of the lane's that is not forced
+  int forced = 0, some = 0;
+#pragma unroll 4
+  for (int i = lane; i < n; i += 32) {
+    const uint32_t k = keys[i];
+    forced += k == kForced;
+    some += k != 0;
+    most = max(most, k == kForced ? 0u : k);
+  }
+  const int both = __reduce_add_sync(0xFFFFFFFFu, forced << 16 | some);
+  forced = both >> 16;
+  const int need = top - forced;
+  if ((both & 0xFFFF) <= top || need > 32) return false;
+  uint32_t bound = kForced;
+  if (need > 0) {
+    // Sorted over the lanes, the largest first.
+    uint32_t x = most;
+#pragma unroll
+    for (int size = 2; size <= 32; size *= 2)
+#pragma unroll
+      for (int o = size / 2; o > 0; o /= 2) {
+        const uint32_t y = __shfl_xor_sync(0xFFFFFFFFu, x, o);
+        const bool keep_max = ((lane & o) == 0) == ((lane & size) == 0);
+        x = keep_max ? max(x, y) : min(x, y);
+      }
+    bound = max(__shfl_sync(0xFFFFFFFFu, x, need - 1), 1u);
+  }
+  const auto lower = (1u << lane) - 1;
+  int n_kept = 0;
+  for (int i0 = 0; i0 < n; i0 += 32) {
+    const uint32_t k = i0 + lane < n ? keys[i0 + lane] : 0u;
+    const uint32_t all = __ballot_sync(0xFFFFFFFFu, k >= bound);
+    if (all == 0) continue;
+    const int to = n_kept + __popc(all & lower);
+    n_kept += __popc(all);
+    if (n_kept > kKept) return false;
+    if (k >= bound) kept[to] = make_uint2(k, static_cast<uint32_t>(i0 + lane));
+  }
+  __syncwarp();
+  const uint2 none = make_uint2(0, 0);
+  const uint2 c0 = lane < n_kept ? kept[lane] : none, c1 = lane + 32 < n_kept ? kept[lane + 32] : none;
+  // How many of the kept come before each: larger ones, and equal ones of lower blocks.
+  int before0 = 0, before1 = 0;
+  for (int y = 0; y < n_kept; ++y) {
+    const uint32_t k = kept[y].x;
+    before0 += k > c0.x || (k == c0.x && y < lane);
+    before1 += k > c1.x || (k == c1.x && y < lane + 32);
+  }
+  const bool on0 = lane < n_kept && before0 < top, on1 = lane + 32 < n_kept && before1 < top;
+  const uint32_t all0 = __ballot_sync(0xFFFFFFFFu, on0), all1 = __ballot_sync(0xFFFFFFFFu, on1);
+  if (on0) out[__popc(all0 & lower)] = static_cast<int32_t>(c0.y);
+  if (on1) out[__popc(all0) + __popc(all1 & lower)] = static_cast<int32_t>(c1.y);
+  return true;
+}
+
 // kSingle: a row a CTA, or a cluster.
 template <int D, bool kSingle>
 __global__ void __launch_bounds__(kSelectThreads) cache_select_kernel(const __grid_constant__ SelectArgs a) {
@@ -309,6 +372,7 @@ __global__ void __launch_bounds__(kSelectThreads) cache_select_kernel(const __gr
   uint32_t* const keys = reinterpret_cast<uint32_t*>(dynamic);
   __shared__ __align__(16) __half w[8][2 * D + 8];
   __shared__ int sums[2][kSelectWarps];
+  __shared__ uint2 kept[kSingle ? 1 : kSelectWarps][kKept];
   grid_dep_launch();
   grid_dep_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
@@ -348,14 +412,19 @@ __global__ void __launch_bounds__(kSelectThreads) cache_select_kernel(const __gr
     }
     const int32_t* table = a.b.table + static_cast<int64_t>(s) * a.b.table_cols;
     const int step = 16 * kSelectWarps * static_cast<int>(ranks);
-    for (int k0 = 16 * (warp * static_cast<int>(ranks) + static_cast<int>(rank)); k0 < blocks; k0 += step) {
+    int k0 = 16 * (warp * static_cast<int>(ranks) + static_cast<int>(rank));
+    int32_t ahead[2];                               // the next blocks' pages
+#pragma unroll
+    for (int y = 0; y < 2; ++y) ahead[y] = k0 + g + 8 * y < blocks ? __ldg(table + k0 + g + 8 * y) : -1;
+    for (; k0 < blocks; k0 += step) {
       int32_t at[2];
       uint4 u[2][kSteps];
       uint32_t byte[2];
 #pragma unroll
       for (int y = 0; y < 2; ++y) {
-        const int k = k0 + g + 8 * y;
-        at[y] = k < blocks ? __ldg(table + k) : -1;
+        at[y] = ahead[y];
+        const int k = k0 + step + g + 8 * y;
+        ahead[y] = k < blocks ? __ldg(table + k) : -1;
       }
 #pragma unroll
       for (int y = 0; y < 2; ++y) {
@@ -412,7 +481,8 @@ __global__ void __launch_bounds__(kSelectThreads) cache_select_kernel(const __gr
       pick<kSelectThreads>(keys, blocks, a.top, a.blocks + ra * a.row_stride + head * a.head_stride, sums);
       return;
     } else {
-      if (warp < n_rows)
+      if (warp < n_rows && !pick_few(keys + warp * a.places, blocks, a.top,
+                                     a.blocks + (ra + warp) * a.row_stride + head * a.head_stride, kept[warp]))
         pick<32>(keys + warp * a.places, blocks, a.top, a.blocks + (ra + warp) * a.row_stride + head * a.head_stride,
                  sums);
       __syncthreads();
