@@ -16,6 +16,7 @@
 #include <cuda_fp16.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "cache.cuh"
 
@@ -177,9 +178,10 @@ __device__ __forceinline__ uint32_t f16_of_bytes(uint32_t biased, uint32_t which
   return r;
 }
 
-// The shared query of one row: w[0 .. D - 1] sums of positive, w[D .. 2 D - 1] of negative parts.  By one warp.
-template <int D>
-__device__ __forceinline__ void shared_query(const SelectArgs& a, const bf16* q, __half* w, int lane) {
+// The shared query of one row: w[0 .. D - 1] sums of positive, w[D .. 2 D - 1] of negative parts, as
+// fp16 or 16-bit whole numbers.  By one warp.
+template <int D, typename T>
+__device__ __forceinline__ void shared_query(const SelectArgs& a, const bf16* q, T* w, int lane) {
   constexpr int kPer = D / 32;
   auto load = [&](int h, float (&x)[kPer]) {
     const uint32_t* at = reinterpret_cast<const uint32_t*>(q + h * D) + lane * (kPer / 2);
@@ -218,8 +220,8 @@ __device__ __forceinline__ void shared_query(const SelectArgs& a, const bf16* q,
   }
 #pragma unroll
   for (int y = 0; y < kPer; ++y) {
-    w[lane * kPer + y] = __int2half_rn(up[y]);
-    w[D + lane * kPer + y] = __int2half_rn(down[y]);
+    w[lane * kPer + y] = static_cast<T>(up[y]);
+    w[D + lane * kPer + y] = static_cast<T>(down[y]);
   }
 }
 
@@ -301,6 +303,19 @@ __device__ __forceinline__ void pick(const uint32_t* keys, int n, int top, int32
   for (int i = taken + tid; i < top; i += kThreads) out[i] = -1;
 }
 
+// Sorted over the lanes of a warp, the largest first.
+__device__ __forceinline__ uint32_t sorted_down(uint32_t x, int lane) {
+#pragma unroll
+  for (int size = 2; size <= 32; size *= 2)
+#pragma unroll
+    for (int o = size / 2; o > 0; o /= 2) {
+      const uint32_t y = __shfl_xor_sync(0xFFFFFFFFu, x, o);
+      const bool keep_max = ((lane & o) == 0) == ((lane & size) == 0);
+      x = keep_max ? max(x, y) : min(x, y);
+    }
+  return x;
+}
+
 // The same by one warp where few blocks are looked for: the smallest of the `need` largest among the
 // lanes' own maxima is a lower bound of the threshold that hardly more keys than needed
 // reach; the rest happens among those, kept with their blocks in `kept`.  False, with nothing written,
@@ -324,17 +339,7 @@ __device__ __forceinline__ bool pick_few(const uint32_t* keys, int n, int top, i
   if ((both & 0xFFFF) <= top || need > 32) return false;
   uint32_t bound = kForced;
   if (need > 0) {
-    // Sorted over the lanes, the largest first.
-    uint32_t x = most;
-#pragma unroll
-    for (int size = 2; size <= 32; size *= 2)
-#pragma unroll
-      for (int o = size / 2; o > 0; o /= 2) {
-        const uint32_t y = __shfl_xor_sync(0xFFFFFFFFu, x, o);
-        const bool keep_max = ((lane & o) == 0) == ((lane & size) == 0);
-        x = keep_max ? max(x, y) : min(x, y);
-      }
-    bound = max(__shfl_sync(0xFFFFFFFFu, x, need - 1), 1u);
+    bound = max(__shfl_sync(0xFFFFFFFFu, sorted_down(most, lane), need - 1), 1u);
   }
   const auto lower = (1u << lane) - 1;
   int n_kept = 0;
@@ -364,15 +369,99 @@ __device__ __forceinline__ bool pick_few(const uint32_t* keys, int n, int top, i
   return true;
 }
 
+// The same by the CTA.  Each warp has a run of blocks; the least of the warps' (top / 8)-th largest lane maxima
+// is a bound that at least `top` keys reach.  Those fit a key a thread, so that a barrier counts them.
+constexpr int kListed = kSelectThreads;
+__device__ __forceinline__ bool pick_some(const uint32_t* keys, int n, int top, int32_t* out, int (*sums)[kSelectWarps],
+                                          uint4* of_warps, uint2* listed) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const auto lower = (1u << lane) - 1;
+  const int rank = (top + kSelectWarps - 1) / kSelectWarps;
+  if (rank > 32) return false;
+  const int each = (n + kSelectThreads - 1) / kSelectThreads * 32, begin = min(n, warp * each), end = min(n, begin + each);
+  uint32_t most = 0;                    // largest key of the lane's that is not forced
+  int forced = 0, some = 0;
+#pragma unroll 4
+  for (int i = begin + lane; i < end; i += 32) {
+    const uint32_t k = keys[i];
+    forced += k == kForced;
+    some += k != 0;
+    most = max(most, k == kForced ? 0u : k);
+  }
+  forced = __reduce_add_sync(0xFFFFFFFFu, forced);
+  some = __reduce_add_sync(0xFFFFFFFFu, some);
+  const uint32_t largest = __reduce_max_sync(0xFFFFFFFFu, most);
+  const uint32_t at_rank = __shfl_sync(0xFFFFFFFFu, sorted_down(most, lane), rank - 1);
+  if (lane == 0) of_warps[warp] = make_uint4(forced, some, largest, at_rank);
+  __syncthreads();
+  uint32_t lo = kForced, hi = 0;
+  forced = some = 0;
+#pragma unroll
+  for (int y = 0; y < kSelectWarps; ++y) {
+    const uint4 v = of_warps[y];
+    forced += v.x;
+    some += v.y;
+    hi = max(hi, v.z);
+    lo = min(lo, v.w);
+  }
+  if (some <= top) return false;
+  lo = forced == top ? kForced : max(lo, 1u);
+  int mine = 0;
+  for (int i0 = begin; i0 < end; i0 += 32)
+    mine += __popc(__ballot_sync(0xFFFFFFFFu, i0 + lane < end && keys[i0 + lane] >= lo));
+  if (lane == 0) sums[0][warp] = mine;
+  __syncthreads();
+  int total = 0, to = 0;
+#pragma unroll
+  for (int y = 0; y < kSelectWarps; ++y) {
+    to += y < warp ? sums[0][y] : 0;
+    total += sums[0][y];
+  }
+  if (total > kListed) return false;
+  for (int i0 = begin; i0 < end; i0 += 32) {
+    const uint32_t k = i0 + lane < end ? keys[i0 + lane] : 0u;
+    const uint32_t all = __ballot_sync(0xFFFFFFFFu, k >= lo);
+    if (k >= lo) listed[to + __popc(all & lower)] = make_uint2(k, static_cast<uint32_t>(i0 + lane));
+    to += __popc(all);
+  }
+  __syncthreads();
+  const uint2 own = tid < total ? listed[tid] : make_uint2(0, 0);
+  // The threshold is in [lo, hi]: at least `top` keys >= lo, fewer > hi.
+  bool fits = total == top;
+  while (!fits && lo < hi) {
+    const uint32_t mid = lo + (hi - lo + 1) / 2;
+    const int x = __syncthreads_count(own.x >= mid);
+    if (x >= top)
+      lo = mid;
+    else
+      hi = mid - 1;
+    fits = x == top;
+  }
+  const int ties = fits ? top : top - __syncthreads_count(own.x > lo);      // of the keys equal to lo, in order
+  const uint32_t same = __ballot_sync(0xFFFFFFFFu, own.x == lo), over = __ballot_sync(0xFFFFFFFFu, own.x > lo);
+  if (lane == 0) sums[0][warp] = __popc(over), sums[1][warp] = __popc(same);
+  __syncthreads();
+  int over_before = __popc(over & lower), same_before = __popc(same & lower);
+  for (int y = 0; y < warp; ++y) {
+    over_before += sums[0][y];
+    same_before += sums[1][y];
+  }
+  if (own.x > lo || (own.x == lo && own.x != 0 && same_before < ties))
+    out[over_before + min(same_before, ties)] = static_cast<int32_t>(own.y);
+  return true;
+}
+
 // kSingle: a row a CTA, or a cluster.
 template <int D, bool kSingle>
 __global__ void __launch_bounds__(kSelectThreads) cache_select_kernel(const __grid_constant__ SelectArgs a) {
   constexpr int kSteps = 2 * D / 64;                // 16-byte loads of a block, four MMAs each
   extern __shared__ uint4 dynamic[];
   uint32_t* const keys = reinterpret_cast<uint32_t*>(dynamic);
-  __shared__ __align__(16) __half w[8][2 * D + 8];
+  using Weight = std::conditional_t<kSingle, int16_t, __half>;
+  __shared__ __align__(16) Weight w[kSingle ? 1 : 8][2 * D + 8];
   __shared__ int sums[2][kSelectWarps];
-  __shared__ uint2 kept[kSingle ? 1 : kSelectWarps][kKept];
+  __shared__ uint2 kept[kSingle ? 1 : kSelectWarps][kSingle ? kListed : kKept];
+  __shared__ uint4 of_warps[kSelectWarps];
   grid_dep_launch();
   grid_dep_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
@@ -398,16 +487,17 @@ __global__ void __launch_bounds__(kSelectThreads) cache_select_kernel(const __gr
     const int p0 = q.kv - q.c + static_cast<int>(ra - q.row0);                  // position of the first
     const int blocks = max(p0 + n_rows - 1 + page, 0) >> a.page_shift;          // of the last
     if (warp < n_rows)
-      shared_query<D>(a, a.q + (ra + warp) * a.q_stride + static_cast<int64_t>(head) * a.group * D, w[warp], lane);
+      shared_query<D, Weight>(a, a.q + (ra + warp) * a.q_stride + static_cast<int64_t>(head) * a.group * D, w[warp], lane);
     __syncthreads();
     uint32_t qf[kSteps][4][2];
 #pragma unroll
     for (int j = 0; j < kSteps; ++j) {
-      const uint32_t* from = reinterpret_cast<const uint32_t*>(&w[g][64 * j + 16 * t]);
+      // The lane's 16 terms of each piece of a block: of row g, or of the one row.
+      const uint32_t* from = reinterpret_cast<const uint32_t*>(&w[kSingle ? 0 : g][64 * j + 16 * t]);
 #pragma unroll
       for (int x = 0; x < 4; ++x) {
-        qf[j][x][0] = g < n_rows ? from[2 * x] : 0u;
-        qf[j][x][1] = g < n_rows ? from[2 * x + 1] : 0u;
+        qf[j][x][0] = kSingle || g < n_rows ? from[2 * x] : 0u;
+        qf[j][x][1] = kSingle || g < n_rows ? from[2 * x + 1] : 0u;
       }
     }
     const int32_t* table = a.b.table + static_cast<int64_t>(s) * a.b.table_cols;
@@ -439,16 +529,36 @@ __global__ void __launch_bounds__(kSelectThreads) cache_select_kernel(const __gr
         for (int j = 0; j < kSteps; ++j) u[y][j] = __ldg(from + 4 * j);
       }
       float c[4] = {0.f, 0.f, 0.f, 0.f};
+      if constexpr (kSingle) {
+        // One row would leave seven eighths of an MMA empty: 16-bit weights with the bytes, two at a time.
+        int part[2] = {0, 0};
 #pragma unroll
-      for (int j = 0; j < kSteps; ++j) {
-        const uint32_t b0[4] = {u[0][j].x, u[0][j].y, u[0][j].z, u[0][j].w};
-        const uint32_t b1[4] = {u[1][j].x, u[1][j].y, u[1][j].z, u[1][j].w};
+        for (int y = 0; y < 2; ++y) {
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          const uint32_t v0 = b0[x] ^ 0x80808080u, v1 = b1[x] ^ 0x80808080u;
-          const uint32_t m[4] = {f16_of_bytes(v0, 0x4140u), f16_of_bytes(v1, 0x4140u), f16_of_bytes(v0, 0x4342u),
-                                 f16_of_bytes(v1, 0x4342u)};
-          mma_f16(c, m, qf[j][x][0], qf[j][x][1]);
+          for (int j = 0; j < kSteps; ++j) {
+            const uint32_t v[4] = {u[y][j].x, u[y][j].y, u[y][j].z, u[y][j].w};
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              part[y] = __dp2a_lo(static_cast<int>(qf[j][x][0]), static_cast<int>(v[x]), part[y]);
+              part[y] = __dp2a_hi(static_cast<int>(qf[j][x][1]), static_cast<int>(v[x]), part[y]);
+            }
+          }
+          part[y] += __shfl_xor_sync(0xFFFFFFFFu, part[y], 1);
+          part[y] += __shfl_xor_sync(0xFFFFFFFFu, part[y], 2);
+          c[2 * y] = static_cast<float>(part[y]);
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < kSteps; ++j) {
+          const uint32_t b0[4] = {u[0][j].x, u[0][j].y, u[0][j].z, u[0][j].w};
+          const uint32_t b1[4] = {u[1][j].x, u[1][j].y, u[1][j].z, u[1][j].w};
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const uint32_t v0 = b0[x] ^ 0x80808080u, v1 = b1[x] ^ 0x80808080u;
+            const uint32_t m[4] = {f16_of_bytes(v0, 0x4140u), f16_of_bytes(v1, 0x4140u), f16_of_bytes(v0, 0x4342u),
+                                   f16_of_bytes(v1, 0x4342u)};
+            mma_f16(c, m, qf[j][x][0], qf[j][x][1]);
+          }
         }
       }
 #pragma unroll
@@ -478,7 +588,8 @@ __global__ void __launch_bounds__(kSelectThreads) cache_select_kernel(const __gr
       __syncthreads();
     }
     if constexpr (kSingle) {
-      pick<kSelectThreads>(keys, blocks, a.top, a.blocks + ra * a.row_stride + head * a.head_stride, sums);
+      if (!pick_some(keys, blocks, a.top, a.blocks + ra * a.row_stride + head * a.head_stride, sums, of_warps, kept[0]))
+        pick<kSelectThreads>(keys, blocks, a.top, a.blocks + ra * a.row_stride + head * a.head_stride, sums);
       return;
     } else {
       if (warp < n_rows && !pick_few(keys + warp * a.places, blocks, a.top,
