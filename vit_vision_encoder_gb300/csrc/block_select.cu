@@ -16,7 +16,6 @@
 #include <cuda_fp16.h>
 
 #include <algorithm>
-#include <type_traits>
 
 #include "cache.cuh"
 
@@ -369,8 +368,8 @@ __device__ __forceinline__ bool pick_few(const uint32_t* keys, int n, int top, i
   return true;
 }
 
-// The same by the CTA.  Each warp has a run of blocks; the least of the warps' (top / 8)-th largest lane maxima
-// is a bound that at least `top` keys reach.  Those fit a key a thread, so that a barrier counts them.
+// The same by the CTA.  The least of the warps' (top / 8)-th largest lane maxima (keys dealt to all lanes in
+// turn) is a bound that at least `top` keys reach.  Those fit a key a thread, so that a barrier counts them.
 constexpr int kListed = kSelectThreads;
 __device__ __forceinline__ bool pick_some(const uint32_t* keys, int n, int top, int32_t* out, int (*sums)[kSelectWarps],
                                           uint4* of_warps, uint2* listed) {
@@ -378,11 +377,10 @@ __device__ __forceinline__ bool pick_some(const uint32_t* keys, int n, int top, 
   const auto lower = (1u << lane) - 1;
   const int rank = (top + kSelectWarps - 1) / kSelectWarps;
   if (rank > 32) return false;
-  const int each = (n + kSelectThreads - 1) / kSelectThreads * 32, begin = min(n, warp * each), end = min(n, begin + each);
   uint32_t most = 0;                    // largest key of the lane's that is not forced
   int forced = 0, some = 0;
 #pragma unroll 4
-  for (int i = begin + lane; i < end; i += 32) {
+  for (int i = tid; i < n; i += kSelectThreads) {
     const uint32_t k = keys[i];
     forced += k == kForced;
     some += k != 0;
@@ -406,6 +404,8 @@ __device__ __forceinline__ bool pick_some(const uint32_t* keys, int n, int top, 
   }
   if (some <= top) return false;
   lo = forced == top ? kForced : max(lo, 1u);
+  // Listed in order: each warp has a run of blocks.
+  const int each = (n + kSelectThreads - 1) / kSelectThreads * 32, begin = min(n, warp * each), end = min(n, begin + each);
   int mine = 0;
   for (int i0 = begin; i0 < end; i0 += 32)
     mine += __popc(__ballot_sync(0xFFFFFFFFu, i0 + lane < end && keys[i0 + lane] >= lo));
@@ -451,30 +451,54 @@ __device__ __forceinline__ bool pick_some(const uint32_t* keys, int n, int top, 
   return true;
 }
 
-// kSingle: a row a CTA, or a cluster.
-template <int D, bool kSingle>
+// The bounds of 16 blocks from k0 on, as a lane of a warp has them: its 16-byte pieces t, t + 4, ... of blocks g and g + 8.
+template <int D>
+struct BoundTile {
+  int32_t at[2];                        // pages; below 0: no block here
+  uint4 u[2][D / 32];
+  uint32_t byte[2];
+  __device__ __forceinline__ void load(const SelectArgs& a, int head, int t) {
+#pragma unroll
+    for (int y = 0; y < 2; ++y) {
+      if (at[y] >= a.n_pages) {
+        report_error(a.status, DS_VIT_ERANGE);
+        at[y] = -1;
+      }
+      const int64_t row = static_cast<int64_t>(max(at[y], 0)) * a.kv_heads + head;
+      const uint4* from = reinterpret_cast<const uint4*>(a.hi_lo + row * 2 * D) + t;
+      byte[y] = __ldg(a.exp + row);
+#pragma unroll
+      for (int j = 0; j < D / 32; ++j) u[y][j] = __ldg(from + 4 * j);
+    }
+  }
+  // The key of block k0 + g + 8 y for a row whose own block is `own`, from the whole number `score`.
+  __device__ __forceinline__ uint32_t key(const SelectArgs& a, int y, int k, int own, float score) const {
+    if (k > own || at[y] < 0) return 0;
+    if (k < a.first || k > own - a.last) return kForced;
+    // times 2^(e - 20): every score is a float
+    return byte[y] == 255u ? kNotFinite : ordered(score * power_of_two(max(static_cast<int>(byte[y]), 21) - 147));
+  }
+};
+
+__device__ __forceinline__ int32_t page_entry(const int32_t* table, int k, int blocks) {
+  return k < blocks ? __ldg(table + k) : -1;
+}
+
+// Up to eight rows of one sequence at a time, for one K/V head.
+template <int D>
 __global__ void __launch_bounds__(kSelectThreads) cache_select_kernel(const __grid_constant__ SelectArgs a) {
-  constexpr int kSteps = 2 * D / 64;                // 16-byte loads of a block, four MMAs each
+  constexpr int kSteps = 2 * D / 64;                // 16-byte pieces of a block that a lane has, four MMAs each
   extern __shared__ uint4 dynamic[];
   uint32_t* const keys = reinterpret_cast<uint32_t*>(dynamic);
-  using Weight = std::conditional_t<kSingle, int16_t, __half>;
-  __shared__ __align__(16) Weight w[kSingle ? 1 : 8][2 * D + 8];
+  __shared__ __align__(16) __half w[8][2 * D + 8];
   __shared__ int sums[2][kSelectWarps];
-  __shared__ uint2 kept[kSingle ? 1 : kSelectWarps][kSingle ? kListed : kKept];
-  __shared__ uint4 of_warps[kSelectWarps];
+  __shared__ uint2 kept[kSelectWarps][kKept];
   grid_dep_launch();
   grid_dep_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
-  uint32_t rank = 0, ranks = 1;
-  if constexpr (kSingle) {
-    rank = cluster_rank();
-    asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(ranks));
-    if (ranks > 1) cluster_sync();                  // the first CTA's shared memory is there
-  }
-  const int64_t tile = blockIdx.x / ranks;
+  const int64_t tile = blockIdx.x;
   const int head = static_cast<int>(tile % a.kv_heads);
   const int64_t r_end = min(static_cast<int64_t>(a.b.rows), (tile / a.kv_heads + 1) * a.tile_rows);
-  const int page = 1 << a.page_shift;
   // The rows of one sequence after another.
   for (int64_t ra = tile / a.kv_heads * a.tile_rows; ra < r_end;) {
     const int s = find_seq(a.b, static_cast<int>(ra), lane);
@@ -485,121 +509,156 @@ __global__ void __launch_bounds__(kSelectThreads) cache_select_kernel(const __gr
     }
     const int n_rows = static_cast<int>(min(r_end, static_cast<int64_t>(q.row0) + q.c) - ra);
     const int p0 = q.kv - q.c + static_cast<int>(ra - q.row0);                  // position of the first
-    const int blocks = max(p0 + n_rows - 1 + page, 0) >> a.page_shift;          // of the last
+    const int blocks = max(p0 + n_rows - 1 + (1 << a.page_shift), 0) >> a.page_shift;     // of the last
     if (warp < n_rows)
-      shared_query<D, Weight>(a, a.q + (ra + warp) * a.q_stride + static_cast<int64_t>(head) * a.group * D, w[warp], lane);
+      shared_query<D>(a, a.q + (ra + warp) * a.q_stride + static_cast<int64_t>(head) * a.group * D, w[warp], lane);
     __syncthreads();
     uint32_t qf[kSteps][4][2];
 #pragma unroll
     for (int j = 0; j < kSteps; ++j) {
-      // The lane's 16 terms of each piece of a block: of row g, or of the one row.
-      const uint32_t* from = reinterpret_cast<const uint32_t*>(&w[kSingle ? 0 : g][64 * j + 16 * t]);
+      // Row g's terms that go with the lane's piece of a block.
+      const uint32_t* from = reinterpret_cast<const uint32_t*>(&w[g][64 * j + 16 * t]);
 #pragma unroll
       for (int x = 0; x < 4; ++x) {
-        qf[j][x][0] = kSingle || g < n_rows ? from[2 * x] : 0u;
-        qf[j][x][1] = kSingle || g < n_rows ? from[2 * x + 1] : 0u;
+        qf[j][x][0] = g < n_rows ? from[2 * x] : 0u;
+        qf[j][x][1] = g < n_rows ? from[2 * x + 1] : 0u;
       }
     }
     const int32_t* table = a.b.table + static_cast<int64_t>(s) * a.b.table_cols;
-    const int step = 16 * kSelectWarps * static_cast<int>(ranks);
-    int k0 = 16 * (warp * static_cast<int>(ranks) + static_cast<int>(rank));
+    BoundTile<D> b;
     int32_t ahead[2];                               // the next blocks' pages
 #pragma unroll
-    for (int y = 0; y < 2; ++y) ahead[y] = k0 + g + 8 * y < blocks ? __ldg(table + k0 + g + 8 * y) : -1;
-    for (; k0 < blocks; k0 += step) {
-      int32_t at[2];
-      uint4 u[2][kSteps];
-      uint32_t byte[2];
+    for (int y = 0; y < 2; ++y) ahead[y] = page_entry(table, 16 * warp + g + 8 * y, blocks);
+    for (int k0 = 16 * warp; k0 < blocks; k0 += 16 * kSelectWarps) {
 #pragma unroll
       for (int y = 0; y < 2; ++y) {
-        at[y] = ahead[y];
-        const int k = k0 + step + g + 8 * y;
-        ahead[y] = k < blocks ? __ldg(table + k) : -1;
+        b.at[y] = ahead[y];
+        ahead[y] = page_entry(table, k0 + 16 * kSelectWarps + g + 8 * y, blocks);
       }
-#pragma unroll
-      for (int y = 0; y < 2; ++y) {
-        if (at[y] >= a.n_pages) {
-          report_error(a.status, DS_VIT_ERANGE);
-          at[y] = -1;
-        }
-        const int64_t row = static_cast<int64_t>(max(at[y], 0)) * a.kv_heads + head;
-        const uint4* from = reinterpret_cast<const uint4*>(a.hi_lo + row * 2 * D) + t;
-        byte[y] = __ldg(a.exp + row);
-#pragma unroll
-        for (int j = 0; j < kSteps; ++j) u[y][j] = __ldg(from + 4 * j);
-      }
+      b.load(a, head, t);
       float c[4] = {0.f, 0.f, 0.f, 0.f};
-      if constexpr (kSingle) {
-        // One row would leave seven eighths of an MMA empty: 16-bit weights with the bytes, two at a time.
-        int part[2] = {0, 0};
 #pragma unroll
-        for (int y = 0; y < 2; ++y) {
+      for (int j = 0; j < kSteps; ++j) {
+        const uint32_t b0[4] = {b.u[0][j].x, b.u[0][j].y, b.u[0][j].z, b.u[0][j].w};
+        const uint32_t b1[4] = {b.u[1][j].x, b.u[1][j].y, b.u[1][j].z, b.u[1][j].w};
 #pragma unroll
-          for (int j = 0; j < kSteps; ++j) {
-            const uint32_t v[4] = {u[y][j].x, u[y][j].y, u[y][j].z, u[y][j].w};
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              part[y] = __dp2a_lo(static_cast<int>(qf[j][x][0]), static_cast<int>(v[x]), part[y]);
-              part[y] = __dp2a_hi(static_cast<int>(qf[j][x][1]), static_cast<int>(v[x]), part[y]);
-            }
-          }
-          part[y] += __shfl_xor_sync(0xFFFFFFFFu, part[y], 1);
-          part[y] += __shfl_xor_sync(0xFFFFFFFFu, part[y], 2);
-          c[2 * y] = static_cast<float>(part[y]);
-        }
-      } else {
-#pragma unroll
-        for (int j = 0; j < kSteps; ++j) {
-          const uint32_t b0[4] = {u[0][j].x, u[0][j].y, u[0][j].z, u[0][j].w};
-          const uint32_t b1[4] = {u[1][j].x, u[1][j].y, u[1][j].z, u[1][j].w};
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            const uint32_t v0 = b0[x] ^ 0x80808080u, v1 = b1[x] ^ 0x80808080u;
-            const uint32_t m[4] = {f16_of_bytes(v0, 0x4140u), f16_of_bytes(v1, 0x4140u), f16_of_bytes(v0, 0x4342u),
-                                   f16_of_bytes(v1, 0x4342u)};
-            mma_f16(c, m, qf[j][x][0], qf[j][x][1]);
-          }
+        for (int x = 0; x < 4; ++x) {
+          const uint32_t v0 = b0[x] ^ 0x80808080u, v1 = b1[x] ^ 0x80808080u;
+          const uint32_t m[4] = {f16_of_bytes(v0, 0x4140u), f16_of_bytes(v1, 0x4140u), f16_of_bytes(v0, 0x4342u),
+                                 f16_of_bytes(v1, 0x4342u)};
+          mma_f16(c, m, qf[j][x][0], qf[j][x][1]);
         }
       }
 #pragma unroll
       for (int y = 0; y < 2; ++y) {
         const int k = k0 + g + 8 * y;
-        const float f = power_of_two(max(static_cast<int>(byte[y]), 21) - 147);   // 2^(e - 20): every score is a float
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-          const int i = 2 * t + x, own = (p0 + i) >> a.page_shift;                // row, and its own block
-          if (i >= n_rows || k >= blocks) continue;
-          uint32_t key = byte[y] == 255u ? kNotFinite : ordered(c[2 * y + x] * f);
-          if (k < a.first || k > own - a.last) key = kForced;
-          if (k > own || at[y] < 0 || p0 + i < 0) key = 0;
-          if (kSingle && ranks > 1) {
-            const uint32_t to = mapa_shared(smem_u32(keys + k), 0);
-            asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(to), "r"(key) : "memory");
-          } else {
-            keys[i * a.places + k] = key;
-          }
+          const int i = 2 * t + x;                  // row
+          if (i < n_rows && k < blocks)
+            keys[i * a.places + k] = b.key(a, y, k, (p0 + i) >> a.page_shift, c[2 * y + x]);
         }
       }
     }
-    if (kSingle && ranks > 1) {
-      cluster_sync();
-      if (rank != 0) return;
-    } else {
-      __syncthreads();
+    __syncthreads();
+    if (warp < n_rows) {
+      const uint32_t* const mine = keys + warp * a.places;
+      int32_t* const out = a.blocks + (ra + warp) * a.row_stride + head * a.head_stride;
+      if (!pick_few(mine, blocks, a.top, out, kept[warp])) pick<32>(mine, blocks, a.top, out, sums);
     }
-    if constexpr (kSingle) {
-      if (!pick_some(keys, blocks, a.top, a.blocks + ra * a.row_stride + head * a.head_stride, sums, of_warps, kept[0]))
-        pick<kSelectThreads>(keys, blocks, a.top, a.blocks + ra * a.row_stride + head * a.head_stride, sums);
-      return;
-    } else {
-      if (warp < n_rows && !pick_few(keys + warp * a.places, blocks, a.top,
-                                     a.blocks + (ra + warp) * a.row_stride + head * a.head_stride, kept[warp]))
-        pick<32>(keys + warp * a.places, blocks, a.top, a.blocks + (ra + warp) * a.row_stride + head * a.head_stride,
-                 sums);
-      __syncthreads();
-    }
+    __syncthreads();
     ra += n_rows;
   }
+}
+
+// One row and K/V head, by a CTA or the CTAs of a cluster.  A row would leave seven eighths of an MMA empty: the
+// products are 16-bit weights times the bytes, two at a time.  Bound by latency (row -> sequence -> table -> bounds,
+// 3.6 us to the first score of 48 rows; then 2 us for every 128 blocks), so the first blocks' bounds are on their way while the query
+// is made, and three CTAs an SM count for more than loads a round ahead (17 us; 20 with the
+// next blocks' bounds in registers and two CTAs).  Two CTAs a row are slower where the rows fill
+// the SMs (21 us): what comes before the first score is done twice.
+template <int D>
+__global__ void __launch_bounds__(kSelectThreads, 3) cache_select_row_kernel(const __grid_constant__ SelectArgs a) {
+  constexpr int kSteps = 2 * D / 64;
+  extern __shared__ uint4 dynamic[];
+  uint32_t* const keys = reinterpret_cast<uint32_t*>(dynamic);
+  __shared__ __align__(16) int16_t w[2 * D];
+  __shared__ int sums[2][kSelectWarps];
+  __shared__ uint4 of_warps[kSelectWarps];
+  __shared__ uint2 listed[kListed];
+  grid_dep_launch();
+  grid_dep_wait();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+  const int rank = static_cast<int>(cluster_rank());
+  uint32_t ranks;
+  asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(ranks));
+  if (ranks > 1) cluster_arrive();
+  const int64_t tile = blockIdx.x / ranks, row = tile / a.kv_heads;
+  const int head = static_cast<int>(tile - row * a.kv_heads);
+  if (warp == kSelectWarps - 1)
+    shared_query<D>(a, a.q + row * a.q_stride + static_cast<int64_t>(head) * a.group * D, w, lane);
+  const int s = find_seq(a.b, static_cast<int>(row), lane);
+  const Seq q = s < 0 ? Seq{0, 0, 0} : load_seq(a.b, a.page_shift, s, a.status);
+  const bool mine = static_cast<unsigned>(row - q.row0) < static_cast<unsigned>(q.c);     // else of no sequence, or refused
+  const int p = q.kv - q.c + static_cast<int>(row - q.row0), own = p >> a.page_shift, blocks = mine ? max(own + 1, 0) : 0;
+  const int32_t* table = a.b.table + static_cast<int64_t>(max(s, 0)) * a.b.table_cols;
+  const int step = 16 * kSelectWarps * static_cast<int>(ranks);
+  int k0 = 16 * (warp * static_cast<int>(ranks) + rank);
+  BoundTile<D> b;
+  int32_t next[2];                                  // the pages of the blocks after them
+#pragma unroll
+  for (int y = 0; y < 2; ++y) {
+    b.at[y] = page_entry(table, k0 + g + 8 * y, blocks);
+    next[y] = page_entry(table, k0 + step + g + 8 * y, blocks);
+  }
+  if (k0 < blocks) b.load(a, head, t);
+  if (ranks > 1) cluster_wait();                    // the first CTA's shared memory is there
+  __syncthreads();
+  for (; k0 < blocks; k0 += step) {
+    int32_t ahead[2];
+#pragma unroll
+    for (int y = 0; y < 2; ++y) ahead[y] = page_entry(table, k0 + 2 * step + g + 8 * y, blocks);
+    int c[2] = {0, 0};
+#pragma unroll
+    for (int j = 0; j < kSteps; ++j) {
+      const uint4* from = reinterpret_cast<const uint4*>(w + 64 * j + 16 * t);
+      const uint4 w0 = from[0], w1 = from[1];
+      const uint32_t wx[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        const uint32_t v[4] = {b.u[y][j].x, b.u[y][j].y, b.u[y][j].z, b.u[y][j].w};
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          c[y] = __dp2a_lo(static_cast<int>(wx[2 * x]), static_cast<int>(v[x]), c[y]);
+          c[y] = __dp2a_hi(static_cast<int>(wx[2 * x + 1]), static_cast<int>(v[x]), c[y]);
+        }
+      }
+    }
+#pragma unroll
+    for (int y = 0; y < 2; ++y) {
+      c[y] += __shfl_xor_sync(0xFFFFFFFFu, c[y], 1);
+      c[y] += __shfl_xor_sync(0xFFFFFFFFu, c[y], 2);
+      const int k = k0 + g + 8 * y;
+      const uint32_t key = b.key(a, y, k, own, static_cast<float>(c[y]));
+      if (t != 0 || k >= blocks) continue;
+      if (ranks > 1) {
+        const uint32_t to = mapa_shared(smem_u32(keys + k), 0);
+        asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(to), "r"(key) : "memory");
+      } else {
+        keys[k] = key;
+      }
+    }
+    b.at[0] = next[0], b.at[1] = next[1];
+    if (k0 + step < blocks) b.load(a, head, t);
+    next[0] = ahead[0], next[1] = ahead[1];
+  }
+  if (ranks > 1)
+    cluster_sync();
+  else
+    __syncthreads();
+  if (rank != 0 || !mine) return;
+  int32_t* const out = a.blocks + row * a.row_stride + head * a.head_stride;
+  if (!pick_some(keys, blocks, a.top, out, sums, of_warps, listed)) pick<kSelectThreads>(keys, blocks, a.top, out, sums);
 }
 
 constexpr int kSelectKeyBytes = 200 * 1024;      // of shared memory, for scores
@@ -676,8 +735,8 @@ int ds_vit_cache_select(const ds_vit_cache* cache, const ds_vit_chunks* chunks, 
            2 * ranks * 16 * kSelectWarps <= chunks->table_cols)
       ranks *= 2;
   const int bytes = std::max(4 * a.tile_rows * a.places, 1024);
-  auto* fn = cache->head_dim == 128 ? (single ? cache_select_kernel<128, true> : cache_select_kernel<128, false>)
-                                    : (single ? cache_select_kernel<64, true> : cache_select_kernel<64, false>);
+  auto* fn = cache->head_dim == 128 ? (single ? cache_select_row_kernel<128> : cache_select_kernel<128>)
+                                    : (single ? cache_select_row_kernel<64> : cache_select_kernel<64>);
   if (allow_smem(reinterpret_cast<const void*>(fn), kSelectKeyBytes + 1024) != cudaSuccess) return DS_VIT_ECUDA;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>((rows + a.tile_rows - 1) / a.tile_rows * c.kv_heads * ranks));

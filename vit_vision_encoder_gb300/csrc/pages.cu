@@ -83,9 +83,6 @@ __device__ __forceinline__ T scan(Shared& sh, int turn, T v, T* total) {
   return x - v + (warp > 0 ? before : 0);
 }
 
-__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
-__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
-
 // Value v of this CTA (the same in its threads) to all CTAs' all[which]; they have it behind the
 // cluster's next barrier, which also orders what the CTAs wrote to memory.
 __device__ __forceinline__ void tell(Shared& sh, int which, int v) {

@@ -608,6 +608,10 @@ __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
 }
 
+// The two halves of it.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
+
 // Arrive on an mbarrier given by its cluster address (possibly the peer's),
 // with the default (CTA-scope release) semantics: it signals TMEM reads that
 // tcgen05.wait::ld and tcgen05.fence::before_thread_sync already ordered; a
