@@ -3,8 +3,8 @@
 //
 // Bounds: each completed page is read once, by one warp a K/V head; bound by memory.
 //
-// Selection: a CTA takes a K/V head of up to eight rows of one sequence.  The scores are
-// a product of the blocks' bounds [blocks, 2 D] with the rows' shared queries [2 D, 8]
+// Selection: a CTA takes a K/V head of up to sixteen rows of one sequence.  The scores are
+// a product of the blocks' bounds [blocks, 2 D] with the rows' shared queries [2 D, 16]
 // on warp MMAs, blocks in the place of M: both operands are small whole numbers, exact in
 // fp16 (|n| <= 1024, |H| <= 127), and so is every partial sum (< 2^24), so the list does not depend on
 // the order of anything.  The order of the 2 D terms is free, so a lane uses the 16 bytes
@@ -160,7 +160,7 @@ struct SelectArgs {
   int places;                // scores of a row in shared memory
 };
 
-constexpr int kSelectWarps = 8, kSelectThreads = 32 * kSelectWarps;
+constexpr int kSelectWarps = 8, kSelectThreads = 32 * kSelectWarps, kTileRows = 16;
 constexpr uint32_t kForced = 0xFFFFFFFFu, kNotFinite = 0xFFFFFFFEu;   // above every score's number; 0: not a candidate
 
 // A whole number that orders like the float (finite: under kNotFinite, over 0).
@@ -318,8 +318,8 @@ __device__ __forceinline__ uint32_t sorted_down(uint32_t x, int lane) {
 // The same by one warp where few blocks are looked for: the smallest of the `need` largest among the
 // lanes' own maxima is a lower bound of the threshold that hardly more keys than needed
 // reach; the rest happens among those, kept with their blocks in `kept`.  False, with nothing written,
-// where there are more than kKept of them or more than 32 are looked for.  (532 blocks, 16 of them: 83 us for 16 thousand lists,
-// 137 by the threshold's bits.)
+// where there are more than kKept of them or more than 32 are looked for.  (532 blocks, 16 of them: 83 us for 16
+// thousand lists, 137 by the threshold's bits, as measured when it was brought in.)
 constexpr int kKept = 64;
 __device__ __forceinline__ bool pick_few(const uint32_t* keys, int n, int top, int32_t* out, uint2* kept) {
   const int lane = threadIdx.x & 31;
@@ -484,13 +484,15 @@ __device__ __forceinline__ int32_t page_entry(const int32_t* table, int k, int b
   return k < blocks ? __ldg(table + k) : -1;
 }
 
-// Up to eight rows of one sequence at a time, for one K/V head.
+// Up to sixteen rows of one sequence at a time, for one K/V head.  Bound by instructions: half of them widen the bounds
+// for the MMAs (shared by the rows), half pick.  2048 rows of 8 heads over 532 blocks: 56 us; 63 with eight
+// rows; 86 with eight and their weights kept in registers, which leaves two CTAs an SM instead of four.
 template <int D>
-__global__ void __launch_bounds__(kSelectThreads) cache_select_kernel(const __grid_constant__ SelectArgs a) {
+__global__ void __launch_bounds__(kSelectThreads, 4) cache_select_kernel(const __grid_constant__ SelectArgs a) {
   constexpr int kSteps = 2 * D / 64;                // 16-byte pieces of a block that a lane has, four MMAs each
   extern __shared__ uint4 dynamic[];
   uint32_t* const keys = reinterpret_cast<uint32_t*>(dynamic);
-  __shared__ __align__(16) __half w[8][2 * D + 8];
+  __shared__ __align__(16) __half w[kTileRows][2 * D + 8];
   __shared__ int sums[2][kSelectWarps];
   __shared__ uint2 kept[kSelectWarps][kKept];
   grid_dep_launch();
@@ -510,20 +512,13 @@ __global__ void __launch_bounds__(kSelectThreads) cache_select_kernel(const __gr
     const int n_rows = static_cast<int>(min(r_end, static_cast<int64_t>(q.row0) + q.c) - ra);
     const int p0 = q.kv - q.c + static_cast<int>(ra - q.row0);                  // position of the first
     const int blocks = max(p0 + n_rows - 1 + (1 << a.page_shift), 0) >> a.page_shift;     // of the last
-    if (warp < n_rows)
-      shared_query<D>(a, a.q + (ra + warp) * a.q_stride + static_cast<int64_t>(head) * a.group * D, w[warp], lane);
-    __syncthreads();
-    uint32_t qf[kSteps][4][2];
-#pragma unroll
-    for (int j = 0; j < kSteps; ++j) {
-      // Row g's terms that go with the lane's piece of a block.
-      const uint32_t* from = reinterpret_cast<const uint32_t*>(&w[g][64 * j + 16 * t]);
-#pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        qf[j][x][0] = g < n_rows ? from[2 * x] : 0u;
-        qf[j][x][1] = g < n_rows ? from[2 * x + 1] : 0u;
-      }
+    for (int i = warp; i < kTileRows; i += kSelectWarps) {
+      if (i < n_rows)
+        shared_query<D>(a, a.q + (ra + i) * a.q_stride + static_cast<int64_t>(head) * a.group * D, w[i], lane);
+      else
+        for (int x = lane; x < 2 * D; x += 32) w[i][x] = __half(0.f);
     }
+    __syncthreads();
     const int32_t* table = a.b.table + static_cast<int64_t>(s) * a.b.table_cols;
     BoundTile<D> b;
     int32_t ahead[2];                               // the next blocks' pages
@@ -536,7 +531,7 @@ __global__ void __launch_bounds__(kSelectThreads) cache_select_kernel(const __gr
         ahead[y] = page_entry(table, k0 + 16 * kSelectWarps + g + 8 * y, blocks);
       }
       b.load(a, head, t);
-      float c[4] = {0.f, 0.f, 0.f, 0.f};
+      float c[2][4] = {};
 #pragma unroll
       for (int j = 0; j < kSteps; ++j) {
         const uint32_t b0[4] = {b.u[0][j].x, b.u[0][j].y, b.u[0][j].z, b.u[0][j].w};
@@ -546,24 +541,30 @@ __global__ void __launch_bounds__(kSelectThreads) cache_select_kernel(const __gr
           const uint32_t v0 = b0[x] ^ 0x80808080u, v1 = b1[x] ^ 0x80808080u;
           const uint32_t m[4] = {f16_of_bytes(v0, 0x4140u), f16_of_bytes(v1, 0x4140u), f16_of_bytes(v0, 0x4342u),
                                  f16_of_bytes(v1, 0x4342u)};
-          mma_f16(c, m, qf[j][x][0], qf[j][x][1]);
+          // Row g's terms that go with the lane's piece of a block, and row g + 8's.
+          const uint2 w0 = *reinterpret_cast<const uint2*>(&w[g][64 * j + 16 * t + 4 * x]);
+          mma_f16(c[0], m, w0.x, w0.y);
+          if (n_rows > 8) {
+            const uint2 w1 = *reinterpret_cast<const uint2*>(&w[g + 8][64 * j + 16 * t + 4 * x]);
+            mma_f16(c[1], m, w1.x, w1.y);
+          }
         }
       }
 #pragma unroll
       for (int y = 0; y < 2; ++y) {
         const int k = k0 + g + 8 * y;
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const int i = 2 * t + x;                  // row
+        for (int x = 0; x < 4; ++x) {
+          const int i = 2 * t + (x & 1) + 8 * (x >> 1);      // row
           if (i < n_rows && k < blocks)
-            keys[i * a.places + k] = b.key(a, y, k, (p0 + i) >> a.page_shift, c[2 * y + x]);
+            keys[i * a.places + k] = b.key(a, y, k, (p0 + i) >> a.page_shift, c[x >> 1][2 * y + (x & 1)]);
         }
       }
     }
     __syncthreads();
-    if (warp < n_rows) {
-      const uint32_t* const mine = keys + warp * a.places;
-      int32_t* const out = a.blocks + (ra + warp) * a.row_stride + head * a.head_stride;
+    for (int i = warp; i < n_rows; i += kSelectWarps) {
+      const uint32_t* const mine = keys + i * a.places;
+      int32_t* const out = a.blocks + (ra + i) * a.row_stride + head * a.head_stride;
       if (!pick_few(mine, blocks, a.top, out, kept[warp])) pick<32>(mine, blocks, a.top, out, sums);
     }
     __syncthreads();
@@ -728,7 +729,7 @@ int ds_vit_cache_select(const ds_vit_cache* cache, const ds_vit_chunks* chunks, 
   const bool single = chunks->max_rows < 8 || units <= 4 * static_cast<int64_t>(num_sms()) || 8 * a.places > kSelectKeyBytes;
   a.tile_rows = 1;
   if (!single)
-    for (a.tile_rows = 8; 4 * static_cast<int64_t>(a.tile_rows) * a.places > kSelectKeyBytes;) a.tile_rows /= 2;
+    for (a.tile_rows = kTileRows; 4 * static_cast<int64_t>(a.tile_rows) * a.places > kSelectKeyBytes;) a.tile_rows /= 2;
   int ranks = 1;
   if (single)
     while (ranks < 8 && 2 * ranks * units <= 2 * static_cast<int64_t>(num_sms()) &&
