@@ -48,6 +48,7 @@ struct BlockArgs {
   int top;
   int* status;
   int64_t items;
+  bool wide;                 // keys begin on 32-byte boundaries
   int warp_shift;            // warps of a CTA per item: 1 << warp_shift
 };
 
@@ -81,6 +82,13 @@ __device__ __forceinline__ float min_nan(float a, float b) {
   return r;
 }
 
+// 32 bytes by one load.
+__device__ __forceinline__ void ldg256(const uint4* from, uint4& a, uint4& b) {
+  asm("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+      : "=r"(a.x), "=r"(a.y), "=r"(a.z), "=r"(a.w), "=r"(b.x), "=r"(b.y), "=r"(b.z), "=r"(b.w)
+      : "l"(from));
+}
+
 // The two e4m3 values in the upper half of a register as fp16.
 __device__ __forceinline__ uint32_t e4m3x2_hi_to_f16x2(uint32_t four) {
   uint32_t r;
@@ -93,6 +101,8 @@ struct Frag {
   static constexpr int kK = E4M3 ? D / 64 : D / 32;      // 16-byte pieces of a key that a lane holds
   static constexpr int kV = D == 128 && !E4M3 ? 2 : 1;   // pieces of a value
   static constexpr int kM = D / 16;                      // row tiles of the output
+  // The first 16 bytes of a key are piece 0 of lane group member t = 0; pieces 2i and 2i + 1 of a lane lie side by side.
+  static __device__ __forceinline__ int piece(int t, int j) { return kK == 1 ? t : 8 * (j >> 1) + 2 * t + (j & 1); }
   // A dim of accumulator row tile m, rows g and g + 8, of lane group g.
   static __device__ __forceinline__ int dim(int g, int m, int half) {
     return kV == 2 ? 64 * half + 8 * g + m : (D / 8) * g + 2 * m + half;
@@ -150,7 +160,7 @@ __global__ void __launch_bounds__(kThreads, NT == 2 ? 2 : D == 128 ? 3 : 4) bloc
     if constexpr (!E4M3) {
 #pragma unroll
       for (int j = 0; j < kK; ++j) {
-        const uint4 u = on ? __ldg(from + 4 * j + t) : zero;
+        const uint4 u = on ? __ldg(from + F::piece(t, j)) : zero;
         qf[n][j][0] = u.x, qf[n][j][1] = u.y, qf[n][j][2] = u.z, qf[n][j][3] = u.w;
       }
     } else {
@@ -160,7 +170,7 @@ __global__ void __launch_bounds__(kThreads, NT == 2 ? 2 : D == 128 ? 3 : 4) bloc
       for (int j = 0; j < kK; ++j)
 #pragma unroll
         for (int y = 0; y < 2; ++y) {
-          u[j][y] = on ? __ldg(from + 8 * j + 2 * t + y) : zero;
+          u[j][y] = on ? __ldg(from + 2 * F::piece(t, j) + y) : zero;
           const uint32_t m = __vmaxu2(__vmaxu2(u[j][y].x & 0x7FFF7FFFu, u[j][y].y & 0x7FFF7FFFu),
                                       __vmaxu2(u[j][y].z & 0x7FFF7FFFu, u[j][y].w & 0x7FFF7FFFu));
           top = max(top, max(m & 0xFFFFu, m >> 16));
@@ -240,16 +250,21 @@ __global__ void __launch_bounds__(kThreads, NT == 2 ? 2 : D == 128 ? 3 : 4) bloc
   uint4 v[4][kV];                             // e4m3 at D 64: 8 bytes of each
   uint32_t kb[2], vb[2];                      // exponents of keys g, g + 8
   // Whole tiles, all but the last of a row's own block, are loaded without conditions.
-  const uint8_t* const k_lane = a.c.k + g * kRow + 16 * t;
+  const uint8_t* const k_lane = a.c.k + g * kRow + 16 * F::piece(t, 0);
   const uint8_t* const v_lane = a.c.v + 2 * t * kRow + (E4M3 && D == 64 ? 8 : 16) * g;
   auto load_k = [&](int64_t r0, int n) {
-    auto load = [&](auto on) {
+    auto load = [&](bool whole, auto on) {
       const uint8_t* const from = k_lane + r0 * kRow;
 #pragma unroll
       for (int y = 0; y < 2; ++y) {
+        const uint4* const at_y = reinterpret_cast<const uint4*>(from + 8 * y * kRow);
+        if (kK > 1 && whole && a.wide) {
 #pragma unroll
-        for (int j = 0; j < kK; ++j)
-          k[y][j] = on(g + 8 * y) ? __ldg(reinterpret_cast<const uint4*>(from + 8 * y * kRow) + 4 * j) : make_uint4(0, 0, 0, 0);
+          for (int j = 0; j + 1 < kK; j += 2) ldg256(at_y + 4 * j, k[y][j], k[y][j + 1]);
+        } else {
+#pragma unroll
+          for (int j = 0; j < kK; ++j) k[y][j] = on(g + 8 * y) ? __ldg(at_y + F::piece(0, j)) : make_uint4(0, 0, 0, 0);
+        }
         if constexpr (E4M3) {
           kb[y] = on(g + 8 * y) ? __ldg(a.c.k_exp + r0 + g + 8 * y) : 127u;
           vb[y] = on(g + 8 * y) ? __ldg(a.c.v_exp + r0 + g + 8 * y) : 127u;
@@ -257,9 +272,9 @@ __global__ void __launch_bounds__(kThreads, NT == 2 ? 2 : D == 128 ? 3 : 4) bloc
       }
     };
     if (n == 16)
-      load([](int) { return true; });
+      load(true, [](int) { return true; });
     else
-      load([n](int key) { return key < n; });
+      load(false, [n](int key) { return key < n; });
   };
   auto load_v = [&](int64_t r0, int n) {
     auto load = [&](auto on) {
@@ -601,6 +616,7 @@ extern "C" int ds_vit_cache_attention_blocks(const ds_vit_cache* cache, const ds
   a.head_stride = head_stride;
   a.top = top;
   a.status = reinterpret_cast<int*>(status);
+  a.wide = aligned(cache->k, 32);
   const bool e4m3 = cache->kind == DS_VIT_CACHE_E4M3;
   return cache->head_dim == 128 ? (e4m3 ? launch_blocks<128, true>(a, stream) : launch_blocks<128, false>(a, stream))
                                 : (e4m3 ? launch_blocks<64, true>(a, stream) : launch_blocks<64, false>(a, stream));
