@@ -246,12 +246,17 @@ __global__ void __launch_bounds__(kThreads, NT == 2 ? 2 : D == 128 ? 3 : 4) bloc
   };
 
   constexpr int kRow = E4M3 ? D : 2 * D;      // bytes of a key
+  // Rows g and g + 8 of the scores are keys key0 and key0 + 8, so that their rows 2t, 2t + 1, 8 + 2t and 9 + 2t are
+  // keys t, t + 4, t + 8 and t + 12: whose values lane group member t is given (below).
+  const int key0 = (g >> 1) + 4 * (g & 1);
   uint4 k[2][kK];
   uint4 v[4][kV];                             // e4m3 at D 64: 8 bytes of each
-  uint32_t kb[2], vb[2];                      // exponents of keys g, g + 8
+  uint32_t kb[2], vb[2];                      // exponents of keys key0, key0 + 8
   // Whole tiles, all but the last of a row's own block, are loaded without conditions.
-  const uint8_t* const k_lane = a.c.k + g * kRow + 16 * F::piece(t, 0);
-  const uint8_t* const v_lane = a.c.v + 2 * t * kRow + (E4M3 && D == 64 ? 8 : 16) * g;
+  const uint8_t* const k_lane = a.c.k + key0 * kRow + 16 * F::piece(t, 0);
+  // Values: eight lanes read a line of one key; what lane (g, t) needs of key 4y + t is with lane 8t + g.
+  const uint8_t* const v_lane = a.c.v + (lane >> 3) * kRow + (E4M3 && D == 64 ? 8 : 16) * (lane & 7);
+  const int v_from = 8 * t + g;
   auto load_k = [&](int64_t r0, int n) {
     auto load = [&](bool whole, auto on) {
       const uint8_t* const from = k_lane + r0 * kRow;
@@ -263,11 +268,11 @@ __global__ void __launch_bounds__(kThreads, NT == 2 ? 2 : D == 128 ? 3 : 4) bloc
           for (int j = 0; j + 1 < kK; j += 2) ldg256(at_y + 4 * j, k[y][j], k[y][j + 1]);
         } else {
 #pragma unroll
-          for (int j = 0; j < kK; ++j) k[y][j] = on(g + 8 * y) ? __ldg(at_y + F::piece(0, j)) : make_uint4(0, 0, 0, 0);
+          for (int j = 0; j < kK; ++j) k[y][j] = on(key0 + 8 * y) ? __ldg(at_y + F::piece(0, j)) : make_uint4(0, 0, 0, 0);
         }
         if constexpr (E4M3) {
-          kb[y] = on(g + 8 * y) ? __ldg(a.c.k_exp + r0 + g + 8 * y) : 127u;
-          vb[y] = on(g + 8 * y) ? __ldg(a.c.v_exp + r0 + g + 8 * y) : 127u;
+          kb[y] = on(key0 + 8 * y) ? __ldg(a.c.k_exp + r0 + key0 + 8 * y) : 127u;
+          vb[y] = on(key0 + 8 * y) ? __ldg(a.c.v_exp + r0 + key0 + 8 * y) : 127u;
         }
       }
     };
@@ -281,14 +286,14 @@ __global__ void __launch_bounds__(kThreads, NT == 2 ? 2 : D == 128 ? 3 : 4) bloc
       const uint8_t* const from = v_lane + r0 * kRow;
 #pragma unroll
       for (int y = 0; y < 4; ++y) {
-        const int key = (y & 1) + 8 * (y >> 1);
+        const bool here = on(4 * y + (lane >> 3));
         if constexpr (E4M3 && D == 64) {
-          const uint2 u = on(2 * t + key) ? __ldg(reinterpret_cast<const uint2*>(from + key * kRow)) : make_uint2(0, 0);
+          const uint2 u = here ? __ldg(reinterpret_cast<const uint2*>(from + 4 * y * kRow)) : make_uint2(0, 0);
           v[y][0] = make_uint4(u.x, u.y, 0, 0);
         } else {
 #pragma unroll
           for (int z = 0; z < kV; ++z)
-            v[y][z] = on(2 * t + key) ? __ldg(reinterpret_cast<const uint4*>(from + key * kRow) + 8 * z) : make_uint4(0, 0, 0, 0);
+            v[y][z] = here ? __ldg(reinterpret_cast<const uint4*>(from + 4 * y * kRow) + 8 * z) : make_uint4(0, 0, 0, 0);
         }
       }
     };
@@ -354,7 +359,7 @@ __global__ void __launch_bounds__(kThreads, NT == 2 ? 2 : D == 128 ? 3 : 4) bloc
     n_keys = next();
     if (n_keys > 0) load_k(row0, n_keys);
 
-    // Scores (log2) of keys g (0, 1) and g + 8 (2, 3), heads 2t and 2t + 1.
+    // Scores (log2) of keys key0 (0, 1) and key0 + 8 (2, 3), heads 2t and 2t + 1.
     bool raise = false;
 #pragma unroll
     for (int n = 0; n < NT; ++n)
@@ -362,7 +367,7 @@ __global__ void __launch_bounds__(kThreads, NT == 2 ? 2 : D == 128 ? 3 : 4) bloc
       for (int x = 0; x < 4; ++x) {
         // (0 times a factor past all floats stays 0, NaN stays.)
         float z = c[n][x] * (E4M3 ? min_nan(kf[x >> 1] * unit[n][x & 1], 3e38f) : a.scale_log2);
-        if (n_here < 16 && g + 8 * (x >> 1) >= n_here) z = -INFINITY;
+        if (n_here < 16 && key0 + 8 * (x >> 1) >= n_here) z = -INFINITY;
         c[n][x] = z;
         raise |= z > m[n][x & 1] + (E4M3 ? kLag8 : kLag16);
         if constexpr (E4M3) raise |= z + ve[x >> 1] > r[n][x & 1] + kLag8;
@@ -408,6 +413,17 @@ __global__ void __launch_bounds__(kThreads, NT == 2 ? 2 : D == 128 ? 3 : 4) bloc
       pf[n][0] = transposed(E4M3 ? pack_f16x2(w[0], w[1]) : pack_bf16x2(w[0], w[1]));
       pf[n][1] = transposed(E4M3 ? pack_f16x2(w[2], w[3]) : pack_bf16x2(w[2], w[3]));
     }
+#pragma unroll
+    for (int y = 0; y < 4; ++y)
+#pragma unroll
+      for (int z = 0; z < kV; ++z) {
+        v[y][z].x = __shfl_sync(0xFFFFFFFFu, v[y][z].x, v_from);
+        v[y][z].y = __shfl_sync(0xFFFFFFFFu, v[y][z].y, v_from);
+        if constexpr (!E4M3 || D != 64) {
+          v[y][z].z = __shfl_sync(0xFFFFFFFFu, v[y][z].z, v_from);
+          v[y][z].w = __shfl_sync(0xFFFFFFFFu, v[y][z].w, v_from);
+        }
+      }
 #pragma unroll
     for (int y = 0; y < kM; ++y) {
       uint32_t af[4];
