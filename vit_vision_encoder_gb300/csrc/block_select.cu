@@ -57,7 +57,7 @@ template <int D, bool E4M3>
 __global__ void __launch_bounds__(32 * kBoundWarps) cache_bounds_kernel(const __grid_constant__ BoundsArgs a) {
   constexpr int kPer = E4M3 ? 16 : 8;                       // values in 16 bytes
   constexpr int kLanes = D / kPer, kKeys = 32 / kLanes;     // lanes of a key, keys of a load
-  constexpr int kLoads = 16 / kKeys;                        // of 16 keys
+  constexpr int kLoads = 32 / kKeys;                        // of 32 keys, in flight together
   grid_dep_launch();
   grid_dep_wait();
   const int lane = threadIdx.x & 31, s = blockIdx.y;
@@ -72,16 +72,18 @@ __global__ void __launch_bounds__(32 * kBoundWarps) cache_bounds_kernel(const __
       float hi[kPer], lo[kPer];
 #pragma unroll
       for (int x = 0; x < kPer; ++x) hi[x] = -INFINITY, lo[x] = INFINITY;
-      for (int k0 = 0; k0 < page; k0 += 16) {
+      for (int k0 = 0; k0 < page; k0 += 32) {
         uint4 u[kLoads];
         uint32_t byte[kLoads];
 #pragma unroll
         for (int y = 0; y < kLoads; ++y) {
+          if (y * kKeys >= 16 && page == 16) break;
           u[y] = from[(k0 + y * kKeys) * kLanes];
           byte[y] = E4M3 ? a.c.k_exp[row0 + k0 + y * kKeys] : 0u;
         }
 #pragma unroll
         for (int y = 0; y < kLoads; ++y) {
+          if (y * kKeys >= 16 && page == 16) break;
           const uint32_t w[4] = {u[y].x, u[y].y, u[y].z, u[y].w};
 #pragma unroll
           for (int x = 0; x < 4; ++x) {
