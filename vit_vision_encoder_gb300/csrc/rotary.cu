@@ -5,8 +5,14 @@
 // the chain load -> norm -> store at one token a sequence.  D / 16 lanes hold one head, 16
 // values each: the 16-byte pieces l and l + D / 16 of the row, so that both loads
 // of a warp are whole lines and both members of every pair lie in one lane under either
-// pairing (the norm's sum is the only exchange between lanes).  A warp takes a row's
-// heads kBatch passes at a time, or a part of them where there are few rows.
+// pairing (the norm's sum is the only exchange between lanes).  A pass is the 512 / D heads that a
+// warp holds at a time; a warp takes up to kBatch passes of a row's queries or of its keys together, one pass where
+// there are few rows.  The norm's weights go into the row's sines and cosines once a batch:
+//   y_a = f (x_a [g_a cos] - x_b [g_b sin]),  y_b = f (x_b [g_b cos] + x_a [g_a sin]).
+// 8500 rows of 40 and 8 heads of 128: 36.5 us, 84% of the rate of a plain copy; batches of 4 passes 38.5, of 6 38.0 (as many as
+// the registers of four CTAs an SM hold), queries and keys mixed in a batch and the weights
+// multiplied into each head 41; the next batch's loads ahead of the work gained nothing.  48 rows 3.1 us, a
+// launch and three dependent trips to memory.
 //
 // Angles: positions are whole numbers, so the fraction of a turn is
 // pos * (freq / 2 pi) modulo 1 in 64-bit fixed point, exact but for the frequency's own
@@ -22,7 +28,8 @@ namespace dsvit {
 namespace {
 
 constexpr int kWarps = 4;
-constexpr int kBatch = 4;    // passes whose loads are in flight together
+constexpr int kBatch = 5;    // passes whose loads are in flight together
+constexpr int kWarpsPerSm = 16;
 
 struct RotaryArgs {
   ds_vit_rotary r;
@@ -34,7 +41,8 @@ struct RotaryArgs {
   const int32_t* pos;
   int64_t pos_stride;
   int64_t rows;
-  int parts;                 // warps a row's passes are dealt to
+  int batches[2];            // of a row's q, k: batch b has passes b, b + batches, ...
+  int64_t each;              // batches of a warp, one behind the other
   float eps;
 };
 
@@ -47,7 +55,7 @@ __device__ __forceinline__ int pair_of(int l, int j) {
 }
 
 template <int D, bool kAdjacent>
-__global__ void __launch_bounds__(32 * kWarps) qk_norm_rope_kernel(const __grid_constant__ RotaryArgs a) {
+__global__ void __launch_bounds__(32 * kWarps, kWarpsPerSm / kWarps) qk_norm_rope_kernel(const __grid_constant__ RotaryArgs a) {
   constexpr int kLanes = D / 16, kHeads = 32 / kLanes, kOwn = D / 64;
   grid_dep_launch();
   const int lane = threadIdx.x & 31, l = lane % kLanes, h0 = lane / kLanes;
@@ -59,96 +67,100 @@ __global__ void __launch_bounds__(32 * kWarps) qk_norm_rope_kernel(const __grid_
     axis[i] = a.r.axis[lane * kOwn + i];
   }
   grid_dep_wait();
-  const int total = a.heads[0] + a.heads[1], passes = (total + kHeads - 1) / kHeads;
-  uint4 g[2][2];
+  const int per_row = a.batches[0] + a.batches[1];
+  const int64_t begin = (static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5)) * a.each;
+  const int64_t end = min(begin + a.each, a.rows * per_row);
+  if (begin >= end) return;
+  int64_t row = begin / per_row;
+  int batch = static_cast<int>(begin - row * per_row);
+  bool turned = false;                  // whether c and s are the row's
+  float c[8], s[8];
+  for (int64_t u = begin; u < end; ++u) {
+    const int x = batch >= a.batches[0], first = x ? batch - a.batches[0] : batch;
+    const int heads = x ? a.heads[1] : a.heads[0], step = x ? a.batches[1] : a.batches[0];
+    const bf16* const from = (x ? a.x[1] + row * a.x_stride[1] : a.x[0] + row * a.x_stride[0]) + 8 * l;
+    bf16* const to = (x ? a.y[1] + row * a.y_stride[1] : a.y[0] + row * a.y_stride[0]) + 8 * l;
+    const bf16* const norm = x ? a.norm[1] : a.norm[0];
+    uint4 lo[kBatch], hi[kBatch];
 #pragma unroll
-  for (int x = 0; x < 2; ++x) {
-    g[x][0] = g[x][1] = make_uint4(0, 0, 0, 0);
-    if (a.norm[x] != nullptr) {
-      g[x][0] = __ldg(reinterpret_cast<const uint4*>(a.norm[x]) + l);
-      g[x][1] = __ldg(reinterpret_cast<const uint4*>(a.norm[x]) + l + kLanes);
+    for (int y = 0; y < kBatch; ++y) {
+      const int h = (first + y * step) * kHeads + h0;
+      lo[y] = hi[y] = make_uint4(0, 0, 0, 0);
+      if (h < heads) {
+        lo[y] = *reinterpret_cast<const uint4*>(from + h * D);
+        hi[y] = *reinterpret_cast<const uint4*>(from + h * D + D / 2);
+      }
     }
-  }
-  const int64_t units = a.rows * a.parts, step = static_cast<int64_t>(gridDim.x) * kWarps;
-  for (int64_t u = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5); u < units; u += step) {
-    const int64_t row = u / a.parts;
-    const int part = static_cast<int>(u - row * a.parts);
-    int32_t at[kOwn];
+    uint4 g[2] = {make_uint4(0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u),      // ones
+                  make_uint4(0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u)};
+    if (norm != nullptr) {
+      g[0] = __ldg(reinterpret_cast<const uint4*>(norm) + l);
+      g[1] = __ldg(reinterpret_cast<const uint4*>(norm) + l + kLanes);
+    }
+    if (!turned) {
+      float co[kOwn], so[kOwn];
 #pragma unroll
-    for (int i = 0; i < kOwn; ++i) at[i] = __ldg(a.pos + axis[i] * a.pos_stride + row);
-    float c[8], s[8];
-    for (int p0 = part; p0 < passes; p0 += kBatch * a.parts) {
-      uint4 lo[kBatch], hi[kBatch];
-#pragma unroll
-      for (int y = 0; y < kBatch; ++y) {
-        const int h = (p0 + y * a.parts) * kHeads + h0;
-        if (h < total) {
-          const int x = h >= a.heads[0];
-          const uint4* from =
-              reinterpret_cast<const uint4*>(a.x[x] + row * a.x_stride[x] + (x ? h - a.heads[0] : h) * D) + l;
-          lo[y] = from[0];
-          hi[y] = from[kLanes];
-        } else {
-          lo[y] = hi[y] = make_uint4(0, 0, 0, 0);
-        }
-      }
-      if (p0 == part) {
-        float co[kOwn], so[kOwn];
-#pragma unroll
-        for (int i = 0; i < kOwn; ++i) {
-          const uint64_t t = static_cast<uint64_t>(static_cast<int64_t>(at[i])) * turn[i];
-          sincospif(static_cast<float>(static_cast<int32_t>(t >> 32)) * 0x1p-31f, &so[i], &co[i]);
-        }
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const int p = pair_of<D, kAdjacent>(l, j), i = kOwn == 2 ? j & 1 : 0;
-          c[j] = __shfl_sync(0xFFFFFFFFu, co[i], p / kOwn);
-          s[j] = __shfl_sync(0xFFFFFFFFu, so[i], p / kOwn);
-        }
+      for (int i = 0; i < kOwn; ++i) {
+        const int32_t at = __ldg(a.pos + axis[i] * a.pos_stride + row);
+        const uint64_t t = static_cast<uint64_t>(static_cast<int64_t>(at)) * turn[i];
+        sincospif(static_cast<float>(static_cast<int32_t>(t >> 32)) * 0x1p-31f, &so[i], &co[i]);
       }
 #pragma unroll
-      for (int y = 0; y < kBatch; ++y) {
-        const int h = (p0 + y * a.parts) * kHeads + h0;
-        if ((p0 + y * a.parts) >= passes) break;
-        const int x = h >= a.heads[0];
-        float v[16];
-        const uint32_t w[8] = {lo[y].x, lo[y].y, lo[y].z, lo[y].w, hi[y].x, hi[y].y, hi[y].z, hi[y].w};
-        float sum = 0.f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          v[2 * i] = bf16lo(w[i]);
-          v[2 * i + 1] = bf16hi(w[i]);
-          sum = fmaf(v[2 * i], v[2 * i], sum);
-          sum = fmaf(v[2 * i + 1], v[2 * i + 1], sum);
-        }
-#pragma unroll
-        for (int o = kLanes / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-        if (a.norm[x] != nullptr) {
-          const float f = rsqrtf(sum * (1.f / D) + a.eps);
-          const uint4 g0 = x ? g[1][0] : g[0][0], g1 = x ? g[1][1] : g[0][1];
-          const uint32_t gw[8] = {g0.x, g0.y, g0.z, g0.w, g1.x, g1.y, g1.z, g1.w};
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            v[2 * i] *= f * bf16lo(gw[i]);
-            v[2 * i + 1] *= f * bf16hi(gw[i]);
-          }
-        }
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          // Pair j's members among the lane's values: (j, j + 8), or (2j, 2j + 1).
-          const int m0 = kAdjacent ? 2 * j : j, m1 = kAdjacent ? 2 * j + 1 : j + 8;
-          const float v0 = v[m0], v1 = v[m1];
-          v[m0] = v0 * c[j] - v1 * s[j];
-          v[m1] = v1 * c[j] + v0 * s[j];
-        }
-        if (h < total) {
-          uint4* to = reinterpret_cast<uint4*>(a.y[x] + row * a.y_stride[x] + (x ? h - a.heads[0] : h) * D) + l;
-          to[0] = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
-                             pack_bf16x2(v[6], v[7]));
-          to[kLanes] = make_uint4(pack_bf16x2(v[8], v[9]), pack_bf16x2(v[10], v[11]), pack_bf16x2(v[12], v[13]),
-                                  pack_bf16x2(v[14], v[15]));
-        }
+      for (int j = 0; j < 8; ++j) {
+        const int p = pair_of<D, kAdjacent>(l, j), i = kOwn == 2 ? j & 1 : 0;
+        c[j] = __shfl_sync(0xFFFFFFFFu, co[i], p / kOwn);
+        s[j] = __shfl_sync(0xFFFFFFFFu, so[i], p / kOwn);
       }
+    }
+    const uint32_t gw[8] = {g[0].x, g[0].y, g[0].z, g[0].w, g[1].x, g[1].y, g[1].z, g[1].w};
+    float gc[16], gs[16];                // of each value: g times the pair's cosine, sine
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const int j = kAdjacent ? i / 2 : i & 7;
+      const float gi = i & 1 ? bf16hi(gw[i / 2]) : bf16lo(gw[i / 2]);
+      gc[i] = gi * c[j];
+      gs[i] = gi * s[j];
+    }
+#pragma unroll
+    for (int y = 0; y < kBatch; ++y) {
+      if ((first + y * step) * kHeads >= heads) break;
+      const int h = (first + y * step) * kHeads + h0;
+      const uint32_t w[8] = {lo[y].x, lo[y].y, lo[y].z, lo[y].w, hi[y].x, hi[y].y, hi[y].z, hi[y].w};
+      float v[16], f = 1.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        v[2 * i] = bf16lo(w[i]);
+        v[2 * i + 1] = bf16hi(w[i]);
+      }
+      if (norm != nullptr) {
+        float sum[2] = {0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < 16; ++i) sum[i & 1] = fmaf(v[i], v[i], sum[i & 1]);
+        float all = sum[0] + sum[1];
+#pragma unroll
+        for (int o = kLanes / 2; o > 0; o >>= 1) all += __shfl_xor_sync(0xFFFFFFFFu, all, o);
+        f = rsqrtf(all * (1.f / D) + a.eps);
+      }
+      float r[16];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        // Pair j's members among the lane's values: (j, j + 8), or (2j, 2j + 1).
+        const int m0 = kAdjacent ? 2 * j : j, m1 = kAdjacent ? 2 * j + 1 : j + 8;
+        r[m0] = (v[m0] * gc[m0] - v[m1] * gs[m1]) * f;
+        r[m1] = (v[m1] * gc[m1] + v[m0] * gs[m0]) * f;
+      }
+      if (h < heads) {
+        *reinterpret_cast<uint4*>(to + h * D) =
+            make_uint4(pack_bf16x2(r[0], r[1]), pack_bf16x2(r[2], r[3]), pack_bf16x2(r[4], r[5]), pack_bf16x2(r[6], r[7]));
+        *reinterpret_cast<uint4*>(to + h * D + D / 2) = make_uint4(pack_bf16x2(r[8], r[9]), pack_bf16x2(r[10], r[11]),
+                                                                   pack_bf16x2(r[12], r[13]), pack_bf16x2(r[14], r[15]));
+      }
+    }
+    turned = true;
+    if (++batch == per_row) {
+      batch = 0;
+      ++row;
+      turned = false;
     }
   }
 }
@@ -229,11 +241,20 @@ int ds_vit_qk_norm_rope(const ds_vit_rotary* rotary, const void* q, int64_t q_st
   a.rows = rows;
   a.eps = eps;
   // Few rows: a pass a warp, as long as that is no more warps than run at once.
-  const int passes = (heads + kv_heads + 512 / d - 1) / (512 / d);
-  const int64_t warps = 32 * static_cast<int64_t>(num_sms());
-  a.parts = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(passes, warps / rows)));
-  const int64_t units = rows * a.parts;
-  const unsigned blocks = static_cast<unsigned>(std::min((units + kWarps - 1) / kWarps, warps / kWarps));
+  const int64_t warps = kWarpsPerSm * static_cast<int64_t>(num_sms());
+  int per_batch = kBatch, per_row;
+  for (;; --per_batch) {
+    per_row = 0;
+    for (int x = 0; x < 2; ++x) {
+      const int passes = (a.heads[x] + 512 / d - 1) / (512 / d);
+      a.batches[x] = (passes + per_batch - 1) / per_batch;
+      per_row += a.batches[x];
+    }
+    if (per_batch == 1 || 2 * rows * per_row > warps) break;
+  }
+  const int64_t batches = rows * per_row;
+  a.each = (batches + warps - 1) / warps;
+  const unsigned blocks = static_cast<unsigned>(((batches + a.each - 1) / a.each + kWarps - 1) / kWarps);
   const bool adj = rotary->pairing == DS_VIT_ROPE_ADJACENT;
   auto* fn = d == 128 ? (adj ? qk_norm_rope_kernel<128, true> : qk_norm_rope_kernel<128, false>)
                       : (adj ? qk_norm_rope_kernel<64, true> : qk_norm_rope_kernel<64, false>);
