@@ -84,3 +84,23 @@ def test_attention_refused(dv):
                dict(top=-1), dict(top=4097)):
         assert _attend(dv, ca, ch, **kw) == dv.EINVAL, kw
     assert _attend(dv, ca, ch, rows=2 ** 28) == dv.ERANGE                       # 8 heads
+
+
+def test_binding_refuses(dv):
+    """Tensors that the binding can tell are wrong (none of them on a GPU: nothing is called)."""
+    torch = pytest.importorskip("torch")
+    z = lambda s, t=torch.bfloat16: torch.zeros(s, dtype=t)   # noqa: E731
+    i32 = lambda *s: torch.zeros(s, dtype=torch.int32)        # noqa: E731
+    cache = dv.KvCache(z((3, 2, 16, 64)), z((3, 2, 16, 64)))
+    chunks = dv.Chunks(i32(2), i32(1), i32(1, 3), 1)
+    bounds = dv.KeyBounds.empty(cache)
+    for call in (lambda: dv.cache_bounds(cache, chunks, bounds, 1), lambda: dv.cache_select(cache, chunks, bounds, z((1, 4, 64)), 2),
+                 lambda: dv.cache_attention_blocks(cache, chunks, z((1, 4, 64)), i32(1, 2, 2))):
+        with pytest.raises(dv.DsVitError):
+            call()
+    lists = dv._block_lists
+    assert lists(i32(5, 2, 7), 5, 2, -1, "") == (7, 14, 7)
+    assert lists(i32(2, 5, 9).transpose(0, 1)[..., 1:8], 5, 2, -1, "") == (7, 9, 45)
+    for t in (i32(5, 2, 7).long(), i32(5, 3, 7), i32(4, 2, 7), i32(5, 2), i32(5, 7, 2).transpose(1, 2)):
+        with pytest.raises(dv.DsVitError):
+            lists(t, 5, 2, -1, "")

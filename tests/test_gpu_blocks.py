@@ -603,6 +603,44 @@ def test_lists_laid_out_otherwise(dv):
         dv.cache_attention_blocks(st.cache, st.chunks, q, blocks.transpose(1, 2).contiguous().transpose(1, 2))
 
 
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+def test_a_cache_past_32_bits(dv, kind):
+    """Pages whose bytes, and whose values, lie past 2^32: the same as at the front of the cache."""
+    heads, page, dim, used = 8, 64, 128, 9
+    n = 34000 if kind == "bf16" else 67000
+    cache = dv.KvCache.empty(n, heads, page, dim, dv.CACHE_BF16 if kind == "bf16" else dv.CACHE_E4M3)
+    assert cache.k.numel() * cache.k.element_size() > 2 ** 32
+    for t in (cache.k, cache.v):
+        if kind == "bf16":
+            t[:used].copy_(torch.randn(t[:used].shape, device="cuda"))
+        else:
+            t[:used].copy_(torch.randint(0, 120, t[:used].shape, device="cuda"))
+    if kind == "e4m3":
+        for e in (cache.k_exp, cache.v_exp):
+            e[:used].copy_(torch.randint(118, 124, e[:used].shape, device="cuda"))
+    copies = dv.PageCopies(used)
+    copies.src.copy_(torch.arange(used))
+    copies.dst.copy_(torch.arange(n - used, n))
+    copies.count.fill_(used)
+    bounds = dv.KeyBounds.empty(cache)
+    q = torch.randn((40, 40, dim), device="cuda").bfloat16()
+    got = []
+    for rows, kv in ((1, used * page), (40, used * page - 5)):
+        for first in (0, n - used):
+            table = torch.arange(first, first + used, device="cuda").int()[None].contiguous()
+            ch = dv.Chunks(torch.tensor([0, rows]).int().cuda(), torch.tensor([kv]).int().cuda(), table, rows)
+            whole = dv.Chunks(torch.tensor([0, kv]).int().cuda(), torch.tensor([kv]).int().cuda(), table, kv)
+            status = dv.cache_copy(cache, copies)
+            dv.cache_bounds(cache, whole, bounds, kv, status)
+            blocks, _ = dv.cache_select(cache, ch, bounds, q[:rows], 5, 1, 1, status=status)
+            out, _ = dv.cache_attention_blocks(cache, ch, q[:rows], blocks, status=status)
+            torch.cuda.synchronize()
+            assert int(status.item()) == dv.OK
+            got.append((blocks, out))
+        assert torch.equal(got[-1][0], got[-2][0]) and torch.equal(got[-1][1], got[-2][1])
+        assert torch.isfinite(got[-1][1]).all() and (got[-1][1] != 0).any()
+
+
 def test_no_rows(dv):
     st = make(dv, [1], [20], 2, 64, 16, "bf16")
     q = torch.zeros((0, 4, 64), dtype=torch.bfloat16, device="cuda")

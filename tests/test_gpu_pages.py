@@ -357,6 +357,38 @@ def test_captured_calls(dv):
         b.check()
 
 
+def test_calls_behind_one_another(dv):
+    """Nothing is looked at between the calls, which start while the ones before them end."""
+    r = random.Random(11)
+    b = Both(dv, 300, 16, 40, 30)
+    todo = []
+    for turn in range(60):
+        kids = list(range(10 + turn % 20, 20 + turn % 20))
+        n = [r.randint(1, 400) for _ in range(3)]
+        todo.append((b.i32([0, 1, 2] + kids), b.i32(n + [0] * 10), b.i32([r.randrange(3) for _ in kids]), b.i32(kids)))
+    for slots, lens, src, dst in todo:
+        dv.pages_resize(b.pool, b.tables, slots, lens, b.copies, b.status)
+        dv.pages_fork(b.pool, b.tables, src, dst, b.copies, b.status)
+        dv.pages_compact(b.pool, b.tables, b.copies, b.status)
+    bad = False
+    for slots, lens, src, dst in todo:
+        bad |= not b.m.resize(slots.tolist(), lens.tolist(), 300)
+        bad |= not b.m.fork(src.tolist(), dst.tolist(), 300)
+        b.m.compact(300)
+    b.check(dv.ECAP if bad else dv.OK)
+
+
+def test_as_many_slots_as_there_may_be(dv):
+    n = dv.MAX_SLOTS
+    b = Both(dv, 100, 128, n, 3)
+    b.resize([n - 1, 0, n - 32, 31], [300, 5, 129, 256])
+    b.fork([n - 1, n - 32], [n - 2, n - 31])
+    b.resize([n - 1], [0])
+    b.compact()
+    with pytest.raises(dv.DsVitError):
+        dv.pages_compact(b.pool, dv.PageTables.empty(n + 1, 3), b.copies)
+
+
 # ------------------------------------------------------------------ contents
 
 def pages(dv, kind, n, heads, page, dim, seed=0):

@@ -21,7 +21,7 @@ TOK_START, TOK_IMAGE, TOK_NEWLINE, TOK_END = 0, 1, 2, 3
 CACHE_BF16, CACHE_E4M3 = 0, 1
 ROPE_HALF_VECTOR, ROPE_ADJACENT = 1, 2
 EPI_BIAS, EPI_BIAS_GELU, EPI_BIAS_RESID, EPI_QKV_ROPE, EPI_SWIGLU = 0, 1, 2, 3, 4
-SELECT_MAX_COLS, SELECT_MAX_TOP = 49152, 4096
+MAX_SLOTS, SELECT_MAX_COLS, SELECT_MAX_TOP = 65536, 49152, 4096
 MAX_LAYERS, MAX_IMAGES, MAX_PATCHES, MAX_TOKENS = 32, 64, 9216, 1024
 NOALLOC_MAX_PATCHES, NOALLOC_SCRATCH_BYTES = 1024, 21 * 1024 * 1024
 
