@@ -573,7 +573,7 @@ int launch_blocks(BlockArgs a, void* stream) {
   a.head_tiles = (a.group + 8 * nt - 1) / (8 * nt);
   a.items = static_cast<int64_t>(a.b.rows) * a.c.kv_heads * a.head_tiles;
   // Warps that share an item: as many as fill the SMs with twelve each, of two tiles at least.
-  const int64_t room = 12 * static_cast<int64_t>(num_sms());
+  const int64_t room = (nt == 2 ? 24 : 12) * static_cast<int64_t>(num_sms());
   const int tiles = a.top << (a.c.page_shift - 4);
   int sharers = 1;
   while (sharers < 8 * kWarps && 2 * sharers * a.items <= room && 4 * sharers <= tiles) sharers *= 2;
