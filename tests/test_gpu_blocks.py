@@ -189,6 +189,14 @@ SELECT = [
     ([30], [25], 2, 64, 16, 4, 3, 1, 1),                              # front padding
     ([1], [9000], 2, 64, 16, 8, 300, 5, 9),
     ([1, 1], [20000, 19000], 1, 64, 16, 5, 33, 1, 1),                 # more than a thousand blocks
+    ([260], [3000], 4, 64, 16, 4, 40, 1, 2),                          # many rows: more than 32 of 187, more than 128, ...
+    ([260], [3000], 4, 64, 16, 4, 128, 1, 2),
+    ([260], [3000], 4, 64, 16, 4, 150, 0, 1),
+    ([260], [3000], 4, 64, 16, 4, 20, 9, 11),                         # ... nothing but forced ones
+    ([300], [9000], 3, 64, 16, 3, 100, 1, 2),                         # 562 blocks
+    ([1], [9000], 2, 64, 16, 8, 100, 60, 40),                         # one row: nothing but forced ones
+    ([1], [9000], 2, 64, 16, 8, 256, 1, 1),
+    ([1], [9000], 2, 64, 16, 8, 257, 1, 1),
 ]
 
 
@@ -213,6 +221,16 @@ def test_select_ties_go_to_the_lowest_block(dv):
         st.bounds.exp.copy_(torch.from_numpy(st.exp))
         check_select(dv, st, 8, 6, 1, 1)
         check_select(dv, st, 8, 20, 0, 1, q=torch.zeros((st.rows, 8, 64), dtype=torch.bfloat16, device="cuda"))
+    for q, kv in (([1], [9000]), ([200], [5000])):      # more of a kind than the lists in between hold
+        st = make(dv, q, kv, 4, 64, 16, "bf16")
+        for few in (0, 3):
+            st.exp[:], st.hi_lo[:] = 120, 5
+            if few:
+                st.hi_lo[::few] = 6
+            st.bounds.hi_lo.copy_(torch.from_numpy(st.hi_lo))
+            st.bounds.exp.copy_(torch.from_numpy(st.exp))
+            for top in (6, 33, 70, 130, 300):
+                check_select(dv, st, 8, top, 2, 2)
 
 
 def test_select_over_extremes(dv):

@@ -226,12 +226,21 @@ __device__ __forceinline__ void shared_query(const SelectArgs& a, const bf16* q,
   }
 }
 
-// The list of one row from its keys, by `kThreads` threads (a warp or the CTA).
+// The list of one row from its n keys, by `kThreads` threads (a warp or the CTA); up to the next multiple
+// of four the places behind them hold 0.  The threshold is known to be in [lo, hi]: at least `top` keys >= lo, fewer > hi,
+// unless there are no more candidates than that.
 template <int kThreads>
-__device__ __forceinline__ void pick(const uint32_t* keys, int n, int top, int32_t* out, int (*sums)[kSelectWarps]) {
+__device__ __forceinline__ void pick(const uint32_t* keys, int n, int top, int32_t* out, int (*sums)[kSelectWarps],
+                                     uint32_t lo, uint32_t hi) {
   const int tid = threadIdx.x & (kThreads - 1), lane = threadIdx.x & 31, warp = tid >> 5;
   int turn = 0;
-  auto total = [&](int x) {             // over the group
+  auto count = [&](uint32_t from) {     // keys >= from
+    int x = 0;
+#pragma unroll 2
+    for (int i = 4 * tid; i < n; i += 4 * kThreads) {
+      const uint4 k = *reinterpret_cast<const uint4*>(keys + i);
+      x += (k.x >= from) + (k.y >= from) + (k.z >= from) + (k.w >= from);
+    }
     x = __reduce_add_sync(0xFFFFFFFFu, x);
     if constexpr (kThreads > 32) {
       if (lane == 0) sums[turn][warp] = x;
@@ -243,26 +252,22 @@ __device__ __forceinline__ void pick(const uint32_t* keys, int n, int top, int32
     }
     return x;
   };
-  auto count = [&](uint32_t from) {     // keys >= from
-    int x = 0;
-#pragma unroll 4
-    for (int i = tid; i < n; i += kThreads) x += keys[i] >= from;
-    return total(x);
-  };
-  // The threshold: all keys over it are taken, and the first `ties` of those equal to it.
+  // All keys over the threshold are taken, and the first `ties` of those equal to it.
   uint32_t over = 0;
   int ties = 0;
   if (count(1) > top) {
-    uint32_t t = 0;                     // the largest with at least `top` keys >= t, built from the top bit
     bool fits = false;
-    for (int bit = 31; bit >= 0 && !fits; --bit) {
-      const uint32_t to = t | 1u << bit;
-      const int x = count(to);
-      if (x >= top) t = to;
+    while (!fits && lo < hi) {
+      const uint32_t mid = lo + (hi - lo + 1) / 2;
+      const int x = count(mid);
+      if (x >= top)
+        lo = mid;
+      else
+        hi = mid - 1;
       fits = x == top;
     }
-    over = fits ? t - 1 : t;
-    ties = fits ? 0 : top - (t == kForced ? 0 : count(t + 1));
+    over = fits ? lo - 1 : lo;
+    ties = fits ? 0 : top - (lo == kForced ? 0 : count(lo + 1));
   }
   const auto lower = (1u << lane) - 1;
   // Each warp of the group has a run of blocks; what the warps before it take comes first.
@@ -317,67 +322,105 @@ __device__ __forceinline__ uint32_t sorted_down(uint32_t x, int lane) {
   return x;
 }
 
-// The same by one warp where few blocks are looked for: the smallest of the `need` largest among the
-// lanes' own maxima is a lower bound of the threshold that hardly more keys than needed
-// reach; the rest happens among those, kept with their blocks in `kept`.  False, with nothing written,
-// where there are more than kKept of them or more than 32 are looked for.  (532 blocks, 16 of them: 83 us for 16
-// thousand lists, 137 by the threshold's bits, as measured when it was brought in.)
-constexpr int kKept = 64;
-__device__ __forceinline__ bool pick_few(const uint32_t* keys, int n, int top, int32_t* out, uint2* kept) {
+// The same by one warp where few blocks of many are looked for.  Each lane finds its own kTop-th largest key; the
+// (need / kTop)-th largest of those is a bound that at least `need` keys reach and not many more do.  Those are listed,
+// and held by the lanes, a few each, while the threshold is searched.  False, with nothing written, where more than that
+// reach it, with what is known of the threshold.  (532 blocks, 16 of them, as measured when it was brought in: 83 us for 16 thousand
+// lists, 137 by counting all keys; 3750 blocks, 128 of them, 8 thousand lists: 725
+// by counting all keys, 411.)
+constexpr int kHeldMost = 8;
+__host__ __device__ constexpr int held_by_lane(int top) { return top <= 32 ? 2 : kHeldMost; }
+template <int kTop>
+__device__ __forceinline__ bool pick_few(const uint32_t* keys, int n, int top, int32_t* out, uint2* kept, uint32_t& lo,
+                                         uint32_t& hi) {
+  constexpr int kHeld = held_by_lane(32 * kTop), kKept = 32 * kHeld;
   const int lane = threadIdx.x & 31;
-  uint32_t most = 0;                    // largest key of the lane's that is not forced
+  uint32_t most[kTop] = {};             // the lane's largest keys that are not forced, largest first
   int forced = 0, some = 0;
 #pragma unroll 4
   for (int i = lane; i < n; i += 32) {
     const uint32_t k = keys[i];
     forced += k == kForced;
     some += k != 0;
-    most = max(most, k == kForced ? 0u : k);
+    uint32_t x = k == kForced ? 0u : k;
+#pragma unroll
+    for (int y = 0; y < kTop; ++y) {
+      const uint32_t up = max(most[y], x);
+      x = min(most[y], x);
+      most[y] = up;
+    }
   }
-  const int both = __reduce_add_sync(0xFFFFFFFFu, forced << 16 | some);
-  forced = both >> 16;
+  forced = __reduce_add_sync(0xFFFFFFFFu, forced);
+  some = __reduce_add_sync(0xFFFFFFFFu, some);
   const int need = top - forced;
-  if ((both & 0xFFFF) <= top || need > 32) return false;
-  uint32_t bound = kForced;
+  if (some <= top || need > 32 * kTop) {
+    lo = 1;
+    hi = kForced;
+    return false;
+  }
+  lo = hi = kForced;
   if (need > 0) {
-    bound = max(__shfl_sync(0xFFFFFFFFu, sorted_down(most, lane), need - 1), 1u);
+    lo = max(__shfl_sync(0xFFFFFFFFu, sorted_down(most[kTop - 1], lane), (need + kTop - 1) / kTop - 1), 1u);
+    hi = __reduce_max_sync(0xFFFFFFFFu, most[0]);
   }
   const auto lower = (1u << lane) - 1;
   int n_kept = 0;
   for (int i0 = 0; i0 < n; i0 += 32) {
     const uint32_t k = i0 + lane < n ? keys[i0 + lane] : 0u;
-    const uint32_t all = __ballot_sync(0xFFFFFFFFu, k >= bound);
+    const uint32_t all = __ballot_sync(0xFFFFFFFFu, k >= lo);
     if (all == 0) continue;
     const int to = n_kept + __popc(all & lower);
     n_kept += __popc(all);
     if (n_kept > kKept) return false;
-    if (k >= bound) kept[to] = make_uint2(k, static_cast<uint32_t>(i0 + lane));
+    if (k >= lo) kept[to] = make_uint2(k, static_cast<uint32_t>(i0 + lane));
   }
   __syncwarp();
-  const uint2 none = make_uint2(0, 0);
-  const uint2 c0 = lane < n_kept ? kept[lane] : none, c1 = lane + 32 < n_kept ? kept[lane + 32] : none;
-  // How many of the kept come before each: larger ones, and equal ones of lower blocks.
-  int before0 = 0, before1 = 0;
-  for (int y = 0; y < n_kept; ++y) {
-    const uint32_t k = kept[y].x;
-    before0 += k > c0.x || (k == c0.x && y < lane);
-    before1 += k > c1.x || (k == c1.x && y < lane + 32);
+  uint32_t held[kHeld];
+#pragma unroll
+  for (int y = 0; y < kHeld; ++y) held[y] = 32 * y + lane < n_kept ? kept[32 * y + lane].x : 0u;
+  auto count = [&](uint32_t from) {
+    int x = 0;
+#pragma unroll
+    for (int y = 0; y < kHeld; ++y)
+      if (32 * y < n_kept) x += held[y] >= from;
+    return static_cast<int>(__reduce_add_sync(0xFFFFFFFFu, x));
+  };
+  // The threshold is in [lo, hi]: at least `top` keys >= lo, fewer > hi.
+  bool fits = n_kept == top;
+  while (!fits && lo < hi) {
+    const uint32_t mid = lo + (hi - lo + 1) / 2;
+    const int x = count(mid);
+    if (x >= top)
+      lo = mid;
+    else
+      hi = mid - 1;
+    fits = x == top;
   }
-  const bool on0 = lane < n_kept && before0 < top, on1 = lane + 32 < n_kept && before1 < top;
-  const uint32_t all0 = __ballot_sync(0xFFFFFFFFu, on0), all1 = __ballot_sync(0xFFFFFFFFu, on1);
-  if (on0) out[__popc(all0 & lower)] = static_cast<int32_t>(c0.y);
-  if (on1) out[__popc(all0) + __popc(all1 & lower)] = static_cast<int32_t>(c1.y);
+  const int ties = fits || lo == kForced ? top : top - count(lo + 1);       // of the keys equal to lo, in order
+  int taken = 0, same = 0;
+#pragma unroll
+  for (int y = 0; y < kHeld; ++y) {
+    if (32 * y >= n_kept) break;
+    const uint32_t equal = __ballot_sync(0xFFFFFFFFu, held[y] == lo);
+    const bool on = held[y] > lo || (held[y] == lo && same + __popc(equal & lower) < ties);
+    const uint32_t all = __ballot_sync(0xFFFFFFFFu, on);
+    if (on) out[taken + __popc(all & lower)] = static_cast<int32_t>(kept[32 * y + lane].y);
+    taken += __popc(all);
+    same += __popc(equal);
+  }
   return true;
 }
 
 // The same by the CTA.  The least of the warps' (top / 8)-th largest lane maxima (keys dealt to all lanes in
-// turn) is a bound that at least `top` keys reach.  Those fit a key a thread, so that a barrier counts them.
-constexpr int kListed = kSelectThreads;
+// turn) is a bound that at least `top` keys reach.  Those are listed and held, up to kEach a thread.
+constexpr int kEach = 4, kListed = kEach * kSelectThreads;
 __device__ __forceinline__ bool pick_some(const uint32_t* keys, int n, int top, int32_t* out, int (*sums)[kSelectWarps],
-                                          uint4* of_warps, uint2* listed) {
+                                          uint4* of_warps, uint2* listed, uint32_t& lo, uint32_t& hi) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const auto lower = (1u << lane) - 1;
   const int rank = (top + kSelectWarps - 1) / kSelectWarps;
+  lo = 1;
+  hi = kForced;
   if (rank > 32) return false;
   uint32_t most = 0;                    // largest key of the lane's that is not forced
   int forced = 0, some = 0;
@@ -394,18 +437,19 @@ __device__ __forceinline__ bool pick_some(const uint32_t* keys, int n, int top, 
   const uint32_t at_rank = __shfl_sync(0xFFFFFFFFu, sorted_down(most, lane), rank - 1);
   if (lane == 0) of_warps[warp] = make_uint4(forced, some, largest, at_rank);
   __syncthreads();
-  uint32_t lo = kForced, hi = 0;
+  uint32_t least = kForced, largest_of_all = 0;
   forced = some = 0;
 #pragma unroll
   for (int y = 0; y < kSelectWarps; ++y) {
     const uint4 v = of_warps[y];
     forced += v.x;
     some += v.y;
-    hi = max(hi, v.z);
-    lo = min(lo, v.w);
+    largest_of_all = max(largest_of_all, v.z);
+    least = min(least, v.w);
   }
   if (some <= top) return false;
-  lo = forced == top ? kForced : max(lo, 1u);
+  lo = forced == top ? kForced : max(least, 1u);
+  hi = forced == top ? kForced : largest_of_all;
   // Listed in order: each warp has a run of blocks.
   const int each = (n + kSelectThreads - 1) / kSelectThreads * 32, begin = min(n, warp * each), end = min(n, begin + each);
   int mine = 0;
@@ -419,6 +463,7 @@ __device__ __forceinline__ bool pick_some(const uint32_t* keys, int n, int top, 
     to += y < warp ? sums[0][y] : 0;
     total += sums[0][y];
   }
+  __syncthreads();                      // the sums have been read
   if (total > kListed) return false;
   for (int i0 = begin; i0 < end; i0 += 32) {
     const uint32_t k = i0 + lane < end ? keys[i0 + lane] : 0u;
@@ -427,29 +472,62 @@ __device__ __forceinline__ bool pick_some(const uint32_t* keys, int n, int top, 
     to += __popc(all);
   }
   __syncthreads();
-  const uint2 own = tid < total ? listed[tid] : make_uint2(0, 0);
+  // Thread i holds listed key i, which a barrier counts, or keys 4i .. 4i + 3.
+  const int per = total <= kSelectThreads ? 1 : kEach;
+  uint32_t held[kEach], block[kEach];
+#pragma unroll
+  for (int y = 0; y < kEach; ++y) {
+    const uint2 v = y < per && per * tid + y < total ? listed[per * tid + y] : make_uint2(0, 0);
+    held[y] = v.x;
+    block[y] = v.y;
+  }
+  int turn = 0;
+  auto count = [&](uint32_t from) {
+    if (per == 1) return __syncthreads_count(held[0] >= from);
+    int x = 0;
+#pragma unroll
+    for (int y = 0; y < kEach; ++y) x += held[y] >= from;
+    x = __reduce_add_sync(0xFFFFFFFFu, x);
+    if (lane == 0) sums[turn][warp] = x;
+    __syncthreads();
+    const int4 a = *reinterpret_cast<const int4*>(sums[turn]), b = *reinterpret_cast<const int4*>(sums[turn] + 4);
+    turn ^= 1;
+    return a.x + a.y + a.z + a.w + b.x + b.y + b.z + b.w;
+  };
   // The threshold is in [lo, hi]: at least `top` keys >= lo, fewer > hi.
   bool fits = total == top;
   while (!fits && lo < hi) {
     const uint32_t mid = lo + (hi - lo + 1) / 2;
-    const int x = __syncthreads_count(own.x >= mid);
+    const int x = count(mid);
     if (x >= top)
       lo = mid;
     else
       hi = mid - 1;
     fits = x == top;
   }
-  const int ties = fits ? top : top - __syncthreads_count(own.x > lo);      // of the keys equal to lo, in order
-  const uint32_t same = __ballot_sync(0xFFFFFFFFu, own.x == lo), over = __ballot_sync(0xFFFFFFFFu, own.x > lo);
-  if (lane == 0) sums[0][warp] = __popc(over), sums[1][warp] = __popc(same);
-  __syncthreads();
-  int over_before = __popc(over & lower), same_before = __popc(same & lower);
-  for (int y = 0; y < warp; ++y) {
-    over_before += sums[0][y];
-    same_before += sums[1][y];
+  const int ties = fits || lo == kForced ? top : top - count(lo + 1);       // of the keys equal to lo, in order
+  // What comes before this thread's keys: over the threshold in the upper half, equal to it in the lower one.
+  uint32_t here = 0;
+#pragma unroll
+  for (int y = 0; y < kEach; ++y) here += (held[y] > lo ? 0x10000u : 0u) + (held[y] == lo && held[y] != 0 ? 1u : 0u);
+  uint32_t upto = here;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t y = __shfl_up_sync(0xFFFFFFFFu, upto, o);
+    if (lane >= o) upto += y;
   }
-  if (own.x > lo || (own.x == lo && own.x != 0 && same_before < ties))
-    out[over_before + min(same_before, ties)] = static_cast<int32_t>(own.y);
+  if (lane == 31) sums[turn][warp] = static_cast<int>(upto);
+  __syncthreads();
+  uint32_t before = upto - here;
+  for (int y = 0; y < warp; ++y) before += static_cast<uint32_t>(sums[turn][y]);
+  int over = static_cast<int>(before >> 16), same = static_cast<int>(before & 0xFFFFu);
+#pragma unroll
+  for (int y = 0; y < kEach; ++y) {
+    const bool is_over = held[y] > lo, is_same = held[y] == lo && held[y] != 0;
+    if (is_over || (is_same && same < ties)) out[over + min(same, ties)] = static_cast<int32_t>(block[y]);
+    over += is_over;
+    same += is_same;
+  }
   return true;
 }
 
@@ -496,7 +574,7 @@ __global__ void __launch_bounds__(kSelectThreads, 4) cache_select_kernel(const _
   uint32_t* const keys = reinterpret_cast<uint32_t*>(dynamic);
   __shared__ __align__(16) __half w[kTileRows][2 * D + 8];
   __shared__ int sums[2][kSelectWarps];
-  __shared__ uint2 kept[kSelectWarps][kKept];
+  uint2* const kept = reinterpret_cast<uint2*>(keys + a.tile_rows * a.places) + (threadIdx.x >> 5) * 32 * held_by_lane(a.top);
   grid_dep_launch();
   grid_dep_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
@@ -563,11 +641,16 @@ __global__ void __launch_bounds__(kSelectThreads, 4) cache_select_kernel(const _
         }
       }
     }
+    for (int i = warp; i < n_rows; i += kSelectWarps)
+      if (blocks + lane < (blocks + 3) / 4 * 4) keys[i * a.places + blocks + lane] = 0;
     __syncthreads();
     for (int i = warp; i < n_rows; i += kSelectWarps) {
       const uint32_t* const mine = keys + i * a.places;
       int32_t* const out = a.blocks + (ra + i) * a.row_stride + head * a.head_stride;
-      if (!pick_few(mine, blocks, a.top, out, kept[warp])) pick<32>(mine, blocks, a.top, out, sums);
+      uint32_t lo = 1, hi = kForced;
+      const bool few = a.top <= 32 ? pick_few<1>(mine, blocks, a.top, out, kept, lo, hi)
+                                   : a.top <= 128 && pick_few<6>(mine, blocks, a.top, out, kept, lo, hi);
+      if (!few) pick<32>(mine, blocks, a.top, out, sums, lo, hi);
     }
     __syncthreads();
     ra += n_rows;
@@ -586,7 +669,7 @@ __global__ void __launch_bounds__(kSelectThreads, 3) cache_select_row_kernel(con
   extern __shared__ uint4 dynamic[];
   uint32_t* const keys = reinterpret_cast<uint32_t*>(dynamic);
   __shared__ __align__(16) int16_t w[2 * D];
-  __shared__ int sums[2][kSelectWarps];
+  __shared__ __align__(16) int sums[2][kSelectWarps];
   __shared__ uint4 of_warps[kSelectWarps];
   __shared__ uint2 listed[kListed];
   grid_dep_launch();
@@ -655,17 +738,20 @@ __global__ void __launch_bounds__(kSelectThreads, 3) cache_select_row_kernel(con
     if (k0 + step < blocks) b.load(a, head, t);
     next[0] = ahead[0], next[1] = ahead[1];
   }
+  if (rank == 0 && blocks + static_cast<int>(threadIdx.x) < (blocks + 3) / 4 * 4) keys[blocks + threadIdx.x] = 0;
   if (ranks > 1)
     cluster_sync();
   else
     __syncthreads();
   if (rank != 0 || !mine) return;
   int32_t* const out = a.blocks + row * a.row_stride + head * a.head_stride;
-  if (!pick_some(keys, blocks, a.top, out, sums, of_warps, listed)) pick<kSelectThreads>(keys, blocks, a.top, out, sums);
+  uint32_t lo, hi;
+  if (!pick_some(keys, blocks, a.top, out, sums, of_warps, listed, lo, hi))
+    pick<kSelectThreads>(keys, blocks, a.top, out, sums, lo, hi);
 }
 
 constexpr int kSelectKeyBytes = 200 * 1024;      // of shared memory, for scores
-static_assert(4 * DS_VIT_SELECT_MAX_COLS <= kSelectKeyBytes, "one row's scores");
+static_assert(4 * (DS_VIT_SELECT_MAX_COLS + 4) <= kSelectKeyBytes, "one row's scores");
 
 bool bad_bounds(const ds_vit_key_bounds* b) { return !b || !b->hi_lo || !aligned(b->hi_lo, 16) || !b->exp; }
 
@@ -730,17 +816,22 @@ int ds_vit_cache_select(const ds_vit_cache* cache, const ds_vit_chunks* chunks, 
   const int64_t units = rows * c.kv_heads;
   const bool single = chunks->max_rows < 8 || units <= 4 * static_cast<int64_t>(num_sms()) || 8 * a.places > kSelectKeyBytes;
   a.tile_rows = 1;
-  if (!single)
-    for (a.tile_rows = kTileRows; 4 * static_cast<int64_t>(a.tile_rows) * a.places > kSelectKeyBytes;) a.tile_rows /= 2;
+  if (!single) {
+    // Sixteen rows where two CTAs fit an SM (1907 blocks: 16 rows 172 us, 8 rows 148), else eight as long as one fits (3750 blocks:
+    // 8 rows 371 us, 4 rows 389).
+    a.tile_rows = 64 * static_cast<int64_t>(a.places) <= kSelectKeyBytes / 2 ? kTileRows : kTileRows / 2;
+    while (4 * static_cast<int64_t>(a.tile_rows) * a.places > kSelectKeyBytes) a.tile_rows /= 2;
+  }
   int ranks = 1;
   if (single)
     while (ranks < 8 && 2 * ranks * units <= 2 * static_cast<int64_t>(num_sms()) &&
            2 * ranks * 16 * kSelectWarps <= chunks->table_cols)
       ranks *= 2;
-  const int bytes = std::max(4 * a.tile_rows * a.places, 1024);
+  const int kept = single ? 0 : 8 * kSelectThreads * held_by_lane(top);
+  const int bytes = 4 * a.tile_rows * a.places + kept;
   auto* fn = cache->head_dim == 128 ? (single ? cache_select_row_kernel<128> : cache_select_kernel<128>)
                                     : (single ? cache_select_row_kernel<64> : cache_select_kernel<64>);
-  if (allow_smem(reinterpret_cast<const void*>(fn), kSelectKeyBytes + 1024) != cudaSuccess) return DS_VIT_ECUDA;
+  if (allow_smem(reinterpret_cast<const void*>(fn), kSelectKeyBytes + 8 * kSelectThreads * kHeldMost) != cudaSuccess) return DS_VIT_ECUDA;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>((rows + a.tile_rows - 1) / a.tile_rows * c.kv_heads * ranks));
   cfg.blockDim = dim3(kSelectThreads);
