@@ -2,9 +2,7 @@
 // (include/dsvit.h, ds_vit_cache_attention_blocks).
 //
 // Every row and K/V head has keys of its own, which the 8 or so query heads of the group
-// share: 2 * 8 flops a byte of bf16, so the call is bound by the loads, from
-// memory where rows belong to different sequences, from L2 where many rows of one
-// prompt choose among the same pages.  There is nothing for a CTA's warps to share and no use for a tile
+// share: 2 * 8 flops a byte of bf16.  There is nothing for a CTA's warps to share and no use for a tile
 // larger than the group, so keys and values go from the pages straight into
 // registers as fragments of warp MMAs (m16n8k16), 16 keys at a time, with no
 // shared memory and nobody to wait for:
@@ -13,9 +11,19 @@
 //   O^T += V^T P^T: dims in the place of M.  P^T comes out of S^T's accumulators by a transposing
 //                 move between lanes (movmatrix).
 // The order of dims inside a product is free as long as both sides share it, and so
-// is the order of output rows, so each lane loads 16-byte pieces whose values it uses where they
-// lie: 128-byte lines of 8 keys, then of the 4 keys whose values it pairs up.  The next
-// tile's keys are loaded behind the scores' products, its values behind the outputs'.
+// are the order of keys and that of output rows, so each lane uses what it loads where it lies; values, of
+// which a product pairs keys, are loaded by whole lines (eight lanes a key) and passed on between
+// lanes, since a load in which neighbouring lanes read different keys takes L1 a cycle for each.
+// The next tile's keys are loaded behind the scores' products, its values behind the outputs'.
+//
+// What bounds it, 40 query and 8 K/V heads of 128:
+//   rows of different sequences, by memory: 48 rows over 4096 tokens each, bf16, 122 us (97% of the rate of a
+//   plain copy); e4m3, 84 us (71%): twelve warps an SM have 48 KB in flight, and conversions come on top.
+//   Sixteen warps with the queries in shared memory 95, with the next values in registers too 84.
+//   rows of one prompt, by the SM itself: 2048 rows over 1024 tokens each, e4m3, 493 us, bf16 603; all rows over
+//   one block, which L1 then holds, 475 and 541.  316 instructions a tile of 16 keys, more than half of them in the ALU
+//   (conversions, masks, addresses), and L1's data path (with values read as the products want them
+//   503 and 687).  Two tiles a step (604) and four CTAs an SM (529) were slower.
 //
 // Work: an item is a row, a K/V head and up to 8 (16) of its query heads.  One warp takes
 // an item while there are enough of them; with fewer, up to 4 warps of a CTA, then the

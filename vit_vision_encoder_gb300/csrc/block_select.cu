@@ -1,18 +1,18 @@
 // Bounds of the keys of a cache's pages and the choice of the blocks that each row
 // attends to (include/dsvit.h, ds_vit_cache_bounds and ds_vit_cache_select).
 //
-// Bounds: each completed page is read once, by one warp a K/V head; bound by memory.
+// Bounds: each completed page is read once, by one warp a K/V head, 32 keys in flight; bound by memory and, at the
+// sizes of a chunk, by the chain sequence -> table -> keys (13.9 MB of e4m3 pages: 7.4 us).
 //
-// Selection: a CTA takes a K/V head of up to sixteen rows of one sequence.  The scores are
-// a product of the blocks' bounds [blocks, 2 D] with the rows' shared queries [2 D, 16]
-// on warp MMAs, blocks in the place of M: both operands are small whole numbers, exact in
-// fp16 (|n| <= 1024, |H| <= 127), and so is every partial sum (< 2^24), so the list does not depend on
-// the order of anything.  The order of the 2 D terms is free, so a lane uses the 16 bytes
-// that it loads where they lie.  Scores stay in shared memory as whole numbers that order like
-// them; a search for the threshold, bit by bit, counts how many are above it, by one warp
-// a row (or the whole CTA where it has one row), and stops as soon as the count fits.  Single
-// rows of few sequences share the scoring among the CTAs of a cluster, which put
-// their scores into the first one's shared memory.
+// Selection: scores are a product of the blocks' bounds [blocks, 2 D] with the rows' shared
+// queries [2 D, rows].  Both operands are small whole numbers (|n| <= 1024, |H| <= 127) and so is every
+// partial sum (< 2^24): exact in fp16 products and fp32 sums, in any order, so equal inputs give equal lists.  Many
+// rows (up to sixteen of one sequence and K/V head a CTA) go through warp MMAs, blocks in the place of M; the order of the
+// 2 D terms is free, so a lane uses the 16 bytes that it loads where they lie.  A single row goes
+// through 16-bit dot products, by a CTA or by the CTAs of a cluster, which put their scores into the
+// first one's shared memory.  Scores stay in shared memory as whole numbers that order like them
+// ("keys"); the threshold is searched among the few keys over a bound that follows from the largest keys of
+// each lane, and among all keys where those are too many.
 #include <cuda_fp16.h>
 
 #include <algorithm>
@@ -327,7 +327,7 @@ __device__ __forceinline__ uint32_t sorted_down(uint32_t x, int lane) {
 // and held by the lanes, a few each, while the threshold is searched.  False, with nothing written, where more than that
 // reach it, with what is known of the threshold.  (532 blocks, 16 of them, as measured when it was brought in: 83 us for 16 thousand
 // lists, 137 by counting all keys; 3750 blocks, 128 of them, 8 thousand lists: 725
-// by counting all keys, 411.)
+// by counting all keys, 428.)
 constexpr int kHeldMost = 8;
 __host__ __device__ constexpr int held_by_lane(int top) { return top <= 32 ? 2 : kHeldMost; }
 template <int kTop>
