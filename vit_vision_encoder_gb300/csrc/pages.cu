@@ -529,9 +529,10 @@ struct CopyArgs {
 constexpr int kCopyThreads = 256, kCopyWords = 4;    // words a thread has in flight
 
 // CTA (x, y) copies its part x of pages y, y + gridDim.y, ...: what it has to look up is one pair of
-// page numbers.  690 pages of 2 x 131 KB: 65 us, 82% of the rate of a plain copy; 75 with the parts of all pages
-// dealt out in one row, which takes a division and a search for the part.
-__global__ void __launch_bounds__(kCopyThreads, 8) cache_copy_kernel(const __grid_constant__ CopyArgs a) {
+// page numbers.  690 pages of 2 x 131 KB: 53 us, the rate of a plain copy; 65 with eight CTAs an SM, whose 32 registers
+// do not hold the words in flight, 75 with the parts of all pages dealt out in one row, which takes a division and
+// a search for the part.
+__global__ void __launch_bounds__(kCopyThreads, 5) cache_copy_kernel(const __grid_constant__ CopyArgs a) {
   grid_dep_launch();
   grid_dep_wait();
   const int n = __ldg(a.count);
@@ -557,7 +558,7 @@ __global__ void __launch_bounds__(kCopyThreads, 8) cache_copy_kernel(const __gri
         if (first + y * kCopyThreads < a.held_words) v[y] = __ldcs(get + y * kCopyThreads);
 #pragma unroll
       for (int y = 0; y < kCopyWords; ++y)
-        if (first + y * kCopyThreads < a.held_words) put[y * kCopyThreads] = v[y];
+        if (first + y * kCopyThreads < a.held_words) __stcs(put + y * kCopyThreads, v[y]);
       continue;
     }
 #pragma unroll
@@ -706,7 +707,7 @@ int ds_vit_cache_copy(const ds_vit_cache* cache, const ds_vit_key_bounds* bounds
   a.held_tiles = static_cast<int>((a.held_words + kCopyThreads * kCopyWords - 1) / (kCopyThreads * kCopyWords));
   a.status = reinterpret_cast<int*>(status);
   const int parts = 2 * a.held_tiles + (e4m3 || bounds);
-  const dim3 grid(static_cast<unsigned>(parts), static_cast<unsigned>(std::min(copies->cap, (8 * num_sms() + parts - 1) / parts)));
+  const dim3 grid(static_cast<unsigned>(parts), static_cast<unsigned>(std::min(copies->cap, (10 * num_sms() + parts - 1) / parts)));
   return launched(launch_pdl(cache_copy_kernel, grid, dim3(kCopyThreads), 0, static_cast<cudaStream_t>(stream), a));
 }
 
