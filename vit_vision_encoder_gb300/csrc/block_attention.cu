@@ -23,7 +23,8 @@
 //   rows of one prompt, by the SM itself: 2048 rows over 1024 tokens each, e4m3, 493 us, bf16 603; all rows over
 //   one block, which L1 then holds, 475 and 541.  316 instructions a tile of 16 keys, more than half of them in the ALU
 //   (conversions, masks, addresses), and L1's data path (with values read as the products want them
-//   503 and 687).  Two tiles a step (604) and four CTAs an SM (529) were slower.
+//   503 and 687).  Two tiles a step (604), four CTAs an SM (529) and scores from e4m3 MMAs with the queries in
+//   two parts (579) were slower.
 //
 // Work: an item is a row, a K/V head and up to 8 (16) of its query heads.  One warp takes
 // an item while there are enough of them; with fewer, up to 4 warps of a CTA, then the
