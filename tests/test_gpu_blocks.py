@@ -604,6 +604,46 @@ def test_captured_step(dv):
         assert torch.equal(got[0], blocks) and torch.equal(got[1], out) and int(status.item()) == dv.OK
 
 
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+def test_rows_that_are_parts_of_wider_ones(dv, kind):
+    """Queries out of a projection's rows, outputs into wider ones: the same, and what lies beside stays."""
+    st = make(dv, [1, 77, 3], [400, 300, 90], 4, 128, 16, kind, back=2)
+    q = st.queries(20, wide=8)
+    assert q.stride(0) == 28 * 128
+    blocks, _ = dv.cache_select(st.cache, st.chunks, st.bounds, q.contiguous(), 6, 1, 1)
+    want, _ = dv.cache_attention_blocks(st.cache, st.chunks, q.contiguous(), blocks)
+    wide = torch.full((st.rows, 23, 128), 3.0, dtype=torch.bfloat16, device="cuda")
+    got, _ = dv.cache_select(st.cache, st.chunks, st.bounds, q, 6, 1, 1)
+    out, status = dv.cache_attention_blocks(st.cache, st.chunks, q, blocks, out=wide[:, 2:22])
+    torch.cuda.synchronize()
+    n = st.off[-1]
+    assert int(status.item()) == dv.OK and torch.equal(got[:n], blocks[:n]) and torch.equal(out[:n], want[:n])
+    assert (wide[:, :2] == 3).all() and (wide[:, 22:] == 3).all() and (wide[n:] == 3).all()
+
+
+def test_two_streams_at_once(dv):
+    sts = [make(dv, [1, 100], [3000, 2000], 8, 128, 16, kind, seed=i) for i, kind in enumerate(("bf16", "e4m3"))]
+    qs = [st.queries(40) for st in sts]
+
+    def step(st, q):
+        dv.cache_bounds(st.cache, st.chunks, st.bounds, st.rows)
+        blocks, _ = dv.cache_select(st.cache, st.chunks, st.bounds, q, 20, 1, 2)
+        return blocks, dv.cache_attention_blocks(st.cache, st.chunks, q, blocks)[0]
+
+    want = [step(st, q) for st, q in zip(sts, qs)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in sts]
+    got = [[], []]
+    for _ in range(15):
+        for i in range(2):
+            with torch.cuda.stream(streams[i]):
+                got[i].append(step(sts[i], qs[i]))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for blocks, out in got[i]:
+            assert torch.equal(blocks, want[i][0]) and torch.equal(out, want[i][1])
+
+
 def test_lists_laid_out_otherwise(dv):
     """Heads in front of rows, and room between the lists."""
     st = make(dv, [1, 130], [500, 300], 4, 64, 16, "bf16")
