@@ -256,6 +256,26 @@ def test_select_over_extremes(dv):
         assert int(status.item()) == dv.ERANGE and not (out[0] == 2).any()
 
 
+def test_select_sums_at_their_limit(dv):
+    """Shared queries of up to 1024 in every channel and bounds of 125 to 127: sums within a percent of 2^24 that
+    differ in their last bits."""
+    for q, kv in (([1], [900]), ([200], [900])):
+        st = make(dv, q, kv, 4, 128, 16, "bf16", seed=5)
+        r = np.random.default_rng(2)
+        st.hi_lo[:, :, 0] = r.integers(125, 128, st.hi_lo[:, :, 0].shape)
+        st.hi_lo[:, :, 1] = -r.integers(125, 128, st.hi_lo[:, :, 1].shape)
+        st.exp[:] = 120
+        st.bounds.hi_lo.copy_(torch.from_numpy(st.hi_lo))
+        st.bounds.exp.copy_(torch.from_numpy(st.exp))
+        x = np.full((st.rows, 256, 128), 15.875)         # 64 heads of 16 when rounded
+        x[:, ::64] = r.integers(12, 16, (st.rows, 4, 128))
+        x[:, 1] = 15.875                                 # the exponent's
+        x[1::3] *= -1
+        x[2::3] *= r.choice([-1, 1], x[2::3, :1].shape)
+        check_select(dv, st, 256, 9, 1, 1, q=torch.from_numpy(x).bfloat16().cuda())
+        check_select(dv, st, 256, 40, 1, 1, q=torch.from_numpy(x).bfloat16().cuda())
+
+
 def test_select_in_wide_tables(dv):
     """Rows share their loads in smaller groups as the table gets wider."""
     for cols in (3000, 9000, 20000, dv.SELECT_MAX_COLS):

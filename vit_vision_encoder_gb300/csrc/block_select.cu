@@ -6,7 +6,7 @@
 //
 // Selection: scores are a product of the blocks' bounds [blocks, 2 D] with the rows' shared
 // queries [2 D, rows].  Both operands are small whole numbers (|n| <= 1024, |H| <= 127) and so is every
-// partial sum (< 2^24): exact in fp16 products and fp32 sums, in any order, so equal inputs give equal lists.  Many
+// partial sum (2^24 at most): exact in fp16 products and fp32 sums, in any order, so equal inputs give equal lists.  Many
 // rows (up to sixteen of one sequence and K/V head a CTA) go through warp MMAs, blocks in the place of M; the order of the
 // 2 D terms is free, so a lane uses the 16 bytes that it loads where they lie.  A single row goes
 // through 16-bit dot products, by a CTA or by the CTAs of a cluster, which put their scores into the
@@ -16,6 +16,7 @@
 #include <cuda_fp16.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "cache.cuh"
 
@@ -165,65 +166,85 @@ struct SelectArgs {
 constexpr int kSelectWarps = 8, kSelectThreads = 32 * kSelectWarps, kTileRows = 16;
 constexpr uint32_t kForced = 0xFFFFFFFFu, kNotFinite = 0xFFFFFFFEu;   // above every score's number; 0: not a candidate
 
-// A whole number that orders like the float (finite: under kNotFinite, over 0).
-__device__ __forceinline__ uint32_t ordered(float x) {
-  const uint32_t u = __float_as_uint(x + 0.f);
+// A whole number that orders like the float x * by (finite: under kNotFinite, over 0; -0 like 0).
+__device__ __forceinline__ uint32_t ordered(float x, float by) {
+  const uint32_t u = __float_as_uint(fmaf(x, by, 0.f));
   return u ^ (static_cast<uint32_t>(static_cast<int32_t>(u) >> 31) | 0x80000000u);
 }
 
-// Four signed bytes -> fp16 pairs: bytes + 128 become the low bits of 1024 + x.
-__device__ __forceinline__ uint32_t f16_of_bytes(uint32_t biased, uint32_t which) {
-  uint32_t r;
-  const uint32_t h = __byte_perm(biased, 0x64646464u, which);
-  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(h), "r"(0x64806480u));
-  return r;
-}
+// Two of four bytes (0 .. 255) as an fp16 pair in units of 2^-24, the least that fp16 has: the bytes themselves.
+constexpr int kByteUnit = 24;
+__device__ __forceinline__ uint32_t f16_of_bytes(uint32_t bytes, uint32_t which) { return __byte_perm(bytes, 0u, which); }
+
+// Heads of one row and K/V head, D / 32 values of each in a lane: read whenever they are looked at, kAtOnce on their way
+// together, or held.
+template <int D, int kAtOnce>
+struct RowHeads {
+  const bf16* q;
+  int group, lane;
+  template <typename F>
+  __device__ __forceinline__ void each(F&& f) const {
+#pragma unroll kAtOnce
+    for (int h = 0; h < group; ++h) {
+      uint32_t u[D / 64];
+#pragma unroll
+      for (int y = 0; y < D / 64; ++y) u[y] = __ldg(reinterpret_cast<const uint32_t*>(q + h * D) + lane * (D / 64) + y);
+      f(u);
+    }
+  }
+};
+constexpr int kHeldHeads = 8;
+template <int D>
+struct HeldHeads {
+  uint32_t u[kHeldHeads][D / 64];
+  __device__ __forceinline__ void load(const bf16* q, int group, int lane) {
+#pragma unroll
+    for (int h = 0; h < kHeldHeads; ++h)
+#pragma unroll
+      for (int y = 0; y < D / 64; ++y)
+        u[h][y] = h < group ? __ldg(reinterpret_cast<const uint32_t*>(q + h * D) + lane * (D / 64) + y) : 0u;
+  }
+  template <typename F>
+  __device__ __forceinline__ void each(F&& f) const {
+#pragma unroll
+    for (int h = 0; h < kHeldHeads; ++h) f(u[h]);
+  }
+};
 
 // The shared query of one row: w[0 .. D - 1] sums of positive, w[D .. 2 D - 1] of negative parts, as
-// fp16 or 16-bit whole numbers.  By one warp.
-template <int D, typename T>
-__device__ __forceinline__ void shared_query(const SelectArgs& a, const bf16* q, T* w, int lane) {
+// fp16 or 16-bit whole numbers.  By one warp; returns the sum of them all.
+template <int D, typename T, typename Heads>
+__device__ __forceinline__ int shared_query(const SelectArgs& a, const Heads& heads, T* w, int lane) {
   constexpr int kPer = D / 32;
-  auto load = [&](int h, float (&x)[kPer]) {
-    const uint32_t* at = reinterpret_cast<const uint32_t*>(q + h * D) + lane * (kPer / 2);
-#pragma unroll
-    for (int y = 0; y < kPer / 2; ++y) {
-      const uint32_t u = __ldg(at + y);
-      x[2 * y] = bf16lo(u);
-      x[2 * y + 1] = bf16hi(u);
-    }
-  };
   uint32_t top = 0;
-#pragma unroll 4
-  for (int h = 0; h < a.group; ++h) {
-    float x[kPer];
-    load(h, x);
+  heads.each([&](const uint32_t(&u)[D / 64]) {
 #pragma unroll
-    for (int y = 0; y < kPer; ++y) top = max(top, __float_as_uint(x[y]) & 0x7FFFFFFFu);
-  }
+    for (int y = 0; y < D / 64; ++y) top = max(top, max(u[y] << 16 & 0x7FFFFFFFu, u[y] & 0x7FFF0000u));
+  });
   top = __reduce_max_sync(0xFFFFFFFFu, top);
   // 1016 = (1 + 126/128) 2^9
   const int f = least_exponent(top >> 16, 9 - a.log2_group);
   const float by = power_of_two(-f / 2), rest = power_of_two(-f - -f / 2);     // 2^-f may be no float
   int up[kPer] = {}, down[kPer] = {};
   if (top < 0x7F800000u) {
-#pragma unroll 4
-    for (int h = 0; h < a.group; ++h) {
-      float x[kPer];
-      load(h, x);
+    heads.each([&](const uint32_t(&u)[D / 64]) {
 #pragma unroll
       for (int y = 0; y < kPer; ++y) {
-        const int n = __float2int_rn(x[y] * by * rest);
+        const int n = __float2int_rn((y & 1 ? bf16hi(u[y / 2]) : bf16lo(u[y / 2])) * by * rest);
         up[y] += max(n, 0);
         down[y] += min(n, 0);
       }
-    }
+    });
   }
 #pragma unroll
   for (int y = 0; y < kPer; ++y) {
     w[lane * kPer + y] = static_cast<T>(up[y]);
     w[D + lane * kPer + y] = static_cast<T>(down[y]);
   }
+  int sum = 0;
+#pragma unroll
+  for (int y = 0; y < kPer; ++y) sum += up[y] + down[y];
+  return __reduce_add_sync(0xFFFFFFFFu, sum);
 }
 
 // The list of one row from its n keys, by `kThreads` threads (a warp or the CTA); up to the next multiple
@@ -324,44 +345,46 @@ __device__ __forceinline__ uint32_t sorted_down(uint32_t x, int lane) {
 
 // The same by one warp where few blocks of many are looked for.  Each lane finds its own kTop-th largest key; the
 // (need / kTop)-th largest of those is a bound that at least `need` keys reach and not many more do.  Those are listed,
-// and held by the lanes, a few each, while the threshold is searched.  False, with nothing written, where more than that
-// reach it, with what is known of the threshold.  (532 blocks, 16 of them, as measured when it was brought in: 83 us for 16 thousand
+// and held by the lanes, a few each, while the threshold is searched.  False, with nothing written, where too many
+// reach it, with what is known of the threshold.  keys + n up to the next multiple of four are 0.  (532 blocks, 16 of them, as measured when it was brought in: 83 us for 16 thousand
 // lists, 137 by counting all keys; 3750 blocks, 128 of them, 8 thousand lists: 725
 // by counting all keys, 428.)
 constexpr int kHeldMost = 8;
 __host__ __device__ constexpr int held_by_lane(int top) { return top <= 32 ? 2 : kHeldMost; }
 template <int kTop>
-__device__ __forceinline__ bool pick_few(const uint32_t* keys, int n, int top, int32_t* out, uint2* kept, uint32_t& lo,
-                                         uint32_t& hi) {
+__device__ __forceinline__ bool pick_few(const uint32_t* keys, int n, const SelectArgs& a, int32_t* out, uint2* kept,
+                                         uint32_t& lo, uint32_t& hi) {
   constexpr int kHeld = held_by_lane(32 * kTop), kKept = 32 * kHeld;
-  const int lane = threadIdx.x & 31;
-  uint32_t most[kTop] = {};             // the lane's largest keys that are not forced, largest first
-  int forced = 0, some = 0;
-#pragma unroll 4
-  for (int i = lane; i < n; i += 32) {
-    const uint32_t k = keys[i];
-    forced += k == kForced;
-    some += k != 0;
-    uint32_t x = k == kForced ? 0u : k;
+  const int lane = threadIdx.x & 31, top = a.top;
+  uint32_t most[kTop] = {};             // the lane's largest keys, largest first, plus 1: forced ones are 0
+#pragma unroll 2
+  for (int i = 4 * lane; i < n; i += 128) {
+    const uint4 k = *reinterpret_cast<const uint4*>(keys + i);
+    uint32_t x[4] = {k.x + 1, k.y + 1, k.z + 1, k.w + 1};
 #pragma unroll
-    for (int y = 0; y < kTop; ++y) {
-      const uint32_t up = max(most[y], x);
-      x = min(most[y], x);
-      most[y] = up;
-    }
+    for (int z = 0; z < 4; ++z)
+#pragma unroll
+      for (int y = 0; y < kTop; ++y) {
+        const uint32_t up = max(most[y], x[z]);
+        x[z] = min(most[y], x[z]);
+        most[y] = up;
+      }
   }
+  // The forced ones are among the first and the last.
+  const int firsts = min(a.first, n), lasts = min(a.last, n - firsts);
+  int forced = 0;
+  for (int i = lane; i < firsts + lasts; i += 32) forced += keys[i < firsts ? i : n - lasts + i - firsts] == kForced;
   forced = __reduce_add_sync(0xFFFFFFFFu, forced);
-  some = __reduce_add_sync(0xFFFFFFFFu, some);
   const int need = top - forced;
-  if (some <= top || need > 32 * kTop) {
+  if (need > 32 * kTop) {
     lo = 1;
     hi = kForced;
     return false;
   }
   lo = hi = kForced;
   if (need > 0) {
-    lo = max(__shfl_sync(0xFFFFFFFFu, sorted_down(most[kTop - 1], lane), (need + kTop - 1) / kTop - 1), 1u);
-    hi = __reduce_max_sync(0xFFFFFFFFu, most[0]);
+    lo = max(__shfl_sync(0xFFFFFFFFu, sorted_down(most[kTop - 1], lane), (need + kTop - 1) / kTop - 1), 2u) - 1;
+    hi = max(__reduce_max_sync(0xFFFFFFFFu, most[0]), 2u) - 1;
   }
   const auto lower = (1u << lane) - 1;
   int n_kept = 0;
@@ -385,8 +408,8 @@ __device__ __forceinline__ bool pick_few(const uint32_t* keys, int n, int top, i
       if (32 * y < n_kept) x += held[y] >= from;
     return static_cast<int>(__reduce_add_sync(0xFFFFFFFFu, x));
   };
-  // The threshold is in [lo, hi]: at least `top` keys >= lo, fewer > hi.
-  bool fits = n_kept == top;
+  // The threshold is in [lo, hi]: at least `top` keys >= lo, fewer > hi (or all are taken).
+  bool fits = n_kept <= top;
   while (!fits && lo < hi) {
     const uint32_t mid = lo + (hi - lo + 1) / 2;
     const int x = count(mid);
@@ -408,6 +431,7 @@ __device__ __forceinline__ bool pick_few(const uint32_t* keys, int n, int top, i
     taken += __popc(all);
     same += __popc(equal);
   }
+  for (int i = taken + lane; i < top; i += 32) out[i] = -1;
   return true;
 }
 
@@ -531,12 +555,28 @@ __device__ __forceinline__ bool pick_some(const uint32_t* keys, int n, int top, 
   return true;
 }
 
-// The bounds of 16 blocks from k0 on, as a lane of a warp has them: its 16-byte pieces t, t + 4, ... of blocks g and g + 8.
-template <int D>
-struct BoundTile {
-  int32_t at[2];                        // pages; below 0: no block here
-  uint4 u[2][D / 32];
+// What a lane has of 16 blocks from k0 on, but for their bounds: pages and exponents of blocks g and g + 8.
+struct BoundPages {
+  int32_t at[2];                        // below 0: no block here
   uint32_t byte[2];
+  // The key of block k0 + g + 8 y for a row whose own block is `own`, from the whole number `score`, in units of 2^-kUnit.
+  template <int kUnit>
+  __device__ __forceinline__ uint32_t key(const SelectArgs& a, int y, int k, int own, float score) const {
+    if (k > own || at[y] < 0) return 0;
+    if (k < a.first || k > own - a.last) return kForced;
+    return byte[y] == 255u ? kNotFinite : ordered(score, factor<kUnit>(y));
+  }
+  // 2^(e - 20): every score is a float.
+  template <int kUnit>
+  __device__ __forceinline__ float factor(int y) const {
+    return power_of_two(max(static_cast<int>(byte[y]), 21) - 147 + kUnit);
+  }
+};
+
+// And their bounds, pieces t, t + 4, ... of 16 bytes.
+template <int D>
+struct BoundTile : BoundPages {
+  uint4 u[2][D / 32];
   __device__ __forceinline__ void load(const SelectArgs& a, int head, int t) {
 #pragma unroll
     for (int y = 0; y < 2; ++y) {
@@ -551,93 +591,133 @@ struct BoundTile {
       for (int j = 0; j < D / 32; ++j) u[y][j] = __ldg(from + 4 * j);
     }
   }
-  // The key of block k0 + g + 8 y for a row whose own block is `own`, from the whole number `score`.
-  __device__ __forceinline__ uint32_t key(const SelectArgs& a, int y, int k, int own, float score) const {
-    if (k > own || at[y] < 0) return 0;
-    if (k < a.first || k > own - a.last) return kForced;
-    // times 2^(e - 20): every score is a float
-    return byte[y] == 255u ? kNotFinite : ordered(score * power_of_two(max(static_cast<int>(byte[y]), 21) - 147));
-  }
 };
 
 __device__ __forceinline__ int32_t page_entry(const int32_t* table, int k, int blocks) {
   return k < blocks ? __ldg(table + k) : -1;
 }
 
-// Up to sixteen rows of one sequence at a time, for one K/V head.  Bound by instructions: half of them widen the bounds
-// for the MMAs (shared by the rows), half pick.  2048 rows of 8 heads over 532 blocks: 56 us; 63 with eight
-// rows; 86 with eight and their weights kept in registers, which leaves two CTAs an SM instead of four.
+// Up to sixteen rows of one sequence at a time, for one K/V head.  Bound by instructions and what they wait for: a
+// quarter picks, the rest widens the bounds, multiplies, makes keys and shares queries.  Bytes go into the products as they are
+// but for their sign (b + 128 in units of 2^-24), and the sums begin at -128 times that of w: whole
+// numbers of at most 2^24 in any order, 127 |w| of the terms that are in and 128 |w| of the others.  2048 rows of 8
+// heads over 532 blocks: 54 us, over 938 blocks (1024 rows) 48; 56 and 60 with bytes widened to fp16 by a subtraction, four CTAs
+// an SM (64 registers) and each round's bounds loaded when it begins.  Thirty-two rows a CTA, with eight to
+// sixteen warps: 54 to 57 and 53 to 56.
 template <int D>
-__global__ void __launch_bounds__(kSelectThreads, 4) cache_select_kernel(const __grid_constant__ SelectArgs a) {
+__global__ void __launch_bounds__(kSelectThreads, D == 128 ? 3 : 4) cache_select_kernel(const __grid_constant__ SelectArgs a) {
   constexpr int kSteps = 2 * D / 64;                // 16-byte pieces of a block that a lane has, four MMAs each
+  constexpr int kStep = 16 * kSelectWarps;
   extern __shared__ uint4 dynamic[];
   uint32_t* const keys = reinterpret_cast<uint32_t*>(dynamic);
   __shared__ __align__(16) __half w[kTileRows][2 * D + 8];
-  __shared__ int sums[2][kSelectWarps];
+  __shared__ __align__(8) float bias[kTileRows];    // -128 times the sum of w
   uint2* const kept = reinterpret_cast<uint2*>(keys + a.tile_rows * a.places) + (threadIdx.x >> 5) * 32 * held_by_lane(a.top);
   grid_dep_launch();
   grid_dep_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
-  const int64_t tile = blockIdx.x;
-  const int head = static_cast<int>(tile % a.kv_heads);
-  const int64_t r_end = min(static_cast<int64_t>(a.b.rows), (tile / a.kv_heads + 1) * a.tile_rows);
+  const int tile = static_cast<int>(blockIdx.x), head = tile % a.kv_heads;
+  const int r_end = min(a.b.rows, (tile / a.kv_heads + 1) * a.tile_rows);
+  const bf16* const queries = a.q + static_cast<int64_t>(head) * a.group * D;
   // The rows of one sequence after another.
-  for (int64_t ra = tile / a.kv_heads * a.tile_rows; ra < r_end;) {
-    const int s = find_seq(a.b, static_cast<int>(ra), lane);
+  for (int ra = tile / a.kv_heads * a.tile_rows; ra < r_end;) {
+    // Queries are on their way while the sequence is looked up, and the first pages' numbers while they are shared.
+    constexpr int kOwn = (kTileRows + kSelectWarps - 1) / kSelectWarps;
+    HeldHeads<D> held;
+    auto hold = [&](int row) {
+      held.load(queries + row * a.q_stride, row < r_end && a.group <= kHeldHeads ? a.group : 0, lane);
+    };
+    hold(ra + warp);
+    const int s = find_seq(a.b, ra, lane);
     const Seq q = s < 0 ? Seq{0, 0, 0} : load_seq(a.b, a.page_shift, s, a.status);
     if (static_cast<unsigned>(ra - q.row0) >= static_cast<unsigned>(q.c)) {     // of no sequence, or refused
       ++ra;
       continue;
     }
-    const int n_rows = static_cast<int>(min(r_end, static_cast<int64_t>(q.row0) + q.c) - ra);
-    const int p0 = q.kv - q.c + static_cast<int>(ra - q.row0);                  // position of the first
+    const int n_rows = min(r_end, q.row0 + q.c) - ra;
+    const int p0 = q.kv - q.c + ra - q.row0;        // position of the first
     const int blocks = max(p0 + n_rows - 1 + (1 << a.page_shift), 0) >> a.page_shift;     // of the last
-    for (int i = warp; i < kTileRows; i += kSelectWarps) {
-      if (i < n_rows)
-        shared_query<D>(a, a.q + (ra + i) * a.q_stride + static_cast<int64_t>(head) * a.group * D, w[i], lane);
-      else
-        for (int x = lane; x < 2 * D; x += 32) w[i][x] = __half(0.f);
-    }
-    __syncthreads();
     const int32_t* table = a.b.table + static_cast<int64_t>(s) * a.b.table_cols;
     BoundTile<D> b;
-    int32_t ahead[2];                               // the next blocks' pages
+    int32_t ahead[2];                               // the pages of the blocks after them
 #pragma unroll
-    for (int y = 0; y < 2; ++y) ahead[y] = page_entry(table, 16 * warp + g + 8 * y, blocks);
-    for (int k0 = 16 * warp; k0 < blocks; k0 += 16 * kSelectWarps) {
+    for (int y = 0; y < 2; ++y) {
+      b.at[y] = page_entry(table, 16 * warp + g + 8 * y, blocks);
+      ahead[y] = page_entry(table, 16 * warp + kStep + g + 8 * y, blocks);
+    }
+#pragma unroll
+    for (int y = 0; y < kOwn; ++y) {
+      const int i = warp + y * kSelectWarps;
+      if (i >= n_rows) {
+        if (i >= kTileRows) break;
+        for (int x = lane; x < 2 * D; x += 32) w[i][x] = __half(0.f);
+        continue;
+      }
+      const int sum = a.group <= kHeldHeads
+                          ? shared_query<D>(a, held, w[i], lane)
+                          : shared_query<D>(a, RowHeads<D, 8>{queries + static_cast<int64_t>(ra + i) * a.q_stride, a.group, lane}, w[i], lane);
+      if (lane == 0) bias[i] = static_cast<float>(-128 * sum) * power_of_two(-kByteUnit);
+      if (y + 1 < kOwn) hold(ra + i + kSelectWarps);
+    }
+    if (16 * warp < blocks) b.load(a, head, t);
+    __syncthreads();
+    for (int k0 = 16 * warp; k0 < blocks; k0 += kStep) {
+      float c[kTileRows / 8][4];
+#pragma unroll
+      for (int z = 0; z < kTileRows / 8; ++z) {
+        const float2 from = *reinterpret_cast<const float2*>(&bias[8 * z + 2 * t]);
+        c[z][0] = c[z][2] = from.x;
+        c[z][1] = c[z][3] = from.y;
+      }
+      auto products = [&](auto groups) {
+#pragma unroll
+        for (int j = 0; j < kSteps; ++j) {
+          const uint32_t b0[4] = {b.u[0][j].x, b.u[0][j].y, b.u[0][j].z, b.u[0][j].w};
+          const uint32_t b1[4] = {b.u[1][j].x, b.u[1][j].y, b.u[1][j].z, b.u[1][j].w};
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const uint32_t v0 = b0[x] ^ 0x80808080u, v1 = b1[x] ^ 0x80808080u;
+            const uint32_t m[4] = {f16_of_bytes(v0, 0x4140u), f16_of_bytes(v1, 0x4140u), f16_of_bytes(v0, 0x4342u),
+                                   f16_of_bytes(v1, 0x4342u)};
+            // The terms of rows g, g + 8, ... that go with the lane's piece of a block.
+#pragma unroll
+            for (int z = 0; z < decltype(groups)::value; ++z) {
+              const uint2 wz = *reinterpret_cast<const uint2*>(&w[8 * z + g][64 * j + 16 * t + 4 * x]);
+              mma_f16(c[z], m, wz.x, wz.y);
+            }
+          }
+        }
+      };
+      if (n_rows > 8)
+        products(std::integral_constant<int, kTileRows / 8>{});
+      else
+        products(std::integral_constant<int, 1>{});
+      // The next bounds come while these scores become keys.
+      const BoundPages here = b;
 #pragma unroll
       for (int y = 0; y < 2; ++y) {
         b.at[y] = ahead[y];
-        ahead[y] = page_entry(table, k0 + 16 * kSelectWarps + g + 8 * y, blocks);
+        ahead[y] = page_entry(table, k0 + 2 * kStep + g + 8 * y, blocks);
       }
-      b.load(a, head, t);
-      float c[2][4] = {};
-#pragma unroll
-      for (int j = 0; j < kSteps; ++j) {
-        const uint32_t b0[4] = {b.u[0][j].x, b.u[0][j].y, b.u[0][j].z, b.u[0][j].w};
-        const uint32_t b1[4] = {b.u[1][j].x, b.u[1][j].y, b.u[1][j].z, b.u[1][j].w};
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          const uint32_t v0 = b0[x] ^ 0x80808080u, v1 = b1[x] ^ 0x80808080u;
-          const uint32_t m[4] = {f16_of_bytes(v0, 0x4140u), f16_of_bytes(v1, 0x4140u), f16_of_bytes(v0, 0x4342u),
-                                 f16_of_bytes(v1, 0x4342u)};
-          // Row g's terms that go with the lane's piece of a block, and row g + 8's.
-          const uint2 w0 = *reinterpret_cast<const uint2*>(&w[g][64 * j + 16 * t + 4 * x]);
-          mma_f16(c[0], m, w0.x, w0.y);
-          if (n_rows > 8) {
-            const uint2 w1 = *reinterpret_cast<const uint2*>(&w[g + 8][64 * j + 16 * t + 4 * x]);
-            mma_f16(c[1], m, w1.x, w1.y);
-          }
-        }
-      }
+      if (k0 + kStep < blocks) b.load(a, head, t);
+      // Blocks between all rows' forced ones, with pages and scores.
+      const bool plain = n_rows % 8 == 0 && k0 >= a.first && k0 + 15 <= (p0 >> a.page_shift) - a.last &&
+                         __all_sync(0xFFFFFFFFu, min(here.at[0], here.at[1]) >= 0 && max(here.byte[0], here.byte[1]) < 255u);
 #pragma unroll
       for (int y = 0; y < 2; ++y) {
         const int k = k0 + g + 8 * y;
+        const float factor = here.factor<kByteUnit>(y);
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          const int i = 2 * t + (x & 1) + 8 * (x >> 1);      // row
-          if (i < n_rows && k < blocks)
-            keys[i * a.places + k] = b.key(a, y, k, (p0 + i) >> a.page_shift, c[x >> 1][2 * y + (x & 1)]);
+        for (int z = 0; z < kTileRows / 8; ++z) {
+          if (8 * z >= n_rows) break;
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const int i = 2 * t + x + 8 * z;      // row
+            if (plain)
+              keys[i * a.places + k] = ordered(c[z][2 * y + x], factor);
+            else if (i < n_rows && k < blocks)
+              keys[i * a.places + k] = here.key<kByteUnit>(a, y, k, (p0 + i) >> a.page_shift, c[z][2 * y + x]);
+          }
         }
       }
     }
@@ -646,11 +726,12 @@ __global__ void __launch_bounds__(kSelectThreads, 4) cache_select_kernel(const _
     __syncthreads();
     for (int i = warp; i < n_rows; i += kSelectWarps) {
       const uint32_t* const mine = keys + i * a.places;
-      int32_t* const out = a.blocks + (ra + i) * a.row_stride + head * a.head_stride;
+      int32_t* const out = a.blocks + static_cast<int64_t>(ra + i) * a.row_stride + head * a.head_stride;
       uint32_t lo = 1, hi = kForced;
-      const bool few = a.top <= 32 ? pick_few<1>(mine, blocks, a.top, out, kept, lo, hi)
-                                   : a.top <= 128 && pick_few<6>(mine, blocks, a.top, out, kept, lo, hi);
-      if (!few) pick<32>(mine, blocks, a.top, out, sums, lo, hi);
+      const int n = max(p0 + i + (1 << a.page_shift), 0) >> a.page_shift;       // blocks of this row
+      const bool few = a.top <= 32 ? pick_few<1>(mine, n, a, out, kept, lo, hi)
+                                   : a.top <= 128 && pick_few<6>(mine, n, a, out, kept, lo, hi);
+      if (!few) pick<32>(mine, n, a.top, out, nullptr, lo, hi);
     }
     __syncthreads();
     ra += n_rows;
@@ -682,7 +763,7 @@ __global__ void __launch_bounds__(kSelectThreads, 3) cache_select_row_kernel(con
   const int64_t tile = blockIdx.x / ranks, row = tile / a.kv_heads;
   const int head = static_cast<int>(tile - row * a.kv_heads);
   if (warp == kSelectWarps - 1)
-    shared_query<D>(a, a.q + row * a.q_stride + static_cast<int64_t>(head) * a.group * D, w, lane);
+    shared_query<D>(a, RowHeads<D, 4>{a.q + row * a.q_stride + static_cast<int64_t>(head) * a.group * D, a.group, lane}, w, lane);
   const int s = find_seq(a.b, static_cast<int>(row), lane);
   const Seq q = s < 0 ? Seq{0, 0, 0} : load_seq(a.b, a.page_shift, s, a.status);
   const bool mine = static_cast<unsigned>(row - q.row0) < static_cast<unsigned>(q.c);     // else of no sequence, or refused
@@ -725,7 +806,7 @@ __global__ void __launch_bounds__(kSelectThreads, 3) cache_select_row_kernel(con
       c[y] += __shfl_xor_sync(0xFFFFFFFFu, c[y], 1);
       c[y] += __shfl_xor_sync(0xFFFFFFFFu, c[y], 2);
       const int k = k0 + g + 8 * y;
-      const uint32_t key = b.key(a, y, k, own, static_cast<float>(c[y]));
+      const uint32_t key = b.template key<0>(a, y, k, own, static_cast<float>(c[y]));
       if (t != 0 || k >= blocks) continue;
       if (ranks > 1) {
         const uint32_t to = mapa_shared(smem_u32(keys + k), 0);
@@ -817,8 +898,8 @@ int ds_vit_cache_select(const ds_vit_cache* cache, const ds_vit_chunks* chunks, 
   const bool single = chunks->max_rows < 8 || units <= 4 * static_cast<int64_t>(num_sms()) || 8 * a.places > kSelectKeyBytes;
   a.tile_rows = 1;
   if (!single) {
-    // Sixteen rows where two CTAs fit an SM (1907 blocks: 16 rows 172 us, 8 rows 148), else eight as long as one fits (3750 blocks:
-    // 8 rows 371 us, 4 rows 389).
+    // Sixteen rows where two CTAs fit an SM (938 blocks: 16 rows 48 us, 8 rows 52; 1907 blocks: 139 and 112), else eight as
+    // long as one fits (3750 blocks: 8 rows 257 us, 4 rows 310).
     a.tile_rows = 64 * static_cast<int64_t>(a.places) <= kSelectKeyBytes / 2 ? kTileRows : kTileRows / 2;
     while (4 * static_cast<int64_t>(a.tile_rows) * a.places > kSelectKeyBytes) a.tile_rows /= 2;
   }
