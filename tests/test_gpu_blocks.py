@@ -6,7 +6,7 @@ import math
 import numpy as np
 import pytest
 
-from test_gpu_cache import Setup, check_attention, f64
+from test_gpu_cache import Setup, check_attention, f64, quantise
 
 pytestmark = pytest.mark.gpu
 
@@ -148,6 +148,38 @@ def test_bounds_of_extreme_keys(dv):
     assert np.array_equal(b.exp.cpu().numpy()[used], exp[used])
     assert np.array_equal(b.hi_lo.cpu().numpy()[used], hi_lo[used])
     assert (exp[used[4:7]] == 255).all() and exp[used[0]] == 27
+
+
+@pytest.mark.parametrize("kind,large,small", [("bf16", 3.3e38, 1e-9), ("bf16", 1e30, 1e-18), ("bf16", 3.0, 2.0 ** -133),
+                                              ("bf16", 2.0 ** 120, 2.0 ** -100), ("e4m3", 1e30, 1e-18),
+                                              ("e4m3", 200 * 2.0 ** 120, 2.0 ** -110), ("e4m3", 3.3e38, 1e-9)])
+def test_bounds_of_magnitudes_far_apart(dv, kind, large, small):
+    """A channel so small beside the block's largest value that their ratio is no float has its bound a step from 0."""
+    page, dim = 16, 64
+    st = Setup(dv, [64], [64], 1, dim, page, kind, seed=6)
+    x = np.zeros((st.n_pages, 1, page, dim))
+    for j, sign in enumerate((1, -1, 1, -1)):
+        p = int(st.table[0, j])
+        x[p, 0, 3, 5] = large * (1 if j < 2 else -1)
+        x[p, 0, :, 9:40:3] = sign * small            # the channel has no other sign
+        if kind == "e4m3":
+            x[p, 0, 3, 9:40:3] = 0                   # one exponent a key
+        x[p, 0, 7, 41], x[p, 0, 8, 41] = small, -small
+    if kind == "bf16":
+        st.cache.k.copy_(torch.from_numpy(x).bfloat16())
+    else:
+        b, e = quantise(torch.from_numpy(x).bfloat16().double().numpy())
+        st.cache.k.copy_(torch.from_numpy(b))
+        st.cache.k_exp.copy_(torch.from_numpy(e))
+    b = dv.KeyBounds.empty(st.cache)
+    status = dv.cache_bounds(st.cache, st.chunks, b, st.rows)
+    torch.cuda.synchronize()
+    hi_lo, exp = all_bounds(st)
+    used = st.table[0, :4].numpy()
+    assert int(status.item()) == dv.OK and (exp[used] < 255).all()
+    assert (hi_lo[used[::2], 0, 0, 9] == 1).all() and (hi_lo[used[1::2], 0, 1, 9] == -1).all()
+    assert np.array_equal(b.exp.cpu().numpy()[used], exp[used])
+    assert np.array_equal(b.hi_lo.cpu().numpy()[used], hi_lo[used])
 
 
 def test_bounds_hold_every_key(dv):

@@ -125,11 +125,13 @@ __global__ void __launch_bounds__(32 * kBoundWarps) cache_bounds_kernel(const __
       if (lane < kLanes) {
         int8_t* to = a.hi_lo + (at * a.c.kv_heads + head) * 2 * D + lane * kPer;
         uint32_t h[kPer / 4] = {}, l[kPer / 4] = {};
+        // The products, too, are rounded outwards: one that lies under every float is not 0, or the bound would not
+        // hold its key.
 #pragma unroll
         for (int x = 0; x < kPer; ++x) {
           if (!fine) continue;
-          h[x / 4] |= (static_cast<uint32_t>(__float2int_ru(hi[x] * f)) & 255u) << 8 * (x & 3);
-          l[x / 4] |= (static_cast<uint32_t>(__float2int_rd(lo[x] * f)) & 255u) << 8 * (x & 3);
+          h[x / 4] |= (static_cast<uint32_t>(__float2int_ru(__fmul_ru(hi[x], f))) & 255u) << 8 * (x & 3);
+          l[x / 4] |= (static_cast<uint32_t>(__float2int_rd(__fmul_rd(lo[x], f))) & 255u) << 8 * (x & 3);
         }
         if constexpr (E4M3) {
           *reinterpret_cast<uint4*>(to) = make_uint4(h[0], h[1], h[2], h[3]);
