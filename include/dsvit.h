@@ -631,7 +631,8 @@ typedef struct ds_vit_page_copies {
  *
  * ds_vit_pages_compact: afterwards the used pages are 0 .. u - 1, u their number: in
  * order, the used pages from u on take the free places before u, and all tables
- * (every slot) name the new ones.  At most cap pages move; a further call goes on.
+ * (every slot) name the new ones.  At most cap pages move; a further call goes on.  A
+ * count below 0 records DS_VIT_EINVAL, and nothing moves.
  */
 int ds_vit_pages_resize(const ds_vit_page_pool* pool, const ds_vit_page_tables* tables, const int32_t* slot,
                         const int32_t* length, int32_t n, const ds_vit_page_copies* copies, int32_t* status,

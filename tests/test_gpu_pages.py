@@ -340,6 +340,34 @@ def test_entries_left_out(dv):
     assert int(b.status.item()) == dv.EINVAL and int(b.pool.refs.min()) == 0
 
 
+@pytest.mark.parametrize("n_pages", [60, 40000])
+@pytest.mark.parametrize("count", [-1, -3, -2 ** 31])
+@pytest.mark.parametrize("where", ["behind the used ones", "before their end", "the last page"])
+def test_nothing_moves_where_a_count_is_below_zero(dv, n_pages, count, where):
+    """A page of such a count that a table names: reported, and all stays as it was; put right, it is compacted."""
+    b = Both(dv, n_pages, 16, 8, 30)
+    b.resize([0, 1, 2, 3], [33, 200, 480, 5])
+    b.resize([1], [0])                                # thirteen holes in front
+    if where == "the last page":
+        b.m.table[4, 0], b.m.len[4], b.m.refs[n_pages - 1] = n_pages - 1, 9, 1
+        b.tables.table[4, 0], b.tables.kv_len[4], b.pool.refs[n_pages - 1] = n_pages - 1, 9, 1
+        at = n_pages - 1
+    else:
+        at = int(b.m.table[2, 29 if where == "behind the used ones" else 0])
+    b.pool.refs[at] = count
+    refs = b.pool.refs.clone()
+    b.copies.count.fill_(5)
+    dv.pages_compact(b.pool, b.tables, b.copies, b.status)
+    torch.cuda.synchronize()
+    assert int(b.status.item()) == dv.EINVAL and int(b.copies.count.item()) == 0
+    assert torch.equal(b.pool.refs, refs)
+    assert np.array_equal(b.tables.table.cpu().numpy(), b.m.table)
+    assert np.array_equal(b.tables.kv_len.cpu().numpy(), b.m.len)
+    b.status.zero_()
+    b.pool.refs[at] = 1
+    b.compact()
+
+
 def test_captured_calls(dv):
     """A beam search step as a graph: lists and lengths are read anew by every replay."""
     b = Both(dv, 200, 16, 20, 20)

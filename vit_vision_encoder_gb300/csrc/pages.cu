@@ -461,18 +461,29 @@ __global__ void __launch_bounds__(kThreads) pages_compact_kernel(const __grid_co
   cluster_sync();
   const int64_t lane = threadIdx.x + static_cast<int64_t>(cluster_rank()) * kThreads, lanes = kCtas * kThreads;
   int4 v = first_counts(a);
-  tell(sh, 0, count_pages(sh, a, 0, v, [&](int64_t, int count) {
-         if (count < 0 && count != kBehind) report_error(a.status, DS_VIT_EINVAL);
-         return count > 0;
-       }));
+  bool below = false;                   // a count under 0: the table entries that name its page could not be told from moved ones
+  const int here = count_pages(sh, a, 0, v, [&](int64_t p, int count) {
+    below |= count < 0 && p < a.n_pages;
+    return count > 0;
+  });
+  below = __syncthreads_or(below);
+  tell(sh, 0, below ? -1 - here : here);
   cluster_sync();
+  for (int r = 0; r < kCtas; ++r) below |= sh.all[0][r] < 0;
+  if (below) {
+    if (lane == 0) {
+      report_error(a.status, DS_VIT_EINVAL);
+      *a.count = 0;
+    }
+    return;
+  }
   const int64_t used = told(sh, 0);
   const auto hole = [&](int64_t p, int count) { return count == 0 && p < used; };
   const auto mover = [&](int64_t p, int count) { return count > 0 && p >= used; };
   tell(sh, 1, count_pages(sh, a, 1, v, hole));
   tell(sh, 2, count_pages(sh, a, 2, v, mover));
   cluster_sync();
-  // As many holes as movers, unless a count is below 0.
+  // As many holes as movers.
   const int64_t moved = min(min(told(sh, 1), told(sh, 2)), static_cast<int64_t>(a.cap));
   number_pages(sh, a, 0, v, told_before(sh, 1), moved, hole, [&](int64_t j, int32_t page) { a.to[j] = page; });
   __syncthreads();                      // the last scan's sums have been read
