@@ -417,7 +417,9 @@ typedef struct ds_vit_rotary {
  * head_dim/2: one section behind the other, or with `interleaved` pair i at axis
  * a = i mod 3 for a > 0 and i < 3 sections[a], at axis 0 otherwise (then
  * 3 sections[a] is at most head_dim/2 + 2 - a for a = 1, 2).  sections is not
- * looked at with one axis.  Angles are right to 2^-55 turns a position.
+ * looked at with one axis.  Angles are right to 2^-55 turns a position with theta, whose
+ * powers are rounded to double; with inv_freq to 2^-63 up to frequencies of 2^64, and to
+ * inv_freq[i] * 2^-127 beyond.
  * DS_VIT_EINVAL for another head_dim than 64 or 128, other axes, sections or
  * pairings, theta or a frequency that is not positive and finite (theta: over 1).
  */

@@ -1,6 +1,7 @@
 """Argument checks of the norms and rotation without a GPU (refusals come before any CUDA
 call), and the table that ds_vit_rotary_init makes."""
 import ctypes as C
+import random
 from fractions import Fraction
 
 import pytest
@@ -51,6 +52,49 @@ def test_tables(dv):
             assert abs(Fraction(t, 2 ** 64) - want) <= Fraction(1, 2 ** 55) * max(1, int(f) + 1)
     rc, r = _init(dv, axes=3, sections=(24, 20, 20))
     assert list(r.axis) == [0] * 24 + [1] * 20 + [2] * 20
+
+
+def _pi(bits):
+    """pi in units of 2^-bits, by 16 atan(1/5) - 4 atan(1/239)."""
+    def atan_of(x):
+        term = total = (1 << bits) // x
+        n = 1
+        while term:
+            term //= x * x
+            n += 2
+            total += -(term // n) if n % 4 == 3 else term // n
+        return total
+    return 16 * atan_of(5) - 4 * atan_of(239)
+
+
+def test_turns_of_given_frequencies(dv):
+    """Right to 2^-63 turns a position up to frequencies of 2^64, over a radian a position as well as under."""
+    two_pi = Fraction(_pi(400), 2 ** 399)
+    r = random.Random(3)
+    given = [0.99, 1.0, 1.3, 6.283185307179586, 6.5, 100.0, 12345.678, 1e6 + 0.1, 2.0 ** 31 - 0.5, 1e15 + 0.5, 1.7e16, 1e19,
+             2.0 ** 64, 1e-9, 1e-18, 2.0 ** -62, 2.0 ** -64, 1e-30, 1e-300, 5e-324]
+    given += [r.uniform(1, 2) * 2.0 ** r.randint(-70, 63) for _ in range(64 * 20 - len(given))]
+    for i in range(0, len(given), 64):
+        rc, t = _init(dv, inv=given[i:i + 64])
+        assert rc == dv.OK
+        for f, turn in zip(given[i:i + 64], t.turn):
+            off = (Fraction(turn, 2 ** 64) - Fraction(f) / two_pi) % 1
+            assert min(off, 1 - off) <= Fraction(1, 2 ** 63), f
+    assert _init(dv, inv=[1.7e308] * 64)[0] == dv.OK
+
+
+@pytest.mark.parametrize("head_dim", [64, 128])
+@pytest.mark.parametrize("theta", [1.0000001, 2.0, 1e4, 5e5, 1e6, 1e7, 1e300])
+def test_turns_of_a_theta(dv, head_dim, theta):
+    """Right to 2^-55 turns a position: those of theta^(-2i/d) as a double, which is at most 1."""
+    two_pi = Fraction(_pi(400), 2 ** 399)
+    rc, t = _init(dv, head_dim, theta)
+    assert rc == dv.OK
+    for i, turn in zip(range(head_dim // 2), t.turn):
+        # theta^(-2i/d) by its head_dim/2-th power: what lies between a step of 2^-55 turns to either side.
+        lo, hi = ((Fraction(turn, 2 ** 64) + d) * two_pi for d in (Fraction(-1, 2 ** 55), Fraction(1, 2 ** 55)))
+        want = 1 / Fraction(theta) ** i
+        assert (max(lo, 0) ** (head_dim // 2) <= want <= hi ** (head_dim // 2)), i
 
 
 def _call(dv, r, q=P, qs=1024, heads=8, k=P, ks=256, kv=2, rows=0, pos=P, ps=100, qn=None, kn=None, eps=1e-6, qo=P,

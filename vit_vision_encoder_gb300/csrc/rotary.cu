@@ -165,6 +165,22 @@ __global__ void __launch_bounds__(32 * kWarps, kWarpsPerSm / kWarps) qk_norm_rop
   }
 }
 
+// f / 2 pi modulo 1 in units of 2^-64, rounded down, f positive and finite.  f is m 2^-x with m whole and under 2^53;
+// 1 / 2 pi goes in as 128 bits, whose error is f 2^-128 turns.  Whole numbers throughout: the same on every machine.
+uint64_t turns_of(double f) {
+  constexpr uint64_t kHigh = 0x28BE60DB9391054Au, kLow = 0x7F09D5F47D4D3770u;    // 2^128 / 2 pi, rounded down
+  int x;
+  const uint64_t m = static_cast<uint64_t>(std::ldexp(std::frexp(f, &x), 53));
+  const int right = 53 - x + 64;            // the product's place: m kHigh:kLow is in units of 2^(x - 53 - 128) turns
+  const unsigned __int128 low = static_cast<unsigned __int128>(m) * kLow;
+  const unsigned __int128 high = static_cast<unsigned __int128>(m) * kHigh + static_cast<uint64_t>(low >> 64);
+  const uint64_t words[4] = {static_cast<uint64_t>(low), static_cast<uint64_t>(high), static_cast<uint64_t>(high >> 64), 0};
+  if (right <= 0) return right > -64 ? words[0] << -right : 0;
+  if (right >= 192) return 0;
+  const int word = right / 64, bit = right % 64;
+  return words[word] >> bit | (bit ? words[word + 1] << (64 - bit) : 0);
+}
+
 }  // namespace
 
 }  // namespace dsvit
@@ -196,10 +212,7 @@ int ds_vit_rotary_init(int32_t head_dim, double theta, const double* inv_freq, i
   for (int i = 0; i < pairs; ++i) {
     const double f = inv_freq ? inv_freq[i] : std::pow(theta, -static_cast<double>(i) / pairs);
     if (!(f > 0.0 && std::isfinite(f))) return DS_VIT_EINVAL;
-    double turns = f * 0.15915494309189533577;   // 1 / 2 pi
-    turns -= std::floor(turns);
-    // Under 1 by 2^-53 at least, so that the product is under 2^64.
-    r.turn[i] = static_cast<uint64_t>(turns * 0x1p64);
+    r.turn[i] = turns_of(f);
     if (axes == 3 && interleaved)
       r.axis[i] = static_cast<uint8_t>(i % 3 && i < 3 * sections[i % 3] ? i % 3 : 0);
     else if (axes == 3)
