@@ -147,6 +147,24 @@ def test_rows_of_zeros_and_not_finite_ones(dv):
     assert torch.isnan(y[2, 1]).all() and torch.isfinite(y[2, 0]).all() and torch.isfinite(y[3]).all()
 
 
+@pytest.mark.parametrize("pairing", ["half_vector", "adjacent"])
+@pytest.mark.parametrize("rows", [4, 700])
+def test_queries_and_keys_are_treated_alike(dv, pairing, rows):
+    """The same heads as queries and as keys give the same bits, whatever is in other heads, zeros and NaN among them."""
+    g = torch.Generator().manual_seed(rows)
+    x = torch.randn((rows, 12, 64), generator=g).bfloat16().cuda()
+    x[0] = 0
+    x[1, 0, 5] = math.inf
+    x[2, 1, 7] = math.nan
+    w = (1 + 0.3 * torch.randn(64, generator=g)).bfloat16().cuda()
+    r = dv.Rotary(64, pairing=pairing)
+    pos = torch.arange(rows, dtype=torch.int32, device="cuda")
+    y, k = dv.qk_norm_rope(r, x, x[:, :5], pos, w, w)
+    torch.cuda.synchronize()
+    assert torch.equal(y[:, :5].view(torch.int16), k.view(torch.int16))
+    assert torch.isfinite(y[3:]).all() and torch.isfinite(y[1, 1:]).all() and torch.isnan(k[2, 1]).all()
+
+
 def test_positions_of_an_image_prompt(dv):
     """The three axes that the layout of an image span gives, text before it."""
     span, delta = dv.qwen_layout(5, 7, 20)
