@@ -191,7 +191,85 @@ def test_bounds_hold_every_key(dv):
         assert (st.hi_lo[:, :, 0] * step >= k.max(2)).all() and (st.hi_lo[:, :, 1] * step <= k.min(2)).all()
 
 
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("group,dim", [(1, 128), (5, 64), (128, 64)])
+def test_written_bounds_and_scores_from_above(dv, kind, group, dim):
+    """What ds_vit_cache_bounds writes holds every key, and the score from it lies at or over the true sum of products with
+    every key of the block, but for what the rounding of the queries to whole numbers moves."""
+    page, heads = 16, 2
+    st = Setup(dv, [330], [330], heads, dim, page, kind, seed=group)
+    b = dv.KeyBounds.empty(st.cache)
+    status = dv.cache_bounds(st.cache, st.chunks, b, st.rows)
+    torch.cuda.synchronize()
+    assert int(status.item()) == dv.OK
+    used = st.table[0, :330 // page].numpy()             # the last block is not full
+    k = st.held()[0][used]
+    step = 2.0 ** (b.exp.cpu().numpy()[used].astype(float) - 127)[..., None]
+    hi, lo = (b.hi_lo.cpu().numpy()[used, :, i] * step for i in range(2))
+    assert (hi >= k.max(2)).all() and (lo <= k.min(2)).all()
+    assert (hi < k.max(2) + step).all() and (lo > k.min(2) - step).all()
+    q = f64(st.queries(heads * group))[::29]
+    G = 1 << (group - 1).bit_length()
+    for x in q.reshape(-1, heads, group, dim):
+        for h in range(heads):
+            unit = 2.0 ** least(np.abs(x[h]).max() * G, 1016)
+            n = np.rint(x[h] / unit)
+            score = unit * (hi[:, h] @ np.maximum(n, 0).sum(0) + lo[:, h] @ np.minimum(n, 0).sum(0))
+            moved = np.abs(k[:, h]).max(1) @ np.abs(x[h] - unit * n).sum(0)
+            true = (k[:, h] @ x[h].sum(0)).max(1)
+            assert (true <= score + moved + 1e-9 * np.abs(score)).all()
+
+
 # ------------------------------------------------------------------ selection
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("group", [1, 5, 128])
+@pytest.mark.parametrize("n,rows", [(12, 1), (1, 300)])
+def test_the_block_of_a_matching_key_is_chosen(dv, kind, group, n, rows):
+    """Each row's queries lie near one key, twenty times as long, of one block, other blocks hold such keys of other rows:
+    the block is listed."""
+    heads, dim, page, kv, top = 4, 64, 16, 2000, 4
+    g = torch.Generator().manual_seed(group + n)
+    many = 50 if n == 1 else 3                           # directions of a sequence, each with a block of its own
+    base = torch.randn((n, many, heads, dim), generator=g)
+    block = torch.stack([torch.randperm(100, generator=g)[:many] for _ in range(n)])
+    k = torch.randn((n, kv, heads, dim), generator=g)
+    for s in range(n):
+        at = block[s] * page + torch.randint(0, page, (many,), generator=g)
+        k[s, at] = 20 * base[s]
+    cache = dv.KvCache.empty(n * kv // page, heads, page, dim, dv.CACHE_BF16 if kind == "bf16" else dv.CACHE_E4M3)
+    table = torch.randperm(n * kv // page, generator=g).int().view(n, -1).cuda()
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")   # noqa: E731
+    whole = dv.Chunks(i32([kv * s for s in range(n + 1)]), i32([kv] * n), table, kv)
+    status = dv.cache_write(cache, whole, *[k.view(n * kv, heads, dim).bfloat16().cuda()] * 2)
+    bounds = dv.KeyBounds.empty(cache)
+    dv.cache_bounds(cache, whole, bounds, n * kv, status)
+    which = torch.randint(0, many, (n, rows), generator=g)
+    q = torch.stack([base[s, which[s]] for s in range(n)]).view(n * rows, heads, 1, dim)
+    q = (q + 0.2 * torch.randn((n * rows, heads, group, dim), generator=g)).view(n * rows, heads * group, dim)
+    chunks = dv.Chunks(i32([rows * s for s in range(n + 1)]), i32([kv] * n), table, rows)
+    got, _ = dv.cache_select(cache, chunks, bounds, q.bfloat16().cuda(), top, 0, 1, status=status)
+    torch.cuda.synchronize()
+    want = torch.stack([block[s, which[s]] for s in range(n)]).view(n * rows, 1, 1)
+    assert int(status.item()) == dv.OK and (got.cpu() == want).any(-1).all()
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+def test_a_chunk_beside_single_rows(dv, kind):
+    """A prompt's chunk, draft tokens and single tokens of many sequences in one call: tiles of packed rows that hold up
+    to sixteen sequences, as the call has more rows than CTAs' worth."""
+    q = [1] * 13 + [40] + [1] * 30 + [0, 9] + [1] * 20
+    kv = [17 + 37 * i % 900 for i in range(13)] + [700] + [1 + 211 * i % 1000 for i in range(30)] + [64, 300]
+    kv += [16 * i + 16 for i in range(20)]
+    st = make(dv, q, kv, 8, 64, 16, kind, seed=2, front=1, back=3)
+    assert st.rows * 8 > 4 * torch.cuda.get_device_properties(0).multi_processor_count
+    x = st.queries(16)
+    for top in (5, 40):
+        got = check_select(dv, st, 16, top, 1, 2, q=x)
+    blocks = torch.from_numpy(got).int()
+    blocks[:, :, 6:] = -1
+    check_blocks(dv, st, 16, blocks, q=x)
+
 
 def check_select(dv, st, heads, top, first, last, q=None):
     q = st.queries(heads) if q is None else q
