@@ -377,12 +377,7 @@ __device__ __forceinline__ bool pick_few(const uint32_t* keys, int n, const Sele
   int forced = 0;
   for (int i = lane; i < firsts + lasts; i += 32) forced += keys[i < firsts ? i : n - lasts + i - firsts] == kForced;
   forced = __reduce_add_sync(0xFFFFFFFFu, forced);
-  const int need = top - forced;
-  if (need > 32 * kTop) {
-    lo = 1;
-    hi = kForced;
-    return false;
-  }
+  const int need = top - forced;        // at most 32 kTop: the lists this is called for
   lo = hi = kForced;
   if (need > 0) {
     lo = max(__shfl_sync(0xFFFFFFFFu, sorted_down(most[kTop - 1], lane), (need + kTop - 1) / kTop - 1), 2u) - 1;
