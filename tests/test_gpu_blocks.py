@@ -396,6 +396,17 @@ def test_select_in_wide_tables(dv):
         dv.cache_select(st.cache, st.chunks, st.bounds, st.queries(8), 5)
 
 
+@pytest.mark.parametrize("dim", [64, 128])
+def test_select_longer_lists_in_wide_tables(dv, dim):
+    """Tables on both sides of the widths at which two CTAs, with the keys that they hold for longer lists, fit an SM."""
+    st = make(dv, [200], [700], 8, dim, 16, "bf16", cols=700)
+    for cols in (1376, 1408, 1440, 1500, 1568, 1600, 1632, 1800):
+        st.chunks = dv.Chunks(st.chunks.row_off, st.chunks.kv_len,
+                              torch.nn.functional.pad(st.table, (0, cols - st.table.shape[1]), value=-1).cuda(), 200)
+        for top in (32, 33):
+            check_select(dv, st, 8, top, 1, 1)
+
+
 def test_select_long_contexts(dv):
     """Many thousand blocks against the same whole numbers in torch (one sequence, one head)."""
     page, dim, blocks = 16, 64, 30011

@@ -829,6 +829,8 @@ __global__ void __launch_bounds__(kSelectThreads, 3) cache_select_row_kernel(con
 }
 
 constexpr int kSelectKeyBytes = 200 * 1024;      // of shared memory, for scores
+constexpr int kSharedOfSm = 228 * 1024, kSharedOfCta = 1024;      // there is; what the system takes of it for every CTA
+constexpr int kept_bytes(int top) { return 8 * kSelectThreads * held_by_lane(top); }      // keys that are held while a list is picked
 static_assert(4 * (DS_VIT_SELECT_MAX_COLS + 4) <= kSelectKeyBytes, "one row's scores");
 
 bool bad_bounds(const ds_vit_key_bounds* b) { return !b || !b->hi_lo || !aligned(b->hi_lo, 16) || !b->exp; }
@@ -895,9 +897,11 @@ int ds_vit_cache_select(const ds_vit_cache* cache, const ds_vit_chunks* chunks, 
   const bool single = chunks->max_rows < 8 || units <= 4 * static_cast<int64_t>(num_sms()) || 8 * a.places > kSelectKeyBytes;
   a.tile_rows = 1;
   if (!single) {
-    // Sixteen rows where two CTAs fit an SM (938 blocks: 16 rows 48 us, 8 rows 52; 1907 blocks: 139 and 112), else eight as
-    // long as one fits (3750 blocks: 8 rows 257 us, 4 rows 310).
-    a.tile_rows = 64 * static_cast<int64_t>(a.places) <= kSelectKeyBytes / 2 ? kTileRows : kTileRows / 2;
+    // Sixteen rows where two CTAs fit an SM (938 blocks: 16 rows 48 us, 8 rows 52; 1907 blocks: 139 and 112; lists of 64,
+    // which take more to pick: 1400 blocks 76 and 81, 1450 blocks, where one CTA fits, 118 and 85), else eight as long as
+    // one fits (3750 blocks: 8 rows 257 us, 4 rows 310).
+    const int64_t fixed = 2 * kTileRows * (2 * cache->head_dim + 8) + 4 * kTileRows + kept_bytes(top) + kSharedOfCta;
+    a.tile_rows = 2 * (4 * kTileRows * static_cast<int64_t>(a.places) + fixed) <= kSharedOfSm ? kTileRows : kTileRows / 2;
     while (4 * static_cast<int64_t>(a.tile_rows) * a.places > kSelectKeyBytes) a.tile_rows /= 2;
   }
   int ranks = 1;
@@ -905,11 +909,10 @@ int ds_vit_cache_select(const ds_vit_cache* cache, const ds_vit_chunks* chunks, 
     while (ranks < 8 && 2 * ranks * units <= 2 * static_cast<int64_t>(num_sms()) &&
            2 * ranks * 16 * kSelectWarps <= chunks->table_cols)
       ranks *= 2;
-  const int kept = single ? 0 : 8 * kSelectThreads * held_by_lane(top);
-  const int bytes = 4 * a.tile_rows * a.places + kept;
+  const int bytes = 4 * a.tile_rows * a.places + (single ? 0 : kept_bytes(top));
   auto* fn = cache->head_dim == 128 ? (single ? cache_select_row_kernel<128> : cache_select_kernel<128>)
                                     : (single ? cache_select_row_kernel<64> : cache_select_kernel<64>);
-  if (allow_smem(reinterpret_cast<const void*>(fn), kSelectKeyBytes + 8 * kSelectThreads * kHeldMost) != cudaSuccess) return DS_VIT_ECUDA;
+  if (allow_smem(reinterpret_cast<const void*>(fn), kSelectKeyBytes + kept_bytes(DS_VIT_SELECT_MAX_TOP)) != cudaSuccess) return DS_VIT_ECUDA;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>((rows + a.tile_rows - 1) / a.tile_rows * c.kv_heads * ranks));
   cfg.blockDim = dim3(kSelectThreads);
