@@ -594,7 +594,10 @@ int ds_vit_cache_attention(const ds_vit_cache* cache, const ds_vit_chunks* chunk
 #define DS_VIT_MAX_SLOTS 65536
 
 typedef struct ds_vit_page_pool {
-  int32_t* refs;        /* device [n_pages], at least 0: in how many table entries a page is named */
+  int32_t* refs;        /* device [n_pages], at least 0: in how many table entries a page is named.
+                           The calls go by it and do not compare it with the tables: resize,
+                           release and compact record DS_VIT_EINVAL where one is, or would get,
+                           below 0, fork does not look */
   int64_t n_pages;
   int32_t page;         /* tokens per page: 16, 32, 64 or 128 */
 } ds_vit_page_pool;
@@ -703,6 +706,8 @@ int ds_vit_cache_copy(const ds_vit_cache* cache, const ds_vit_key_bounds* bounds
  * taken.  Rows in front of position 0 get -1 throughout, packed rows of no sequence
  * stay as they were.  Bounds are read of every block of the sequences but the
  * rows' own.
+ * Calls of max_rows 8 and more are made for chunks: their rows go in tiles of neighbours, in which
+ * single tokens of many sequences wait for each other.  A call of their own serves those faster.
  * DS_VIT_EINVAL for first < 0, last < 1, top outside first + last ..
  * DS_VIT_SELECT_MAX_TOP, bounds or blocks null or misaligned (hi_lo 16 bytes, blocks 4), a
  * stride of the lists below top (not looked at for one row or one head);

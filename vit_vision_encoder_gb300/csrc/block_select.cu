@@ -2,7 +2,9 @@
 // attends to (include/dsvit.h, ds_vit_cache_bounds and ds_vit_cache_select).
 //
 // Bounds: each completed page is read once, by one warp a K/V head, 32 keys in flight; bound by memory and, at the
-// sizes of a chunk, by the chain sequence -> table -> keys (13.9 MB of e4m3 pages: 7.4 us).
+// sizes of a chunk, by the chain sequence -> table -> keys (13.9 MB of e4m3 pages: 7.4 to 8.2 us).  The grid has the blocks
+// of the longest chunk for every sequence: one of 8192 rows in pages of 16 takes 6.3 us, beside 63 single tokens 41.  (At head
+// dim 64 over bf16 pages the compiler spills 12 bytes.)
 //
 // Selection: scores are a product of the blocks' bounds [blocks, 2 D] with the rows' shared
 // queries [2 D, rows].  Both operands are small whole numbers (|n| <= 1024, |H| <= 127) and so is every
@@ -348,9 +350,8 @@ __device__ __forceinline__ uint32_t sorted_down(uint32_t x, int lane) {
 // The same by one warp where few blocks of many are looked for.  Each lane finds its own kTop-th largest key; the
 // (need / kTop)-th largest of those is a bound that at least `need` keys reach and not many more do.  Those are listed,
 // and held by the lanes, a few each, while the threshold is searched.  False, with nothing written, where too many
-// reach it, with what is known of the threshold.  keys + n up to the next multiple of four are 0.  (532 blocks, 16 of them, as measured when it was brought in: 83 us for 16 thousand
-// lists, 137 by counting all keys; 3750 blocks, 128 of them, 8 thousand lists: 725
-// by counting all keys, 428.)
+// reach it, with what is known of the threshold.  keys + n up to the next multiple of four are 0.  (8 thousand lists
+// of 3750 blocks: 20 of them 255 us, 128 302; 129, which go to the search through all keys, 483, 1024 505.)
 constexpr int kHeldMost = 8;
 __host__ __device__ constexpr int held_by_lane(int top) { return top <= 32 ? 2 : kHeldMost; }
 template <int kTop>
@@ -600,7 +601,8 @@ __device__ __forceinline__ int32_t page_entry(const int32_t* table, int k, int b
 // numbers of at most 2^24 in any order, 127 |w| of the terms that are in and 128 |w| of the others.  2048 rows of 8
 // heads over 532 blocks: 54 us, over 938 blocks (1024 rows) 48; 56 and 60 with bytes widened to fp16 by a subtraction, four CTAs
 // an SM (64 registers) and each round's bounds loaded when it begins.  Thirty-two rows a CTA, with eight to
-// sixteen warps: 54 to 57 and 53 to 56.
+// sixteen warps: 54 to 57 and 53 to 56.  At head dim 128 the third CTA an SM costs 16 bytes
+// of spills.
 template <int D>
 __global__ void __launch_bounds__(kSelectThreads, D == 128 ? 3 : 4) cache_select_kernel(const __grid_constant__ SelectArgs a) {
   constexpr int kSteps = 2 * D / 64;                // 16-byte pieces of a block that a lane has, four MMAs each
@@ -895,6 +897,9 @@ int ds_vit_cache_select(const ds_vit_cache* cache, const ds_vit_chunks* chunks, 
   // Rows of one sequence share the loads of its bounds where there are more than enough CTAs.
   const int64_t units = rows * c.kv_heads;
   const bool single = chunks->max_rows < 8 || units <= 4 * static_cast<int64_t>(num_sms()) || 8 * a.places > kSelectKeyBytes;
+  // 64 sequences over 8000 to 60000 tokens, by single rows and by tiles: 2 rows each 32 and 90 us, 4 rows 52 and 49, 7 rows
+  // 82 and 47.  A tile takes the sequences that its rows belong to one behind the other, and the choice is the call's: 60
+  // single tokens beside a chunk of 1024 rows take 193 us, in a call of their own 19 (the chunk 41).
   a.tile_rows = 1;
   if (!single) {
     // Sixteen rows where two CTAs fit an SM (938 blocks: 16 rows 48 us, 8 rows 52; 1907 blocks: 139 and 112; lists of 64,

@@ -3,7 +3,8 @@
 //
 // The four calls that change tables are chains of small steps over the list, the
 // counts and the entries: bound by latency, a few round trips to L2 each (64 forks 10 us, 240 of 450 pages 17; ending
-// those 20, of which the atomics of one cluster's SMs are half; a pool of 3000 pages compacted 14).  One cluster of
+// those 20, of which the atomics of one cluster's SMs are half; 240 sequences giving up 446 pages each behind a window 16, 64
+// of one page each 2.6; a pool of 3000 pages compacted 11).  One cluster of
 // eight CTAs makes a whole call in one launch; the steps are separated by the cluster's
 // hardware barrier, and sums over its stripes of the pool go from CTA to CTA
 // through distributed shared memory.  Work per list entry is unequal (one sequence
