@@ -33,8 +33,8 @@
 //
 // Weights are rounded where they meet the values, as in the dense attention: to bf16, 2^-8 of each at most, over bf16
 // pages, whose type the product has to share, and to fp16 over e4m3 pages, whose values widen to it exactly.  Their sum
-// takes them whole, in fp32.  Measured beside 64 bits, of the outputs' norm: 48 single rows over bf16 pages 0.0023, 0.0017 of it
-// the outputs' own rounding; e4m3 0.0017.
+// takes them whole, in fp32.  Measured beside 64 bits, of the outputs' norm: 48 single rows over bf16 pages 0.0023, where
+// weights in fp32 give 0.0017 from the outputs' rounding alone; e4m3 0.0017.
 //
 // e4m3: keys widen exactly to fp16, queries are scaled to at most 2^15 by a power of two;
 // the softmax multiplies by each key's factor.  Values widen to fp16, and the weights that meet them

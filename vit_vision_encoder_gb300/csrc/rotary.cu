@@ -165,13 +165,13 @@ __global__ void __launch_bounds__(32 * kWarps, kWarpsPerSm / kWarps) qk_norm_rop
   }
 }
 
-// f / 2 pi modulo 1 in units of 2^-64, rounded down, f positive and finite.  f is m 2^-x with m whole and under 2^53;
+// f / 2 pi modulo 1 in units of 2^-64, rounded down, f positive and finite.  f is m 2^(x - 53) with m whole and under 2^53;
 // 1 / 2 pi goes in as 128 bits, whose error is f 2^-128 turns.  Whole numbers throughout: the same on every machine.
 uint64_t turns_of(double f) {
   constexpr uint64_t kHigh = 0x28BE60DB9391054Au, kLow = 0x7F09D5F47D4D3770u;    // 2^128 / 2 pi, rounded down
   int x;
   const uint64_t m = static_cast<uint64_t>(std::ldexp(std::frexp(f, &x), 53));
-  const int right = 53 - x + 64;            // the product's place: m kHigh:kLow is in units of 2^(x - 53 - 128) turns
+  const int right = 53 - x + 64;            // m kHigh:kLow is in units of 2^(x - 53 - 128) turns: 2^-right of those wanted
   const unsigned __int128 low = static_cast<unsigned __int128>(m) * kLow;
   const unsigned __int128 high = static_cast<unsigned __int128>(m) * kHigh + static_cast<uint64_t>(low >> 64);
   const uint64_t words[4] = {static_cast<uint64_t>(low), static_cast<uint64_t>(high), static_cast<uint64_t>(high >> 64), 0};
